@@ -60,7 +60,12 @@ typedef enum {
     PKV_ERR_CUDA = 4          /* a CUDA runtime/driver call or launch failed */
 } pkv_status;
 
-typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1 } pkv_kv_dtype;
+typedef enum {
+    PKV_KV_BF16 = 0,
+    PKV_KV_FP8_E4M3 = 1,
+    PKV_KV_INT8 = 2, /* records with a scale per row: the pkv_quant_* calls and pkv_copy_blocks only */
+    PKV_KV_FP4 = 3   /* records with a scale per 16 dims: likewise */
+} pkv_kv_dtype;
 
 /* Device error word bits (pkv_device_errors). */
 #define PKV_DEVERR_BLOCK_ID 0x1u  /* a block id outside [0, num_blocks): access skipped */
@@ -438,6 +443,176 @@ pkv_status pkv_decode_attention_static(const pkv_cache_desc *desc, const void *q
                                        int32_t num_seqs, int32_t max_context_len, float sm_scale,
                                        int32_t window, const float *sinks, int32_t chunk_blocks,
                                        void *out, float *lse_out, pkv_stream_t stream);
+
+/* ---- rotary positions: both pair layouts, part of the head, scaled tables ----
+ * The rotation of pkv_append_rope in its general form.  With r = rotary_dim and
+ * (c, s) = cos_sin[p][j], every pair j < r / 2 of a row x at position p becomes
+ *   PKV_ROPE_HALF:        (x[j], x[j + r/2])   -> (a c - b s, b c + a s)
+ *   PKV_ROPE_INTERLEAVED: (x[2j], x[2j + 1])   -> (a c - b s, b c + a s)
+ * (fp32, each product and sum rounded, then one rounding to the row's type);
+ * dims r .. head_dim - 1 pass through.  PKV_ROPE_INVERSE turns by -angle (s
+ * negated): the transpose of the rotation, hence its gradient when c^2 + s^2 = 1
+ * or not -- dL/dx = inverse(dL/dx') -- and the way to re-base a rotated key. */
+#define PKV_ROPE_HALF 0
+#define PKV_ROPE_INTERLEAVED 1
+#define PKV_ROPE_INVERSE 0x1u
+typedef struct {
+    const float *cos_sin; /* fp32 [max_pos][rotary_dim / 2][2], device, 8-byte aligned */
+    int32_t rotary_dim;   /* even, 2 .. head_dim */
+    int32_t layout;       /* PKV_ROPE_HALF or PKV_ROPE_INTERLEAVED */
+    int32_t max_pos;
+    uint32_t flags;       /* PKV_ROPE_INVERSE or 0 */
+} pkv_rope;
+
+typedef enum { PKV_BF16 = 0, PKV_F16 = 1, PKV_F32 = 2 } pkv_dtype;
+
+/* Rows [num_tokens][num_heads][head_dim] by strides, in elements; the head's own
+ * dims are contiguous.  A view into a packed QKV buffer is num_heads rows at
+ * head stride head_dim and token stride (Hq + 2 Hkv) * head_dim. */
+typedef struct {
+    const void *in;
+    void *out;            /* == in with the same strides: in place */
+    int64_t in_token_stride, in_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int32_t num_heads;
+    int32_t reserved;     /* 0 */
+} pkv_rows;
+
+/* Rotate the rows of q and (k != NULL) of k, token i at positions[i].  A
+ * negative position is padding: that token's output rows are left as they are.
+ * One at or beyond max_pos leaves them too and sets PKV_DEVERR_POSITION.
+ *   dtype     : of q and k rows, in and out.    positions: int32 [num_tokens].
+ *   head_dim  : even, 2 .. 512.
+ * In-strides are >= 0 (0 broadcasts a row); out rows must not overlap one
+ * another, nor the inputs unless q->out == q->in with equal strides (likewise
+ * k), nor may q's outputs overlap k's rows or the reverse. */
+pkv_status pkv_rope_rotate(const pkv_rope *rope, int32_t dtype, const int32_t *positions,
+                           int32_t num_tokens, int32_t head_dim, const pkv_rows *q,
+                           const pkv_rows *k, pkv_stream_t stream);
+
+/* Host: pkv_rope_cos_sin_table with the frequencies scaled for contexts longer
+ * than the trained one (L = original_max_pos).  With f_j = theta^(-2j/r) the
+ * unscaled frequency of pair j and w_j = 2 pi / f_j its wavelength:
+ *   PKV_ROPE_SCALE_LINEAR  f_j / factor
+ *   PKV_ROPE_SCALE_NTK     (theta factor^(r/(r-2)))^(-2j/r)
+ *   PKV_ROPE_SCALE_BANDED  f_j if w_j < L / high_freq; f_j / factor if w_j > L /
+ *                          low_freq; between, (1 - m) f_j / factor + m f_j with
+ *                          m = (L / w_j - low_freq) / (high_freq - low_freq)
+ *   PKV_ROPE_SCALE_YARN    (1 - g) f_j / factor + g f_j, g = 1 - clamp((j - lo) /
+ *                          (hi - lo), 0, 1), lo = floor(d(high_freq)), hi =
+ *                          ceil(d(low_freq)) clamped to [0, r - 1] (hi += 0.001 if equal),
+ *                          d(n) = r ln(L / (2 pi n)) / (2 ln theta): high_freq and
+ *                          low_freq are numbers of turns over L
+ * cos and sin are then multiplied by `attention` (1 for none; YaRN's usual
+ * choice is 0.1 ln(factor) + 1).  Angles in double, rounded once to fp32. */
+#define PKV_ROPE_SCALE_NONE 0
+#define PKV_ROPE_SCALE_LINEAR 1
+#define PKV_ROPE_SCALE_NTK 2
+#define PKV_ROPE_SCALE_BANDED 3
+#define PKV_ROPE_SCALE_YARN 4
+typedef struct {
+    int32_t kind;             /* PKV_ROPE_SCALE_* */
+    int32_t original_max_pos; /* L (banded, yarn) */
+    double factor;            /* >= 1 */
+    double low_freq, high_freq; /* banded, yarn: 0 < low_freq < high_freq */
+    double attention;         /* > 0 */
+} pkv_rope_scaling;
+pkv_status pkv_rope_scaled_table(float theta, int32_t rotary_dim, int32_t max_pos,
+                                 const pkv_rope_scaling *scaling, float *host_out);
+
+/* ---- a cache quantised as it is written ---------------------------------
+ * kv_dtype PKV_KV_INT8 and PKV_KV_FP4 pools hold, per (block, KV head), one
+ * record: [num_blocks][Hkv][record bytes].  A record is the codes of the
+ * block's 16 rows, row_bytes each, then the rows' scales:
+ *   PKV_KV_INT8  row_bytes = D: a byte per dim holding code + 128, code in
+ *                [-127, 127]; then fp32 [16], one scale per row.
+ *                value = code * scale.  Record: 16 D + 64 bytes.
+ *   PKV_KV_FP4   row_bytes = D / 2: two e2m1 codes a byte, dim 2i in the low
+ *                nibble; then e4m3 [16][D / 16], a scale per 16 dims.
+ *                value = (e2m1 * scale) * g, g = k_scale[h] / v_scale[h].
+ *                Record: 8 D + D bytes.
+ * The 16-byte chunk c of row r's codes is stored at chunk
+ * c ^ ((r * row_bytes / 128) mod (row_bytes / 16)) of that row: with it a
+ * record copied into shared memory as it stands is read without bank conflicts.
+ * Quantisation of a row x (fp32), every division rounded to fp32:
+ *   int8: scale = amax / 127; code = rne(x / scale), clamped to +-127;
+ *   fp4 : e = e4m3(min(amax16 / (6 g), 448)), t = e * g, code = e2m1(x / t),
+ *         nearest even, saturating;
+ * amax runs over the finite magnitudes; a NaN is stored as 0, an infinity as
+ * the largest code; a zero scale stores zeros.
+ * k_scale, v_scale: fp32 [Hkv], finite and > 0, for PKV_KV_FP4 (as frozen from a
+ * warm-up: amax / 2688 uses the scales' whole range); NULL for PKV_KV_INT8.
+ * Pools are 16-byte aligned.  A ring cache (ring_blocks > 0) is honoured by
+ * append, read and decode; DESC flags are accepted and promise nothing here. */
+
+/* Bytes of one quantised pool; host only, 0 for an invalid desc. */
+uint64_t pkv_quant_cache_bytes(const pkv_cache_desc *desc);
+
+/* Append: token i of sequence s = token_to_seq[i] at positions[i] goes into the
+ * slot pkv_append_rope would use, K rotated (rope != NULL) in fp32 and quantised,
+ * V quantised; q_out[i] = q[i] rotated (rope != NULL, q != NULL), rounded to bf16.
+ * token_to_seq[i] < 0 is padding: nothing of that token is read or written.
+ *   k_new, v_new: bf16, token i's [Hkv][D] rows at i * new_token_stride elements;
+ *   q, q_out    : bf16, token i's [Hq][D] rows at i * q_token_stride /
+ *                 q_out_token_stride; q_out == q rotates in place; q may be NULL,
+ *                 and must be when rope is.
+ * Pointers 16-byte aligned, strides multiples of 8 elements.  Two tokens must not
+ * target the same slot in one call. */
+pkv_status pkv_quant_append(const pkv_cache_desc *desc, const pkv_rope *rope, void *k_pool,
+                            void *v_pool, const float *k_scale, const float *v_scale,
+                            const int32_t *block_tables, int32_t num_seqs,
+                            const int32_t *token_to_seq, const int32_t *positions,
+                            int32_t num_tokens, const void *k_new, const void *v_new,
+                            int64_t new_token_stride, const void *q, void *q_out,
+                            int64_t q_token_stride, int64_t q_out_token_stride,
+                            pkv_stream_t stream);
+
+/* Read rows back: k_out[i][h][:] = the value of K at (token_to_seq[i],
+ * positions[i]), likewise v_out, each rounded to fp32 and then to out_dtype
+ * (PKV_BF16 or PKV_F32).  [num_tokens][Hkv][D] contiguous, 16-byte aligned;
+ * either may be NULL (its pool then too).  token_to_seq[i] < 0 leaves row i as it
+ * is.  A bad position or block id leaves the row and sets its device error bit. */
+pkv_status pkv_quant_read(const pkv_cache_desc *desc, const void *k_pool, const void *v_pool,
+                          const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                          int32_t num_seqs, const int32_t *token_to_seq, const int32_t *positions,
+                          int32_t num_tokens, int32_t out_dtype, void *k_out, void *v_out,
+                          pkv_stream_t stream);
+
+/* Widen whole blocks: block dst_blocks[i] of the bf16 pools k_cache / v_cache
+ * ([dst_num_blocks][Hkv][16][D], as a PKV_KV_BF16 desc describes them) receives
+ * the values of block src_blocks[i] of the quantised pools: a quantised prefix as
+ * pkv_prefill_attention_ragged reads it, or a sequence moved back to a bf16 cache.
+ * dst ids must be distinct.  An id out of range skips the pair and sets
+ * PKV_DEVERR_BLOCK_ID. */
+pkv_status pkv_quant_load_blocks(const pkv_cache_desc *desc, const void *k_pool, const void *v_pool,
+                                 const float *k_scale, const float *v_scale,
+                                 const int32_t *src_blocks, const int32_t *dst_blocks,
+                                 int32_t num_pairs, int64_t dst_num_blocks, void *k_cache,
+                                 void *v_cache, pkv_stream_t stream);
+
+/* Decode attention over quantised pools: pkv_decode_attention's computation and
+ * arguments, with k and v the pools' values.  context_lens[s] may be 0 (o = 0, lse
+ * = -inf, or the sink's logit).  The MMAs take f16 operands: the codes (with their
+ * 16-dim scales, 4-bit) exactly, q scaled by a power of two into f16's range, and
+ * the softmax weights rounded to f16; sums and softmax statistics are fp32.
+ *   chunk_blocks: blocks per chunk; 0 lets the planner choose, else 1..512; a
+ *                 context is cut into at most 512 chunks.
+ *   workspace   : >= pkv_quant_decode_workspace_size(...) bytes, 256-byte aligned,
+ *                 zero-filled before its first use; every call leaves its tickets
+ *                 zeroed.  Calls that share a workspace must not overlap on the GPU. */
+pkv_status pkv_quant_decode(const pkv_cache_desc *desc, const void *q, const void *k_pool,
+                            const void *v_pool, const float *k_scale, const float *v_scale,
+                            const int32_t *block_tables, const int32_t *context_lens,
+                            int32_t num_seqs, int32_t max_context_len, float sm_scale,
+                            int32_t window, const float *sinks, int32_t chunk_blocks, void *out,
+                            float *lse_out, void *workspace, size_t workspace_bytes,
+                            pkv_stream_t stream);
+
+/* Host: workspace bytes pkv_quant_decode needs; 0 when it needs none or the
+ * arguments are invalid. */
+size_t pkv_quant_decode_workspace_size(const pkv_cache_desc *desc, int32_t num_seqs,
+                                       int32_t max_context_len, int32_t window,
+                                       int32_t chunk_blocks);
 
 /* ---- diagnostics --------------------------------------------------------- */
 

@@ -22,6 +22,11 @@ from . import build as _build
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
+KV_INT8 = 2  # quantised pools, records with a scale per row: the pkv_quant_* calls
+KV_FP4 = 3   # quantised pools, records with a scale per 16 dims: likewise
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+ROPE_INVERSE = 0x1  # Rope.flags: turn by the negative angle
 DESC_PREFETCH_KV = 0x1  # pkv_cache_desc.flags: see PKV_DESC_PREFETCH_KV in pkv.h
 DESC_INDEPENDENT = 0x2  # pkv_cache_desc.flags: see PKV_DESC_INDEPENDENT in pkv.h
 DEVERR_BLOCK_ID = 0x1
@@ -55,10 +60,35 @@ def make_desc(*, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per
               kv_dtype=KV_BF16, block_size=16, ring_blocks=0, flags=0) -> CacheDesc:
     """flags: DESC_PREFETCH_KV (see pkv.h) or 0."""
     if isinstance(kv_dtype, str):
-        kv_dtype = KV_FP8_E4M3 if kv_dtype.startswith("fp8") else KV_BF16
+        kv_dtype = {"int8": KV_INT8, "fp4": KV_FP4}.get(
+            kv_dtype, KV_FP8_E4M3 if kv_dtype.startswith("fp8") else KV_BF16)
     return CacheDesc(int(num_q_heads), int(num_kv_heads), int(head_dim), int(block_size),
                      int(kv_dtype), int(max_blocks_per_seq), int(num_blocks), int(ring_blocks),
                      int(flags))
+
+
+class Rope(ctypes.Structure):
+    """pkv_rope; keeps its table alive (see make_rope)."""
+
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("max_pos", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class Rows(ctypes.Structure):
+    """pkv_rows."""
+
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("in_token_stride", ctypes.c_int64), ("in_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("num_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    """pkv_rope_scaling."""
+
+    _fields_ = [("kind", ctypes.c_int32), ("original_max_pos", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("low_freq", ctypes.c_double),
+                ("high_freq", ctypes.c_double), ("attention", ctypes.c_double)]
 
 
 _lock = threading.Lock()
@@ -111,6 +141,16 @@ def load_library():
             "pkv_prefill_ring_commit": (ctypes.c_int, [D, P, P, P, P, P, P, P, P, P, P, i32, i32, P, P,
                                                        f32, i32, P, P, P, ctypes.c_size_t, P]),
             "pkv_prefill_ring_workspace_size": (ctypes.c_size_t, [D, i32, i32, i32]),
+            "pkv_rope_rotate": (ctypes.c_int, [P, i32, P, i32, i32, P, P, P]),
+            "pkv_rope_scaled_table": (ctypes.c_int, [f32, i32, i32, P, P]),
+            "pkv_quant_cache_bytes": (ctypes.c_uint64, [D]),
+            "pkv_quant_append": (ctypes.c_int, [D, P, P, P, P, P, P, i32, P, P, i32, P, P, i64, P, P,
+                                                i64, i64, P]),
+            "pkv_quant_read": (ctypes.c_int, [D, P, P, P, P, P, i32, P, P, i32, i32, P, P, P]),
+            "pkv_quant_load_blocks": (ctypes.c_int, [D, P, P, P, P, P, P, i32, i64, P, P, P]),
+            "pkv_quant_decode": (ctypes.c_int, [D, P, P, P, P, P, P, P, i32, i32, f32, i32, P, i32, P,
+                                                P, P, ctypes.c_size_t, P]),
+            "pkv_quant_decode_workspace_size": (ctypes.c_size_t, [D, i32, i32, i32, i32]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -351,6 +391,228 @@ def pkv_cascade_decode(desc, q, k_cache, v_cache, group_indptr, group_indptr_hos
         _stream(stream)))
 
 
+# ------------------------- rotary positions and the quantised pools --
+#
+# These calls check their tensors (type, device, layout) before the library
+# checks their sizes: a pool of the wrong kind is a ValueError, not a misread.
+
+def _arg(name, t, dtypes, shape=None, dense=True):
+    """t's address, after checking that t is a CUDA tensor on the current
+    device, of one of `dtypes`, contiguous unless told otherwise, and of
+    `shape` (None entries match any size)."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype not in dtypes:
+        raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s: on %s, expected the current CUDA device" % (name, t.device))
+    if dense and not t.is_contiguous():
+        raise ValueError("%s: tensor arguments must be contiguous" % name)
+    if shape is not None:
+        got = tuple(t.shape)
+        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+            raise ValueError("%s: shape %s, expected %s" % (name, got, shape))
+    return t.data_ptr()
+
+
+def _types():
+    """(bf16, fp32, int32, uint8) of torch, looked up on first use."""
+    global _types_cache
+    if _types_cache is None:
+        import torch
+        _types_cache = ((torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,))
+    return _types_cache
+
+
+_types_cache = None
+
+
+def make_rope(cos_sin, rotary_dim=None, layout="half", inverse=False) -> Rope:
+    """A rotation for pkv_rope_rotate and pkv_quant_append: cos_sin is the fp32
+    [max_pos][rotary_dim / 2][2] table on the GPU (pkv_rope_cos_sin_table,
+    pkv_rope_scaled_table), layout "half" or "interleaved"."""
+    layouts = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED, ROPE_HALF: ROPE_HALF,
+               ROPE_INTERLEAVED: ROPE_INTERLEAVED}
+    if layout not in layouts:
+        raise ValueError("rope layout %r" % (layout,))
+    if cos_sin.dim() != 3 or cos_sin.shape[2] != 2:
+        raise ValueError("cos_sin: shape %s, expected [max_pos][rotary_dim / 2][2]" % (tuple(cos_sin.shape),))
+    if rotary_dim is None:
+        rotary_dim = 2 * cos_sin.shape[1]
+    if rotary_dim != 2 * cos_sin.shape[1]:
+        raise ValueError("rotary_dim %d, but the table has %d pairs" % (rotary_dim, cos_sin.shape[1]))
+    r = Rope(_arg("cos_sin", cos_sin, _types()[1]), int(rotary_dim), layouts[layout],
+             int(cos_sin.shape[0]), ROPE_INVERSE if inverse else 0)
+    r.table = cos_sin
+    return r
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}
+
+
+def pkv_rope_scaled_table(theta, rotary_dim, max_pos, kind="none", factor=1.0, original_max_pos=0,
+                          low_freq=1.0, high_freq=0.0, attention=1.0) -> np.ndarray:
+    """Host fp32 [max_pos][rotary_dim/2][2] (cos, sin) table with the frequencies
+    scaled for long contexts; kind: one of ROPE_SCALINGS (see pkv.h).  high_freq
+    0 means 4 for "banded" and 32 for "yarn"."""
+    if kind not in ROPE_SCALINGS:
+        raise ValueError("rope scaling %r, expected one of %s" % (kind, sorted(ROPE_SCALINGS)))
+    if not high_freq:
+        high_freq = 32.0 if kind == "yarn" else 4.0
+    sc = RopeScaling(ROPE_SCALINGS[kind], int(original_max_pos), float(factor), float(low_freq),
+                     float(high_freq), float(attention))
+    out = np.empty((max(0, int(max_pos)), max(0, int(rotary_dim)) // 2, 2), dtype=np.float32)
+    _check(load_library().pkv_rope_scaled_table(float(theta), int(rotary_dim), int(max_pos),
+                                                ctypes.byref(sc), _ptr(out)))
+    return out
+
+
+def _rope_rows(name, x, out, dtypes, num_tokens):
+    if x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError("%s: expected [tokens][heads][head_dim] with contiguous dims" % name)
+    if x.shape[0] != num_tokens:
+        raise ValueError("%s: %d tokens, but %d positions" % (name, x.shape[0], num_tokens))
+    if out is None:
+        out = x
+    elif out.shape != x.shape or (out.shape[2] > 1 and out.stride(2) != 1):
+        raise ValueError("%s_out: expected %s's shape, with contiguous dims" % (name, name))
+    return Rows(_arg(name, x, dtypes, dense=False), _arg(name + "_out", out, (x.dtype,), dense=False),
+                x.stride(0), x.stride(1), out.stride(0), out.stride(1), x.shape[1], 0)
+
+
+def pkv_rope_rotate(rope, positions, q, q_out=None, k=None, k_out=None, stream=None):
+    """Rotate [tokens][heads][head_dim] rows (bf16, f16 or f32; any token and
+    head strides) of q and k at int32 positions; without an out, in place.
+    With make_rope(..., inverse=True) it is the rotation's transpose: the
+    gradient of q from the gradient of its rotated rows."""
+    import torch
+    codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    n = positions.shape[0]
+    rows = _rope_rows("q", q, q_out, tuple(codes), n)
+    krows = None
+    if k is not None:
+        if k.dtype != q.dtype or k.shape[2] != q.shape[2]:
+            raise ValueError("k: expected q's dtype and head_dim")
+        krows = _rope_rows("k", k, k_out, (q.dtype,), n)
+    _check(load_library().pkv_rope_rotate(
+        ctypes.byref(rope), codes[q.dtype], _arg("positions", positions, _types()[2], (n,)), n,
+        q.shape[2], ctypes.byref(rows), None if krows is None else ctypes.byref(krows),
+        _stream(stream)))
+
+
+def pkv_quant_cache_bytes(desc: CacheDesc) -> int:
+    """Bytes of one quantised pool: [num_blocks][Hkv][pkv_quant_record_bytes]."""
+    return int(load_library().pkv_quant_cache_bytes(ctypes.byref(desc)))
+
+
+def pkv_quant_record_bytes(desc: CacheDesc) -> int:
+    """Bytes of one (block, KV head) record; a pool is a uint8 tensor
+    [num_blocks][num_kv_heads][this]."""
+    d = desc.head_dim
+    return 16 * d + 64 if desc.kv_dtype == KV_INT8 else 9 * d
+
+
+def _quant_pools(desc, k_pool, v_pool, k_scale, v_scale):
+    bf16, f32, i32, u8 = _types()
+    shape = (desc.num_blocks, desc.num_kv_heads, pkv_quant_record_bytes(desc))
+    return (_arg("k_pool", k_pool, u8, shape), _arg("v_pool", v_pool, u8, shape),
+            _arg("k_scale", k_scale, f32, (desc.num_kv_heads,)),
+            _arg("v_scale", v_scale, f32, (desc.num_kv_heads,)))
+
+
+def _token_rows(name, x, heads, dim, num_tokens):
+    """[tokens][heads][dim] bf16 rows whose heads are contiguous: (address, token stride)."""
+    at = _arg(name, x, _types()[0], (num_tokens, heads, dim), dense=False)
+    if (dim > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != dim):
+        raise ValueError("%s: a token's heads must be contiguous" % name)
+    return at, (x.stride(0) if num_tokens > 1 else heads * dim)
+
+
+def pkv_quant_append(desc, k_pool, v_pool, block_tables, token_to_seq, positions, k_new, v_new,
+                     q=None, q_out=None, rope=None, k_scale=None, v_scale=None, stream=None):
+    """Quantise the new tokens' K (rotated) and V into their slots, and rotate q
+    into q_out (None: in place).  k_new, v_new and q may be views into one packed
+    QKV buffer.  token_to_seq < 0 marks a padding token."""
+    i32 = _types()[2]
+    n, hkv, dim = positions.shape[0], desc.num_kv_heads, desc.head_dim
+    kp, vp, ks, vs = _quant_pools(desc, k_pool, v_pool, k_scale, v_scale)
+    k_at, k_stride = _token_rows("k_new", k_new, hkv, dim, n)
+    v_at, v_stride = _token_rows("v_new", v_new, hkv, dim, n)
+    if k_stride != v_stride:
+        raise ValueError("k_new and v_new: token strides %d and %d differ" % (k_stride, v_stride))
+    q_at = qo_at = None
+    q_stride = qo_stride = 0
+    if q is not None:
+        q_at, q_stride = _token_rows("q", q, desc.num_q_heads, dim, n)
+        qo_at, qo_stride = (q_at, q_stride) if q_out is None else \
+            _token_rows("q_out", q_out, desc.num_q_heads, dim, n)
+    _check(load_library().pkv_quant_append(
+        ctypes.byref(desc), None if rope is None else ctypes.byref(rope), kp, vp, ks, vs,
+        _arg("block_tables", block_tables, i32, (None, desc.max_blocks_per_seq)),
+        block_tables.shape[0], _arg("token_to_seq", token_to_seq, i32, (n,)),
+        _arg("positions", positions, i32, (n,)), n, k_at, v_at, k_stride, q_at, qo_at, q_stride,
+        qo_stride, _stream(stream)))
+
+
+def pkv_quant_read(desc, k_pool, v_pool, block_tables, token_to_seq, positions, k_out=None,
+                   v_out=None, k_scale=None, v_scale=None, stream=None):
+    """Read the rows at (token_to_seq, positions) back as bf16 or fp32
+    [tokens][Hkv][D]; either output may be None."""
+    bf16, f32, i32, _ = _types()
+    n = positions.shape[0]
+    kp, vp, ks, vs = _quant_pools(desc, k_pool, v_pool, k_scale, v_scale)
+    if k_out is None and v_out is None:
+        raise ValueError("k_out or v_out is needed")
+    out = k_out if k_out is not None else v_out
+    if k_out is not None and v_out is not None and k_out.dtype != v_out.dtype:
+        raise ValueError("k_out and v_out: one dtype")
+    shape = (n, desc.num_kv_heads, desc.head_dim)
+    _check(load_library().pkv_quant_read(
+        ctypes.byref(desc), kp, vp, ks, vs,
+        _arg("block_tables", block_tables, i32, (None, desc.max_blocks_per_seq)),
+        block_tables.shape[0], _arg("token_to_seq", token_to_seq, i32, (n,)),
+        _arg("positions", positions, i32, (n,)), n, 2 if out.dtype == f32[0] else 0,
+        _arg("k_out", k_out, bf16 + f32, shape), _arg("v_out", v_out, bf16 + f32, shape),
+        _stream(stream)))
+
+
+def pkv_quant_load_blocks(desc, k_pool, v_pool, src_blocks, dst_blocks, k_cache, v_cache,
+                          k_scale=None, v_scale=None, stream=None):
+    """Block dst_blocks[i] of the bf16 pools [blocks][Hkv][16][D] receives the
+    values of block src_blocks[i] of the quantised pools."""
+    bf16, _, i32, _ = _types()
+    n = src_blocks.shape[0]
+    kp, vp, ks, vs = _quant_pools(desc, k_pool, v_pool, k_scale, v_scale)
+    shape = (k_cache.shape[0], desc.num_kv_heads, desc.block_size, desc.head_dim)
+    _check(load_library().pkv_quant_load_blocks(
+        ctypes.byref(desc), kp, vp, ks, vs, _arg("src_blocks", src_blocks, i32, (n,)),
+        _arg("dst_blocks", dst_blocks, i32, (n,)), n, shape[0], _arg("k_cache", k_cache, bf16, shape),
+        _arg("v_cache", v_cache, bf16, shape), _stream(stream)))
+
+
+def pkv_quant_decode_workspace_size(desc, num_seqs, max_context_len, window=-1, chunk_blocks=0) -> int:
+    return int(load_library().pkv_quant_decode_workspace_size(
+        ctypes.byref(desc), int(num_seqs), int(max_context_len), int(window), int(chunk_blocks)))
+
+
+def pkv_quant_decode(desc, q, k_pool, v_pool, block_tables, context_lens, max_context_len, sm_scale,
+                     out, lse=None, workspace=None, window=-1, chunk_blocks=0, k_scale=None,
+                     v_scale=None, sinks=None, stream=None):
+    """Decode attention (one query token per sequence) over quantised pools."""
+    bf16, f32, i32, u8 = _types()
+    n = context_lens.shape[0]
+    kp, vp, ks, vs = _quant_pools(desc, k_pool, v_pool, k_scale, v_scale)
+    shape = (n, desc.num_q_heads, desc.head_dim)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().pkv_quant_decode(
+        ctypes.byref(desc), _arg("q", q, bf16, shape), kp, vp, ks, vs,
+        _arg("block_tables", block_tables, i32, (n, desc.max_blocks_per_seq)),
+        _arg("context_lens", context_lens, i32), n, int(max_context_len), float(sm_scale), int(window),
+        _arg("sinks", sinks, f32, (desc.num_q_heads,)), int(chunk_blocks), _arg("out", out, bf16, shape),
+        _arg("lse", lse, f32, shape[:2]), _arg("workspace", workspace, u8), ws_bytes, _stream(stream)))
+
+
 def pkv_device_errors(reset: bool = True) -> int:
     """Synchronously read (and by default clear) the device error word."""
     v = ctypes.c_uint32()
@@ -370,4 +632,5 @@ def pkv_last_error() -> str:
 
 __all__ = [n for n in dir() if n.startswith("pkv_")] + [
     "CacheDesc", "make_desc", "PkvError", "load_library", "library_path", "KV_BF16",
-    "KV_FP8_E4M3", "BoundCall", "bind_decode_step"]
+    "KV_FP8_E4M3", "KV_INT8", "KV_FP4", "Rope", "make_rope", "ROPE_HALF", "ROPE_INTERLEAVED",
+    "ROPE_INVERSE", "ROPE_SCALINGS", "BoundCall", "bind_decode_step"]

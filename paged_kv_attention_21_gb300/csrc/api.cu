@@ -217,7 +217,9 @@ constexpr int kClusterSplits = 4;  // the decode kernel's cluster-merge limit
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-pkv_status check_desc(const pkv_cache_desc* d) {
+bool quantised(const pkv_cache_desc* d) { return d->kv_dtype == PKV_KV_INT8 || d->kv_dtype == PKV_KV_FP4; }
+
+pkv_status check_shape(const pkv_cache_desc* d) {
     if (!d) return fail(PKV_ERR_INVALID_ARG, "desc is NULL");
     if (d->num_q_heads <= 0 || d->num_kv_heads <= 0)
         return fail(PKV_ERR_INVALID_ARG, "head counts must be positive (Hq=%d, Hkv=%d)",
@@ -231,7 +233,7 @@ pkv_status check_desc(const pkv_cache_desc* d) {
     if (d->head_dim != 64 && d->head_dim != 128)
         return fail(PKV_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", d->head_dim);
     if (d->block_size != 16) return fail(PKV_ERR_UNSUPPORTED, "block_size %d (supported: 16)", d->block_size);
-    if (d->kv_dtype != PKV_KV_BF16 && d->kv_dtype != PKV_KV_FP8_E4M3)
+    if (d->kv_dtype != PKV_KV_BF16 && d->kv_dtype != PKV_KV_FP8_E4M3 && !quantised(d))
         return fail(PKV_ERR_UNSUPPORTED, "kv_dtype %d", d->kv_dtype);
     if (d->num_blocks <= 0 || d->num_blocks > 0x7FFFFFFFLL)
         return fail(PKV_ERR_INVALID_ARG, "num_blocks %lld out of range", (long long)d->num_blocks);
@@ -242,6 +244,27 @@ pkv_status check_desc(const pkv_cache_desc* d) {
                     d->max_blocks_per_seq);
     if (d->flags & ~(PKV_DESC_PREFETCH_KV | PKV_DESC_INDEPENDENT))
         return fail(PKV_ERR_INVALID_ARG, "unknown desc flags 0x%x", d->flags);
+    return PKV_OK;
+}
+
+// bf16 and e4m3 pools, for every entry point but the quantised pools' own.
+pkv_status check_desc(const pkv_cache_desc* d) {
+    const pkv_status st = check_shape(d);
+    if (st != PKV_OK) return st;
+    if (quantised(d))
+        return fail(PKV_ERR_UNSUPPORTED, "kv_dtype %d: the pkv_quant_* calls take quantised pools", d->kv_dtype);
+    return PKV_OK;
+}
+
+pkv_status check_quant_desc(const pkv_cache_desc* d, const float* k_scale, const float* v_scale) {
+    const pkv_status st = check_shape(d);
+    if (st != PKV_OK) return st;
+    if (!quantised(d))
+        return fail(PKV_ERR_UNSUPPORTED, "kv_dtype %d is not a quantised pool's (PKV_KV_INT8, PKV_KV_FP4)", d->kv_dtype);
+    if (d->kv_dtype == PKV_KV_FP4 && (!k_scale || !v_scale))
+        return fail(PKV_ERR_INVALID_ARG, "4-bit pools need k_scale and v_scale");
+    if (d->kv_dtype == PKV_KV_INT8 && (k_scale || v_scale))
+        return fail(PKV_ERR_INVALID_ARG, "int8 pools hold their scales: k_scale and v_scale must be NULL");
     return PKV_OK;
 }
 
@@ -988,7 +1011,7 @@ pkv_status pkv_copy_blocks(const pkv_cache_desc* desc, void* k_cache, void* v_ca
                            const int32_t* src_blocks, const int32_t* dst_blocks, int32_t num_pairs,
                            pkv_stream_t stream) {
     g_last_error[0] = 0;
-    pkv_status st = check_desc(desc);
+    pkv_status st = check_shape(desc);
     if (st != PKV_OK) return st;
     if (num_pairs < 0 || num_pairs > 0x7FFFFFFF / 2) return fail(PKV_ERR_INVALID_ARG, "num_pairs %d", num_pairs);
     if (num_pairs == 0) return PKV_OK;
@@ -1006,7 +1029,9 @@ pkv_status pkv_copy_blocks(const pkv_cache_desc* desc, void* k_cache, void* v_ca
     a.dst = dst_blocks;
     a.num_pairs = num_pairs;
     a.num_blocks = desc->num_blocks;
-    a.block_bytes = int64_t(desc->num_kv_heads) * desc->block_size * desc->head_dim * elem_bytes(desc);
+    a.block_bytes = quantised(desc)
+                        ? int64_t(desc->num_kv_heads) * pkv::quant_record_bytes(desc->head_dim, desc->kv_dtype == PKV_KV_FP4)
+                        : int64_t(desc->num_kv_heads) * desc->block_size * desc->head_dim * elem_bytes(desc);
     a.err = err;
     cudaError_t e = pkv::launch_copy_blocks(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "copy launch");
@@ -1370,3 +1395,358 @@ extern "C" pkv_status pkv_decode_attention_static(
                        max_context_len, sm_scale, window, sinks, chunk_blocks, out, lse_out, nullptr, 0,
                        stream, nullptr, Scratch::kStatic);
 }
+
+// ============================== rotary positions and the quantised pools ==
+
+namespace {
+
+pkv_status check_rope(const pkv_rope* r, int head_dim) {
+    if (!r->cos_sin) return fail(PKV_ERR_INVALID_ARG, "rope cos_sin is NULL");
+    if (!aligned(r->cos_sin, 8)) return fail(PKV_ERR_INVALID_ARG, "rope cos_sin must be 8-byte aligned");
+    if (r->rotary_dim < 2 || r->rotary_dim % 2 || r->rotary_dim > head_dim)
+        return fail(PKV_ERR_INVALID_ARG, "rotary_dim %d: even, 2 .. head_dim = %d", r->rotary_dim, head_dim);
+    if (r->layout != PKV_ROPE_HALF && r->layout != PKV_ROPE_INTERLEAVED)
+        return fail(PKV_ERR_INVALID_ARG, "rope layout %d", r->layout);
+    if (r->max_pos <= 0) return fail(PKV_ERR_INVALID_ARG, "rope max_pos must be positive");
+    if (r->flags & ~PKV_ROPE_INVERSE) return fail(PKV_ERR_INVALID_ARG, "unknown rope flags 0x%x", r->flags);
+    return PKV_OK;
+}
+
+// Strided rows of `elem`-byte elements; out rows may not overlap one another,
+// and out is in with the same strides or away from it.
+pkv_status check_rows(const pkv_rows* r, const char* name, int64_t tokens, int64_t d, int64_t elem) {
+    if (r->num_heads < 0) return fail(PKV_ERR_INVALID_ARG, "%s: num_heads %d", name, r->num_heads);
+    if (r->num_heads == 0) return PKV_OK;
+    if (!r->in || !r->out) return fail(PKV_ERR_INVALID_ARG, "%s: null device pointer", name);
+    if (!aligned(r->in, size_t(elem)) || !aligned(r->out, size_t(elem)))
+        return fail(PKV_ERR_INVALID_ARG, "%s: rows must be aligned to their element", name);
+    constexpr int64_t kMost = int64_t(1) << 40;
+    for (int64_t s : {r->in_token_stride, r->in_head_stride, r->out_token_stride, r->out_head_stride})
+        if (s < 0 || s > kMost) return fail(PKV_ERR_INVALID_ARG, "%s: stride %lld", name, (long long)s);
+    const int64_t h = r->num_heads;
+    const int64_t tspan = (tokens - 1) * r->out_token_stride, hspan = (h - 1) * r->out_head_stride;
+    const bool heads_inside = (h == 1 || r->out_head_stride >= d) && (tokens == 1 || r->out_token_stride >= hspan + d);
+    const bool tokens_inside = (tokens == 1 || r->out_token_stride >= d) && (h == 1 || r->out_head_stride >= tspan + d);
+    if (!heads_inside && !tokens_inside) return fail(PKV_ERR_INVALID_ARG, "%s: out rows overlap", name);
+    const bool same = r->in == r->out && (tokens == 1 || r->in_token_stride == r->out_token_stride) &&
+                      (h == 1 || r->in_head_stride == r->out_head_stride);
+    const uintptr_t i0 = reinterpret_cast<uintptr_t>(r->in), o0 = reinterpret_cast<uintptr_t>(r->out);
+    const uintptr_t i1 = i0 + uintptr_t(((tokens - 1) * r->in_token_stride + (h - 1) * r->in_head_stride + d) * elem);
+    const uintptr_t o1 = o0 + uintptr_t((tspan + hspan + d) * elem);
+    // extents that meet under other strides could write what is still to be read
+    if (!same && i0 < o1 && o0 < i1) return fail(PKV_ERR_INVALID_ARG, "%s: out overlaps in with other strides", name);
+    return PKV_OK;
+}
+
+pkv::RotateRows rotate_rows(const pkv_rows* r) {
+    return pkv::RotateRows{r->in, r->out, r->in_token_stride, r->in_head_stride, r->out_token_stride,
+                           r->out_head_stride, r->num_heads};
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_rope_scaled_table(float theta, int32_t rotary_dim, int32_t max_pos,
+                                 const pkv_rope_scaling* scaling, float* host_out) {
+    g_last_error[0] = 0;
+    if (!host_out || !scaling) return fail(PKV_ERR_INVALID_ARG, "null host pointer");
+    if (rotary_dim < 2 || rotary_dim % 2 || max_pos < 0 || !(theta > 1.f) || !std::isfinite(theta))
+        return fail(PKV_ERR_INVALID_ARG, "bad rope table shape (dim=%d, max_pos=%d, theta=%g)", rotary_dim, max_pos,
+                    double(theta));
+    const pkv_rope_scaling& sc = *scaling;
+    if (sc.kind < PKV_ROPE_SCALE_NONE || sc.kind > PKV_ROPE_SCALE_YARN)
+        return fail(PKV_ERR_INVALID_ARG, "rope scaling kind %d", sc.kind);
+    if (!(sc.attention > 0.0) || !std::isfinite(sc.attention))
+        return fail(PKV_ERR_INVALID_ARG, "rope scaling attention %g", sc.attention);
+    if (sc.kind != PKV_ROPE_SCALE_NONE && (!(sc.factor >= 1.0) || !std::isfinite(sc.factor)))
+        return fail(PKV_ERR_INVALID_ARG, "rope scaling factor %g", sc.factor);
+    if (sc.kind == PKV_ROPE_SCALE_NTK && rotary_dim == 2)
+        return fail(PKV_ERR_INVALID_ARG, "ntk scaling needs rotary_dim > 2");
+    if (sc.kind >= PKV_ROPE_SCALE_BANDED &&
+        (sc.original_max_pos <= 0 || !(sc.low_freq > 0.0) || !(sc.high_freq > sc.low_freq) || !std::isfinite(sc.high_freq)))
+        return fail(PKV_ERR_INVALID_ARG, "rope scaling bands: original_max_pos %d, low %g, high %g", sc.original_max_pos,
+                    sc.low_freq, sc.high_freq);
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    const int half = rotary_dim / 2;
+    const double r = rotary_dim, base = theta, L = sc.original_max_pos;
+    double lo = 0.0, hi = 0.0;
+    if (sc.kind == PKV_ROPE_SCALE_YARN) {
+        auto dim_of = [&](double turns) { return r * std::log(L / (kTwoPi * turns)) / (2.0 * std::log(base)); };
+        lo = std::min(std::max(std::floor(dim_of(sc.high_freq)), 0.0), r - 1.0);
+        hi = std::min(std::max(std::ceil(dim_of(sc.low_freq)), 0.0), r - 1.0);
+        if (hi == lo) hi += 0.001;
+    }
+    for (int j = 0; j < half; ++j) {
+        double f = std::pow(base, -(2.0 * j) / r);
+        if (sc.kind == PKV_ROPE_SCALE_LINEAR) {
+            f /= sc.factor;
+        } else if (sc.kind == PKV_ROPE_SCALE_NTK) {
+            f = std::pow(base * std::pow(sc.factor, r / (r - 2.0)), -(2.0 * j) / r);
+        } else if (sc.kind == PKV_ROPE_SCALE_BANDED) {
+            const double wave = kTwoPi / f;
+            const double m = std::min(std::max((L / wave - sc.low_freq) / (sc.high_freq - sc.low_freq), 0.0), 1.0);
+            f = (1.0 - m) * f / sc.factor + m * f;
+        } else if (sc.kind == PKV_ROPE_SCALE_YARN) {
+            const double g = 1.0 - std::min(std::max((j - lo) / (hi - lo), 0.0), 1.0);
+            f = (1.0 - g) * f / sc.factor + g * f;
+        }
+        for (int p = 0; p < max_pos; ++p) {
+            const double ang = double(p) * f;
+            host_out[(size_t(p) * half + j) * 2 + 0] = float(std::cos(ang) * sc.attention);
+            host_out[(size_t(p) * half + j) * 2 + 1] = float(std::sin(ang) * sc.attention);
+        }
+    }
+    return PKV_OK;
+}
+
+pkv_status pkv_rope_rotate(const pkv_rope* rope, int32_t dtype, const int32_t* positions, int32_t num_tokens,
+                           int32_t head_dim, const pkv_rows* q, const pkv_rows* k, pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    if (!rope || !q) return fail(PKV_ERR_INVALID_ARG, "rope or q is NULL");
+    if (dtype != PKV_BF16 && dtype != PKV_F16 && dtype != PKV_F32) return fail(PKV_ERR_UNSUPPORTED, "dtype %d", dtype);
+    if (head_dim < 2 || head_dim > 512 || head_dim % 2) return fail(PKV_ERR_UNSUPPORTED, "head_dim %d: even, 2 .. 512", head_dim);
+    pkv_status st = check_rope(rope, head_dim);
+    if (st != PKV_OK) return st;
+    if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens < 0");
+    if (num_tokens == 0) return PKV_OK;
+    if (!positions) return fail(PKV_ERR_INVALID_ARG, "null device pointer");
+    const int64_t elem = dtype == PKV_F32 ? 4 : 2;
+    st = check_rows(q, "q", num_tokens, head_dim, elem);
+    if (st != PKV_OK) return st;
+    if (k) {
+        st = check_rows(k, "k", num_tokens, head_dim, elem);
+        if (st != PKV_OK) return st;
+    }
+    pkv::RotateArgs a{};
+    a.q = rotate_rows(q);
+    if (k) a.k = rotate_rows(k);
+    if (a.q.num_heads + int64_t(a.k.num_heads) > 65536) return fail(PKV_ERR_UNSUPPORTED, "more than 65536 heads");
+    if (a.q.num_heads + a.k.num_heads == 0) return PKV_OK;
+    st = device_state(&a.err, nullptr);
+    if (st != PKV_OK) return st;
+    a.cos_sin = rope->cos_sin;
+    a.positions = positions;
+    a.num_tokens = num_tokens;
+    a.d = head_dim;
+    a.rotary = rope->rotary_dim;
+    a.interleaved = rope->layout == PKV_ROPE_INTERLEAVED;
+    a.inverse = (rope->flags & PKV_ROPE_INVERSE) ? 1 : 0;
+    a.max_pos = rope->max_pos;
+    a.dtype = dtype;
+    const cudaError_t e = pkv::launch_rope_rotate(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+    return PKV_OK;
+}
+
+uint64_t pkv_quant_cache_bytes(const pkv_cache_desc* desc) {
+    if (check_shape(desc) != PKV_OK || !quantised(desc)) return 0;
+    return uint64_t(desc->num_blocks) * desc->num_kv_heads *
+           pkv::quant_record_bytes(desc->head_dim, desc->kv_dtype == PKV_KV_FP4);
+}
+
+}  // extern "C"
+
+namespace {
+
+pkv_status quant_args(const pkv_cache_desc* desc, const void* k_pool, const void* v_pool, const float* k_scale,
+                      const float* v_scale, pkv_stream_t stream, pkv::QuantArgs* a) {
+    *a = pkv::QuantArgs{};
+    const pkv_status st = device_state(&a->err, nullptr);
+    if (st != PKV_OK) return st;
+    a->k_pool = const_cast<void*>(k_pool);
+    a->v_pool = const_cast<void*>(v_pool);
+    a->k_scale = k_scale;
+    a->v_scale = v_scale;
+    a->num_blocks = desc->num_blocks;
+    a->hq = desc->num_q_heads;
+    a->hkv = desc->num_kv_heads;
+    a->d = desc->head_dim;
+    a->fp4 = desc->kv_dtype == PKV_KV_FP4 ? 1 : 0;
+    a->mbps = desc->max_blocks_per_seq;
+    a->ring = desc->ring_blocks;
+    a->stream = reinterpret_cast<cudaStream_t>(stream);
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_quant_append(const pkv_cache_desc* desc, const pkv_rope* rope, void* k_pool, void* v_pool,
+                            const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                            int32_t num_seqs, const int32_t* token_to_seq, const int32_t* positions,
+                            int32_t num_tokens, const void* k_new, const void* v_new, int64_t new_token_stride,
+                            const void* q, void* q_out, int64_t q_token_stride, int64_t q_out_token_stride,
+                            pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    pkv_status st = check_quant_desc(desc, k_scale, v_scale);
+    if (st != PKV_OK) return st;
+    if (rope && (st = check_rope(rope, desc->head_dim)) != PKV_OK) return st;
+    if (num_tokens < 0 || num_seqs < 0) return fail(PKV_ERR_INVALID_ARG, "negative count");
+    if (num_tokens == 0) return PKV_OK;
+    if (!k_pool || !v_pool || !block_tables || !token_to_seq || !positions || !k_new || !v_new || (q && !q_out))
+        return fail(PKV_ERR_INVALID_ARG, "null device pointer");
+    if (q && !rope) return fail(PKV_ERR_INVALID_ARG, "q is given without a rotation");
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+        (q && (!aligned(q, 16) || !aligned(q_out, 16))))
+        return fail(PKV_ERR_INVALID_ARG, "the pools, k_new, v_new, q and q_out must be 16-byte aligned");
+    const int64_t kvrow = int64_t(desc->num_kv_heads) * desc->head_dim, qrow = int64_t(desc->num_q_heads) * desc->head_dim;
+    if (new_token_stride % 8 || new_token_stride < kvrow)
+        return fail(PKV_ERR_INVALID_ARG, "new_token_stride %lld: a multiple of 8, at least %lld", (long long)new_token_stride,
+                    (long long)kvrow);
+    if (q && (q_token_stride % 8 || q_out_token_stride % 8 || q_token_stride < qrow || q_out_token_stride < qrow))
+        return fail(PKV_ERR_INVALID_ARG, "q token strides %lld, %lld: multiples of 8, at least %lld",
+                    (long long)q_token_stride, (long long)q_out_token_stride, (long long)qrow);
+    if (q && q == q_out && q_token_stride != q_out_token_stride)
+        return fail(PKV_ERR_INVALID_ARG, "q in place needs one token stride");
+    pkv::QuantArgs a;
+    st = quant_args(desc, k_pool, v_pool, k_scale, v_scale, stream, &a);
+    if (st != PKV_OK) return st;
+    a.block_tables = block_tables;
+    a.token_to_seq = token_to_seq;
+    a.positions = positions;
+    a.num_tokens = num_tokens;
+    a.num_seqs = num_seqs;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.new_stride = new_token_stride;
+    a.q = q;
+    a.q_out = q_out;
+    a.q_stride = q_token_stride;
+    a.q_out_stride = q_out_token_stride;
+    if (rope) {
+        a.cos_sin = rope->cos_sin;
+        a.rotary = rope->rotary_dim;
+        a.interleaved = rope->layout == PKV_ROPE_INTERLEAVED;
+        a.inverse = (rope->flags & PKV_ROPE_INVERSE) ? 1 : 0;
+        a.max_pos = rope->max_pos;
+    }
+    const cudaError_t e = pkv::launch_quant_append(a);
+    if (e != cudaSuccess) return cuda_fail(e, "quantising append launch");
+    return PKV_OK;
+}
+
+pkv_status pkv_quant_read(const pkv_cache_desc* desc, const void* k_pool, const void* v_pool, const float* k_scale,
+                          const float* v_scale, const int32_t* block_tables, int32_t num_seqs,
+                          const int32_t* token_to_seq, const int32_t* positions, int32_t num_tokens,
+                          int32_t out_dtype, void* k_out, void* v_out, pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    pkv_status st = check_quant_desc(desc, k_scale, v_scale);
+    if (st != PKV_OK) return st;
+    if (out_dtype != PKV_BF16 && out_dtype != PKV_F32) return fail(PKV_ERR_UNSUPPORTED, "out_dtype %d", out_dtype);
+    if (num_tokens < 0 || num_seqs < 0) return fail(PKV_ERR_INVALID_ARG, "negative count");
+    if (num_tokens == 0) return PKV_OK;
+    if (!block_tables || !token_to_seq || !positions || (!k_out && !v_out) || (k_out && !k_pool) || (v_out && !v_pool))
+        return fail(PKV_ERR_INVALID_ARG, "null device pointer");
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+        return fail(PKV_ERR_INVALID_ARG, "the pools and outputs must be 16-byte aligned");
+    pkv::QuantArgs a;
+    st = quant_args(desc, k_pool, v_pool, k_scale, v_scale, stream, &a);
+    if (st != PKV_OK) return st;
+    a.block_tables = block_tables;
+    a.token_to_seq = token_to_seq;
+    a.positions = positions;
+    a.num_tokens = num_tokens;
+    a.num_seqs = num_seqs;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
+    const cudaError_t e = pkv::launch_quant_read(a);
+    if (e != cudaSuccess) return cuda_fail(e, "quantised read launch");
+    return PKV_OK;
+}
+
+pkv_status pkv_quant_load_blocks(const pkv_cache_desc* desc, const void* k_pool, const void* v_pool,
+                                 const float* k_scale, const float* v_scale, const int32_t* src_blocks,
+                                 const int32_t* dst_blocks, int32_t num_pairs, int64_t dst_num_blocks, void* k_cache,
+                                 void* v_cache, pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    pkv_status st = check_quant_desc(desc, k_scale, v_scale);
+    if (st != PKV_OK) return st;
+    if (num_pairs < 0) return fail(PKV_ERR_INVALID_ARG, "num_pairs %d", num_pairs);
+    if (dst_num_blocks <= 0 || dst_num_blocks > 0x7FFFFFFFLL)
+        return fail(PKV_ERR_INVALID_ARG, "dst_num_blocks %lld out of range", (long long)dst_num_blocks);
+    if (num_pairs == 0) return PKV_OK;
+    if (!k_pool || !v_pool || !src_blocks || !dst_blocks || !k_cache || !v_cache)
+        return fail(PKV_ERR_INVALID_ARG, "null device pointer");
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return fail(PKV_ERR_INVALID_ARG, "the pools must be 16-byte aligned");
+    if (desc->num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", desc->num_kv_heads);
+    pkv::QuantArgs a;
+    st = quant_args(desc, k_pool, v_pool, k_scale, v_scale, stream, &a);
+    if (st != PKV_OK) return st;
+    a.src_blocks = src_blocks;
+    a.dst_blocks = dst_blocks;
+    a.num_tokens = num_pairs;
+    a.dst_num_blocks = dst_num_blocks;
+    a.k_out = k_cache;
+    a.v_out = v_cache;
+    const cudaError_t e = pkv::launch_quant_load(a);
+    if (e != cudaSuccess) return cuda_fail(e, "quantised block load launch");
+    return PKV_OK;
+}
+
+size_t pkv_quant_decode_workspace_size(const pkv_cache_desc* desc, int32_t num_seqs, int32_t max_context_len,
+                                       int32_t window, int32_t chunk_blocks) {
+    (void)desc;
+    (void)num_seqs;
+    (void)max_context_len;
+    (void)window;
+    (void)chunk_blocks;
+    return 0;
+}
+
+pkv_status pkv_quant_decode(const pkv_cache_desc* desc, const void* q, const void* k_pool, const void* v_pool,
+                            const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                            const int32_t* context_lens, int32_t num_seqs, int32_t max_context_len, float sm_scale,
+                            int32_t window, const float* sinks, int32_t chunk_blocks, void* out, float* lse_out,
+                            void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    pkv_status st = check_quant_desc(desc, k_scale, v_scale);
+    if (st != PKV_OK) return st;
+    if (num_seqs < 0 || num_seqs > 65535)
+        return fail(PKV_ERR_INVALID_ARG, "num_seqs %d out of range [0, 65535]", num_seqs);
+    if (desc->num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", desc->num_kv_heads);
+    if (num_seqs == 0) return PKV_OK;
+    if (!q || !k_pool || !v_pool || !block_tables || !context_lens || !out)
+        return fail(PKV_ERR_INVALID_ARG, "null device pointer");
+    st = check_ring_window(desc, window, max_context_len);
+    if (st != PKV_OK) return st;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16))
+        return fail(PKV_ERR_INVALID_ARG, "q, out and the pools must be 16-byte aligned");
+    if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return fail(PKV_ERR_INVALID_ARG, "sm_scale must be finite and > 0");
+    if (chunk_blocks < 0 || chunk_blocks > 512) return fail(PKV_ERR_INVALID_ARG, "chunk_blocks %d outside [0, 512]", chunk_blocks);
+    (void)workspace;
+    (void)workspace_bytes;
+    pkv::QuantDecodeArgs a{};
+    st = device_state(&a.err, nullptr);
+    if (st != PKV_OK) return st;
+    a.q = q;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.sinks = sinks;
+    a.out = out;
+    a.lse_out = lse_out;
+    a.num_blocks = desc->num_blocks;
+    a.num_seqs = num_seqs;
+    a.hq = desc->num_q_heads;
+    a.hkv = desc->num_kv_heads;
+    a.group = desc->num_q_heads / desc->num_kv_heads;
+    a.d = desc->head_dim;
+    a.fp4 = desc->kv_dtype == PKV_KV_FP4 ? 1 : 0;
+    a.mbps = desc->max_blocks_per_seq;
+    a.ring = desc->ring_blocks;
+    a.window = window;
+    a.max_ctx = max_context_len;
+    a.sm_scale = sm_scale;
+    const cudaError_t e = pkv::launch_quant_decode(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "quantised decode launch");
+    return PKV_OK;
+}
+
+}  // extern "C"

@@ -195,6 +195,71 @@ int prefill_tc_q_tile(int group);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                               const CUtensorMap& vmap, cudaStream_t stream);
 
+// Rotary positions over strided rows (rope_quant.cu).
+struct RotateRows {
+    const void* in;
+    void* out;
+    int64_t in_token, in_head, out_token, out_head;  // strides in elements
+    int32_t num_heads;
+};
+struct RotateArgs {
+    RotateRows q, k;  // k.num_heads == 0: q alone
+    const float* cos_sin;
+    const int32_t* positions;
+    int32_t num_tokens, d, rotary, interleaved, inverse, max_pos, dtype;
+    uint32_t* err;
+};
+cudaError_t launch_rope_rotate(const RotateArgs& a, cudaStream_t stream);
+
+// The quantised pools' append, row read and block widening (rope_quant.cu).
+struct QuantArgs {
+    void* k_pool;
+    void* v_pool;
+    const float* k_scale;  // 4-bit pools only
+    const float* v_scale;
+    const int32_t* block_tables;
+    const int32_t* token_to_seq;
+    const int32_t* positions;
+    const void* k_new;
+    const void* v_new;
+    const void* q;  // nullable
+    void* q_out;
+    void* k_out;  // read: rows; load: the bf16 pools
+    void* v_out;
+    const float* cos_sin;  // nullable
+    const int32_t* src_blocks;
+    const int32_t* dst_blocks;
+    int64_t new_stride, q_stride, q_out_stride;  // elements per token
+    int64_t num_blocks, dst_num_blocks;
+    int32_t num_tokens;  // load: pairs of blocks
+    int32_t num_seqs, hq, hkv, d, fp4, mbps, ring, rotary, interleaved, inverse, max_pos, out_f32;
+    uint32_t* err;
+    cudaStream_t stream;
+};
+cudaError_t launch_quant_append(const QuantArgs& a);
+cudaError_t launch_quant_read(const QuantArgs& a);
+cudaError_t launch_quant_load(const QuantArgs& a);
+int quant_record_bytes(int d, int fp4);
+
+// Decode attention over quantised pools (quant_decode.cu).
+struct QuantDecodeArgs {
+    const void* q;
+    const void* k_pool;
+    const void* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const float* sinks;  // nullable
+    void* out;
+    float* lse_out;  // nullable
+    int64_t num_blocks;
+    int32_t num_seqs, hq, hkv, group, d, fp4, mbps, ring, window, max_ctx;
+    float sm_scale;
+    uint32_t* err;
+};
+cudaError_t launch_quant_decode(const QuantDecodeArgs& a, cudaStream_t stream);
+
 // Tensor-map box shape used by the attention kernels for a pool:
 // innermost box extent in elements, and the swizzle.
 struct BoxShape {

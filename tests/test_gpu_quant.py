@@ -1,0 +1,497 @@
+"""The quantised pools on the GPU: append and read-back bit for bit, widening,
+decode attention against 64 bits, and a sequence served through all of them."""
+import numpy as np
+import pytest
+import torch
+
+import _quant as Q
+import paged_kv_attention_21_gb300 as pkv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def dev(x):
+    return None if x is None else torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def bf(x):
+    return torch.from_numpy(np.ascontiguousarray(x, np.float32)).bfloat16().to(DEV)
+
+
+def desc_of(fmt, hq, hkv, d, nb, mbps, ring=0):
+    return pkv.make_desc(num_q_heads=hq, num_kv_heads=hkv, head_dim=d, num_blocks=nb,
+                         max_blocks_per_seq=mbps, kv_dtype=fmt, ring_blocks=ring)
+
+
+# ------------------------------------------------------------ append, read --
+
+def expected_append(fmt, d, pools, tables, ring, tts, pos, k, v, scales, cs, layout):
+    """The pools after the append, from the definition, row by row."""
+    out = [p.copy() for p in pools]
+    for i, (s, p) in enumerate(zip(tts, pos)):
+        if s < 0:
+            continue
+        b = p // 16 % ring if ring else p // 16
+        kr = Q.rotate(k[i], cs[p], layout, np.float32) if cs is not None else k[i]
+        for which, rows in ((0, kr), (1, v[i])):
+            for h in range(rows.shape[0]):
+                g = 1.0 if scales[which] is None else scales[which][h]
+                Q.put_row(fmt, d, out[which][tables[s, b], h], p % 16, *Q.quantise(fmt, rows[h], g))
+    return out
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hq,hkv,d,r,layout,packed,ring", [
+    (8, 2, 64, 64, "half", False, 0), (16, 2, 128, 128, "half", True, 0), (5, 5, 128, 64, "interleaved", True, 0),
+    (16, 1, 64, 18, "half", False, 3), (3, 3, 128, 0, "half", True, 0), (4, 4, 64, 32, "interleaved", False, 0)])
+def test_append_is_the_definition_bit_for_bit(fmt, hq, hkv, d, r, layout, packed, ring):
+    rng = np.random.default_rng(hq * d + r)
+    lens = [1, 16, 17, 40, 3]
+    n = sum(lens)
+    nb, mbps = 16, max(3, ring)
+    tables = np.full((len(lens), mbps), -1, np.int32)
+    perm = iter(rng.permutation(nb))
+    for s, ln in enumerate(lens):
+        for b in range((ln + 15) // 16):
+            tables[s, b] = next(perm)
+    tts = np.repeat(np.arange(len(lens)), lens).astype(np.int32)
+    pos = np.concatenate([np.arange(ln) for ln in lens]).astype(np.int32)
+    if ring:  # far positions, each slot still its own
+        pos = pos + 16 * ring * 5
+    order = rng.permutation(n)
+    tts, pos = tts[order], pos[order]
+    tts[2] = -1  # padding
+    qkv = Q.bf16(rng.standard_normal((n, hq + 2 * hkv, d)) * np.exp(rng.standard_normal((n, hq + 2 * hkv, 1))))
+    qkv[0, hq] = 0.0            # a zero row
+    qkv[1, hq + hkv, :16] = 0.0  # a zero block of a row
+    qkv[3, hq, 5] = 1e-30
+    k, v = qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    scales = ((0.0017 * (1 + rng.random(hkv))).astype(np.float32),
+              (0.0017 * (1 + rng.random(hkv))).astype(np.float32)) if fmt == "fp4" else (None, None)
+    rec = Q.record_bytes(fmt, d)
+    pools = [rng.integers(0, 256, (nb, hkv, rec)).astype(np.uint8) for _ in range(2)]
+    cs = pkv.pkv_rope_scaled_table(1e4, r, 400, kind="yarn", factor=4.0, original_max_pos=100,
+                                   attention=1.1) if r else None
+    rope = pkv.make_rope(dev(cs), layout=layout) if r else None
+    buf = bf(qkv)
+    qd, kd, vd = buf[:, :hq], buf[:, hq:hq + hkv], buf[:, hq + hkv:]
+    if not packed:
+        qd, kd, vd = qd.contiguous(), kd.contiguous(), vd.contiguous()
+    gp = [dev(p) for p in pools]
+    qo = torch.full((n, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    dd = desc_of(fmt, hq, hkv, d, nb, mbps, ring)
+    ks, vs = (dev(s) for s in scales)
+    pkv.pkv_quant_append(dd, gp[0], gp[1], dev(tables), dev(tts), dev(pos), kd, vd,
+                         q=qd if r else None, q_out=qo if r else None, rope=rope, k_scale=ks, v_scale=vs)
+    ref = expected_append(fmt, d, pools, tables, ring, tts, pos, k, v, scales, cs, layout)
+    assert pkv.pkv_device_errors() == 0
+    for which in (0, 1):
+        assert np.array_equal(gp[which].cpu().numpy(), ref[which]), "pool %d" % which
+    if r:
+        want = np.stack([Q.rotate(qkv[i, :hq], cs[p], layout, np.float32) for i, p in enumerate(pos)])
+        want = torch.from_numpy(want).bfloat16()
+        want[2] = 7.0
+        assert torch.equal(qo.cpu(), want)
+        pkv.pkv_quant_append(dd, gp[0], gp[1], dev(tables), dev(tts), dev(pos), kd, vd, q=qd, rope=rope,
+                             k_scale=ks, v_scale=vs)  # q in place, the same bits
+        want[2] = torch.from_numpy(qkv[2, :hq]).bfloat16()
+        assert torch.equal(qd.cpu(), want)
+    # read back, both types, and one of the two alone
+    for dtype in (torch.float32, torch.bfloat16):
+        outs = [torch.full((n, hkv, d), 7.0, dtype=dtype, device=DEV) for _ in range(2)]
+        pkv.pkv_quant_read(dd, gp[0], gp[1], dev(tables), dev(tts), dev(pos), outs[0], outs[1],
+                           k_scale=ks, v_scale=vs)
+        alone = torch.empty_like(outs[1])
+        alone.fill_(7.0)
+        pkv.pkv_quant_read(dd, gp[0], gp[1], dev(tables), dev(tts), dev(pos), v_out=alone, k_scale=ks,
+                           v_scale=vs)
+        assert torch.equal(alone, outs[1])
+        for which in (0, 1):
+            vals = Q.pool_values(fmt, d, ref[which], np.ones(hkv) if scales[which] is None else scales[which])
+            b = pos // 16 % ring if ring else pos // 16
+            want = vals[tables[tts, b], :, pos % 16].astype(np.float32)  # the fp64 product, rounded once
+            want[2] = 7.0
+            assert torch.equal(outs[which].cpu(), torch.from_numpy(want).to(dtype))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+def test_append_of_values_that_are_not_finite_and_of_extremes(fmt):
+    d, nb = 64, 2
+    rows = np.zeros((12, d), np.float32)
+    rng = np.random.default_rng(1)
+    rows[:] = rng.standard_normal((12, d))
+    rows[0, 3] = np.nan
+    rows[1, 4], rows[1, 20] = np.inf, -np.inf
+    rows[2] = np.nan
+    rows[3] = np.inf
+    rows[4] = 3e38
+    rows[5] = 1e-38
+    rows[6] = 1e-40 * np.arange(d)
+    rows[7] = 0.0
+    rows[8] = -0.0
+    rows[9, 0] = 3.3e38
+    rows[10] *= 1e-20
+    rows[11] *= 1e20
+    rows = Q.bf16(rows)
+    tables = np.array([[1]], np.int32)
+    g = np.array([4 / 2688], np.float32) if fmt == "fp4" else None
+    pools = [np.zeros((nb, 1, Q.record_bytes(fmt, d)), np.uint8) for _ in range(2)]
+    tts, pos = np.zeros(12, np.int32), np.arange(12, dtype=np.int32)
+    gp = [dev(p) for p in pools]
+    pkv.pkv_quant_append(desc_of(fmt, 1, 1, d, nb, 1), gp[0], gp[1], dev(tables), dev(tts), dev(pos),
+                         bf(rows[:, None]), bf(rows[:, None]), k_scale=dev(g), v_scale=dev(g))
+    ref = expected_append(fmt, d, pools, tables, 0, tts, pos, rows[:, None], rows[:, None], (g, g), None, "half")
+    for which in (0, 1):
+        assert np.array_equal(gp[which].cpu().numpy(), ref[which])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+def test_bad_tokens_are_flagged_and_skipped(fmt):
+    d, hkv, nb = 128, 2, 3
+    dd = desc_of(fmt, 4, hkv, d, nb, 2)
+    tables = dev(np.array([[0, 5], [-1, 2]], np.int32))
+    tts = dev(np.array([2, 0, 0, 0, 1, -1, 1], np.int32))
+    pos = dev(np.array([0, 32, -1, 16, 0, 999, 17], np.int32))
+    x = torch.randn(7, hkv, d, device=DEV).bfloat16()
+    g = torch.full((hkv,), 0.002, device=DEV) if fmt == "fp4" else None
+    pools = [torch.zeros(nb, hkv, Q.record_bytes(fmt, d), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    pkv.pkv_quant_append(dd, pools[0], pools[1], tables, tts, pos, x, x, k_scale=g, v_scale=g)
+    assert pkv.pkv_device_errors() == pkv.DEVERR_POSITION | pkv.DEVERR_BLOCK_ID
+    for p in pools:
+        used = p.view(nb, -1).ne(0).any(1).tolist()
+        assert used == [False, False, True]
+    out = torch.full((7, hkv, d), 7.0, device=DEV)
+    pkv.pkv_quant_read(dd, pools[0], pools[1], tables, tts, pos, out, k_scale=g, v_scale=g)
+    assert pkv.pkv_device_errors() == pkv.DEVERR_POSITION | pkv.DEVERR_BLOCK_ID
+    assert torch.all(out[:6] == 7) and not torch.any(out[6] == 7)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hkv,d", [(1, 64), (8, 64), (3, 128), (8, 128)])
+def test_load_blocks_and_copy_blocks(fmt, hkv, d):
+    rng = np.random.default_rng(hkv + d)
+    c = Q.QuantCase(rng, fmt, [16 * 5], hkv, hkv, d, extra=3, poison=False)
+    dd = desc_of(fmt, hkv, hkv, d, c.nb, c.mbps)
+    gp = [dev(p) for p in c.pools]
+    src = np.array([4, 0, 7, c.nb, 2], np.int32)
+    dst = np.array([1, 3, 0, 2, 9], np.int32)
+    outs = [torch.full((6, hkv, 16, d), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    pkv.pkv_quant_load_blocks(dd, gp[0], gp[1], dev(src), dev(dst), outs[0], outs[1],
+                              k_scale=dev(c.k_scale), v_scale=dev(c.v_scale))
+    assert pkv.pkv_device_errors() == pkv.DEVERR_BLOCK_ID
+    for which, g in ((0, c.k_scale), (1, c.v_scale)):
+        vals = Q.pool_values(fmt, d, c.pools[which], np.ones(hkv) if g is None else g)
+        want = torch.full((6, hkv, 16, d), 7.0, dtype=torch.bfloat16)
+        for s, t in ((4, 1), (0, 3), (7, 0)):
+            want[t] = torch.from_numpy(vals[s].astype(np.float32)).bfloat16()
+        assert torch.equal(outs[which].cpu(), want)
+    pkv.pkv_copy_blocks(dd, gp[0], gp[1], dev(np.array([4, 2], np.int32)), dev(np.array([0, 6], np.int32)))
+    for which in (0, 1):
+        want = c.pools[which].copy()
+        want[0], want[6] = want[4], want[2]
+        assert np.array_equal(gp[which].cpu().numpy(), want)
+
+
+# ---------------------------------------------------------------- decode --
+
+def run_decode(c, sm_scale=None, window=-1, chunk=0, sinks=None, max_len=None, ws=None, lens=None):
+    dd = desc_of(c.fmt, c.hq, c.hkv, c.d, c.nb, c.mbps, c.ring)
+    lens = c.lens if lens is None else lens
+    max_len = max(1, int(lens.max())) if max_len is None else max_len
+    sm_scale = c.d ** -0.5 if sm_scale is None else sm_scale
+    if ws is None:
+        need = pkv.pkv_quant_decode_workspace_size(dd, len(lens), max_len, window, chunk)
+        ws = torch.zeros(max(256, need), dtype=torch.uint8, device=DEV)
+    q = bf(c.q)
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], float("nan"), device=DEV)
+    pkv.pkv_quant_decode(dd, q, dev(c.pools[0]), dev(c.pools[1]), dev(c.tables), dev(lens), max_len,
+                         sm_scale, out, lse, ws, window=window, chunk_blocks=chunk, k_scale=dev(c.k_scale),
+                         v_scale=dev(c.v_scale), sinks=dev(sinks))
+    torch.cuda.synchronize()
+    return out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+
+
+def check_decode(c, got, window=-1, sinks=None, sm_scale=None, seqs=None):
+    o, lse = got
+    sm_scale = c.d ** -0.5 if sm_scale is None else sm_scale
+    for s in range(len(c.lens)) if seqs is None else seqs:
+        n = int(c.lens[s])
+        lo = max(0, n - window) if window > 0 else 0
+        ro, rl, tol, ltol = Q.attention(c.q[s].astype(np.float64), c.rows(0, s, lo, n), c.rows(1, s, lo, n),
+                                        np.float64(np.float32(sm_scale)), sinks)
+        assert np.all(np.isfinite(o[s])), s
+        err = np.abs(o[s] - ro)  # an empty row's bound is 0: it is exactly 0
+        assert np.all(err <= tol), "sequence %d (length %d): %.3g of the bound" % (s, n, (err / (tol + 1e-300)).max())
+        fin = np.isfinite(rl)
+        assert np.array_equal(fin, np.isfinite(lse[s]))
+        assert np.all(np.abs(lse[s][fin] - rl[fin]) <= ltol[fin]), s
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 2), (7, 1), (16, 2), (9, 1), (16, 1), (24, 8), (30, 2)])
+def test_decode_lengths_and_groups(fmt, d, hq, hkv):
+    rng = np.random.default_rng(hq * 131 + d)
+    c = Q.QuantCase(rng, fmt, [1, 0, 16, 17, 31, 100, 255, 33, 640], hq, hkv, d)
+    check_decode(c, run_decode(c))
+    assert pkv.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (16, 1, 128), (4, 4, 128)])
+@pytest.mark.parametrize("chunk", [1, 2, 3, 5, 8, 40])
+def test_decode_splits(fmt, hq, hkv, d, chunk):
+    """1 .. 64 chunks a sequence, a last chunk of one key, empty sequences beside
+    long ones; the same workspace for every call, left with its tickets at zero."""
+    rng = np.random.default_rng(chunk)
+    c = Q.QuantCase(rng, fmt, [1009, 0, 16 * chunk, 16 * chunk + 1, 5, 320], hq, hkv, d)
+    dd = desc_of(fmt, hq, hkv, d, c.nb, c.mbps)
+    ws = torch.zeros(max(256, pkv.pkv_quant_decode_workspace_size(dd, 6, 1009, -1, chunk)), dtype=torch.uint8,
+                     device=DEV)
+    first = run_decode(c, chunk=chunk, ws=ws)
+    check_decode(c, first)
+    again = run_decode(c, chunk=chunk, ws=ws)
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("window", [1, 2, 16, 17, 100, 5000])
+@pytest.mark.parametrize("chunk", [0, 2])
+def test_decode_windows_and_sinks(fmt, window, chunk):
+    rng = np.random.default_rng(window)
+    hq, hkv, d = 12, 3, 64
+    c = Q.QuantCase(rng, fmt, [1, 15, 16, 17, 64, 301, 0, 700], hq, hkv, d)
+    sinks = rng.standard_normal(hq).astype(np.float32)
+    sinks[0], sinks[1], sinks[2] = 30.0, -30.0, -np.inf
+    check_decode(c, run_decode(c, window=window, chunk=chunk), window)
+    o, lse = run_decode(c, window=window, chunk=chunk, sinks=sinks)
+    check_decode(c, (o, lse), window, sinks)
+    assert np.all(o[6] == 0) and np.array_equal(lse[6], sinks.astype(np.float64))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_ring(fmt, d):
+    rng = np.random.default_rng(9)
+    for window, ring in ((128, 9), (16, 2), (33, 4), (600, 40)):
+        c = Q.QuantCase(rng, fmt, [1, window, window + 1, 977, 16 * ring * 3], 8, 2, d, ring=ring)
+        check_decode(c, run_decode(c, window=window), window)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("value,qvalue", [(1e-3, 1.0), (30.0, 1.0), (1.0, 1e-6), (1.0, 3e5), (1.0, 40.0)])
+def test_decode_magnitudes(fmt, value, qvalue):
+    """Small and large caches; q below f16's normal range and beyond its largest;
+    logits that concentrate the softmax on one key."""
+    rng = np.random.default_rng(4)
+    c = Q.QuantCase(rng, fmt, [300, 17, 900], 8, 2, 128, value=value)
+    c.q = Q.bf16(c.q * qvalue)
+    sm = 128 ** -0.5 / (1.0 if qvalue < 100 else qvalue)
+    check_decode(c, run_decode(c, sm_scale=sm), sm_scale=sm)
+
+
+def test_decode_rows_of_very_different_scales():
+    """int8 rows whose scales span 2^-8 .. 2^8, largest first, last and in between."""
+    rng = np.random.default_rng(8)
+    for order in (1, -1, 0):
+        c = Q.QuantCase(rng, "int8", [320], 4, 2, 64)
+        at = 16 * 64
+        for which in (0, 1):
+            sc = np.ascontiguousarray(c.pools[which][..., at:]).view(np.float32)
+            t = np.arange(320)
+            f = 2.0 ** (8 - 16 * t / 319) if order == 1 else 2.0 ** (-8 + 16 * t / 319) if order == -1 else \
+                2.0 ** rng.integers(-8, 9, 320)
+            if which == 0:
+                f = np.sqrt(np.sqrt(f))
+            for i in range(320):
+                sc[c.tables[0, i // 16], :, i % 16] *= f[i]
+            c.pools[which][..., at:] = sc.view(np.uint8).reshape(c.pools[which][..., at:].shape)
+        check_decode(c, run_decode(c, sm_scale=0.01), sm_scale=0.01)
+
+
+def test_decode_bad_blocks_and_lengths_are_flagged():
+    rng = np.random.default_rng(2)
+    c = Q.QuantCase(rng, "fp4", [100, 50], 8, 2, 64, poison=False)
+    c.tables[0, 3] = c.nb
+    run_decode(c)
+    assert pkv.pkv_device_errors() == pkv.DEVERR_BLOCK_ID
+    c.tables[0, 3] = -5
+    run_decode(c, chunk=2)
+    assert pkv.pkv_device_errors() == pkv.DEVERR_BLOCK_ID
+    c.tables[0, 3] = 0
+    o, lse = run_decode(c, max_len=64)  # sequence 0 is cut at the bound, sequence 1 is whole
+    assert pkv.pkv_device_errors() == pkv.DEVERR_LENGTH
+    check_decode(c, (o, lse), seqs=[1])
+    full = c.lens.copy()
+    c.lens = np.array([64, 50], np.int32)
+    check_decode(c, (o, lse))
+    c.lens = full
+
+
+def test_decode_two_streams_two_workspaces_and_graphs():
+    rng = np.random.default_rng(6)
+    cases = [Q.QuantCase(rng, fmt, [900, 33, 500, 1], 16, 2, 128) for fmt in ("int8", "fp4")]
+    runs = []
+    for c in cases:
+        dd = desc_of(c.fmt, c.hq, c.hkv, c.d, c.nb, c.mbps)
+        t = dict(desc=dd, q=bf(c.q), k_pool=dev(c.pools[0]), v_pool=dev(c.pools[1]), block_tables=dev(c.tables),
+                 context_lens=dev(c.lens), max_context_len=900, sm_scale=c.d ** -0.5,
+                 out=torch.zeros(4, 16, 128, dtype=torch.bfloat16, device=DEV),
+                 lse=torch.zeros(4, 16, device=DEV), chunk_blocks=4,
+                 workspace=torch.zeros(max(256, pkv.pkv_quant_decode_workspace_size(dd, 4, 900, -1, 4)),
+                                       dtype=torch.uint8, device=DEV),
+                 k_scale=dev(c.k_scale), v_scale=dev(c.v_scale))
+        runs.append(t)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(20):
+        for t, s in zip(runs, streams):
+            pkv.pkv_quant_decode(stream=s, **t)
+    torch.cuda.synchronize()
+    for c, t in zip(cases, runs):
+        check_decode(c, (t["out"].double().cpu().numpy(), t["lse"].double().cpu().numpy()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for t in runs:
+            pkv.pkv_quant_decode(**t)
+    for c, t in zip(cases, runs):  # other queries and lengths in the same buffers
+        c.q = Q.bf16(rng.standard_normal(c.q.shape))
+        c.lens = np.array([17, 33, 499, 1], np.int32)
+        t["q"].copy_(bf(c.q))
+        t["context_lens"].copy_(dev(c.lens))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for c, t in zip(cases, runs):
+        check_decode(c, (t["out"].double().cpu().numpy(), t["lse"].double().cpu().numpy()))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+def test_pool_offsets_past_32_bits(fmt):
+    """The last blocks of a pool of more than 2^32 bytes: append, read, widen, decode."""
+    hq, hkv, d = 8, 8, 128
+    rec = Q.record_bytes(fmt, d)
+    nb = (1 << 32) // (hkv * rec) + 40
+    pools = [torch.empty(nb, hkv, rec, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    n = 70
+    tables = torch.arange(nb - 5, nb, dtype=torch.int32, device=DEV)[None]
+    dd = desc_of(fmt, hq, hkv, d, nb, 5)
+    g = torch.full((hkv,), 4.0 / 2688, device=DEV) if fmt == "fp4" else None
+    k, v = (torch.randn(n, hkv, d, device=DEV).bfloat16() for _ in range(2))
+    tts, pos = torch.zeros(n, dtype=torch.int32, device=DEV), torch.arange(n, dtype=torch.int32, device=DEV)
+    pkv.pkv_quant_append(dd, pools[0], pools[1], tables, tts, pos, k, v, k_scale=g, v_scale=g)
+    ko, vo = (torch.empty(n, hkv, d, device=DEV) for _ in range(2))
+    pkv.pkv_quant_read(dd, pools[0], pools[1], tables, tts, pos, ko, vo, k_scale=g, v_scale=g)
+    kb, vb = (torch.zeros(5, hkv, 16, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    pkv.pkv_quant_load_blocks(dd, pools[0], pools[1], tables[0], torch.arange(5, dtype=torch.int32, device=DEV),
+                              kb, vb, k_scale=g, v_scale=g)
+    assert torch.equal(kb.transpose(1, 2).reshape(80, hkv, d)[:n], ko.bfloat16())
+    assert torch.equal(vb.transpose(1, 2).reshape(80, hkv, d)[:n], vo.bfloat16())
+    q = torch.randn(1, hq, d, device=DEV).bfloat16()
+    out = torch.empty_like(q)
+    ws = torch.zeros(max(256, pkv.pkv_quant_decode_workspace_size(dd, 1, n)), dtype=torch.uint8, device=DEV)
+    pkv.pkv_quant_decode(dd, q, pools[0], pools[1], tables, torch.tensor([n], dtype=torch.int32, device=DEV), n,
+                         d ** -0.5, out, None, ws, k_scale=g, v_scale=g)
+    ro, _, tol, _ = Q.attention(q[0].double().cpu().numpy(), ko.double().cpu().numpy(), vo.double().cpu().numpy(),
+                                np.float64(np.float32(d ** -0.5)))
+    # the rows read back were rounded to fp32: 2^-24 more on each product
+    assert np.all(np.abs(out[0].double().cpu().numpy() - ro) <= tol * 1.001)
+    assert pkv.pkv_device_errors() == 0
+    for name, src in (("k", k), ("v", v)):  # and the values are the rows' own, within a step
+        err = (dict(k=ko, v=vo)[name] - src.float()).abs().amax()
+        assert err <= src.float().abs().amax() / (127 if fmt == "int8" else 5)
+
+
+# ------------------------------------------------- a sequence, end to end --
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("layout,r", [("half", 128), ("interleaved", 64)])
+def test_a_batch_served_through_the_quantised_cache(fmt, layout, r):
+    """A prompt in two chunks (append, widen, ragged prefill), then four decode
+    steps (append with the rotation of q, decode), against 64-bit attention over
+    the definition's rows; YaRN positions, q and k in one packed buffer."""
+    rng = np.random.default_rng(77)
+    hq, hkv, d, steps = 8, 2, 128, 4
+    prompts = [53, 7, 96]
+    b = len(prompts)
+    total = [p + steps for p in prompts]
+    mbps = max((t + 15) // 16 for t in total)
+    nb = sum((t + 15) // 16 for t in total) + 2
+    perm = list(rng.permutation(nb))
+    tables = np.full((b, mbps), -1, np.int32)
+    for s, t in enumerate(total):
+        for i in range((t + 15) // 16):
+            tables[s, i] = perm.pop()
+    cs = pkv.pkv_rope_scaled_table(1e4, r, 200, kind="yarn", factor=4.0, original_max_pos=50, attention=1.1386)
+    rope = pkv.make_rope(dev(cs), layout=layout)
+    dd = desc_of(fmt, hq, hkv, d, nb, mbps)
+    g = np.full(hkv, 5.0 / 2688, np.float32) if fmt == "fp4" else None
+    gd = dev(g)
+    pools = [torch.zeros(nb, hkv, Q.record_bytes(fmt, d), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    qkv = [Q.bf16(rng.standard_normal((t, hq + 2 * hkv, d))) for t in total]
+    sm = np.float64(np.float32(d ** -0.5))
+
+    # the definition's rows of every sequence
+    def stored(x, rotated):
+        rows = np.empty((len(x), hkv, d))
+        for p in range(len(x)):
+            y = Q.rotate(x[p], cs[p], layout, np.float32) if rotated else x[p]
+            for h in range(hkv):
+                gh = 1.0 if g is None else g[h]
+                rows[p, h] = Q.row_values(fmt, *Q.quantise(fmt, y[h], gh), gh)
+        return rows
+    keys = [stored(x[:, hq:hq + hkv], True) for x in qkv]
+    vals = [stored(x[:, hq + hkv:], False) for x in qkv]
+    turned = [Q.bf16(np.stack([Q.rotate(x[p, :hq], cs[p], layout, np.float32) for p in range(len(x))])) for x in qkv]
+
+    # prompt chunks
+    cuts = [(0, [20, 5, 48]), ([20, 5, 48], prompts)]
+    staged = [torch.zeros(nb, hkv, 16, d, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    bdesc = pkv.make_desc(num_q_heads=hq, num_kv_heads=hkv, head_dim=d, num_blocks=nb, max_blocks_per_seq=mbps)
+    for lo, hi in cuts:
+        lo = [0] * b if lo == 0 else lo
+        rows = bf(np.concatenate([x[a:e] for x, a, e in zip(qkv, lo, hi)]))
+        tts = np.repeat(np.arange(b), [e - a for a, e in zip(lo, hi)]).astype(np.int32)
+        pos = np.concatenate([np.arange(a, e) for a, e in zip(lo, hi)]).astype(np.int32)
+        q = torch.empty(len(pos), hq, d, dtype=torch.bfloat16, device=DEV)
+        pkv.pkv_quant_append(dd, pools[0], pools[1], dev(tables), dev(tts), dev(pos), rows[:, hq:hq + hkv],
+                             rows[:, hq + hkv:], q=rows[:, :hq], q_out=q, rope=rope, k_scale=gd, v_scale=gd)
+        ids = np.unique(np.concatenate([tables[s, :(e + 15) // 16] for s, e in enumerate(hi)])).astype(np.int32)
+        pkv.pkv_quant_load_blocks(dd, pools[0], pools[1], dev(ids), dev(ids), staged[0], staged[1], k_scale=gd,
+                                  v_scale=gd)
+        qo = np.concatenate(([0], np.cumsum([e - a for a, e in zip(lo, hi)]))).astype(np.int32)
+        lens = np.array(hi, np.int32)
+        out = torch.empty_like(q)
+        pkv.pkv_prefill_attention_ragged(bdesc, q, dev(qo), staged[0], staged[1], dev(tables), dev(lens), float(sm),
+                                         out, qo_indptr_host=qo, kv_lens_host=lens)
+        got = out.double().cpu().numpy()
+        for i, (s, p) in enumerate(zip(tts, pos)):
+            # the widened rows are the values rounded to bf16, which is what the prefill attends
+            ro, _, tol, _ = Q.attention(turned[s][p].astype(np.float64), Q.bf16(keys[s][:p + 1]).astype(np.float64),
+                                        Q.bf16(vals[s][:p + 1]).astype(np.float64), sm)
+            # and its weights are bf16: 2^-8 of sum w |v| <= max |v| in the bound's place of f16's 2^-11
+            tol = tol + 2.0 ** -8 * np.abs(vals[s][:p + 1]).max()
+            assert np.all(np.abs(got[i] - ro) <= tol), (i, s, p)
+
+    # decode steps
+    ws = torch.zeros(max(256, pkv.pkv_quant_decode_workspace_size(dd, b, max(total), -1, 2)), dtype=torch.uint8,
+                     device=DEV)
+    tts = dev(np.arange(b, dtype=np.int32))
+    for step in range(steps):
+        pos = np.array(prompts, np.int32) + step
+        rows = bf(np.stack([x[p] for x, p in zip(qkv, pos)]))
+        q = torch.empty(b, hq, d, dtype=torch.bfloat16, device=DEV)
+        pkv.pkv_quant_append(dd, pools[0], pools[1], dev(tables), tts, dev(pos), rows[:, hq:hq + hkv],
+                             rows[:, hq + hkv:], q=rows[:, :hq], q_out=q, rope=rope, k_scale=gd, v_scale=gd)
+        out = torch.empty_like(q)
+        lse = torch.empty(b, hq, device=DEV)
+        pkv.pkv_quant_decode(dd, q, pools[0], pools[1], dev(tables), dev(pos + 1), max(total), float(sm), out, lse,
+                             ws, chunk_blocks=2, k_scale=gd, v_scale=gd)
+        for s, p in enumerate(pos):
+            assert np.array_equal(q[s].float().cpu().numpy(), turned[s][p])
+            ro, rl, tol, ltol = Q.attention(turned[s][p].astype(np.float64), keys[s][:p + 1], vals[s][:p + 1], sm)
+            assert np.all(np.abs(out[s].double().cpu().numpy() - ro) <= tol)
+            assert np.all(np.abs(lse[s].double().cpu().numpy() - rl) <= ltol)
+    assert pkv.pkv_device_errors() == 0
