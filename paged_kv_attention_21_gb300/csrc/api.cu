@@ -1687,14 +1687,48 @@ pkv_status pkv_quant_load_blocks(const pkv_cache_desc* desc, const void* k_pool,
     return PKV_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// Chunk length (blocks) and chunks per (sequence, KV head).  A ragged batch
+// averages about half its longest context; aim for one wave of resident CTAs.
+pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_ctx, int window, int num_sms,
+                             int chunk_req, int* chunk_out, int* splits_out) {
+    const int mb = max_visible_blocks(max_ctx, window);
+    int chunk = chunk_req;
+    if (chunk <= 0) {
+        const double pairs = double(num_seqs) * desc->num_kv_heads;
+        const double slots = double(std::max(num_sms, 1)) *
+                             pkv::quant_decode_ctas(desc->head_dim, desc->kv_dtype == PKV_KV_FP4,
+                                                    desc->num_q_heads / desc->num_kv_heads);
+        chunk = int(std::ceil(pairs * std::max(1.0, 0.55 * mb) / slots));
+        chunk = std::max(32, std::min(128, chunk));
+        chunk = std::max(chunk, (mb + pkv::kQuantMaxSplits - 1) / pkv::kQuantMaxSplits);
+        chunk = std::min(chunk, mb);
+    }
+    if (chunk > pkv::kQuantMaxChunk || (mb + chunk - 1) / chunk > pkv::kQuantMaxSplits)
+        return fail(PKV_ERR_UNSUPPORTED, "context of %d blocks needs more than %d chunks of %d blocks", mb,
+                    pkv::kQuantMaxSplits, std::min(chunk, pkv::kQuantMaxChunk));
+    *chunk_out = chunk;
+    *splits_out = (mb + chunk - 1) / chunk;
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t pkv_quant_decode_workspace_size(const pkv_cache_desc* desc, int32_t num_seqs, int32_t max_context_len,
                                        int32_t window, int32_t chunk_blocks) {
-    (void)desc;
-    (void)num_seqs;
-    (void)max_context_len;
-    (void)window;
-    (void)chunk_blocks;
-    return 0;
+    if (check_shape(desc) != PKV_OK || !quantised(desc) || num_seqs <= 0 || max_context_len < 1 || chunk_blocks < 0 ||
+        chunk_blocks > pkv::kQuantMaxChunk)
+        return 0;
+    int sms = 0;
+    if (chunk_blocks == 0 && device_state(nullptr, &sms) != PKV_OK) return 0;
+    int c = 0, s = 0;
+    if (plan_quant_decode(desc, num_seqs, max_context_len, window, sms, chunk_blocks, &c, &s) != PKV_OK) return 0;
+    return decode_ws_layout(desc, num_seqs, s).total;
 }
 
 pkv_status pkv_quant_decode(const pkv_cache_desc* desc, const void* q, const void* k_pool, const void* v_pool,
@@ -1716,12 +1750,25 @@ pkv_status pkv_quant_decode(const pkv_cache_desc* desc, const void* q, const voi
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16))
         return fail(PKV_ERR_INVALID_ARG, "q, out and the pools must be 16-byte aligned");
     if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return fail(PKV_ERR_INVALID_ARG, "sm_scale must be finite and > 0");
-    if (chunk_blocks < 0 || chunk_blocks > 512) return fail(PKV_ERR_INVALID_ARG, "chunk_blocks %d outside [0, 512]", chunk_blocks);
-    (void)workspace;
-    (void)workspace_bytes;
+    if (chunk_blocks < 0 || chunk_blocks > pkv::kQuantMaxChunk)
+        return fail(PKV_ERR_INVALID_ARG, "chunk_blocks %d outside [0, %d]", chunk_blocks, pkv::kQuantMaxChunk);
     pkv::QuantDecodeArgs a{};
-    st = device_state(&a.err, nullptr);
+    int sms = 0;
+    st = device_state(&a.err, &sms);
     if (st != PKV_OK) return st;
+    st = plan_quant_decode(desc, num_seqs, max_context_len, window, sms, chunk_blocks, &a.chunk_blocks, &a.max_splits);
+    if (st != PKV_OK) return st;
+    const DecodeWs ws = decode_ws_layout(desc, num_seqs, a.max_splits);
+    if (ws.total > 0) {
+        if (!workspace) return fail(PKV_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", ws.total);
+        if (!aligned(workspace, 256)) return fail(PKV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+        if (workspace_bytes < ws.total)
+            return fail(PKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, ws.total);
+        uint8_t* wsb = static_cast<uint8_t*>(workspace);
+        a.counters = reinterpret_cast<uint32_t*>(wsb + ws.counters);
+        a.part_lse = reinterpret_cast<float*>(wsb + ws.lse);
+        a.part_o = reinterpret_cast<float*>(wsb + ws.o);
+    }
     a.q = q;
     a.k_pool = k_pool;
     a.v_pool = v_pool;

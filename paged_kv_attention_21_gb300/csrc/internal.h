@@ -253,12 +253,18 @@ struct QuantDecodeArgs {
     const float* sinks;  // nullable
     void* out;
     float* lse_out;  // nullable
+    uint32_t* counters;  // [num_seqs * hkv], zero on entry and exit (more than one chunk)
+    float* part_lse;     // [num_seqs * hkv * max_splits * group]
+    float* part_o;       // [num_seqs * hkv * max_splits * group * d]
     int64_t num_blocks;
-    int32_t num_seqs, hq, hkv, group, d, fp4, mbps, ring, window, max_ctx;
+    int32_t num_seqs, hq, hkv, group, d, fp4, mbps, ring, window, max_ctx, chunk_blocks, max_splits;
     float sm_scale;
     uint32_t* err;
 };
+constexpr int kQuantMaxChunk = 512;   // blocks per CTA
+constexpr int kQuantMaxSplits = 512;  // chunks per (sequence, KV head)
 cudaError_t launch_quant_decode(const QuantDecodeArgs& a, cudaStream_t stream);
+int quant_decode_ctas(int d, int fp4, int group);  // resident per SM
 
 // Tensor-map box shape used by the attention kernels for a pool:
 // innermost box extent in elements, and the swizzle.

@@ -1,10 +1,41 @@
-// quant_decode.cu -- decode attention over the quantised paged pools.
+// quant_decode.cu -- split-KV GQA decode attention over the quantised pools.
 //
 //   o = softmax(sm_scale * q k^T) v over the visible keys, k and v the records'
-//   values; a sink logit joins the normaliser with a zero value.
+//   values (int8 code * row scale; e2m1 * 16-dim scale * head scale); a sink
+//   logit joins the normaliser with a zero value.
 //
-// One warp per (sequence, query head): lane l owns dims [l D/32, (l + 1) D/32),
-// one pass over the keys with a running maximum and sum in fp32.
+// Work decomposition.  The visible blocks of every (sequence, KV head) are cut
+// into chunks (the planner in api.cu); a CTA owns one chunk and its 4 warps
+// take the chunk's blocks round-robin, each with its own ring of bulk copies (a
+// K record and a V record per stage: one untiled copy each, since a record holds
+// codes and scales side by side, already in the bank-conflict-free order).  The
+// warps' states meet in shared memory; a sequence of several chunks merges
+// through the workspace, the last chunk to take its ticket joining all of them
+// in chunk order.
+//
+// The MMAs run transposed: S^T = K Q^T and O^T += V^T P^T (m16n8k16, f16 ->
+// fp32), so the 16 tokens of a block (S^T) and the head's dims (O^T) fill the
+// m16 side and up to 8 query heads the n8 side: a group of at most 8 heads
+// pads nothing, and a lane's softmax state is that of its two heads.  Both
+// products allow any order of their summed index, which is used to read codes
+// as they lie:
+//   S^T: lane (g, t) reads dims [t D/4, (t+1) D/4) of two tokens' rows, k-step j
+//        taking dims t D/4 + 4j .. + 3; q takes the same order;
+//   O^T: lane (g, t) reads dims [g D/8, (g+1) D/8) of four tokens' rows, m-tile i
+//        taking dims g D/8 + 2i (row g) and + 1 (row g + 8); token slot k of a
+//        block is row slot_row(k), for S^T and O^T alike.
+// P^T in the second product's operand layout is the first's result transposed
+// per 8x8: one movmatrix each.
+//
+// Operands are exact: codes are integers below 128, or e2m1 times e4m3 (6
+// significant bits, at least 2^-10), q is scaled by a power of two into f16's
+// range.  The int8 row scale of K multiplies the logit, that of V the weight
+// (normalised by a power of two that follows the largest seen, so the weight
+// stays in f16's range).  Weights are rounded to f16 (2^-11); the statistics,
+// l and O are fp32.
+//
+// Roofline: HBM.  Per token and KV head 2 (D + 4) bytes (int8) or 2 (D/2 + D/16)
+// (4-bit) against 4 D G flops.
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -13,74 +44,658 @@ namespace pkv {
 
 namespace {
 
-template <int D, bool kFp4>
-__global__ void __launch_bounds__(128) quant_decode_kernel(QuantDecodeArgs a) {
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+
+template <int D, bool kFp4, int NT>
+struct Cfg {
+    using R = QuantRecord<D, kFp4>;
+    static constexpr int kTile = (R::kBytes + 127) / 128 * 128;  // a record in shared memory
+    static constexpr int kStage = 2 * kTile;                     // K + V
+    static constexpr int kStages = kFp4 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 5);
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kCombStride = D + 4;
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kComb = kWarps * kHeads * kCombStride * 4;
+    static constexpr int kSmem = (kRing > kComb ? kRing : kComb) + 128;
+    // registers: NT * D / 4 accumulators and NT * D / 8 of q
+    static constexpr int kCtas = NT * D > 128 ? 3 : 4;
+};
+
+// The row of a block that token slot k (0..7; slot k + 8 is row + 8) stands for:
+// pairs swapped where that spreads the rows one load touches over all banks.
+template <int kRowBytes>
+__device__ __forceinline__ constexpr int slot_row(int k) {
+    return kRowBytes == 128 ? k : kRowBytes == 64 ? k ^ ((k >> 1) & 1) : k ^ ((k >> 2) & 1);
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t hsub2_bits(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Four bytes of e2m1 pairs -> four f16x2 words.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&d)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, e;\n\tmov.b32 {a, b, c, e}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, e;\n\t}"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(w));
+}
+
+// Two e4m3 scales (bytes lo, hi) -> f16x2.
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t lo, uint32_t hi) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(d) : "r"(lo | (hi << 8)));
+    return d;
+}
+
+// Codes + 128 in bytes 0, 1 (or 2, 3) of w -> their f16 values: 0x6400 | u is
+// 1024 + u, less 1152 (both exact).
+template <bool kHigh>
+__device__ __forceinline__ uint32_t int8x2(uint32_t w) {
+    return hsub2_bits(__byte_perm(w, 0x64646464u, kHigh ? 0x4342 : 0x4140), 0x64806480u);
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// A warp's running state: lane (g, t) holds heads 2t, 2t + 1 (+ 8 nt).
+template <int D, int NT>
+struct State {
+    float mu[NT][2];  // what is subtracted from the logits (exp2 domain), -inf before any key
+    float l[NT][2];   // this lane's share of sum 2^(x - mu)
+    float o[NT][D / 16][4];
+    float vfac;       // int8: the power of two on V's row scales, inf before any key
+};
+
+constexpr float kGrow = 8.f;    // logits may exceed mu by this before it moves (2^8 fits f16)
+constexpr float kVGrow = 64.f;  // normalised V scales may reach this (2^8 * 64 fits f16)
+
+// One block: tok_base is its first token's position, keys in [lo, ctx) are visible.
+template <int D, bool kFp4, int NT>
+__device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2], const uint8_t* kt,
+                                       const uint8_t* vt, int lane, int tok_base, int lo, int ctx, float sl) {
+    using R = QuantRecord<D, kFp4>;
+    constexpr int RB = R::kRowBytes;
+    const int g = lane >> 2, t = lane & 3;
+    const int row = slot_row<RB>(g);  // and row + 8
+
+    // ---- S^T = K Q^T: 16 token slots x 8 heads
+    float s[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    uint32_t kw[2][RB / 16];  // this lane's RB/4 bytes of each row
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint8_t* base = kt + half * 8 * RB;
+        if constexpr (RB == 128) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                *reinterpret_cast<uint4*>(&kw[half][4 * c]) =
+                    *reinterpret_cast<const uint4*>(base + quant_chunk<RB>(row, 2 * t + c));
+        } else if constexpr (RB == 64) {
+            *reinterpret_cast<uint4*>(&kw[half][0]) = *reinterpret_cast<const uint4*>(base + quant_chunk<RB>(row, t));
+        } else {
+            *reinterpret_cast<uint2*>(&kw[half][0]) =
+                *reinterpret_cast<const uint2*>(base + quant_chunk<RB>(row, t >> 1) + 8 * (t & 1));
+        }
+    }
+    float ks[2];  // int8: the rows' K scales
+    if constexpr (kFp4) {
+        uint32_t sc[2][D / 64];  // f16x2, both halves the scale of 16 dims
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint8_t* p = kt + R::kScales + (row + 8 * half) * R::kScaleBytes + t * (D / 64);
+            if constexpr (D == 128) {
+                const uint32_t b = *reinterpret_cast<const uint16_t*>(p);
+                const uint32_t v = e4m3x2(b & 0xFFu, b >> 8);
+                sc[half][0] = __byte_perm(v, v, 0x1010);
+                sc[half][1] = __byte_perm(v, v, 0x3232);
+            } else {
+                sc[half][0] = e4m3x2(*p, *p);
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {  // a word: 8 dims, two k-steps
+            uint32_t r0[4], r1[4];
+            e2m1x8(kw[0][w], r0);
+            e2m1x8(kw[1][w], r1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r0[i] = hmul2_bits(r0[i], sc[0][w / 2]);
+                r1[i] = hmul2_bits(r1[i], sc[1][w / 2]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t a[4] = {r0[2 * j], r1[2 * j], r0[2 * j + 1], r1[2 * j + 1]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816<true>(s[n], a, qb[n][2 * w + j][0], qb[n][2 * w + j][1]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+            ks[half] = *reinterpret_cast<const float*>(kt + R::kScales + (row + 8 * half) * 4);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            const uint32_t a[4] = {int8x2<false>(kw[0][j]), int8x2<false>(kw[1][j]), int8x2<true>(kw[0][j]),
+                                   int8x2<true>(kw[1][j])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816<true>(s[n], a, qb[n][j][0], qb[n][j][1]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            s[n][0] *= ks[0];
+            s[n][1] *= ks[0];
+            s[n][2] *= ks[1];
+            s[n][3] *= ks[1];
+        }
+    }
+
+    // ---- V's scales, zero on invisible tokens
+    const bool edge = tok_base < lo || tok_base + kBlockSize > ctx;
+    const int base = tok_base - lo;
+    const uint32_t cnt = static_cast<uint32_t>(ctx - lo);
+    auto visible = [&](int r) { return static_cast<uint32_t>(base + r) < cnt; };
+    const int ta = slot_row<RB>(2 * t), tb = slot_row<RB>(2 * t + 1);  // O^T's token slots: rows ta, tb (+ 8)
+    uint32_t vs2[2];  // 4-bit: f16x2 scales of (ta, tb) and of (ta + 8, tb + 8)
+    float vs[2];      // int8: normalised scales of S^T's rows
+    if constexpr (kFp4) {
+        const uint8_t* p = vt + R::kScales + (D == 128 ? g : g >> 1);
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = p[((i & 1 ? tb : ta) + (i & 2 ? 8 : 0)) * R::kScaleBytes];
+        if (edge) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!visible((i & 1 ? tb : ta) + (i & 2 ? 8 : 0))) b[i] = 0;
+        }
+        vs2[0] = e4m3x2(b[0], b[1]);
+        vs2[1] = e4m3x2(b[2], b[3]);
+    } else {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            vs[half] = *reinterpret_cast<const float*>(vt + R::kScales + (row + 8 * half) * 4);
+            if (edge && !visible(row + 8 * half)) vs[half] = 0.f;
+        }
+    }
+    if (edge) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (!visible(row)) s[n][0] = s[n][1] = -INFINITY;
+            if (!visible(row + 8)) s[n][2] = s[n][3] = -INFINITY;
+        }
+    }
+
+    // ---- softmax: p = 2^(s sl - mu), mu moving only when a logit exceeds it by 2^8
+    float p[NT][4];
+    bool grow = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[n][e] = __fmaf_rn(s[n][e], sl, -st.mu[n][e & 1]);
+        grow = grow || !(fmaxf(fmaxf(p[n][0], p[n][1]), fmaxf(p[n][2], p[n][3])) <= kGrow);
+    }
+    if constexpr (!kFp4) grow = grow || !(fmaxf(vs[0], vs[1]) * st.vfac <= kVGrow);
+    if (__any_sync(0xFFFFFFFFu, grow)) {
+        float vmul = 1.f;
+        if constexpr (!kFp4) {
+            float m = fmaxf(vs[0], vs[1]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+            if (!(m * st.vfac <= kVGrow)) {
+                // 2^-ceil-ish of the largest scale: m * vfac in [1, 2), at most 2^100
+                const uint32_t ex = __float_as_uint(m) >> 23;  // m >= 0
+                const float nf = ex < 27u ? __uint_as_float(227u << 23) : __uint_as_float((254u - min(ex, 253u)) << 23);
+                // nf / vfac, exactly (it only shrinks; below 2^-126 O still is 0)
+                const int step = static_cast<int>(__float_as_uint(nf) >> 23) - static_cast<int>(__float_as_uint(st.vfac) >> 23);
+                if (st.vfac != INFINITY) vmul = step < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + step) << 23);
+                st.vfac = nf;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float mx = fmaxf(s[n][c], s[n][c + 2]) * sl;
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+                const float mn = fmaxf(st.mu[n][c], mx);
+                const float keep = mn == -INFINITY ? 1.f : fast_exp2(st.mu[n][c] - mn);
+                st.mu[n][c] = mn;
+                st.l[n][c] *= keep;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    st.o[n][i][c] *= keep * vmul;
+                    st.o[n][i][c + 2] *= keep * vmul;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[n][e] = __fmaf_rn(s[n][e], sl, -st.mu[n][e & 1]);
+        }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[n][e] = fast_exp2(p[n][e]);
+        st.l[n][0] += p[n][0] + p[n][2];
+        st.l[n][1] += p[n][1] + p[n][3];
+        if constexpr (!kFp4) {
+            const float f0 = vs[0] * st.vfac, f1 = vs[1] * st.vfac;
+            p[n][0] *= f0;
+            p[n][1] *= f0;
+            p[n][2] *= f1;
+            p[n][3] *= f1;
+        }
+        pb[n][0] = movmatrix(pack2<true>(p[n][0], p[n][1]));
+        pb[n][1] = movmatrix(pack2<true>(p[n][2], p[n][3]));
+    }
+
+    // ---- O^T += V^T P^T: D dims x 8 heads
+    constexpr int VB = RB / 8;  // this lane's bytes of a token's row
+    constexpr int VW = VB / 4;
+    uint32_t vw[4][VW];  // rows ta, tb, ta + 8, tb + 8
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (i & 1 ? tb : ta);
+        const uint8_t* q = vt + (i & 2 ? 8 * RB : 0) + quant_chunk<RB>(r, g * VB / 16) + (g * VB) % 16;
+        if constexpr (VB == 16) {
+            *reinterpret_cast<uint4*>(vw[i]) = *reinterpret_cast<const uint4*>(q);
+        } else if constexpr (VB == 8) {
+            *reinterpret_cast<uint2*>(vw[i]) = *reinterpret_cast<const uint2*>(q);
+        } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(q);
+        }
+    }
+    if constexpr (kFp4) {
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {  // a word: 8 dims, four m-tiles
+            uint32_t even[2][4], odd[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t x = vw[2 * h][w], y = vw[2 * h + 1][w];
+                e2m1x8((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), even[h]);
+                e2m1x8(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), odd[h]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a[4] = {hmul2_bits(even[0][i], vs2[0]), hmul2_bits(odd[0][i], vs2[0]),
+                                       hmul2_bits(even[1][i], vs2[1]), hmul2_bits(odd[1][i], vs2[1])};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816<true>(st.o[n][4 * w + i], a, pb[n][0], pb[n][1]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {  // a word: 4 dims, two m-tiles
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t lo2 = __byte_perm(vw[0][w], vw[1][w], i ? 0x7362 : 0x5140);
+                const uint32_t hi2 = __byte_perm(vw[2][w], vw[3][w], i ? 0x7362 : 0x5140);
+                const uint32_t a[4] = {int8x2<false>(lo2), int8x2<true>(lo2), int8x2<false>(hi2), int8x2<true>(hi2)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816<true>(st.o[n][2 * w + i], a, pb[n][0], pb[n][1]);
+            }
+        }
+    }
+}
+
+template <int D, bool kFp4, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_decode_kernel(QuantDecodeArgs a) {
+    using C = Cfg<D, kFp4, NT>;
+    using R = QuantRecord<D, kFp4>;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ uint64_t bars[kWarps][C::kStages];
+    __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_v[kWarps];
+    __shared__ int s_flag;
+    uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+    const int G = a.group;
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kWarps; ++w)
+            for (int i = 0; i < C::kStages; ++i) mbar_init(&bars[w][i], 1);
+        s_flag = 0;
+        fence_barrier_init();
+    }
     pdl_wait();
     pdl_launch_dependents();
-    using R = QuantRecord<D, kFp4>;
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int seq = blockIdx.y;
-    const int hq = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (hq >= a.hq) return;
-    const int h = hq / a.group;
+
+    const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.mbps;
+    // without a window a chunk's blocks do not depend on the length: the ids are
+    // read while it is in flight
+    int id_next = 0;
+    const int early = split * a.chunk_blocks + warp + lane * kWarps;
+    if (a.window <= 0 && lane * kWarps < a.chunk_blocks && early < a.mbps) id_next = bt[early];
     int ctx = a.context_lens[seq];
     if (ctx > a.max_ctx) {
-        if (lane == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
+        if (threadIdx.x == 0 && split == 0 && kvh == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
         ctx = a.max_ctx;
     }
     const int lo = a.window > 0 && ctx > a.window ? ctx - a.window : 0;
-    const float kg = kFp4 ? a.k_scale[h] : 1.f, vg = kFp4 ? a.v_scale[h] : 1.f;
-    const size_t row0 = static_cast<size_t>(seq) * a.hq + hq;
-    float q[E], o[E] = {};
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        q[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[row0 * D + lane * E + e]) * a.sm_scale * kg;
-    float m = a.sinks ? a.sinks[hq] : -INFINITY;
-    float l = a.sinks ? 1.f : 0.f;
-    for (int t = lo; t < ctx; ++t) {
-        const int b = t / kBlockSize, r = t % kBlockSize;
-        int blk = a.block_tables[static_cast<size_t>(seq) * a.mbps + (a.ring > 0 ? b % a.ring : b)];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-            blk = 0;
+    const size_t head0 = static_cast<size_t>(seq) * a.hq + kvh * G;  // the group's first row of q, out, lse
+    if (ctx <= 0) {
+        if (split == 0) {
+            for (int i = threadIdx.x; i < G * D; i += kThreads)
+                static_cast<__nv_bfloat16*>(a.out)[head0 * D + i] = __float2bfloat16_rn(0.f);
+            if (a.lse_out && threadIdx.x < G)
+                a.lse_out[head0 + threadIdx.x] = a.sinks ? a.sinks[kvh * G + threadIdx.x] : -INFINITY;
         }
-        const size_t at = (static_cast<size_t>(blk) * a.hkv + h) * R::kBytes;
-        const uint8_t* kr = static_cast<const uint8_t*>(a.k_pool) + at;
-        const uint8_t* vr = static_cast<const uint8_t*>(a.v_pool) + at;
-        float k[E], v[E], x = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            k[e] = quant_value<D, kFp4>(kr, r, lane * E + e, 1.f);
-            v[e] = quant_value<D, kFp4>(vr, r, lane * E + e, vg);
-            x += q[e] * k[e];
-        }
-#pragma unroll
-        for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
-        const float mn = fmaxf(m, x);
-        const float keep = m == -INFINITY ? 0.f : expf(m - mn), p = expf(x - mn);
-        l = l * keep + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * v[e];
-        m = mn;
+        return;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int first_blk = lo / kBlockSize, last_blk = (ctx - 1) / kBlockSize;
+    const int nsplit = (last_blk - first_blk + a.chunk_blocks) / a.chunk_blocks;
+    if (split >= nsplit) return;
+    const int b0 = first_blk + split * a.chunk_blocks;
+    const int b1 = min(last_blk + 1, b0 + a.chunk_blocks);
+    const int my_n = b1 - b0 > warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;
+    __syncthreads();  // the barriers are initialised
+
+    // ids of this warp's blocks, 32 at a time: lane k holds that of block
+    // 32 batch + k.  A bad id is flagged and reads block 0.
+    auto fetch_ids = [&](int batch) {
+        const int k = 32 * batch + lane;
+        int id = 0;
+        if (k < my_n) {
+            const int lb = b0 + warp + k * kWarps;
+            id = bt[a.ring > 0 ? lb % a.ring : lb];
+        }
+        return id;
+    };
+    auto check_id = [&](int id, int batch) {
+        if (32 * batch + lane < my_n && (id < 0 || id >= a.num_blocks)) {
+            flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+            id = 0;
+        }
+        return id;
+    };
+    if (a.window > 0) id_next = fetch_ids(0);
+    int id_cur = 0;
+    const uint8_t* pool = static_cast<const uint8_t*>(lane == 0 ? a.k_pool : a.v_pool);
+    uint8_t* ring = smem + warp * C::kStages * C::kStage;
+    // block k of this warp into its stage: lane 0 brings K, lane 1 V
+    auto load = [&](int k, int stage) {
+        if ((k & 31) == 0) {
+            id_cur = check_id(id_next, k >> 5);
+            id_next = fetch_ids((k >> 5) + 1);
+        }
+        const int id = __shfl_sync(0xFFFFFFFFu, id_cur, k & 31);
+        if (lane < 2 && k < my_n) {
+            if (lane == 0) mbar_arrive_expect_tx(&bars[warp][stage], 2 * R::kBytes);
+            bulk_load(ring + stage * C::kStage + lane * C::kTile, pool + (static_cast<size_t>(id) * a.hkv + kvh) * R::kBytes,
+                      R::kBytes, &bars[warp][stage]);
+        }
+    };
+    // earlier kernels wrote the pools through the generic proxy
+    fence_proxy_async_global();
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        static_cast<__nv_bfloat16*>(a.out)[row0 * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-    if (a.lse_out && lane == 0) a.lse_out[row0] = l > 0.f ? m + logf(l) : -INFINITY;
+    for (int k = 0; k < C::kStages; ++k) load(k, k);
+
+    // ---- q: lane (g, t) holds head g's dims t D/4 + 4j .. + 3 for k-step j, as
+    // f16 scaled by 2^(12 - e), e the exponent of the group's largest |q|
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t qb[NT][D / 16][2];
+    float qmax = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            uint2 v = make_uint2(0u, 0u);
+            if (g + 8 * n < G)
+                v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + (head0 + g + 8 * n) * D +
+                                                    t * (D / 4) + 4 * j);
+            qb[n][j][0] = v.x;
+            qb[n][j][1] = v.y;
+            qmax = fmaxf(qmax, fmaxf(fmaxf(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x))),
+                                     fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y)))));
+        }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, x));
+    const int qe = qmax > 0.f && qmax < INFINITY ? max(12, static_cast<int>(__float_as_uint(qmax) >> 23)) : 139;
+    const float qf = __uint_as_float(static_cast<uint32_t>(266 - qe) << 23);  // 2^(139 - qe)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                qb[n][j][i] = pack2<true>(bf16_lo(qb[n][j][i]) * qf, bf16_hi(qb[n][j][i]) * qf);
+    float sl = a.sm_scale * 1.4426950408889634f;
+    if constexpr (kFp4) sl *= a.k_scale[kvh];
+    sl = ldexpf(sl, qe - 139);
+
+    State<D, NT> st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        st.mu[n][0] = st.mu[n][1] = -INFINITY;
+        st.l[n][0] = st.l[n][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.o[n][i][0] = st.o[n][i][1] = st.o[n][i][2] = st.o[n][i][3] = 0.f;
+    }
+    st.vfac = INFINITY;
+
+    int stage = 0, k = 0;
+    uint32_t phase = 0;
+    bool failed = false;
+    for (; k < my_n; ++k) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars[warp][stage], phase))) {
+            failed = true;
+            break;
+        }
+        const uint8_t* kt = ring + stage * C::kStage;
+        attend<D, kFp4, NT>(st, qb, kt, kt + C::kTile, lane, (b0 + warp + k * kWarps) * kBlockSize, lo, ctx, sl);
+        __syncwarp();  // every lane's reads of the stage are done
+        load(k + C::kStages, stage);
+        if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    if (failed) {
+        // the copies in flight land before the CTA leaves (bounded waits)
+        for (int kk = k; kk < min(my_n, k + C::kStages); ++kk)
+            (void)mbar_wait(&bars[warp][kk % C::kStages], (kk / C::kStages) & 1);
+        if (lane == 0) {
+            flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            atomicOr(&s_flag, 1);
+        }
+    }
+
+    // ---- the 4 warps' states meet
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) st.l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, st.l[n][c], x);
+    __syncthreads();  // every warp is done with its ring
+    float* comb = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int h = 2 * t + c + 8 * n;
+            float* cw = comb + (warp * C::kHeads + h) * C::kCombStride + g * (D / 8);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                *reinterpret_cast<float2*>(cw + 2 * i) = make_float2(st.o[n][i][c], st.o[n][i][c + 2]);
+            if (g == 0) {
+                s_m[warp][h] = st.mu[n][c];
+                s_l[warp][h] = st.l[n][c];
+            }
+        }
+    if (lane == 0) s_v[warp] = kFp4 || st.vfac == INFINITY ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(st.vfac));
+    __syncthreads();
+    const bool cta_failed = s_flag != 0;
+    const size_t pair = static_cast<size_t>(seq) * a.hkv + kvh;
+    if (threadIdx.x < G) {
+        // per head: the warps' weights 2^(mu_w - M) / L, V's scale folded in,
+        // replace s_m; the chunk's lse goes to s_l[0]
+        const int h = threadIdx.x;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
+        float f[kWarps], L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            f[w] = s_m[w][h] == -INFINITY ? 0.f : fast_exp2(s_m[w][h] - M);
+            L += f[w] * s_l[w][h];
+        }
+        float lse = !cta_failed && L != 0.f ? M * 0.6931471805599453f + logf(L) : -INFINITY;
+        float inv = !cta_failed && L != 0.f ? (kFp4 ? a.v_scale[kvh] : 1.f) / L : 0.f;
+        if (a.sinks && nsplit == 1) {
+            // lse' = ln(e^lse + e^sink), o scaled by e^(lse - lse')
+            const float sk = a.sinks[kvh * G + h];
+            const float hi = fmaxf(lse, sk);
+            const float both = hi == -INFINITY ? hi : hi + logf(expf(lse - hi) + expf(sk - hi));
+            if (lse != -INFINITY) inv *= expf(lse - both);
+            lse = both;
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s_m[w][h] = f[w] == 0.f ? 0.f : f[w] * inv * s_v[w];
+        s_l[0][h] = lse;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), d = 4 * (i % (D / 4));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!cta_failed) {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float wt = s_m[w][h];
+                const float4 x = *reinterpret_cast<const float4*>(comb + (w * C::kHeads + h) * C::kCombStride + d);
+                v.x += wt * x.x;
+                v.y += wt * x.y;
+                v.z += wt * x.z;
+                v.w += wt * x.w;
+            }
+        }
+        if (nsplit == 1) {
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
+                make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+            if (a.lse_out && d == 0) a.lse_out[head0 + h] = s_l[0][h];
+        } else {
+            const size_t prow = (pair * a.max_splits + split) * G + h;
+            *reinterpret_cast<float4*>(a.part_o + prow * D + d) = v;
+            if (d == 0) a.part_lse[prow] = s_l[0][h];
+        }
+    }
+    if (nsplit == 1) return;
+
+    // ---- the last chunk of this (sequence, KV head) to arrive joins them all
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s_flag = static_cast<int>(atomicAdd(&a.counters[pair], 1u));
+    __syncthreads();
+    if (s_flag != nsplit - 1) return;
+    __threadfence();
+    float* wts = reinterpret_cast<float*>(smem);  // [nsplit][16], then the rows' sums
+    float* row_inv = wts + a.max_splits * 16;
+    {
+        const int h = threadIdx.x >> 3, sub = threadIdx.x & 7;  // 16 heads x 8 threads
+        const float* pl = a.part_lse + pair * a.max_splits * G + h;
+        float M = -INFINITY;
+        if (h < G)
+            for (int i = sub; i < nsplit; i += 8) M = fmaxf(M, __ldcg(pl + static_cast<size_t>(i) * G));
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
+        const float sk = a.sinks && h < G ? a.sinks[kvh * G + h] : -INFINITY;
+        M = fmaxf(M, sk);
+        float W = 0.f;
+        if (h < G)
+            for (int i = sub; i < nsplit; i += 8) {
+                const float l = __ldcg(pl + static_cast<size_t>(i) * G);
+                const float w = l == -INFINITY ? 0.f : expf(l - M);
+                wts[i * 16 + h] = w;
+                W += w;
+            }
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) W += __shfl_xor_sync(0xFFFFFFFFu, W, x);
+        if (sub == 0 && h < G) {
+            if (sk != -INFINITY) W += expf(sk - M);
+            row_inv[h] = W != 0.f ? 1.f / W : 0.f;
+            if (a.lse_out) a.lse_out[head0 + h] = W != 0.f ? M + logf(W) : -INFINITY;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), d = 4 * (i % (D / 4));
+        const float* po = a.part_o + (pair * a.max_splits * G + h) * D + d;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = 0; c < nsplit; ++c) {
+            const float w = wts[c * 16 + h];
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(c) * G * D));
+            if (w != 0.f) {
+                v.x += w * x.x;
+                v.y += w * x.y;
+                v.z += w * x.z;
+                v.w += w * x.w;
+            }
+        }
+        const float inv = row_inv[h];
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
+            make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
+    }
+    if (threadIdx.x == 0) a.counters[pair] = 0u;
+}
+
+template <int D, bool kFp4, int NT>
+cudaError_t launch_t(const QuantDecodeArgs& a, cudaStream_t stream) {
+    using C = Cfg<D, kFp4, NT>;
+    static_assert(C::kSmem <= 227 * 1024, "shared memory budget");
+    static_assert((kQuantMaxSplits + 1) * 16 * 4 <= C::kSmem - 128, "merge weights");
+    auto kern = quant_decode_kernel<D, kFp4, NT>;
+    // a per-device function attribute, set on the first launch on each device
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    return launch_pdl(kern, dim3(a.max_splits, a.hkv, a.num_seqs), dim3(kThreads), C::kSmem, stream, a);
 }
 
 template <int D, bool kFp4>
-cudaError_t launch_t(const QuantDecodeArgs& a, cudaStream_t stream) {
-    return launch_pdl(quant_decode_kernel<D, kFp4>, dim3((a.hq + 3) / 4, a.num_seqs), dim3(128), 0, stream, a);
+cudaError_t launch_g(const QuantDecodeArgs& a, cudaStream_t stream) {
+    return a.group <= 8 ? launch_t<D, kFp4, 1>(a, stream) : launch_t<D, kFp4, 2>(a, stream);
 }
 
 }  // namespace
 
+int quant_decode_ctas(int d, int fp4, int group) {
+    const bool two = group > 8;
+    if (d == 64) return two ? Cfg<64, true, 2>::kCtas : Cfg<64, true, 1>::kCtas;
+    (void)fp4;
+    return two ? Cfg<128, true, 2>::kCtas : Cfg<128, true, 1>::kCtas;
+}
+
 cudaError_t launch_quant_decode(const QuantDecodeArgs& a, cudaStream_t stream) {
-    if (a.d == 64) return a.fp4 ? launch_t<64, true>(a, stream) : launch_t<64, false>(a, stream);
-    return a.fp4 ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);
+    if (a.d == 64) return a.fp4 ? launch_g<64, true>(a, stream) : launch_g<64, false>(a, stream);
+    return a.fp4 ? launch_g<128, true>(a, stream) : launch_g<128, false>(a, stream);
 }
 
 }  // namespace pkv
