@@ -73,18 +73,4 @@ __device__ __forceinline__ uint32_t fp4x2_to_f16x2(uint32_t byte) {
     return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
 
-// Value of dim d of a record's row.
-template <int D, bool kFp4>
-__device__ __forceinline__ float quant_value(const uint8_t* rec, int row, int d, float g) {
-    using R = QuantRecord<D, kFp4>;
-    if constexpr (kFp4) {
-        const uint32_t v2 = fp4x2_to_f16x2(rec[quant_byte<R::kRowBytes>(row, d / 2)]);
-        const float v = __half2float(__ushort_as_half(static_cast<unsigned short>((d & 1) ? v2 >> 16 : v2 & 0xFFFFu)));
-        return __fmul_rn(v * e4m3_float(rec[R::kScales + row * R::kScaleBytes + d / 16]), g);
-    } else {
-        const float sc = *reinterpret_cast<const float*>(rec + R::kScales + row * 4);
-        return __fmul_rn(static_cast<float>(rec[quant_byte<R::kRowBytes>(row, d)]) - 128.f, sc);
-    }
-}
-
 }  // namespace pkv

@@ -1,5 +1,11 @@
 // rope_quant.cu -- rotary positions in both pair layouts, and the quantised
 // pools' append, row read and block widening (formats: include/pkv.h).
+//
+// All four move bytes: each lane handles 16 bytes of 16-bit values (8 dims) at a
+// time, so that a warp's loads and stores of a row are whole lines, and several
+// rows per thread, all loads ahead of the first use, so that enough bytes are in
+// flight.  The rotation's (cos, sin) pairs are read once per thread and used for
+// all of its rows.
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -8,9 +14,7 @@ namespace pkv {
 
 namespace {
 
-// ------------------------------------------------------------- rotation --
-//
-// One thread per (token, head, element pair or passing element).
+// ---------------------------------------------------------- conversions --
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T x) {
@@ -31,13 +35,131 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
     return __float2bfloat16_rn(x);
 }
 
+// The 16 / sizeof(T) elements of a 16-byte vector.
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[N]) {
+    static_assert(N * sizeof(T) == 16, "one vector");
+    const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f32(e[i]);
+}
+template <typename T, int N>
+__device__ __forceinline__ uint4 pack(const float (&x)[N]) {
+    uint4 v;
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = from_f32<T>(x[i]);
+    return v;
+}
+
 // x' = (a c - b s, b c + a s), each op rounded
 __device__ __forceinline__ float2 turn(float a, float b, float c, float s) {
     return make_float2(__fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)), __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
 }
 
+// ------------------------------------------------------------- rotation --
+//
+// Rows by strides.  A thread takes one vector position of kRows heads of a token:
+// with half-split pairs the vectors at j and j + r/2, with interleaved pairs one
+// vector; positions past the rotary dims copy a vector (out of place only).
+
+struct RotateRow {
+    const uint8_t* in;
+    uint8_t* out;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) rope_rotate_kernel(RotateArgs a) {
+__device__ __forceinline__ RotateRow rotate_row(const RotateArgs& a, long long i, int h) {
+    const bool is_k = h >= a.q.num_heads;
+    const RotateRows& r = is_k ? a.k : a.q;
+    if (is_k) h -= a.q.num_heads;
+    return RotateRow{static_cast<const uint8_t*>(r.in) + (i * r.in_token + h * r.in_head) * static_cast<long long>(sizeof(T)),
+                     static_cast<uint8_t*>(r.out) + (i * r.out_token + h * r.out_head) * static_cast<long long>(sizeof(T))};
+}
+
+template <typename T, bool kHalf, int kRows>
+__global__ void __launch_bounds__(256) rope_vector_kernel(RotateArgs a, int vectors, int slots, int first_token) {
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int N = 16 / sizeof(T);
+    constexpr int kPairs = kHalf ? N : N / 2;
+    const unsigned idx = blockIdx.x * 256u + threadIdx.x;
+    const int v = static_cast<int>(idx % vectors);
+    const unsigned rest = idx / vectors;
+    const int slot = static_cast<int>(rest % slots);
+    const long long i = first_token + static_cast<long long>(rest / slots);
+    if (i >= a.num_tokens) return;
+    const int heads = a.q.num_heads + a.k.num_heads;
+    const int h0 = slot * kRows;
+    const int p = a.positions[i];
+    if (p < 0) return;
+    if (p >= a.max_pos) {
+        if (v == 0 && slot == 0) flag_error(a.err, PKV_DEVERR_POSITION);
+        return;
+    }
+    const int half = a.rotary / 2;
+    const int turns = kHalf ? half / N : a.rotary / N;  // vector positions that rotate
+    if (v >= turns) {
+        const int at = (a.rotary + (v - turns) * N) * static_cast<int>(sizeof(T));
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            if (h0 + r < heads) {
+                const RotateRow row = rotate_row<T>(a, i, h0 + r);
+                if (row.in != row.out) *reinterpret_cast<uint4*>(row.out + at) = *reinterpret_cast<const uint4*>(row.in + at);
+            }
+        return;
+    }
+    uint4 x[kRows], y[kHalf ? kRows : 1];
+    const int at = v * 16, mate = at + half * static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (h0 + r < heads) {
+            const RotateRow row = rotate_row<T>(a, i, h0 + r);
+            x[r] = *reinterpret_cast<const uint4*>(row.in + at);
+            if constexpr (kHalf) y[r] = *reinterpret_cast<const uint4*>(row.in + mate);
+        }
+    float c[kPairs], s[kPairs];
+    const float4* cs = reinterpret_cast<const float4*>(a.cos_sin + (static_cast<size_t>(p) * half + v * kPairs) * 2);
+#pragma unroll
+    for (int j = 0; j < kPairs; j += 2) {
+        const float4 t = cs[j / 2];
+        c[j] = t.x;
+        s[j] = a.inverse ? -t.y : t.y;
+        c[j + 1] = t.z;
+        s[j + 1] = a.inverse ? -t.w : t.w;
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (h0 + r < heads) {
+            const RotateRow row = rotate_row<T>(a, i, h0 + r);
+            float f[N];
+            unpack<T>(x[r], f);
+            if constexpr (kHalf) {
+                float g[N];
+                unpack<T>(y[r], g);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float2 z = turn(f[j], g[j], c[j], s[j]);
+                    f[j] = z.x;
+                    g[j] = z.y;
+                }
+                *reinterpret_cast<uint4*>(row.out + mate) = pack<T>(g);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; j += 2) {
+                    const float2 z = turn(f[j], f[j + 1], c[j / 2], s[j / 2]);
+                    f[j] = z.x;
+                    f[j + 1] = z.y;
+                }
+            }
+            *reinterpret_cast<uint4*>(row.out + at) = pack<T>(f);
+        }
+}
+
+// Rows that no 16-byte vector fits (their address, stride, rotary or head dims):
+// one thread per (token, head, pair or passing element).
+template <typename T>
+__global__ void __launch_bounds__(256) rope_scalar_kernel(RotateArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int half = a.rotary / 2;
@@ -47,7 +169,6 @@ __global__ void __launch_bounds__(256) rope_rotate_kernel(RotateArgs a) {
     const long long row = idx / items;
     const int heads = a.q.num_heads + a.k.num_heads;
     const long long i = row / heads;
-    int h = static_cast<int>(row % heads);
     if (i >= a.num_tokens) return;
     const int p = a.positions[i];
     if (p < 0) return;
@@ -55,11 +176,9 @@ __global__ void __launch_bounds__(256) rope_rotate_kernel(RotateArgs a) {
         if (it == 0) flag_error(a.err, PKV_DEVERR_POSITION);
         return;
     }
-    const bool is_k = h >= a.q.num_heads;
-    const RotateRows& r = is_k ? a.k : a.q;
-    if (is_k) h -= a.q.num_heads;
-    const T* in = static_cast<const T*>(r.in) + i * r.in_token + h * r.in_head;
-    T* out = static_cast<T*>(r.out) + i * r.out_token + h * r.out_head;
+    const RotateRow r = rotate_row<T>(a, i, static_cast<int>(row % heads));
+    const T* in = reinterpret_cast<const T*>(r.in);
+    T* out = reinterpret_cast<T*>(r.out);
     if (it >= half) {
         out[it + half] = in[it + half];
         return;
@@ -74,15 +193,15 @@ __global__ void __launch_bounds__(256) rope_rotate_kernel(RotateArgs a) {
 
 // --------------------------------------------------------------- append --
 //
-// One warp per (token, row); rows are the Hkv K heads, the Hkv V heads and
-// the Hq query heads.  Lane l owns dims [l D/32, (l + 1) D/32).
+// D/8 lanes per row, 8 dims each; rows are the Hq query heads, the Hkv K heads
+// and the Hkv V heads of a token, kRows consecutive ones per thread.
 
 // The block and slot of a token: false for padding and for a bad position or
 // block id (flagged by `report`).
-__device__ __forceinline__ bool quant_slot(const QuantArgs& a, int i, bool report, int* blk, int* row) {
+__device__ __forceinline__ bool quant_slot(const QuantArgs& a, long long i, bool report, int* blk, int* row) {
     const int s = a.token_to_seq[i];
-    if (s < 0) return false;
     const int p = a.positions[i];
+    if (s < 0) return false;
     const int tb = a.ring > 0 ? (p / kBlockSize) % a.ring : p / kBlockSize;
     if (s >= a.num_seqs || p < 0 || tb >= a.mbps || (a.cos_sin != nullptr && p >= a.max_pos)) {
         if (report) flag_error(a.err, PKV_DEVERR_POSITION);
@@ -97,124 +216,270 @@ __device__ __forceinline__ bool quant_slot(const QuantArgs& a, int i, bool repor
     return true;
 }
 
+// 8 dims of a K or V row (dims 8 lane .. 8 lane + 7 of the row's lanes) into its record.
 template <int D, bool kFp4>
-__global__ void __launch_bounds__(256) quant_append_kernel(QuantArgs a) {
+__device__ __forceinline__ void store_row(uint8_t* rec, int row, int lane, const float (&v)[8], float g, bool ok) {
+    using R = QuantRecord<D, kFp4>;
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_magnitude(v[e]));
+    if constexpr (kFp4) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        const uint32_t sc = fp4_scale_code(amax, g);
+        const float t = __fmul_rn(e4m3_float(sc), g);
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) w |= fp4_pair(fp4_quotient(v[e], t), fp4_quotient(v[e + 1], t)) << (4 * e);
+        if (ok) {
+            *reinterpret_cast<uint32_t*>(rec + quant_byte<R::kRowBytes>(row, 4 * lane)) = w;
+            if (!(lane & 1)) rec[R::kScales + row * R::kScaleBytes + lane / 2] = static_cast<uint8_t>(sc);
+        }
+    } else {
+#pragma unroll
+        for (int o = 1; o < D / 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        const float sc = __fdiv_rn(amax, 127.f);
+        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e / 4] |= int8_code(v[e], sc) << (8 * (e % 4));
+        if (ok) {
+            *reinterpret_cast<uint2*>(rec + quant_byte<R::kRowBytes>(row, 8 * lane)) = make_uint2(w[0], w[1]);
+            if (lane == 0) *reinterpret_cast<float*>(rec + R::kScales + row * 4) = sc;
+        }
+    }
+}
+
+template <int D, bool kFp4, int kRows>
+__global__ void __launch_bounds__(256) quant_append_kernel(QuantArgs a, int slots) {
     pdl_wait();
     pdl_launch_dependents();
     using R = QuantRecord<D, kFp4>;
-    constexpr int E = D / 32;  // dims of a lane
-    const int lane = threadIdx.x & 31;
-    const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int rows = 2 * a.hkv + (a.q ? a.hq : 0);
-    const long long i = w / rows;
-    int r = static_cast<int>(w % rows);
-    if (i >= a.num_tokens) return;
-    int blk, row;
-    if (!quant_slot(a, static_cast<int>(i), lane == 0, &blk, &row)) return;
-    const int p = a.positions[i];
-    const bool is_k = r < a.hkv, is_q = r >= 2 * a.hkv;
-    const int h = is_q ? r - 2 * a.hkv : is_k ? r : r - a.hkv;
-    const __nv_bfloat16* x =
-        is_q ? static_cast<const __nv_bfloat16*>(a.q) + i * a.q_stride + static_cast<size_t>(h) * D
-             : static_cast<const __nv_bfloat16*>(is_k ? a.k_new : a.v_new) + i * a.new_stride + static_cast<size_t>(h) * D;
-    float v[E];
+    constexpr int kLanes = D / 8;
+    const int lane = threadIdx.x % kLanes;
+    const long long group = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+    const long long i = group / slots;
+    const int r0 = static_cast<int>(group % slots) * kRows;
+    const int hq = a.q ? a.hq : 0;
+    const int rows = hq + 2 * a.hkv;
+    const int d0 = 8 * lane;
+    // every lane stays to the end: rows share shuffles with their warp
+    int blk = 0, row = 0, p = 0;
+    bool ok = i < a.num_tokens;
+    if (ok) {
+        ok = quant_slot(a, i, lane == 0 && r0 == 0, &blk, &row);
+        p = a.positions[i];
+    }
+    uint4 x[kRows], y[kRows];
     const int half = a.rotary / 2;
+    const bool rope = a.cos_sin != nullptr && d0 < a.rotary;
+    // half-split pairs whose partners fill an aligned vector too
+    const bool mates = rope && !a.interleaved && a.rotary % 16 == 0;
+    const int mate = d0 < half ? d0 + half : d0 - half;
+    auto source = [&](int r) {
+        return r < hq ? static_cast<const __nv_bfloat16*>(a.q) + i * a.q_stride + static_cast<size_t>(r) * D
+               : r < hq + a.hkv
+                   ? static_cast<const __nv_bfloat16*>(a.k_new) + i * a.new_stride + static_cast<size_t>(r - hq) * D
+                   : static_cast<const __nv_bfloat16*>(a.v_new) + i * a.new_stride + static_cast<size_t>(r - hq - a.hkv) * D;
+    };
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int d = lane * E + e;
-        v[e] = __bfloat162float(x[d]);
-        if (a.cos_sin && (is_k || is_q) && d < a.rotary) {
-            const bool second = a.interleaved ? (d & 1) : d >= half;
-            const int j = a.interleaved ? d >> 1 : second ? d - half : d;
-            const int mate = a.interleaved ? d ^ 1 : second ? d - half : d + half;
-            const float* cs = a.cos_sin + (static_cast<size_t>(p) * half + j) * 2;
-            const float m = __bfloat162float(x[mate]);
-            const float s = a.inverse ? -cs[1] : cs[1];
-            v[e] = second ? turn(m, v[e], cs[0], s).y : turn(v[e], m, cs[0], s).x;
+    for (int n = 0; n < kRows; ++n) {
+        x[n] = y[n] = make_uint4(0u, 0u, 0u, 0u);
+        const int r = r0 + n;
+        if (ok && r < rows) {
+            const __nv_bfloat16* src = source(r);
+            x[n] = *reinterpret_cast<const uint4*>(src + d0);
+            if (mates && r < hq + a.hkv) y[n] = *reinterpret_cast<const uint4*>(src + mate);
         }
     }
-    __syncwarp();  // q in place: every lane has read its pairs
-    if (is_q) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.q_out) + i * a.q_out_stride + static_cast<size_t>(h) * D;
+    // (cos, sin) of this lane's dims: pair j of dim d0 + e is d0 + e (or less r/2) when
+    // half-split, (d0 + e) / 2 when interleaved
+    float c[8], sn[8];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[lane * E + e] = __float2bfloat16_rn(v[e]);
-        return;
+    for (int e = 0; e < 8; ++e) {
+        c[e] = 1.f;
+        sn[e] = 0.f;
     }
-    uint8_t* rec = static_cast<uint8_t*>(is_k ? a.k_pool : a.v_pool) + (static_cast<size_t>(blk) * a.hkv + h) * R::kBytes;
-    float amax = 0.f;
+    if (ok && rope && r0 < hq + a.hkv) {
+        const float* cs = a.cos_sin + static_cast<size_t>(p) * a.rotary;
 #pragma unroll
-    for (int e = 0; e < E; ++e) amax = fmaxf(amax, finite_magnitude(v[e]));
-    if constexpr (kFp4) {
-        constexpr int kLanes = 16 / E;  // lanes of one scale
+        for (int e = 0; e < 8; ++e) {
+            const int d = d0 + e;
+            if (d >= a.rotary) continue;
+            const int j = a.interleaved ? d >> 1 : d < half ? d : d - half;
+            const float2 t = *reinterpret_cast<const float2*>(cs + 2 * j);
+            c[e] = t.x;
+            sn[e] = a.inverse ? -t.y : t.y;
+        }
+    }
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        const float g = (is_k ? a.k_scale : a.v_scale)[h];
-        const uint32_t sc = fp4_scale_code(amax, g);
-        const float t = __fmul_rn(e4m3_float(sc), g);
+    for (int n = 0; n < kRows; ++n) {
+        const int r = r0 + n;
+        const bool live = ok && r < rows;
+        float v[8];
+        unpack<__nv_bfloat16>(x[n], v);
+        if (rope && r < hq + a.hkv) {
+            if (a.interleaved) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            rec[quant_byte<R::kRowBytes>(row, (lane * E + e) / 2)] =
-                static_cast<uint8_t>(fp4_pair(fp4_quotient(v[e], t), fp4_quotient(v[e + 1], t)));
-        if (lane % kLanes == 0) rec[R::kScales + row * R::kScaleBytes + lane / kLanes] = static_cast<uint8_t>(sc);
-    } else {
+                for (int e = 0; e < 8; e += 2)
+                    if (d0 + e < a.rotary) {
+                        const float2 z = turn(v[e], v[e + 1], c[e], sn[e]);
+                        v[e] = z.x;
+                        v[e + 1] = z.y;
+                    }
+            } else {
+                float m[8];
+                unpack<__nv_bfloat16>(y[n], m);
+                if (!mates && live) {
+                    const __nv_bfloat16* src = source(r);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        const float sc = __fdiv_rn(amax, 127.f);
+                    for (int e = 0; e < 8; ++e)
+                        if (d0 + e < a.rotary) m[e] = __bfloat162float(src[d0 + e < half ? d0 + e + half : d0 + e - half]);
+                }
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            rec[quant_byte<R::kRowBytes>(row, lane * E + e)] = static_cast<uint8_t>(int8_code(v[e], sc));
-        if (lane == 0) *reinterpret_cast<float*>(rec + R::kScales + row * 4) = sc;
+                for (int e = 0; e < 8; ++e)
+                    if (d0 + e < a.rotary)
+                        v[e] = d0 + e < half ? turn(v[e], m[e], c[e], sn[e]).x : turn(m[e], v[e], c[e], sn[e]).y;
+            }
+        }
+        __syncwarp();  // q in place: the row's lanes have read their pairs
+        if (r < hq) {
+            if (live)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) + i * a.q_out_stride +
+                                          static_cast<size_t>(r) * D + d0) = pack<__nv_bfloat16>(v);
+        }
+        // rows of one warp may be of different kinds: the shuffles below are
+        // for all of them, the stores for K and V rows
+        const bool is_k = r < hq + a.hkv;
+        const int h = is_k ? r - hq : r - hq - a.hkv;
+        const bool kv = live && r >= hq;
+        if (__any_sync(0xFFFFFFFFu, kv)) {
+            uint8_t* rec = nullptr;
+            float g = 1.f;
+            if (kv) {
+                rec = static_cast<uint8_t*>(is_k ? a.k_pool : a.v_pool) + (static_cast<size_t>(blk) * a.hkv + h) * R::kBytes;
+                if constexpr (kFp4) g = (is_k ? a.k_scale : a.v_scale)[h];
+            }
+            store_row<D, kFp4>(rec, row, lane, v, g, kv);
+        }
     }
 }
 
 // ----------------------------------------------------------------- read --
 
+// 8 values of a record's row (dims 8 lane ..), each rounded to fp32 once.
+template <int D, bool kFp4>
+struct RowPart {
+    uint2 codes;  // 4-bit: codes.x
+    float scale;
+};
+
+template <int D, bool kFp4>
+__device__ __forceinline__ RowPart<D, kFp4> fetch_row(const uint8_t* rec, int row, int lane) {
+    using R = QuantRecord<D, kFp4>;
+    RowPart<D, kFp4> p;
+    if constexpr (kFp4) {
+        p.codes.x = *reinterpret_cast<const uint32_t*>(rec + quant_byte<R::kRowBytes>(row, 4 * lane));
+        p.scale = __uint_as_float(rec[R::kScales + row * R::kScaleBytes + lane / 2]);  // its code, widened below
+    } else {
+        p.codes = *reinterpret_cast<const uint2*>(rec + quant_byte<R::kRowBytes>(row, 8 * lane));
+        p.scale = *reinterpret_cast<const float*>(rec + R::kScales + row * 4);
+    }
+    return p;
+}
+
+template <int D, bool kFp4>
+__device__ __forceinline__ void widen_row(const RowPart<D, kFp4>& p, float g, float (&v)[8]) {
+    if constexpr (kFp4) {
+        const float e = e4m3_float(__float_as_uint(p.scale));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t f = fp4x2_to_f16x2((p.codes.x >> (8 * i)) & 0xFFu);
+            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&f));
+            v[2 * i] = __fmul_rn(z.x * e, g);
+            v[2 * i + 1] = __fmul_rn(z.y * e, g);
+        }
+    } else {
+        (void)g;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t u = ((i < 4 ? p.codes.x : p.codes.y) >> (8 * (i % 4))) & 0xFFu;
+            v[i] = __fmul_rn(static_cast<float>(u) - 128.f, p.scale);
+        }
+    }
+}
+
+// D/8 lanes per (token, head), K and V of it in one thread.
 template <int D, bool kFp4>
 __global__ void __launch_bounds__(256) quant_read_kernel(QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int d = static_cast<int>(idx % D);
-    const int h = static_cast<int>((idx / D) % a.hkv);
-    const long long i = idx / D / a.hkv;
+    constexpr int kLanes = D / 8;
+    const int lane = threadIdx.x % kLanes;
+    const long long group = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+    const long long i = group / a.hkv;
+    const int h = static_cast<int>(group % a.hkv);
     if (i >= a.num_tokens) return;
     int blk, row;
-    if (!quant_slot(a, static_cast<int>(i), d == 0, &blk, &row)) return;
+    if (!quant_slot(a, i, lane == 0 && h == 0, &blk, &row)) return;
     const size_t at = (static_cast<size_t>(blk) * a.hkv + h) * QuantRecord<D, kFp4>::kBytes;
-    const size_t to = (static_cast<size_t>(i) * a.hkv + h) * D + d;
+    RowPart<D, kFp4> part[2];
+#pragma unroll
+    for (int pool = 0; pool < 2; ++pool)
+        if (pool ? a.v_out : a.k_out)
+            part[pool] = fetch_row<D, kFp4>(static_cast<const uint8_t*>(pool ? a.v_pool : a.k_pool) + at, row, lane);
+    const size_t to = (static_cast<size_t>(i) * a.hkv + h) * D + 8 * lane;
 #pragma unroll
     for (int pool = 0; pool < 2; ++pool) {
-        const void* src = pool ? a.v_pool : a.k_pool;
         void* dst = pool ? a.v_out : a.k_out;
         if (!dst) continue;
-        const float g = kFp4 ? (pool ? a.v_scale : a.k_scale)[h] : 1.f;
-        const float v = quant_value<D, kFp4>(static_cast<const uint8_t*>(src) + at, row, d, g);
-        if (a.out_f32)
-            static_cast<float*>(dst)[to] = v;
-        else
-            static_cast<__nv_bfloat16*>(dst)[to] = __float2bfloat16_rn(v);
+        float v[8];
+        widen_row<D, kFp4>(part[pool], kFp4 ? (pool ? a.v_scale : a.k_scale)[h] : 1.f, v);
+        if (a.out_f32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + to);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + to) = pack<__nv_bfloat16>(v);
+        }
     }
 }
 
-template <int D, bool kFp4>
-__global__ void __launch_bounds__(256) quant_load_kernel(QuantArgs a) {
+// A CTA per (pair, kHeads heads): thread (row, lane) widens 8 dims of each of
+// their records, K and V.
+template <int D, bool kFp4, int kHeads>
+__global__ void __launch_bounds__(2 * D) quant_load_kernel(QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int i = blockIdx.x;
-    const int h = blockIdx.y;
-    const int src = a.src_blocks[i], dst = a.dst_blocks[i];
+    constexpr int kLanes = D / 8;
+    const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+    const int src = a.src_blocks[blockIdx.x], dst = a.dst_blocks[blockIdx.x];
     if (src < 0 || src >= a.num_blocks || dst < 0 || dst >= a.dst_num_blocks) {
         if (threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
         return;
     }
-    const uint8_t* rec = static_cast<const uint8_t*>(blockIdx.z ? a.v_pool : a.k_pool) +
-                         (static_cast<size_t>(src) * a.hkv + h) * QuantRecord<D, kFp4>::kBytes;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(blockIdx.z ? a.v_out : a.k_out) +
-                         (static_cast<size_t>(dst) * a.hkv + h) * kBlockSize * D;
-    const float g = kFp4 ? (blockIdx.z ? a.v_scale : a.k_scale)[h] : 1.f;
-    for (int e = threadIdx.x; e < kBlockSize * D; e += blockDim.x)
-        out[e] = __float2bfloat16_rn(quant_value<D, kFp4>(rec, e / D, e % D, g));
+    const int h0 = blockIdx.y * kHeads;
+    RowPart<D, kFp4> part[2][kHeads];
+#pragma unroll
+    for (int n = 0; n < kHeads; ++n)
+#pragma unroll
+        for (int pool = 0; pool < 2; ++pool)
+            if (h0 + n < a.hkv)
+                part[pool][n] = fetch_row<D, kFp4>(static_cast<const uint8_t*>(pool ? a.v_pool : a.k_pool) +
+                                                       (static_cast<size_t>(src) * a.hkv + h0 + n) * QuantRecord<D, kFp4>::kBytes,
+                                                   row, lane);
+#pragma unroll
+    for (int n = 0; n < kHeads; ++n)
+#pragma unroll
+        for (int pool = 0; pool < 2; ++pool)
+            if (h0 + n < a.hkv) {
+                float v[8];
+                widen_row<D, kFp4>(part[pool][n], kFp4 ? (pool ? a.v_scale : a.k_scale)[h0 + n] : 1.f, v);
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(pool ? a.v_out : a.k_out) +
+                                     ((static_cast<size_t>(dst) * a.hkv + h0 + n) * kBlockSize + row) * D + 8 * lane;
+                *reinterpret_cast<uint4*>(out) = pack<__nv_bfloat16>(v);
+            }
 }
+
+// ------------------------------------------------------------- launches --
 
 cudaError_t grid_of(long long threads, dim3* grid) {
     const long long blocks = (threads + 255) / 256;
@@ -222,6 +487,8 @@ cudaError_t grid_of(long long threads, dim3* grid) {
     *grid = dim3(static_cast<unsigned>(blocks));
     return cudaSuccess;
 }
+
+constexpr long long kBusyThreads = 152LL * 512;  // 16 warps an SM: enough to give a thread more rows
 
 template <template <int, bool> class F>
 cudaError_t by_format(const QuantArgs& a) {
@@ -231,24 +498,75 @@ cudaError_t by_format(const QuantArgs& a) {
 
 template <int D, bool kFp4>
 struct AppendLaunch {
-    static cudaError_t go(const QuantArgs& a) {
+    template <int kRows>
+    static cudaError_t rows(const QuantArgs& a, int rows) {
+        const int slots = (rows + kRows - 1) / kRows;
         dim3 grid;
-        const cudaError_t e = grid_of(32LL * a.num_tokens * (2 * a.hkv + (a.q ? a.hq : 0)), &grid);
-        return e != cudaSuccess ? e : launch_pdl(quant_append_kernel<D, kFp4>, grid, dim3(256), 0, a.stream, a);
+        const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * slots * (D / 8), &grid);
+        return e != cudaSuccess ? e : launch_pdl(quant_append_kernel<D, kFp4, kRows>, grid, dim3(256), 0, a.stream, a, slots);
+    }
+    static cudaError_t go(const QuantArgs& a) {
+        const int n = 2 * a.hkv + (a.q ? a.hq : 0);
+        return static_cast<long long>(a.num_tokens) * n * (D / 8) >= 4 * kBusyThreads ? rows<4>(a, n) : rows<1>(a, n);
     }
 };
 template <int D, bool kFp4>
 struct ReadLaunch {
     static cudaError_t go(const QuantArgs& a) {
         dim3 grid;
-        const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * a.hkv * D, &grid);
+        const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * a.hkv * (D / 8), &grid);
         return e != cudaSuccess ? e : launch_pdl(quant_read_kernel<D, kFp4>, grid, dim3(256), 0, a.stream, a);
     }
 };
 template <int D, bool kFp4>
 struct LoadLaunch {
     static cudaError_t go(const QuantArgs& a) {
-        return launch_pdl(quant_load_kernel<D, kFp4>, dim3(a.num_tokens, a.hkv, 2), dim3(256), 0, a.stream, a);
+        if (static_cast<long long>(a.num_tokens) * a.hkv * 2 * D >= 16 * kBusyThreads)
+            return launch_pdl(quant_load_kernel<D, kFp4, 4>, dim3(a.num_tokens, (a.hkv + 3) / 4), dim3(2 * D), 0, a.stream, a);
+        return launch_pdl(quant_load_kernel<D, kFp4, 1>, dim3(a.num_tokens, a.hkv), dim3(2 * D), 0, a.stream, a);
+    }
+};
+
+template <typename T>
+struct RotateLaunch {
+    static bool vectors_fit(const RotateArgs& a) {
+        constexpr int N = 16 / sizeof(T);
+        auto rows = [](const RotateRows& r) {
+            return r.num_heads == 0 ||
+                   ((reinterpret_cast<uintptr_t>(r.in) | reinterpret_cast<uintptr_t>(r.out)) % 16 == 0 &&
+                    (r.in_token | r.in_head | r.out_token | r.out_head) % N == 0);
+        };
+        return a.d % N == 0 && a.rotary % (a.interleaved ? N : 2 * N) == 0 &&
+               reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0 && rows(a.q) && rows(a.k);
+    }
+    template <bool kHalf, int kRows>
+    static cudaError_t vectors(const RotateArgs& a, int count, cudaStream_t stream) {
+        const int slots = (a.q.num_heads + a.k.num_heads + kRows - 1) / kRows;
+        const long long per_token = static_cast<long long>(count) * slots;
+        const long long most = (0xFFFFFFFFLL - 256) / per_token;  // thread indexes are 32 bits wide
+        for (long long i = 0; i < a.num_tokens; i += most) {
+            const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
+            const cudaError_t e = launch_pdl(rope_vector_kernel<T, kHalf, kRows>, dim3(static_cast<unsigned>((n * per_token + 255) / 256)),
+                                             dim3(256), 0, stream, a, count, slots, static_cast<int>(i));
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
+    template <bool kHalf>
+    static cudaError_t by_rows(const RotateArgs& a, cudaStream_t stream) {
+        constexpr int N = 16 / sizeof(T);
+        const bool in_place = a.q.in == a.q.out && (a.k.num_heads == 0 || a.k.in == a.k.out);
+        const int count = (kHalf ? a.rotary / 2 : a.rotary) / N + (in_place ? 0 : (a.d - a.rotary) / N);
+        const long long one = static_cast<long long>(a.num_tokens) * (a.q.num_heads + a.k.num_heads) * count;
+        if (one >= 4 * kBusyThreads) return vectors<kHalf, 4>(a, count, stream);
+        return vectors<kHalf, 1>(a, count, stream);
+    }
+    static cudaError_t go(const RotateArgs& a, cudaStream_t stream) {
+        if (vectors_fit(a)) return a.interleaved ? by_rows<false>(a, stream) : by_rows<true>(a, stream);
+        dim3 grid;
+        const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * (a.q.num_heads + a.k.num_heads) *
+                                          (a.d - a.rotary / 2), &grid);
+        return e != cudaSuccess ? e : launch_pdl(rope_scalar_kernel<T>, grid, dim3(256), 0, stream, a);
     }
 };
 
@@ -260,14 +578,10 @@ int quant_record_bytes(int d, int fp4) {
 }
 
 cudaError_t launch_rope_rotate(const RotateArgs& a, cudaStream_t stream) {
-    dim3 grid;
-    const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * (a.q.num_heads + a.k.num_heads) *
-                                      (a.d - a.rotary / 2), &grid);
-    if (e != cudaSuccess) return e;
     switch (a.dtype) {
-        case PKV_BF16: return launch_pdl(rope_rotate_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, a);
-        case PKV_F16: return launch_pdl(rope_rotate_kernel<__half>, grid, dim3(256), 0, stream, a);
-        default: return launch_pdl(rope_rotate_kernel<float>, grid, dim3(256), 0, stream, a);
+        case PKV_BF16: return RotateLaunch<__nv_bfloat16>::go(a, stream);
+        case PKV_F16: return RotateLaunch<__half>::go(a, stream);
+        default: return RotateLaunch<float>::go(a, stream);
     }
 }
 
