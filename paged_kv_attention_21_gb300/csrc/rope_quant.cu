@@ -91,33 +91,33 @@ __global__ void __launch_bounds__(256) rope_vector_kernel(RotateArgs a, int vect
     if (i >= a.num_tokens) return;
     const int heads = a.q.num_heads + a.k.num_heads;
     const int h0 = slot * kRows;
-    const int p = a.positions[i];
-    if (p < 0) return;
-    if (p >= a.max_pos) {
-        if (v == 0 && slot == 0) flag_error(a.err, PKV_DEVERR_POSITION);
-        return;
-    }
     const int half = a.rotary / 2;
     const int turns = kHalf ? half / N : a.rotary / N;  // vector positions that rotate
-    if (v >= turns) {
-        const int at = (a.rotary + (v - turns) * N) * static_cast<int>(sizeof(T));
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            if (h0 + r < heads) {
-                const RotateRow row = rotate_row<T>(a, i, h0 + r);
-                if (row.in != row.out) *reinterpret_cast<uint4*>(row.out + at) = *reinterpret_cast<const uint4*>(row.in + at);
-            }
-        return;
-    }
+    const bool pass = v >= turns;
+    // the rows' loads do not wait for the position's
     uint4 x[kRows], y[kHalf ? kRows : 1];
-    const int at = v * 16, mate = at + half * static_cast<int>(sizeof(T));
+    const int at = pass ? (a.rotary + (v - turns) * N) * static_cast<int>(sizeof(T)) : v * 16;
+    const int mate = at + half * static_cast<int>(sizeof(T));
+    const int p = a.positions[i];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
         if (h0 + r < heads) {
             const RotateRow row = rotate_row<T>(a, i, h0 + r);
             x[r] = *reinterpret_cast<const uint4*>(row.in + at);
-            if constexpr (kHalf) y[r] = *reinterpret_cast<const uint4*>(row.in + mate);
+            if constexpr (kHalf)
+                if (!pass) y[r] = *reinterpret_cast<const uint4*>(row.in + mate);
         }
+    if (p < 0) return;
+    if (p >= a.max_pos) {
+        if (v == 0 && slot == 0) flag_error(a.err, PKV_DEVERR_POSITION);
+        return;
+    }
+    if (pass) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            if (h0 + r < heads) *reinterpret_cast<uint4*>(rotate_row<T>(a, i, h0 + r).out + at) = x[r];
+        return;
+    }
     float c[kPairs], s[kPairs];
     const float4* cs = reinterpret_cast<const float4*>(a.cos_sin + (static_cast<size_t>(p) * half + v * kPairs) * 2);
 #pragma unroll
@@ -196,11 +196,9 @@ __global__ void __launch_bounds__(256) rope_scalar_kernel(RotateArgs a) {
 // D/8 lanes per row, 8 dims each; rows are the Hq query heads, the Hkv K heads
 // and the Hkv V heads of a token, kRows consecutive ones per thread.
 
-// The block and slot of a token: false for padding and for a bad position or
+// The block and slot of position p of sequence s: false for padding and for a bad position or
 // block id (flagged by `report`).
-__device__ __forceinline__ bool quant_slot(const QuantArgs& a, long long i, bool report, int* blk, int* row) {
-    const int s = a.token_to_seq[i];
-    const int p = a.positions[i];
+__device__ __forceinline__ bool quant_slot(const QuantArgs& a, int s, int p, bool report, int* blk, int* row) {
     if (s < 0) return false;
     const int tb = a.ring > 0 ? (p / kBlockSize) % a.ring : p / kBlockSize;
     if (s >= a.num_seqs || p < 0 || tb >= a.mbps || (a.cos_sin != nullptr && p >= a.max_pos)) {
@@ -248,7 +246,12 @@ __device__ __forceinline__ void store_row(uint8_t* rec, int row, int lane, const
     }
 }
 
-template <int D, bool kFp4, int kRows>
+// How a row's pairs are found: any rotary dim element by element (or none), or
+// every lane's 8 dims inside the rotary dims or outside them, their partners in one
+// vector (half-split, r a multiple of 16) or in the lane (interleaved, r of 8).
+enum Pairs { kAnyPairs, kHalfPairs, kLanePairs };
+
+template <int D, bool kFp4, int kRows, int kPairs>
 __global__ void __launch_bounds__(256) quant_append_kernel(QuantArgs a, int slots) {
     pdl_wait();
     pdl_launch_dependents();
@@ -259,55 +262,66 @@ __global__ void __launch_bounds__(256) quant_append_kernel(QuantArgs a, int slot
     const long long i = group / slots;
     const int r0 = static_cast<int>(group % slots) * kRows;
     const int hq = a.q ? a.hq : 0;
-    const int rows = hq + 2 * a.hkv;
+    const int turned = hq + a.hkv;  // rows that rotate
+    const int rows = turned + a.hkv;
     const int d0 = 8 * lane;
-    // every lane stays to the end: rows share shuffles with their warp
-    int blk = 0, row = 0, p = 0;
-    bool ok = i < a.num_tokens;
-    if (ok) {
-        ok = quant_slot(a, i, lane == 0 && r0 == 0, &blk, &row);
-        p = a.positions[i];
-    }
-    uint4 x[kRows], y[kRows];
     const int half = a.rotary / 2;
     const bool rope = a.cos_sin != nullptr && d0 < a.rotary;
-    // half-split pairs whose partners fill an aligned vector too
-    const bool mates = rope && !a.interleaved && a.rotary % 16 == 0;
-    const int mate = d0 < half ? d0 + half : d0 - half;
+    const bool second = kPairs == kHalfPairs && d0 >= half;
     auto source = [&](int r) {
         return r < hq ? static_cast<const __nv_bfloat16*>(a.q) + i * a.q_stride + static_cast<size_t>(r) * D
-               : r < hq + a.hkv
-                   ? static_cast<const __nv_bfloat16*>(a.k_new) + i * a.new_stride + static_cast<size_t>(r - hq) * D
-                   : static_cast<const __nv_bfloat16*>(a.v_new) + i * a.new_stride + static_cast<size_t>(r - hq - a.hkv) * D;
+               : r < turned ? static_cast<const __nv_bfloat16*>(a.k_new) + i * a.new_stride + static_cast<size_t>(r - hq) * D
+                            : static_cast<const __nv_bfloat16*>(a.v_new) + i * a.new_stride + static_cast<size_t>(r - turned) * D;
     };
+    // the rows' loads do not wait for the token's slot.  Every lane stays to the
+    // end: rows share shuffles with their warp.
+    uint4 x[kRows], y[kPairs == kHalfPairs ? kRows : 1];
+    const bool in = i < a.num_tokens;
+    int s = -1, p = 0;
+    if (in) {
+        s = a.token_to_seq[i];
+        p = a.positions[i];
+    }
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
-        x[n] = y[n] = make_uint4(0u, 0u, 0u, 0u);
-        const int r = r0 + n;
-        if (ok && r < rows) {
-            const __nv_bfloat16* src = source(r);
+        x[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && r0 + n < rows) {
+            const __nv_bfloat16* src = source(r0 + n);
             x[n] = *reinterpret_cast<const uint4*>(src + d0);
-            if (mates && r < hq + a.hkv) y[n] = *reinterpret_cast<const uint4*>(src + mate);
+            if constexpr (kPairs == kHalfPairs)
+                if (rope && r0 + n < turned) y[n] = *reinterpret_cast<const uint4*>(src + (second ? d0 - half : d0 + half));
         }
     }
-    // (cos, sin) of this lane's dims: pair j of dim d0 + e is d0 + e (or less r/2) when
-    // half-split, (d0 + e) / 2 when interleaved
-    float c[8], sn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        c[e] = 1.f;
-        sn[e] = 0.f;
-    }
-    if (ok && rope && r0 < hq + a.hkv) {
+    int blk = 0, row = 0;
+    const bool ok = in && quant_slot(a, s, p, lane == 0 && r0 == 0, &blk, &row);
+    // (cos, sin) of this lane's dims
+    constexpr int kCs = kPairs == kLanePairs ? 4 : 8;
+    float c[kCs], sn[kCs];
+    if (ok && rope && r0 < turned) {
         const float* cs = a.cos_sin + static_cast<size_t>(p) * a.rotary;
+        if constexpr (kPairs == kAnyPairs) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int d = d0 + e;
-            if (d >= a.rotary) continue;
-            const int j = a.interleaved ? d >> 1 : d < half ? d : d - half;
-            const float2 t = *reinterpret_cast<const float2*>(cs + 2 * j);
-            c[e] = t.x;
-            sn[e] = a.inverse ? -t.y : t.y;
+            for (int e = 0; e < 8; ++e) {
+                const int d = d0 + e;
+                if (d >= a.rotary) continue;
+                const float2 t = *reinterpret_cast<const float2*>(cs + 2 * (a.interleaved ? d >> 1 : d < half ? d : d - half));
+                c[e] = t.x;
+                sn[e] = t.y;
+            }
+        } else {
+            const float4* t4 = reinterpret_cast<const float4*>(cs + (kPairs == kLanePairs ? d0 : 2 * (second ? d0 - half : d0)));
+#pragma unroll
+            for (int e = 0; e < kCs; e += 2) {
+                const float4 t = t4[e / 2];
+                c[e] = t.x;
+                sn[e] = t.y;
+                c[e + 1] = t.z;
+                sn[e + 1] = t.w;
+            }
+        }
+        if (a.inverse) {
+#pragma unroll
+            for (int e = 0; e < kCs; ++e) sn[e] = -sn[e];
         }
     }
 #pragma unroll
@@ -316,42 +330,42 @@ __global__ void __launch_bounds__(256) quant_append_kernel(QuantArgs a, int slot
         const bool live = ok && r < rows;
         float v[8];
         unpack<__nv_bfloat16>(x[n], v);
-        if (rope && r < hq + a.hkv) {
-            if (a.interleaved) {
+        if (live && rope && r < turned) {
+            if constexpr (kPairs == kLanePairs) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2)
-                    if (d0 + e < a.rotary) {
-                        const float2 z = turn(v[e], v[e + 1], c[e], sn[e]);
-                        v[e] = z.x;
-                        v[e + 1] = z.y;
-                    }
-            } else {
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 z = turn(v[e], v[e + 1], c[e / 2], sn[e / 2]);
+                    v[e] = z.x;
+                    v[e + 1] = z.y;
+                }
+            } else if constexpr (kPairs == kHalfPairs) {
                 float m[8];
                 unpack<__nv_bfloat16>(y[n], m);
-                if (!mates && live) {
-                    const __nv_bfloat16* src = source(r);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (d0 + e < a.rotary) m[e] = __bfloat162float(src[d0 + e < half ? d0 + e + half : d0 + e - half]);
+                for (int e = 0; e < 8; ++e) v[e] = second ? turn(m[e], v[e], c[e], sn[e]).y : turn(v[e], m[e], c[e], sn[e]).x;
+            } else {
+                const __nv_bfloat16* src = source(r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int d = d0 + e;
+                    if (d >= a.rotary) continue;
+                    const bool b = a.interleaved ? d & 1 : d >= half;
+                    const float m = __bfloat162float(src[a.interleaved ? d ^ 1 : b ? d - half : d + half]);
+                    v[e] = b ? turn(m, v[e], c[e], sn[e]).y : turn(v[e], m, c[e], sn[e]).x;
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (d0 + e < a.rotary)
-                        v[e] = d0 + e < half ? turn(v[e], m[e], c[e], sn[e]).x : turn(m[e], v[e], c[e], sn[e]).y;
             }
         }
         __syncwarp();  // q in place: the row's lanes have read their pairs
-        if (r < hq) {
-            if (live)
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) + i * a.q_out_stride +
-                                          static_cast<size_t>(r) * D + d0) = pack<__nv_bfloat16>(v);
+        if (live && r < hq) {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) + i * a.q_out_stride + static_cast<size_t>(r) * D +
+                                      d0) = pack<__nv_bfloat16>(v);
         }
-        // rows of one warp may be of different kinds: the shuffles below are
-        // for all of them, the stores for K and V rows
-        const bool is_k = r < hq + a.hkv;
-        const int h = is_k ? r - hq : r - hq - a.hkv;
+        // a warp's rows may be of different kinds: the shuffles below are for all
+        // of them, the stores for K and V rows
         const bool kv = live && r >= hq;
         if (__any_sync(0xFFFFFFFFu, kv)) {
+            const bool is_k = r < turned;
+            const int h = is_k ? r - hq : r - turned;
             uint8_t* rec = nullptr;
             float g = 1.f;
             if (kv) {
@@ -419,7 +433,7 @@ __global__ void __launch_bounds__(256) quant_read_kernel(QuantArgs a) {
     const int h = static_cast<int>(group % a.hkv);
     if (i >= a.num_tokens) return;
     int blk, row;
-    if (!quant_slot(a, i, lane == 0 && h == 0, &blk, &row)) return;
+    if (!quant_slot(a, a.token_to_seq[i], a.positions[i], lane == 0 && h == 0, &blk, &row)) return;
     const size_t at = (static_cast<size_t>(blk) * a.hkv + h) * QuantRecord<D, kFp4>::kBytes;
     RowPart<D, kFp4> part[2];
 #pragma unroll
@@ -498,16 +512,25 @@ cudaError_t by_format(const QuantArgs& a) {
 
 template <int D, bool kFp4>
 struct AppendLaunch {
-    template <int kRows>
+    template <int kRows, int kPairs>
     static cudaError_t rows(const QuantArgs& a, int rows) {
         const int slots = (rows + kRows - 1) / kRows;
         dim3 grid;
         const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * slots * (D / 8), &grid);
-        return e != cudaSuccess ? e : launch_pdl(quant_append_kernel<D, kFp4, kRows>, grid, dim3(256), 0, a.stream, a, slots);
+        return e != cudaSuccess ? e
+                                : launch_pdl(quant_append_kernel<D, kFp4, kRows, kPairs>, grid, dim3(256), 0, a.stream, a, slots);
+    }
+    template <int kPairs>
+    static cudaError_t pairs(const QuantArgs& a) {
+        const int n = 2 * a.hkv + (a.q ? a.hq : 0);
+        return static_cast<long long>(a.num_tokens) * n * (D / 8) >= 4 * kBusyThreads ? rows<2, kPairs>(a, n) : rows<1, kPairs>(a, n);
     }
     static cudaError_t go(const QuantArgs& a) {
-        const int n = 2 * a.hkv + (a.q ? a.hq : 0);
-        return static_cast<long long>(a.num_tokens) * n * (D / 8) >= 4 * kBusyThreads ? rows<4>(a, n) : rows<1>(a, n);
+        if (a.cos_sin && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0) {
+            if (!a.interleaved && a.rotary % 16 == 0) return pairs<kHalfPairs>(a);
+            if (a.interleaved && a.rotary % 8 == 0) return pairs<kLanePairs>(a);
+        }
+        return pairs<kAnyPairs>(a);
     }
 };
 template <int D, bool kFp4>
@@ -555,10 +578,12 @@ struct RotateLaunch {
     template <bool kHalf>
     static cudaError_t by_rows(const RotateArgs& a, cudaStream_t stream) {
         constexpr int N = 16 / sizeof(T);
+        // in place nothing passes (with one of q and k in place, its passing dims
+        // are written back as they are: the same bytes, by the thread that read them)
         const bool in_place = a.q.in == a.q.out && (a.k.num_heads == 0 || a.k.in == a.k.out);
         const int count = (kHalf ? a.rotary / 2 : a.rotary) / N + (in_place ? 0 : (a.d - a.rotary) / N);
         const long long one = static_cast<long long>(a.num_tokens) * (a.q.num_heads + a.k.num_heads) * count;
-        if (one >= 4 * kBusyThreads) return vectors<kHalf, 4>(a, count, stream);
+        if (one >= 4 * kBusyThreads) return vectors<kHalf, kHalf ? 4 : 8>(a, count, stream);
         return vectors<kHalf, 1>(a, count, stream);
     }
     static cudaError_t go(const RotateArgs& a, cudaStream_t stream) {
