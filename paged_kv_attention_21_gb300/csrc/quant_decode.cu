@@ -6,9 +6,9 @@
 //
 // Work decomposition.  The visible blocks of every (sequence, KV head) are cut
 // into chunks (the planner in api.cu); a CTA owns one chunk and its 4 warps
-// take the chunk's blocks round-robin, each with its own ring of bulk copies (a
-// K record and a V record per stage: one untiled copy each, since a record holds
-// codes and scales side by side, already in the bank-conflict-free order).  The
+// take the chunk's blocks round-robin, each with its own ring of asynchronous
+// copies (a K record and a V record per stage, 16 bytes a lane; a record holds codes
+// and scales side by side, already in the bank-conflict-free order).  The
 // warps' states meet in shared memory; a sequence of several chunks merges
 // through the workspace, the last chunk to take its ticket joining all of them
 // in chunk order.
@@ -53,6 +53,9 @@ struct Cfg {
     static constexpr int kTile = (R::kBytes + 127) / 128 * 128;  // a record in shared memory
     static constexpr int kStage = 2 * kTile;                     // K + V
     static constexpr int kStages = kFp4 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 5);
+    static constexpr int kFull = R::kBytes / 512;                // 16-byte copies of a whole warp per record
+    static constexpr int kTail = R::kBytes % 512 / 16;           // lanes of the rest: K's, then V's
+    static_assert(R::kBytes % 16 == 0 && 2 * kTail <= 32, "one copy brings both tails");
     static constexpr int kHeads = 8 * NT;
     static constexpr int kCombStride = D + 4;
     static constexpr int kRing = kWarps * kStages * kStage;
@@ -96,10 +99,10 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&d)[4]) {
         : "r"(w));
 }
 
-// Two e4m3 scales (bytes lo, hi) -> f16x2.
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t lo, uint32_t hi) {
+// Two e4m3 scales (the low and high byte) -> f16x2.
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t pair) {
     uint32_t d;
-    asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(d) : "r"(lo | (hi << 8)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(pair)));
     return d;
 }
 
@@ -110,11 +113,14 @@ __device__ __forceinline__ uint32_t int8x2(uint32_t w) {
     return hsub2_bits(__byte_perm(w, 0x64646464u, kHigh ? 0x4342 : 0x4140), 0x64806480u);
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most N of this thread's latest groups are still in flight.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A warp's running state: lane (g, t) holds heads 2t, 2t + 1 (+ 8 nt).
@@ -165,12 +171,12 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
         for (int half = 0; half < 2; ++half) {
             const uint8_t* p = kt + R::kScales + (row + 8 * half) * R::kScaleBytes + t * (D / 64);
             if constexpr (D == 128) {
-                const uint32_t b = *reinterpret_cast<const uint16_t*>(p);
-                const uint32_t v = e4m3x2(b & 0xFFu, b >> 8);
+                const uint32_t v = e4m3x2(*reinterpret_cast<const uint16_t*>(p));
                 sc[half][0] = __byte_perm(v, v, 0x1010);
                 sc[half][1] = __byte_perm(v, v, 0x3232);
             } else {
-                sc[half][0] = e4m3x2(*p, *p);
+                const uint32_t v = e4m3x2(*p);
+                sc[half][0] = __byte_perm(v, v, 0x1010);
             }
         }
 #pragma unroll
@@ -228,8 +234,8 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
             for (int i = 0; i < 4; ++i)
                 if (!visible((i & 1 ? tb : ta) + (i & 2 ? 8 : 0))) b[i] = 0;
         }
-        vs2[0] = e4m3x2(b[0], b[1]);
-        vs2[1] = e4m3x2(b[2], b[3]);
+        vs2[0] = e4m3x2(__byte_perm(b[0], b[1], 0x0040));
+        vs2[1] = e4m3x2(__byte_perm(b[2], b[3], 0x0040));
     } else {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -364,19 +370,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     using C = Cfg<D, kFp4, NT>;
     using R = QuantRecord<D, kFp4>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ uint64_t bars[kWarps][C::kStages];
     __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_v[kWarps];
     __shared__ int s_flag;
     uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
     const int G = a.group;
-    if (threadIdx.x == 0) {
-        for (int w = 0; w < kWarps; ++w)
-            for (int i = 0; i < C::kStages; ++i) mbar_init(&bars[w][i], 1);
-        s_flag = 0;
-        fence_barrier_init();
-    }
     pdl_wait();
     pdl_launch_dependents();
 
@@ -408,8 +407,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     const int b0 = first_blk + split * a.chunk_blocks;
     const int b1 = min(last_blk + 1, b0 + a.chunk_blocks);
     const int my_n = b1 - b0 > warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;
-    __syncthreads();  // the barriers are initialised
-
     // ids of this warp's blocks, 32 at a time: lane k holds that of block
     // 32 batch + k.  A bad id is flagged and reads block 0.
     auto fetch_ids = [&](int batch) {
@@ -430,25 +427,33 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     };
     if (a.window > 0) id_next = fetch_ids(0);
     int id_cur = 0;
-    const uint8_t* pool = static_cast<const uint8_t*>(lane == 0 ? a.k_pool : a.v_pool);
+    // block k of this warp into its stage: 16 bytes a lane, the two records' last
+    // lines together; every call commits one group, empty past the warp's end
+    const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool) + static_cast<size_t>(kvh) * R::kBytes + lane * 16;
+    const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool) + static_cast<size_t>(kvh) * R::kBytes + lane * 16;
+    const uint8_t* tp = lane < C::kTail ? kp : vp - C::kTail * 16;
+    const uint32_t block_bytes = static_cast<uint32_t>(a.hkv) * R::kBytes;
     uint8_t* ring = smem + warp * C::kStages * C::kStage;
-    // block k of this warp into its stage: lane 0 brings K, lane 1 V
-    auto load = [&](int k, int stage) {
+    const uint32_t to = smem_u32(ring) + lane * 16;
+    const uint32_t to_tail = to + (lane < C::kTail ? 0 : C::kTile - C::kTail * 16) + C::kFull * 512;
+    auto load = [&](int k, uint32_t stage_offset) {
         if ((k & 31) == 0) {
             id_cur = check_id(id_next, k >> 5);
             id_next = fetch_ids((k >> 5) + 1);
         }
-        const int id = __shfl_sync(0xFFFFFFFFu, id_cur, k & 31);
-        if (lane < 2 && k < my_n) {
-            if (lane == 0) mbar_arrive_expect_tx(&bars[warp][stage], 2 * R::kBytes);
-            bulk_load(ring + stage * C::kStage + lane * C::kTile, pool + (static_cast<size_t>(id) * a.hkv + kvh) * R::kBytes,
-                      R::kBytes, &bars[warp][stage]);
-        }
-    };
-    // earlier kernels wrote the pools through the generic proxy
-    fence_proxy_async_global();
+        const uint64_t off = static_cast<uint64_t>(block_bytes) * static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id_cur, k & 31));
+        if (k < my_n) {
 #pragma unroll
-    for (int k = 0; k < C::kStages; ++k) load(k, k);
+            for (int i = 0; i < C::kFull; ++i) {
+                copy16(to + stage_offset + 512 * i, kp + off + 512 * i);
+                copy16(to + stage_offset + C::kTile + 512 * i, vp + off + 512 * i);
+            }
+            if (lane < 2 * C::kTail) copy16(to_tail + stage_offset, tp + off + C::kFull * 512);
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < C::kStages - 1; ++k) load(k, k * C::kStage);
 
     // ---- q: lane (g, t) holds head g's dims t D/4 + 4j .. + 3 for k-step j, as
     // f16 scaled by 2^(12 - e), e the exponent of the group's largest |q|
@@ -493,32 +498,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     }
     st.vfac = INFINITY;
 
-    int stage = 0, k = 0;
-    uint32_t phase = 0;
-    bool failed = false;
-    for (; k < my_n; ++k) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars[warp][stage], phase))) {
-            failed = true;
-            break;
-        }
-        const uint8_t* kt = ring + stage * C::kStage;
+    // block k sits in stage k mod kStages; block k + kStages - 1 goes where block
+    // k - 1 was, which every lane has read by the time all pass the __syncwarp
+    uint32_t here = 0, next = (C::kStages - 1) * C::kStage;
+    for (int k = 0; k < my_n; ++k) {
+        copy_wait<C::kStages - 2>();  // this lane's copies of block k have landed
+        __syncwarp();                 // and every lane's
+        load(k + C::kStages - 1, next);
+        const uint8_t* kt = ring + here;
         attend<D, kFp4, NT>(st, qb, kt, kt + C::kTile, lane, (b0 + warp + k * kWarps) * kBlockSize, lo, ctx, sl);
-        __syncwarp();  // every lane's reads of the stage are done
-        load(k + C::kStages, stage);
-        if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-        }
+        next = here;
+        here = here + C::kStage == C::kStages * C::kStage ? 0 : here + C::kStage;
     }
-    if (failed) {
-        // the copies in flight land before the CTA leaves (bounded waits)
-        for (int kk = k; kk < min(my_n, k + C::kStages); ++kk)
-            (void)mbar_wait(&bars[warp][kk % C::kStages], (kk / C::kStages) & 1);
-        if (lane == 0) {
-            flag_error(a.err, PKV_DEVERR_TIMEOUT);
-            atomicOr(&s_flag, 1);
-        }
-    }
+    copy_wait<0>();
 
     // ---- the 4 warps' states meet
 #pragma unroll
@@ -545,7 +537,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
         }
     if (lane == 0) s_v[warp] = kFp4 || st.vfac == INFINITY ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(st.vfac));
     __syncthreads();
-    const bool cta_failed = s_flag != 0;
     const size_t pair = static_cast<size_t>(seq) * a.hkv + kvh;
     if (threadIdx.x < G) {
         // per head: the warps' weights 2^(mu_w - M) / L, V's scale folded in,
@@ -560,8 +551,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
             f[w] = s_m[w][h] == -INFINITY ? 0.f : fast_exp2(s_m[w][h] - M);
             L += f[w] * s_l[w][h];
         }
-        float lse = !cta_failed && L != 0.f ? M * 0.6931471805599453f + logf(L) : -INFINITY;
-        float inv = !cta_failed && L != 0.f ? (kFp4 ? a.v_scale[kvh] : 1.f) / L : 0.f;
+        float lse = L != 0.f ? M * 0.6931471805599453f + logf(L) : -INFINITY;
+        float inv = L != 0.f ? (kFp4 ? a.v_scale[kvh] : 1.f) / L : 0.f;
         if (a.sinks && nsplit == 1) {
             // lse' = ln(e^lse + e^sink), o scaled by e^(lse - lse')
             const float sk = a.sinks[kvh * G + h];
@@ -578,16 +569,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     for (int i = threadIdx.x; i < G * (D / 4); i += kThreads) {
         const int h = i / (D / 4), d = 4 * (i % (D / 4));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!cta_failed) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float wt = s_m[w][h];
-                const float4 x = *reinterpret_cast<const float4*>(comb + (w * C::kHeads + h) * C::kCombStride + d);
-                v.x += wt * x.x;
-                v.y += wt * x.y;
-                v.z += wt * x.z;
-                v.w += wt * x.w;
-            }
+        for (int w = 0; w < kWarps; ++w) {
+            const float wt = s_m[w][h];
+            const float4 x = *reinterpret_cast<const float4*>(comb + (w * C::kHeads + h) * C::kCombStride + d);
+            v.x += wt * x.x;
+            v.y += wt * x.y;
+            v.z += wt * x.z;
+            v.w += wt * x.w;
         }
         if (nsplit == 1) {
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
