@@ -51,8 +51,11 @@ template <int D, bool kFp4, int NT>
 struct Cfg {
     using R = QuantRecord<D, kFp4>;
     static constexpr int kTile = (R::kBytes + 127) / 128 * 128;  // a record in shared memory
-    static constexpr int kStage = 2 * kTile;                     // K + V
-    static constexpr int kStages = kFp4 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 5);
+    static constexpr int kBlock = 2 * kTile;                     // K + V
+    // blocks of one loop pass: two share its softmax vote and loop overhead
+    static constexpr int NB = !kFp4 && D == 128 ? 1 : 2;
+    static constexpr int kStage = NB * kBlock;
+    static constexpr int kStages = kFp4 ? (D == 128 ? 3 : 4) : 3;
     static constexpr int kFull = R::kBytes / 512;                // 16-byte copies of a whole warp per record
     static constexpr int kTail = R::kBytes % 512 / 16;           // lanes of the rest: K's, then V's
     static_assert(R::kBytes % 16 == 0 && 2 * kTail <= 32, "one copy brings both tails");
@@ -60,7 +63,9 @@ struct Cfg {
     static constexpr int kCombStride = D + 4;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kComb = kWarps * kHeads * kCombStride * 4;
-    static constexpr int kSmem = (kRing > kComb ? kRing : kComb) + 128;
+    static constexpr int kMerge = (kQuantMaxSplits + 1) * 16 * 4;
+    static constexpr int kMost = kRing > kComb ? kRing : kComb;
+    static constexpr int kSmem = (kMost > kMerge ? kMost : kMerge) + 128;
     // registers: NT * D / 4 accumulators and NT * D / 8 of q
     static constexpr int kCtas = NT * D > 128 ? 3 : 4;
 };
@@ -123,32 +128,25 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's running state: lane (g, t) holds heads 2t, 2t + 1 (+ 8 nt).
+// A warp's running state: lane (g, t) holds heads 2t, 2t + 1 (+ 8 nt) as a pair.
 template <int D, int NT>
 struct State {
-    float mu[NT][2];  // what is subtracted from the logits (exp2 domain), -inf before any key
-    float l[NT][2];   // this lane's share of sum 2^(x - mu)
+    float mu[NT][2];    // what is subtracted from the logits (exp2 domain), -inf before any key
+    uint64_t l[NT];     // this lane's share of sum 2^(x - mu), both heads
     float o[NT][D / 16][4];
-    float vfac;       // int8: the power of two on V's row scales, inf before any key
+    float vfac;         // int8: the power of two on V's row scales, inf before any key
 };
 
 constexpr float kGrow = 8.f;    // logits may exceed mu by this before it moves (2^8 fits f16)
 constexpr float kVGrow = 64.f;  // normalised V scales may reach this (2^8 * 64 fits f16)
 
-// One block: tok_base is its first token's position, keys in [lo, ctx) are visible.
+// S^T = K Q^T of one block: 16 token slots x 8 NT heads.
 template <int D, bool kFp4, int NT>
-__device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2], const uint8_t* kt,
-                                       const uint8_t* vt, int lane, int tok_base, int lo, int ctx, float sl) {
+__device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&qb)[NT][D / 16][2], const uint8_t* kt, int row,
+                                       int t) {
     using R = QuantRecord<D, kFp4>;
     constexpr int RB = R::kRowBytes;
-    const int g = lane >> 2, t = lane & 3;
-    const int row = slot_row<RB>(g);  // and row + 8
-
-    // ---- S^T = K Q^T: 16 token slots x 8 heads
-    float s[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-    uint32_t kw[2][RB / 16];  // this lane's RB/4 bytes of each row
+    uint32_t kw[2][RB / 16];  // this lane's RB/4 bytes of rows row and row + 8
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const uint8_t* base = kt + half * 8 * RB;
@@ -164,7 +162,8 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
                 *reinterpret_cast<const uint2*>(base + quant_chunk<RB>(row, t >> 1) + 8 * (t & 1));
         }
     }
-    float ks[2];  // int8: the rows' K scales
+#pragma unroll
+    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
     if constexpr (kFp4) {
         uint32_t sc[2][D / 64];  // f16x2, both halves the scale of 16 dims
 #pragma unroll
@@ -198,132 +197,28 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
         }
     } else {
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-            ks[half] = *reinterpret_cast<const float*>(kt + R::kScales + (row + 8 * half) * 4);
-#pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             const uint32_t a[4] = {int8x2<false>(kw[0][j]), int8x2<false>(kw[1][j]), int8x2<true>(kw[0][j]),
                                    int8x2<true>(kw[1][j])};
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_16816<true>(s[n], a, qb[n][j][0], qb[n][j][1]);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            s[n][0] *= ks[0];
-            s[n][1] *= ks[0];
-            s[n][2] *= ks[1];
-            s[n][3] *= ks[1];
-        }
     }
+}
 
-    // ---- V's scales, zero on invisible tokens
-    const bool edge = tok_base < lo || tok_base + kBlockSize > ctx;
-    const int base = tok_base - lo;
-    const uint32_t cnt = static_cast<uint32_t>(ctx - lo);
-    auto visible = [&](int r) { return static_cast<uint32_t>(base + r) < cnt; };
-    const int ta = slot_row<RB>(2 * t), tb = slot_row<RB>(2 * t + 1);  // O^T's token slots: rows ta, tb (+ 8)
-    uint32_t vs2[2];  // 4-bit: f16x2 scales of (ta, tb) and of (ta + 8, tb + 8)
-    float vs[2];      // int8: normalised scales of S^T's rows
-    if constexpr (kFp4) {
-        const uint8_t* p = vt + R::kScales + (D == 128 ? g : g >> 1);
-        uint32_t b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = p[((i & 1 ? tb : ta) + (i & 2 ? 8 : 0)) * R::kScaleBytes];
-        if (edge) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (!visible((i & 1 ? tb : ta) + (i & 2 ? 8 : 0))) b[i] = 0;
-        }
-        vs2[0] = e4m3x2(__byte_perm(b[0], b[1], 0x0040));
-        vs2[1] = e4m3x2(__byte_perm(b[2], b[3], 0x0040));
-    } else {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            vs[half] = *reinterpret_cast<const float*>(vt + R::kScales + (row + 8 * half) * 4);
-            if (edge && !visible(row + 8 * half)) vs[half] = 0.f;
-        }
-    }
-    if (edge) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (!visible(row)) s[n][0] = s[n][1] = -INFINITY;
-            if (!visible(row + 8)) s[n][2] = s[n][3] = -INFINITY;
-        }
-    }
-
-    // ---- softmax: p = 2^(s sl - mu), mu moving only when a logit exceeds it by 2^8
-    float p[NT][4];
-    bool grow = false;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[n][e] = __fmaf_rn(s[n][e], sl, -st.mu[n][e & 1]);
-        grow = grow || !(fmaxf(fmaxf(p[n][0], p[n][1]), fmaxf(p[n][2], p[n][3])) <= kGrow);
-    }
-    if constexpr (!kFp4) grow = grow || !(fmaxf(vs[0], vs[1]) * st.vfac <= kVGrow);
-    if (__any_sync(0xFFFFFFFFu, grow)) {
-        float vmul = 1.f;
-        if constexpr (!kFp4) {
-            float m = fmaxf(vs[0], vs[1]);
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-            if (!(m * st.vfac <= kVGrow)) {
-                // 2^-ceil-ish of the largest scale: m * vfac in [1, 2), at most 2^100
-                const uint32_t ex = __float_as_uint(m) >> 23;  // m >= 0
-                const float nf = ex < 27u ? __uint_as_float(227u << 23) : __uint_as_float((254u - min(ex, 253u)) << 23);
-                // nf / vfac, exactly (it only shrinks; below 2^-126 O still is 0)
-                const int step = static_cast<int>(__float_as_uint(nf) >> 23) - static_cast<int>(__float_as_uint(st.vfac) >> 23);
-                if (st.vfac != INFINITY) vmul = step < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + step) << 23);
-                st.vfac = nf;
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float mx = fmaxf(s[n][c], s[n][c + 2]) * sl;
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
-                const float mn = fmaxf(st.mu[n][c], mx);
-                const float keep = mn == -INFINITY ? 1.f : fast_exp2(st.mu[n][c] - mn);
-                st.mu[n][c] = mn;
-                st.l[n][c] *= keep;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    st.o[n][i][c] *= keep * vmul;
-                    st.o[n][i][c + 2] *= keep * vmul;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[n][e] = __fmaf_rn(s[n][e], sl, -st.mu[n][e & 1]);
-        }
-    }
-    uint32_t pb[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[n][e] = fast_exp2(p[n][e]);
-        st.l[n][0] += p[n][0] + p[n][2];
-        st.l[n][1] += p[n][1] + p[n][3];
-        if constexpr (!kFp4) {
-            const float f0 = vs[0] * st.vfac, f1 = vs[1] * st.vfac;
-            p[n][0] *= f0;
-            p[n][1] *= f0;
-            p[n][2] *= f1;
-            p[n][3] *= f1;
-        }
-        pb[n][0] = movmatrix(pack2<true>(p[n][0], p[n][1]));
-        pb[n][1] = movmatrix(pack2<true>(p[n][2], p[n][3]));
-    }
-
-    // ---- O^T += V^T P^T: D dims x 8 heads
+// O^T += V^T P^T of one block: D dims x 8 NT heads.  vs2: f16x2 scales (4-bit) of
+// rows (ta, tb) and (ta + 8, tb + 8).
+template <int D, bool kFp4, int NT>
+__device__ __forceinline__ void accumulate(float (&o)[NT][D / 16][4], const uint32_t (&pb)[NT][2], const uint8_t* vt, int g,
+                                           int ta, int tb, const uint32_t (&vs2)[2]) {
+    using R = QuantRecord<D, kFp4>;
+    constexpr int RB = R::kRowBytes;
     constexpr int VB = RB / 8;  // this lane's bytes of a token's row
     constexpr int VW = VB / 4;
     uint32_t vw[4][VW];  // rows ta, tb, ta + 8, tb + 8
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = (i & 1 ? tb : ta);
-        const uint8_t* q = vt + (i & 2 ? 8 * RB : 0) + quant_chunk<RB>(r, g * VB / 16) + (g * VB) % 16;
+        const uint8_t* q = vt + (i & 2 ? 8 * RB : 0) + quant_chunk<RB>(i & 1 ? tb : ta, g * VB / 16) + (g * VB) % 16;
         if constexpr (VB == 16) {
             *reinterpret_cast<uint4*>(vw[i]) = *reinterpret_cast<const uint4*>(q);
         } else if constexpr (VB == 8) {
@@ -347,10 +242,11 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
                 const uint32_t a[4] = {hmul2_bits(even[0][i], vs2[0]), hmul2_bits(odd[0][i], vs2[0]),
                                        hmul2_bits(even[1][i], vs2[1]), hmul2_bits(odd[1][i], vs2[1])};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_16816<true>(st.o[n][4 * w + i], a, pb[n][0], pb[n][1]);
+                for (int n = 0; n < NT; ++n) mma_16816<true>(o[n][4 * w + i], a, pb[n][0], pb[n][1]);
             }
         }
     } else {
+        (void)vs2;
 #pragma unroll
         for (int w = 0; w < VW; ++w) {  // a word: 4 dims, two m-tiles
 #pragma unroll
@@ -359,10 +255,161 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
                 const uint32_t hi2 = __byte_perm(vw[2][w], vw[3][w], i ? 0x7362 : 0x5140);
                 const uint32_t a[4] = {int8x2<false>(lo2), int8x2<true>(lo2), int8x2<false>(hi2), int8x2<true>(hi2)};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_16816<true>(st.o[n][2 * w + i], a, pb[n][0], pb[n][1]);
+                for (int n = 0; n < NT; ++n) mma_16816<true>(o[n][2 * w + i], a, pb[n][0], pb[n][1]);
             }
         }
     }
+}
+
+// NB consecutive blocks, K and V records of block i at stage + i * kBlock: tok_base is
+// the first one's first position, keys in [lo, hi) take part.
+template <int D, bool kFp4, int NT>
+__device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2], const uint8_t* stage,
+                                       int lane, int tok_base, int lo, int hi, float sl) {
+    using C = Cfg<D, kFp4, NT>;
+    using R = QuantRecord<D, kFp4>;
+    constexpr int RB = R::kRowBytes, NB = C::NB;
+    const int g = lane >> 2, t = lane & 3;
+    const int row = slot_row<RB>(g);                                    // S^T's rows: row, row + 8
+    const int ta = slot_row<RB>(2 * t), tb = slot_row<RB>(2 * t + 1);  // O^T's token slots: rows ta, tb (+ 8)
+    const bool edge = tok_base < lo || tok_base + NB * kBlockSize > hi;
+    const uint32_t cnt = static_cast<uint32_t>(hi - lo);
+    auto visible = [&](int b, int r) { return static_cast<uint32_t>(tok_base - lo + b * kBlockSize + r) < cnt; };
+
+    float s[NB][NT][4];
+    float kf[NB][2];      // what a row's logits are scaled by
+    float vs[NB][2];      // int8: the rows' V scales
+    uint32_t vs2[NB][2];  // 4-bit: V's f16x2 scales of rows (ta, tb) and (ta + 8, tb + 8)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint8_t* kt = stage + b * C::kBlock;
+        const uint8_t* vt = kt + C::kTile;
+        scores<D, kFp4, NT>(s[b], qb, kt, row, t);
+        kf[b][0] = kf[b][1] = sl;
+        vs2[b][0] = vs2[b][1] = 0u;
+        if constexpr (kFp4) {
+            const uint8_t* p = vt + R::kScales + (D == 128 ? g : g >> 1);
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = p[((i & 1 ? tb : ta) + (i & 2 ? 8 : 0)) * R::kScaleBytes];
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!visible(b, (i & 1 ? tb : ta) + (i & 2 ? 8 : 0))) c[i] = 0;
+            }
+            vs2[b][0] = e4m3x2(__byte_perm(c[0], c[1], 0x0040));
+            vs2[b][1] = e4m3x2(__byte_perm(c[2], c[3], 0x0040));
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                kf[b][h] = *reinterpret_cast<const float*>(kt + R::kScales + (row + 8 * h) * 4) * sl;
+                vs[b][h] = *reinterpret_cast<const float*>(vt + R::kScales + (row + 8 * h) * 4);
+            }
+        }
+        if (edge) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (!visible(b, row + 8 * h)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[b][n][2 * h] = s[b][n][2 * h + 1] = -INFINITY;
+                    kf[b][h] = sl;  // > 0: the product stays -inf
+                    vs[b][h] = 0.f;
+                }
+        }
+    }
+
+    // ---- softmax: p = 2^(s kf - mu), mu moving only when a logit exceeds it by 2^8
+    uint64_t p[NB][NT][2];  // row, row + 8: a pair of heads each
+    auto logits = [&]() {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    p[b][n][h] = fma_f32x2(pack_f32x2(s[b][n][2 * h], s[b][n][2 * h + 1]), pack_f32x2(kf[b][h], kf[b][h]),
+                                           pack_f32x2(-st.mu[n][0], -st.mu[n][1]));
+    };
+    logits();
+    float top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x, y;
+                unpack_f32x2(p[b][n][h], x, y);
+                top = fmax3(top, x, y);  // +inf while mu is -inf: a pass's first block has a visible key
+            }
+    bool grow = top > kGrow;
+    if constexpr (!kFp4) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) grow = grow || !(fmaxf(vs[b][0], vs[b][1]) * st.vfac <= kVGrow);
+    }
+    if (__any_sync(0xFFFFFFFFu, grow)) {
+        float vmul = 1.f;
+        if constexpr (!kFp4) {
+            float m = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) m = fmaxf(m, fmaxf(vs[b][0], vs[b][1]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+            if (!(m * st.vfac <= kVGrow)) {
+                // the power of two that brings the largest scale into [1, 2), at most 2^100
+                const uint32_t ex = __float_as_uint(m) >> 23;  // m >= 0
+                const float nf = ex < 27u ? __uint_as_float(227u << 23) : __uint_as_float((254u - min(ex, 253u)) << 23);
+                // nf / vfac, exactly (it only shrinks; below 2^-126 O still is 0)
+                const int step = static_cast<int>(__float_as_uint(nf) >> 23) - static_cast<int>(__float_as_uint(st.vfac) >> 23);
+                if (st.vfac != INFINITY) vmul = step < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + step) << 23);
+                st.vfac = nf;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float keep[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) mx = fmax3(mx, s[b][n][c] * kf[b][0], s[b][n][c + 2] * kf[b][1]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+                const float mn = fmaxf(st.mu[n][c], mx);
+                keep[c] = mn == -INFINITY ? 1.f : fast_exp2(st.mu[n][c] - mn);
+                st.mu[n][c] = mn;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    st.o[n][i][c] *= keep[c] * vmul;
+                    st.o[n][i][c + 2] *= keep[c] * vmul;
+                }
+            }
+            st.l[n] = mul_f32x2(st.l[n], pack_f32x2(keep[0], keep[1]));
+        }
+        logits();
+    }
+    uint32_t pb[NB][NT][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x, y;
+                unpack_f32x2(p[b][n][h], x, y);
+                x = fast_exp2(x);
+                y = fast_exp2(y);
+                st.l[n] = add_f32x2(st.l[n], pack_f32x2(x, y));
+                if constexpr (!kFp4) {
+                    const float f = vs[b][h] * st.vfac;
+                    x *= f;
+                    y *= f;
+                }
+                pb[b][n][h] = movmatrix(pack2<true>(x, y));
+            }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        accumulate<D, kFp4, NT>(st.o, pb[b], stage + b * C::kBlock + C::kTile, g, ta, tb, vs2[b]);
 }
 
 template <int D, bool kFp4, int NT>
@@ -383,8 +430,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     // without a window a chunk's blocks do not depend on the length: the ids are
     // read while it is in flight
     int id_next = 0;
-    const int early = split * a.chunk_blocks + warp + lane * kWarps;
-    if (a.window <= 0 && lane * kWarps < a.chunk_blocks && early < a.mbps) id_next = bt[early];
+    const int early = C::NB * (warp + kWarps * (lane / C::NB)) + lane % C::NB;
+    if (a.window <= 0 && early < a.chunk_blocks && split * a.chunk_blocks + early < a.mbps)
+        id_next = bt[split * a.chunk_blocks + early];
     int ctx = a.context_lens[seq];
     if (ctx > a.max_ctx) {
         if (threadIdx.x == 0 && split == 0 && kvh == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
@@ -406,54 +454,60 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     if (split >= nsplit) return;
     const int b0 = first_blk + split * a.chunk_blocks;
     const int b1 = min(last_blk + 1, b0 + a.chunk_blocks);
-    const int my_n = b1 - b0 > warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;
-    // ids of this warp's blocks, 32 at a time: lane k holds that of block
-    // 32 batch + k.  A bad id is flagged and reads block 0.
+    const int hi = min(ctx, b1 * kBlockSize);
+    // this warp's passes: NB blocks each, warp after warp
+    const int passes = ((b1 - b0 + C::NB - 1) / C::NB - warp + kWarps - 1) / kWarps;
+
+    // ids of this warp's blocks, 32 at a time: lane k holds that of its block 32
+    // batch + k.  A bad id is flagged and reads block 0.
+    auto logical = [&](int k) { return b0 + C::NB * (warp + kWarps * (k / C::NB)) + k % C::NB; };
     auto fetch_ids = [&](int batch) {
-        const int k = 32 * batch + lane;
-        int id = 0;
-        if (k < my_n) {
-            const int lb = b0 + warp + k * kWarps;
-            id = bt[a.ring > 0 ? lb % a.ring : lb];
-        }
-        return id;
+        const int lb = logical(32 * batch + lane);
+        return lb < b1 ? bt[a.ring > 0 ? lb % a.ring : lb] : 0;
     };
     auto check_id = [&](int id, int batch) {
-        if (32 * batch + lane < my_n && (id < 0 || id >= a.num_blocks)) {
-            flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+        if (id < 0 || id >= a.num_blocks) {
+            if (logical(32 * batch + lane) < b1) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
             id = 0;
         }
         return id;
     };
     if (a.window > 0) id_next = fetch_ids(0);
     int id_cur = 0;
-    // block k of this warp into its stage: 16 bytes a lane, the two records' last
-    // lines together; every call commits one group, empty past the warp's end
+    // a pass's blocks into a stage: 16 bytes a lane, the two records' last lines
+    // together; every call commits one group, empty past the warp's end
     const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool) + static_cast<size_t>(kvh) * R::kBytes + lane * 16;
     const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool) + static_cast<size_t>(kvh) * R::kBytes + lane * 16;
-    const uint8_t* tp = lane < C::kTail ? kp : vp - C::kTail * 16;
+    const uint8_t* tp = (lane < C::kTail ? kp : vp - C::kTail * 16) + C::kFull * 512;
     const uint32_t block_bytes = static_cast<uint32_t>(a.hkv) * R::kBytes;
     uint8_t* ring = smem + warp * C::kStages * C::kStage;
     const uint32_t to = smem_u32(ring) + lane * 16;
     const uint32_t to_tail = to + (lane < C::kTail ? 0 : C::kTile - C::kTail * 16) + C::kFull * 512;
-    auto load = [&](int k, uint32_t stage_offset) {
-        if ((k & 31) == 0) {
-            id_cur = check_id(id_next, k >> 5);
-            id_next = fetch_ids((k >> 5) + 1);
+    auto load = [&](int pass, uint32_t stage) {
+        const int k0 = pass * C::NB;
+        if ((k0 & 31) == 0) {
+            id_cur = check_id(id_next, k0 >> 5);
+            id_next = fetch_ids((k0 >> 5) + 1);
         }
-        const uint64_t off = static_cast<uint64_t>(block_bytes) * static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id_cur, k & 31));
-        if (k < my_n) {
 #pragma unroll
-            for (int i = 0; i < C::kFull; ++i) {
-                copy16(to + stage_offset + 512 * i, kp + off + 512 * i);
-                copy16(to + stage_offset + C::kTile + 512 * i, vp + off + 512 * i);
+        for (int b = 0; b < C::NB; ++b) {
+            const uint32_t id = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id_cur, (k0 + b) & 31));
+            if (logical(k0 + b) < b1) {
+                const uint8_t* ks = kp + static_cast<uint64_t>(block_bytes) * id;
+                const uint8_t* vs = vp + static_cast<uint64_t>(block_bytes) * id;
+                const uint32_t dst = stage + b * C::kBlock;
+#pragma unroll
+                for (int i = 0; i < C::kFull; ++i) {
+                    copy16(to + dst + 512 * i, ks + 512 * i);
+                    copy16(to + dst + C::kTile + 512 * i, vs + 512 * i);
+                }
+                if (lane < 2 * C::kTail) copy16(to_tail + dst, tp + static_cast<uint64_t>(block_bytes) * id);
             }
-            if (lane < 2 * C::kTail) copy16(to_tail + stage_offset, tp + off + C::kFull * 512);
         }
         copy_commit();
     };
 #pragma unroll
-    for (int k = 0; k < C::kStages - 1; ++k) load(k, k * C::kStage);
+    for (int i = 0; i < C::kStages - 1; ++i) load(i, i * C::kStage);
 
     // ---- q: lane (g, t) holds head g's dims t D/4 + 4j .. + 3 for k-step j, as
     // f16 scaled by 2^(12 - e), e the exponent of the group's largest |q|
@@ -492,33 +546,37 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         st.mu[n][0] = st.mu[n][1] = -INFINITY;
-        st.l[n][0] = st.l[n][1] = 0.f;
+        st.l[n] = 0;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) st.o[n][i][0] = st.o[n][i][1] = st.o[n][i][2] = st.o[n][i][3] = 0.f;
     }
     st.vfac = INFINITY;
 
-    // block k sits in stage k mod kStages; block k + kStages - 1 goes where block
-    // k - 1 was, which every lane has read by the time all pass the __syncwarp
+    // pass i sits in stage i mod kStages; pass i + kStages - 1 goes where pass i - 1
+    // was, which every lane has read by the time all are past the __syncwarp
     uint32_t here = 0, next = (C::kStages - 1) * C::kStage;
-    for (int k = 0; k < my_n; ++k) {
-        copy_wait<C::kStages - 2>();  // this lane's copies of block k have landed
+    int tok = (b0 + C::NB * warp) * kBlockSize;
+    for (int i = 0; i < passes; ++i) {
+        copy_wait<C::kStages - 2>();  // this lane's copies of pass i have landed
         __syncwarp();                 // and every lane's
-        load(k + C::kStages - 1, next);
-        const uint8_t* kt = ring + here;
-        attend<D, kFp4, NT>(st, qb, kt, kt + C::kTile, lane, (b0 + warp + k * kWarps) * kBlockSize, lo, ctx, sl);
+        load(i + C::kStages - 1, next);
+        attend<D, kFp4, NT>(st, qb, ring + here, lane, tok, lo, hi, sl);
+        tok += kWarps * C::NB * kBlockSize;
         next = here;
         here = here + C::kStage == C::kStages * C::kStage ? 0 : here + C::kStage;
     }
     copy_wait<0>();
 
     // ---- the 4 warps' states meet
+    float l[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        unpack_f32x2(st.l[n], l[n][0], l[n][1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) st.l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, st.l[n][c], x);
+            for (int x = 4; x < 32; x <<= 1) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], x);
+    }
     __syncthreads();  // every warp is done with its ring
     float* comb = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -532,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
                 *reinterpret_cast<float2*>(cw + 2 * i) = make_float2(st.o[n][i][c], st.o[n][i][c + 2]);
             if (g == 0) {
                 s_m[warp][h] = st.mu[n][c];
-                s_l[warp][h] = st.l[n][c];
+                s_l[warp][h] = l[n][c];
             }
         }
     if (lane == 0) s_v[warp] = kFp4 || st.vfac == INFINITY ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(st.vfac));
@@ -652,7 +710,6 @@ template <int D, bool kFp4, int NT>
 cudaError_t launch_t(const QuantDecodeArgs& a, cudaStream_t stream) {
     using C = Cfg<D, kFp4, NT>;
     static_assert(C::kSmem <= 227 * 1024, "shared memory budget");
-    static_assert((kQuantMaxSplits + 1) * 16 * 4 <= C::kSmem - 128, "merge weights");
     auto kern = quant_decode_kernel<D, kFp4, NT>;
     // a per-device function attribute, set on the first launch on each device
     static bool attr_set[64] = {};
