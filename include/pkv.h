@@ -596,7 +596,7 @@ pkv_status pkv_quant_load_blocks(const pkv_cache_desc *desc, const void *k_pool,
  * 16-dim scales, 4-bit) exactly, q scaled by a power of two into f16's range, and
  * the softmax weights rounded to f16; sums and softmax statistics are fp32.
  *   chunk_blocks: blocks per chunk; 0 lets the planner choose, else 1..512; a
- *                 context is cut into at most 512 chunks.
+ *                 context is cut into at most 256 chunks.
  *   workspace   : >= pkv_quant_decode_workspace_size(...) bytes, 256-byte aligned,
  *                 zero-filled before its first use; every call leaves its tickets
  *                 zeroed.  Calls that share a workspace must not overlap on the GPU. */

@@ -1691,27 +1691,45 @@ pkv_status pkv_quant_load_blocks(const pkv_cache_desc* desc, const void* k_pool,
 
 namespace {
 
-// Chunk length (blocks) and chunks per (sequence, KV head).  A ragged batch
-// averages about half its longest context; aim for one wave of resident CTAs.
+// Chunk length (blocks), chunks per (sequence, KV head), and whether those merge in a
+// cluster or by tickets.  Measured on 4-bit D128 and int8 D64 pools, 8 heads a group:
+//   * a ragged batch averages about half its longest context: chunks aim for one wave
+//     of resident CTAs, at least 32 blocks (a start and an end cost a warp about 3
+//     blocks' work: 120 x 8 pairs of 64..2048 blocks took 544 us with 64-block chunks,
+//     488 with 128, 470 with 256), at most 128, or 256 from 4 waves of such chunks on;
+//   * 2..8 chunks merge in a cluster while the whole grid is resident (32 pairs of
+//     16..256 blocks: 10.1 us, 12.4 by tickets); beyond, clusters wait for their
+//     places (1024 CTAs on 608: 23.0 us, 18.9 by tickets);
+//   * so a grid that stays resident takes up to 8 chunks, of at least 8 blocks (2 pairs
+//     of 48 blocks: 5.5 us in 6 chunks, 6.7 in one), short contexts only while half the
+//     GPU would idle (128 pairs of 48 blocks: 13.7 us in 6 chunks, 7.7 in one) and from
+//     32 blocks on (8 pairs of 16 blocks: 4.3 us in 2 chunks, 3.8 in one).
+struct QuantPlan {
+    int chunk, splits;
+    bool cluster;
+};
 pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_ctx, int window, int num_sms,
-                             int chunk_req, int* chunk_out, int* splits_out) {
+                             int chunk_req, QuantPlan* out) {
     const int mb = max_visible_blocks(max_ctx, window);
+    const double pairs = double(num_seqs) * desc->num_kv_heads;
+    const double slots = double(std::max(num_sms, 1)) *
+                         pkv::quant_decode_ctas(desc->head_dim, desc->num_q_heads / desc->num_kv_heads);
     int chunk = chunk_req;
     if (chunk <= 0) {
-        const double pairs = double(num_seqs) * desc->num_kv_heads;
-        const double slots = double(std::max(num_sms, 1)) *
-                             pkv::quant_decode_ctas(desc->head_dim, desc->kv_dtype == PKV_KV_FP4,
-                                                    desc->num_q_heads / desc->num_kv_heads);
-        chunk = int(std::ceil(pairs * std::max(1.0, 0.55 * mb) / slots));
-        chunk = std::max(32, std::min(128, chunk));
+        const int cap = pairs * (0.55 * mb / 256 + 0.5) >= 4.0 * slots ? 256 : 128;
+        chunk = std::max(32, std::min(cap, int(std::ceil(pairs * std::max(1.0, 0.55 * mb) / slots))));
+        const int eighth = (((mb + 7) / 8 + 7) / 8) * 8;
+        const double ctas = pairs * ((mb + eighth - 1) / eighth);
+        if (mb >= 32 && eighth <= chunk && ctas <= (mb <= 48 ? 0.5 * slots : slots)) chunk = eighth;
         chunk = std::max(chunk, (mb + pkv::kQuantMaxSplits - 1) / pkv::kQuantMaxSplits);
         chunk = std::min(chunk, mb);
     }
     if (chunk > pkv::kQuantMaxChunk || (mb + chunk - 1) / chunk > pkv::kQuantMaxSplits)
         return fail(PKV_ERR_UNSUPPORTED, "context of %d blocks needs more than %d chunks of %d blocks", mb,
                     pkv::kQuantMaxSplits, std::min(chunk, pkv::kQuantMaxChunk));
-    *chunk_out = chunk;
-    *splits_out = (mb + chunk - 1) / chunk;
+    out->chunk = chunk;
+    out->splits = (mb + chunk - 1) / chunk;
+    out->cluster = out->splits > 1 && out->splits <= pkv::kQuantCluster && pairs * out->splits <= slots;
     return PKV_OK;
 }
 
@@ -1725,10 +1743,10 @@ size_t pkv_quant_decode_workspace_size(const pkv_cache_desc* desc, int32_t num_s
         chunk_blocks > pkv::kQuantMaxChunk)
         return 0;
     int sms = 0;
-    if (chunk_blocks == 0 && device_state(nullptr, &sms) != PKV_OK) return 0;
-    int c = 0, s = 0;
-    if (plan_quant_decode(desc, num_seqs, max_context_len, window, sms, chunk_blocks, &c, &s) != PKV_OK) return 0;
-    return decode_ws_layout(desc, num_seqs, s).total;
+    if (device_state(nullptr, &sms) != PKV_OK) return 0;
+    QuantPlan plan;
+    if (plan_quant_decode(desc, num_seqs, max_context_len, window, sms, chunk_blocks, &plan) != PKV_OK) return 0;
+    return plan.cluster ? 0 : decode_ws_layout(desc, num_seqs, plan.splits).total;
 }
 
 pkv_status pkv_quant_decode(const pkv_cache_desc* desc, const void* q, const void* k_pool, const void* v_pool,
@@ -1756,10 +1774,14 @@ pkv_status pkv_quant_decode(const pkv_cache_desc* desc, const void* q, const voi
     int sms = 0;
     st = device_state(&a.err, &sms);
     if (st != PKV_OK) return st;
-    st = plan_quant_decode(desc, num_seqs, max_context_len, window, sms, chunk_blocks, &a.chunk_blocks, &a.max_splits);
+    QuantPlan plan;
+    st = plan_quant_decode(desc, num_seqs, max_context_len, window, sms, chunk_blocks, &plan);
     if (st != PKV_OK) return st;
+    a.chunk_blocks = plan.chunk;
+    a.max_splits = plan.splits;
+    a.cluster = plan.cluster ? 1 : 0;
     const DecodeWs ws = decode_ws_layout(desc, num_seqs, a.max_splits);
-    if (ws.total > 0) {
+    if (ws.total > 0 && !plan.cluster) {
         if (!workspace) return fail(PKV_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", ws.total);
         if (!aligned(workspace, 256)) return fail(PKV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
         if (workspace_bytes < ws.total)

@@ -258,13 +258,15 @@ struct QuantDecodeArgs {
     float* part_o;       // [num_seqs * hkv * max_splits * group * d]
     int64_t num_blocks;
     int32_t num_seqs, hq, hkv, group, d, fp4, mbps, ring, window, max_ctx, chunk_blocks, max_splits;
+    int32_t cluster;  // the chunks of a (sequence, KV head) are one cluster (at most kQuantCluster)
     float sm_scale;
     uint32_t* err;
 };
+constexpr int kQuantCluster = 8;      // most chunks merged inside a cluster
 constexpr int kQuantMaxChunk = 512;   // blocks per CTA
-constexpr int kQuantMaxSplits = 512;  // chunks per (sequence, KV head)
+constexpr int kQuantMaxSplits = 256;  // chunks per (sequence, KV head)
 cudaError_t launch_quant_decode(const QuantDecodeArgs& a, cudaStream_t stream);
-int quant_decode_ctas(int d, int fp4, int group);  // resident per SM
+int quant_decode_ctas(int d, int group);  // resident per SM
 
 // Tensor-map box shape used by the attention kernels for a pool:
 // innermost box extent in elements, and the swizzle.

@@ -63,9 +63,8 @@ struct Cfg {
     static constexpr int kCombStride = D + 4;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kComb = kWarps * kHeads * kCombStride * 4;
-    static constexpr int kMerge = (kQuantMaxSplits + 1) * 16 * 4;
-    static constexpr int kMost = kRing > kComb ? kRing : kComb;
-    static constexpr int kSmem = (kMost > kMerge ? kMost : kMerge) + 128;
+    static constexpr int kMerge = kComb + (kQuantMaxSplits + 1) * 16 * 4;
+    static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 128;
     // registers: NT * D / 4 accumulators and NT * D / 8 of q
     static constexpr int kCtas = NT * D > 128 ? 3 : 4;
 };
@@ -434,12 +433,27 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     if (a.window <= 0 && early < a.chunk_blocks && split * a.chunk_blocks + early < a.mbps)
         id_next = bt[split * a.chunk_blocks + early];
     int ctx = a.context_lens[seq];
+    // q, read while the length and the ids are in flight: lane (g, t) holds head g's
+    // dims t D/4 + 4j .. + 3 for k-step j
+    const size_t head0 = static_cast<size_t>(seq) * a.hq + kvh * G;  // the group's first row of q, out, lse
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t qb[NT][D / 16][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            uint2 v = make_uint2(0u, 0u);
+            if (g + 8 * n < G)
+                v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + (head0 + g + 8 * n) * D +
+                                                    t * (D / 4) + 4 * j);
+            qb[n][j][0] = v.x;
+            qb[n][j][1] = v.y;
+        }
     if (ctx > a.max_ctx) {
         if (threadIdx.x == 0 && split == 0 && kvh == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
         ctx = a.max_ctx;
     }
     const int lo = a.window > 0 && ctx > a.window ? ctx - a.window : 0;
-    const size_t head0 = static_cast<size_t>(seq) * a.hq + kvh * G;  // the group's first row of q, out, lse
     if (ctx <= 0) {
         if (split == 0) {
             for (int i = threadIdx.x; i < G * D; i += kThreads)
@@ -509,24 +523,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) load(i, i * C::kStage);
 
-    // ---- q: lane (g, t) holds head g's dims t D/4 + 4j .. + 3 for k-step j, as
-    // f16 scaled by 2^(12 - e), e the exponent of the group's largest |q|
-    const int g = lane >> 2, t = lane & 3;
-    uint32_t qb[NT][D / 16][2];
+    // ---- q as f16, scaled by 2^(12 - e), e the exponent of the group's largest |q|
     float qmax = 0.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            uint2 v = make_uint2(0u, 0u);
-            if (g + 8 * n < G)
-                v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + (head0 + g + 8 * n) * D +
-                                                    t * (D / 4) + 4 * j);
-            qb[n][j][0] = v.x;
-            qb[n][j][1] = v.y;
-            qmax = fmaxf(qmax, fmaxf(fmaxf(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x))),
-                                     fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y)))));
-        }
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                qmax = fmax3(qmax, fabsf(bf16_lo(qb[n][j][i])), fabsf(bf16_hi(qb[n][j][i])));
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, x));
     const int qe = qmax > 0.f && qmax < INFINITY ? max(12, static_cast<int>(__float_as_uint(qmax) >> 23)) : 139;
@@ -640,6 +645,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
                 make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
             if (a.lse_out && d == 0) a.lse_out[head0 + h] = s_l[0][h];
+        } else if (a.cluster) {  // the chunk's state stays here, in place of warp 0's rows
+            *reinterpret_cast<float4*>(comb + h * C::kCombStride + d) = v;
         } else {
             const size_t prow = (pair * a.max_splits + split) * G + h;
             *reinterpret_cast<float4*>(a.part_o + prow * D + d) = v;
@@ -648,31 +655,96 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     }
     if (nsplit == 1) return;
 
+    if (a.cluster) {
+        // ---- the chunks of this (sequence, KV head) are one cluster: after the barrier
+        // each joins its share of the output from its peers' shared memory
+        cluster_sync();
+        float* wts = comb + C::kHeads * C::kCombStride;  // warp 1's rows, free now: [chunk][16]
+        float* row_inv = wts + kQuantCluster * 16;
+        if (threadIdx.x < G) {
+            const int h = threadIdx.x;
+            const float sk = a.sinks ? a.sinks[kvh * G + h] : -INFINITY;
+            float l[kQuantCluster], M = sk;
+#pragma unroll
+            for (int c = 0; c < kQuantCluster; ++c) {
+                l[c] = c < nsplit ? ld_cluster_f32(cluster_map(smem_u32(&s_l[0][h]), c)) : -INFINITY;
+                M = fmaxf(M, l[c]);
+            }
+            float W = sk == -INFINITY ? 0.f : expf(sk - M);
+#pragma unroll
+            for (int c = 0; c < kQuantCluster; ++c) {
+                const float w = l[c] == -INFINITY ? 0.f : expf(l[c] - M);
+                wts[c * 16 + h] = w;
+                W += w;
+            }
+            row_inv[h] = W != 0.f ? 1.f / W : 0.f;
+            if (a.lse_out && split == 0) a.lse_out[head0 + h] = W != 0.f ? M + logf(W) : -INFINITY;
+        }
+        __syncthreads();
+        const int total = G * (D / 4);
+        for (int i = split * total / nsplit + threadIdx.x; i < (split + 1) * total / nsplit; i += kThreads) {
+            const int h = i / (D / 4), d = 4 * (i % (D / 4));
+            const uint32_t at = smem_u32(comb + h * C::kCombStride + d);
+            float4 x[kQuantCluster];
+#pragma unroll
+            for (int c = 0; c < kQuantCluster; ++c)
+                if (c < nsplit) x[c] = ld_cluster_f32x4(cluster_map(at, c));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < kQuantCluster; ++c) {
+                const float w = wts[c * 16 + h];
+                if (c < nsplit && w != 0.f) {
+                    v.x += w * x[c].x;
+                    v.y += w * x[c].y;
+                    v.z += w * x[c].z;
+                    v.w += w * x[c].w;
+                }
+            }
+            const float inv = row_inv[h];
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
+                make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
+        }
+        cluster_sync();  // no chunk leaves while a peer may still read its state
+        return;
+    }
+
     // ---- the last chunk of this (sequence, KV head) to arrive joins them all
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) s_flag = static_cast<int>(atomicAdd(&a.counters[pair], 1u));
+    if (threadIdx.x == 0) {
+        __threadfence();  // cumulative: the CTA's states, written before the barrier, are out first
+        s_flag = static_cast<int>(atomicAdd(&a.counters[pair], 1u));
+        __threadfence();
+    }
     __syncthreads();
     if (s_flag != nsplit - 1) return;
-    __threadfence();
-    float* wts = reinterpret_cast<float*>(smem);  // [nsplit][16], then the rows' sums
-    float* row_inv = wts + a.max_splits * 16;
+    float* sums = comb;                                            // [warp][head][D]
+    float* wts = comb + kWarps * C::kHeads * C::kCombStride;  // [chunk][G], then 1 / the sum per head
+    float* row_inv = wts + kQuantMaxSplits * 16;
     {
+        // the chunks' lse, one round trip for all: wts[chunk][G] until they are weights
+        const float* pl = a.part_lse + pair * a.max_splits * G;
+        for (int i = threadIdx.x; i < nsplit * G; i += 4 * kThreads) {
+            float l[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) l[u] = __ldcg(pl + min(i + u * kThreads, nsplit * G - 1));
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u * kThreads < nsplit * G) wts[i + u * kThreads] = l[u];
+        }
+        __syncthreads();
         const int h = threadIdx.x >> 3, sub = threadIdx.x & 7;  // 16 heads x 8 threads
-        const float* pl = a.part_lse + pair * a.max_splits * G + h;
-        float M = -INFINITY;
+        const float sk = a.sinks && h < G ? a.sinks[kvh * G + h] : -INFINITY;
+        float M = sk;
         if (h < G)
-            for (int i = sub; i < nsplit; i += 8) M = fmaxf(M, __ldcg(pl + static_cast<size_t>(i) * G));
+            for (int i = sub; i < nsplit; i += 8) M = fmaxf(M, wts[i * G + h]);
 #pragma unroll
         for (int x = 1; x < 8; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
-        const float sk = a.sinks && h < G ? a.sinks[kvh * G + h] : -INFINITY;
-        M = fmaxf(M, sk);
         float W = 0.f;
         if (h < G)
             for (int i = sub; i < nsplit; i += 8) {
-                const float l = __ldcg(pl + static_cast<size_t>(i) * G);
+                const float l = wts[i * G + h];
                 const float w = l == -INFINITY ? 0.f : expf(l - M);
-                wts[i * 16 + h] = w;
+                wts[i * G + h] = w;
                 W += w;
             }
 #pragma unroll
@@ -684,20 +756,52 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
         }
     }
     __syncthreads();
+    // a warp takes every 4th chunk's whole state, kAhead chunks' loads in flight (past the
+    // end the last chunk's again, weighted 0); the warps' sums meet in shared memory
+    {
+        constexpr int kSlots = C::kHeads * D / 128;  // float4s of a state per lane
+        constexpr int kAhead = kSlots > 8 ? 1 : 2;
+        const float* po = a.part_o + pair * a.max_splits * G * D;
+        float4 v[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = warp; c0 < nsplit; c0 += kAhead * kWarps) {
+            float4 x[kAhead][kSlots];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int j = 0; j < kSlots; ++j)
+                    x[u][j] = __ldcg(reinterpret_cast<const float4*>(
+                        po + static_cast<size_t>(min(c0 + u * kWarps, nsplit - 1)) * G * D + min(4 * (lane + 32 * j), G * D - 4)));
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int j = 0; j < kSlots; ++j) {
+                    const int c = c0 + u * kWarps, h = min(4 * (lane + 32 * j) / D, G - 1);
+                    const float w = c < nsplit ? wts[c * G + h] : 0.f;
+                    v[j].x += w * x[u][j].x;
+                    v[j].y += w * x[u][j].y;
+                    v[j].z += w * x[u][j].z;
+                    v[j].w += w * x[u][j].w;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            const int i = 4 * (lane + 32 * j);
+            *reinterpret_cast<float4*>(sums + (warp * C::kHeads + i / D) * C::kCombStride + i % D) = v[j];
+        }
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < G * (D / 4); i += kThreads) {
         const int h = i / (D / 4), d = 4 * (i % (D / 4));
-        const float* po = a.part_o + (pair * a.max_splits * G + h) * D + d;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = 0; c < nsplit; ++c) {
-            const float w = wts[c * 16 + h];
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(c) * G * D));
-            if (w != 0.f) {
-                v.x += w * x.x;
-                v.y += w * x.y;
-                v.z += w * x.z;
-                v.w += w * x.w;
-            }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(sums + (w * C::kHeads + h) * C::kCombStride + d);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
         }
         const float inv = row_inv[h];
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
@@ -722,7 +826,9 @@ cudaError_t launch_t(const QuantDecodeArgs& a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    return launch_pdl(kern, dim3(a.max_splits, a.hkv, a.num_seqs), dim3(kThreads), C::kSmem, stream, a);
+    static_assert((kQuantCluster + 1) * 16 <= C::kHeads * C::kCombStride, "cluster merge weights");
+    return launch_pdl_cluster(kern, dim3(a.max_splits, a.hkv, a.num_seqs), dim3(kThreads), C::kSmem, stream,
+                              a.cluster ? static_cast<unsigned>(a.max_splits) : 1u, a);
 }
 
 template <int D, bool kFp4>
@@ -732,10 +838,9 @@ cudaError_t launch_g(const QuantDecodeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int quant_decode_ctas(int d, int fp4, int group) {
+int quant_decode_ctas(int d, int group) {
     const bool two = group > 8;
     if (d == 64) return two ? Cfg<64, true, 2>::kCtas : Cfg<64, true, 1>::kCtas;
-    (void)fp4;
     return two ? Cfg<128, true, 2>::kCtas : Cfg<128, true, 1>::kCtas;
 }
 
