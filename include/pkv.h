@@ -597,9 +597,10 @@ pkv_status pkv_quant_load_blocks(const pkv_cache_desc *desc, const void *k_pool,
  * the softmax weights rounded to f16; sums and softmax statistics are fp32.
  *   chunk_blocks: blocks per chunk; 0 lets the planner choose, else 1..512; a
  *                 context is cut into at most 256 chunks.
- *   workspace   : >= pkv_quant_decode_workspace_size(...) bytes, 256-byte aligned,
- *                 zero-filled before its first use; every call leaves its tickets
- *                 zeroed.  Calls that share a workspace must not overlap on the GPU. */
+ *   workspace   : >= pkv_quant_decode_workspace_size(...) bytes, 256-byte aligned, no
+ *                 initial contents.  Calls that share a workspace must not overlap on
+ *                 the GPU (nor the replays of graphs that captured them).
+ * One launch, or two where a sequence's chunks merge through the workspace. */
 pkv_status pkv_quant_decode(const pkv_cache_desc *desc, const void *q, const void *k_pool,
                             const void *v_pool, const float *k_scale, const float *v_scale,
                             const int32_t *block_tables, const int32_t *context_lens,

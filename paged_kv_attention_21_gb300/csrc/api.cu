@@ -1692,18 +1692,22 @@ pkv_status pkv_quant_load_blocks(const pkv_cache_desc* desc, const void* k_pool,
 namespace {
 
 // Chunk length (blocks), chunks per (sequence, KV head), and whether those merge in a
-// cluster or by tickets.  Measured on 4-bit D128 and int8 D64 pools, 8 heads a group:
+// cluster or by a second launch.  Measured on 4-bit D128 pools, 8 heads a group, with
+// contexts between a sixteenth (or half) of the longest and the longest; "pairs" are
+// sequences x KV heads:
 //   * a ragged batch averages about half its longest context: chunks aim for one wave
-//     of resident CTAs, at least 32 blocks (a start and an end cost a warp about 3
-//     blocks' work: 120 x 8 pairs of 64..2048 blocks took 544 us with 64-block chunks,
-//     488 with 128, 470 with 256), at most 128, or 256 from 4 waves of such chunks on;
-//   * 2..8 chunks merge in a cluster while the whole grid is resident (32 pairs of
-//     16..256 blocks: 10.1 us, 12.4 by tickets); beyond, clusters wait for their
-//     places (1024 CTAs on 608: 23.0 us, 18.9 by tickets);
-//   * so a grid that stays resident takes up to 8 chunks, of at least 8 blocks (2 pairs
-//     of 48 blocks: 5.5 us in 6 chunks, 6.7 in one), short contexts only while half the
-//     GPU would idle (128 pairs of 48 blocks: 13.7 us in 6 chunks, 7.7 in one) and from
-//     32 blocks on (8 pairs of 16 blocks: 4.3 us in 2 chunks, 3.8 in one).
+//     of resident CTAs, at most 128 blocks, or 256 from 4 waves of such chunks on (960
+//     pairs of up to 2048 blocks: 544 us with 64-block chunks, 488, 470 and 480 with
+//     128, 256 and 512, before the merge left the kernel);
+//   * at least 8 blocks, a pass of each warp, and at most 64 chunks (2 pairs of 256
+//     blocks: 5.9 us with 8-block chunks, 7.9 with 32; 8 pairs of 2048: 21.6 us with
+//     8, 15.4 with 16, 13.0 with 32);
+//   * a context of at most 48 blocks stays one chunk unless half the GPU would idle (128
+//     pairs: 7.3 us in one chunk, 9.9 in six; 8 pairs: 6.5 and 5.6);
+//   * 2..8 chunks merge in a cluster while the whole grid is resident (beyond, clusters
+//     wait for their places: 1024 CTAs on 608 took 22.6 us, 18.8 merged through the
+//     workspace), and a grid of a quarter to half of that takes 8 chunks for it (32 pairs
+//     of 256 blocks: 9.4 us, 10.6 with 16-block chunks merged by the second launch).
 struct QuantPlan {
     int chunk, splits;
     bool cluster;
@@ -1716,11 +1720,16 @@ pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_c
                          pkv::quant_decode_ctas(desc->head_dim, desc->num_q_heads / desc->num_kv_heads);
     int chunk = chunk_req;
     if (chunk <= 0) {
+        auto whole = [](int blocks) { return (blocks + 7) / 8 * 8; };  // a pass of each warp
         const int cap = pairs * (0.55 * mb / 256 + 0.5) >= 4.0 * slots ? 256 : 128;
-        chunk = std::max(32, std::min(cap, int(std::ceil(pairs * std::max(1.0, 0.55 * mb) / slots))));
-        const int eighth = (((mb + 7) / 8 + 7) / 8) * 8;
+        const double wave = pairs * std::max(1.0, 0.55 * mb) / slots;
+        chunk = whole(std::max((mb + 63) / 64, int(std::ceil(std::min(wave, double(cap))))));
+        const int eighth = whole((mb + 7) / 8);
         const double ctas = pairs * ((mb + eighth - 1) / eighth);
-        if (mb >= 32 && eighth <= chunk && ctas <= (mb <= 48 ? 0.5 * slots : slots)) chunk = eighth;
+        if (mb <= 48)
+            chunk = ctas <= 0.4 * slots && mb >= 32 ? eighth : mb;
+        else if (chunk < eighth && ctas > 0.25 * slots && ctas <= 0.5 * slots)
+            chunk = eighth;
         chunk = std::max(chunk, (mb + pkv::kQuantMaxSplits - 1) / pkv::kQuantMaxSplits);
         chunk = std::min(chunk, mb);
     }
@@ -1731,6 +1740,20 @@ pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_c
     out->splits = (mb + chunk - 1) / chunk;
     out->cluster = out->splits > 1 && out->splits <= pkv::kQuantCluster && pairs * out->splits <= slots;
     return PKV_OK;
+}
+
+struct QuantWs {
+    size_t lse, o, total;
+};
+
+// The chunks' states; none where one chunk or a cluster needs no workspace.
+QuantWs quant_ws_layout(const pkv_cache_desc* d, int num_seqs, const QuantPlan& plan) {
+    QuantWs w{};
+    if (plan.splits == 1 || plan.cluster) return w;
+    const size_t rows = size_t(num_seqs) * d->num_q_heads * plan.splits;
+    w.o = align256(rows * sizeof(float));
+    w.total = w.o + align256(rows * d->head_dim * sizeof(float));
+    return w;
 }
 
 }  // namespace
@@ -1746,7 +1769,7 @@ size_t pkv_quant_decode_workspace_size(const pkv_cache_desc* desc, int32_t num_s
     if (device_state(nullptr, &sms) != PKV_OK) return 0;
     QuantPlan plan;
     if (plan_quant_decode(desc, num_seqs, max_context_len, window, sms, chunk_blocks, &plan) != PKV_OK) return 0;
-    return plan.cluster ? 0 : decode_ws_layout(desc, num_seqs, plan.splits).total;
+    return quant_ws_layout(desc, num_seqs, plan).total;
 }
 
 pkv_status pkv_quant_decode(const pkv_cache_desc* desc, const void* q, const void* k_pool, const void* v_pool,
@@ -1780,14 +1803,13 @@ pkv_status pkv_quant_decode(const pkv_cache_desc* desc, const void* q, const voi
     a.chunk_blocks = plan.chunk;
     a.max_splits = plan.splits;
     a.cluster = plan.cluster ? 1 : 0;
-    const DecodeWs ws = decode_ws_layout(desc, num_seqs, a.max_splits);
-    if (ws.total > 0 && !plan.cluster) {
+    const QuantWs ws = quant_ws_layout(desc, num_seqs, plan);
+    if (ws.total > 0) {
         if (!workspace) return fail(PKV_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", ws.total);
         if (!aligned(workspace, 256)) return fail(PKV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
         if (workspace_bytes < ws.total)
             return fail(PKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, ws.total);
         uint8_t* wsb = static_cast<uint8_t*>(workspace);
-        a.counters = reinterpret_cast<uint32_t*>(wsb + ws.counters);
         a.part_lse = reinterpret_cast<float*>(wsb + ws.lse);
         a.part_o = reinterpret_cast<float*>(wsb + ws.o);
     }

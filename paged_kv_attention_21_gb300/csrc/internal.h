@@ -253,9 +253,8 @@ struct QuantDecodeArgs {
     const float* sinks;  // nullable
     void* out;
     float* lse_out;  // nullable
-    uint32_t* counters;  // [num_seqs * hkv], zero on entry and exit (more than one chunk)
-    float* part_lse;     // [num_seqs * hkv * max_splits * group]
-    float* part_o;       // [num_seqs * hkv * max_splits * group * d]
+    float* part_lse;     // [num_seqs * hkv * max_splits * group]: the chunks' states, merged by
+    float* part_o;       // [num_seqs * hkv * max_splits * group * d]   the launch that follows
     int64_t num_blocks;
     int32_t num_seqs, hq, hkv, group, d, fp4, mbps, ring, window, max_ctx, chunk_blocks, max_splits;
     int32_t cluster;  // the chunks of a (sequence, KV head) are one cluster (at most kQuantCluster)

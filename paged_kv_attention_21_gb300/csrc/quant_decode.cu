@@ -6,12 +6,14 @@
 //
 // Work decomposition.  The visible blocks of every (sequence, KV head) are cut
 // into chunks (the planner in api.cu); a CTA owns one chunk and its 4 warps
-// take the chunk's blocks round-robin, each with its own ring of asynchronous
-// copies (a K record and a V record per stage, 16 bytes a lane; a record holds codes
-// and scales side by side, already in the bank-conflict-free order).  The
-// warps' states meet in shared memory; a sequence of several chunks merges
-// through the workspace, the last chunk to take its ticket joining all of them
-// in chunk order.
+// take the chunk's blocks round-robin, NB at a time, each with its own ring of
+// asynchronous copies (a K record and a V record per block, 16 bytes a lane; a record
+// holds codes and scales side by side, already in the bank-conflict-free order).
+// The warps' states meet in shared memory.  The chunks of a sequence merge in a
+// thread-block cluster where the whole grid is resident, else by a second launch over
+// the fp32 states they leave in the workspace: a last-chunk ticket in this kernel cost
+// 3 to 6 us of fence, atomic and serial merge (2 pairs of 2048 blocks 12.8 us, 7.9 with
+// the second launch; 960 pairs 434 us, 424), and its registers slowed the main loop 3 %.
 //
 // The MMAs run transposed: S^T = K Q^T and O^T += V^T P^T (m16n8k16, f16 ->
 // fp32), so the 16 tokens of a block (S^T) and the head's dims (O^T) fill the
@@ -34,8 +36,16 @@
 // stays in f16's range).  Weights are rounded to f16 (2^-11); the statistics,
 // l and O are fp32.
 //
-// Roofline: HBM.  Per token and KV head 2 (D + 4) bytes (int8) or 2 (D/2 + D/16)
-// (4-bit) against 4 D G flops.
+// What bounds it.  Per token and KV head it reads 2 (D + 4) bytes (int8) or 2 (D/2 + D/16)
+// (4-bit) for 4 D G flops: HBM by the roofline.  int8 gets there (one steady wave:
+// 5.9-6.2 TB/s).  A 4-bit block of D = 128 is 2304 bytes and costs a warp about 270
+// instructions beside 16 MMAs, which hold the issue port for 8 cycles each (an MMA with 4
+// independent FMAs measured 11.7 cycles, alone 8.0): some 400 issue cycles where HBM
+// delivers a block every 404.  So one steady wave runs at 6.0 TB/s, its compute alone (all
+// blocks from L2) at 6.08 and its copies alone at 6.9.  Tried and dropped: one bulk copy
+// per record (5.49 TB/s: a copy's issue costs a warp more than 5 per-lane ones), one block
+// per pass (5.60), 5 or 6 CTAs per SM (5.49, 4.07: the port, not latency, is short),
+// 8-warp CTAs (long batch 462 us, 426 with 4 warps).
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -63,8 +73,7 @@ struct Cfg {
     static constexpr int kCombStride = D + 4;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kComb = kWarps * kHeads * kCombStride * 4;
-    static constexpr int kMerge = kComb + (kQuantMaxSplits + 1) * 16 * 4;
-    static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 128;
+    static constexpr int kSmem = (kRing > kComb ? kRing : kComb) + 128;
     // registers: NT * D / 4 accumulators and NT * D / 8 of q
     static constexpr int kCtas = NT * D > 128 ? 3 : 4;
 };
@@ -411,13 +420,69 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
         accumulate<D, kFp4, NT>(st.o, pb[b], stage + b * C::kBlock + C::kTile, g, ta, tb, vs2[b]);
 }
 
+// The chunks of a (sequence, KV head) are one cluster: each joins its share of the
+// output from its peers' shared memory (states in comb's first rows, their lse).
+// Out of line, so that the merge's registers do not weigh on the main loop.
 template <int D, bool kFp4, int NT>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_decode_kernel(QuantDecodeArgs a) {
+__device__ __noinline__ void merge_cluster(const QuantDecodeArgs& a, float* comb, const float* lse, int split, int kvh,
+                                           size_t head0, int nsplit) {
+    using C = Cfg<D, kFp4, NT>;
+    const int G = a.group;
+    cluster_sync();
+    float* wts = comb + C::kHeads * C::kCombStride;  // warp 1's rows, free now: [chunk][16]
+    float* row_inv = wts + kQuantCluster * 16;
+    if (threadIdx.x < G) {
+        const int h = threadIdx.x;
+        const float sk = a.sinks ? a.sinks[kvh * G + h] : -INFINITY;
+        float l[kQuantCluster], M = sk;
+#pragma unroll
+        for (int c = 0; c < kQuantCluster; ++c) {
+            l[c] = c < nsplit ? ld_cluster_f32(cluster_map(smem_u32(&lse[h]), c)) : -INFINITY;
+            M = fmaxf(M, l[c]);
+        }
+        float W = sk == -INFINITY ? 0.f : expf(sk - M);
+#pragma unroll
+        for (int c = 0; c < kQuantCluster; ++c) {
+            const float w = l[c] == -INFINITY ? 0.f : expf(l[c] - M);
+            wts[c * 16 + h] = w;
+            W += w;
+        }
+        row_inv[h] = W != 0.f ? 1.f / W : 0.f;
+        if (a.lse_out && split == 0) a.lse_out[head0 + h] = W != 0.f ? M + logf(W) : -INFINITY;
+    }
+    __syncthreads();
+    const int total = G * (D / 4);
+    for (int i = split * total / nsplit + threadIdx.x; i < (split + 1) * total / nsplit; i += kThreads) {
+        const int h = i / (D / 4), d = 4 * (i % (D / 4));
+        const uint32_t at = smem_u32(comb + h * C::kCombStride + d);
+        float4 x[kQuantCluster];
+#pragma unroll
+        for (int c = 0; c < kQuantCluster; ++c)
+            if (c < nsplit) x[c] = ld_cluster_f32x4(cluster_map(at, c));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kQuantCluster; ++c) {
+            const float w = wts[c * 16 + h];
+            if (c < nsplit && w != 0.f) {
+                v.x += w * x[c].x;
+                v.y += w * x[c].y;
+                v.z += w * x[c].z;
+                v.w += w * x[c].w;
+            }
+        }
+        const float inv = row_inv[h];
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
+            make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
+    }
+    cluster_sync();  // no chunk leaves while a peer may still read its state
+}
+
+template <int D, bool kFp4, int NT, bool kCluster>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_decode_kernel(const __grid_constant__ QuantDecodeArgs a) {
     using C = Cfg<D, kFp4, NT>;
     using R = QuantRecord<D, kFp4>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_v[kWarps];
-    __shared__ int s_flag;
     uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
@@ -645,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
                 make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
             if (a.lse_out && d == 0) a.lse_out[head0 + h] = s_l[0][h];
-        } else if (a.cluster) {  // the chunk's state stays here, in place of warp 0's rows
+        } else if (kCluster) {  // the chunk's state stays here, in place of warp 0's rows
             *reinterpret_cast<float4*>(comb + h * C::kCombStride + d) = v;
         } else {
             const size_t prow = (pair * a.max_splits + split) * G + h;
@@ -653,168 +718,126 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
             if (d == 0) a.part_lse[prow] = s_l[0][h];
         }
     }
-    if (nsplit == 1) return;
-
-    if (a.cluster) {
-        // ---- the chunks of this (sequence, KV head) are one cluster: after the barrier
-        // each joins its share of the output from its peers' shared memory
-        cluster_sync();
-        float* wts = comb + C::kHeads * C::kCombStride;  // warp 1's rows, free now: [chunk][16]
-        float* row_inv = wts + kQuantCluster * 16;
-        if (threadIdx.x < G) {
-            const int h = threadIdx.x;
-            const float sk = a.sinks ? a.sinks[kvh * G + h] : -INFINITY;
-            float l[kQuantCluster], M = sk;
-#pragma unroll
-            for (int c = 0; c < kQuantCluster; ++c) {
-                l[c] = c < nsplit ? ld_cluster_f32(cluster_map(smem_u32(&s_l[0][h]), c)) : -INFINITY;
-                M = fmaxf(M, l[c]);
-            }
-            float W = sk == -INFINITY ? 0.f : expf(sk - M);
-#pragma unroll
-            for (int c = 0; c < kQuantCluster; ++c) {
-                const float w = l[c] == -INFINITY ? 0.f : expf(l[c] - M);
-                wts[c * 16 + h] = w;
-                W += w;
-            }
-            row_inv[h] = W != 0.f ? 1.f / W : 0.f;
-            if (a.lse_out && split == 0) a.lse_out[head0 + h] = W != 0.f ? M + logf(W) : -INFINITY;
-        }
-        __syncthreads();
-        const int total = G * (D / 4);
-        for (int i = split * total / nsplit + threadIdx.x; i < (split + 1) * total / nsplit; i += kThreads) {
-            const int h = i / (D / 4), d = 4 * (i % (D / 4));
-            const uint32_t at = smem_u32(comb + h * C::kCombStride + d);
-            float4 x[kQuantCluster];
-#pragma unroll
-            for (int c = 0; c < kQuantCluster; ++c)
-                if (c < nsplit) x[c] = ld_cluster_f32x4(cluster_map(at, c));
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < kQuantCluster; ++c) {
-                const float w = wts[c * 16 + h];
-                if (c < nsplit && w != 0.f) {
-                    v.x += w * x[c].x;
-                    v.y += w * x[c].y;
-                    v.z += w * x[c].z;
-                    v.w += w * x[c].w;
-                }
-            }
-            const float inv = row_inv[h];
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
-                make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
-        }
-        cluster_sync();  // no chunk leaves while a peer may still read its state
-        return;
-    }
-
-    // ---- the last chunk of this (sequence, KV head) to arrive joins them all
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();  // cumulative: the CTA's states, written before the barrier, are out first
-        s_flag = static_cast<int>(atomicAdd(&a.counters[pair], 1u));
-        __threadfence();
-    }
-    __syncthreads();
-    if (s_flag != nsplit - 1) return;
-    float* sums = comb;                                            // [warp][head][D]
-    float* wts = comb + kWarps * C::kHeads * C::kCombStride;  // [chunk][G], then 1 / the sum per head
-    float* row_inv = wts + kQuantMaxSplits * 16;
-    {
-        // the chunks' lse, one round trip for all: wts[chunk][G] until they are weights
-        const float* pl = a.part_lse + pair * a.max_splits * G;
-        for (int i = threadIdx.x; i < nsplit * G; i += 4 * kThreads) {
-            float l[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) l[u] = __ldcg(pl + min(i + u * kThreads, nsplit * G - 1));
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i + u * kThreads < nsplit * G) wts[i + u * kThreads] = l[u];
-        }
-        __syncthreads();
-        const int h = threadIdx.x >> 3, sub = threadIdx.x & 7;  // 16 heads x 8 threads
-        const float sk = a.sinks && h < G ? a.sinks[kvh * G + h] : -INFINITY;
-        float M = sk;
-        if (h < G)
-            for (int i = sub; i < nsplit; i += 8) M = fmaxf(M, wts[i * G + h]);
-#pragma unroll
-        for (int x = 1; x < 8; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
-        float W = 0.f;
-        if (h < G)
-            for (int i = sub; i < nsplit; i += 8) {
-                const float l = wts[i * G + h];
-                const float w = l == -INFINITY ? 0.f : expf(l - M);
-                wts[i * G + h] = w;
-                W += w;
-            }
-#pragma unroll
-        for (int x = 1; x < 8; x <<= 1) W += __shfl_xor_sync(0xFFFFFFFFu, W, x);
-        if (sub == 0 && h < G) {
-            if (sk != -INFINITY) W += expf(sk - M);
-            row_inv[h] = W != 0.f ? 1.f / W : 0.f;
-            if (a.lse_out) a.lse_out[head0 + h] = W != 0.f ? M + logf(W) : -INFINITY;
-        }
-    }
-    __syncthreads();
-    // a warp takes every 4th chunk's whole state, kAhead chunks' loads in flight (past the
-    // end the last chunk's again, weighted 0); the warps' sums meet in shared memory
-    {
-        constexpr int kSlots = C::kHeads * D / 128;  // float4s of a state per lane
-        constexpr int kAhead = kSlots > 8 ? 1 : 2;
-        const float* po = a.part_o + pair * a.max_splits * G * D;
-        float4 v[kSlots];
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = warp; c0 < nsplit; c0 += kAhead * kWarps) {
-            float4 x[kAhead][kSlots];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-                for (int j = 0; j < kSlots; ++j)
-                    x[u][j] = __ldcg(reinterpret_cast<const float4*>(
-                        po + static_cast<size_t>(min(c0 + u * kWarps, nsplit - 1)) * G * D + min(4 * (lane + 32 * j), G * D - 4)));
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-                for (int j = 0; j < kSlots; ++j) {
-                    const int c = c0 + u * kWarps, h = min(4 * (lane + 32 * j) / D, G - 1);
-                    const float w = c < nsplit ? wts[c * G + h] : 0.f;
-                    v[j].x += w * x[u][j].x;
-                    v[j].y += w * x[u][j].y;
-                    v[j].z += w * x[u][j].z;
-                    v[j].w += w * x[u][j].w;
-                }
-        }
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-            const int i = 4 * (lane + 32 * j);
-            *reinterpret_cast<float4*>(sums + (warp * C::kHeads + i / D) * C::kCombStride + i % D) = v[j];
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * (D / 4); i += kThreads) {
-        const int h = i / (D / 4), d = 4 * (i % (D / 4));
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float4 x = *reinterpret_cast<const float4*>(sums + (w * C::kHeads + h) * C::kCombStride + d);
-            v.x += x.x;
-            v.y += x.y;
-            v.z += x.z;
-            v.w += x.w;
-        }
-        const float inv = row_inv[h];
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (head0 + h) * D + d) =
-            make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
-    }
-    if (threadIdx.x == 0) a.counters[pair] = 0u;
+    if constexpr (kCluster)
+        if (nsplit > 1) merge_cluster<D, kFp4, NT>(a, comb, s_l[0], split, kvh, head0, nsplit);
 }
 
-template <int D, bool kFp4, int NT>
+// ------------------------------------------------------------- merge --
+//
+// The chunks' states of kHeads query heads of one (sequence, KV head) -> their output
+// rows.  kHeads * D / 4 threads hold a float4 column each; where that is less than the
+// CTA, thread groups take every kGroups-th chunk and meet in shared memory in a fixed
+// order.  8 chunks' loads are in flight beside the lse.
+template <int D, int kHeads>
+__global__ void __launch_bounds__(kThreads) quant_merge_kernel(const __grid_constant__ QuantDecodeArgs a) {
+    constexpr int kCols = D / 4, kWide = kHeads * kCols, kGroups = kThreads / kWide;
+    static_assert(kWide <= kThreads && kThreads % kWide == 0, "whole thread groups");
+    __shared__ float wts[kHeads][kQuantMaxSplits];
+    __shared__ float s_inv[kHeads];
+    __shared__ float4 s_sum[kGroups > 1 ? kThreads : 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blocks = (a.group + kHeads - 1) / kHeads;  // CTAs per (sequence, KV head)
+    const int kvh = blockIdx.x / blocks, g0 = blockIdx.x % blocks * kHeads, seq = blockIdx.y;
+    const int heads = min(kHeads, a.group - g0);
+    const size_t row0 = static_cast<size_t>(seq) * a.hq + kvh * a.group + g0;
+    // the lengths and sinks are older than the launch this one follows, which started
+    // only after its own predecessors: they are read before the wait for it
+    const int ctx = min(a.context_lens[seq], a.max_ctx);
+    const int lo = a.window > 0 && ctx > a.window ? ctx - a.window : 0;
+    const int nsplit = ctx <= 0 ? 1 : ((ctx - 1) / kBlockSize - lo / kBlockSize + a.chunk_blocks) / a.chunk_blocks;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (nsplit == 1) return;  // its chunk wrote the output
+    const size_t part = (static_cast<size_t>(seq) * a.hkv + kvh) * a.max_splits * a.group + g0;
+    // this thread's column; heads past the group read the last one's and write nothing
+    const int col = threadIdx.x % kWide, h = min(col / kCols, heads - 1), first = threadIdx.x / kWide;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + (part + h) * D) + col % kCols;
+    const size_t step = static_cast<size_t>(a.group) * kCols;
+    float4 x[8];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = po[min(c0 + u * kGroups, nsplit - 1) * step];
+    };
+    fetch(first);
+    for (int i = warp; i < heads; i += kWarps) {
+        constexpr int kPer = kQuantMaxSplits / 32;
+        const float sk = a.sinks ? a.sinks[kvh * a.group + g0 + i] : -INFINITY;
+        float l[kPer], M = sk;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int c = lane + 32 * u;
+            l[u] = c < nsplit ? a.part_lse[part + static_cast<size_t>(c) * a.group + i] : -INFINITY;
+        }
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) M = fmaxf(M, l[u]);
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, s));
+        float W = 0.f;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            if (32 * u >= nsplit) break;
+            const float w = l[u] == -INFINITY ? 0.f : expf(l[u] - M);
+            wts[i][lane + 32 * u] = w;
+            W += w;
+        }
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) W += __shfl_xor_sync(0xFFFFFFFFu, W, s);
+        if (sk != -INFINITY) W += expf(sk - M);
+        if (lane == 0) {
+            s_inv[i] = W != 0.f ? 1.f / W : 0.f;
+            if (a.lse_out) a.lse_out[row0 + i] = W != 0.f ? M + logf(W) : -INFINITY;
+        }
+    }
+    __syncthreads();
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = first; c0 < nsplit;) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int c = c0 + u * kGroups;
+            const float w = c < nsplit ? wts[h][c] : 0.f;
+            v.x += w * x[u].x;
+            v.y += w * x[u].y;
+            v.z += w * x[u].z;
+            v.w += w * x[u].w;
+        }
+        c0 += 8 * kGroups;
+        if (c0 < nsplit) fetch(c0);
+    }
+    if constexpr (kGroups > 1) {
+        s_sum[threadIdx.x] = v;
+        __syncthreads();
+        if (first > 0) return;
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) {
+            const float4 y = s_sum[i * kWide + col];
+            v.x += y.x;
+            v.y += y.y;
+            v.z += y.z;
+            v.w += y.w;
+        }
+    }
+    if (col / kCols >= heads) return;
+    const float inv = s_inv[h];
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (row0 + h) * D + 4 * (col % kCols)) =
+        make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
+}
+
+template <int D>
+cudaError_t launch_merge_states(const QuantDecodeArgs& a, cudaStream_t stream) {
+    // a head per CTA while all of them are resident at once; the widest CTAs beyond
+    constexpr int kMost = 4 * kThreads / D;
+    if (static_cast<long long>(a.num_seqs) * a.hq <= 152 * 16)
+        return launch_pdl(quant_merge_kernel<D, 1>, dim3(a.hq, a.num_seqs), dim3(kThreads), 0, stream, a);
+    return launch_pdl(quant_merge_kernel<D, kMost>, dim3(a.hkv * ((a.group + kMost - 1) / kMost), a.num_seqs), dim3(kThreads), 0,
+                      stream, a);
+}
+
+template <int D, bool kFp4, int NT, bool kCluster>
 cudaError_t launch_t(const QuantDecodeArgs& a, cudaStream_t stream) {
     using C = Cfg<D, kFp4, NT>;
     static_assert(C::kSmem <= 227 * 1024, "shared memory budget");
-    auto kern = quant_decode_kernel<D, kFp4, NT>;
+    static_assert((kQuantCluster + 1) * 16 <= C::kHeads * C::kCombStride, "cluster merge weights");
+    auto kern = quant_decode_kernel<D, kFp4, NT, kCluster>;
     // a per-device function attribute, set on the first launch on each device
     static bool attr_set[64] = {};
     int dev = 0;
@@ -826,14 +849,16 @@ cudaError_t launch_t(const QuantDecodeArgs& a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    static_assert((kQuantCluster + 1) * 16 <= C::kHeads * C::kCombStride, "cluster merge weights");
-    return launch_pdl_cluster(kern, dim3(a.max_splits, a.hkv, a.num_seqs), dim3(kThreads), C::kSmem, stream,
-                              a.cluster ? static_cast<unsigned>(a.max_splits) : 1u, a);
+    e = launch_pdl_cluster(kern, dim3(a.max_splits, a.hkv, a.num_seqs), dim3(kThreads), C::kSmem, stream,
+                           kCluster ? static_cast<unsigned>(a.max_splits) : 1u, a);
+    if (e != cudaSuccess || kCluster || a.max_splits == 1) return e;
+    return launch_merge_states<D>(a, stream);
 }
 
 template <int D, bool kFp4>
 cudaError_t launch_g(const QuantDecodeArgs& a, cudaStream_t stream) {
-    return a.group <= 8 ? launch_t<D, kFp4, 1>(a, stream) : launch_t<D, kFp4, 2>(a, stream);
+    if (a.cluster) return a.group <= 8 ? launch_t<D, kFp4, 1, true>(a, stream) : launch_t<D, kFp4, 2, true>(a, stream);
+    return a.group <= 8 ? launch_t<D, kFp4, 1, false>(a, stream) : launch_t<D, kFp4, 2, false>(a, stream);
 }
 
 }  // namespace
