@@ -551,7 +551,9 @@ uint64_t pkv_quant_cache_bytes(const pkv_cache_desc *desc);
 /* Append: token i of sequence s = token_to_seq[i] at positions[i] goes into the
  * slot pkv_append_rope would use, K rotated (rope != NULL) in fp32 and quantised,
  * V quantised; q_out[i] = q[i] rotated (rope != NULL, q != NULL), rounded to bf16.
- * token_to_seq[i] < 0 is padding: nothing of that token is written.
+ * token_to_seq[i] < 0 is padding: nothing of that token is written.  A sequence or
+ * position out of range skips the token, a bad block id its K and V; either sets its
+ * device error bit.
  *   k_new, v_new: bf16, token i's [Hkv][D] rows at i * new_token_stride elements;
  *   q, q_out    : bf16, token i's [Hq][D] rows at i * q_token_stride /
  *                 q_out_token_stride; q_out == q rotates in place; q may be NULL,

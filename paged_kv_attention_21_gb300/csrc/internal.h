@@ -207,7 +207,10 @@ struct RotateArgs {
     const float* cos_sin;
     const int32_t* positions;
     int32_t num_tokens, d, rotary, interleaved, inverse, max_pos, dtype;
-    uint32_t* err;
+    uint32_t* err;  // null: bad positions are skipped without a flag
+    // the append's q rows: tokens whose sequence or table position is bad are skipped too
+    const int32_t* token_to_seq;  // nullable
+    int32_t num_seqs, mbps, ring;
 };
 cudaError_t launch_rope_rotate(const RotateArgs& a, cudaStream_t stream);
 
@@ -233,6 +236,9 @@ struct QuantArgs {
     int64_t num_blocks, dst_num_blocks;
     int32_t num_tokens;  // load: pairs of blocks
     int32_t num_seqs, hq, hkv, d, fp4, mbps, ring, rotary, interleaved, inverse, max_pos, out_f32;
+    // append: the launch before it in the stream shares nothing with it and waited for
+    // what came earlier, so this one waits for it only before it ends
+    int32_t defer_wait;
     uint32_t* err;
     cudaStream_t stream;
 };

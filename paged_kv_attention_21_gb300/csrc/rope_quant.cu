@@ -57,65 +57,65 @@ __device__ __forceinline__ float2 turn(float a, float b, float c, float s) {
     return make_float2(__fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)), __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
 }
 
-// ------------------------------------------------------------- rotation --
-//
-// Rows by strides.  A thread takes one vector position of kRows heads of a token:
-// with half-split pairs the vectors at j and j + r/2, with interleaved pairs one
-// vector; positions past the rotary dims copy a vector (out of place only).
-
-struct RotateRow {
-    const uint8_t* in;
-    uint8_t* out;
-};
-
-template <typename T>
-__device__ __forceinline__ RotateRow rotate_row(const RotateArgs& a, long long i, int h) {
-    const bool is_k = h >= a.q.num_heads;
-    const RotateRows& r = is_k ? a.k : a.q;
-    if (is_k) h -= a.q.num_heads;
-    return RotateRow{static_cast<const uint8_t*>(r.in) + (i * r.in_token + h * r.in_head) * static_cast<long long>(sizeof(T)),
-                     static_cast<uint8_t*>(r.out) + (i * r.out_token + h * r.out_head) * static_cast<long long>(sizeof(T))};
+// Whether position p of sequence s has a table entry.
+__device__ __forceinline__ bool token_in_table(int s, int p, int num_seqs, int mbps, int ring) {
+    const int tb = ring > 0 ? (p / kBlockSize) % ring : p / kBlockSize;
+    return s >= 0 && s < num_seqs && p >= 0 && tb < mbps;
 }
 
+// ------------------------------------------------------------- rotation --
+//
+// Rows by strides.  A thread takes one vector position of kRows heads of a token, all of
+// q or all of k: with half-split pairs the vectors at j and j + r/2, with interleaved
+// pairs one vector; positions past the rotary dims copy a vector (out of place only).
+// It moves each byte once, so HBM bounds it; what it fights is the address arithmetic (one
+// base per thread, then the head stride) and latency (kRows vectors in flight before
+// anything waits, the position and table entry among them).
+
 template <typename T, bool kHalf, int kRows>
-__global__ void __launch_bounds__(256) rope_vector_kernel(RotateArgs a, int vectors, int slots, int first_token) {
+__global__ void __launch_bounds__(256) rope_vector_kernel(const __grid_constant__ RotateArgs a, unsigned vectors,
+                                                          unsigned q_slots, unsigned slots, int first_token) {
     pdl_wait();
     pdl_launch_dependents();
     constexpr int N = 16 / sizeof(T);
     constexpr int kPairs = kHalf ? N : N / 2;
     const unsigned idx = blockIdx.x * 256u + threadIdx.x;
-    const int v = static_cast<int>(idx % vectors);
-    const unsigned rest = idx / vectors;
-    const int slot = static_cast<int>(rest % slots);
-    const long long i = first_token + static_cast<long long>(rest / slots);
+    const unsigned rest = idx / vectors, v = idx - rest * vectors;
+    const unsigned token = rest / slots;
+    unsigned slot = rest - token * slots;
+    const long long i = first_token + static_cast<long long>(token);
     if (i >= a.num_tokens) return;
-    const int heads = a.q.num_heads + a.k.num_heads;
-    const int h0 = slot * kRows;
+    const bool is_k = slot >= q_slots;
+    if (is_k) slot -= q_slots;
+    const int h0 = static_cast<int>(slot) * kRows;
+    const int rows = min(kRows, (is_k ? a.k.num_heads : a.q.num_heads) - h0);
+    const int64_t in_head = is_k ? a.k.in_head : a.q.in_head, out_head = is_k ? a.k.out_head : a.q.out_head;
     const int half = a.rotary / 2;
-    const int turns = kHalf ? half / N : a.rotary / N;  // vector positions that rotate
+    const unsigned turns = static_cast<unsigned>(kHalf ? half : a.rotary) / N;  // vector positions that rotate
     const bool pass = v >= turns;
+    const int at = pass ? a.rotary + static_cast<int>(v - turns) * N : static_cast<int>(v) * N;
+    const T* in = static_cast<const T*>(is_k ? a.k.in : a.q.in) + i * (is_k ? a.k.in_token : a.q.in_token) + h0 * in_head + at;
+    T* out = static_cast<T*>(is_k ? a.k.out : a.q.out) + i * (is_k ? a.k.out_token : a.q.out_token) + h0 * out_head + at;
     // the rows' loads do not wait for the position's
     uint4 x[kRows], y[kHalf ? kRows : 1];
-    const int at = pass ? (a.rotary + (v - turns) * N) * static_cast<int>(sizeof(T)) : v * 16;
-    const int mate = at + half * static_cast<int>(sizeof(T));
     const int p = a.positions[i];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-        if (h0 + r < heads) {
-            const RotateRow row = rotate_row<T>(a, i, h0 + r);
-            x[r] = *reinterpret_cast<const uint4*>(row.in + at);
+        if (r < rows) {
+            x[r] = *reinterpret_cast<const uint4*>(in + r * in_head);
             if constexpr (kHalf)
-                if (!pass) y[r] = *reinterpret_cast<const uint4*>(row.in + mate);
+                if (!pass) y[r] = *reinterpret_cast<const uint4*>(in + r * in_head + half);
         }
     if (p < 0) return;
     if (p >= a.max_pos) {
-        if (v == 0 && slot == 0) flag_error(a.err, PKV_DEVERR_POSITION);
+        if (v == 0 && h0 == 0) flag_error(a.err, PKV_DEVERR_POSITION);
         return;
     }
+    if (a.token_to_seq && !token_in_table(a.token_to_seq[i], p, a.num_seqs, a.mbps, a.ring)) return;
     if (pass) {
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
-            if (h0 + r < heads) *reinterpret_cast<uint4*>(rotate_row<T>(a, i, h0 + r).out + at) = x[r];
+            if (r < rows) *reinterpret_cast<uint4*>(out + r * out_head) = x[r];
         return;
     }
     float c[kPairs], s[kPairs];
@@ -130,8 +130,7 @@ __global__ void __launch_bounds__(256) rope_vector_kernel(RotateArgs a, int vect
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-        if (h0 + r < heads) {
-            const RotateRow row = rotate_row<T>(a, i, h0 + r);
+        if (r < rows) {
             float f[N];
             unpack<T>(x[r], f);
             if constexpr (kHalf) {
@@ -143,7 +142,7 @@ __global__ void __launch_bounds__(256) rope_vector_kernel(RotateArgs a, int vect
                     f[j] = z.x;
                     g[j] = z.y;
                 }
-                *reinterpret_cast<uint4*>(row.out + mate) = pack<T>(g);
+                *reinterpret_cast<uint4*>(out + r * out_head + half) = pack<T>(g);
             } else {
 #pragma unroll
                 for (int j = 0; j < N; j += 2) {
@@ -152,14 +151,14 @@ __global__ void __launch_bounds__(256) rope_vector_kernel(RotateArgs a, int vect
                     f[j + 1] = z.y;
                 }
             }
-            *reinterpret_cast<uint4*>(row.out + at) = pack<T>(f);
+            *reinterpret_cast<uint4*>(out + r * out_head) = pack<T>(f);
         }
 }
 
 // Rows that no 16-byte vector fits (their address, stride, rotary or head dims):
 // one thread per (token, head, pair or passing element).
 template <typename T>
-__global__ void __launch_bounds__(256) rope_scalar_kernel(RotateArgs a) {
+__global__ void __launch_bounds__(256) rope_scalar_kernel(const __grid_constant__ RotateArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int half = a.rotary / 2;
@@ -176,9 +175,12 @@ __global__ void __launch_bounds__(256) rope_scalar_kernel(RotateArgs a) {
         if (it == 0) flag_error(a.err, PKV_DEVERR_POSITION);
         return;
     }
-    const RotateRow r = rotate_row<T>(a, i, static_cast<int>(row % heads));
-    const T* in = reinterpret_cast<const T*>(r.in);
-    T* out = reinterpret_cast<T*>(r.out);
+    if (a.token_to_seq && !token_in_table(a.token_to_seq[i], p, a.num_seqs, a.mbps, a.ring)) return;
+    int h = static_cast<int>(row % heads);
+    const RotateRows& r = h >= a.q.num_heads ? a.k : a.q;
+    if (h >= a.q.num_heads) h -= a.q.num_heads;
+    const T* in = static_cast<const T*>(r.in) + i * r.in_token + h * r.in_head;
+    T* out = static_cast<T*>(r.out) + i * r.out_token + h * r.out_head;
     if (it >= half) {
         out[it + half] = in[it + half];
         return;
@@ -193,89 +195,124 @@ __global__ void __launch_bounds__(256) rope_scalar_kernel(RotateArgs a) {
 
 // --------------------------------------------------------------- append --
 //
-// D/8 lanes per row, 8 dims each; rows are the Hq query heads, the Hkv K heads
-// and the Hkv V heads of a token, kRows consecutive ones per thread.
+// D/16 lanes per row, two vectors of 8 dims each: a rotation's pair of vectors where the
+// pairs are half-split, so that every byte and every (cos, sin) is read once.  A thread's
+// rows are kRows query, K or V heads of one token.
 
-// The block and slot of position p of sequence s: false for padding and for a bad position or
-// block id (flagged by `report`).
-__device__ __forceinline__ bool quant_slot(const QuantArgs& a, int s, int p, bool report, int* blk, int* row) {
+// The sequence and position of a token: false for padding and, flagged by `report`,
+// for a bad one.
+__device__ __forceinline__ bool quant_token(const QuantArgs& a, int s, int p, bool report) {
     if (s < 0) return false;
-    const int tb = a.ring > 0 ? (p / kBlockSize) % a.ring : p / kBlockSize;
-    if (s >= a.num_seqs || p < 0 || tb >= a.mbps || (a.cos_sin != nullptr && p >= a.max_pos)) {
-        if (report) flag_error(a.err, PKV_DEVERR_POSITION);
-        return false;
-    }
-    *row = p % kBlockSize;
-    *blk = a.block_tables[static_cast<size_t>(s) * a.mbps + tb];
-    if (*blk < 0 || *blk >= a.num_blocks) {
-        if (report) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-        return false;
-    }
-    return true;
+    if (token_in_table(s, p, a.num_seqs, a.mbps, a.ring) && (a.cos_sin == nullptr || p < a.max_pos)) return true;
+    if (report) flag_error(a.err, PKV_DEVERR_POSITION);
+    return false;
 }
 
-// 8 dims of a K or V row (dims 8 lane .. 8 lane + 7 of the row's lanes) into its record.
+// The block of a good token; false for a bad id.
+__device__ __forceinline__ bool quant_block(const QuantArgs& a, int s, int p, bool report, int* blk) {
+    const int tb = a.ring > 0 ? (p / kBlockSize) % a.ring : p / kBlockSize;
+    *blk = a.block_tables[static_cast<size_t>(s) * a.mbps + tb];
+    if (*blk >= 0 && *blk < a.num_blocks) return true;
+    if (report) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+    return false;
+}
+
+// A lane's two vectors of a K or V row, dims 8 c0 .. and 8 c1 .., into its record.  split:
+// the other half of each vector's 16 dims is in lane ^ 1; else c1 = c0 + 1 and they are
+// the lane's own.
 template <int D, bool kFp4>
-__device__ __forceinline__ void store_row(uint8_t* rec, int row, int lane, const float (&v)[8], float g, bool ok) {
+__device__ __forceinline__ void store_row(uint8_t* rec, int row, int lane, int c0, int c1, bool split, const float (&v0)[8],
+                                          const float (&v1)[8], float g, bool ok) {
     using R = QuantRecord<D, kFp4>;
-    float amax = 0.f;
+    float m0 = 0.f, m1 = 0.f;  // over all but NaN
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_magnitude(v[e]));
+    for (int e = 0; e < 8; e += 2) {
+        m0 = fmax3(m0, fabsf(v0[e]), fabsf(v0[e + 1]));
+        m1 = fmax3(m1, fabsf(v1[e]), fabsf(v1[e + 1]));
+    }
+    if (__any_sync(0xFFFFFFFFu, fmaxf(m0, m1) == INFINITY)) {
+        m0 = m1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            m0 = fmaxf(m0, finite_magnitude(v0[e]));
+            m1 = fmaxf(m1, finite_magnitude(v1[e]));
+        }
+    }
+    float y0[8], y1[8];
     if constexpr (kFp4) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        const uint32_t sc = fp4_scale_code(amax, g);
-        const float t = __fmul_rn(e4m3_float(sc), g);
-        uint32_t w = 0;
+        const float o0 = __shfl_xor_sync(0xFFFFFFFFu, m0, 1), o1 = __shfl_xor_sync(0xFFFFFFFFu, m1, 1);
+        const float own = fmaxf(m0, m1);
+        const uint32_t s0 = fp4_scale_code(split ? fmaxf(m0, o0) : own, g);
+        const uint32_t s1 = split ? fp4_scale_code(fmaxf(m1, o1), g) : s0;
+        quotients(v0, __fmul_rn(e4m3_float(s0), g), y0);
+        quotients(v1, __fmul_rn(e4m3_float(s1), g), y1);
+        uint32_t w0 = 0, w1 = 0;
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) w |= fp4_pair(fp4_quotient(v[e], t), fp4_quotient(v[e + 1], t)) << (4 * e);
+        for (int e = 0; e < 8; e += 2) {
+            w0 |= fp4_pair(y0[e], y0[e + 1]) << (4 * e);
+            w1 |= fp4_pair(y1[e], y1[e + 1]) << (4 * e);
+        }
         if (ok) {
-            *reinterpret_cast<uint32_t*>(rec + quant_byte<R::kRowBytes>(row, 4 * lane)) = w;
-            if (!(lane & 1)) rec[R::kScales + row * R::kScaleBytes + lane / 2] = static_cast<uint8_t>(sc);
+            *reinterpret_cast<uint32_t*>(rec + quant_byte<R::kRowBytes>(row, 4 * c0)) = w0;
+            *reinterpret_cast<uint32_t*>(rec + quant_byte<R::kRowBytes>(row, 4 * c1)) = w1;
+            uint8_t* sc = rec + R::kScales + row * R::kScaleBytes;
+            if (!split || !(lane & 1)) sc[c0 / 2] = static_cast<uint8_t>(s0);
+            if (split && !(lane & 1)) sc[c1 / 2] = static_cast<uint8_t>(s1);
         }
     } else {
+        float amax = fmaxf(m0, m1);
 #pragma unroll
-        for (int o = 1; o < D / 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        for (int o = 1; o < D / 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
         const float sc = __fdiv_rn(amax, 127.f);
-        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e / 4] |= int8_code(v[e], sc) << (8 * (e % 4));
+        quotients(v0, sc, y0);
+        quotients(v1, sc, y1);
         if (ok) {
-            *reinterpret_cast<uint2*>(rec + quant_byte<R::kRowBytes>(row, 8 * lane)) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(rec + quant_byte<R::kRowBytes>(row, 8 * c0)) = int8_codes(y0);
+            *reinterpret_cast<uint2*>(rec + quant_byte<R::kRowBytes>(row, 8 * c1)) = int8_codes(y1);
             if (lane == 0) *reinterpret_cast<float*>(rec + R::kScales + row * 4) = sc;
         }
     }
 }
 
-// How a row's pairs are found: any rotary dim element by element (or none), or
-// every lane's 8 dims inside the rotary dims or outside them, their partners in one
-// vector (half-split, r a multiple of 16) or in the lane (interleaved, r of 8).
+// How a row's pairs are found: any rotary dim (or none) element by element; half-split
+// with r a multiple of 32, a lane holding both vectors of its pairs; interleaved with r a
+// multiple of 16, a lane's 16 dims all inside the rotary dims or all outside.
 enum Pairs { kAnyPairs, kHalfPairs, kLanePairs };
 
 template <int D, bool kFp4, int kRows, int kPairs>
-__global__ void __launch_bounds__(256) quant_append_kernel(QuantArgs a, int slots) {
-    pdl_wait();
-    pdl_launch_dependents();
+__global__ void __launch_bounds__(256) quant_append_kernel(const __grid_constant__ QuantArgs a, unsigned q_slots,
+                                                           unsigned kv_slots, int first_token) {
+    if (!a.defer_wait) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     using R = QuantRecord<D, kFp4>;
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / 16;
     const int lane = threadIdx.x % kLanes;
-    const long long group = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
-    const long long i = group / slots;
-    const int r0 = static_cast<int>(group % slots) * kRows;
-    const int hq = a.q ? a.hq : 0;
-    const int turned = hq + a.hkv;  // rows that rotate
-    const int rows = turned + a.hkv;
-    const int d0 = 8 * lane;
+    const unsigned group = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    const unsigned slots = q_slots + 2 * kv_slots;
+    const unsigned token = group / slots;
+    unsigned slot = group - token * slots;
+    const long long i = first_token + static_cast<long long>(token);
+    // a thread's rows are query, K or V heads h0 .. h0 + rows - 1
+    const bool is_q = slot < q_slots;
+    const bool report = lane == 0 && slot == 0, report_block = lane == 0 && slot == q_slots;
+    if (!is_q) slot -= q_slots;
+    const bool is_v = !is_q && slot >= kv_slots;
+    if (is_v) slot -= kv_slots;
+    const int h0 = static_cast<int>(slot) * kRows;
+    const int rows = min(kRows, (is_q ? a.hq : a.hkv) - h0);
     const int half = a.rotary / 2;
-    const bool rope = a.cos_sin != nullptr && d0 < a.rotary;
-    const bool second = kPairs == kHalfPairs && d0 >= half;
-    auto source = [&](int r) {
-        return r < hq ? static_cast<const __nv_bfloat16*>(a.q) + i * a.q_stride + static_cast<size_t>(r) * D
-               : r < turned ? static_cast<const __nv_bfloat16*>(a.k_new) + i * a.new_stride + static_cast<size_t>(r - hq) * D
-                            : static_cast<const __nv_bfloat16*>(a.v_new) + i * a.new_stride + static_cast<size_t>(r - turned) * D;
-    };
-    // the rows' loads do not wait for the token's slot.  Every lane stays to the
-    // end: rows share shuffles with their warp.
-    uint4 x[kRows], y[kPairs == kHalfPairs ? kRows : 1];
+    // the lane's vectors
+    const int turning = a.rotary / 16;  // lanes that rotate (vector paths)
+    const bool split = kPairs == kHalfPairs && !is_v && lane < turning;
+    const int c0 = split ? lane : 2 * lane, c1 = split ? lane + turning : c0 + 1;
+    const bool rope = a.cos_sin != nullptr && !is_v && (kPairs == kAnyPairs ? 8 * c0 < a.rotary : lane < turning);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_q ? a.q : is_v ? a.v_new : a.k_new) +
+                               i * (is_q ? a.q_stride : a.new_stride) + h0 * D;
+    // the rows' loads do not wait for the token's position, nor the rotation for its
+    // block.  Every lane stays to the end: rows share shuffles with their warp.
+    uint4 x[kRows][2];
     const bool in = i < a.num_tokens;
     int s = -1, p = 0;
     if (in) {
@@ -284,34 +321,40 @@ __global__ void __launch_bounds__(256) quant_append_kernel(QuantArgs a, int slot
     }
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
-        x[n] = make_uint4(0u, 0u, 0u, 0u);
-        if (in && r0 + n < rows) {
-            const __nv_bfloat16* src = source(r0 + n);
-            x[n] = *reinterpret_cast<const uint4*>(src + d0);
-            if constexpr (kPairs == kHalfPairs)
-                if (rope && r0 + n < turned) y[n] = *reinterpret_cast<const uint4*>(src + (second ? d0 - half : d0 + half));
+        x[n][0] = x[n][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && n < rows) {
+            x[n][0] = *reinterpret_cast<const uint4*>(src + n * D + 8 * c0);
+            x[n][1] = *reinterpret_cast<const uint4*>(src + n * D + 8 * c1);
         }
     }
-    int blk = 0, row = 0;
-    const bool ok = in && quant_slot(a, s, p, lane == 0 && r0 == 0, &blk, &row);
-    // (cos, sin) of this lane's dims
-    constexpr int kCs = kPairs == kLanePairs ? 4 : 8;
+    float g[kRows];  // 4-bit: the heads' scales
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) {
+        g[n] = 1.f;
+        if (kFp4 && in && !is_q && n < rows) g[n] = (is_v ? a.v_scale : a.k_scale)[h0 + n];
+    }
+    const bool ok = in && quant_token(a, s, p, report);
+    int blk = 0;
+    const bool stored = ok && !is_q && quant_block(a, s, p, report_block, &blk);
+    // (cos, sin) of the lane's pairs: 8 on the vector paths (of c0 with c1, or of the 16
+    // dims), else one per dim
+    constexpr int kCs = kPairs == kAnyPairs ? 16 : 8;
     float c[kCs], sn[kCs];
-    if (ok && rope && r0 < turned) {
+    if (ok && rope) {
         const float* cs = a.cos_sin + static_cast<size_t>(p) * a.rotary;
         if constexpr (kPairs == kAnyPairs) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int d = d0 + e;
+            for (int e = 0; e < 16; ++e) {
+                const int d = 8 * c0 + e;
                 if (d >= a.rotary) continue;
                 const float2 t = *reinterpret_cast<const float2*>(cs + 2 * (a.interleaved ? d >> 1 : d < half ? d : d - half));
                 c[e] = t.x;
                 sn[e] = t.y;
             }
         } else {
-            const float4* t4 = reinterpret_cast<const float4*>(cs + (kPairs == kLanePairs ? d0 : 2 * (second ? d0 - half : d0)));
+            const float4* t4 = reinterpret_cast<const float4*>(cs + 16 * lane);
 #pragma unroll
-            for (int e = 0; e < kCs; e += 2) {
+            for (int e = 0; e < 8; e += 2) {
                 const float4 t = t4[e / 2];
                 c[e] = t.x;
                 sn[e] = t.y;
@@ -324,57 +367,57 @@ __global__ void __launch_bounds__(256) quant_append_kernel(QuantArgs a, int slot
             for (int e = 0; e < kCs; ++e) sn[e] = -sn[e];
         }
     }
+    __syncwarp();  // q in place: the rows' lanes have read their vectors
+    uint8_t* rec = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(blk) * a.hkv + h0) * R::kBytes;
+    __nv_bfloat16* q_out = static_cast<__nv_bfloat16*>(a.q_out) + i * a.q_out_stride + h0 * D;
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
-        const int r = r0 + n;
-        const bool live = ok && r < rows;
-        float v[8];
-        unpack<__nv_bfloat16>(x[n], v);
-        if (live && rope && r < turned) {
-            if constexpr (kPairs == kLanePairs) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 z = turn(v[e], v[e + 1], c[e / 2], sn[e / 2]);
-                    v[e] = z.x;
-                    v[e + 1] = z.y;
-                }
-            } else if constexpr (kPairs == kHalfPairs) {
-                float m[8];
-                unpack<__nv_bfloat16>(y[n], m);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = second ? turn(m[e], v[e], c[e], sn[e]).y : turn(v[e], m[e], c[e], sn[e]).x;
-            } else {
-                const __nv_bfloat16* src = source(r);
+        const bool live = ok && n < rows;
+        float v0[8], v1[8];
+        unpack<__nv_bfloat16>(x[n][0], v0);
+        unpack<__nv_bfloat16>(x[n][1], v1);
+        if (live && rope) {
+            if constexpr (kPairs == kHalfPairs) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int d = d0 + e;
+                    const float2 z = turn(v0[e], v1[e], c[e], sn[e]);
+                    v0[e] = z.x;
+                    v1[e] = z.y;
+                }
+            } else if constexpr (kPairs == kLanePairs) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 z0 = turn(v0[e], v0[e + 1], c[e / 2], sn[e / 2]);
+                    const float2 z1 = turn(v1[e], v1[e + 1], c[4 + e / 2], sn[4 + e / 2]);
+                    v0[e] = z0.x;
+                    v0[e + 1] = z0.y;
+                    v1[e] = z1.x;
+                    v1[e + 1] = z1.y;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int d = 8 * c0 + e;
                     if (d >= a.rotary) continue;
                     const bool b = a.interleaved ? d & 1 : d >= half;
-                    const float m = __bfloat162float(src[a.interleaved ? d ^ 1 : b ? d - half : d + half]);
-                    v[e] = b ? turn(m, v[e], c[e], sn[e]).y : turn(v[e], m, c[e], sn[e]).x;
+                    const float m = __bfloat162float(src[n * D + (a.interleaved ? d ^ 1 : b ? d - half : d + half)]);
+                    float& v = e < 8 ? v0[e] : v1[e - 8];
+                    v = b ? turn(m, v, c[e], sn[e]).y : turn(v, m, c[e], sn[e]).x;
                 }
             }
         }
-        __syncwarp();  // q in place: the row's lanes have read their pairs
-        if (live && r < hq) {
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) + i * a.q_out_stride + static_cast<size_t>(r) * D +
-                                      d0) = pack<__nv_bfloat16>(v);
+        if constexpr (kPairs == kAnyPairs) __syncwarp();  // q in place: the row's lanes have read their partners
+        if (live && is_q) {
+            *reinterpret_cast<uint4*>(q_out + n * D + 8 * c0) = pack<__nv_bfloat16>(v0);
+            *reinterpret_cast<uint4*>(q_out + n * D + 8 * c1) = pack<__nv_bfloat16>(v1);
         }
-        // a warp's rows may be of different kinds: the shuffles below are for all
-        // of them, the stores for K and V rows
-        const bool kv = live && r >= hq;
-        if (__any_sync(0xFFFFFFFFu, kv)) {
-            const bool is_k = r < turned;
-            const int h = is_k ? r - hq : r - turned;
-            uint8_t* rec = nullptr;
-            float g = 1.f;
-            if (kv) {
-                rec = static_cast<uint8_t*>(is_k ? a.k_pool : a.v_pool) + (static_cast<size_t>(blk) * a.hkv + h) * R::kBytes;
-                if constexpr (kFp4) g = (is_k ? a.k_scale : a.v_scale)[h];
-            }
-            store_row<D, kFp4>(rec, row, lane, v, g, kv);
-        }
+        // a warp's rows may be of different kinds: the shuffles are for all of them, the
+        // stores for K and V rows
+        const bool kv = stored && n < rows;
+        if (__any_sync(0xFFFFFFFFu, kv))
+            store_row<D, kFp4>(rec + n * R::kBytes, p % kBlockSize, lane, c0, c1, split, v0, v1, g[n], kv);
     }
+    if (a.defer_wait && blockIdx.x == 0) pdl_wait();  // the grid ends after the one before it
 }
 
 // ----------------------------------------------------------------- read --
@@ -423,17 +466,20 @@ __device__ __forceinline__ void widen_row(const RowPart<D, kFp4>& p, float g, fl
 
 // D/8 lanes per (token, head), K and V of it in one thread.
 template <int D, bool kFp4>
-__global__ void __launch_bounds__(256) quant_read_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(256) quant_read_kernel(const __grid_constant__ QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     constexpr int kLanes = D / 8;
     const int lane = threadIdx.x % kLanes;
     const long long group = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
-    const long long i = group / a.hkv;
-    const int h = static_cast<int>(group % a.hkv);
+    // groups past 32 bits divide as 64-bit numbers
+    const long long i = group <= 0xFFFFFFFFLL ? static_cast<unsigned>(group) / static_cast<unsigned>(a.hkv) : group / a.hkv;
+    const int h = static_cast<int>(group - i * a.hkv);
     if (i >= a.num_tokens) return;
-    int blk, row;
-    if (!quant_slot(a, a.token_to_seq[i], a.positions[i], lane == 0 && h == 0, &blk, &row)) return;
+    const int s = a.token_to_seq[i], p = a.positions[i], row = p % kBlockSize;
+    int blk;
+    const bool report = lane == 0 && h == 0;
+    if (!quant_token(a, s, p, report) || !quant_block(a, s, p, report, &blk)) return;
     const size_t at = (static_cast<size_t>(blk) * a.hkv + h) * QuantRecord<D, kFp4>::kBytes;
     RowPart<D, kFp4> part[2];
 #pragma unroll
@@ -460,7 +506,7 @@ __global__ void __launch_bounds__(256) quant_read_kernel(QuantArgs a) {
 // A CTA per (pair, kHeads heads): thread (row, lane) widens 8 dims of each of
 // their records, K and V.
 template <int D, bool kFp4, int kHeads>
-__global__ void __launch_bounds__(2 * D) quant_load_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(2 * D) quant_load_kernel(const __grid_constant__ QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     constexpr int kLanes = D / 8;
@@ -502,6 +548,8 @@ cudaError_t grid_of(long long threads, dim3* grid) {
     return cudaSuccess;
 }
 
+constexpr int kBusyRows = 1;
+constexpr long long kSplitThreads = 3 << 16;
 constexpr long long kBusyThreads = 152LL * 512;  // 16 warps an SM: enough to give a thread more rows
 
 template <template <int, bool> class F>
@@ -513,22 +561,52 @@ cudaError_t by_format(const QuantArgs& a) {
 template <int D, bool kFp4>
 struct AppendLaunch {
     template <int kRows, int kPairs>
-    static cudaError_t rows(const QuantArgs& a, int rows) {
-        const int slots = (rows + kRows - 1) / kRows;
-        dim3 grid;
-        const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * slots * (D / 8), &grid);
-        return e != cudaSuccess ? e
-                                : launch_pdl(quant_append_kernel<D, kFp4, kRows, kPairs>, grid, dim3(256), 0, a.stream, a, slots);
+    static cudaError_t rows(const QuantArgs& a) {
+        constexpr int kPerBlock = 256 / (D / 16);
+        const unsigned q_slots = a.q ? (a.hq + kRows - 1) / kRows : 0, kv_slots = (a.hkv + kRows - 1) / kRows;
+        const long long slots = q_slots + 2LL * kv_slots;
+        const long long most = (0xFFFFFFFFLL - kPerBlock) / slots;  // group indexes are 32 bits wide
+        for (long long i = 0; i < a.num_tokens; i += most) {
+            const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
+            const cudaError_t e = launch_pdl(quant_append_kernel<D, kFp4, kRows, kPairs>,
+                                             dim3(static_cast<unsigned>((n * slots + kPerBlock - 1) / kPerBlock)), dim3(256), 0,
+                                             a.stream, a, q_slots, kv_slots, static_cast<int>(i));
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
     }
     template <int kPairs>
     static cudaError_t pairs(const QuantArgs& a) {
-        const int n = 2 * a.hkv + (a.q ? a.hq : 0);
-        return static_cast<long long>(a.num_tokens) * n * (D / 8) >= 4 * kBusyThreads ? rows<2, kPairs>(a, n) : rows<1, kPairs>(a, n);
+        const long long n = static_cast<long long>(a.num_tokens) * (2 * a.hkv + (a.q ? a.hq : 0)) * (D / 16);
+        if (!a.q || n < kSplitThreads) return rows<1, kPairs>(a);
+        // many tokens: q through the rotation's kernel, whose threads take four rows, K and V
+        // beside it (4096 tokens of 32 + 8 heads: 27.6 us in one launch)
+        RotateArgs r{};
+        r.q = RotateRows{a.q, a.q_out, a.q_stride, D, a.q_out_stride, D, a.hq};
+        r.cos_sin = a.cos_sin;
+        r.positions = a.positions;
+        r.num_tokens = a.num_tokens;
+        r.d = D;
+        r.rotary = a.rotary;
+        r.interleaved = a.interleaved;
+        r.inverse = a.inverse;
+        r.max_pos = a.max_pos;
+        r.dtype = PKV_BF16;
+        r.token_to_seq = a.token_to_seq;
+        r.num_seqs = a.num_seqs;
+        r.mbps = a.mbps;
+        r.ring = a.ring;
+        const cudaError_t e = launch_rope_rotate(r, a.stream);
+        if (e != cudaSuccess) return e;
+        QuantArgs kv = a;
+        kv.q = nullptr;
+        kv.defer_wait = 1;
+        return rows<kBusyRows, kPairs>(kv);
     }
     static cudaError_t go(const QuantArgs& a) {
         if (a.cos_sin && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0) {
-            if (!a.interleaved && a.rotary % 16 == 0) return pairs<kHalfPairs>(a);
-            if (a.interleaved && a.rotary % 8 == 0) return pairs<kLanePairs>(a);
+            if (!a.interleaved && a.rotary % 32 == 0) return pairs<kHalfPairs>(a);
+            if (a.interleaved && a.rotary % 16 == 0) return pairs<kLanePairs>(a);
         }
         return pairs<kAnyPairs>(a);
     }
@@ -564,13 +642,14 @@ struct RotateLaunch {
     }
     template <bool kHalf, int kRows>
     static cudaError_t vectors(const RotateArgs& a, int count, cudaStream_t stream) {
-        const int slots = (a.q.num_heads + a.k.num_heads + kRows - 1) / kRows;
+        const unsigned q_slots = (a.q.num_heads + kRows - 1) / kRows, slots = q_slots + (a.k.num_heads + kRows - 1) / kRows;
         const long long per_token = static_cast<long long>(count) * slots;
         const long long most = (0xFFFFFFFFLL - 256) / per_token;  // thread indexes are 32 bits wide
         for (long long i = 0; i < a.num_tokens; i += most) {
             const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
             const cudaError_t e = launch_pdl(rope_vector_kernel<T, kHalf, kRows>, dim3(static_cast<unsigned>((n * per_token + 255) / 256)),
-                                             dim3(256), 0, stream, a, count, slots, static_cast<int>(i));
+                                             dim3(256), 0, stream, a, static_cast<unsigned>(count), q_slots, slots,
+                                             static_cast<int>(i));
             if (e != cudaSuccess) return e;
         }
         return cudaSuccess;
@@ -583,7 +662,7 @@ struct RotateLaunch {
         const bool in_place = a.q.in == a.q.out && (a.k.num_heads == 0 || a.k.in == a.k.out);
         const int count = (kHalf ? a.rotary / 2 : a.rotary) / N + (in_place ? 0 : (a.d - a.rotary) / N);
         const long long one = static_cast<long long>(a.num_tokens) * (a.q.num_heads + a.k.num_heads) * count;
-        if (one >= 4 * kBusyThreads) return vectors<kHalf, kHalf ? 4 : 8>(a, count, stream);
+        if (one >= 4 * kBusyThreads) return vectors<kHalf, 4>(a, count, stream);
         return vectors<kHalf, 1>(a, count, stream);
     }
     static cudaError_t go(const RotateArgs& a, cudaStream_t stream) {

@@ -116,6 +116,51 @@ def test_append_is_the_definition_bit_for_bit(fmt, hq, hkv, d, r, layout, packed
 
 
 @pytest.mark.parametrize("fmt", ["int8", "fp4"])
+def test_append_rounds_quotients_at_the_borders(fmt):
+    """K rows of chosen fp32 values -- k = 1 rotated by (cos, sin) = (value, 0) -- that
+    sit on, and a few steps beside, the borders between codes, under scales of random
+    significands and exponents: every quotient must round as the division does."""
+    rng = np.random.default_rng(12)
+    d, n = 128, 512
+    half = d // 2
+    mids = (np.arange(127) + 0.5) if fmt == "int8" else np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    cs = np.zeros((n, half, 2), np.float32)
+    g = np.ones(1, np.float32) * np.float32(1.2345e-3)
+    for i in range(n):
+        if i % 2 and fmt == "fp4":  # all-ones and near-power-of-two significands too
+            g_amax = np.float32(2.0 ** rng.integers(-6, 6) * (2 - 2.0 ** -23 * rng.integers(0, 4)))
+        else:
+            g_amax = np.float32(2.0 ** rng.integers(-6, 6) * (1 + rng.random()))
+        row = np.empty(half, np.float32)
+        for b in range(0, half, 16):
+            # the scale that this amax gives, then values at its borders
+            _, sc = Q.quantise(fmt, np.concatenate(([g_amax], np.zeros(half - 1))).astype(np.float32), g[0])
+            t = (np.frombuffer(sc.tobytes(), np.float32)[0] if fmt == "int8"
+                 else np.float32(Q.e4m3_values(sc[:1])[0] * g[0]))
+            v = (rng.choice(mids, 16).astype(np.float64) * np.float64(t)).astype(np.float32)
+            v = (v.view(np.int32) + rng.integers(-2, 3, 16).astype(np.int32)).view(np.float32)
+            v = np.clip(v * rng.choice([-1, 1], 16), -g_amax, g_amax).astype(np.float32)
+            v[0] = g_amax
+            row[b:b + 16] = v
+        cs[i, :, 0] = row
+    k = np.zeros((n, 1, d), np.float32)
+    k[..., :half] = 1.0
+    k[:, :, half:][..., ::7] = -0.0
+    v = Q.bf16(rng.standard_normal((n, 1, d)))
+    tables = np.arange(n // 16, dtype=np.int32)[None]
+    tts, pos = np.zeros(n, np.int32), np.arange(n, dtype=np.int32)
+    scale = g if fmt == "fp4" else None
+    pools = [np.zeros((n // 16, 1, Q.record_bytes(fmt, d)), np.uint8) for _ in range(2)]
+    gp = [dev(p) for p in pools]
+    pkv.pkv_quant_append(desc_of(fmt, 1, 1, d, n // 16, n // 16), gp[0], gp[1], dev(tables), dev(tts), dev(pos),
+                         bf(k), bf(v), rope=pkv.make_rope(dev(cs)), q=bf(k), q_out=bf(k), k_scale=dev(scale),
+                         v_scale=dev(scale))
+    ref = expected_append(fmt, d, pools, tables, 0, tts, pos, k, v, (scale, scale), cs, "half")
+    for which in (0, 1):
+        assert np.array_equal(gp[which].cpu().numpy(), ref[which])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
 def test_append_of_values_that_are_not_finite_and_of_extremes(fmt):
     d, nb = 64, 2
     rows = np.zeros((12, d), np.float32)
