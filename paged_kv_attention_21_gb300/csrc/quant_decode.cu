@@ -270,8 +270,10 @@ __device__ __forceinline__ void accumulate(float (&o)[NT][D / 16][4], const uint
 }
 
 // NB consecutive blocks, K and V records of block i at stage + i * kBlock: tok_base is
-// the first one's first position, keys in [lo, hi) take part.
-template <int D, bool kFp4, int NT>
+// the first one's first position, keys in [lo, hi) take part.  kEdge: some of the blocks'
+// tokens may lie outside (masking them as they come cost 24 instructions a block in the
+// passes that have none).
+template <int D, bool kFp4, int NT, bool kEdge>
 __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2], const uint8_t* stage,
                                        int lane, int tok_base, int lo, int hi, float sl) {
     using C = Cfg<D, kFp4, NT>;
@@ -280,7 +282,6 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
     const int g = lane >> 2, t = lane & 3;
     const int row = slot_row<RB>(g);                                    // S^T's rows: row, row + 8
     const int ta = slot_row<RB>(2 * t), tb = slot_row<RB>(2 * t + 1);  // O^T's token slots: rows ta, tb (+ 8)
-    const bool edge = tok_base < lo || tok_base + NB * kBlockSize > hi;
     const uint32_t cnt = static_cast<uint32_t>(hi - lo);
     auto visible = [&](int b, int r) { return static_cast<uint32_t>(tok_base - lo + b * kBlockSize + r) < cnt; };
 
@@ -300,7 +301,7 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
             uint32_t c[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = p[((i & 1 ? tb : ta) + (i & 2 ? 8 : 0)) * R::kScaleBytes];
-            if (edge) {
+            if constexpr (kEdge) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (!visible(b, (i & 1 ? tb : ta) + (i & 2 ? 8 : 0))) c[i] = 0;
@@ -314,7 +315,7 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
                 vs[b][h] = *reinterpret_cast<const float*>(vt + R::kScales + (row + 8 * h) * 4);
             }
         }
-        if (edge) {
+        if constexpr (kEdge) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (!visible(b, row + 8 * h)) {
@@ -562,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     uint8_t* ring = smem + warp * C::kStages * C::kStage;
     const uint32_t to = smem_u32(ring) + lane * 16;
     const uint32_t to_tail = to + (lane < C::kTail ? 0 : C::kTile - C::kTail * 16) + C::kFull * 512;
+    int lb = b0 + C::NB * warp;  // the next pass's first block
     auto load = [&](int pass, uint32_t stage) {
         const int k0 = pass * C::NB;
         if ((k0 & 31) == 0) {
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
 #pragma unroll
         for (int b = 0; b < C::NB; ++b) {
             const uint32_t id = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id_cur, (k0 + b) & 31));
-            if (logical(k0 + b) < b1) {
+            if (lb + b < b1) {
                 const uint8_t* ks = kp + static_cast<uint64_t>(block_bytes) * id;
                 const uint8_t* vs = vp + static_cast<uint64_t>(block_bytes) * id;
                 const uint32_t dst = stage + b * C::kBlock;
@@ -583,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
                 if (lane < 2 * C::kTail) copy16(to_tail + dst, tp + static_cast<uint64_t>(block_bytes) * id);
             }
         }
+        lb += kWarps * C::NB;
         copy_commit();
     };
 #pragma unroll
@@ -630,7 +633,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
         copy_wait<C::kStages - 2>();  // this lane's copies of pass i have landed
         __syncwarp();                 // and every lane's
         load(i + C::kStages - 1, next);
-        attend<D, kFp4, NT>(st, qb, ring + here, lane, tok, lo, hi, sl);
+        if (tok >= lo && tok + C::NB * kBlockSize <= hi)
+            attend<D, kFp4, NT, false>(st, qb, ring + here, lane, tok, lo, hi, sl);
+        else
+            attend<D, kFp4, NT, true>(st, qb, ring + here, lane, tok, lo, hi, sl);
         tok += kWarps * C::NB * kBlockSize;
         next = here;
         here = here + C::kStage == C::kStages * C::kStage ? 0 : here + C::kStage;
