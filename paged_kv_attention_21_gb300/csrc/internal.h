@@ -236,9 +236,6 @@ struct QuantArgs {
     int64_t num_blocks, dst_num_blocks;
     int32_t num_tokens;  // load: pairs of blocks
     int32_t num_seqs, hq, hkv, d, fp4, mbps, ring, rotary, interleaved, inverse, max_pos, out_f32;
-    // append: the launch before it in the stream shares nothing with it and waited for
-    // what came earlier, so this one waits for it only before it ends
-    int32_t defer_wait;
     uint32_t* err;
     cudaStream_t stream;
 };

@@ -73,13 +73,10 @@ __device__ __forceinline__ bool token_in_table(int s, int p, int num_seqs, int m
 // anything waits, the position and table entry among them).
 
 template <typename T, bool kHalf, int kRows>
-__global__ void __launch_bounds__(256) rope_vector_kernel(const __grid_constant__ RotateArgs a, unsigned vectors,
-                                                          unsigned q_slots, unsigned slots, int first_token) {
-    pdl_wait();
-    pdl_launch_dependents();
+__device__ __forceinline__ void rotate_vectors(const RotateArgs& a, unsigned idx, unsigned vectors, unsigned q_slots,
+                                               unsigned slots, int first_token) {
     constexpr int N = 16 / sizeof(T);
     constexpr int kPairs = kHalf ? N : N / 2;
-    const unsigned idx = blockIdx.x * 256u + threadIdx.x;
     const unsigned rest = idx / vectors, v = idx - rest * vectors;
     const unsigned token = rest / slots;
     unsigned slot = rest - token * slots;
@@ -153,6 +150,14 @@ __global__ void __launch_bounds__(256) rope_vector_kernel(const __grid_constant_
             }
             *reinterpret_cast<uint4*>(out + r * out_head) = pack<T>(f);
         }
+}
+
+template <typename T, bool kHalf, int kRows>
+__global__ void __launch_bounds__(256) rope_vector_kernel(const __grid_constant__ RotateArgs a, unsigned vectors,
+                                                          unsigned q_slots, unsigned slots, int first_token) {
+    pdl_wait();
+    pdl_launch_dependents();
+    rotate_vectors<T, kHalf, kRows>(a, blockIdx.x * 256u + threadIdx.x, vectors, q_slots, slots, first_token);
 }
 
 // Rows that no 16-byte vector fits (their address, stride, rotary or head dims):
@@ -280,16 +285,12 @@ __device__ __forceinline__ void store_row(uint8_t* rec, int row, int lane, int c
 enum Pairs { kAnyPairs, kHalfPairs, kLanePairs };
 
 template <int D, bool kFp4, int kRows, int kPairs>
-__global__ void __launch_bounds__(256) quant_append_kernel(const __grid_constant__ QuantArgs a, unsigned q_slots,
-                                                           unsigned kv_slots, int first_token) {
-    if (!a.defer_wait) {
-        pdl_wait();
-        pdl_launch_dependents();
-    }
+__device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, unsigned q_slots, unsigned kv_slots,
+                                            int first_token) {
     using R = QuantRecord<D, kFp4>;
     constexpr int kLanes = D / 16;
     const int lane = threadIdx.x % kLanes;
-    const unsigned group = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    const unsigned group = block * (256 / kLanes) + threadIdx.x / kLanes;
     const unsigned slots = q_slots + 2 * kv_slots;
     const unsigned token = group / slots;
     unsigned slot = group - token * slots;
@@ -417,7 +418,31 @@ __global__ void __launch_bounds__(256) quant_append_kernel(const __grid_constant
         if (__any_sync(0xFFFFFFFFu, kv))
             store_row<D, kFp4>(rec + n * R::kBytes, p % kBlockSize, lane, c0, c1, split, v0, v1, g[n], kv);
     }
-    if (a.defer_wait && blockIdx.x == 0) pdl_wait();  // the grid ends after the one before it
+}
+
+template <int D, bool kFp4, int kRows, int kPairs>
+__global__ void __launch_bounds__(256) quant_append_kernel(const __grid_constant__ QuantArgs a, unsigned q_slots,
+                                                           unsigned kv_slots, int first_token) {
+    pdl_wait();  // dependents start as its CTAs leave: triggered here they took the slots of its last waves
+    append_rows<D, kFp4, kRows, kPairs>(a, blockIdx.x, q_slots, kv_slots, first_token);
+}
+
+// Many tokens: blocks that rotate q as the rotation's kernel does (four heads a thread,
+// bound by HBM) evenly among blocks that quantise K and V (bound by instruction issue),
+// so that each SM runs both.
+template <int D, bool kFp4, int kPairs>
+__global__ void __launch_bounds__(256, 4) quant_append_mixed_kernel(const __grid_constant__ QuantArgs a,
+                                                                    const __grid_constant__ RotateArgs r, unsigned vectors,
+                                                                    unsigned q_slots, unsigned q_blocks, unsigned kv_slots,
+                                                                    unsigned blocks) {
+    pdl_wait();
+    // of the first b blocks, b q_blocks / blocks rotate
+    const unsigned before = static_cast<unsigned>(static_cast<uint64_t>(blockIdx.x) * q_blocks / blocks);
+    const unsigned after = static_cast<unsigned>((static_cast<uint64_t>(blockIdx.x) + 1) * q_blocks / blocks);
+    if (after > before)
+        rotate_vectors<__nv_bfloat16, kPairs == kHalfPairs, 4>(r, before * 256u + threadIdx.x, vectors, q_slots, q_slots, 0);
+    else
+        append_rows<D, kFp4, 1, kPairs>(a, blockIdx.x - before, 0, kv_slots, 0);
 }
 
 // ----------------------------------------------------------------- read --
@@ -468,7 +493,6 @@ __device__ __forceinline__ void widen_row(const RowPart<D, kFp4>& p, float g, fl
 template <int D, bool kFp4>
 __global__ void __launch_bounds__(256) quant_read_kernel(const __grid_constant__ QuantArgs a) {
     pdl_wait();
-    pdl_launch_dependents();
     constexpr int kLanes = D / 8;
     const int lane = threadIdx.x % kLanes;
     const long long group = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
@@ -508,7 +532,6 @@ __global__ void __launch_bounds__(256) quant_read_kernel(const __grid_constant__
 template <int D, bool kFp4, int kHeads>
 __global__ void __launch_bounds__(2 * D) quant_load_kernel(const __grid_constant__ QuantArgs a) {
     pdl_wait();
-    pdl_launch_dependents();
     constexpr int kLanes = D / 8;
     const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
     const int src = a.src_blocks[blockIdx.x], dst = a.dst_blocks[blockIdx.x];
@@ -548,8 +571,7 @@ cudaError_t grid_of(long long threads, dim3* grid) {
     return cudaSuccess;
 }
 
-constexpr int kBusyRows = 1;
-constexpr long long kSplitThreads = 3 << 16;
+constexpr long long kMixedThreads = 3 << 16;
 constexpr long long kBusyThreads = 152LL * 512;  // 16 warps an SM: enough to give a thread more rows
 
 template <template <int, bool> class F>
@@ -578,9 +600,15 @@ struct AppendLaunch {
     template <int kPairs>
     static cudaError_t pairs(const QuantArgs& a) {
         const long long n = static_cast<long long>(a.num_tokens) * (2 * a.hkv + (a.q ? a.hq : 0)) * (D / 16);
-        if (!a.q || n < kSplitThreads) return rows<1, kPairs>(a);
-        // many tokens: q through the rotation's kernel, whose threads take four rows, K and V
-        // beside it (4096 tokens of 32 + 8 heads: 27.6 us in one launch)
+        if constexpr (kPairs != kAnyPairs) {
+            // (4096 tokens of 32 + 8 heads took 27.6 us through the kernel above, 24.1 with q in
+            // a launch of its own; 256 tokens of 8 K and V heads 3.3 and 3.4)
+            if (a.q && n >= kMixedThreads && n < 0x7FFFFFFFLL) return mixed<kPairs>(a);
+        }
+        return rows<1, kPairs>(a);
+    }
+    template <int kPairs>
+    static cudaError_t mixed(const QuantArgs& a) {
         RotateArgs r{};
         r.q = RotateRows{a.q, a.q_out, a.q_stride, D, a.q_out_stride, D, a.hq};
         r.cos_sin = a.cos_sin;
@@ -596,12 +624,16 @@ struct AppendLaunch {
         r.num_seqs = a.num_seqs;
         r.mbps = a.mbps;
         r.ring = a.ring;
-        const cudaError_t e = launch_rope_rotate(r, a.stream);
-        if (e != cudaSuccess) return e;
+        constexpr int kPerBlock = 256 / (D / 16);
+        const unsigned vectors = static_cast<unsigned>((kPairs == kHalfPairs ? a.rotary / 2 : a.rotary) / 8 +
+                                                       (a.q == a.q_out ? 0 : (D - a.rotary) / 8));
+        const unsigned q_slots = (a.hq + 3) / 4, kv_slots = a.hkv, tokens = static_cast<unsigned>(a.num_tokens);
+        const unsigned q_blocks = static_cast<unsigned>((static_cast<uint64_t>(tokens) * q_slots * vectors + 255) / 256);
+        const unsigned kv_blocks = static_cast<unsigned>((static_cast<uint64_t>(tokens) * 2 * kv_slots + kPerBlock - 1) / kPerBlock);
         QuantArgs kv = a;
         kv.q = nullptr;
-        kv.defer_wait = 1;
-        return rows<kBusyRows, kPairs>(kv);
+        return launch_pdl(quant_append_mixed_kernel<D, kFp4, kPairs>, dim3(q_blocks + kv_blocks), dim3(256), 0, a.stream, kv, r,
+                          vectors, q_slots, q_blocks, kv_slots, q_blocks + kv_blocks);
     }
     static cudaError_t go(const QuantArgs& a) {
         if (a.cos_sin && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0) {
