@@ -393,31 +393,30 @@ def pkv_cascade_decode(desc, q, k_cache, v_cache, group_indptr, group_indptr_hos
 
 # ------------------------- rotary positions and the quantised pools --
 #
-# These calls check their tensors (type, device, layout) before the library
-# checks their sizes: a pool of the wrong kind is a ValueError, not a misread.
+# These calls check their tensors (type, device, shape, layout) before the library
+# checks its arguments: a pool of the wrong kind is a ValueError, not a misread.  The
+# checks and the call run in the extension module _marshal (csrc/marshal.cpp).
 
-def _refuse(name, t, dtypes, device, shape, dense):
-    """Raise for the first of _at's checks that t fails."""
-    if t.dtype not in dtypes:
-        raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
-    if not t.is_cuda or t.get_device() != device:
-        raise ValueError("%s: on %s, expected the current CUDA device" % (name, t.device))
-    if t.shape != shape:
-        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if dense and not t.is_contiguous():
-        raise ValueError("%s: tensor arguments must be contiguous" % name)
-    raise AssertionError(name)
+_marshal = None
 
 
-def _at(name, t, dtype, device, shape, dense=True):
-    """t's address (None for None), after checking that it is a `dtype` tensor
-    of `shape` on CUDA device `device`, contiguous unless told otherwise."""
-    if t is None:
-        return None
-    if (t.dtype is dtype and t.get_device() == device and t.shape == shape
-            and (not dense or t.is_contiguous())):
-        return t.data_ptr()
-    _refuse(name, t, (dtype,), device, shape, dense)
+def _checked():
+    """The extension module, loaded beside the library on first use."""
+    global _marshal
+    if _marshal is None:
+        with _lock:
+            if _marshal is None:
+                import importlib.util
+                import torch  # noqa: F401 -- the module links torch's libraries
+                if not os.path.exists(_build.MARSHAL_PATH):
+                    raise RuntimeError("_marshal.so is not built (%s); run __graft_entry__.build()"
+                                       % _build.MARSHAL_PATH)
+                spec = importlib.util.spec_from_file_location("_marshal", _build.MARSHAL_PATH)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.init(_build.LIB_PATH)
+                _marshal = module
+    return _marshal
 
 
 _torch = None   # the module, once a call has needed it
@@ -425,20 +424,18 @@ _have_cuda = False
 
 
 def _here(stream):
-    """(torch, the current device's index, the launch stream's address); without
-    a CUDA device an index that no tensor has."""
+    """(the current device's index, the launch stream's address); without a CUDA
+    device an index that no tensor has."""
     global _torch, _have_cuda
     if not _have_cuda:
         import torch
         _torch, _have_cuda = torch, torch.cuda.is_available()
         if not _have_cuda:
-            return torch, -2, None
+            return -2, None
     device = _torch.cuda.current_device()
     if stream is None:
-        stream = _torch._C._cuda_getCurrentRawStream(device)  # current_stream() builds an object: 1 us
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    return _torch, device, stream
+        return device, _torch._C._cuda_getCurrentRawStream(device)  # current_stream() builds an object: 1 us
+    return device, stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def make_rope(cos_sin, rotary_dim=None, layout="half", inverse=False) -> Rope:
@@ -455,9 +452,13 @@ def make_rope(cos_sin, rotary_dim=None, layout="half", inverse=False) -> Rope:
         rotary_dim = 2 * cos_sin.shape[1]
     if rotary_dim != 2 * cos_sin.shape[1]:
         raise ValueError("rotary_dim %d, but the table has %d pairs" % (rotary_dim, cos_sin.shape[1]))
-    torch, device, _ = _here(None)
-    r = Rope(_at("cos_sin", cos_sin, torch.float32, device, cos_sin.shape), int(rotary_dim),
-             layouts[layout], int(cos_sin.shape[0]), ROPE_INVERSE if inverse else 0)
+    device, _ = _here(None)
+    if str(cos_sin.dtype) != "torch.float32" or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin: dtype %s, expected contiguous torch.float32" % cos_sin.dtype)
+    if cos_sin.get_device() != device:
+        raise ValueError("cos_sin: on %s, expected the current CUDA device" % cos_sin.device)
+    r = Rope(cos_sin.data_ptr(), int(rotary_dim), layouts[layout], int(cos_sin.shape[0]),
+             ROPE_INVERSE if inverse else 0)
     r.table = cos_sin
     return r
 
@@ -482,43 +483,13 @@ def pkv_rope_scaled_table(theta, rotary_dim, max_pos, kind="none", factor=1.0, o
     return out
 
 
-def _rope_rows(name, x, out, dtype, device, num_tokens):
-    if x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
-        raise ValueError("%s: expected [tokens][heads][head_dim] with contiguous dims" % name)
-    shape = x.shape
-    if shape[0] != num_tokens:
-        raise ValueError("%s: %d tokens, but %d positions" % (name, shape[0], num_tokens))
-    at = _at(name, x, dtype, device, shape, False)
-    st = x.stride()
-    if out is None:
-        return Rows(at, at, st[0], st[1], st[0], st[1], shape[1], 0)
-    to = _at(name + "_out", out, dtype, device, shape, False)
-    so = out.stride()
-    if shape[2] > 1 and so[2] != 1:
-        raise ValueError("%s_out: expected contiguous dims" % name)
-    return Rows(at, to, st[0], st[1], so[0], so[1], shape[1], 0)
-
-
 def pkv_rope_rotate(rope, positions, q, q_out=None, k=None, k_out=None, stream=None):
     """Rotate [tokens][heads][head_dim] rows (bf16, f16 or f32; any token and
     head strides) of q and k at int32 positions; without an out, in place.
     With make_rope(..., inverse=True) it is the rotation's transpose: the
     gradient of q from the gradient of its rotated rows."""
-    torch, device, stream = _here(stream)
-    dtype = q.dtype
-    code = 0 if dtype is torch.bfloat16 else 1 if dtype is torch.float16 else 2
-    if code == 2 and dtype is not torch.float32:
-        raise ValueError("q: dtype %s, expected bfloat16, float16 or float32" % dtype)
-    n = positions.shape[0]
-    rows = _rope_rows("q", q, q_out, dtype, device, n)
-    krows = None
-    if k is not None:
-        if k.shape[-1] != q.shape[-1]:
-            raise ValueError("k: expected q's head_dim")
-        krows = ctypes.byref(_rope_rows("k", k, k_out, dtype, device, n))
-    _check(load_library().pkv_rope_rotate(
-        ctypes.byref(rope), code, _at("positions", positions, torch.int32, device, (n,)), n,
-        q.shape[2], ctypes.byref(rows), krows, stream))
+    device, stream = _here(stream)
+    _check(_checked().rope_rotate(rope, positions, q, q_out, k, k_out, device, stream))
 
 
 def pkv_quant_cache_bytes(desc: CacheDesc) -> int:
@@ -533,90 +504,32 @@ def pkv_quant_record_bytes(desc: CacheDesc) -> int:
     return 16 * d + 64 if desc.kv_dtype == KV_INT8 else 9 * d
 
 
-def _quant_pools(desc, device, torch, k_pool, v_pool, k_scale, v_scale):
-    hkv, dim, u8 = desc.num_kv_heads, desc.head_dim, torch.uint8
-    shape = (desc.num_blocks, hkv, 16 * dim + 64 if desc.kv_dtype == KV_INT8 else 9 * dim)
-    if k_scale is None and v_scale is None:
-        return _at("k_pool", k_pool, u8, device, shape), _at("v_pool", v_pool, u8, device, shape), None, None
-    f32 = torch.float32
-    return (_at("k_pool", k_pool, u8, device, shape), _at("v_pool", v_pool, u8, device, shape),
-            _at("k_scale", k_scale, f32, device, (hkv,)), _at("v_scale", v_scale, f32, device, (hkv,)))
-
-
-def _token_rows(name, x, dtype, device, shape):
-    """[tokens][heads][dim] rows whose heads are contiguous: (address, token stride)."""
-    at = _at(name, x, dtype, device, shape, False)
-    n, heads, dim = shape
-    st = x.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != dim):
-        raise ValueError("%s: a token's heads must be contiguous" % name)
-    return at, (st[0] if n > 1 else heads * dim)
-
-
 def pkv_quant_append(desc, k_pool, v_pool, block_tables, token_to_seq, positions, k_new, v_new,
                      q=None, q_out=None, rope=None, k_scale=None, v_scale=None, stream=None):
     """Quantise the new tokens' K (rotated) and V into their slots, and rotate q
     into q_out (None: in place).  k_new, v_new and q may be views into one packed
     QKV buffer.  token_to_seq < 0 marks a padding token."""
-    torch, device, stream = _here(stream)
-    i32, bf16 = torch.int32, torch.bfloat16
-    n, seqs, dim = positions.shape[0], block_tables.shape[0], desc.head_dim
-    kp, vp, ks, vs = _quant_pools(desc, device, torch, k_pool, v_pool, k_scale, v_scale)
-    shape = (n, desc.num_kv_heads, dim)
-    k_at, k_stride = _token_rows("k_new", k_new, bf16, device, shape)
-    v_at, v_stride = _token_rows("v_new", v_new, bf16, device, shape)
-    if k_stride != v_stride:
-        raise ValueError("k_new and v_new: token strides %d and %d differ" % (k_stride, v_stride))
-    q_at = qo_at = None
-    q_stride = qo_stride = 0
-    if q is not None:
-        shape = (n, desc.num_q_heads, dim)
-        qo_at, qo_stride = q_at, q_stride = _token_rows("q", q, bf16, device, shape)
-        if q_out is not None:
-            qo_at, qo_stride = _token_rows("q_out", q_out, bf16, device, shape)
-    _check(load_library().pkv_quant_append(
-        ctypes.byref(desc), None if rope is None else ctypes.byref(rope), kp, vp, ks, vs,
-        _at("block_tables", block_tables, i32, device, (seqs, desc.max_blocks_per_seq)), seqs,
-        _at("token_to_seq", token_to_seq, i32, device, (n,)),
-        _at("positions", positions, i32, device, (n,)), n, k_at, v_at, k_stride, q_at, qo_at, q_stride,
-        qo_stride, stream))
+    device, stream = _here(stream)
+    _check(_checked().quant_append(desc, k_pool, v_pool, k_scale, v_scale, device, stream, rope,
+                                   block_tables, token_to_seq, positions, k_new, v_new, q, q_out))
 
 
 def pkv_quant_read(desc, k_pool, v_pool, block_tables, token_to_seq, positions, k_out=None,
                    v_out=None, k_scale=None, v_scale=None, stream=None):
     """Read the rows at (token_to_seq, positions) back as bf16 or fp32
     [tokens][Hkv][D]; either output may be None."""
-    torch, device, stream = _here(stream)
-    i32 = torch.int32
-    n, seqs = positions.shape[0], block_tables.shape[0]
-    kp, vp, ks, vs = _quant_pools(desc, device, torch, k_pool, v_pool, k_scale, v_scale)
-    if k_out is None and v_out is None:
-        raise ValueError("k_out or v_out is needed")
-    dtype = (v_out if k_out is None else k_out).dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
-        raise ValueError("outputs: dtype %s, expected bfloat16 or float32" % dtype)
-    shape = (n, desc.num_kv_heads, desc.head_dim)
-    _check(load_library().pkv_quant_read(
-        ctypes.byref(desc), kp, vp, ks, vs,
-        _at("block_tables", block_tables, i32, device, (seqs, desc.max_blocks_per_seq)), seqs,
-        _at("token_to_seq", token_to_seq, i32, device, (n,)),
-        _at("positions", positions, i32, device, (n,)), n, 2 if dtype is torch.float32 else 0,
-        _at("k_out", k_out, dtype, device, shape), _at("v_out", v_out, dtype, device, shape), stream))
+    device, stream = _here(stream)
+    _check(_checked().quant_read(desc, k_pool, v_pool, k_scale, v_scale, device, stream, block_tables,
+                                 token_to_seq, positions, k_out, v_out))
 
 
 def pkv_quant_load_blocks(desc, k_pool, v_pool, src_blocks, dst_blocks, k_cache, v_cache,
                           k_scale=None, v_scale=None, stream=None):
     """Block dst_blocks[i] of the bf16 pools [blocks][Hkv][16][D] receives the
     values of block src_blocks[i] of the quantised pools."""
-    torch, device, stream = _here(stream)
-    n, i32 = src_blocks.shape[0], torch.int32
-    kp, vp, ks, vs = _quant_pools(desc, device, torch, k_pool, v_pool, k_scale, v_scale)
-    shape = (k_cache.shape[0], desc.num_kv_heads, desc.block_size, desc.head_dim)
-    _check(load_library().pkv_quant_load_blocks(
-        ctypes.byref(desc), kp, vp, ks, vs, _at("src_blocks", src_blocks, i32, device, (n,)),
-        _at("dst_blocks", dst_blocks, i32, device, (n,)), n, shape[0],
-        _at("k_cache", k_cache, torch.bfloat16, device, shape),
-        _at("v_cache", v_cache, torch.bfloat16, device, shape), stream))
+    device, stream = _here(stream)
+    _check(_checked().quant_load_blocks(desc, k_pool, v_pool, k_scale, v_scale, device, stream,
+                                        src_blocks, dst_blocks, k_cache, v_cache))
 
 
 def pkv_quant_decode_workspace_size(desc, num_seqs, max_context_len, window=-1, chunk_blocks=0) -> int:
@@ -628,21 +541,10 @@ def pkv_quant_decode(desc, q, k_pool, v_pool, block_tables, context_lens, max_co
                      out, lse=None, workspace=None, window=-1, chunk_blocks=0, k_scale=None,
                      v_scale=None, sinks=None, stream=None):
     """Decode attention (one query token per sequence) over quantised pools."""
-    torch, device, stream = _here(stream)
-    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    n, hq = context_lens.shape[0], desc.num_q_heads
-    kp, vp, ks, vs = _quant_pools(desc, device, torch, k_pool, v_pool, k_scale, v_scale)
-    shape = (n, hq, desc.head_dim)
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        ws_bytes = workspace.numel()
-        ws = _at("workspace", workspace, torch.uint8, device, workspace.shape)
-    _check(load_library().pkv_quant_decode(
-        ctypes.byref(desc), _at("q", q, bf16, device, shape), kp, vp, ks, vs,
-        _at("block_tables", block_tables, i32, device, (n, desc.max_blocks_per_seq)),
-        _at("context_lens", context_lens, i32, device, (n,)), n, max_context_len, sm_scale, window,
-        _at("sinks", sinks, f32, device, (hq,)), chunk_blocks, _at("out", out, bf16, device, shape),
-        _at("lse", lse, f32, device, (n, hq)), ws, ws_bytes, stream))
+    device, stream = _here(stream)
+    _check(_checked().quant_decode(desc, k_pool, v_pool, k_scale, v_scale, device, stream, q,
+                                   block_tables, context_lens, max_context_len, sm_scale, window,
+                                   sinks, chunk_blocks, out, lse, workspace))
 
 
 def pkv_device_errors(reset: bool = True) -> int:

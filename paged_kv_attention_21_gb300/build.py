@@ -3,19 +3,24 @@
 Each .cu translation unit compiles in parallel to an object file, then nvcc
 links them into ``paged_kv_attention_21_gb300/_build/libpkv.so`` with the
 CUDA runtime linked statically (the tensor-map encoder is fetched from the
-driver at run time, so libcuda is not linked).
+driver at run time, so libcuda is not linked).  Beside them g++ compiles the
+binding's argument checks (``csrc/marshal.cpp``, against torch's headers) into
+``_build/_marshal.so``.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libpkv.so")
+MARSHAL_PATH = os.path.join(OUT_DIR, "_marshal.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,10 +43,26 @@ def _deps():
     return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "pkv.h")]
 
 
+def _compile_marshal():
+    """The binding's extension module; raises with the compiler's output."""
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    lib = os.path.join(torch_dir, "lib")
+    tmp = MARSHAL_PATH + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", tmp,
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on marshal.cpp:\n%s%s" % (r.stdout, r.stderr))
+    os.replace(tmp, MARSHAL_PATH)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
     return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
 
 
@@ -63,8 +84,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        marshal = ex.submit(_compile_marshal)
         objs = list(ex.map(compile_one, srcs))
+        marshal.result()
     tmp = LIB_PATH + ".tmp.%d" % os.getpid()
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
