@@ -1420,22 +1420,39 @@ pkv_status check_rows(const pkv_rows* r, const char* name, int64_t tokens, int64
     if (!r->in || !r->out) return fail(PKV_ERR_INVALID_ARG, "%s: null device pointer", name);
     if (!aligned(r->in, size_t(elem)) || !aligned(r->out, size_t(elem)))
         return fail(PKV_ERR_INVALID_ARG, "%s: rows must be aligned to their element", name);
-    constexpr int64_t kMost = int64_t(1) << 40;
-    for (int64_t s : {r->in_token_stride, r->in_head_stride, r->out_token_stride, r->out_head_stride})
-        if (s < 0 || s > kMost) return fail(PKV_ERR_INVALID_ARG, "%s: stride %lld", name, (long long)s);
     const int64_t h = r->num_heads;
-    const int64_t tspan = (tokens - 1) * r->out_token_stride, hspan = (h - 1) * r->out_head_stride;
+    constexpr int64_t kMost = int64_t(1) << 46;  // elements from first row to last: beyond any memory, and no sum overflows
+    auto sound = [](int64_t stride, int64_t n) { return stride >= 0 && (n == 1 || stride <= kMost / (n - 1)); };
+    for (int64_t s : {r->in_token_stride, r->out_token_stride})
+        if (!sound(s, tokens)) return fail(PKV_ERR_INVALID_ARG, "%s: token stride %lld", name, (long long)s);
+    for (int64_t s : {r->in_head_stride, r->out_head_stride})
+        if (!sound(s, h)) return fail(PKV_ERR_INVALID_ARG, "%s: head stride %lld", name, (long long)s);
+    const int64_t tspan = tokens == 1 ? 0 : (tokens - 1) * r->out_token_stride;
+    const int64_t hspan = h == 1 ? 0 : (h - 1) * r->out_head_stride;
     const bool heads_inside = (h == 1 || r->out_head_stride >= d) && (tokens == 1 || r->out_token_stride >= hspan + d);
     const bool tokens_inside = (tokens == 1 || r->out_token_stride >= d) && (h == 1 || r->out_head_stride >= tspan + d);
     if (!heads_inside && !tokens_inside) return fail(PKV_ERR_INVALID_ARG, "%s: out rows overlap", name);
     const bool same = r->in == r->out && (tokens == 1 || r->in_token_stride == r->out_token_stride) &&
                       (h == 1 || r->in_head_stride == r->out_head_stride);
     const uintptr_t i0 = reinterpret_cast<uintptr_t>(r->in), o0 = reinterpret_cast<uintptr_t>(r->out);
-    const uintptr_t i1 = i0 + uintptr_t(((tokens - 1) * r->in_token_stride + (h - 1) * r->in_head_stride + d) * elem);
+    const int64_t ispan = (tokens == 1 ? 0 : (tokens - 1) * r->in_token_stride) + (h == 1 ? 0 : (h - 1) * r->in_head_stride);
+    const uintptr_t i1 = i0 + uintptr_t((ispan + d) * elem);
     const uintptr_t o1 = o0 + uintptr_t((tspan + hspan + d) * elem);
     // extents that meet under other strides could write what is still to be read
     if (!same && i0 < o1 && o0 < i1) return fail(PKV_ERR_INVALID_ARG, "%s: out overlaps in with other strides", name);
     return PKV_OK;
+}
+
+// Whether bf16 rows of `row` elements at x (strides sx) and y (sy, both at least row) share bytes;
+// where the strides differ, whether their extents do.
+bool rows_meet(const void* x, int64_t sx, const void* y, int64_t sy, int64_t row, int64_t n) {
+    const uintptr_t lo = std::min(reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(y));
+    const uintptr_t delta = std::max(reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(y)) - lo;
+    const int64_t s = lo == reinterpret_cast<uintptr_t>(x) ? sx : sy;
+    if (delta >= 2 * (uintptr_t(n - 1) * uintptr_t(s) + uintptr_t(row))) return false;
+    if (n == 1 || sx != sy) return true;
+    const uintptr_t at = delta % (2 * uintptr_t(s));
+    return at < 2 * uintptr_t(row) || at > 2 * uintptr_t(s - row);
 }
 
 pkv::RotateRows rotate_rows(const pkv_rows* r) {
@@ -1600,6 +1617,8 @@ pkv_status pkv_quant_append(const pkv_cache_desc* desc, const pkv_rope* rope, vo
                     (long long)q_token_stride, (long long)q_out_token_stride, (long long)qrow);
     if (q && q == q_out && q_token_stride != q_out_token_stride)
         return fail(PKV_ERR_INVALID_ARG, "q in place needs one token stride");
+    if (q && q != q_out && rows_meet(q, q_token_stride, q_out, q_out_token_stride, qrow, num_tokens))
+        return fail(PKV_ERR_INVALID_ARG, "q_out overlaps q");
     pkv::QuantArgs a;
     st = quant_args(desc, k_pool, v_pool, k_scale, v_scale, stream, &a);
     if (st != PKV_OK) return st;

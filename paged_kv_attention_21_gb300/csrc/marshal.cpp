@@ -197,6 +197,7 @@ PyObject* guarded(Py_ssize_t nargs, Py_ssize_t want, F body) {
     return nullptr;
 }
 
+// The library's call, which throws nothing: an exception must not leave while the lock is away.
 template <typename F>
 pkv_status without_gil(F call) {
     pkv_status st;
@@ -224,8 +225,9 @@ PyObject* rope_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (tensor(a[4], "k").sizes()[2] != dim) throw Refusal(PyExc_ValueError, "k: expected q's head_dim");
         }
         const int32_t* positions = indexes(a[1], "positions", device, {tokens});
+        const int32_t num_tokens = count(tokens, "positions");
         return without_gil([&] {
-            return g_lib.rope_rotate(&rope, code, positions, count(tokens, "positions"), dim, &rows, has_k ? &krows : nullptr,
+            return g_lib.rope_rotate(&rope, code, positions, num_tokens, dim, &rows, has_k ? &krows : nullptr,
                                      stream);
         });
     });
@@ -255,10 +257,10 @@ PyObject* quant_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
             qo_stride = q_stride;
             if (a[7] != Py_None) q_out = token_rows(a[7], "q_out", p.device, tokens, p.desc.num_q_heads, dim, &qo_stride);
         }
+        const int32_t num_seqs = count(seqs, "block_tables"), num_tokens = count(tokens, "positions");
         return without_gil([&] {
-            return g_lib.append(&p.desc, has_rope ? &rope : nullptr, p.k, p.v, p.k_scale, p.v_scale, tables,
-                                count(seqs, "block_tables"), tts, positions, count(tokens, "positions"), k, v, k_stride, q, q_out,
-                                q_stride, qo_stride, p.stream);
+            return g_lib.append(&p.desc, has_rope ? &rope : nullptr, p.k, p.v, p.k_scale, p.v_scale, tables, num_seqs, tts,
+                                positions, num_tokens, k, v, k_stride, q, q_out, q_stride, qo_stride, p.stream);
         });
     });
 }
@@ -278,9 +280,9 @@ PyObject* quant_read(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const int32_t* positions = indexes(a[2], "positions", p.device, {tokens});
         void* k = address(a[3], "k_out", type, p.device, {tokens, p.desc.num_kv_heads, p.desc.head_dim});
         void* v = address(a[4], "v_out", type, p.device, {tokens, p.desc.num_kv_heads, p.desc.head_dim});
+        const int32_t num_seqs = count(seqs, "block_tables"), num_tokens = count(tokens, "positions");
         return without_gil([&] {
-            return g_lib.read(&p.desc, p.k, p.v, p.k_scale, p.v_scale, tables, count(seqs, "block_tables"), tts, positions,
-                              count(tokens, "positions"), type == at::kFloat ? PKV_F32 : PKV_BF16, k, v, p.stream);
+            return g_lib.read(&p.desc, p.k, p.v, p.k_scale, p.v_scale, tables, num_seqs, tts, positions, num_tokens, type == at::kFloat ? PKV_F32 : PKV_BF16, k, v, p.stream);
         });
     });
 }
@@ -296,9 +298,9 @@ PyObject* quant_load_blocks(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const std::initializer_list<int64_t> shape = {blocks, p.desc.num_kv_heads, p.desc.block_size, p.desc.head_dim};
         void* k = address(a[2], "k_cache", at::kBFloat16, p.device, shape);
         void* v = address(a[3], "v_cache", at::kBFloat16, p.device, shape);
+        const int32_t num_pairs = count(pairs, "src_blocks");
         return without_gil([&] {
-            return g_lib.load_blocks(&p.desc, p.k, p.v, p.k_scale, p.v_scale, src, dst, count(pairs, "src_blocks"), blocks, k, v,
-                                     p.stream);
+            return g_lib.load_blocks(&p.desc, p.k, p.v, p.k_scale, p.v_scale, src, dst, num_pairs, blocks, k, v, p.stream);
         });
     });
 }
@@ -320,8 +322,9 @@ PyObject* quant_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
         float* lse = static_cast<float*>(address(a[9], "lse", at::kFloat, p.device, {seqs, hq}));
         void* ws = address(a[10], "workspace", at::kByte, p.device, {kAny});
         const size_t ws_bytes = ws ? static_cast<size_t>(rows_of(a[10], "workspace")) : 0;
+        const int32_t num_seqs = count(seqs, "context_lens");
         return without_gil([&] {
-            return g_lib.decode(&p.desc, q, p.k, p.v, p.k_scale, p.v_scale, tables, lens, count(seqs, "context_lens"), max_len,
+            return g_lib.decode(&p.desc, q, p.k, p.v, p.k_scale, p.v_scale, tables, lens, num_seqs, max_len,
                                 static_cast<float>(sm_scale), window, sinks, chunk, out, lse, ws, ws_bytes, p.stream);
         });
     });

@@ -591,18 +591,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) load(i, i * C::kStage);
 
-    // ---- q as f16, scaled by 2^(12 - e), e the exponent of the group's largest |q|
-    float qmax = 0.f;
+    // ---- q as f16, scaled by 2^(12 - e), e the exponent of the group's largest finite |q|
+    auto largest = [&](bool finite) {  // of the finite ones, or of all but NaN
+        float m = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                qmax = fmax3(qmax, fabsf(bf16_lo(qb[n][j][i])), fabsf(bf16_hi(qb[n][j][i])));
+                for (int i = 0; i < 2; ++i) {
+                    const float x = bf16_lo(qb[n][j][i]), y = bf16_hi(qb[n][j][i]);
+                    m = finite ? fmax3(m, finite_magnitude(x), finite_magnitude(y)) : fmax3(m, fabsf(x), fabsf(y));
+                }
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, x));
-    const int qe = qmax > 0.f && qmax < INFINITY ? max(12, static_cast<int>(__float_as_uint(qmax) >> 23)) : 139;
+        for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+        return m;
+    };
+    float qmax = largest(false);
+    if (qmax == INFINITY) qmax = largest(true);  // an infinity is its own head's affair
+    const int qe = qmax > 0.f ? max(12, static_cast<int>(__float_as_uint(qmax) >> 23)) : 139;
     const float qf = __uint_as_float(static_cast<uint32_t>(266 - qe) << 23);  // 2^(139 - qe)
 #pragma unroll
     for (int n = 0; n < NT; ++n)

@@ -100,6 +100,7 @@ def pool_values(fmt, d, pool, g):
     codes = pool[..., at]
     if fmt == "int8":
         s = np.ascontiguousarray(pool[..., 16 * rb:]).view(np.float32)
+        s = np.where(np.isnan(s), np.float32(np.nan), s)  # quiet: random bytes may be a signalling NaN
         return (codes.astype(np.float64) - 128) * s[..., None].astype(np.float64)
     c = np.stack((codes & 15, codes >> 4), -1).reshape(codes.shape[:-1] + (d,))
     v = E2M1[c & 7] * np.where(c & 8, -1.0, 1.0)
@@ -147,8 +148,8 @@ def attention(q, keys, vals, sm_scale, sinks=None):
         if every.size == 0:
             continue
         m = every.max()
-        total = np.exp(every - m).sum()
-        lse[h] = m + np.log(total)
+        total = np.exp(every - m).sum() if m > -np.inf else 0.0
+        lse[h] = m + np.log(total) if total else -np.inf
         w = np.exp(x - lse[h])
         o[h] = w @ v if n else 0.0
         mass = w @ np.abs(v) if n else np.zeros(d)

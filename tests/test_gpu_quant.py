@@ -238,6 +238,189 @@ def test_load_blocks_and_copy_blocks(fmt, hkv, d):
         assert np.array_equal(gp[which].cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hq,hkv,d,r,layout,where", [
+    (8, 2, 64, 64, "half", "packed"), (8, 2, 64, 32, "half", "in place"), (12, 3, 128, 128, "half", "in place"),
+    (5, 1, 128, 48, "interleaved", "packed"), (6, 6, 64, 64, "interleaved", "in place"),
+    (16, 1, 128, 96, "half", "alternating"), (6, 2, 128, 18, "half", "in place")])
+def test_append_of_many_tokens_is_the_append_of_few(fmt, hq, hkv, d, r, layout, where):
+    """One call of so many tokens that q gets blocks of its own, against calls of 500:
+    the same bits in pools and q_out, padding, bad positions, bad blocks and a ring
+    included (a bad block keeps its token's q)."""
+    rng = np.random.default_rng(hq * d + r)
+    n = (3 << 16) // ((hq + 2 * hkv) * (d // 16)) + 777
+    seqs, ring = 37, 0 if where == "packed" else 8
+    mbps = ((n // seqs + 16) // 16 if not ring else ring) + 1
+    pos = (np.arange(n) // seqs).astype(np.int32)
+    if ring:  # the last rounds of the ring: every slot its own
+        pos = pos % (16 * ring) + 16 * ring * 3
+    tts = (np.arange(n) % seqs).astype(np.int32)
+    if ring:
+        tts[seqs * 16 * ring:] = -1  # further tokens would meet the first ones' slots
+    nb = seqs * mbps
+    tables = rng.permutation(nb).astype(np.int32).reshape(seqs, mbps)
+    tables[3, 0], tables[5, 0] = nb, -1
+    tts[[7, n // 2, n - 2]] = -1
+    tts[100], pos[200], pos[300] = seqs, -5, 10 ** 6
+    cs = pkv.pkv_rope_scaled_table(1e4, r, 16 * ring * 4 if ring else n // seqs + 1)
+    rope = pkv.make_rope(dev(cs), layout=layout, inverse=where == "alternating")
+    buf = torch.randn(n, hq + 2 * hkv, d, device=DEV).bfloat16()
+    k, v = buf[:, hq:hq + hkv], buf[:, hq + hkv:]
+    g = dev(np.full(hkv, 4 / 2688, np.float32)) if fmt == "fp4" else None
+    dd = desc_of(fmt, hq, hkv, d, nb, mbps, ring)
+    td, sd, pd = dev(tables), dev(tts), dev(pos)
+
+    def run(step):
+        pools = [torch.full((nb, hkv, Q.record_bytes(fmt, d)), 77, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        if where == "alternating":  # q and q_out rows in turn in one buffer
+            both = torch.full((n, 2, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+            both[:, 0] = buf[:, :hq]
+            q, qo = both[:, 0], both[:, 1]
+        elif where == "packed":
+            q, qo = buf[:, :hq], torch.full((n, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        else:
+            q, qo = buf[:, :hq].clone(), None
+        for i in range(0, n, step):
+            at = slice(i, i + step)
+            pkv.pkv_quant_append(dd, pools[0], pools[1], td, sd[at], pd[at], k[at], v[at], q=q[at],
+                                 q_out=None if qo is None else qo[at], rope=rope, k_scale=g, v_scale=g)
+        assert pkv.pkv_device_errors() == pkv.DEVERR_POSITION | pkv.DEVERR_BLOCK_ID
+        return pools + [q, q if qo is None else qo]
+    many, few = run(n), run(500)
+    for a, b in zip(many, few):
+        assert torch.equal(a, b)
+    # the rotation itself, bit for bit
+    x = buf[:, :hq].float().cpu().numpy()
+    got = many[3].cpu()
+    for i in list(range(0, n, 97)) + [3, 5, 7, 100, 200, 300]:
+        bad = tts[i] < 0 or tts[i] >= seqs or pos[i] < 0 or pos[i] >= len(cs)
+        if bad:
+            want = torch.from_numpy(x[i]).bfloat16() if where == "in place" else torch.full((hq, d), 7.0).bfloat16()
+        else:
+            want = torch.from_numpy(Q.rotate(x[i], cs[pos[i]], layout, np.float32,
+                                             inverse=where == "alternating")).bfloat16()
+        assert torch.equal(got[i], want), i
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hkv,d", [(3, 128), (8, 64), (5, 64)])
+def test_load_of_many_blocks_is_the_load_of_few(fmt, hkv, d):
+    """So many pairs that a CTA takes four heads (groups of four left incomplete too)."""
+    rec, pairs = Q.record_bytes(fmt, d), 16 * 152 * 512 // (2 * d * hkv) + 11
+    gen = torch.Generator().manual_seed(d)
+    nb = 97
+    pools = [torch.randint(0, 256, (nb, hkv, rec), generator=gen, dtype=torch.uint8) for _ in range(2)]
+    for p in pools:  # scales that are numbers
+        at = p[..., 16 * Q.row_bytes(fmt, d):]
+        at.copy_(torch.rand(nb, hkv, 16, generator=gen).view(torch.uint8) if fmt == "int8" else at % 0x7F)
+    pools = [p.to(DEV) for p in pools]
+    src = torch.randint(0, nb, (pairs,), generator=gen).int()
+    dst = torch.randperm(pairs, generator=gen).int()
+    src[5], dst[9] = nb, -1
+    src, dst = src.to(DEV), dst.to(DEV)
+    g = torch.rand(hkv, generator=gen).to(DEV) + 0.01 if fmt == "fp4" else None
+    dd = desc_of(fmt, hkv, hkv, d, nb, 4)
+
+    def run(step):
+        outs = [torch.full((pairs, hkv, 16, d), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        for i in range(0, pairs, step):
+            pkv.pkv_quant_load_blocks(dd, pools[0], pools[1], src[i:i + step], dst[i:i + step], outs[0], outs[1],
+                                      k_scale=g, v_scale=g)
+        assert pkv.pkv_device_errors() == pkv.DEVERR_BLOCK_ID
+        return outs
+    for a, b in zip(run(pairs), run(50)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+def test_the_binding_refuses_tensors_that_do_not_fit(fmt):
+    hq, hkv, d, nb, mbps, n = 8, 2, 64, 4, 2, 3
+    dd = desc_of(fmt, hq, hkv, d, nb, mbps)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    ok = dict(k_pool=torch.zeros(nb, hkv, Q.record_bytes(fmt, d), dtype=torch.uint8, device=DEV),
+              block_tables=torch.zeros(1, mbps, **i32), token_to_seq=torch.full((n,), -1, **i32),
+              positions=torch.zeros(n, **i32))
+    ok["v_pool"] = ok["k_pool"].clone()
+    if fmt == "fp4":
+        ok.update(k_scale=torch.ones(hkv, device=DEV), v_scale=torch.ones(hkv, device=DEV))
+    bf16 = dict(dtype=torch.bfloat16, device=DEV)
+    x, q = torch.zeros(n, hkv, d, **bf16), torch.zeros(n, hq, d, **bf16)
+    rope = pkv.make_rope(torch.zeros(8, d // 2, 2, device=DEV))
+
+    def refused(fn, error, text, base, **kw):
+        with pytest.raises(error, match=text):
+            fn(desc=dd, **dict(base, **kw))
+    app = dict(ok, k_new=x, v_new=x, q=q, rope=rope)
+    pkv.pkv_quant_append(desc=dd, **app)  # all padding: nothing is written
+    assert not torch.any(ok["k_pool"]) and not torch.any(ok["v_pool"])
+    f = pkv.pkv_quant_append
+    refused(f, TypeError, "k_new: expected a tensor", app, k_new=[1.0])
+    refused(f, ValueError, "k_new is None", app, k_new=None)
+    refused(f, ValueError, "k_new: dtype", app, k_new=x.float())
+    refused(f, ValueError, "k_new: shape", app, k_new=x[:2])
+    refused(f, ValueError, "heads must be contiguous", app, k_new=torch.zeros(n, d, hkv, **bf16).transpose(1, 2))
+    refused(f, ValueError, "strides .* differ", app, k_new=torch.zeros(n, 2 * hkv, d, **bf16)[:, :hkv])
+    refused(f, ValueError, "q: shape", app, q=x)
+    refused(f, ValueError, "q_out: dtype", app, q_out=q.half())
+    refused(f, ValueError, "k_pool: dtype", app, k_pool=ok["k_pool"].to(torch.int8))
+    refused(f, ValueError, "v_pool: shape", app, v_pool=ok["v_pool"][..., 1:])
+    refused(f, ValueError, "v_pool: .*contiguous", app,
+            v_pool=torch.zeros(hkv, nb, ok["k_pool"].shape[2], dtype=torch.uint8, device=DEV).transpose(0, 1))
+    refused(f, ValueError, "positions: dtype", app, positions=ok["positions"].long())
+    refused(f, ValueError, "token_to_seq: shape", app, token_to_seq=ok["token_to_seq"][:1])
+    refused(f, ValueError, "block_tables: shape", app, block_tables=torch.zeros(1, mbps + 1, **i32))
+    refused(f, ValueError, "positions: on cpu", app, positions=ok["positions"].cpu())
+    refused(f, TypeError, "bytes-like", app, rope=3)
+    refused(f, pkv.PkvError, "without a rotation", app, rope=None)
+    refused(f, pkv.PkvError, "rotary_dim", app, rope=pkv.make_rope(torch.zeros(8, d, 2, device=DEV)))
+    scales = dict(k_scale=None) if fmt == "fp4" else dict(k_scale=torch.ones(hkv, device=DEV))
+    refused(f, pkv.PkvError, "k_scale", app, **scales)
+    refused(f, ValueError, "v_scale: shape", app, v_scale=torch.ones(hkv + 1, device=DEV))
+    flat = torch.zeros(n * hkv * d + 8, **bf16)
+    refused(f, pkv.PkvError, "aligned", app, k_new=flat[1:1 + x.numel()].view(x.shape))
+    read = dict(ok, k_out=x.clone(), v_out=x.clone())
+    f = pkv.pkv_quant_read
+    refused(f, ValueError, "k_out or v_out", read, k_out=None, v_out=None)
+    refused(f, ValueError, "dtype", read, k_out=x.half(), v_out=x.half())
+    refused(f, ValueError, "v_out: dtype", read, v_out=x.float())
+    refused(f, ValueError, "k_out: shape", read, k_out=q)
+    bases = {k: ok[k] for k in ("k_pool", "v_pool", "k_scale", "v_scale") if k in ok}
+    cache = torch.zeros(5, hkv, 16, d, **bf16)
+    load = dict(bases, src_blocks=torch.zeros(2, **i32), dst_blocks=torch.zeros(2, **i32), k_cache=cache,
+                v_cache=cache.clone())
+    f = pkv.pkv_quant_load_blocks
+    refused(f, ValueError, "dst_blocks: shape", load, dst_blocks=torch.zeros(3, **i32))
+    refused(f, ValueError, "v_cache: shape", load, v_cache=cache[:4])
+    refused(f, ValueError, "k_cache: dtype", load, k_cache=cache.half())
+    qd = torch.zeros(2, hq, d, **bf16)
+    dec = dict(bases, q=qd, block_tables=torch.zeros(2, mbps, **i32), context_lens=torch.zeros(2, **i32),
+               max_context_len=32, sm_scale=1.0, out=torch.empty_like(qd))
+    f = pkv.pkv_quant_decode
+    refused(f, ValueError, "q: shape", dec, q=q)
+    refused(f, ValueError, "lse: dtype", dec, lse=torch.zeros(2, hq, dtype=torch.float64, device=DEV))
+    refused(f, ValueError, "sinks: shape", dec, sinks=torch.zeros(hkv, device=DEV))
+    refused(f, ValueError, "does not fit", dec, max_context_len=1 << 40)
+    refused(f, TypeError, "real number|float", dec, sm_scale="1")
+    refused(f, TypeError, "integer", dec, window=1.5)
+    f = pkv.pkv_rope_rotate
+    for bad, error, text in ((dict(q=q.double()), ValueError, "q: dtype"), (dict(q=q[0]), ValueError, "q: expected"),
+                             (dict(q=q.transpose(1, 2)), ValueError, "contiguous dims"),
+                             (dict(k=x[:2]), ValueError, "k: 2 tokens"), (dict(k=x.half()), ValueError, "k: dtype"),
+                             (dict(q_out=q[..., :32]), ValueError, "q_out: shape"),
+                             (dict(k=x[..., :32]), ValueError, "head_dim")):
+        with pytest.raises(error, match=text):
+            f(**dict(dict(rope=rope, positions=ok["positions"], q=q), **bad))
+    # calls without tokens or sequences do nothing
+    none = torch.zeros(0, **i32)
+    pkv.pkv_quant_append(desc=dd, **dict(app, token_to_seq=none, positions=none, k_new=x[:0], v_new=x[:0], q=q[:0]))
+    pkv.pkv_quant_read(desc=dd, **dict(read, token_to_seq=none, positions=none, k_out=x[:0], v_out=None))
+    pkv.pkv_quant_load_blocks(desc=dd, **dict(load, src_blocks=none, dst_blocks=none))
+    pkv.pkv_quant_decode(desc=dd, **dict(dec, q=qd[:0], out=qd[:0], context_lens=none,
+                                         block_tables=torch.zeros(0, mbps, **i32)))
+    pkv.pkv_rope_rotate(rope, none, q[:0])
+    assert pkv.pkv_device_errors() == 0
+
+
 # ---------------------------------------------------------------- decode --
 
 def run_decode(c, sm_scale=None, window=-1, chunk=0, sinks=None, max_len=None, ws=None, lens=None):
@@ -289,7 +472,7 @@ def test_decode_lengths_and_groups(fmt, d, hq, hkv):
 @pytest.mark.parametrize("chunk", [1, 2, 3, 5, 8, 40])
 def test_decode_splits(fmt, hq, hkv, d, chunk):
     """1 .. 64 chunks a sequence, a last chunk of one key, empty sequences beside
-    long ones; the same workspace for every call, left with its tickets at zero."""
+    long ones; the same workspace for every call, whatever the last one left in it."""
     rng = np.random.default_rng(chunk)
     c = Q.QuantCase(rng, fmt, [1009, 0, 16 * chunk, 16 * chunk + 1, 5, 320], hq, hkv, d)
     dd = desc_of(fmt, hq, hkv, d, c.nb, c.mbps)
@@ -373,6 +556,52 @@ def test_decode_bad_blocks_and_lengths_are_flagged():
     c.lens = np.array([64, 50], np.int32)
     check_decode(c, (o, lse))
     c.lens = full
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 64), (7, 1, 128), (12, 1, 128), (5, 1, 64), (18, 2, 64)])
+def test_decode_many_sequences_merge_in_wide_ctas(fmt, hq, hkv, d):
+    """More rows than the narrow merge takes (152 * 16): several heads a CTA, groups that
+    fill no whole number of CTAs, empty and one-chunk sequences in between."""
+    rng = np.random.default_rng(hq + d)
+    n = 2432 // hq + 9
+    lens = rng.integers(0, 60, n)
+    c = Q.QuantCase(rng, fmt, lens, hq, hkv, d)
+    check_decode(c, run_decode(c, chunk=1), seqs=range(0, n, 3))
+    sinks = rng.standard_normal(hq).astype(np.float32)
+    check_decode(c, run_decode(c, chunk=1, window=20, sinks=sinks), 20, sinks, seqs=range(1, n, 5))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 128), (9, 1, 64)])
+def test_decode_most_chunks(fmt, hq, hkv, d):
+    """256 chunks are the most; a bound that needs one more is refused."""
+    rng = np.random.default_rng(3)
+    c = Q.QuantCase(rng, fmt, [4096, 4081, 17], hq, hkv, d)
+    check_decode(c, run_decode(c, chunk=1))
+    c = Q.QuantCase(rng, fmt, [4097], hq, hkv, d)
+    with pytest.raises(pkv.PkvError, match="chunks"):
+        run_decode(c, chunk=1)
+    check_decode(c, run_decode(c, chunk=2))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (11, 1)])
+def test_decode_a_query_head_that_is_not_finite_spoils_no_other(fmt, bad, hq, hkv):
+    """The group's heads share q's power of two: an infinity must not set it (the others,
+    beyond f16's range here, would overflow)."""
+    rng = np.random.default_rng(5)
+    c = Q.QuantCase(rng, fmt, [300, 40], hq, hkv, 64)
+    c.q = Q.bf16(c.q * 3e5)
+    whole = c.q.copy()
+    c.q[0, 1, 7] = bad
+    o, lse = run_decode(c, sm_scale=1e-6)
+    assert not np.any(np.isfinite(o[0, 1]))
+    c.q = whole
+    o2, lse2 = run_decode(c, sm_scale=1e-6)
+    o[0, 1], lse[0, 1] = o2[0, 1], lse2[0, 1]
+    check_decode(c, (o, lse), sm_scale=1e-6)
 
 
 def test_decode_two_streams_two_workspaces_and_graphs():
@@ -545,3 +774,69 @@ def test_a_batch_served_through_the_quantised_cache(fmt, layout, r):
             assert np.all(np.abs(out[s].double().cpu().numpy() - ro) <= tol)
             assert np.all(np.abs(lse[s].double().cpu().numpy() - rl) <= ltol)
     assert pkv.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+def test_captured_serving_steps_are_the_eager_ones(fmt):
+    """Append (q in place) then decode, the launches overlapping as they do in a stream:
+    40 steps without a synchronisation, and the same steps as replays of one graph whose
+    positions and lengths move on the device, give the same bits as one step at a time."""
+    hq, hkv, d, b, steps = 16, 2, 128, 5, 40
+    start = torch.tensor([0, 15, 250, 31, 700], dtype=torch.int32, device=DEV)
+    mbps = (700 + steps) // 16 + 1
+    nb = b * mbps
+    gen = torch.Generator().manual_seed(2)
+    tables = torch.randperm(nb, generator=gen).int().view(b, mbps).to(DEV)
+    dd = desc_of(fmt, hq, hkv, d, nb, mbps)
+    g = torch.full((hkv,), 4 / 2688, device=DEV) if fmt == "fp4" else None
+    rope = pkv.make_rope(dev(pkv.pkv_rope_scaled_table(1e4, d, 800)))
+    tts = torch.arange(b, dtype=torch.int32, device=DEV)
+    rows = torch.randn(steps, b, hq + 2 * hkv, d, generator=gen).bfloat16().to(DEV)
+    old = torch.randn(700, hkv, d, generator=gen).bfloat16().to(DEV)
+    ws = torch.zeros(max(256, pkv.pkv_quant_decode_workspace_size(dd, b, 740, -1, 4)), dtype=torch.uint8, device=DEV)
+
+    def fresh():
+        pools = [torch.zeros(nb, hkv, Q.record_bytes(fmt, d), dtype=torch.uint8, device=DEV) for _ in range(2)]
+        for s, n in enumerate(start.tolist()):
+            at = torch.arange(n, dtype=torch.int32, device=DEV)
+            pkv.pkv_quant_append(dd, pools[0], pools[1], tables, torch.full_like(at, s), at, old[:n], old[:n],
+                                 k_scale=g, v_scale=g)
+        return pools
+
+    def step(pools, buf, pos, lens, out):
+        pkv.pkv_quant_append(dd, pools[0], pools[1], tables, tts, pos, buf[:, hq:hq + hkv], buf[:, hq + hkv:],
+                             q=buf[:, :hq], q_out=out, rope=rope, k_scale=g, v_scale=g)
+        pkv.pkv_quant_decode(dd, out, pools[0], pools[1], tables, lens, 740, d ** -0.5, out, None, ws,
+                             chunk_blocks=4, k_scale=g, v_scale=g)
+
+    results = []
+    for wait in (True, False):
+        pools = fresh()
+        pos = [start + i for i in range(steps)]
+        lens = [p + 1 for p in pos]
+        outs = torch.zeros(steps, b, hq, d, dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            step(pools, rows[i], pos[i], lens[i], outs[i])
+            if wait:
+                torch.cuda.synchronize()
+        results.append(pools + [outs])
+    pools, outs = fresh(), torch.zeros(steps, b, hq, d, dtype=torch.bfloat16, device=DEV)
+    buf, pos, lens = rows[0].clone(), start.clone(), start + 1
+    out = torch.zeros(b, hq, d, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(pools, buf, pos, lens, out)
+        pos += 1
+        lens += 1
+    for i in range(steps):
+        buf.copy_(rows[i])
+        graph.replay()
+        outs[i].copy_(out)
+    torch.cuda.synchronize()
+    results.append(pools + [outs])
+    assert pkv.pkv_device_errors() == 0
+    for other in results[1:]:
+        for a, c in zip(results[0], other):
+            assert torch.equal(a, c)

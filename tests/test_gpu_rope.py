@@ -180,3 +180,36 @@ def test_offsets_past_32_bits():
     pos = torch.tensor([1, 30, 63], dtype=torch.int32, device=DEV)
     pkv.pkv_rope_rotate(pkv.make_rope(t), pos, x, out)
     check(out, x.cpu(), cs, pos.tolist(), "half")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("hq,hkv,d,r", [(32, 8, 128, 128), (5, 3, 128, 64), (9, 0, 96, 32)])
+def test_many_rows_are_turned_as_few_are(dtype, layout, hq, hkv, d, r):
+    """So many rows that a thread takes four heads (heads that are no multiple of four,
+    passing dims, padding and bad positions included), against calls of few tokens."""
+    n = 4 * 152 * 512 * 16 // ((hq + hkv) * r * dtype.itemsize // (2 if layout == "half" else 1)) + 13
+    cs, t = table(1e4, r, 500)
+    rope = pkv.make_rope(t, layout=layout)
+    gen = torch.Generator().manual_seed(n)
+    pos = torch.randint(0, 500, (n,), generator=gen).int()
+    pos[[0, 5, n - 1]] = torch.tensor([-1, 500, -7], dtype=torch.int32)
+    pd = pos.to(DEV)
+    x = torch.randn(n, hq + hkv, d, generator=gen).to(dtype).to(DEV)
+
+    def run(step, in_place):
+        src = x.clone() if in_place else x
+        out = src if in_place else torch.full_like(x, 7.0)
+        for i in range(0, n, step):
+            at = slice(i, i + step)
+            pkv.pkv_rope_rotate(rope, pd[at], src[at, :hq], None if in_place else out[at, :hq],
+                                src[at, hq:] if hkv else None, None if in_place or not hkv else out[at, hq:])
+        assert pkv.pkv_device_errors() == pkv.DEVERR_POSITION
+        return out
+    few = run(997, False)
+    check(few[::31], x[::31].cpu(), cs, pos[::31].tolist(), layout)
+    assert torch.equal(run(n, False), few)
+    padded = torch.tensor([0, 5, n - 1], device=DEV)
+    assert torch.all(few[padded] == 7)
+    few[padded] = x[padded]
+    assert torch.equal(run(n, True), few)

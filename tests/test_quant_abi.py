@@ -112,6 +112,10 @@ def test_rope_refusals(lib):
     assert status(lib, call(q=rows(out_token_stride=255)), "overlap") == 1
     assert status(lib, call(q=rows(out=0x1000, out_token_stride=512)), "overlaps in") == 1
     assert status(lib, call(q=rows(out=0x1040)), "overlaps in") == 1
+    # strides whose extents would not fit 64 bits
+    assert status(lib, call(q=rows(in_token_stride=1 << 46), tokens=2 ** 31 - 1), "stride") == 1
+    assert status(lib, call(q=rows(out_token_stride=2 ** 63 - 1)), "stride") == 1
+    assert status(lib, call(q=rows(in_head_stride=1 << 62)), "stride") == 1
     assert status(lib, call(k=rows(num_heads=-1)), "num_heads") == 1
     assert call(tokens=0) == 0
     assert call(q=rows(num_heads=0)) == 0
@@ -142,6 +146,11 @@ def test_append_refusals(lib):
     assert status(lib, call(stride=260), "stride") == 1
     assert status(lib, call(qs=1000), "stride") == 1
     assert status(lib, call(qs=2048), "in place") == 1
+    # q_out partly on q: a shifted row, a row of the next token, other strides
+    assert status(lib, call(qo=P.value + 16), "q_out overlaps q") == 1
+    assert status(lib, call(qo=P.value + 2 * 1024 - 16), "q_out overlaps q") == 1
+    assert status(lib, call(qo=P.value + 2 * 1032, qs=2048, qos=2048, n=3, q=P.value + 4096), "q_out overlaps q") == 1
+    assert status(lib, call(qo=P.value + 2 * 4096, qs=2048, qos=4096, n=5), "q_out overlaps q") == 1
     assert call(n=0) == 0
 
 
@@ -195,7 +204,7 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError, match="pairs"):
         pkv.make_rope(z(4, 32, 2), rotary_dim=32)
     with pytest.raises(ValueError, match="layout"):
-        pkv.make_rope(z(4, 32, 2), layout="neox")
+        pkv.make_rope(z(4, 32, 2), layout="swapped")
     d = desc()
     pool = z(10, 2, 2112, dtype=torch.uint8)
     with pytest.raises(ValueError, match="k_pool.*device"):
