@@ -1,11 +1,12 @@
 // rope_quant.cu -- rotary positions in both pair layouts, and the quantised
 // pools' append, row read and block widening (formats: include/pkv.h).
 //
-// All four move bytes: each lane handles 16 bytes of 16-bit values (8 dims) at a
-// time, so that a warp's loads and stores of a row are whole lines, and several
-// rows per thread, all loads ahead of the first use, so that enough bytes are in
-// flight.  The rotation's (cos, sin) pairs are read once per thread and used for
-// all of its rows.
+// All four move bytes, and a call is short: one to three waves of blocks whose loads
+// depend on one another twice (the position, then its table entry or block).  So a lane
+// handles 16 bytes of 16-bit values (8 dims) at a time, a warp's loads and stores of a row
+// being whole lines; the rows are loaded before the position is waited for; where there
+// are many rows a thread of the rotation takes four, whose (cos, sin) it reads once; and
+// blocks are small, so that the last wave is.
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -13,6 +14,8 @@
 namespace pkv {
 
 namespace {
+
+constexpr int kRopeThreads = 64, kAppendThreads = 128;
 
 // ---------------------------------------------------------- conversions --
 
@@ -70,7 +73,9 @@ __device__ __forceinline__ bool token_in_table(int s, int p, int num_seqs, int m
 // pairs one vector; positions past the rotary dims copy a vector (out of place only).
 // It moves each byte once, so HBM bounds it; what it fights is the address arithmetic (one
 // base per thread, then the head stride) and latency (kRows vectors in flight before
-// anything waits, the position and table entry among them).
+// anything waits, the position among them).  4096 tokens of 32 + 8 heads of 128, in place in
+// a packed buffer (84 MB), from a replayed graph: 15.3 us, 5.6 TB/s; 16.0 in blocks of 256
+// threads, 17.8 with a head a thread, 16.5 with two.
 
 template <typename T, bool kHalf, int kRows>
 __device__ __forceinline__ void rotate_vectors(const RotateArgs& a, unsigned idx, unsigned vectors, unsigned q_slots,
@@ -153,11 +158,11 @@ __device__ __forceinline__ void rotate_vectors(const RotateArgs& a, unsigned idx
 }
 
 template <typename T, bool kHalf, int kRows>
-__global__ void __launch_bounds__(256) rope_vector_kernel(const __grid_constant__ RotateArgs a, unsigned vectors,
+__global__ void __launch_bounds__(kRopeThreads, 16) rope_vector_kernel(const __grid_constant__ RotateArgs a, unsigned vectors,
                                                           unsigned q_slots, unsigned slots, int first_token) {
     pdl_wait();
     pdl_launch_dependents();
-    rotate_vectors<T, kHalf, kRows>(a, blockIdx.x * 256u + threadIdx.x, vectors, q_slots, slots, first_token);
+    rotate_vectors<T, kHalf, kRows>(a, blockIdx.x * kRopeThreads + threadIdx.x, vectors, q_slots, slots, first_token);
 }
 
 // Rows that no 16-byte vector fits (their address, stride, rotary or head dims):
@@ -203,6 +208,12 @@ __global__ void __launch_bounds__(256) rope_scalar_kernel(const __grid_constant_
 // D/16 lanes per row, two vectors of 8 dims each: a rotation's pair of vectors where the
 // pairs are half-split, so that every byte and every (cos, sin) is read once.  A thread's
 // rows are kRows query, K or V heads of one token.
+//
+// The quantisation takes some 500 instructions per warp and 512 values, so that K and V
+// of 4096 tokens of 8 heads of 128 (21 MB) take 9.8 us in a replayed graph where HBM would
+// take 3.2, and with 32 rotated q heads (88 MB) 20.4 where it would take 13.0.  32 dims a
+// lane, which halves the instructions, took 8.6 and 20.3, but the 16 heads' rows of 256
+// tokens 3.1 us instead of 2.6, and 999 tokens of 64 + 8 heads of 64 5.8 instead of 4.3.
 
 // The sequence and position of a token: false for padding and, flagged by `report`,
 // for a bad one.
@@ -213,11 +224,13 @@ __device__ __forceinline__ bool quant_token(const QuantArgs& a, int s, int p, bo
     return false;
 }
 
-// The block of a good token; false for a bad id.
-__device__ __forceinline__ bool quant_block(const QuantArgs& a, int s, int p, bool report, int* blk) {
+// The block id of a good token, and whether it is one.
+__device__ __forceinline__ int quant_block(const QuantArgs& a, int s, int p) {
     const int tb = a.ring > 0 ? (p / kBlockSize) % a.ring : p / kBlockSize;
-    *blk = a.block_tables[static_cast<size_t>(s) * a.mbps + tb];
-    if (*blk >= 0 && *blk < a.num_blocks) return true;
+    return a.block_tables[static_cast<size_t>(s) * a.mbps + tb];
+}
+__device__ __forceinline__ bool good_block(const QuantArgs& a, int blk, bool report) {
+    if (blk >= 0 && blk < a.num_blocks) return true;
     if (report) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
     return false;
 }
@@ -290,7 +303,7 @@ __device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, 
     using R = QuantRecord<D, kFp4>;
     constexpr int kLanes = D / 16;
     const int lane = threadIdx.x % kLanes;
-    const unsigned group = block * (256 / kLanes) + threadIdx.x / kLanes;
+    const unsigned group = block * (blockDim.x / kLanes) + threadIdx.x / kLanes;
     const unsigned slots = q_slots + 2 * kv_slots;
     const unsigned token = group / slots;
     unsigned slot = group - token * slots;
@@ -335,8 +348,8 @@ __device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, 
         if (kFp4 && in && !is_q && n < rows) g[n] = (is_v ? a.v_scale : a.k_scale)[h0 + n];
     }
     const bool ok = in && quant_token(a, s, p, report);
-    int blk = 0;
-    const bool stored = ok && !is_q && quant_block(a, s, p, report_block, &blk);
+    int blk = 0;  // looked at after the rotation, whose loads are then in flight beside it
+    if (ok && !is_q) blk = quant_block(a, s, p);
     // (cos, sin) of the lane's pairs: 8 on the vector paths (of c0 with c1, or of the 16
     // dims), else one per dim
     constexpr int kCs = kPairs == kAnyPairs ? 16 : 8;
@@ -369,7 +382,6 @@ __device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, 
         }
     }
     __syncwarp();  // q in place: the rows' lanes have read their vectors
-    uint8_t* rec = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(blk) * a.hkv + h0) * R::kBytes;
     __nv_bfloat16* q_out = static_cast<__nv_bfloat16*>(a.q_out) + i * a.q_out_stride + h0 * D;
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
@@ -414,14 +426,15 @@ __device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, 
         }
         // a warp's rows may be of different kinds: the shuffles are for all of them, the
         // stores for K and V rows
-        const bool kv = stored && n < rows;
+        const bool kv = ok && !is_q && n < rows && good_block(a, blk, report_block && n == 0);
+        uint8_t* rec = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(blk) * a.hkv + h0) * R::kBytes;
         if (__any_sync(0xFFFFFFFFu, kv))
             store_row<D, kFp4>(rec + n * R::kBytes, p % kBlockSize, lane, c0, c1, split, v0, v1, g[n], kv);
     }
 }
 
 template <int D, bool kFp4, int kRows, int kPairs>
-__global__ void __launch_bounds__(256) quant_append_kernel(const __grid_constant__ QuantArgs a, unsigned q_slots,
+__global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(const __grid_constant__ QuantArgs a, unsigned q_slots,
                                                            unsigned kv_slots, int first_token) {
     pdl_wait();  // dependents start as its CTAs leave: triggered here they took the slots of its last waves
     append_rows<D, kFp4, kRows, kPairs>(a, blockIdx.x, q_slots, kv_slots, first_token);
@@ -431,7 +444,7 @@ __global__ void __launch_bounds__(256) quant_append_kernel(const __grid_constant
 // bound by HBM) evenly among blocks that quantise K and V (bound by instruction issue),
 // so that each SM runs both.
 template <int D, bool kFp4, int kPairs>
-__global__ void __launch_bounds__(256, 4) quant_append_mixed_kernel(const __grid_constant__ QuantArgs a,
+__global__ void __launch_bounds__(kRopeThreads, 16) quant_append_mixed_kernel(const __grid_constant__ QuantArgs a,
                                                                     const __grid_constant__ RotateArgs r, unsigned vectors,
                                                                     unsigned q_slots, unsigned q_blocks, unsigned kv_slots,
                                                                     unsigned blocks) {
@@ -440,7 +453,7 @@ __global__ void __launch_bounds__(256, 4) quant_append_mixed_kernel(const __grid
     const unsigned before = static_cast<unsigned>(static_cast<uint64_t>(blockIdx.x) * q_blocks / blocks);
     const unsigned after = static_cast<unsigned>((static_cast<uint64_t>(blockIdx.x) + 1) * q_blocks / blocks);
     if (after > before)
-        rotate_vectors<__nv_bfloat16, kPairs == kHalfPairs, 4>(r, before * 256u + threadIdx.x, vectors, q_slots, q_slots, 0);
+        rotate_vectors<__nv_bfloat16, kPairs == kHalfPairs, 4>(r, before * kRopeThreads + threadIdx.x, vectors, q_slots, q_slots, 0);
     else
         append_rows<D, kFp4, 1, kPairs>(a, blockIdx.x - before, 0, kv_slots, 0);
 }
@@ -501,9 +514,10 @@ __global__ void __launch_bounds__(256) quant_read_kernel(const __grid_constant__
     const int h = static_cast<int>(group - i * a.hkv);
     if (i >= a.num_tokens) return;
     const int s = a.token_to_seq[i], p = a.positions[i], row = p % kBlockSize;
-    int blk;
     const bool report = lane == 0 && h == 0;
-    if (!quant_token(a, s, p, report) || !quant_block(a, s, p, report, &blk)) return;
+    if (!quant_token(a, s, p, report)) return;
+    const int blk = quant_block(a, s, p);
+    if (!good_block(a, blk, report)) return;
     const size_t at = (static_cast<size_t>(blk) * a.hkv + h) * QuantRecord<D, kFp4>::kBytes;
     RowPart<D, kFp4> part[2];
 #pragma unroll
@@ -584,14 +598,15 @@ template <int D, bool kFp4>
 struct AppendLaunch {
     template <int kRows, int kPairs>
     static cudaError_t rows(const QuantArgs& a) {
-        constexpr int kPerBlock = 256 / (D / 16);
+        constexpr int kPerBlock = kAppendThreads / (D / 16);
         const unsigned q_slots = a.q ? (a.hq + kRows - 1) / kRows : 0, kv_slots = (a.hkv + kRows - 1) / kRows;
         const long long slots = q_slots + 2LL * kv_slots;
         const long long most = (0xFFFFFFFFLL - kPerBlock) / slots;  // group indexes are 32 bits wide
         for (long long i = 0; i < a.num_tokens; i += most) {
             const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
             const cudaError_t e = launch_pdl(quant_append_kernel<D, kFp4, kRows, kPairs>,
-                                             dim3(static_cast<unsigned>((n * slots + kPerBlock - 1) / kPerBlock)), dim3(256), 0,
+                                             dim3(static_cast<unsigned>((n * slots + kPerBlock - 1) / kPerBlock)),
+                                             dim3(kAppendThreads), 0,
                                              a.stream, a, q_slots, kv_slots, static_cast<int>(i));
             if (e != cudaSuccess) return e;
         }
@@ -601,8 +616,9 @@ struct AppendLaunch {
     static cudaError_t pairs(const QuantArgs& a) {
         const long long n = static_cast<long long>(a.num_tokens) * (2 * a.hkv + (a.q ? a.hq : 0)) * (D / 16);
         if constexpr (kPairs != kAnyPairs) {
-            // (4096 tokens of 32 + 8 heads took 27.6 us through the kernel above, 24.1 with q in
-            // a launch of its own; 256 tokens of 8 K and V heads 3.3 and 3.4)
+            // (4-bit, 32 + 8 heads of 128: 4096 tokens 23.2 us through the kernel above and 19.8
+            // mixed, 512 tokens 4.3 and 3.6, 256 tokens 3.1 and 2.9, 64 tokens 2.6 both; 64 + 8
+            // heads of 64: 512 tokens, just below this bound, 3.4 and 3.6)
             if (a.q && n >= kMixedThreads && n < 0x7FFFFFFFLL) return mixed<kPairs>(a);
         }
         return rows<1, kPairs>(a);
@@ -624,15 +640,16 @@ struct AppendLaunch {
         r.num_seqs = a.num_seqs;
         r.mbps = a.mbps;
         r.ring = a.ring;
-        constexpr int kPerBlock = 256 / (D / 16);
+        constexpr int kPerBlock = kRopeThreads / (D / 16);
         const unsigned vectors = static_cast<unsigned>((kPairs == kHalfPairs ? a.rotary / 2 : a.rotary) / 8 +
                                                        (a.q == a.q_out ? 0 : (D - a.rotary) / 8));
-        const unsigned q_slots = (a.hq + 3) / 4, kv_slots = a.hkv, tokens = static_cast<unsigned>(a.num_tokens);
-        const unsigned q_blocks = static_cast<unsigned>((static_cast<uint64_t>(tokens) * q_slots * vectors + 255) / 256);
-        const unsigned kv_blocks = static_cast<unsigned>((static_cast<uint64_t>(tokens) * 2 * kv_slots + kPerBlock - 1) / kPerBlock);
+        const unsigned q_slots = (a.hq + 3) / 4, kv_slots = a.hkv;
+        const uint64_t tokens = static_cast<uint64_t>(a.num_tokens);
+        const unsigned q_blocks = static_cast<unsigned>((tokens * q_slots * vectors + kRopeThreads - 1) / kRopeThreads);
+        const unsigned kv_blocks = static_cast<unsigned>((tokens * 2 * kv_slots + kPerBlock - 1) / kPerBlock);
         QuantArgs kv = a;
         kv.q = nullptr;
-        return launch_pdl(quant_append_mixed_kernel<D, kFp4, kPairs>, dim3(q_blocks + kv_blocks), dim3(256), 0, a.stream, kv, r,
+        return launch_pdl(quant_append_mixed_kernel<D, kFp4, kPairs>, dim3(q_blocks + kv_blocks), dim3(kRopeThreads), 0, a.stream, kv, r,
                           vectors, q_slots, q_blocks, kv_slots, q_blocks + kv_blocks);
     }
     static cudaError_t go(const QuantArgs& a) {
@@ -679,9 +696,9 @@ struct RotateLaunch {
         const long long most = (0xFFFFFFFFLL - 256) / per_token;  // thread indexes are 32 bits wide
         for (long long i = 0; i < a.num_tokens; i += most) {
             const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
-            const cudaError_t e = launch_pdl(rope_vector_kernel<T, kHalf, kRows>, dim3(static_cast<unsigned>((n * per_token + 255) / 256)),
-                                             dim3(256), 0, stream, a, static_cast<unsigned>(count), q_slots, slots,
-                                             static_cast<int>(i));
+            const unsigned blocks = static_cast<unsigned>((n * per_token + kRopeThreads - 1) / kRopeThreads);
+            const cudaError_t e = launch_pdl(rope_vector_kernel<T, kHalf, kRows>, dim3(blocks), dim3(kRopeThreads), 0, stream, a,
+                                             static_cast<unsigned>(count), q_slots, slots, static_cast<int>(i));
             if (e != cudaSuccess) return e;
         }
         return cudaSuccess;
