@@ -165,42 +165,183 @@ __global__ void __launch_bounds__(kRopeThreads, 16) rope_vector_kernel(const __g
     rotate_vectors<T, kHalf, kRows>(a, blockIdx.x * kRopeThreads + threadIdx.x, vectors, q_slots, slots, first_token);
 }
 
-// Rows that no 16-byte vector fits (their address, stride, rotary or head dims):
-// one thread per (token, head, pair or passing element).
-template <typename T>
-__global__ void __launch_bounds__(256) rope_scalar_kernel(const __grid_constant__ RotateArgs a) {
+// Rows of vectors whose rotary dims are not: the first `turn_warps` warps turn the vectors
+// that hold rotary dims, `lanes` a row, a row's lanes in one warp (32 / lanes units of kRows
+// heads), each looking its elements' partners up in the row -- with interleaved pairs they
+// are its own -- before any lane of the warp stores, so that in place is safe.  The other
+// warps copy the vectors that pass whole (out of place only).
+// 9265 tokens of 8 + 4 heads of 64, 18 dims turning, out of place (28 MB, 4.3 us of HBM): 6.3 us
+// interleaved; half-split 9.2, bound by the lookups of partners, 12.0 with the passing
+// vectors' lanes in the turning warps, 12.9 with partners from shuffles, 36.6 with a thread
+// per pair and per passing element.
+template <typename T, int kRows>
+__device__ __forceinline__ void rotate_partial(const RotateArgs& a, unsigned warp, unsigned lanes, unsigned turn_warps,
+                                               unsigned q_slots, unsigned slots, int first_token) {
+    constexpr int N = 16 / sizeof(T);
+    const unsigned lane = threadIdx.x % 32u;
+    const bool turns = warp < turn_warps;
+    unsigned rest, v;  // the unit, and the vector of its rows
+    bool live = true;
+    if (turns) {
+        const unsigned units = 32u / lanes, unit = lane / lanes;
+        live = unit < units;
+        rest = warp * units + unit;
+        v = lane - unit * lanes;
+    } else {
+        const unsigned passing = static_cast<unsigned>(a.d) / N - lanes, idx = (warp - turn_warps) * 32u + lane;
+        rest = idx / passing;
+        v = lanes + idx - rest * passing;
+    }
+    const unsigned token = rest / slots;
+    unsigned slot = rest - token * slots;
+    const long long i = first_token + static_cast<long long>(token);
+    const bool is_k = slot >= q_slots;
+    if (is_k) slot -= q_slots;
+    const int h0 = static_cast<int>(slot) * kRows, d0 = static_cast<int>(v) * N;
+    const int rows = live && i < a.num_tokens ? min(kRows, (is_k ? a.k.num_heads : a.q.num_heads) - h0) : 0;
+    const int64_t in_head = is_k ? a.k.in_head : a.q.in_head, out_head = is_k ? a.k.out_head : a.q.out_head;
+    const T* in = static_cast<const T*>(is_k ? a.k.in : a.q.in) + i * (is_k ? a.k.in_token : a.q.in_token) + h0 * in_head;
+    uint4 x[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (r < rows) x[r] = *reinterpret_cast<const uint4*>(in + r * in_head + d0);
+    int p = -1;
+    if (rows > 0) p = a.positions[i];
+    bool ok = p >= 0;
+    if (ok && p >= a.max_pos) {
+        if (d0 == 0 && h0 == 0) flag_error(a.err, PKV_DEVERR_POSITION);
+        ok = false;
+    }
+    if (ok && a.token_to_seq) ok = token_in_table(a.token_to_seq[i], p, a.num_seqs, a.mbps, a.ring);
+    if (turns) {
+        if (ok) {
+            const int half = a.rotary / 2;
+            const float2* cs = reinterpret_cast<const float2*>(a.cos_sin) + static_cast<size_t>(p) * half;
+            float2 t[N];
+            T m[kRows][N];  // partners
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int n = d0 + e;
+                if (n >= a.rotary) continue;
+                if (a.interleaved) {
+                    if (e % 2 == 0) t[e] = cs[n / 2];
+                    continue;
+                }
+                t[e] = cs[n < half ? n : n - half];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    if (r < rows) m[r][e] = in[r * in_head + (n < half ? n + half : n - half)];
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                if (r >= rows) break;
+                T* f = reinterpret_cast<T*>(&x[r]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const int n = d0 + e;
+                    if (n >= a.rotary) continue;
+                    if (a.interleaved) {
+                        if (e % 2) continue;
+                        const float2 z = turn(to_f32(f[e]), to_f32(f[e + 1]), t[e].x, a.inverse ? -t[e].y : t[e].y);
+                        f[e] = from_f32<T>(z.x);
+                        f[e + 1] = from_f32<T>(z.y);
+                        continue;
+                    }
+                    // the first of a pair: own c - other s; the second: own c + other s
+                    const float own = __fmul_rn(to_f32(f[e]), t[e].x), other = __fmul_rn(to_f32(m[r][e]), t[e].y);
+                    f[e] = from_f32<T>(__fadd_rn(own, (n < half) != static_cast<bool>(a.inverse) ? -other : other));
+                }
+            }
+        }
+        __syncwarp();
+    }
+    if (!ok) return;
+    T* out = static_cast<T*>(is_k ? a.k.out : a.q.out) + i * (is_k ? a.k.out_token : a.q.out_token) + h0 * out_head + d0;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (r < rows) *reinterpret_cast<uint4*>(out + r * out_head) = x[r];
+}
+
+// Its warps: those that turn, and with those that copy.
+struct PartialWarps {
+    unsigned lanes;
+    long long turning, all;
+};
+PartialWarps partial_warps(const RotateArgs& a, int n, bool in_place, long long slots) {
+    PartialWarps w;
+    w.lanes = static_cast<unsigned>((a.rotary + n - 1) / n);
+    const long long units = 32 / w.lanes, passing = a.d / n - w.lanes;
+    w.turning = (slots + units - 1) / units;
+    w.all = w.turning + (in_place ? 0 : (slots * passing + 31) / 32);
+    return w;
+}
+
+template <typename T, int kRows>
+__global__ void __launch_bounds__(kRopeThreads) rope_partial_kernel(const __grid_constant__ RotateArgs a, unsigned lanes,
+                                                                    unsigned turn_warps, unsigned q_slots, unsigned slots,
+                                                                    int first_token) {
     pdl_wait();
     pdl_launch_dependents();
+    rotate_partial<T, kRows>(a, (blockIdx.x * kRopeThreads + threadIdx.x) / 32u, lanes, turn_warps, q_slots, slots, first_token);
+}
+
+// Rows that start on no 16-byte boundary, are not whole vectors or are longer than a warp's:
+// a thread takes kPairRun pairs of a row element by element, or 16 bytes of the dims that
+// pass (out of place only), as one vector where `vec` says that rows allow it.
+constexpr int kPairRun = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_constant__ RotateArgs a, unsigned pair_items,
+                                                                unsigned items, bool vec, int first_token) {
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int N = 16 / sizeof(T);
     const int half = a.rotary / 2;
-    const int items = a.d - half;  // pairs, then the dims that pass
-    const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int it = static_cast<int>(idx % items);
-    const long long row = idx / items;
-    const int heads = a.q.num_heads + a.k.num_heads;
-    const long long i = row / heads;
+    const unsigned idx = blockIdx.x * kRopeThreads + threadIdx.x, heads = a.q.num_heads + a.k.num_heads;
+    const unsigned row = idx / items, it = idx - row * items, token = row / heads;
+    int h = static_cast<int>(row - token * heads);
+    const long long i = first_token + static_cast<long long>(token);
     if (i >= a.num_tokens) return;
     const int p = a.positions[i];
     if (p < 0) return;
     if (p >= a.max_pos) {
-        if (it == 0) flag_error(a.err, PKV_DEVERR_POSITION);
+        if (it == 0 && h == 0) flag_error(a.err, PKV_DEVERR_POSITION);
         return;
     }
-    if (a.token_to_seq && !token_in_table(a.token_to_seq[i], p, a.num_seqs, a.mbps, a.ring)) return;
-    int h = static_cast<int>(row % heads);
     const RotateRows& r = h >= a.q.num_heads ? a.k : a.q;
     if (h >= a.q.num_heads) h -= a.q.num_heads;
     const T* in = static_cast<const T*>(r.in) + i * r.in_token + h * r.in_head;
     T* out = static_cast<T*>(r.out) + i * r.out_token + h * r.out_head;
-    if (it >= half) {
-        out[it + half] = in[it + half];
+    if (it < pair_items) {
+        const int j0 = static_cast<int>(it) * kPairRun, n = min(kPairRun, half - j0);
+        const float2* cs = reinterpret_cast<const float2*>(a.cos_sin) + static_cast<size_t>(p) * half + j0;
+        const int e0 = a.interleaved ? 2 * j0 : j0, step = a.interleaved ? 2 : 1, away = a.interleaved ? 1 : half;
+        T x[kPairRun], y[kPairRun];
+        float2 t[kPairRun];
+#pragma unroll
+        for (int u = 0; u < kPairRun; ++u)
+            if (u < n) {
+                x[u] = in[e0 + u * step];
+                y[u] = in[e0 + u * step + away];
+                t[u] = cs[u];
+            }
+#pragma unroll
+        for (int u = 0; u < kPairRun; ++u)
+            if (u < n) {
+                const float2 z = turn(to_f32(x[u]), to_f32(y[u]), t[u].x, a.inverse ? -t[u].y : t[u].y);
+                out[e0 + u * step] = from_f32<T>(z.x);
+                out[e0 + u * step + away] = from_f32<T>(z.y);
+            }
         return;
     }
-    const float* cs = a.cos_sin + (static_cast<size_t>(p) * half + it) * 2;
-    const int e0 = a.interleaved ? 2 * it : it;
-    const int e1 = a.interleaved ? 2 * it + 1 : it + half;
-    const float2 y = turn(to_f32(in[e0]), to_f32(in[e1]), cs[0], a.inverse ? -cs[1] : cs[1]);
-    out[e0] = from_f32<T>(y.x);
-    out[e1] = from_f32<T>(y.y);
+    const int d0 = (a.rotary / N + static_cast<int>(it - pair_items)) * N;
+    if (vec && d0 >= a.rotary) {
+        *reinterpret_cast<uint4*>(out + d0) = *reinterpret_cast<const uint4*>(in + d0);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        if (d0 + e >= a.rotary && d0 + e < a.d) out[d0 + e] = in[d0 + e];
 }
 
 // --------------------------------------------------------------- append --
@@ -361,6 +502,7 @@ __device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, 
             for (int e = 0; e < 16; ++e) {
                 const int d = 8 * c0 + e;
                 if (d >= a.rotary) continue;
+                if (a.interleaved && e % 2) continue;  // its pair's
                 const float2 t = *reinterpret_cast<const float2*>(cs + 2 * (a.interleaved ? d >> 1 : d < half ? d : d - half));
                 c[e] = t.x;
                 sn[e] = t.y;
@@ -407,13 +549,22 @@ __device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, 
                     v1[e] = z1.x;
                     v1[e + 1] = z1.y;
                 }
+            } else if (a.interleaved) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    if (8 * c0 + e >= a.rotary) continue;
+                    float* v = e < 8 ? v0 + e : v1 + (e - 8);
+                    const float2 z = turn(v[0], v[1], c[e], sn[e]);
+                    v[0] = z.x;
+                    v[1] = z.y;
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int d = 8 * c0 + e;
                     if (d >= a.rotary) continue;
-                    const bool b = a.interleaved ? d & 1 : d >= half;
-                    const float m = __bfloat162float(src[n * D + (a.interleaved ? d ^ 1 : b ? d - half : d + half)]);
+                    const bool b = d >= half;
+                    const float m = __bfloat162float(src[n * D + (b ? d - half : d + half)]);
                     float& v = e < 8 ? v0[e] : v1[e - 8];
                     v = b ? turn(m, v, c[e], sn[e]).y : turn(v, m, c[e], sn[e]).x;
                 }
@@ -446,15 +597,19 @@ __global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(const __gr
 template <int D, bool kFp4, int kPairs>
 __global__ void __launch_bounds__(kRopeThreads, 16) quant_append_mixed_kernel(const __grid_constant__ QuantArgs a,
                                                                     const __grid_constant__ RotateArgs r, unsigned vectors,
-                                                                    unsigned q_slots, unsigned q_blocks, unsigned kv_slots,
-                                                                    unsigned blocks) {
+                                                                    unsigned lanes, unsigned turn_warps, unsigned q_slots, unsigned q_blocks,
+                                                                    unsigned kv_slots, unsigned blocks) {
     pdl_wait();
     // of the first b blocks, b q_blocks / blocks rotate
     const unsigned before = static_cast<unsigned>(static_cast<uint64_t>(blockIdx.x) * q_blocks / blocks);
     const unsigned after = static_cast<unsigned>((static_cast<uint64_t>(blockIdx.x) + 1) * q_blocks / blocks);
-    if (after > before)
-        rotate_vectors<__nv_bfloat16, kPairs == kHalfPairs, 4>(r, before * kRopeThreads + threadIdx.x, vectors, q_slots, q_slots, 0);
-    else
+    if (after > before) {
+        const unsigned thread = before * kRopeThreads + threadIdx.x;
+        if (kPairs == kAnyPairs && lanes)
+            rotate_partial<__nv_bfloat16, 4>(r, thread / 32u, lanes, turn_warps, q_slots, q_slots, 0);
+        else
+            rotate_vectors<__nv_bfloat16, kPairs != kLanePairs, 4>(r, thread, vectors, q_slots, q_slots, 0);
+    } else
         append_rows<D, kFp4, 1, kPairs>(a, blockIdx.x - before, 0, kv_slots, 0);
 }
 
@@ -615,7 +770,7 @@ struct AppendLaunch {
     template <int kPairs>
     static cudaError_t pairs(const QuantArgs& a) {
         const long long n = static_cast<long long>(a.num_tokens) * (2 * a.hkv + (a.q ? a.hq : 0)) * (D / 16);
-        if constexpr (kPairs != kAnyPairs) {
+        if (a.cos_sin) {
             // (4-bit, 32 + 8 heads of 128: 4096 tokens 23.2 us through the kernel above and 19.8
             // mixed, 512 tokens 4.3 and 3.6, 256 tokens 3.1 and 2.9, 64 tokens 2.6 both; 64 + 8
             // heads of 64: 512 tokens, just below this bound, 3.4 and 3.6)
@@ -641,16 +796,21 @@ struct AppendLaunch {
         r.mbps = a.mbps;
         r.ring = a.ring;
         constexpr int kPerBlock = kRopeThreads / (D / 16);
-        const unsigned vectors = static_cast<unsigned>((kPairs == kHalfPairs ? a.rotary / 2 : a.rotary) / 8 +
+        // q's pairs: as vectors, half-split with r a multiple of 16 too, or looked up in the row
+        const bool whole = kPairs != kAnyPairs ||
+                           (!a.interleaved && a.rotary % 16 == 0 && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0);
+        const unsigned vectors = static_cast<unsigned>((kPairs != kLanePairs ? a.rotary / 2 : a.rotary) / 8 +
                                                        (a.q == a.q_out ? 0 : (D - a.rotary) / 8));
         const unsigned q_slots = (a.hq + 3) / 4, kv_slots = a.hkv;
         const uint64_t tokens = static_cast<uint64_t>(a.num_tokens);
-        const unsigned q_blocks = static_cast<unsigned>((tokens * q_slots * vectors + kRopeThreads - 1) / kRopeThreads);
+        const PartialWarps w = partial_warps(r, 8, a.q == a.q_out, static_cast<long long>(tokens * q_slots));
+        const uint64_t q_threads = whole ? tokens * q_slots * vectors : static_cast<uint64_t>(w.all) * 32;
+        const unsigned q_blocks = static_cast<unsigned>((q_threads + kRopeThreads - 1) / kRopeThreads);
         const unsigned kv_blocks = static_cast<unsigned>((tokens * 2 * kv_slots + kPerBlock - 1) / kPerBlock);
         QuantArgs kv = a;
         kv.q = nullptr;
         return launch_pdl(quant_append_mixed_kernel<D, kFp4, kPairs>, dim3(q_blocks + kv_blocks), dim3(kRopeThreads), 0, a.stream, kv, r,
-                          vectors, q_slots, q_blocks, kv_slots, q_blocks + kv_blocks);
+                          vectors, whole ? 0u : w.lanes, static_cast<unsigned>(w.turning), q_slots, q_blocks, kv_slots, q_blocks + kv_blocks);
     }
     static cudaError_t go(const QuantArgs& a) {
         if (a.cos_sin && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0) {
@@ -679,16 +839,19 @@ struct LoadLaunch {
 
 template <typename T>
 struct RotateLaunch {
-    static bool vectors_fit(const RotateArgs& a) {
-        constexpr int N = 16 / sizeof(T);
+    static constexpr int N = 16 / sizeof(T);
+    // every row starts on a 16-byte boundary and is whole vectors
+    static bool rows_fit(const RotateArgs& a) {
         auto rows = [](const RotateRows& r) {
             return r.num_heads == 0 ||
                    ((reinterpret_cast<uintptr_t>(r.in) | reinterpret_cast<uintptr_t>(r.out)) % 16 == 0 &&
                     (r.in_token | r.in_head | r.out_token | r.out_head) % N == 0);
         };
-        return a.d % N == 0 && a.rotary % (a.interleaved ? N : 2 * N) == 0 &&
-               reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0 && rows(a.q) && rows(a.k);
+        return a.d % N == 0 && rows(a.q) && rows(a.k);
     }
+    // in place nothing passes (with one of q and k in place, its passing dims are
+    // written back as they are: the same bytes, by the thread that read them)
+    static bool in_place(const RotateArgs& a) { return a.q.in == a.q.out && (a.k.num_heads == 0 || a.k.in == a.k.out); }
     template <bool kHalf, int kRows>
     static cudaError_t vectors(const RotateArgs& a, int count, cudaStream_t stream) {
         const unsigned q_slots = (a.q.num_heads + kRows - 1) / kRows, slots = q_slots + (a.k.num_heads + kRows - 1) / kRows;
@@ -705,21 +868,49 @@ struct RotateLaunch {
     }
     template <bool kHalf>
     static cudaError_t by_rows(const RotateArgs& a, cudaStream_t stream) {
-        constexpr int N = 16 / sizeof(T);
-        // in place nothing passes (with one of q and k in place, its passing dims
-        // are written back as they are: the same bytes, by the thread that read them)
-        const bool in_place = a.q.in == a.q.out && (a.k.num_heads == 0 || a.k.in == a.k.out);
-        const int count = (kHalf ? a.rotary / 2 : a.rotary) / N + (in_place ? 0 : (a.d - a.rotary) / N);
+        const int count = (kHalf ? a.rotary / 2 : a.rotary) / N + (in_place(a) ? 0 : (a.d - a.rotary) / N);
         const long long one = static_cast<long long>(a.num_tokens) * (a.q.num_heads + a.k.num_heads) * count;
         if (one >= 4 * kBusyThreads) return vectors<kHalf, 4>(a, count, stream);
         return vectors<kHalf, 1>(a, count, stream);
     }
+    template <int kRows>
+    static cudaError_t partial(const RotateArgs& a, cudaStream_t stream) {
+        const unsigned q_slots = (a.q.num_heads + kRows - 1) / kRows, slots = q_slots + (a.k.num_heads + kRows - 1) / kRows;
+        const long long most = (0xFFFFFFFFLL / 32 - kRopeThreads) / (static_cast<long long>(slots) * (a.d / N));  // 32-bit threads
+        for (long long i = 0; i < a.num_tokens; i += most) {
+            const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
+            const PartialWarps w = partial_warps(a, N, in_place(a), n * slots);
+            const unsigned blocks = static_cast<unsigned>((w.all * 32 + kRopeThreads - 1) / kRopeThreads);
+            const cudaError_t e = launch_pdl(rope_partial_kernel<T, kRows>, dim3(blocks), dim3(kRopeThreads), 0, stream, a, w.lanes,
+                                             static_cast<unsigned>(w.turning), q_slots, slots, static_cast<int>(i));
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
+    static cudaError_t any(const RotateArgs& a, bool vec, cudaStream_t stream) {
+        const unsigned pair_items = static_cast<unsigned>((a.rotary / 2 + kPairRun - 1) / kPairRun);
+        const unsigned items = pair_items + (in_place(a) || a.rotary == a.d ? 0u : static_cast<unsigned>((a.d + N - 1) / N - a.rotary / N));
+        const long long per_token = static_cast<long long>(items) * (a.q.num_heads + a.k.num_heads);
+        const long long most = (0xFFFFFFFFLL - kRopeThreads) / per_token;  // thread indexes are 32 bits wide
+        for (long long i = 0; i < a.num_tokens; i += most) {
+            const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
+            const unsigned blocks = static_cast<unsigned>((n * per_token + kRopeThreads - 1) / kRopeThreads);
+            const cudaError_t e = launch_pdl(rope_any_kernel<T>, dim3(blocks), dim3(kRopeThreads), 0, stream, a, pair_items, items,
+                                             vec, static_cast<int>(i));
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
     static cudaError_t go(const RotateArgs& a, cudaStream_t stream) {
-        if (vectors_fit(a)) return a.interleaved ? by_rows<false>(a, stream) : by_rows<true>(a, stream);
-        dim3 grid;
-        const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * (a.q.num_heads + a.k.num_heads) *
-                                          (a.d - a.rotary / 2), &grid);
-        return e != cudaSuccess ? e : launch_pdl(rope_scalar_kernel<T>, grid, dim3(256), 0, stream, a);
+        const bool vec = rows_fit(a);
+        if (vec && a.rotary % (a.interleaved ? N : 2 * N) == 0 && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0)
+            return a.interleaved ? by_rows<false>(a, stream) : by_rows<true>(a, stream);
+        if (vec && (a.rotary + N - 1) / N <= 32) {
+            const long long one = static_cast<long long>(a.num_tokens) * (a.q.num_heads + a.k.num_heads) *
+                                  (in_place(a) ? (a.rotary + N - 1) / N : a.d / N);
+            return one >= 4 * kBusyThreads ? partial<4>(a, stream) : partial<1>(a, stream);
+        }
+        return any(a, vec, stream);
     }
 };
 

@@ -242,7 +242,8 @@ def test_load_blocks_and_copy_blocks(fmt, hkv, d):
 @pytest.mark.parametrize("hq,hkv,d,r,layout,where", [
     (8, 2, 64, 64, "half", "packed"), (8, 2, 64, 32, "half", "in place"), (12, 3, 128, 128, "half", "in place"),
     (5, 1, 128, 48, "interleaved", "packed"), (6, 6, 64, 64, "interleaved", "in place"),
-    (16, 1, 128, 96, "half", "alternating"), (6, 2, 128, 18, "half", "in place")])
+    (16, 1, 128, 96, "half", "alternating"), (6, 2, 128, 18, "half", "in place"),
+    (5, 1, 64, 16, "half", "packed"), (9, 3, 64, 50, "half", "alternating"), (6, 2, 128, 22, "interleaved", "in place")])
 def test_append_of_many_tokens_is_the_append_of_few(fmt, hq, hkv, d, r, layout, where):
     """One call of so many tokens that q gets blocks of its own, against calls of 500:
     the same bits in pools and q_out, padding, bad positions, bad blocks and a ring

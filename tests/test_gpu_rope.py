@@ -35,7 +35,8 @@ def check(got, x, cs, pos, layout, inverse=False):
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("tokens,hq,hkv,d,r", [
     (1, 1, 0, 64, 64), (5, 8, 2, 64, 32), (33, 32, 8, 128, 128), (7, 3, 1, 128, 64), (9, 5, 2, 80, 80),
-    (4, 2, 2, 96, 18), (3, 2, 1, 6, 2), (2, 4, 1, 512, 512), (17, 7, 7, 128, 16), (301, 16, 4, 128, 96)])
+    (4, 2, 2, 96, 18), (3, 2, 1, 6, 2), (2, 4, 1, 512, 512), (17, 7, 7, 128, 16), (301, 16, 4, 128, 96),
+    (5, 2, 1, 512, 18), (11, 3, 2, 256, 250), (29, 5, 1, 8, 6)])
 def test_rotation(dtype, layout, tokens, hq, hkv, d, r):
     gen = torch.Generator().manual_seed(tokens * d + r)
     cs, t = table(1e4, r, 777, kind="linear", factor=2.0)
@@ -57,8 +58,9 @@ def test_rotation(dtype, layout, tokens, hq, hkv, d, r):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("where", ["packed", "head_major", "odd_offset", "broadcast"])
-def test_strides_in_place_and_out(dtype, layout, where):
-    tokens, hq, hkv, d, r = 37, 6, 2, 64, 48
+@pytest.mark.parametrize("r", [48, 18])
+def test_strides_in_place_and_out(dtype, layout, where, r):
+    tokens, hq, hkv, d = 37, 6, 2, 64
     gen = torch.Generator().manual_seed(5)
     cs, t = table(1e4, r, 100)
     pos = torch.randint(0, 100, (tokens,), generator=gen).int()
@@ -184,7 +186,7 @@ def test_offsets_past_32_bits():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
-@pytest.mark.parametrize("hq,hkv,d,r", [(32, 8, 128, 128), (5, 3, 128, 64), (9, 0, 96, 32)])
+@pytest.mark.parametrize("hq,hkv,d,r", [(32, 8, 128, 128), (5, 3, 128, 64), (9, 0, 96, 32), (6, 2, 64, 18)])
 def test_many_rows_are_turned_as_few_are(dtype, layout, hq, hkv, d, r):
     """So many rows that a thread takes four heads (heads that are no multiple of four,
     passing dims, padding and bad positions included), against calls of few tokens."""
