@@ -1,10 +1,13 @@
 """Attention over a paged KV cache, hand-written CUDA for GB300 (sm_103a).
 
-A thin ctypes binding over ``libpkv.so`` (C ABI in ``include/pkv.h``).  Each
+A thin binding over ``libpkv.so`` (C ABI in ``include/pkv.h``).  Each
 function carries the C entry point's name and only marshals arguments: torch
 tensors become pointers (device memory, or pinned host memory where the C
 declaration allows it), the current torch stream becomes the launch stream,
-and a non-OK status raises :class:`PkvError` with the library's message.  Every step of the computation runs in the library's kernels; if the
+and a non-OK status raises :class:`PkvError` with the library's message.  The
+calls go through ctypes, those on rotary positions and quantised pools through
+an extension module that first checks each tensor's type, device, shape and
+layout.  Every step of the computation runs in the library's kernels; if the
 library is missing the call fails loudly -- there is no fallback.
 
 PyTorch is used here for device memory and streams only.

@@ -37,15 +37,16 @@
 // l and O are fp32.
 //
 // What bounds it.  Per token and KV head it reads 2 (D + 4) bytes (int8) or 2 (D/2 + D/16)
-// (4-bit) for 4 D G flops: HBM by the roofline.  int8 gets there (one steady wave:
-// 5.9-6.2 TB/s).  A 4-bit block of D = 128 is 2304 bytes and costs a warp about 270
-// instructions beside 16 MMAs, which hold the issue port for 8 cycles each (an MMA with 4
-// independent FMAs measured 11.7 cycles, alone 8.0): some 400 issue cycles where HBM
-// delivers a block every 404.  So one steady wave runs at 6.0 TB/s, its compute alone (all
-// blocks from L2) at 6.08 and its copies alone at 6.9.  Tried and dropped: one bulk copy
-// per record (5.49 TB/s: a copy's issue costs a warp more than 5 per-lane ones), one block
-// per pass (5.60), 5 or 6 CTAs per SM (5.49, 4.07: the port, not latency, is short),
-// 8-warp CTAs (long batch 462 us, 426 with 4 warps).
+// (4-bit) for 4 D G flops: HBM by the roofline.  int8 gets there (76 sequences x 8 KV heads
+// of 512 blocks, one steady wave: 6.18 TB/s at D = 128, 5.98 at 64; its copies alone 6.58
+// and 6.50).  A 4-bit block of D = 128 is 2304 bytes and costs a warp about 264 instructions
+// beside 16 MMAs, which hold the issue port for 8 cycles each (an MMA with 4 independent
+// FMAs measured 11.7 cycles, alone 8.0): some 390 issue cycles where HBM delivers a block
+// every 404.  So one steady wave runs at 6.20 TB/s and its copies alone at 6.89; at D = 64,
+// half the bytes for more than half the instructions, at 5.12 and 6.18.  Tried and dropped:
+// one bulk copy per record (5.49 TB/s where this was 6.01: a copy's issue costs a warp more
+// than 5 per-lane ones), one block per pass (5.60), 5 or 6 CTAs per SM (5.49, 4.07: the port,
+// not latency, is short), 8-warp CTAs (long batch 462 us, 426 with 4 warps).
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
