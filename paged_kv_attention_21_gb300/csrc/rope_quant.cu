@@ -657,43 +657,54 @@ __device__ __forceinline__ void widen_row(const RowPart<D, kFp4>& p, float g, fl
     }
 }
 
-// D/8 lanes per (token, head), K and V of it in one thread.
-template <int D, bool kFp4>
-__global__ void __launch_bounds__(256) quant_read_kernel(const __grid_constant__ QuantArgs a) {
+// D/8 lanes per token and kRows heads, K and V of them in one thread: four heads where there
+// are many rows, for fewer waves of the chain position, block id, row (4096 tokens of 8
+// heads of 128, 4-bit: 6.0 us with one, 5.3 with two, 4.8 with four; 16384 tokens 24.4,
+// 20.7, 18.8; below the bound, 4096 tokens of 8 heads of 64: 6.2 with one, 6.7 with two).
+// Blocks of 128 threads took the 4.8 to 4.45, and left the calls with one head a thread.
+constexpr int read_threads(int rows) { return rows > 1 ? 128 : 256; }
+
+template <int D, bool kFp4, int kRows>
+__global__ void __launch_bounds__(read_threads(kRows)) quant_read_kernel(const __grid_constant__ QuantArgs a, unsigned slots) {
     pdl_wait();
     constexpr int kLanes = D / 8;
     const int lane = threadIdx.x % kLanes;
-    const long long group = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+    const long long group = static_cast<long long>(blockIdx.x) * (read_threads(kRows) / kLanes) + threadIdx.x / kLanes;
     // groups past 32 bits divide as 64-bit numbers
-    const long long i = group <= 0xFFFFFFFFLL ? static_cast<unsigned>(group) / static_cast<unsigned>(a.hkv) : group / a.hkv;
-    const int h = static_cast<int>(group - i * a.hkv);
+    const long long i = group <= 0xFFFFFFFFLL ? static_cast<unsigned>(group) / slots : group / slots;
+    const int h0 = static_cast<int>(group - i * slots) * kRows;
     if (i >= a.num_tokens) return;
     const int s = a.token_to_seq[i], p = a.positions[i], row = p % kBlockSize;
-    const bool report = lane == 0 && h == 0;
+    const bool report = lane == 0 && h0 == 0;
     if (!quant_token(a, s, p, report)) return;
     const int blk = quant_block(a, s, p);
     if (!good_block(a, blk, report)) return;
-    const size_t at = (static_cast<size_t>(blk) * a.hkv + h) * QuantRecord<D, kFp4>::kBytes;
-    RowPart<D, kFp4> part[2];
+    const size_t at = (static_cast<size_t>(blk) * a.hkv + h0) * QuantRecord<D, kFp4>::kBytes;
+    RowPart<D, kFp4> part[2][kRows];
 #pragma unroll
-    for (int pool = 0; pool < 2; ++pool)
-        if (pool ? a.v_out : a.k_out)
-            part[pool] = fetch_row<D, kFp4>(static_cast<const uint8_t*>(pool ? a.v_pool : a.k_pool) + at, row, lane);
-    const size_t to = (static_cast<size_t>(i) * a.hkv + h) * D + 8 * lane;
+    for (int n = 0; n < kRows; ++n)
 #pragma unroll
-    for (int pool = 0; pool < 2; ++pool) {
-        void* dst = pool ? a.v_out : a.k_out;
-        if (!dst) continue;
-        float v[8];
-        widen_row<D, kFp4>(part[pool], kFp4 ? (pool ? a.v_scale : a.k_scale)[h] : 1.f, v);
-        if (a.out_f32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + to);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + to) = pack<__nv_bfloat16>(v);
+        for (int pool = 0; pool < 2; ++pool)
+            if ((pool ? a.v_out : a.k_out) && h0 + n < a.hkv)
+                part[pool][n] = fetch_row<D, kFp4>(static_cast<const uint8_t*>(pool ? a.v_pool : a.k_pool) + at +
+                                                       n * QuantRecord<D, kFp4>::kBytes, row, lane);
+    const size_t to = (static_cast<size_t>(i) * a.hkv + h0) * D + 8 * lane;
+#pragma unroll
+    for (int n = 0; n < kRows; ++n)
+#pragma unroll
+        for (int pool = 0; pool < 2; ++pool) {
+            void* dst = pool ? a.v_out : a.k_out;
+            if (!dst || h0 + n >= a.hkv) continue;
+            float v[8];
+            widen_row<D, kFp4>(part[pool][n], kFp4 ? (pool ? a.v_scale : a.k_scale)[h0 + n] : 1.f, v);
+            if (a.out_f32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + to + n * D);
+                o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + to + n * D) = pack<__nv_bfloat16>(v);
+            }
         }
-    }
 }
 
 // A CTA per (pair, kHeads heads): thread (row, lane) widens 8 dims of each of
@@ -732,13 +743,6 @@ __global__ void __launch_bounds__(2 * D) quant_load_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------- launches --
-
-cudaError_t grid_of(long long threads, dim3* grid) {
-    const long long blocks = (threads + 255) / 256;
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    *grid = dim3(static_cast<unsigned>(blocks));
-    return cudaSuccess;
-}
 
 constexpr long long kMixedThreads = 3 << 16;
 constexpr long long kBusyThreads = 152LL * 512;  // 16 warps an SM: enough to give a thread more rows
@@ -822,10 +826,17 @@ struct AppendLaunch {
 };
 template <int D, bool kFp4>
 struct ReadLaunch {
+    template <int kRows>
+    static cudaError_t rows(const QuantArgs& a) {
+        const unsigned slots = static_cast<unsigned>((a.hkv + kRows - 1) / kRows);
+        constexpr int kThreads = read_threads(kRows);
+        const long long blocks = (static_cast<long long>(a.num_tokens) * slots * (D / 8) + kThreads - 1) / kThreads;
+        if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+        return launch_pdl(quant_read_kernel<D, kFp4, kRows>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, a.stream, a, slots);
+    }
     static cudaError_t go(const QuantArgs& a) {
-        dim3 grid;
-        const cudaError_t e = grid_of(static_cast<long long>(a.num_tokens) * a.hkv * (D / 8), &grid);
-        return e != cudaSuccess ? e : launch_pdl(quant_read_kernel<D, kFp4>, grid, dim3(256), 0, a.stream, a);
+        if (static_cast<long long>(a.num_tokens) * a.hkv * (D / 8) >= 4 * kBusyThreads) return rows<4>(a);
+        return rows<1>(a);
     }
 };
 template <int D, bool kFp4>

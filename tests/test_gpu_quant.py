@@ -334,6 +334,43 @@ def test_load_of_many_blocks_is_the_load_of_few(fmt, hkv, d):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hkv,d,out", [(3, 128, torch.float32), (8, 64, torch.bfloat16), (5, 128, torch.bfloat16)])
+def test_read_of_many_rows_is_the_read_of_few(fmt, hkv, d, out):
+    """So many rows that a thread takes four heads (groups of four left incomplete too),
+    the same row twice, padding, bad positions and blocks among them."""
+    gen = torch.Generator().manual_seed(d + hkv)
+    n, nb, mbps, seqs = 4 * 152 * 512 // (hkv * d // 8) + 13, 61, 7, 9
+    pools = [torch.randint(0, 256, (nb, hkv, Q.record_bytes(fmt, d)), generator=gen, dtype=torch.uint8) for _ in range(2)]
+    for p in pools:  # scales that are numbers
+        at = p[..., 16 * Q.row_bytes(fmt, d):]
+        at.copy_(torch.rand(nb, hkv, 16, generator=gen).view(torch.uint8) if fmt == "int8" else at % 0x7F)
+    pools = [p.to(DEV) for p in pools]
+    tables = torch.randint(0, nb, (seqs, mbps), generator=gen).int()
+    tables[2, 3], tables[4, 0] = nb, -1
+    tts = torch.randint(0, seqs, (n,), generator=gen).int()
+    pos = torch.randint(0, 16 * mbps, (n,), generator=gen).int()
+    tts[[3, n // 2]], tts[9], pos[11], pos[n - 1] = -1, seqs, -4, 16 * mbps
+    tables, tts, pos = tables.to(DEV), tts.to(DEV), pos.to(DEV)
+    g = torch.rand(hkv, generator=gen).to(DEV) + 0.01 if fmt == "fp4" else None
+    dd = desc_of(fmt, hkv, hkv, d, nb, mbps)
+
+    def run(step, which=(0, 1)):
+        outs = [torch.full((n, hkv, d), 7.0, dtype=out, device=DEV) for _ in range(2)]
+        for i in range(0, n, step):
+            at = slice(i, i + step)
+            pkv.pkv_quant_read(dd, pools[0] if 0 in which else None, pools[1] if 1 in which else None, tables, tts[at],
+                               pos[at], outs[0][at] if 0 in which else None, outs[1][at] if 1 in which else None,
+                               k_scale=g, v_scale=g)
+        assert pkv.pkv_device_errors() == pkv.DEVERR_POSITION | pkv.DEVERR_BLOCK_ID
+        return outs
+    few = run(300)
+    many = run(n)
+    assert torch.equal(many[0], few[0]) and torch.equal(many[1], few[1])
+    assert torch.all(few[0][torch.tensor([3, 9, 11, n // 2, n - 1], device=DEV)] == 7)
+    assert torch.equal(run(n, (1,))[1], few[1]) and torch.equal(run(n, (0,))[0], few[0])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
 def test_the_binding_refuses_tensors_that_do_not_fit(fmt):
     hq, hkv, d, nb, mbps, n = 8, 2, 64, 4, 2, 3
     dd = desc_of(fmt, hq, hkv, d, nb, mbps)
