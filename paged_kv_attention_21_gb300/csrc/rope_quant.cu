@@ -347,14 +347,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_con
 // --------------------------------------------------------------- append --
 //
 // D/16 lanes per row, two vectors of 8 dims each: a rotation's pair of vectors where the
-// pairs are half-split, so that every byte and every (cos, sin) is read once.  A thread's
-// rows are kRows query, K or V heads of one token.
+// pairs are half-split, so that every byte and every (cos, sin) is read once.
 //
-// The quantisation takes some 500 instructions per warp and 512 values, so that K and V
-// of 4096 tokens of 8 heads of 128 (21 MB) take 9.8 us in a replayed graph where HBM would
-// take 3.2, and with 32 rotated q heads (88 MB) 20.4 where it would take 13.0.  32 dims a
-// lane, which halves the instructions, took 8.6 and 20.3, but the 16 heads' rows of 256
-// tokens 3.1 us instead of 2.6, and 999 tokens of 64 + 8 heads of 64 5.8 instead of 4.3.
+// The quantisation takes some 470 instructions per warp and 512 values, so that K and V
+// of 4096 tokens of 8 heads of 128 (21 MB) take 8.9 us in a replayed graph where HBM would
+// take 3.2, and with 32 rotated q heads (88 MB) 20 where it would take 13.0.  32 dims a
+// lane, which halves the instructions, were tried when those took 9.8 and 20.4: 8.6 and
+// 20.3, but K and V of 256 tokens 3.1 us instead of 2.6, and 999 tokens of 64 + 8 heads of
+// 64 5.8 instead of 4.3.
 
 // The sequence and position of a token: false for padding and, flagged by `report`,
 // for a bad one.
@@ -438,59 +438,39 @@ __device__ __forceinline__ void store_row(uint8_t* rec, int row, int lane, int c
 // multiple of 16, a lane's 16 dims all inside the rotary dims or all outside.
 enum Pairs { kAnyPairs, kHalfPairs, kLanePairs };
 
-template <int D, bool kFp4, int kRows, int kPairs>
-__device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, unsigned q_slots, unsigned kv_slots,
-                                            int first_token) {
+template <int D, bool kFp4, int kPairs, int kThreads>
+__device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, int first_token) {
     using R = QuantRecord<D, kFp4>;
     constexpr int kLanes = D / 16;
     const int lane = threadIdx.x % kLanes;
-    const unsigned group = block * (blockDim.x / kLanes) + threadIdx.x / kLanes;
-    const unsigned slots = q_slots + 2 * kv_slots;
-    const unsigned token = group / slots;
-    unsigned slot = group - token * slots;
+    const unsigned group = block * (kThreads / kLanes) + threadIdx.x / kLanes, slots = 2u * static_cast<unsigned>(a.hkv);
+    const unsigned token = group / slots, slot = group - token * slots;
     const long long i = first_token + static_cast<long long>(token);
-    // a thread's rows are query, K or V heads h0 .. h0 + rows - 1
-    const bool is_q = slot < q_slots;
-    const bool report = lane == 0 && slot == 0, report_block = lane == 0 && slot == q_slots;
-    if (!is_q) slot -= q_slots;
-    const bool is_v = !is_q && slot >= kv_slots;
-    if (is_v) slot -= kv_slots;
-    const int h0 = static_cast<int>(slot) * kRows;
-    const int rows = min(kRows, (is_q ? a.hq : a.hkv) - h0);
+    const bool is_v = slot >= static_cast<unsigned>(a.hkv), report = lane == 0 && slot == 0;
+    const int h = static_cast<int>(is_v ? slot - a.hkv : slot);
     const int half = a.rotary / 2;
     // the lane's vectors
     const int turning = a.rotary / 16;  // lanes that rotate (vector paths)
     const bool split = kPairs == kHalfPairs && !is_v && lane < turning;
     const int c0 = split ? lane : 2 * lane, c1 = split ? lane + turning : c0 + 1;
     const bool rope = a.cos_sin != nullptr && !is_v && (kPairs == kAnyPairs ? 8 * c0 < a.rotary : lane < turning);
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_q ? a.q : is_v ? a.v_new : a.k_new) +
-                               i * (is_q ? a.q_stride : a.new_stride) + h0 * D;
-    // the rows' loads do not wait for the token's position, nor the rotation for its
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? a.v_new : a.k_new) + i * a.new_stride + h * D;
+    // the row's loads do not wait for the token's position, nor the rotation for its
     // block.  Every lane stays to the end: rows share shuffles with their warp.
-    uint4 x[kRows][2];
+    uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
     const bool in = i < a.num_tokens;
     int s = -1, p = 0;
+    float g = 1.f;  // 4-bit: the head's scale
     if (in) {
         s = a.token_to_seq[i];
         p = a.positions[i];
-    }
-#pragma unroll
-    for (int n = 0; n < kRows; ++n) {
-        x[n][0] = x[n][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (in && n < rows) {
-            x[n][0] = *reinterpret_cast<const uint4*>(src + n * D + 8 * c0);
-            x[n][1] = *reinterpret_cast<const uint4*>(src + n * D + 8 * c1);
-        }
-    }
-    float g[kRows];  // 4-bit: the heads' scales
-#pragma unroll
-    for (int n = 0; n < kRows; ++n) {
-        g[n] = 1.f;
-        if (kFp4 && in && !is_q && n < rows) g[n] = (is_v ? a.v_scale : a.k_scale)[h0 + n];
+        x0 = *reinterpret_cast<const uint4*>(src + 8 * c0);
+        x1 = *reinterpret_cast<const uint4*>(src + 8 * c1);
+        if (kFp4) g = (is_v ? a.v_scale : a.k_scale)[h];
     }
     const bool ok = in && quant_token(a, s, p, report);
     int blk = 0;  // looked at after the rotation, whose loads are then in flight beside it
-    if (ok && !is_q) blk = quant_block(a, s, p);
+    if (ok) blk = quant_block(a, s, p);
     // (cos, sin) of the lane's pairs: 8 on the vector paths (of c0 with c1, or of the 16
     // dims), else one per dim
     constexpr int kCs = kPairs == kAnyPairs ? 16 : 8;
@@ -523,94 +503,101 @@ __device__ __forceinline__ void append_rows(const QuantArgs& a, unsigned block, 
             for (int e = 0; e < kCs; ++e) sn[e] = -sn[e];
         }
     }
-    __syncwarp();  // q in place: the rows' lanes have read their vectors
-    __nv_bfloat16* q_out = static_cast<__nv_bfloat16*>(a.q_out) + i * a.q_out_stride + h0 * D;
+    float v0[8], v1[8];
+    unpack<__nv_bfloat16>(x0, v0);
+    unpack<__nv_bfloat16>(x1, v1);
+    if (ok && rope) {
+        if constexpr (kPairs == kHalfPairs) {
 #pragma unroll
-    for (int n = 0; n < kRows; ++n) {
-        const bool live = ok && n < rows;
-        float v0[8], v1[8];
-        unpack<__nv_bfloat16>(x[n][0], v0);
-        unpack<__nv_bfloat16>(x[n][1], v1);
-        if (live && rope) {
-            if constexpr (kPairs == kHalfPairs) {
+            for (int e = 0; e < 8; ++e) {
+                const float2 z = turn(v0[e], v1[e], c[e], sn[e]);
+                v0[e] = z.x;
+                v1[e] = z.y;
+            }
+        } else if constexpr (kPairs == kLanePairs) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 z = turn(v0[e], v1[e], c[e], sn[e]);
-                    v0[e] = z.x;
-                    v1[e] = z.y;
-                }
-            } else if constexpr (kPairs == kLanePairs) {
+            for (int e = 0; e < 8; e += 2) {
+                const float2 z0 = turn(v0[e], v0[e + 1], c[e / 2], sn[e / 2]);
+                const float2 z1 = turn(v1[e], v1[e + 1], c[4 + e / 2], sn[4 + e / 2]);
+                v0[e] = z0.x;
+                v0[e + 1] = z0.y;
+                v1[e] = z1.x;
+                v1[e + 1] = z1.y;
+            }
+        } else if (a.interleaved) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 z0 = turn(v0[e], v0[e + 1], c[e / 2], sn[e / 2]);
-                    const float2 z1 = turn(v1[e], v1[e + 1], c[4 + e / 2], sn[4 + e / 2]);
-                    v0[e] = z0.x;
-                    v0[e + 1] = z0.y;
-                    v1[e] = z1.x;
-                    v1[e + 1] = z1.y;
-                }
-            } else if (a.interleaved) {
+            for (int e = 0; e < 16; e += 2) {
+                if (8 * c0 + e >= a.rotary) continue;
+                float* v = e < 8 ? v0 + e : v1 + (e - 8);
+                const float2 z = turn(v[0], v[1], c[e], sn[e]);
+                v[0] = z.x;
+                v[1] = z.y;
+            }
+        } else {
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    if (8 * c0 + e >= a.rotary) continue;
-                    float* v = e < 8 ? v0 + e : v1 + (e - 8);
-                    const float2 z = turn(v[0], v[1], c[e], sn[e]);
-                    v[0] = z.x;
-                    v[1] = z.y;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int d = 8 * c0 + e;
-                    if (d >= a.rotary) continue;
-                    const bool b = d >= half;
-                    const float m = __bfloat162float(src[n * D + (b ? d - half : d + half)]);
-                    float& v = e < 8 ? v0[e] : v1[e - 8];
-                    v = b ? turn(m, v, c[e], sn[e]).y : turn(v, m, c[e], sn[e]).x;
-                }
+            for (int e = 0; e < 16; ++e) {
+                const int d = 8 * c0 + e;
+                if (d >= a.rotary) continue;
+                const float m = __bfloat162float(src[d >= half ? d - half : d + half]);
+                float& v = e < 8 ? v0[e] : v1[e - 8];
+                v = d >= half ? turn(m, v, c[e], sn[e]).y : turn(v, m, c[e], sn[e]).x;
             }
         }
-        if constexpr (kPairs == kAnyPairs) __syncwarp();  // q in place: the row's lanes have read their partners
-        if (live && is_q) {
-            *reinterpret_cast<uint4*>(q_out + n * D + 8 * c0) = pack<__nv_bfloat16>(v0);
-            *reinterpret_cast<uint4*>(q_out + n * D + 8 * c1) = pack<__nv_bfloat16>(v1);
-        }
-        // a warp's rows may be of different kinds: the shuffles are for all of them, the
-        // stores for K and V rows
-        const bool kv = ok && !is_q && n < rows && good_block(a, blk, report_block && n == 0);
-        uint8_t* rec = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(blk) * a.hkv + h0) * R::kBytes;
-        if (__any_sync(0xFFFFFFFFu, kv))
-            store_row<D, kFp4>(rec + n * R::kBytes, p % kBlockSize, lane, c0, c1, split, v0, v1, g[n], kv);
     }
+    const bool stored = ok && good_block(a, blk, report);
+    uint8_t* rec = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(blk) * a.hkv + h) * R::kBytes;
+    if (__any_sync(0xFFFFFFFFu, stored)) store_row<D, kFp4>(rec, p % kBlockSize, lane, c0, c1, split, v0, v1, g, stored);
 }
 
-template <int D, bool kFp4, int kRows, int kPairs>
-__global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(const __grid_constant__ QuantArgs a, unsigned q_slots,
-                                                           unsigned kv_slots, int first_token) {
-    pdl_wait();  // dependents start as its CTAs leave: triggered here they took the slots of its last waves
-    append_rows<D, kFp4, kRows, kPairs>(a, blockIdx.x, q_slots, kv_slots, first_token);
-}
-
-// Many tokens: blocks that rotate q as the rotation's kernel does (four heads a thread,
-// bound by HBM) evenly among blocks that quantise K and V (bound by instruction issue),
-// so that each SM runs both.
 template <int D, bool kFp4, int kPairs>
-__global__ void __launch_bounds__(kRopeThreads, 16) quant_append_mixed_kernel(const __grid_constant__ QuantArgs a,
-                                                                    const __grid_constant__ RotateArgs r, unsigned vectors,
-                                                                    unsigned lanes, unsigned turn_warps, unsigned q_slots, unsigned q_blocks,
-                                                                    unsigned kv_slots, unsigned blocks) {
+__global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(const __grid_constant__ QuantArgs a, int first_token) {
+    pdl_wait();  // dependents start as its CTAs leave: triggered here they took the slots of its last waves
+    append_rows<D, kFp4, kPairs, kAppendThreads>(a, blockIdx.x, first_token);
+}
+
+// With q: blocks that rotate it as the rotation's kernels do (four heads a thread, bound
+// by HBM) beside blocks that quantise K and V (bound by instruction issue).  While the whole
+// call is a few waves, K and V go first, whose chain of loads and work is the longer; beyond,
+// the two kinds alternate evenly, so that each SM runs both (4-bit, 32 + 8 heads of 128, K and
+// V first against alternating: 1024 tokens 5.5 and 5.7 us, 4096 tokens 19.8 and 19.9, 16384
+// tokens 71.0 and 67.4; 64 + 8 heads of 64: 1024 tokens 4.1 and 4.8).  Heads of q as rows
+// beside those of K and V took 2.4 instead of 2.2 us for 16 tokens, 3.1 instead of 2.75 for 256, 6.7
+// instead of 5.5 for 1024, 23.6 instead of 19.9 for 4096.  Where q's pairs are looked up a thread
+// takes two heads (18 of 128 dims, 16 + 4 heads, 4096 tokens: 17.1 us, 24.8 with four heads, whose
+// registers spill, 20.8 with one).
+constexpr int kPartialHeads = 2;
+
+struct MixPlan {
+    unsigned vectors;           // of a q row that a thread of rotate_vectors takes one of,
+    unsigned lanes, turn_warps;  // or rotate_partial's, where lanes > 0
+    unsigned q_slots, q_blocks, blocks;
+    bool kv_first;
+};
+
+template <int D, bool kFp4, int kPairs>
+__global__ void __launch_bounds__(kRopeThreads, 16) quant_append_q_kernel(const __grid_constant__ QuantArgs a,
+                                                                              const __grid_constant__ RotateArgs r, MixPlan m,
+                                                                              int first_token) {
     pdl_wait();
-    // of the first b blocks, b q_blocks / blocks rotate
-    const unsigned before = static_cast<unsigned>(static_cast<uint64_t>(blockIdx.x) * q_blocks / blocks);
-    const unsigned after = static_cast<unsigned>((static_cast<uint64_t>(blockIdx.x) + 1) * q_blocks / blocks);
+    const unsigned kv_blocks = m.blocks - m.q_blocks;
+    // q blocks among the first blockIdx.x, and among one more
+    unsigned before, after;
+    if (m.kv_first) {
+        before = blockIdx.x < kv_blocks ? 0 : blockIdx.x - kv_blocks;
+        after = blockIdx.x < kv_blocks ? 0 : before + 1;
+    } else {
+        before = static_cast<unsigned>(static_cast<uint64_t>(blockIdx.x) * m.q_blocks / m.blocks);
+        after = static_cast<unsigned>((static_cast<uint64_t>(blockIdx.x) + 1) * m.q_blocks / m.blocks);
+    }
     if (after > before) {
         const unsigned thread = before * kRopeThreads + threadIdx.x;
-        if (kPairs == kAnyPairs && lanes)
-            rotate_partial<__nv_bfloat16, 4>(r, thread / 32u, lanes, turn_warps, q_slots, q_slots, 0);
+        if (kPairs == kAnyPairs && m.lanes)
+            rotate_partial<__nv_bfloat16, kPartialHeads>(r, thread / 32u, m.lanes, m.turn_warps, m.q_slots, m.q_slots, first_token);
         else
-            rotate_vectors<__nv_bfloat16, kPairs != kLanePairs, 4>(r, thread, vectors, q_slots, q_slots, 0);
-    } else
-        append_rows<D, kFp4, 1, kPairs>(a, blockIdx.x - before, 0, kv_slots, 0);
+            rotate_vectors<__nv_bfloat16, kPairs != kLanePairs, 4>(r, thread, m.vectors, m.q_slots, m.q_slots, first_token);
+    } else {
+        append_rows<D, kFp4, kPairs, kRopeThreads>(a, blockIdx.x - before, first_token);
+    }
 }
 
 // ----------------------------------------------------------------- read --
@@ -744,7 +731,7 @@ __global__ void __launch_bounds__(2 * D) quant_load_kernel(const __grid_constant
 
 // ------------------------------------------------------------- launches --
 
-constexpr long long kMixedThreads = 3 << 16;
+constexpr long long kFewWaves = 1 << 25;         // an append's elements of q, K and V
 constexpr long long kBusyThreads = 152LL * 512;  // 16 warps an SM: enough to give a thread more rows
 
 template <template <int, bool> class F>
@@ -755,35 +742,28 @@ cudaError_t by_format(const QuantArgs& a) {
 
 template <int D, bool kFp4>
 struct AppendLaunch {
-    template <int kRows, int kPairs>
-    static cudaError_t rows(const QuantArgs& a) {
-        constexpr int kPerBlock = kAppendThreads / (D / 16);
-        const unsigned q_slots = a.q ? (a.hq + kRows - 1) / kRows : 0, kv_slots = (a.hkv + kRows - 1) / kRows;
-        const long long slots = q_slots + 2LL * kv_slots;
-        const long long most = (0xFFFFFFFFLL - kPerBlock) / slots;  // group indexes are 32 bits wide
+    // launches of as many tokens as 32-bit thread indexes reach
+    template <typename F>
+    static cudaError_t runs(const QuantArgs& a, long long threads_per_token, F launch) {
+        const long long most = (0xFFFFFFFFLL / 2) / threads_per_token;
         for (long long i = 0; i < a.num_tokens; i += most) {
-            const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
-            const cudaError_t e = launch_pdl(quant_append_kernel<D, kFp4, kRows, kPairs>,
-                                             dim3(static_cast<unsigned>((n * slots + kPerBlock - 1) / kPerBlock)),
-                                             dim3(kAppendThreads), 0,
-                                             a.stream, a, q_slots, kv_slots, static_cast<int>(i));
+            const cudaError_t e = launch(static_cast<int>(i), a.num_tokens - i < most ? a.num_tokens - i : most);
             if (e != cudaSuccess) return e;
         }
         return cudaSuccess;
     }
     template <int kPairs>
     static cudaError_t pairs(const QuantArgs& a) {
-        const long long n = static_cast<long long>(a.num_tokens) * (2 * a.hkv + (a.q ? a.hq : 0)) * (D / 16);
-        if (a.cos_sin) {
-            // (4-bit, 32 + 8 heads of 128: 4096 tokens 23.2 us through the kernel above and 19.8
-            // mixed, 512 tokens 4.3 and 3.6, 256 tokens 3.1 and 2.9, 64 tokens 2.6 both; 64 + 8
-            // heads of 64: 512 tokens, just below this bound, 3.4 and 3.6)
-            if (a.q && n >= kMixedThreads && n < 0x7FFFFFFFLL) return mixed<kPairs>(a);
-        }
-        return rows<1, kPairs>(a);
+        const long long kv_threads = 2LL * a.hkv * (D / 16);
+        if (a.q) return with_q<kPairs>(a, kv_threads);
+        return runs(a, kv_threads, [&](int first, long long n) {
+            return launch_pdl(quant_append_kernel<D, kFp4, kPairs>,
+                              dim3(static_cast<unsigned>((n * kv_threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0,
+                              a.stream, a, first);
+        });
     }
     template <int kPairs>
-    static cudaError_t mixed(const QuantArgs& a) {
+    static cudaError_t with_q(const QuantArgs& a, long long kv_threads) {
         RotateArgs r{};
         r.q = RotateRows{a.q, a.q_out, a.q_stride, D, a.q_out_stride, D, a.hq};
         r.cos_sin = a.cos_sin;
@@ -799,22 +779,29 @@ struct AppendLaunch {
         r.num_seqs = a.num_seqs;
         r.mbps = a.mbps;
         r.ring = a.ring;
-        constexpr int kPerBlock = kRopeThreads / (D / 16);
         // q's pairs: as vectors, half-split with r a multiple of 16 too, or looked up in the row
         const bool whole = kPairs != kAnyPairs ||
                            (!a.interleaved && a.rotary % 16 == 0 && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0);
-        const unsigned vectors = static_cast<unsigned>((kPairs != kLanePairs ? a.rotary / 2 : a.rotary) / 8 +
-                                                       (a.q == a.q_out ? 0 : (D - a.rotary) / 8));
-        const unsigned q_slots = (a.hq + 3) / 4, kv_slots = a.hkv;
-        const uint64_t tokens = static_cast<uint64_t>(a.num_tokens);
-        const PartialWarps w = partial_warps(r, 8, a.q == a.q_out, static_cast<long long>(tokens * q_slots));
-        const uint64_t q_threads = whole ? tokens * q_slots * vectors : static_cast<uint64_t>(w.all) * 32;
-        const unsigned q_blocks = static_cast<unsigned>((q_threads + kRopeThreads - 1) / kRopeThreads);
-        const unsigned kv_blocks = static_cast<unsigned>((tokens * 2 * kv_slots + kPerBlock - 1) / kPerBlock);
-        QuantArgs kv = a;
-        kv.q = nullptr;
-        return launch_pdl(quant_append_mixed_kernel<D, kFp4, kPairs>, dim3(q_blocks + kv_blocks), dim3(kRopeThreads), 0, a.stream, kv, r,
-                          vectors, whole ? 0u : w.lanes, static_cast<unsigned>(w.turning), q_slots, q_blocks, kv_slots, q_blocks + kv_blocks);
+        const bool in_place = a.q == a.q_out;
+        const long long q_slots = whole ? (a.hq + 3) / 4 : (a.hq + kPartialHeads - 1) / kPartialHeads;
+        const long long vectors = (kPairs != kLanePairs ? a.rotary / 2 : a.rotary) / 8 + (in_place ? 0 : (D - a.rotary) / 8);
+        return runs(a, kv_threads + q_slots * (D / 8) + 32, [&](int first, long long n) {
+            MixPlan m{};
+            m.q_slots = static_cast<unsigned>(q_slots);
+            long long q_threads = n * q_slots * vectors;
+            if (whole) {
+                m.vectors = static_cast<unsigned>(vectors);
+            } else {
+                const PartialWarps w = partial_warps(r, 8, in_place, n * q_slots);
+                m.lanes = w.lanes;
+                m.turn_warps = static_cast<unsigned>(w.turning);
+                q_threads = w.all * 32;
+            }
+            m.q_blocks = static_cast<unsigned>((q_threads + kRopeThreads - 1) / kRopeThreads);
+            m.blocks = m.q_blocks + static_cast<unsigned>((n * kv_threads + kRopeThreads - 1) / kRopeThreads);
+            m.kv_first = n * (2LL * a.hkv + a.hq) * D < kFewWaves;
+            return launch_pdl(quant_append_q_kernel<D, kFp4, kPairs>, dim3(m.blocks), dim3(kRopeThreads), 0, a.stream, a, r, m, first);
+        });
     }
     static cudaError_t go(const QuantArgs& a) {
         if (a.cos_sin && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0) {
