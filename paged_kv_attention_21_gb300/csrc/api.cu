@@ -1717,7 +1717,14 @@ namespace {
 //   * a ragged batch averages about half its longest context: chunks aim for one wave
 //     of resident CTAs, at most 128 blocks, or 256 from 4 waves of such chunks on (960
 //     pairs of up to 2048 blocks: 544 us with 64-block chunks, 488, 470 and 480 with
-//     128, 256 and 512, before the merge left the kernel);
+//     128, 256 and 512, before the merge left the kernel).  A pair's last chunk is half
+//     empty on average: that is taken off the wave while it is less than a quarter of it
+//     (128 pairs of up to 252 blocks: 18.0 us with 32-block chunks, 17.0 with 40; 256 of up
+//     to 128: 19.8 and 18.0; 416 of up to 188: 30.5 with 40, 32.5 with the 64 that this
+//     would give);
+//   * at most 128 blocks stay one chunk where the pairs alone fill 0.8 of the wave (512
+//     pairs of 63 to 128 blocks: 31.2 us, 36.3 in 64-block chunks; 960 of up to 125: 40.4 and
+//     43.2; of 188 blocks 496 pairs took 40.0 and 34.5);
 //   * at least 8 blocks, a pass of each warp, and at most 64 chunks (2 pairs of 256
 //     blocks: 5.9 us with 8-block chunks, 7.9 with 32; 8 pairs of 2048: 21.6 us with
 //     8, 15.4 with 16, 13.0 with 32);
@@ -1741,11 +1748,14 @@ pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_c
     if (chunk <= 0) {
         auto whole = [](int blocks) { return (blocks + 7) / 8 * 8; };  // a pass of each warp
         const int cap = pairs * (0.55 * mb / 256 + 0.5) >= 4.0 * slots ? 256 : 128;
-        const double wave = pairs * std::max(1.0, 0.55 * mb) / slots;
+        const double room = pairs < 0.45 * slots ? slots - 0.5 * pairs : slots;  // less half a chunk of each pair's last
+        const double wave = pairs * std::max(1.0, 0.55 * mb) / room;
         chunk = whole(std::max((mb + 63) / 64, int(std::ceil(std::min(wave, double(cap))))));
         const int eighth = whole((mb + 7) / 8);
         const double ctas = pairs * ((mb + eighth - 1) / eighth);
-        if (mb <= 48)
+        if (pairs >= 0.8 * slots && mb <= 128)
+            chunk = mb;
+        else if (mb <= 48)
             chunk = ctas <= 0.4 * slots && mb >= 32 ? eighth : mb;
         else if (chunk < eighth && ctas > 0.25 * slots && ctas <= 0.5 * slots)
             chunk = eighth;
