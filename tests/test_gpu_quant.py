@@ -624,6 +624,26 @@ def test_decode_most_chunks(fmt, hq, hkv, d):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("chunk", [0, 1])
+def test_decode_most_sequences(fmt, chunk):
+    """65535 sequences share the blocks of a few; their neighbours' lengths differ, some are
+    empty or below zero (taken as empty)."""
+    rng = np.random.default_rng(1)
+    hq, hkv, d, n = 3, 1, 64, 65535
+    c = Q.QuantCase(rng, fmt, [32, 32, 27, 16, 1, 0], hq, hkv, d, poison=False)
+    pick = rng.integers(0, 6, n)
+    q = rng.standard_normal((64, hq, d))
+    c.q = Q.bf16(q)[rng.integers(0, 64, n)]
+    c.tables, c.lens = c.tables[pick], c.lens[pick]
+    c.lens[7], c.lens[n - 1] = -1, -2 ** 31
+    got = run_decode(c, chunk=chunk, max_len=32)
+    for s in (7, n - 1):
+        assert not np.any(got[0][s]) and np.all(np.isneginf(got[1][s]))
+    check_decode(c, got, seqs=[s for s in list(range(0, n, 1009)) + [1, 2, 3, n - 2] if c.lens[s] >= 0])
+    assert pkv.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
 @pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
 @pytest.mark.parametrize("hq,hkv", [(4, 1), (11, 1)])
 def test_decode_a_query_head_that_is_not_finite_spoils_no_other(fmt, bad, hq, hkv):
