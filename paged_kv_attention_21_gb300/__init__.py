@@ -422,23 +422,9 @@ def _checked():
     return _marshal
 
 
-_torch = None   # the module, once a call has needed it
-_have_cuda = False
-
-
-def _here(stream):
-    """(the current device's index, the launch stream's address); without a CUDA
-    device an index that no tensor has."""
-    global _torch, _have_cuda
-    if not _have_cuda:
-        import torch
-        _torch, _have_cuda = torch, torch.cuda.is_available()
-        if not _have_cuda:
-            return -2, None
-    device = _torch.cuda.current_device()
-    if stream is None:
-        return device, _torch._C._cuda_getCurrentRawStream(device)  # current_stream() builds an object: 1 us
-    return device, stream if isinstance(stream, int) else stream.cuda_stream
+def _address(stream):
+    """A launch stream's address; None stands for torch's current stream."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def make_rope(cos_sin, rotary_dim=None, layout="half", inverse=False) -> Rope:
@@ -455,10 +441,10 @@ def make_rope(cos_sin, rotary_dim=None, layout="half", inverse=False) -> Rope:
         rotary_dim = 2 * cos_sin.shape[1]
     if rotary_dim != 2 * cos_sin.shape[1]:
         raise ValueError("rotary_dim %d, but the table has %d pairs" % (rotary_dim, cos_sin.shape[1]))
-    device, _ = _here(None)
     if str(cos_sin.dtype) != "torch.float32" or not cos_sin.is_contiguous():
         raise ValueError("cos_sin: dtype %s, expected contiguous torch.float32" % cos_sin.dtype)
-    if cos_sin.get_device() != device:
+    import torch
+    if not cos_sin.is_cuda or cos_sin.get_device() != torch.cuda.current_device():
         raise ValueError("cos_sin: on %s, expected the current CUDA device" % cos_sin.device)
     r = Rope(cos_sin.data_ptr(), int(rotary_dim), layouts[layout], int(cos_sin.shape[0]),
              ROPE_INVERSE if inverse else 0)
@@ -491,8 +477,7 @@ def pkv_rope_rotate(rope, positions, q, q_out=None, k=None, k_out=None, stream=N
     head strides) of q and k at int32 positions; without an out, in place.
     With make_rope(..., inverse=True) it is the rotation's transpose: the
     gradient of q from the gradient of its rotated rows."""
-    device, stream = _here(stream)
-    _check(_checked().rope_rotate(rope, positions, q, q_out, k, k_out, device, stream))
+    _check(_checked().rope_rotate(rope, positions, q, q_out, k, k_out, _address(stream)))
 
 
 def pkv_quant_cache_bytes(desc: CacheDesc) -> int:
@@ -512,8 +497,7 @@ def pkv_quant_append(desc, k_pool, v_pool, block_tables, token_to_seq, positions
     """Quantise the new tokens' K (rotated) and V into their slots, and rotate q
     into q_out (None: in place).  k_new, v_new and q may be views into one packed
     QKV buffer.  token_to_seq < 0 marks a padding token."""
-    device, stream = _here(stream)
-    _check(_checked().quant_append(desc, k_pool, v_pool, k_scale, v_scale, device, stream, rope,
+    _check(_checked().quant_append(desc, k_pool, v_pool, k_scale, v_scale, _address(stream), rope,
                                    block_tables, token_to_seq, positions, k_new, v_new, q, q_out))
 
 
@@ -521,8 +505,7 @@ def pkv_quant_read(desc, k_pool, v_pool, block_tables, token_to_seq, positions, 
                    v_out=None, k_scale=None, v_scale=None, stream=None):
     """Read the rows at (token_to_seq, positions) back as bf16 or fp32
     [tokens][Hkv][D]; either output may be None."""
-    device, stream = _here(stream)
-    _check(_checked().quant_read(desc, k_pool, v_pool, k_scale, v_scale, device, stream, block_tables,
+    _check(_checked().quant_read(desc, k_pool, v_pool, k_scale, v_scale, _address(stream), block_tables,
                                  token_to_seq, positions, k_out, v_out))
 
 
@@ -530,8 +513,7 @@ def pkv_quant_load_blocks(desc, k_pool, v_pool, src_blocks, dst_blocks, k_cache,
                           k_scale=None, v_scale=None, stream=None):
     """Block dst_blocks[i] of the bf16 pools [blocks][Hkv][16][D] receives the
     values of block src_blocks[i] of the quantised pools."""
-    device, stream = _here(stream)
-    _check(_checked().quant_load_blocks(desc, k_pool, v_pool, k_scale, v_scale, device, stream,
+    _check(_checked().quant_load_blocks(desc, k_pool, v_pool, k_scale, v_scale, _address(stream),
                                         src_blocks, dst_blocks, k_cache, v_cache))
 
 
@@ -544,8 +526,7 @@ def pkv_quant_decode(desc, q, k_pool, v_pool, block_tables, context_lens, max_co
                      out, lse=None, workspace=None, window=-1, chunk_blocks=0, k_scale=None,
                      v_scale=None, sinks=None, stream=None):
     """Decode attention (one query token per sequence) over quantised pools."""
-    device, stream = _here(stream)
-    _check(_checked().quant_decode(desc, k_pool, v_pool, k_scale, v_scale, device, stream, q,
+    _check(_checked().quant_decode(desc, k_pool, v_pool, k_scale, v_scale, _address(stream), q,
                                    block_tables, context_lens, max_context_len, sm_scale, window,
                                    sinks, chunk_blocks, out, lse, workspace))
 
