@@ -165,7 +165,13 @@ __global__ void __launch_bounds__(kRopeThreads, 16) rope_vector_kernel(const __g
     rotate_vectors<T, kHalf, kRows>(a, blockIdx.x * kRopeThreads + threadIdx.x, vectors, q_slots, slots, first_token);
 }
 
-// Rows of vectors whose rotary dims are not: the first `turn_warps` warps turn the vectors
+// The warps of rotate_partial: those that turn, then those that copy.
+struct PartialWarps {
+    unsigned lanes;  // vectors of a row that hold rotary dims
+    unsigned turning, all;
+};
+
+// Rows of vectors whose rotary dims are not: the first `turning` warps turn the vectors
 // that hold rotary dims, `lanes` a row, a row's lanes in one warp (32 / lanes units of kRows
 // heads), each looking its elements' partners up in the row -- with interleaved pairs they
 // are its own -- before any lane of the warp stores, so that in place is safe.  The other
@@ -175,11 +181,12 @@ __global__ void __launch_bounds__(kRopeThreads, 16) rope_vector_kernel(const __g
 // vectors' lanes in the turning warps, 12.9 with partners from shuffles, 36.6 with a thread
 // per pair and per passing element.
 template <typename T, int kRows>
-__device__ __forceinline__ void rotate_partial(const RotateArgs& a, unsigned warp, unsigned lanes, unsigned turn_warps,
-                                               unsigned q_slots, unsigned slots, int first_token) {
+__device__ __forceinline__ void rotate_partial(const RotateArgs& a, unsigned warp, const PartialWarps& w, unsigned q_slots,
+                                               unsigned slots, int first_token) {
     constexpr int N = 16 / sizeof(T);
-    const unsigned lane = threadIdx.x % 32u;
-    const bool turns = warp < turn_warps;
+    if (warp >= w.all) return;
+    const unsigned lane = threadIdx.x % 32u, lanes = w.lanes;
+    const bool turns = warp < w.turning;
     unsigned rest, v;  // the unit, and the vector of its rows
     bool live = true;
     if (turns) {
@@ -188,7 +195,7 @@ __device__ __forceinline__ void rotate_partial(const RotateArgs& a, unsigned war
         rest = warp * units + unit;
         v = lane - unit * lanes;
     } else {
-        const unsigned passing = static_cast<unsigned>(a.d) / N - lanes, idx = (warp - turn_warps) * 32u + lane;
+        const unsigned passing = static_cast<unsigned>(a.d) / N - lanes, idx = (warp - w.turning) * 32u + lane;
         rest = idx / passing;
         v = lanes + idx - rest * passing;
     }
@@ -262,27 +269,20 @@ __device__ __forceinline__ void rotate_partial(const RotateArgs& a, unsigned war
         if (r < rows) *reinterpret_cast<uint4*>(out + r * out_head) = x[r];
 }
 
-// Its warps: those that turn, and with those that copy.
-struct PartialWarps {
-    unsigned lanes;
-    long long turning, all;
-};
-PartialWarps partial_warps(const RotateArgs& a, int n, bool in_place, long long slots) {
-    PartialWarps w;
-    w.lanes = static_cast<unsigned>((a.rotary + n - 1) / n);
-    const long long units = 32 / w.lanes, passing = a.d / n - w.lanes;
-    w.turning = (slots + units - 1) / units;
-    w.all = w.turning + (in_place ? 0 : (slots * passing + 31) / 32);
-    return w;
+// Of n elements a vector, for `units` groups of rows (the caller bounds them).
+PartialWarps partial_warps(const RotateArgs& a, int n, bool in_place, long long units) {
+    const long long lanes = (a.rotary + n - 1) / n, per_warp = 32 / lanes, passing = in_place ? 0 : a.d / n - lanes;
+    const long long turning = (units + per_warp - 1) / per_warp;
+    return PartialWarps{static_cast<unsigned>(lanes), static_cast<unsigned>(turning),
+                        static_cast<unsigned>(turning + (units * passing + 31) / 32)};
 }
 
 template <typename T, int kRows>
-__global__ void __launch_bounds__(kRopeThreads) rope_partial_kernel(const __grid_constant__ RotateArgs a, unsigned lanes,
-                                                                    unsigned turn_warps, unsigned q_slots, unsigned slots,
-                                                                    int first_token) {
+__global__ void __launch_bounds__(kRopeThreads) rope_partial_kernel(const __grid_constant__ RotateArgs a, const PartialWarps w,
+                                                                    unsigned q_slots, unsigned slots, int first_token) {
     pdl_wait();
     pdl_launch_dependents();
-    rotate_partial<T, kRows>(a, (blockIdx.x * kRopeThreads + threadIdx.x) / 32u, lanes, turn_warps, q_slots, slots, first_token);
+    rotate_partial<T, kRows>(a, (blockIdx.x * kRopeThreads + threadIdx.x) / 32u, w, q_slots, slots, first_token);
 }
 
 // Rows that start on no 16-byte boundary, are not whole vectors or are longer than a warp's:
@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(const __gr
 constexpr int kPartialHeads = 2;
 
 struct MixPlan {
-    unsigned vectors;           // of a q row that a thread of rotate_vectors takes one of,
-    unsigned lanes, turn_warps;  // or rotate_partial's, where lanes > 0
+    unsigned vectors;  // of a q row that a thread of rotate_vectors takes one of, or 0
+    PartialWarps w;    // and rotate_partial's
     unsigned q_slots, q_blocks, blocks;
     bool kv_first;
 };
@@ -591,8 +591,8 @@ __global__ void __launch_bounds__(kRopeThreads, 16) quant_append_q_kernel(const 
     }
     if (after > before) {
         const unsigned thread = before * kRopeThreads + threadIdx.x;
-        if (kPairs == kAnyPairs && m.lanes)
-            rotate_partial<__nv_bfloat16, kPartialHeads>(r, thread / 32u, m.lanes, m.turn_warps, m.q_slots, m.q_slots, first_token);
+        if (kPairs == kAnyPairs && m.vectors == 0)
+            rotate_partial<__nv_bfloat16, kPartialHeads>(r, thread / 32u, m.w, m.q_slots, m.q_slots, first_token);
         else
             rotate_vectors<__nv_bfloat16, kPairs != kLanePairs, 4>(r, thread, m.vectors, m.q_slots, m.q_slots, first_token);
     } else {
@@ -734,6 +734,24 @@ __global__ void __launch_bounds__(2 * D) quant_load_kernel(const __grid_constant
 constexpr long long kFewWaves = 1 << 25;         // an append's elements of q, K and V
 constexpr long long kBusyThreads = 152LL * 512;  // 16 warps an SM: enough to give a thread more rows
 
+// Launches over as many tokens as 32-bit thread indexes reach: launch(args, first token, tokens),
+// with args that end at the launch's last token, so that none is taken twice.
+template <typename Args, typename F>
+cudaError_t token_runs(const Args& a, long long threads_per_token, F launch) {
+    const long long most = (1LL << 31) / threads_per_token;
+    if (most == 0) return cudaErrorInvalidValue;
+    for (long long i = 0; i < a.num_tokens; i += most) {
+        const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
+        Args run = a;
+        run.num_tokens = static_cast<int32_t>(i + n);
+        const cudaError_t e = launch(run, static_cast<int>(i), n);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+dim3 blocks_of(long long threads, int per_block) { return dim3(static_cast<unsigned>((threads + per_block - 1) / per_block)); }
+
 template <template <int, bool> class F>
 cudaError_t by_format(const QuantArgs& a) {
     if (a.d == 64) return a.fp4 ? F<64, true>::go(a) : F<64, false>::go(a);
@@ -742,24 +760,13 @@ cudaError_t by_format(const QuantArgs& a) {
 
 template <int D, bool kFp4>
 struct AppendLaunch {
-    // launches of as many tokens as 32-bit thread indexes reach
-    template <typename F>
-    static cudaError_t runs(const QuantArgs& a, long long threads_per_token, F launch) {
-        const long long most = (0xFFFFFFFFLL / 2) / threads_per_token;
-        for (long long i = 0; i < a.num_tokens; i += most) {
-            const cudaError_t e = launch(static_cast<int>(i), a.num_tokens - i < most ? a.num_tokens - i : most);
-            if (e != cudaSuccess) return e;
-        }
-        return cudaSuccess;
-    }
     template <int kPairs>
     static cudaError_t pairs(const QuantArgs& a) {
         const long long kv_threads = 2LL * a.hkv * (D / 16);
         if (a.q) return with_q<kPairs>(a, kv_threads);
-        return runs(a, kv_threads, [&](int first, long long n) {
-            return launch_pdl(quant_append_kernel<D, kFp4, kPairs>,
-                              dim3(static_cast<unsigned>((n * kv_threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0,
-                              a.stream, a, first);
+        return token_runs(a, kv_threads, [&](const QuantArgs& run, int first, long long n) {
+            return launch_pdl(quant_append_kernel<D, kFp4, kPairs>, blocks_of(n * kv_threads, kAppendThreads), dim3(kAppendThreads), 0,
+                              a.stream, run, first);
         });
     }
     template <int kPairs>
@@ -785,22 +792,21 @@ struct AppendLaunch {
         const bool in_place = a.q == a.q_out;
         const long long q_slots = whole ? (a.hq + 3) / 4 : (a.hq + kPartialHeads - 1) / kPartialHeads;
         const long long vectors = (kPairs != kLanePairs ? a.rotary / 2 : a.rotary) / 8 + (in_place ? 0 : (D - a.rotary) / 8);
-        return runs(a, kv_threads + q_slots * (D / 8) + 32, [&](int first, long long n) {
+        return token_runs(a, kv_threads + q_slots * (D / 8 + 32), [&](const QuantArgs& run, int first, long long n) {
+            r.num_tokens = run.num_tokens;
             MixPlan m{};
             m.q_slots = static_cast<unsigned>(q_slots);
             long long q_threads = n * q_slots * vectors;
             if (whole) {
                 m.vectors = static_cast<unsigned>(vectors);
             } else {
-                const PartialWarps w = partial_warps(r, 8, in_place, n * q_slots);
-                m.lanes = w.lanes;
-                m.turn_warps = static_cast<unsigned>(w.turning);
-                q_threads = w.all * 32;
+                m.w = partial_warps(r, 8, in_place, n * q_slots);
+                q_threads = 32LL * m.w.all;
             }
-            m.q_blocks = static_cast<unsigned>((q_threads + kRopeThreads - 1) / kRopeThreads);
-            m.blocks = m.q_blocks + static_cast<unsigned>((n * kv_threads + kRopeThreads - 1) / kRopeThreads);
+            m.q_blocks = blocks_of(q_threads, kRopeThreads).x;
+            m.blocks = m.q_blocks + blocks_of(n * kv_threads, kRopeThreads).x;
             m.kv_first = n * (2LL * a.hkv + a.hq) * D < kFewWaves;
-            return launch_pdl(quant_append_q_kernel<D, kFp4, kPairs>, dim3(m.blocks), dim3(kRopeThreads), 0, a.stream, a, r, m, first);
+            return launch_pdl(quant_append_q_kernel<D, kFp4, kPairs>, dim3(m.blocks), dim3(kRopeThreads), 0, a.stream, run, r, m, first);
         });
     }
     static cudaError_t go(const QuantArgs& a) {
@@ -854,15 +860,10 @@ struct RotateLaunch {
     static cudaError_t vectors(const RotateArgs& a, int count, cudaStream_t stream) {
         const unsigned q_slots = (a.q.num_heads + kRows - 1) / kRows, slots = q_slots + (a.k.num_heads + kRows - 1) / kRows;
         const long long per_token = static_cast<long long>(count) * slots;
-        const long long most = (0xFFFFFFFFLL - 256) / per_token;  // thread indexes are 32 bits wide
-        for (long long i = 0; i < a.num_tokens; i += most) {
-            const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
-            const unsigned blocks = static_cast<unsigned>((n * per_token + kRopeThreads - 1) / kRopeThreads);
-            const cudaError_t e = launch_pdl(rope_vector_kernel<T, kHalf, kRows>, dim3(blocks), dim3(kRopeThreads), 0, stream, a,
-                                             static_cast<unsigned>(count), q_slots, slots, static_cast<int>(i));
-            if (e != cudaSuccess) return e;
-        }
-        return cudaSuccess;
+        return token_runs(a, per_token, [&](const RotateArgs& run, int first, long long n) {
+            return launch_pdl(rope_vector_kernel<T, kHalf, kRows>, blocks_of(n * per_token, kRopeThreads), dim3(kRopeThreads), 0, stream,
+                              run, static_cast<unsigned>(count), q_slots, slots, first);
+        });
     }
     template <bool kHalf>
     static cudaError_t by_rows(const RotateArgs& a, cudaStream_t stream) {
@@ -874,30 +875,20 @@ struct RotateLaunch {
     template <int kRows>
     static cudaError_t partial(const RotateArgs& a, cudaStream_t stream) {
         const unsigned q_slots = (a.q.num_heads + kRows - 1) / kRows, slots = q_slots + (a.k.num_heads + kRows - 1) / kRows;
-        const long long most = (0xFFFFFFFFLL / 32 - kRopeThreads) / (static_cast<long long>(slots) * (a.d / N));  // 32-bit threads
-        for (long long i = 0; i < a.num_tokens; i += most) {
-            const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
+        return token_runs(a, static_cast<long long>(slots) * (a.d / N + 32), [&](const RotateArgs& run, int first, long long n) {
             const PartialWarps w = partial_warps(a, N, in_place(a), n * slots);
-            const unsigned blocks = static_cast<unsigned>((w.all * 32 + kRopeThreads - 1) / kRopeThreads);
-            const cudaError_t e = launch_pdl(rope_partial_kernel<T, kRows>, dim3(blocks), dim3(kRopeThreads), 0, stream, a, w.lanes,
-                                             static_cast<unsigned>(w.turning), q_slots, slots, static_cast<int>(i));
-            if (e != cudaSuccess) return e;
-        }
-        return cudaSuccess;
+            return launch_pdl(rope_partial_kernel<T, kRows>, blocks_of(32LL * w.all, kRopeThreads), dim3(kRopeThreads), 0, stream, run, w,
+                              q_slots, slots, first);
+        });
     }
     static cudaError_t any(const RotateArgs& a, bool vec, cudaStream_t stream) {
         const unsigned pair_items = static_cast<unsigned>((a.rotary / 2 + kPairRun - 1) / kPairRun);
         const unsigned items = pair_items + (in_place(a) || a.rotary == a.d ? 0u : static_cast<unsigned>((a.d + N - 1) / N - a.rotary / N));
         const long long per_token = static_cast<long long>(items) * (a.q.num_heads + a.k.num_heads);
-        const long long most = (0xFFFFFFFFLL - kRopeThreads) / per_token;  // thread indexes are 32 bits wide
-        for (long long i = 0; i < a.num_tokens; i += most) {
-            const long long n = a.num_tokens - i < most ? a.num_tokens - i : most;
-            const unsigned blocks = static_cast<unsigned>((n * per_token + kRopeThreads - 1) / kRopeThreads);
-            const cudaError_t e = launch_pdl(rope_any_kernel<T>, dim3(blocks), dim3(kRopeThreads), 0, stream, a, pair_items, items,
-                                             vec, static_cast<int>(i));
-            if (e != cudaSuccess) return e;
-        }
-        return cudaSuccess;
+        return token_runs(a, per_token, [&](const RotateArgs& run, int first, long long n) {
+            return launch_pdl(rope_any_kernel<T>, blocks_of(n * per_token, kRopeThreads), dim3(kRopeThreads), 0, stream, run, pair_items,
+                              items, vec, first);
+        });
     }
     static cudaError_t go(const RotateArgs& a, cudaStream_t stream) {
         const bool vec = rows_fit(a);

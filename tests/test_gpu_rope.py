@@ -36,7 +36,7 @@ def check(got, x, cs, pos, layout, inverse=False):
 @pytest.mark.parametrize("tokens,hq,hkv,d,r", [
     (1, 1, 0, 64, 64), (5, 8, 2, 64, 32), (33, 32, 8, 128, 128), (7, 3, 1, 128, 64), (9, 5, 2, 80, 80),
     (4, 2, 2, 96, 18), (3, 2, 1, 6, 2), (2, 4, 1, 512, 512), (17, 7, 7, 128, 16), (301, 16, 4, 128, 96),
-    (5, 2, 1, 512, 18), (11, 3, 2, 256, 250), (29, 5, 1, 8, 6)])
+    (5, 2, 1, 512, 18), (11, 3, 2, 256, 250), (29, 5, 1, 8, 6), (1, 1, 0, 64, 62), (3, 5, 2, 64, 50)])
 def test_rotation(dtype, layout, tokens, hq, hkv, d, r):
     gen = torch.Generator().manual_seed(tokens * d + r)
     cs, t = table(1e4, r, 777, kind="linear", factor=2.0)
@@ -58,7 +58,7 @@ def test_rotation(dtype, layout, tokens, hq, hkv, d, r):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("where", ["packed", "head_major", "odd_offset", "broadcast"])
-@pytest.mark.parametrize("r", [48, 18])
+@pytest.mark.parametrize("r", [48, 18, 62])
 def test_strides_in_place_and_out(dtype, layout, where, r):
     tokens, hq, hkv, d = 37, 6, 2, 64
     gen = torch.Generator().manual_seed(5)
@@ -215,3 +215,22 @@ def test_many_rows_are_turned_as_few_are(dtype, layout, hq, hkv, d, r):
     assert torch.all(few[padded] == 7)
     few[padded] = x[padded]
     assert torch.equal(run(n, True), few)
+
+
+def test_more_threads_than_one_launch_reaches():
+    """In place, so many rows that they take several launches: each row turns once, those
+    beside the launches' borders included."""
+    tokens, heads = 1_500_000_000, 3
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("40 GB of device memory")
+    cs = torch.tensor([[[1.0, 0.0]], [[0.6, 0.8]]], device=DEV)
+    x = torch.zeros(tokens, heads, 2, dtype=torch.bfloat16, device=DEV)
+    x[..., 0] = 1.0
+    pos = torch.ones(tokens, dtype=torch.int32, device=DEV)
+    pkv.pkv_rope_rotate(pkv.make_rope(cs), pos, x)
+    want = torch.tensor([0.6, 0.8]).bfloat16().view(torch.int32).item()  # a pair's bits
+    pairs = x.view(torch.int32).view(-1)
+    for i in range(0, pairs.numel(), 1 << 29):
+        assert torch.all(pairs[i:i + (1 << 29)] == want), i
+    del x, pos, pairs
+    torch.cuda.empty_cache()
