@@ -47,9 +47,12 @@ __device__ __forceinline__ float finite_magnitude(float x) {
 // smaller quotients become code 0 however they round.  The remainder is taken as q t - x
 // so that a zero keeps its sign.  Rows with NaN, infinities or such t divide one by one.
 // (With a division per value the append of 4096 tokens of 32 + 8 heads of 128 took 36 us.)
-__device__ __forceinline__ void quotients(const float (&x)[8], float t, float (&y)[8]) {
-    const bool plain = t >= 8.077935669463161e-28f && t <= 1.2379400392853803e27f;  // 2^-90, 2^90
-    const float r = __frcp_rn(plain ? t : 1.f);
+__device__ __forceinline__ bool plain_divisor(float t) {
+    return t >= 8.077935669463161e-28f && t <= 1.2379400392853803e27f;  // 2^-90, 2^90
+}
+__device__ __forceinline__ float divisor_reciprocal(float t) { return __frcp_rn(plain_divisor(t) ? t : 1.f); }
+// r: divisor_reciprocal(t)
+__device__ __forceinline__ void quotients(const float (&x)[8], float t, float r, float (&y)[8]) {
     const uint64_t rr = pack_f32x2(r, r), tt = pack_f32x2(t, t), nr = pack_f32x2(-r, -r), m1 = pack_f32x2(-1.f, -1.f);
     uint64_t sums = 0;
 #pragma unroll
@@ -64,7 +67,7 @@ __device__ __forceinline__ void quotients(const float (&x)[8], float t, float (&
     float sum, sum1;
     unpack_f32x2(sums, sum, sum1);
     sum += sum1;
-    if (!plain || sum - sum != 0.f) {  // an infinity's remainder is a NaN, and an overflowed sum is taken along
+    if (!plain_divisor(t) || sum - sum != 0.f) {  // an infinity's remainder is a NaN, and an overflowed sum is taken along
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float q = t > 0.f ? __fdiv_rn(x[e], t) : 0.f;

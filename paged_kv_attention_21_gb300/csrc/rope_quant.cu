@@ -399,12 +399,15 @@ __device__ __forceinline__ void store_row(uint8_t* rec, int row, int lane, int c
     }
     float y0[8], y1[8];
     if constexpr (kFp4) {
-        const float o0 = __shfl_xor_sync(0xFFFFFFFFu, m0, 1), o1 = __shfl_xor_sync(0xFFFFFFFFu, m1, 1);
-        const float own = fmaxf(m0, m1);
-        const uint32_t s0 = fp4_scale_code(split ? fmaxf(m0, o0) : own, g);
-        const uint32_t s1 = split ? fp4_scale_code(fmaxf(m1, o1), g) : s0;
-        quotients(v0, __fmul_rn(e4m3_float(s0), g), y0);
-        quotients(v1, __fmul_rn(e4m3_float(s1), g), y1);
+        // a lane finds one scale: of its own 16 dims, or where they are split, an even lane that
+        // of both c0 vectors and an odd one that of both c1
+        const bool odd = lane & 1;
+        const float theirs = __shfl_xor_sync(0xFFFFFFFFu, odd ? m0 : m1, 1);
+        const uint32_t code = fp4_scale_code(split ? fmaxf(odd ? m1 : m0, theirs) : fmaxf(m0, m1), g);
+        const float t = __fmul_rn(e4m3_float(code), g), r = divisor_reciprocal(t);
+        const float other_t = __shfl_xor_sync(0xFFFFFFFFu, t, 1), other_r = __shfl_xor_sync(0xFFFFFFFFu, r, 1);
+        quotients(v0, split && odd ? other_t : t, split && odd ? other_r : r, y0);
+        quotients(v1, split && !odd ? other_t : t, split && !odd ? other_r : r, y1);
         uint32_t w0 = 0, w1 = 0;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -414,17 +417,15 @@ __device__ __forceinline__ void store_row(uint8_t* rec, int row, int lane, int c
         if (ok) {
             *reinterpret_cast<uint32_t*>(rec + quant_byte<R::kRowBytes>(row, 4 * c0)) = w0;
             *reinterpret_cast<uint32_t*>(rec + quant_byte<R::kRowBytes>(row, 4 * c1)) = w1;
-            uint8_t* sc = rec + R::kScales + row * R::kScaleBytes;
-            if (!split || !(lane & 1)) sc[c0 / 2] = static_cast<uint8_t>(s0);
-            if (split && !(lane & 1)) sc[c1 / 2] = static_cast<uint8_t>(s1);
+            rec[R::kScales + row * R::kScaleBytes + (split && odd ? c1 : c0) / 2] = static_cast<uint8_t>(code);
         }
     } else {
         float amax = fmaxf(m0, m1);
 #pragma unroll
         for (int o = 1; o < D / 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        const float sc = __fdiv_rn(amax, 127.f);
-        quotients(v0, sc, y0);
-        quotients(v1, sc, y1);
+        const float sc = __fdiv_rn(amax, 127.f), r = divisor_reciprocal(sc);
+        quotients(v0, sc, r, y0);
+        quotients(v1, sc, r, y1);
         if (ok) {
             *reinterpret_cast<uint2*>(rec + quant_byte<R::kRowBytes>(row, 8 * c0)) = int8_codes(y0);
             *reinterpret_cast<uint2*>(rec + quant_byte<R::kRowBytes>(row, 8 * c1)) = int8_codes(y1);
