@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_con
 // D/16 lanes per row, two vectors of 8 dims each: a rotation's pair of vectors where the
 // pairs are half-split, so that every byte and every (cos, sin) is read once.
 //
-// The quantisation takes some 470 instructions per warp and 512 values, so that K and V
-// of 4096 tokens of 8 heads of 128 (21 MB) take 8.9 us in a replayed graph where HBM would
+// The quantisation takes some 430 instructions per warp and 512 values, so that K and V
+// of 4096 tokens of 8 heads of 128 (21 MB) take 8.8 us in a replayed graph where HBM would
 // take 3.2, and with 32 rotated q heads (88 MB) 20 where it would take 13.0.  32 dims a
 // lane, which halves the instructions, were tried when those took 9.8 and 20.4: 8.6 and
 // 20.3, but K and V of 256 tokens 3.1 us instead of 2.6, and 999 tokens of 64 + 8 heads of
