@@ -451,8 +451,9 @@ pkv_status pkv_decode_attention_static(const pkv_cache_desc *desc, const void *q
  *   PKV_ROPE_INTERLEAVED: (x[2j], x[2j + 1])   -> (a c - b s, b c + a s)
  * (fp32, each product and sum rounded, then one rounding to the row's type);
  * dims r .. head_dim - 1 pass through.  PKV_ROPE_INVERSE turns by -angle (s
- * negated): the transpose of the rotation, hence its gradient when c^2 + s^2 = 1
- * or not -- dL/dx = inverse(dL/dx') -- and the way to re-base a rotated key. */
+ * negated): the transpose of the rotation, hence its gradient, dL/dx =
+ * inverse(dL/dx'), whether c^2 + s^2 = 1 or not; where it is, also the way back
+ * from a rotated key. */
 #define PKV_ROPE_HALF 0
 #define PKV_ROPE_INTERLEAVED 1
 #define PKV_ROPE_INVERSE 0x1u
