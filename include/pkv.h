@@ -63,7 +63,7 @@ typedef enum {
 typedef enum {
     PKV_KV_BF16 = 0,
     PKV_KV_FP8_E4M3 = 1,
-    PKV_KV_INT8 = 2, /* records with a scale per row: the pkv_quant_* calls and pkv_copy_blocks only */
+    PKV_KV_INT8 = 2, /* records with a scale per row: the pkv_quant_* calls, pkv_copy_blocks, pkv_decode_plan */
     PKV_KV_FP4 = 3   /* records with a scale per 16 dims: likewise */
 } pkv_kv_dtype;
 
@@ -266,7 +266,8 @@ size_t pkv_decode_workspace_size(const pkv_cache_desc *desc, int32_t num_seqs,
 /* ---- a4: the split planner (InferX, "Measured": a kernel launched with too
  * few CTAs cost 3.9x).  Host only.  Chooses the chunk length in whole blocks
  * so that the (sequence, KV head, chunk) CTAs fill the GPU several times
- * over; each sequence then has ceil(visible blocks / chunk) chunks.
+ * over; each sequence then has ceil(visible blocks / chunk) chunks.  A
+ * quantised desc gets the plan of pkv_quant_decode.
  *   num_sms: SM count to plan for (<= 0: the current device's). */
 pkv_status pkv_decode_plan(const pkv_cache_desc *desc, int32_t num_seqs,
                            int32_t max_context_len, int32_t window, int32_t num_sms,

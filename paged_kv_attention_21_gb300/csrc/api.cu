@@ -368,6 +368,14 @@ bool plan_short_query(int max_kv, int max_q, int window, int* chunk_out, int* sp
     return true;
 }
 
+// A quantised pool's decode plan; defined with its entry points.
+struct QuantPlan {
+    int chunk, splits;
+    bool cluster;
+};
+pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_ctx, int window, int num_sms,
+                             int chunk_req, QuantPlan* out);
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct DecodeWs {
@@ -450,7 +458,7 @@ pkv_status pkv_decode_plan(const pkv_cache_desc* desc, int32_t num_seqs, int32_t
                            int32_t window, int32_t num_sms, int32_t* chunk_blocks_out,
                            int32_t* max_splits_out) {
     g_last_error[0] = 0;
-    pkv_status st = check_desc(desc);
+    pkv_status st = check_shape(desc);
     if (st != PKV_OK) return st;
     if (!chunk_blocks_out || !max_splits_out) return fail(PKV_ERR_INVALID_ARG, "null output pointer");
     if (num_seqs < 0 || max_context_len < 1)
@@ -458,6 +466,14 @@ pkv_status pkv_decode_plan(const pkv_cache_desc* desc, int32_t num_seqs, int32_t
     if (num_sms <= 0) {
         st = device_state(nullptr, &num_sms);
         if (st != PKV_OK) return st;
+    }
+    if (quantised(desc)) {
+        QuantPlan plan;
+        st = plan_quant_decode(desc, num_seqs, max_context_len, window, num_sms, 0, &plan);
+        if (st != PKV_OK) return st;
+        *chunk_blocks_out = plan.chunk;
+        *max_splits_out = plan.splits;
+        return PKV_OK;
     }
     int c = 0, s = 0;
     st = plan_decode(desc, num_seqs, max_context_len, window, num_sms, 0, &c, &s);
@@ -1734,10 +1750,6 @@ namespace {
 //     wait for their places: 1024 CTAs on 608 took 22.6 us, 18.8 merged through the
 //     workspace), and a grid of a quarter to half of that takes 8 chunks for it (32 pairs
 //     of 256 blocks: 9.4 us, 10.6 with 16-block chunks merged by the second launch).
-struct QuantPlan {
-    int chunk, splits;
-    bool cluster;
-};
 pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_ctx, int window, int num_sms,
                              int chunk_req, QuantPlan* out) {
     const int mb = max_visible_blocks(max_ctx, window);
