@@ -268,21 +268,28 @@ pkv_status check_quant_desc(const pkv_cache_desc* d, const float* k_scale, const
     return PKV_OK;
 }
 
-// Decode over a ring cache needs a window whose keys the ring holds: the
-// window spans at most ceil((W - 1) / 16) + 1 blocks.  Also the bound on
-// max_context_len: the table capacity, or none with a ring.
+// Tokens that a sequence's table covers, at most the 32 bits of a length.
+int table_tokens(const pkv_cache_desc* d) {
+    return int(std::min<int64_t>(int64_t(d->max_blocks_per_seq) * d->block_size, INT32_MAX));
+}
+
+// Most blocks that a window of W > 0 keys touches: ceil((W - 1) / 16) + 1.  Lengths and
+// windows run to the end of 32 bits: every sum with one is taken in 64.
+int64_t window_blocks(int64_t window) { return (window + 14) / 16 + 1; }
+
+// Decode over a ring cache needs a window whose keys the ring holds.  Also the
+// bound on max_context_len: the table capacity, or none with a ring.
 pkv_status check_ring_window(const pkv_cache_desc* d, int window, int max_context_len) {
     if (d->ring_blocks > 0) {
         if (window <= 0) return fail(PKV_ERR_INVALID_ARG, "a ring cache needs a sliding window");
-        if ((window - 1 + d->block_size - 1) / d->block_size + 1 > d->ring_blocks)
+        if (window_blocks(window) > d->ring_blocks)
             return fail(PKV_ERR_INVALID_ARG, "window %d needs more than ring_blocks = %d blocks", window,
                         d->ring_blocks);
         if (max_context_len < 1) return fail(PKV_ERR_INVALID_ARG, "max_context_len %d < 1", max_context_len);
         return PKV_OK;
     }
-    if (max_context_len < 1 || max_context_len > d->max_blocks_per_seq * d->block_size)
-        return fail(PKV_ERR_INVALID_ARG, "max_context_len %d outside [1, %d]", max_context_len,
-                    d->max_blocks_per_seq * d->block_size);
+    if (max_context_len < 1 || max_context_len > table_tokens(d))
+        return fail(PKV_ERR_INVALID_ARG, "max_context_len %d outside [1, %d]", max_context_len, table_tokens(d));
     return PKV_OK;
 }
 
@@ -291,9 +298,9 @@ int elem_bytes(const pkv_cache_desc* d) { return d->kv_dtype == PKV_KV_FP8_E4M3 
 // ---------------------------------------------------------------- planner --
 
 int max_visible_blocks(int max_ctx, int window) {
-    int mb = (max_ctx + 15) / 16;
-    if (window > 0) mb = std::min(mb, (window + 14) / 16 + 1);
-    return std::max(mb, 1);
+    int64_t mb = (int64_t(max_ctx) + 15) / 16;
+    if (window > 0) mb = std::min(mb, window_blocks(window));
+    return int(std::max<int64_t>(mb, 1));
 }
 
 int resident_ctas(int d, int fp8) {
@@ -359,10 +366,10 @@ pkv_status plan_decode(const pkv_cache_desc* desc, int num_seqs, int max_ctx, in
 // verify and cascade workloads that measured 1.2-1.3x faster than a one-wave
 // plan.  False when the longest KV range does not fit kSqMaxSplits chunks.
 bool plan_short_query(int max_kv, int max_q, int window, int* chunk_out, int* splits_out) {
-    int mb = std::max(1, (max_kv + 15) / 16);
-    if (window > 0) mb = std::min(mb, (window + max_q + 14) / 16 + 1);
-    if (mb > pkv::kSqMaxSplits * pkv::kSqMaxChunk) return false;
-    const int chunk = (mb + pkv::kSqMaxSplits - 1) / pkv::kSqMaxSplits;
+    int64_t blocks = std::max<int64_t>(1, (int64_t(max_kv) + 15) / 16);
+    if (window > 0) blocks = std::min(blocks, window_blocks(int64_t(window) + max_q));
+    if (blocks > pkv::kSqMaxSplits * pkv::kSqMaxChunk) return false;
+    const int mb = int(blocks), chunk = (mb + pkv::kSqMaxSplits - 1) / pkv::kSqMaxSplits;
     *chunk_out = chunk;
     *splits_out = (mb + chunk - 1) / chunk;
     return true;
@@ -710,7 +717,7 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const int32_t
             if (kv_lens_host) {
                 if (kv_lens_host[s] < ql)
                     return fail(PKV_ERR_INVALID_ARG, "sequence %d: kv_len %d < q_len %d", s, kv_lens_host[s], ql);
-                if (kv_lens_host[s] > desc->max_blocks_per_seq * desc->block_size)
+                if (kv_lens_host[s] > table_tokens(desc))
                     return fail(PKV_ERR_INVALID_ARG, "sequence %d: kv_len %d beyond the table", s, kv_lens_host[s]);
             }
         }
@@ -723,7 +730,7 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const int32_t
     // at most 64 query rows (tokens x heads of a group) per sequence: the
     // decode-shaped short-query kernel (needs the host query lengths)
     int sq_chunk = 0, sq_splits = 0;
-    int kv_bound = desc->max_blocks_per_seq * desc->block_size;
+    int kv_bound = table_tokens(desc);
     if (kv_lens_host) {
         kv_bound = 0;
         for (int s2 = 0; s2 < num_seqs; ++s2) kv_bound = std::max(kv_bound, kv_lens_host[s2]);
@@ -803,12 +810,12 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const int32_t
 
 // Staging blocks per sequence of a ring-cache prefill: the chunk's window
 // reaches window - 1 keys before its first token, from a block boundary.
-int ring_stage_cap(int window, int max_q) { return (window - 1 + max_q + 15) / 16 + 1; }
+int64_t ring_stage_cap(int window, int max_q) { return window_blocks(int64_t(window) + max_q); }
 
 struct RingWs {
     size_t tables, lens, k, v, total;
 };
-RingWs ring_ws_layout(const pkv_cache_desc* d, int num_seqs, int cap) {
+RingWs ring_ws_layout(const pkv_cache_desc* d, int num_seqs, int64_t cap) {
     RingWs w{};
     const size_t blocks = size_t(num_seqs) * cap;
     const size_t block_bytes = size_t(d->num_kv_heads) * d->block_size * d->head_dim * 2;
@@ -885,13 +892,13 @@ pkv_status pkv_prefill_ring_commit(const pkv_cache_desc* desc, const void* q, co
         const int lo = std::max(0, kv_lens_host[s] - ql - window + 1);
         stage_lens_host[static_cast<size_t>(s)] = kv_lens_host[s] - (lo - lo % 16);
     }
-    const int cap = ring_stage_cap(window, max_q);
+    const int64_t cap = ring_stage_cap(window, max_q);
     const RingWs ws = ring_ws_layout(desc, num_seqs, cap);
     if (!workspace) return fail(PKV_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", ws.total);
     if (!aligned(workspace, 256)) return fail(PKV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     if (workspace_bytes < ws.total)
         return fail(PKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, ws.total);
-    if (int64_t(num_seqs) * cap > 0x7FFFFFFFLL) return fail(PKV_ERR_UNSUPPORTED, "staging table too large");
+    if (num_seqs * cap > 0x7FFFFFFFLL) return fail(PKV_ERR_UNSUPPORTED, "staging table too large");
     uint32_t* err = nullptr;
     st = device_state(&err, nullptr);
     if (st != PKV_OK) return st;
@@ -918,7 +925,7 @@ pkv_status pkv_prefill_ring_commit(const pkv_cache_desc* desc, const void* q, co
     g.mbps = desc->max_blocks_per_seq;
     g.ring = desc->ring_blocks;
     g.window = window;
-    g.cap = cap;
+    g.cap = int(cap);
     g.fp8 = fp8 ? 1 : 0;
     g.total_q = total_q_tokens;
     g.num_blocks = desc->num_blocks;
@@ -934,8 +941,8 @@ pkv_status pkv_prefill_ring_commit(const pkv_cache_desc* desc, const void* q, co
     pkv_cache_desc staged = *desc;
     staged.kv_dtype = PKV_KV_BF16;
     staged.ring_blocks = 0;
-    staged.num_blocks = static_cast<int64_t>(num_seqs) * cap;
-    staged.max_blocks_per_seq = cap;
+    staged.num_blocks = num_seqs * cap;
+    staged.max_blocks_per_seq = int(cap);
     return prefill_impl(&staged, q, qo_indptr, g.k_stage, g.v_stage, k_scale, v_scale, g.stage_tables,
                         g.stage_lens, num_seqs, total_q_tokens, qo_indptr_host, stage_lens_host.data(),
                         sm_scale, 1, window, out, lse_out, stream, fp8);
@@ -1141,7 +1148,7 @@ pkv_status pkv_cascade_decode(const pkv_cache_desc* desc, const void* q, const v
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
         return fail(PKV_ERR_INVALID_ARG, "q, out and the pools must be 16-byte aligned");
     if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return fail(PKV_ERR_INVALID_ARG, "sm_scale must be finite and > 0");
-    const int cap = desc->max_blocks_per_seq * desc->block_size;
+    const int cap = table_tokens(desc);
     if (max_suffix_len < 1 || max_suffix_len > cap)
         return fail(PKV_ERR_INVALID_ARG, "max_suffix_len %d outside [1, %d]", max_suffix_len, cap);
     if (group_indptr_host[0] != 0 || group_indptr_host[num_groups] != num_seqs)

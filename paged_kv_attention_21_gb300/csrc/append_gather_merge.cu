@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(256) commit_ring_kernel(RingStageArgs a) {
     if (t >= q0 + q_len) return;  // a row past the batch's last sequence
     const int kv_len = a.kv_lens[s];
     const int p = kv_len - q_len + static_cast<int>(t - q0);
-    if (p < 0 || p < kv_len - a.ring * kBlockSize) return;  // overwritten within this chunk
+    if (p < 0 || p < kv_len - static_cast<long long>(a.ring) * kBlockSize) return;  // overwritten within this chunk
     const int entry = (p / kBlockSize) % a.ring;
     const int blk = a.block_tables[static_cast<size_t>(s) * a.mbps + entry];
     if (blk < 0 || blk >= a.num_blocks) {

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return;
     }
     int kv_len = a.kv_lens[seq];
-    const int cap = a.mbps * kBlockSize;
+    const int cap = min(a.mbps, 0x7FFFFFFF / kBlockSize) * kBlockSize;
     if (kv_len > cap) {
         if (threadIdx.x == 0 && blockIdx.x == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
         kv_len = cap;

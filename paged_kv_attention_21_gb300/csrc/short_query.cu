@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kSqThreads) short_query_kernel(const PrefillAr
     const int rows = q_len * G;
     if (q_len <= 0 || 16 * tile >= rows) return;  // no rows in this tile
     int kv_len = a.kv_lens[seq];
-    const int cap = a.mbps * kBlockSize;
+    const int cap = min(a.mbps, 0x7FFFFFFF / kBlockSize) * kBlockSize;
     if (q0 < 0 || q0 + q_len > a.total_q || rows > 16 * a.sq_row_tiles || (a.causal && kv_len < q_len)) {
         if (threadIdx.x == 0 && split == 0 && blockIdx.y == 0) flag_error(a.err, PKV_DEVERR_POSITION);
         return;
