@@ -271,7 +271,7 @@ __device__ __forceinline__ void accumulate(float (&o)[NT][D / 16][4], const uint
 }
 
 // NB consecutive blocks, K and V records of block i at stage + i * kBlock: tok_base is
-// the first one's first position, keys in [lo, hi) take part.  kEdge: some of the blocks'
+// the first one's first position in the chunk, keys in [lo, hi) of it take part.  kEdge: some of the blocks'
 // tokens may lie outside (masking them as they come cost 24 instructions a block in the
 // passes that have none).
 template <int D, bool kFp4, int NT, bool kEdge>
@@ -535,7 +535,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     if (split >= nsplit) return;
     const int b0 = first_blk + split * a.chunk_blocks;
     const int b1 = min(last_blk + 1, b0 + a.chunk_blocks);
-    const int hi = min(ctx, b1 * kBlockSize);
+    // the chunk's visible keys from its first block's first key on: a ring's positions run to
+    // the end of 32 bits, which a pass's own must not pass
+    const int lo_here = max(lo - b0 * kBlockSize, 0);
+    const int hi_here = b1 > last_blk ? ctx - b0 * kBlockSize : (b1 - b0) * kBlockSize;
     // this warp's passes: NB blocks each, warp after warp
     const int passes = ((b1 - b0 + C::NB - 1) / C::NB - warp + kWarps - 1) / kWarps;
 
@@ -636,15 +639,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     // pass i sits in stage i mod kStages; pass i + kStages - 1 goes where pass i - 1
     // was, which every lane has read by the time all are past the __syncwarp
     uint32_t here = 0, next = (C::kStages - 1) * C::kStage;
-    int tok = (b0 + C::NB * warp) * kBlockSize;
+    int tok = C::NB * warp * kBlockSize;
     for (int i = 0; i < passes; ++i) {
         copy_wait<C::kStages - 2>();  // this lane's copies of pass i have landed
         __syncwarp();                 // and every lane's
         load(i + C::kStages - 1, next);
-        if (tok >= lo && tok + C::NB * kBlockSize <= hi)
-            attend<D, kFp4, NT, false>(st, qb, ring + here, lane, tok, lo, hi, sl);
+        if (tok >= lo_here && tok + C::NB * kBlockSize <= hi_here)
+            attend<D, kFp4, NT, false>(st, qb, ring + here, lane, tok, lo_here, hi_here, sl);
         else
-            attend<D, kFp4, NT, true>(st, qb, ring + here, lane, tok, lo, hi, sl);
+            attend<D, kFp4, NT, true>(st, qb, ring + here, lane, tok, lo_here, hi_here, sl);
         tok += kWarps * C::NB * kBlockSize;
         next = here;
         here = here + C::kStage == C::kStages * C::kStage ? 0 : here + C::kStage;

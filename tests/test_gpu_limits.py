@@ -79,3 +79,36 @@ def test_quantised_decode_with_a_window_near_32_bits(fmt, hkv, chunk):
         assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
     assert not torch.any(outs[0][1] == 7) and not torch.any(outs[0][0][4])
     assert pkv.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("hq,d", [(4, 64), (12, 64), (4, 128)])
+def test_quantised_ring_decode_at_the_longest_contexts(fmt, hq, d):
+    """A ring's contexts that end at the last positions of 32 bits: the same keys under a
+    window as contexts that lie whole turns of the ring earlier, hence the same bits."""
+    rng = np.random.default_rng(hq)
+    ring = 16
+    near = np.array([MOST, MOST - 1, MOST - 15, MOST - 16, MOST - 17, MOST - 300], np.int32)
+    early = (near.astype(np.int64) % (16 * ring) + 16 * ring * 3).astype(np.int32)
+    c = Q.QuantCase(rng, fmt, early, hq, 1, d, ring=ring, poison=False)
+    for pool in c.pools:  # slots that no window reaches hold no numbers
+        at = pool[..., 16 * Q.row_bytes(fmt, d):]
+        at = at.view(np.float32) if fmt == "int8" else at.reshape(at.shape[:2] + (16, d // 16))
+        for s, n in enumerate(early):
+            for t in range(n - 16 * ring, n - 100):
+                at[c.tables[s, t // 16 % ring], :, t % 16] = np.nan if fmt == "int8" else 0x7F
+    dd = pkv.make_desc(num_q_heads=hq, num_kv_heads=1, head_dim=d, num_blocks=c.nb, max_blocks_per_seq=c.mbps,
+                       kv_dtype=fmt, ring_blocks=ring)
+    pools, q = [dev(p) for p in c.pools], torch.from_numpy(c.q).bfloat16().to(DEV)
+    for chunk in (0, 1, 3):
+        outs = []
+        for lens in (early, near):
+            ws = torch.zeros(max(256, pkv.pkv_quant_decode_workspace_size(dd, 6, MOST, 100, chunk)),
+                             dtype=torch.uint8, device=DEV)
+            out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device=DEV)
+            pkv.pkv_quant_decode(dd, q, pools[0], pools[1], dev(c.tables), dev(lens), MOST, d ** -0.5, out, lse, ws,
+                                 window=100, chunk_blocks=chunk, k_scale=dev(c.k_scale), v_scale=dev(c.v_scale))
+            outs.append((out, lse))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+        assert torch.all(torch.isfinite(outs[0][1])) and torch.all(torch.isfinite(outs[0][0]))
+    assert pkv.pkv_device_errors() == 0
