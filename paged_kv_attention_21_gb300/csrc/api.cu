@@ -1748,15 +1748,20 @@ namespace {
 //   * at most 128 blocks stay one chunk where the pairs alone fill 0.8 of the wave (512
 //     pairs of 63 to 128 blocks: 31.2 us, 36.3 in 64-block chunks; 960 of up to 125: 40.4 and
 //     43.2; of 188 blocks 496 pairs took 40.0 and 34.5);
-//   * at least 8 blocks, a pass of each warp, and at most 64 chunks (2 pairs of 256
-//     blocks: 5.9 us with 8-block chunks, 7.9 with 32; 8 pairs of 2048: 21.6 us with
-//     8, 15.4 with 16, 13.0 with 32);
+//   * at least 8 blocks, a pass of each warp, and at most 64 chunks while those stay within
+//     the 128 (256) blocks (2 pairs of 256 blocks: 5.9 us with 8-block chunks, 7.9 with 32; 8
+//     pairs of 2048: 21.6 us with 8, 15.4 with 16, 13.0 with 32);
 //   * a context of at most 48 blocks stays one chunk unless half the GPU would idle (128
 //     pairs: 7.3 us in one chunk, 9.9 in six; 8 pairs: 6.5 and 5.6);
 //   * 2..8 chunks merge in a cluster while the whole grid is resident (beyond, clusters
 //     wait for their places: 1024 CTAs on 608 took 22.6 us, 18.8 merged through the
-//     workspace), and a grid of a quarter to half of that takes 8 chunks for it (32 pairs
-//     of 256 blocks: 9.4 us, 10.6 with 16-block chunks merged by the second launch).
+//     workspace), and a grid of a quarter to half of that takes 8 chunks for it while they
+//     are at most 128 blocks (32 pairs of 256 blocks: 9.4 us, 10.6 with 16-block chunks merged
+//     by the second launch; of 1024 blocks 20.0 and, with the wave's 32, 16.2 where lengths
+//     are ragged, 22.1 and 25.1 where they are equal; of 2048 blocks 35.0 and 25.1, 37.2 and
+//     36.0; of 4096 63.0 and 38.5, 67.6 and 58.6; int8 D128 of 4096 75.6 and 56.1, 89.3 and
+//     93.3).
+// Only a context of more than kQuantMaxSplits chunks of kQuantMaxChunk blocks has no plan.
 pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_ctx, int window, int num_sms,
                              int chunk_req, QuantPlan* out) {
     const int mb = max_visible_blocks(max_ctx, window);
@@ -1769,18 +1774,19 @@ pkv_status plan_quant_decode(const pkv_cache_desc* desc, int num_seqs, int max_c
         const int cap = pairs * (0.55 * mb / 256 + 0.5) >= 4.0 * slots ? 256 : 128;
         const double room = pairs < 0.45 * slots ? slots - 0.5 * pairs : slots;  // less half a chunk of each pair's last
         const double wave = pairs * std::max(1.0, 0.55 * mb) / room;
-        chunk = whole(std::max((mb + 63) / 64, int(std::ceil(std::min(wave, double(cap))))));
+        chunk = whole(std::min(cap, std::max((mb + 63) / 64, int(std::ceil(std::min(wave, double(cap)))))));
         const int eighth = whole((mb + 7) / 8);
         const double ctas = pairs * ((mb + eighth - 1) / eighth);
         if (pairs >= 0.8 * slots && mb <= 128)
             chunk = mb;
         else if (mb <= 48)
             chunk = ctas <= 0.4 * slots && mb >= 32 ? eighth : mb;
-        else if (chunk < eighth && ctas > 0.25 * slots && ctas <= 0.5 * slots)
+        else if (chunk < eighth && eighth <= 128 && ctas > 0.25 * slots && ctas <= 0.5 * slots)
             chunk = eighth;
         chunk = std::max(chunk, (mb + pkv::kQuantMaxSplits - 1) / pkv::kQuantMaxSplits);
         chunk = std::min(chunk, mb);
     }
+    // a chunk longer than the most: of kQuantMaxSplits chunks, the planner's only reason for one
     if (chunk > pkv::kQuantMaxChunk || (mb + chunk - 1) / chunk > pkv::kQuantMaxSplits)
         return fail(PKV_ERR_UNSUPPORTED, "context of %d blocks needs more than %d chunks of %d blocks", mb,
                     pkv::kQuantMaxSplits, std::min(chunk, pkv::kQuantMaxChunk));

@@ -1,0 +1,66 @@
+"""Quantised decode over long contexts and long chunks, against 64 bits within a bound that
+a wrong block exceeds (test_quant_bound.py)."""
+import numpy as np
+import pytest
+import torch
+
+import _quant as Q
+import _quant_bound as B
+import paged_kv_attention_21_gb300 as pkv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def dev(x):
+    return None if x is None else torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def decode(p, q, tables, lens, window=-1, chunk=0, ring=0, max_len=None, sinks=None, sm_scale=None):
+    """out, lse as fp64 arrays; the planned call where chunk is 0."""
+    b, hq, d = q.shape
+    dd = pkv.make_desc(num_q_heads=hq, num_kv_heads=p.hkv, head_dim=d, num_blocks=p.nb,
+                       max_blocks_per_seq=tables.shape[1], kv_dtype=p.fmt, ring_blocks=ring)
+    max_len = int(max(lens)) if max_len is None else max_len
+    need = pkv.pkv_quant_decode_workspace_size(dd, b, max_len, window, chunk)
+    ws = torch.zeros(max(256, need), dtype=torch.uint8, device=DEV)
+    qd = torch.from_numpy(q).bfloat16().to(DEV)
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], float("nan"), device=DEV)
+    pkv.pkv_quant_decode(dd, qd, dev(p.raw[0]), dev(p.raw[1]), dev(tables), dev(np.asarray(lens, np.int32)), max_len,
+                         d ** -0.5 if sm_scale is None else sm_scale, out, lse, ws, window=window, chunk_blocks=chunk,
+                         k_scale=dev(p.scales[0]), v_scale=dev(p.scales[1]), sinks=dev(sinks))
+    torch.cuda.synchronize()
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def within(got, ref, tol, what):
+    err = np.abs(got - ref)
+    assert np.all(err <= tol), "%s: %.3g of the bound" % (what, (err / tol).max())
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("b,hkv,group,d,ctx", [(4, 8, 2, 64, 70000), (3, 8, 2, 128, 70000), (15, 1, 12, 128, 131072),
+                                               (1, 1, 4, 64, 600000), (2, 2, 3, 128, 600000)])
+def test_planned_decode_of_long_contexts(fmt, b, hkv, group, d, ctx):
+    """Contexts past 65536 and 524288 tokens with default arguments.  Tables repeat a few
+    blocks, so that the pool stays small: a row counts as often as it stands in the context."""
+    rng = np.random.default_rng(ctx + b)
+    p = B.Pools(rng, fmt, 40, hkv, d)
+    tables = rng.integers(0, p.nb, (b, (ctx + 15) // 16)).astype(np.int32)
+    lens = [int(x) for x in rng.integers(ctx // 2, ctx, b)]
+    lens[0] = ctx - 7
+    q = Q.bf16(rng.standard_normal((b, hkv * group, d)))
+    o, lse = decode(p, q, tables, lens, max_len=ctx)
+    every = np.arange(p.nb)
+    for s in range(b) if b < 5 else (0, 7, b - 1):
+        n = lens[s]
+        copies = np.zeros((p.nb, 16))
+        np.add.at(copies, tables[s, :n // 16], 1)
+        copies[tables[s, n // 16], :n % 16] += 1
+        ro, rl, tol, ltol = B.attention(fmt, q[s].astype(np.float64), p.rows(0, every, 0, 16 * p.nb),
+                                        p.rows(1, every, 0, 16 * p.nb), np.float64(np.float32(d ** -0.5)), 512,
+                                        p.units(every, 0, 16 * p.nb), copies.reshape(-1))
+        within(o[s], ro, tol, "o of sequence %d" % s)
+        within(lse[s], rl, ltol, "lse of sequence %d" % s)
+    assert pkv.pkv_device_errors() == 0
