@@ -624,7 +624,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
                 qb[n][j][i] = pack2<true>(bf16_lo(qb[n][j][i]) * qf, bf16_hi(qb[n][j][i]) * qf);
     float sl = a.sm_scale * 1.4426950408889634f;
     if constexpr (kFp4) sl *= a.k_scale[kvh];
-    sl = ldexpf(sl, qe - 139);
+    // never 0, which would turn a masked logit, -inf, into a NaN
+    sl = fmaxf(ldexpf(sl, qe - 139), 1.401298464324817e-45f);
 
     State<D, NT> st;
 #pragma unroll
