@@ -148,6 +148,9 @@ struct State {
 
 constexpr float kGrow = 8.f;    // logits may exceed mu by this before it moves (2^8 fits f16)
 constexpr float kVGrow = 64.f;  // normalised V scales may reach this (2^8 * 64 fits f16)
+// From logits of this size on every pass rounds them before mu leaves them: fused, the largest
+// would keep what mu's rounding took, up to 2^8 of a logit of 2^32, a weight of 2^256.
+constexpr float kFar = 16777216.f;
 
 // S^T = K Q^T of one block: 16 token slots x 8 NT heads.
 template <int D, bool kFp4, int NT>
@@ -271,20 +274,19 @@ __device__ __forceinline__ void accumulate(float (&o)[NT][D / 16][4], const uint
 }
 
 // NB consecutive blocks, K and V records of block i at stage + i * kBlock: tok_base is
-// the first one's first position in the chunk, keys in [lo, hi) of it take part.  kEdge: some of the blocks'
+// the first one's first position, keys in [lo, hi) take part.  kEdge: some of the blocks'
 // tokens may lie outside (masking them as they come cost 24 instructions a block in the
-// passes that have none).
+// passes that have none), or, 4-bit, the logits may reach kFar.
 template <int D, bool kFp4, int NT, bool kEdge>
 __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2], const uint8_t* stage,
-                                       int lane, int tok_base, int lo, int hi, float sl) {
+                                       int lane, uint32_t tok_base, uint32_t lo, uint32_t hi, float sl) {
     using C = Cfg<D, kFp4, NT>;
     using R = QuantRecord<D, kFp4>;
     constexpr int RB = R::kRowBytes, NB = C::NB;
     const int g = lane >> 2, t = lane & 3;
     const int row = slot_row<RB>(g);                                    // S^T's rows: row, row + 8
     const int ta = slot_row<RB>(2 * t), tb = slot_row<RB>(2 * t + 1);  // O^T's token slots: rows ta, tb (+ 8)
-    const uint32_t cnt = static_cast<uint32_t>(hi - lo);
-    auto visible = [&](int b, int r) { return static_cast<uint32_t>(tok_base - lo + b * kBlockSize + r) < cnt; };
+    auto visible = [&](int b, int r) { return tok_base - lo + static_cast<uint32_t>(b * kBlockSize + r) < hi - lo; };
 
     float s[NB][NT][4];
     float kf[NB][2];      // what a row's logits are scaled by
@@ -329,6 +331,7 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
     }
 
     // ---- softmax: p = 2^(s kf - mu), mu moving only when a logit exceeds it by 2^8
+    constexpr bool kMayBeFar = kEdge || !kFp4;
     uint64_t p[NB][NT][2];  // row, row + 8: a pair of heads each
     auto logits = [&]() {
 #pragma unroll
@@ -353,6 +356,12 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
                 top = fmax3(top, x, y);  // +inf while mu is -inf: a pass's first block has a visible key
             }
     bool grow = top > kGrow;
+    if constexpr (kMayBeFar) {
+        float far = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) far = fmax3(far, fabsf(st.mu[n][0]), fabsf(st.mu[n][1]));
+        grow = grow || far > kFar;
+    }
     if constexpr (!kFp4) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) grow = grow || !(fmaxf(vs[b][0], vs[b][1]) * st.vfac <= kVGrow);
@@ -382,7 +391,7 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
             for (int c = 0; c < 2; ++c) {
                 float mx = -INFINITY;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) mx = fmax3(mx, s[b][n][c] * kf[b][0], s[b][n][c + 2] * kf[b][1]);
+                for (int b = 0; b < NB; ++b) mx = fmax3(mx, __fmul_rn(s[b][n][c], kf[b][0]), __fmul_rn(s[b][n][c + 2], kf[b][1]));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
                 const float mn = fmaxf(st.mu[n][c], mx);
@@ -396,7 +405,18 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
             }
             st.l[n] = mul_f32x2(st.l[n], pack_f32x2(keep[0], keep[1]));
         }
-        logits();
+        if constexpr (kMayBeFar) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        p[b][n][h] = pack_f32x2(__fsub_rn(__fmul_rn(s[b][n][2 * h], kf[b][h]), st.mu[n][0]),
+                                                __fsub_rn(__fmul_rn(s[b][n][2 * h + 1], kf[b][h]), st.mu[n][1]));
+        } else {
+            logits();
+        }
     }
     uint32_t pb[NB][NT][2];
 #pragma unroll
@@ -535,10 +555,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     if (split >= nsplit) return;
     const int b0 = first_blk + split * a.chunk_blocks;
     const int b1 = min(last_blk + 1, b0 + a.chunk_blocks);
-    // the chunk's visible keys from its first block's first key on: a ring's positions run to
-    // the end of 32 bits, which a pass's own must not pass
-    const int lo_here = max(lo - b0 * kBlockSize, 0);
-    const int hi_here = b1 > last_blk ? ctx - b0 * kBlockSize : (b1 - b0) * kBlockSize;
+    const int hi = b1 > last_blk ? ctx : b1 * kBlockSize;
     // this warp's passes: NB blocks each, warp after warp
     const int passes = ((b1 - b0 + C::NB - 1) / C::NB - warp + kWarps - 1) / kWarps;
 
@@ -627,6 +644,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     // never 0, which would turn a masked logit, -inf, into a NaN
     sl = fmaxf(ldexpf(sl, qe - 139), 1.401298464324817e-45f);
 
+    // 4-bit: a key is at most 6 * 448, q as scaled below 2^13
+    const bool far = kFp4 && sl * (D * 8192.f * 2688.f) > kFar;
+
     State<D, NT> st;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -640,15 +660,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     // pass i sits in stage i mod kStages; pass i + kStages - 1 goes where pass i - 1
     // was, which every lane has read by the time all are past the __syncwarp
     uint32_t here = 0, next = (C::kStages - 1) * C::kStage;
-    int tok = C::NB * warp * kBlockSize;
+    // a ring's positions run to the end of 31 bits, a pass's last beyond: unsigned
+    uint32_t tok = (b0 + C::NB * warp) * kBlockSize;
     for (int i = 0; i < passes; ++i) {
         copy_wait<C::kStages - 2>();  // this lane's copies of pass i have landed
         __syncwarp();                 // and every lane's
         load(i + C::kStages - 1, next);
-        if (tok >= lo_here && tok + C::NB * kBlockSize <= hi_here)
-            attend<D, kFp4, NT, false>(st, qb, ring + here, lane, tok, lo_here, hi_here, sl);
+        if (!far && tok >= static_cast<uint32_t>(lo) && tok + C::NB * kBlockSize <= static_cast<uint32_t>(hi))
+            attend<D, kFp4, NT, false>(st, qb, ring + here, lane, tok, lo, hi, sl);
         else
-            attend<D, kFp4, NT, true>(st, qb, ring + here, lane, tok, lo_here, hi_here, sl);
+            attend<D, kFp4, NT, true>(st, qb, ring + here, lane, tok, lo, hi, sl);
         tok += kWarps * C::NB * kBlockSize;
         next = here;
         here = here + C::kStage == C::kStages * C::kStage ? 0 : here + C::kStage;

@@ -1,4 +1,5 @@
-"""Quantised decode where magnitudes lie far apart: scales whose product leaves fp32's range."""
+"""Quantised decode where magnitudes lie far apart: scales whose product leaves fp32's range,
+logits beyond 2^28."""
 import numpy as np
 import pytest
 
@@ -34,3 +35,35 @@ def test_logits_below_all_numbers_weigh_alike(fmt, d, qvalue, sm_scale):
     o, lse = decode(p, q, tables, lens, sm_scale=sm_scale)
     check(fmt, p, q, tables, lens, o, lse, sm_scale)
     assert pkv.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [4, 13])
+@pytest.mark.parametrize("power", [20, 28, 40, 90])
+def test_logits_whose_step_passes_one_leave_one_key(fmt, d, hq, power):
+    """Logits of up to 2^93, steps of 2^70 apart: the largest one's row is the output wherever
+    the second is further below than the logits' own rounding."""
+    rng = np.random.default_rng(hq + power)
+    p = B.Pools(rng, fmt, 60, 1, d)
+    lens = [900, 33, 1]
+    tables = np.array([rng.permutation(60)[:57] for _ in lens], np.int32)
+    q = Q.bf16(rng.standard_normal((3, hq, d)) * 2.0 ** power)
+    o, lse = decode(p, q, tables, lens)
+    assert np.all(np.isfinite(o)) and np.all(np.isfinite(lse))
+    clear = 0
+    for s, n in enumerate(lens):
+        k, v = p.rows(0, tables[s], 0, n)[:, 0], p.rows(1, tables[s], 0, n)[:, 0]
+        x = np.float64(np.float32(d ** -0.5)) * (q[s].astype(np.float64) @ k.T)
+        err = (d + 16) * 2.0 ** -23 * d ** -0.5 * (np.abs(q[s].astype(np.float64)) @ np.abs(k).T).max(1)
+        at = x.argmax(1)
+        within(lse[s], x.max(1), err + 2.0 ** -22 * np.abs(x.max(1)) + np.log(n), "lse of sequence %d" % s)
+        for h in range(hq):
+            rest = np.delete(x[h], at[h])
+            if n == 1 or x[h].max() - rest.max() > 2 * err[h] + 40:
+                # bf16's half a step, 2^-8 of the result; int8: the weight 1 x row scale is rounded
+                # to f16 before it, 2^-11 of the value; the products and sums in fp32, some 2^-20
+                tol = (2.0 ** -8 * (1 + 2.0 ** -10) + 2.0 ** -11 * (fmt == "int8") + 2.0 ** -20) * np.abs(v[at[h]])
+                within(o[s, h], v[at[h]], tol + 2.0 ** -120, "o of head %d" % h)
+                clear += 1
+    assert clear > hq
