@@ -597,8 +597,9 @@ pkv_status pkv_quant_load_blocks(const pkv_cache_desc *desc, const void *k_pool,
 /* Decode attention over quantised pools: pkv_decode_attention's computation and
  * arguments, with k and v the pools' values.  context_lens[s] may be 0 or less (o = 0,
  * lse = -inf, or the sink's logit).  The MMAs take f16 operands: the codes (with their
- * 16-dim scales, 4-bit) exactly, q scaled by a power of two into f16's range, and
- * the softmax weights rounded to f16; sums and softmax statistics are fp32.
+ * 16-dim scales, 4-bit) exactly, q scaled by a power of two into f16's range (exactly,
+ * but for dims below 2^-19 of their head's largest, which are rounded by at most 2^-27 of
+ * it), and the softmax weights rounded to f16; sums and softmax statistics are fp32.
  *   chunk_blocks: blocks per chunk; 0 lets the planner choose, else 1..512; a
  *                 context is cut into at most 256 chunks.
  *   workspace   : >= pkv_quant_decode_workspace_size(...) bytes, 256-byte aligned, no

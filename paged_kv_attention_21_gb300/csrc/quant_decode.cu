@@ -30,8 +30,9 @@
 // per 8x8: one movmatrix each.
 //
 // Operands are exact: codes are integers below 128, or e2m1 times e4m3 (6
-// significant bits, at least 2^-10), q is scaled by a power of two into f16's
-// range.  The int8 row scale of K multiplies the logit, that of V the weight
+// significant bits, at least 2^-10), q is scaled by a power of two into f16's range: one
+// for the group's heads, or where they lie more than 2^10 apart one for each (a common one
+// rounds a head away beside one of 2^40 times its size).  The int8 row scale of K multiplies the logit, that of V the weight
 // (normalised by a power of two that follows the largest seen, so the weight
 // stays in f16's range).  Weights are rounded to f16 (2^-11); the statistics,
 // l and O are fp32.
@@ -276,10 +277,13 @@ __device__ __forceinline__ void accumulate(float (&o)[NT][D / 16][4], const uint
 // NB consecutive blocks, K and V records of block i at stage + i * kBlock: tok_base is
 // the first one's first position, keys in [lo, hi) take part.  kEdge: some of the blocks'
 // tokens may lie outside (masking them as they come cost 24 instructions a block in the
-// passes that have none), or, 4-bit, the logits may reach kFar.
+// passes that have none), the group's heads have scales of their own (a pair of them instead
+// of one, in every pass, cost the 4-bit kernel of D = 128 1.7 %), or, 4-bit, the logits may
+// reach kFar.  sl: what the logits are scaled by; kEdge: head_sl[h] those of head h.
 template <int D, bool kFp4, int NT, bool kEdge>
 __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2], const uint8_t* stage,
-                                       int lane, uint32_t tok_base, uint32_t lo, uint32_t hi, float sl) {
+                                       int lane, uint32_t tok_base, uint32_t lo, uint32_t hi,
+                                       const float* head_sl, float sl) {
     using C = Cfg<D, kFp4, NT>;
     using R = QuantRecord<D, kFp4>;
     constexpr int RB = R::kRowBytes, NB = C::NB;
@@ -289,7 +293,7 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
     auto visible = [&](int b, int r) { return tok_base - lo + static_cast<uint32_t>(b * kBlockSize + r) < hi - lo; };
 
     float s[NB][NT][4];
-    float kf[NB][2];      // what a row's logits are scaled by
+    float ks[NB][2];      // int8: the rows' K scales
     float vs[NB][2];      // int8: the rows' V scales
     uint32_t vs2[NB][2];  // 4-bit: V's f16x2 scales of rows (ta, tb) and (ta + 8, tb + 8)
 #pragma unroll
@@ -297,7 +301,6 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
         const uint8_t* kt = stage + b * C::kBlock;
         const uint8_t* vt = kt + C::kTile;
         scores<D, kFp4, NT>(s[b], qb, kt, row, t);
-        kf[b][0] = kf[b][1] = sl;
         vs2[b][0] = vs2[b][1] = 0u;
         if constexpr (kFp4) {
             const uint8_t* p = vt + R::kScales + (D == 128 ? g : g >> 1);
@@ -314,7 +317,7 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                kf[b][h] = *reinterpret_cast<const float*>(kt + R::kScales + (row + 8 * h) * 4) * sl;
+                ks[b][h] = *reinterpret_cast<const float*>(kt + R::kScales + (row + 8 * h) * 4);
                 vs[b][h] = *reinterpret_cast<const float*>(vt + R::kScales + (row + 8 * h) * 4);
             }
         }
@@ -324,13 +327,21 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
                 if (!visible(b, row + 8 * h)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) s[b][n][2 * h] = s[b][n][2 * h + 1] = -INFINITY;
-                    kf[b][h] = sl;  // > 0: the product stays -inf
+                    ks[b][h] = 1.f;  // > 0: the product stays -inf
                     vs[b][h] = 0.f;
                 }
         }
     }
 
     // ---- softmax: p = 2^(s kf - mu), mu moving only when a logit exceeds it by 2^8
+    auto kf = [&](int b, int n, int h) {
+        if constexpr (kEdge) {
+            const uint64_t two = *reinterpret_cast<const uint64_t*>(head_sl + 2 * t + 8 * n);
+            return kFp4 ? two : mul_f32x2(pack_f32x2(ks[b][h], ks[b][h]), two);
+        }
+        const float f = kFp4 ? sl : ks[b][h] * sl;
+        return pack_f32x2(f, f);
+    };
     constexpr bool kMayBeFar = kEdge || !kFp4;
     uint64_t p[NB][NT][2];  // row, row + 8: a pair of heads each
     auto logits = [&]() {
@@ -340,8 +351,13 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    p[b][n][h] = fma_f32x2(pack_f32x2(s[b][n][2 * h], s[b][n][2 * h + 1]), pack_f32x2(kf[b][h], kf[b][h]),
+                    p[b][n][h] = fma_f32x2(pack_f32x2(s[b][n][2 * h], s[b][n][2 * h + 1]), kf(b, n, h),
                                            pack_f32x2(-st.mu[n][0], -st.mu[n][1]));
+    };
+    auto logit = [&](int b, int n, int i) {  // rounded
+        float k[2];
+        unpack_f32x2(kf(b, n, i / 2), k[0], k[1]);
+        return __fmul_rn(s[b][n][i], k[i % 2]);
     };
     logits();
     float top = -INFINITY;
@@ -391,7 +407,7 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
             for (int c = 0; c < 2; ++c) {
                 float mx = -INFINITY;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) mx = fmax3(mx, __fmul_rn(s[b][n][c], kf[b][0]), __fmul_rn(s[b][n][c + 2], kf[b][1]));
+                for (int b = 0; b < NB; ++b) mx = fmax3(mx, logit(b, n, c), logit(b, n, c + 2));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
                 const float mn = fmaxf(st.mu[n][c], mx);
@@ -412,8 +428,8 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        p[b][n][h] = pack_f32x2(__fsub_rn(__fmul_rn(s[b][n][2 * h], kf[b][h]), st.mu[n][0]),
-                                                __fsub_rn(__fmul_rn(s[b][n][2 * h + 1], kf[b][h]), st.mu[n][1]));
+                        p[b][n][h] = pack_f32x2(__fsub_rn(logit(b, n, 2 * h), st.mu[n][0]),
+                                                __fsub_rn(logit(b, n, 2 * h + 1), st.mu[n][1]));
         } else {
             logits();
         }
@@ -504,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     using C = Cfg<D, kFp4, NT>;
     using R = QuantRecord<D, kFp4>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ __align__(8) float s_sl[kWarps][16];
     __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_v[kWarps];
     uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -612,40 +629,47 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) load(i, i * C::kStage);
 
-    // ---- q as f16, scaled by 2^(12 - e), e the exponent of the group's largest finite |q|
-    auto largest = [&](bool finite) {  // of the finite ones, or of all but NaN
-        float m = 0.f;
+    // ---- q as f16, scaled by 2^(12 - e), e the exponent of the group's largest |q|, or where
+    // a head's is below 2^-10 of that, of its own
+    float m[NT], all = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float x = bf16_lo(qb[n][j][i]), y = bf16_hi(qb[n][j][i]);
-                    m = finite ? fmax3(m, finite_magnitude(x), finite_magnitude(y)) : fmax3(m, fabsf(x), fabsf(y));
-                }
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-        return m;
-    };
-    float qmax = largest(false);
-    if (qmax == INFINITY) qmax = largest(true);  // an infinity is its own head's affair
-    const int qe = qmax > 0.f ? max(12, static_cast<int>(__float_as_uint(qmax) >> 23)) : 139;
-    const float qf = __uint_as_float(static_cast<uint32_t>(266 - qe) << 23);  // 2^(139 - qe)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        m[n] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                qb[n][j][i] = pack2<true>(bf16_lo(qb[n][j][i]) * qf, bf16_hi(qb[n][j][i]) * qf);
-    float sl = a.sm_scale * 1.4426950408889634f;
-    if constexpr (kFp4) sl *= a.k_scale[kvh];
-    // never 0, which would turn a masked logit, -inf, into a NaN
-    sl = fmaxf(ldexpf(sl, qe - 139), 1.401298464324817e-45f);
-
-    // 4-bit: a key is at most 6 * 448, q as scaled below 2^13
-    const bool far = kFp4 && sl * (D * 8192.f * 2688.f) > kFar;
+            for (int i = 0; i < 2; ++i) m[n] = fmax3(m[n], fabsf(bf16_lo(qb[n][j][i])), fabsf(bf16_hi(qb[n][j][i])));
+        m[n] = fmaxf(m[n], __shfl_xor_sync(0xFFFFFFFFu, m[n], 1));
+        m[n] = fmaxf(m[n], __shfl_xor_sync(0xFFFFFFFFu, m[n], 2));
+        all = fmaxf(all, m[n]);
+    }
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) all = fmaxf(all, __shfl_xor_sync(0xFFFFFFFFu, all, x));
+    bool apart = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) apart = apart || (m[n] > 0.f && m[n] < all * 9.765625e-4f);
+    apart = __any_sync(0xFFFFFFFFu, apart);
+    float scale = a.sm_scale * 1.4426950408889634f;
+    if constexpr (kFp4) scale *= a.k_scale[kvh];
+    float sl = 0.f;  // what the logits are scaled by, times log2 e: where apart, of the lane's last head
+    bool far = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float top = apart ? m[n] : all;
+        const int qe = top > 0.f ? max(12, static_cast<int>(__float_as_uint(top) >> 23)) : 139;
+        const float qf = __uint_as_float(static_cast<uint32_t>(266 - qe) << 23);  // 2^(139 - qe)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) qb[n][j][i] = pack2<true>(bf16_lo(qb[n][j][i]) * qf, bf16_hi(qb[n][j][i]) * qf);
+        // never 0, which would turn a masked logit, -inf, into a NaN
+        sl = fmaxf(ldexpf(scale, qe - 139), 1.401298464324817e-45f);
+        if (t == 0) s_sl[warp][g + 8 * n] = sl;
+        // 4-bit: a key is at most 6 * 448, q as scaled below 2^13
+        far = far || (kFp4 && !(sl * (D * 8192.f * 2688.f) <= kFar));
+    }
+    const bool care = apart || __any_sync(0xFFFFFFFFu, far);
+    __syncwarp();
 
     State<D, NT> st;
 #pragma unroll
@@ -666,10 +690,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
         copy_wait<C::kStages - 2>();  // this lane's copies of pass i have landed
         __syncwarp();                 // and every lane's
         load(i + C::kStages - 1, next);
-        if (!far && tok >= static_cast<uint32_t>(lo) && tok + C::NB * kBlockSize <= static_cast<uint32_t>(hi))
-            attend<D, kFp4, NT, false>(st, qb, ring + here, lane, tok, lo, hi, sl);
+        if (!care && tok >= static_cast<uint32_t>(lo) && tok + C::NB * kBlockSize <= static_cast<uint32_t>(hi))
+            attend<D, kFp4, NT, false>(st, qb, ring + here, lane, tok, lo, hi, s_sl[warp], sl);
         else
-            attend<D, kFp4, NT, true>(st, qb, ring + here, lane, tok, lo, hi, sl);
+            attend<D, kFp4, NT, true>(st, qb, ring + here, lane, tok, lo, hi, s_sl[warp], sl);
         tok += kWarps * C::NB * kBlockSize;
         next = here;
         here = here + C::kStage == C::kStages * C::kStage ? 0 : here + C::kStage;

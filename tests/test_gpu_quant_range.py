@@ -1,5 +1,5 @@
 """Quantised decode where magnitudes lie far apart: scales whose product leaves fp32's range,
-logits beyond 2^28."""
+logits beyond 2^28, query heads of one group."""
 import numpy as np
 import pytest
 
@@ -67,3 +67,20 @@ def test_logits_whose_step_passes_one_leave_one_key(fmt, d, hq, power):
                 within(o[s, h], v[at[h]], tol + 2.0 ** -120, "o of head %d" % h)
                 clear += 1
     assert clear > hq
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [4, 8, 13])
+@pytest.mark.parametrize("power", [22, 40, 100, -22, -40, -90])
+def test_a_query_head_far_from_the_others_of_its_group_spoils_none(fmt, d, hq, power):
+    rng = np.random.default_rng(hq)
+    p = B.Pools(rng, fmt, 60, 1, d)
+    lens = [900, 33]
+    tables = np.array([rng.permutation(60)[:57] for _ in lens], np.int32)
+    q = Q.bf16(rng.standard_normal((2, hq, d)))
+    q[:, hq - 2] *= np.float32(2.0 ** power)
+    o, lse = decode(p, q, tables, lens)
+    assert np.all(np.isfinite(o)) and np.all(np.isfinite(lse))
+    check(fmt, p, q, tables, lens, o, lse, d ** -0.5,
+          heads=[h for h in range(hq) if h != hq - 2 or power < 0])
