@@ -599,7 +599,8 @@ pkv_status pkv_quant_load_blocks(const pkv_cache_desc *desc, const void *k_pool,
  * lse = -inf, or the sink's logit).  The MMAs take f16 operands: the codes (with their
  * 16-dim scales, 4-bit) exactly, q scaled by a power of two into f16's range (exactly,
  * but for dims below 2^-19 of their head's largest, which are rounded by at most 2^-27 of
- * it), and the softmax weights rounded to f16; sums and softmax statistics are fp32.
+ * it), and the softmax weights (int8: times V's row scale) rounded to f16, by 2^-11
+ * of them or 2^-25 of the head's largest; sums and softmax statistics are fp32.
  *   chunk_blocks: blocks per chunk; 0 lets the planner choose, else 1..512; a
  *                 context is cut into at most 256 chunks.
  *   workspace   : >= pkv_quant_decode_workspace_size(...) bytes, 256-byte aligned, no

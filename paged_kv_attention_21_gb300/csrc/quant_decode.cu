@@ -32,10 +32,12 @@
 // Operands are exact: codes are integers below 128, or e2m1 times e4m3 (6
 // significant bits, at least 2^-10), q is scaled by a power of two into f16's range: one
 // for the group's heads, or where they lie more than 2^10 apart one for each (a common one
-// rounds a head away beside one of 2^40 times its size).  The int8 row scale of K multiplies the logit, that of V the weight
-// (normalised by a power of two that follows the largest seen, so the weight
-// stays in f16's range).  Weights are rounded to f16 (2^-11); the statistics,
-// l and O are fp32.
+// rounds a head away beside one of 2^40 times its size).  The int8 row
+// scale of K multiplies the logit, that of V the weight, and a power of two for each head
+// brings their product into f16's range: it follows the largest product, not the largest
+// scale, so that a row of little weight takes no bits from the others.  What goes into the
+// MMA is rounded to f16 (by 2^-11 of it or 2^-25 of the largest weight, int8: 2^-29 of the
+// largest product); the statistics, l and O are fp32.
 //
 // What bounds it.  Per token and KV head it reads 2 (D + 4) bytes (int8) or 2 (D/2 + D/16)
 // (4-bit) for 4 D G flops: HBM by the roofline.  int8 gets there (76 sequences x 8 KV heads
@@ -144,11 +146,11 @@ struct State {
     float mu[NT][2];    // what is subtracted from the logits (exp2 domain), -inf before any key
     uint64_t l[NT];     // this lane's share of sum 2^(x - mu), both heads
     float o[NT][D / 16][4];
-    float vfac;         // int8: the power of two on V's row scales, inf before any key
+    float vf[NT][2];    // int8: the powers of two on weight x V row scale, inf before any key
 };
 
 constexpr float kGrow = 8.f;    // logits may exceed mu by this before it moves (2^8 fits f16)
-constexpr float kVGrow = 64.f;  // normalised V scales may reach this (2^8 * 64 fits f16)
+constexpr float kVGrow = 32768.f;  // int8: weight x V row scale x vf may reach this (it fits f16)
 // From logits of this size on every pass rounds them before mu leaves them: fused, the largest
 // would keep what mu's rounding took, up to 2^8 of a logit of 2^32, a weight of 2^256.
 constexpr float kFar = 16777216.f;
@@ -378,61 +380,93 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
         for (int n = 0; n < NT; ++n) far = fmax3(far, fabsf(st.mu[n][0]), fabsf(st.mu[n][1]));
         grow = grow || far > kFar;
     }
-    if constexpr (!kFp4) {
+    // int8: the logits' weights, those of O times V's row scale and vf; whether one is too large
+    uint64_t sum[NT];
+    auto weigh = [&]() {
+        float most = 0.f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) grow = grow || !(fmaxf(vs[b][0], vs[b][1]) * st.vfac <= kVGrow);
-    }
-    if (__any_sync(0xFFFFFFFFu, grow)) {
-        float vmul = 1.f;
-        if constexpr (!kFp4) {
-            float m = 0.f;
+        for (int n = 0; n < NT; ++n) sum[n] = 0;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) m = fmaxf(m, fmaxf(vs[b][0], vs[b][1]));
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-            if (!(m * st.vfac <= kVGrow)) {
-                // the power of two that brings the largest scale into [1, 2), at most 2^100
-                const uint32_t ex = __float_as_uint(m) >> 23;  // m >= 0
-                const float nf = ex < 27u ? __uint_as_float(227u << 23) : __uint_as_float((254u - min(ex, 253u)) << 23);
-                // nf / vfac, exactly (it only shrinks; below 2^-126 O still is 0)
-                const int step = static_cast<int>(__float_as_uint(nf) >> 23) - static_cast<int>(__float_as_uint(st.vfac) >> 23);
-                if (st.vfac != INFINITY) vmul = step < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + step) << 23);
-                st.vfac = nf;
-            }
-        }
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float keep[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) mx = fmax3(mx, logit(b, n, c), logit(b, n, c + 2));
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
-                const float mn = fmaxf(st.mu[n][c], mx);
-                keep[c] = mn == -INFINITY ? 1.f : fast_exp2(st.mu[n][c] - mn);
-                st.mu[n][c] = mn;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    st.o[n][i][c] *= keep[c] * vmul;
-                    st.o[n][i][c + 2] *= keep[c] * vmul;
+                for (int h = 0; h < 2; ++h) {
+                    float x, y;
+                    unpack_f32x2(p[b][n][h], x, y);
+                    const uint64_t w = pack_f32x2(fast_exp2(x), fast_exp2(y));
+                    sum[n] = add_f32x2(sum[n], w);
+                    p[b][n][h] = mul_f32x2(mul_f32x2(w, pack_f32x2(vs[b][h], vs[b][h])), pack_f32x2(st.vf[n][0], st.vf[n][1]));
+                    unpack_f32x2(p[b][n][h], x, y);
+                    most = fmax3(most, x, y);
                 }
+        return most > kVGrow;
+    };
+    // int8: with 8 heads a group the weights come before the one vote; with 16, whose weights
+    // would not fit the registers beside the logits, after it, with a vote of their own (64
+    // sequences of up to 2048 keys, 16 heads: 19.3 us, 20.1 with one; 8 heads: 14.3 and 14.0)
+    constexpr bool kAhead = !kFp4 && NT == 1;
+    if constexpr (kAhead) grow = weigh() || grow;
+    for (int turn = 0;; ++turn) {
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float keep[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mx = -INFINITY, scale;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) mx = fmax3(mx, logit(b, n, c), logit(b, n, c + 2));
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+                    if constexpr (!kFp4) mx = ceilf(mx);  // so that mu moves by whole powers of two, and vf with it
+                    const float mn = fmaxf(st.mu[n][c], mx), up = mn - st.mu[n][c];
+                    keep[c] = mn == -INFINITY ? 1.f : fast_exp2(-up);
+                    st.mu[n][c] = mn;
+                    scale = keep[c];
+                    if constexpr (!kFp4) {
+                        // vf brings the largest product here into [2^4, 2^5), but those before, which mu
+                        // has made 2^-up of what they were, to no more than it did; 2^120 at most
+                        float m = 0.f;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                m = fmaxf(m, fast_exp2(__fsub_rn(logit(b, n, c + 2 * h), mn)) * vs[b][h]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+                        const int moved = static_cast<int>(fminf(up, 1024.f)), old = __float_as_uint(st.vf[n][c]) >> 23;
+                        const int now = min(min(258 - static_cast<int>(__float_as_uint(m) >> 23), 247), old + moved);  // exponents
+                        st.vf[n][c] = __uint_as_float(static_cast<uint32_t>(now) << 23);
+                        // O times keep and the change of vf: at most 1, and below 2^-126 O still is 0
+                        const int step = now - old - moved;
+                        scale = step < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + step) << 23);
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        st.o[n][i][c] *= scale;
+                        st.o[n][i][c + 2] *= scale;
+                    }
+                }
+                st.l[n] = mul_f32x2(st.l[n], pack_f32x2(keep[0], keep[1]));
             }
-            st.l[n] = mul_f32x2(st.l[n], pack_f32x2(keep[0], keep[1]));
+            if constexpr (kMayBeFar) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            p[b][n][h] = pack_f32x2(__fsub_rn(logit(b, n, 2 * h), st.mu[n][0]),
+                                                    __fsub_rn(logit(b, n, 2 * h + 1), st.mu[n][1]));
+            } else {
+                logits();
+            }
+            if constexpr (kAhead) weigh();
         }
-        if constexpr (kMayBeFar) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        p[b][n][h] = pack_f32x2(__fsub_rn(logit(b, n, 2 * h), st.mu[n][0]),
-                                                __fsub_rn(logit(b, n, 2 * h + 1), st.mu[n][1]));
-        } else {
-            logits();
-        }
+        if constexpr (kFp4 || kAhead) break;
+        grow = weigh();
+        if (turn == 1 || !__any_sync(0xFFFFFFFFu, grow)) break;
     }
     uint32_t pb[NB][NT][2];
 #pragma unroll
@@ -443,16 +477,17 @@ __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT
             for (int h = 0; h < 2; ++h) {
                 float x, y;
                 unpack_f32x2(p[b][n][h], x, y);
-                x = fast_exp2(x);
-                y = fast_exp2(y);
-                st.l[n] = add_f32x2(st.l[n], pack_f32x2(x, y));
-                if constexpr (!kFp4) {
-                    const float f = vs[b][h] * st.vfac;
-                    x *= f;
-                    y *= f;
+                if constexpr (kFp4) {
+                    x = fast_exp2(x);
+                    y = fast_exp2(y);
+                    st.l[n] = add_f32x2(st.l[n], pack_f32x2(x, y));
                 }
                 pb[b][n][h] = movmatrix(pack2<true>(x, y));
             }
+    if constexpr (!kFp4) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) st.l[n] = add_f32x2(st.l[n], sum[n]);
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
         accumulate<D, kFp4, NT>(st.o, pb[b], stage + b * C::kBlock + C::kTile, g, ta, tb, vs2[b]);
@@ -521,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
     using R = QuantRecord<D, kFp4>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ __align__(8) float s_sl[kWarps][16];
-    __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_v[kWarps];
+    __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_v[kFp4 ? 1 : kWarps][16];
     uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
@@ -675,11 +710,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         st.mu[n][0] = st.mu[n][1] = -INFINITY;
+        st.vf[n][0] = st.vf[n][1] = INFINITY;
         st.l[n] = 0;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) st.o[n][i][0] = st.o[n][i][1] = st.o[n][i][2] = st.o[n][i][3] = 0.f;
     }
-    st.vfac = INFINITY;
 
     // pass i sits in stage i mod kStages; pass i + kStages - 1 goes where pass i - 1
     // was, which every lane has read by the time all are past the __syncwarp
@@ -724,9 +759,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
             if (g == 0) {
                 s_m[warp][h] = st.mu[n][c];
                 s_l[warp][h] = l[n][c];
+                // 1 / vf
+                if constexpr (!kFp4)
+                    s_v[warp][h] = st.vf[n][c] == INFINITY ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(st.vf[n][c]));
             }
         }
-    if (lane == 0) s_v[warp] = kFp4 || st.vfac == INFINITY ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(st.vfac));
     __syncthreads();
     const size_t pair = static_cast<size_t>(seq) * a.hkv + kvh;
     if (threadIdx.x < G) {
@@ -753,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, kFp4, NT>::kCtas)) quant_dec
             lse = both;
         }
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s_m[w][h] = f[w] == 0.f ? 0.f : f[w] * inv * s_v[w];
+        for (int w = 0; w < kWarps; ++w) s_m[w][h] = f[w] == 0.f ? 0.f : f[w] * inv * (kFp4 ? 1.f : s_v[w][h]);
         s_l[0][h] = lse;
     }
     __syncthreads();

@@ -1,5 +1,6 @@
 """Quantised decode where magnitudes lie far apart: scales whose product leaves fp32's range,
-logits beyond 2^28, query heads of one group."""
+logits beyond 2^28, query heads of one group, V rows of one
+sequence."""
 import numpy as np
 import pytest
 
@@ -84,3 +85,87 @@ def test_a_query_head_far_from_the_others_of_its_group_spoils_none(fmt, d, hq, p
     assert np.all(np.isfinite(o)) and np.all(np.isfinite(lse))
     check(fmt, p, q, tables, lens, o, lse, d ** -0.5,
           heads=[h for h in range(hq) if h != hq - 2 or power < 0])
+
+
+def outlier_case(rng, d, hq, n, at, logit, power):
+    """An int8 pool in which the rows `at` have a V scale 2^power above the others' and
+    a K row that gives every head, whose queries share a direction, about `logit`."""
+    p = B.Pools(rng, "int8", (n + 15) // 16 + 2, 1, d)
+    table = rng.permutation(p.nb)[:(n + 15) // 16].astype(np.int32)
+    base = rng.standard_normal(d)
+    q = Q.bf16((base + 0.1 * rng.standard_normal((1, hq, d))))
+    kcode = np.rint(127 * base / np.abs(base).max()).astype(np.int64)
+    kscale = np.float32(logit * d ** 0.5 / float(kcode @ base))
+    for t in at:
+        b, r = table[t // 16], t % 16
+        codes = (kcode if kscale > 0 else -kcode) + 128
+        _, vscale = Q.get_row("int8", d, p.raw[1][b, 0], r)
+        vcodes, _ = Q.get_row("int8", d, p.raw[1][b, 0], r)
+        Q.put_row("int8", d, p.raw[0][b, 0], r, codes.astype(np.uint8),
+                  np.frombuffer(np.abs(kscale).tobytes(), np.uint8))
+        big = np.float32(np.frombuffer(vscale.tobytes(), np.float32)[0] * np.float32(2.0 ** power))
+        Q.put_row("int8", d, p.raw[1][b, 0], r, vcodes, np.frombuffer(big.tobytes(), np.uint8))
+        p.v_unit[b, 0, r] = big
+    one = np.ones(1)
+    p.values = [Q.pool_values("int8", d, raw, one) for raw in p.raw]
+    return p, q, table[None]
+
+
+@pytest.mark.parametrize("d,hq", [(64, 5), (128, 4), (64, 12), (128, 16)])
+@pytest.mark.parametrize("power", [10, 24, 60, -24, -60])
+@pytest.mark.parametrize("where", ["first", "last", "spread"])
+@pytest.mark.parametrize("chunk", [512, 8])
+def test_a_v_row_of_little_weight_spoils_none_by_its_scale(d, hq, power, where, chunk):
+    """Rows with almost no weight under V scales far above the others' (the others keep their
+    bits), or with almost all of it under scales far below."""
+    rng = np.random.default_rng(hq + power if power > 0 else 1000 - power)
+    n = 700
+    at = {"first": [0], "last": [n - 1], "spread": [3, 90, 91, 300, 511, 640]}[where]
+    p, q, tables = outlier_case(rng, d, hq, n, at, -120.0 if power > 0 else 25.0, power)
+    o, lse = decode(p, q, tables, [n], chunk=chunk)
+    check("int8", p, q, tables, [n], o, lse, d ** -0.5, chunk)
+
+
+@pytest.mark.parametrize("d,hq", [(64, 5), (128, 16)])
+def test_v_scales_that_rise_and_fall_with_the_weights(d, hq):
+    """Logits that rise by 60 over the context while the V scales fall by 2^70, and the other way:
+    early products that later ones leave far behind, and products that keep growing."""
+    rng = np.random.default_rng(d)
+    n = 1040
+    for up in (1, -1):
+        p = B.Pools(rng, "int8", n // 16, 1, d)
+        table = rng.permutation(p.nb).astype(np.int32)
+        base = rng.standard_normal(d)
+        q = Q.bf16((base + 0.05 * rng.standard_normal((1, hq, d))))
+        code = np.rint(127 * base / np.abs(base).max()).astype(np.int64) + 128
+        for t in range(n):
+            b, r = table[t // 16], t % 16
+            part = (t if up > 0 else n - t) / n
+            ks = np.float32(60 * part * d ** 0.5 / float((code - 128) @ base))
+            vs = np.float32(2.0 ** (20 - 70 * part) * (1 + rng.random()))
+            Q.put_row("int8", d, p.raw[0][b, 0], r, code.astype(np.uint8), np.frombuffer(ks.tobytes(), np.uint8))
+            vcodes, _ = Q.get_row("int8", d, p.raw[1][b, 0], r)
+            Q.put_row("int8", d, p.raw[1][b, 0], r, vcodes, np.frombuffer(vs.tobytes(), np.uint8))
+            p.v_unit[b, 0, r] = vs
+        p.values = [Q.pool_values("int8", d, raw, np.ones(1)) for raw in p.raw]
+        for chunk in (512, 3):
+            o, lse = decode(p, q, table[None], [n], chunk=chunk)
+            check("int8", p, q, table[None], [n], o, lse, d ** -0.5, chunk)
+
+
+def test_v_rows_that_are_all_zero():
+    """Zero V scales, at first and throughout: nothing but zeros until the first number."""
+    rng = np.random.default_rng(0)
+    p = B.Pools(rng, "int8", 40, 1, 64)
+    tables = np.arange(40, dtype=np.int32)[None]
+    tail = p.raw[1][..., 16 * 64:].copy().view(np.float32)
+    tail[:35] = 0
+    p.raw[1][..., 16 * 64:] = tail.view(np.uint8)
+    p.values[1] = Q.pool_values("int8", 64, p.raw[1], np.ones(1))
+    p.v_unit[:35] = 0
+    q = Q.bf16(rng.standard_normal((1, 4, 64)))
+    for n in (16, 560, 640):
+        o, lse = decode(p, q, tables, [n])
+        check("int8", p, q, tables, [n], o, lse, 0.125)
+        if n <= 560:
+            assert not np.any(o)
