@@ -64,3 +64,71 @@ def test_planned_decode_of_long_contexts(fmt, b, hkv, group, d, ctx):
         within(o[s], ro, tol, "o of sequence %d" % s)
         within(lse[s], rl, ltol, "lse of sequence %d" % s)
     assert pkv.pkv_device_errors() == 0
+
+
+def check(p, q, tables, lens, got, chunk, window=-1, ring=0, sinks=None):
+    d = q.shape[2]
+    for s, n in enumerate(lens):
+        lo = max(0, n - window) if window > 0 else 0
+        t = np.arange((n + 15) // 16)
+        line = tables[s][t % ring] if ring else tables[s]
+        ro, rl, tol, ltol = B.attention(p.fmt, q[s].astype(np.float64), p.rows(0, line, lo, n), p.rows(1, line, lo, n),
+                                        np.float64(np.float32(d ** -0.5)), chunk, p.units(line, lo, n), sinks=sinks)
+        within(got[0][s], ro, tol, "o of sequence %d" % s)
+        within(got[1][s], rl, ltol, "lse of sequence %d" % s)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 2), (128, 4, 1), (64, 13, 1), (128, 32, 2)])
+@pytest.mark.parametrize("chunk", [129, 200, 256, 512])
+def test_chunks_of_more_blocks_than_a_warp_holds_ids(fmt, d, hq, hkv, chunk):
+    """A warp holds 32 block ids at a time, a chunk's 128: contexts that end on either side of
+    the second and later ones, tables scattered."""
+    rng = np.random.default_rng(chunk + d)
+    lens = [16 * 128, 16 * 128 + 1, 16 * 129 + 5, 16 * chunk - 3, 16 * chunk + 17, 9000, 100]
+    n = [(x + 15) // 16 for x in lens]
+    p = B.Pools(rng, fmt, sum(n) + 3, hkv, d)
+    perm, tables, at = rng.permutation(p.nb).astype(np.int32), np.full((len(lens), max(n)), -1, np.int32), 0
+    for s, k in enumerate(n):
+        tables[s, :k] = perm[at:at + k]
+        at += k
+    q = Q.bf16(rng.standard_normal((len(lens), hq, d)))
+    sinks = rng.standard_normal(hq).astype(np.float32)
+    check(p, q, tables, lens, decode(p, q, tables, lens, chunk=chunk, sinks=sinks), chunk, sinks=sinks)
+    window = 16 * 140 + 3  # a window's first block starts a chunk anywhere in the table
+    check(p, q, tables, lens, decode(p, q, tables, lens, chunk=chunk, window=window), chunk, window)
+    assert pkv.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("chunk", [200, 512])
+def test_a_ring_that_wraps_within_a_chunk(fmt, d, chunk):
+    """Windows of 251 blocks over a ring of 252, at turns that put the ring's end into the first
+    ids of a warp, into the second, and between."""
+    rng = np.random.default_rng(d)
+    window, ring = 16 * 250 - 15, 252
+    lens = [4000, 4100, 16 * 252 + 900, 16 * 252 * 2 + 16 * 130, 16 * 252 * 3 - 1, 16 * 252 * 3 + 16 * 128 + 2]
+    p = B.Pools(rng, fmt, ring * len(lens), 1, d)
+    tables = rng.permutation(p.nb).astype(np.int32).reshape(len(lens), ring)
+    q = Q.bf16(rng.standard_normal((len(lens), 5, d)))
+    got = decode(p, q, tables, lens, chunk=chunk, window=window, ring=ring)
+    check(p, q, tables, lens, got, chunk, window, ring)
+    assert pkv.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+@pytest.mark.parametrize("at", [128, 131, 255, 256, 290])
+def test_a_bad_block_id_among_a_warps_later_ones_is_flagged(fmt, at):
+    """And one behind the end is not looked at."""
+    rng = np.random.default_rng(at)
+    p = B.Pools(rng, fmt, 300, 1, 64)
+    tables = rng.permutation(300).astype(np.int32)[None]
+    q = Q.bf16(rng.standard_normal((1, 3, 64)))
+    for bad in (p.nb, -1, 2 ** 31 - 1, -2 ** 31):
+        tables[0, at] = bad
+        o, lse = decode(p, q, tables, [16 * (at + 1)], chunk=512, max_len=16 * 300)
+        assert pkv.pkv_device_errors() == pkv.DEVERR_BLOCK_ID and np.all(np.isfinite(lse))
+        got = decode(p, q, tables, [16 * at], chunk=512, max_len=16 * 300)
+        assert pkv.pkv_device_errors() == 0
+        check(p, q, tables, [16 * at], got, 512)
