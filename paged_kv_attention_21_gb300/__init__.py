@@ -412,8 +412,8 @@ def _checked():
                 import importlib.util
                 import torch  # noqa: F401 -- the module links torch's libraries
                 if not os.path.exists(_build.MARSHAL_PATH):
-                    raise RuntimeError("_marshal.so is not built (%s); run __graft_entry__.build()"
-                                       % _build.MARSHAL_PATH)
+                    raise RuntimeError("_marshal.so is not built (%s); run __graft_entry__.build() "
+                                       "where torch is installed" % _build.MARSHAL_PATH)
                 spec = importlib.util.spec_from_file_location("_marshal", _build.MARSHAL_PATH)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)

@@ -5,15 +5,19 @@ links them into ``paged_kv_attention_21_gb300/_build/libpkv.so`` with the
 CUDA runtime linked statically (the tensor-map encoder is fetched from the
 driver at run time, so libcuda is not linked).  Beside them g++ compiles the
 binding's argument checks (``csrc/marshal.cpp``, against torch's headers) into
-``_build/_marshal.so``.
+``_build/_marshal.so``.  The library needs nvcc alone: without torch it is built
+by itself, and where the binding's module does not compile it is linked all the
+same before that is reported.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +25,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libpkv.so")
 MARSHAL_PATH = os.path.join(OUT_DIR, "_marshal.so")
+STAMP_PATH = os.path.join(OUT_DIR, "_marshal.for")  # what _marshal.so was built against
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -39,13 +44,34 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "pkv.h")]
+def _deps(binding: bool):
+    names = [f for f in os.listdir(CSRC) if f.endswith(".cpp") == binding]
+    return [os.path.join(CSRC, f) for f in names] + [os.path.join(INCLUDE, "pkv.h"), __file__]
+
+
+def _torch_dir():
+    """Where torch is installed, or None."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else list(spec.submodule_search_locations)[0]
+
+
+def _binding_for():
+    """The torch and Python whose ABI the binding's module is bound to; None without torch."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return "torch %s at %s, python %s\n" % (version, torch_dir, sys.version.split()[0])
 
 
 def _compile_marshal():
-    """The binding's extension module; raises with the compiler's output."""
-    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    """The binding's extension module, where there is torch; raises with the compiler's output."""
+    torch_dir, stamp = _torch_dir(), _binding_for()
+    if torch_dir is None:
+        return
     lib = os.path.join(torch_dir, "lib")
     tmp = MARSHAL_PATH + ".tmp.%d" % os.getpid()
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
@@ -59,20 +85,41 @@ def _compile_marshal():
     if r.returncode != 0:
         raise RuntimeError("g++ failed on marshal.cpp:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, MARSHAL_PATH)
+    with open(STAMP_PATH, "w") as f:
+        f.write(stamp)
+
+
+def _newer(path, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB_PATH, _deps(False))
+
+
+def binding_up_to_date() -> bool:
+    """Built from the current source, for the installed torch and this Python (or no torch)."""
+    stamp = _binding_for()
+    if stamp is None:
+        return True
+    if not _newer(MARSHAL_PATH, _deps(True)) or not os.path.exists(STAMP_PATH):
+        return False
+    with open(STAMP_PATH) as f:
+        return f.read() == stamp
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
-    return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
+    return library_up_to_date() and binding_up_to_date()
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every kernel TU and link libpkv.so; returns its path."""
-    if not force and up_to_date():
-        return LIB_PATH
+    """Compile every kernel TU and link libpkv.so, and the binding's module beside it;
+    returns the library's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
+    if not force and library_up_to_date():
+        if not binding_up_to_date():
+            _compile_marshal()
+        return LIB_PATH
     nvcc = _nvcc()
     srcs = sources()
 
@@ -89,17 +136,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
         marshal = ex.submit(_compile_marshal)
         objs = list(ex.map(compile_one, srcs))
-        marshal.result()
     tmp = LIB_PATH + ".tmp.%d" % os.getpid()
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB_PATH)
+    marshal.result()  # the library stands, whatever became of the binding's module
     return LIB_PATH
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv,
                 extra_flags=["-Xptxas", "-v"] if "--ptxas" in sys.argv else []))
