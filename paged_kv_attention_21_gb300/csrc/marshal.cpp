@@ -120,6 +120,23 @@ T structure(PyObject* o, const char* name) {
     return v;
 }
 
+// The rotation behind o.  The table that make_rope keeps beside its address (a structure that
+// was filled by hand has none) was on the device that was current then: it must be on this one.
+pkv_rope rotation(PyObject* o, int64_t device) {
+    const pkv_rope r = structure<pkv_rope>(o, "rope");
+    PyObject* table = PyObject_GetAttrString(o, "table");
+    if (!table) {
+        PyErr_Clear();
+        return r;
+    }
+    const bool is_tensor = THPVariable_Check(table);
+    const c10::Device on = is_tensor ? THPVariable_Unpack(table).device() : c10::Device(c10::kCPU);
+    Py_DECREF(table);
+    if (is_tensor && (!on.is_cuda() || on.index() != device))
+        throw Refusal(PyExc_ValueError, "rope table: on %s, expected the current CUDA device", on.str().c_str());
+    return r;
+}
+
 struct Pools {
     pkv_cache_desc desc;
     void *k, *v;
@@ -215,8 +232,9 @@ pkv_status without_gil(F call) {
 // rope, positions, q, q_out, k, k_out, stream
 PyObject* rope_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 7, [&] {
-        const pkv_rope rope = structure<pkv_rope>(a[0], "rope");
-        const int64_t device = current_device(), tokens = rows_of(a[1], "positions");
+        const int64_t device = current_device();
+        const pkv_rope rope = rotation(a[0], device);
+        const int64_t tokens = rows_of(a[1], "positions");
         const pkv_stream_t stream = stream_of(a[6], device);
         const at::Tensor& q = tensor(a[2], "q");
         const at::ScalarType type = q.scalar_type();
@@ -248,7 +266,7 @@ PyObject* quant_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const int64_t tokens = rows_of(a[3], "positions"), seqs = rows_of(a[1], "block_tables"), dim = p.desc.head_dim;
         pkv_rope rope;
         const bool has_rope = a[0] != Py_None;
-        if (has_rope) rope = structure<pkv_rope>(a[0], "rope");
+        if (has_rope) rope = rotation(a[0], p.device);
         const int32_t* tables = indexes(a[1], "block_tables", p.device, {seqs, p.desc.max_blocks_per_seq});
         const int32_t* tts = indexes(a[2], "token_to_seq", p.device, {tokens});
         const int32_t* positions = indexes(a[3], "positions", p.device, {tokens});
