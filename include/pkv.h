@@ -559,7 +559,8 @@ uint64_t pkv_quant_cache_bytes(const pkv_cache_desc *desc);
  *   k_new, v_new: bf16, token i's [Hkv][D] rows at i * new_token_stride elements;
  *   q, q_out    : bf16, token i's [Hq][D] rows at i * q_token_stride /
  *                 q_out_token_stride; q_out == q rotates in place, else it shares no
- *                 bytes with q, k_new or v_new; q may be NULL, and must be when rope is.
+ *                 bytes with q, and in no case any with k_new or v_new (refused); q may be
+ *                 NULL, and must be when rope is.
  * Pointers 16-byte aligned, strides multiples of 8 elements.  Two tokens must not
  * target the same slot in one call. */
 pkv_status pkv_quant_append(const pkv_cache_desc *desc, const pkv_rope *rope, void *k_pool,

@@ -1466,16 +1466,19 @@ pkv_status check_rows(const pkv_rows* r, const char* name, int64_t tokens, int64
     return PKV_OK;
 }
 
-// Whether bf16 rows of `row` elements at x (strides sx) and y (sy, both at least row) share bytes;
-// where the strides differ, whether their extents do.
-bool rows_meet(const void* x, int64_t sx, const void* y, int64_t sy, int64_t row, int64_t n) {
-    const uintptr_t lo = std::min(reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(y));
-    const uintptr_t delta = std::max(reinterpret_cast<uintptr_t>(x), reinterpret_cast<uintptr_t>(y)) - lo;
-    const int64_t s = lo == reinterpret_cast<uintptr_t>(x) ? sx : sy;
-    if (delta >= 2 * (uintptr_t(n - 1) * uintptr_t(s) + uintptr_t(row))) return false;
+// Whether n bf16 rows of rx elements at x (stride sx >= rx) and n of ry at y (sy >= ry) share
+// bytes; where the strides differ, whether their extents do.
+bool rows_meet(const void* x, int64_t sx, int64_t rx, const void* y, int64_t sy, int64_t ry, int64_t n) {
+    if (reinterpret_cast<uintptr_t>(x) > reinterpret_cast<uintptr_t>(y)) {
+        std::swap(x, y);
+        std::swap(sx, sy);
+        std::swap(rx, ry);
+    }
+    const uintptr_t delta = reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x);
+    if (delta >= 2 * (uintptr_t(n - 1) * uintptr_t(sx) + uintptr_t(rx))) return false;
     if (n == 1 || sx != sy) return true;
-    const uintptr_t at = delta % (2 * uintptr_t(s));
-    return at < 2 * uintptr_t(row) || at > 2 * uintptr_t(s - row);
+    const uintptr_t at = delta % (2 * uintptr_t(sx));  // of a row of y behind the row of x before it
+    return at < 2 * uintptr_t(rx) || at > 2 * uintptr_t(sx - ry);
 }
 
 pkv::RotateRows rotate_rows(const pkv_rows* r) {
@@ -1640,8 +1643,12 @@ pkv_status pkv_quant_append(const pkv_cache_desc* desc, const pkv_rope* rope, vo
                     (long long)q_token_stride, (long long)q_out_token_stride, (long long)qrow);
     if (q && q == q_out && q_token_stride != q_out_token_stride)
         return fail(PKV_ERR_INVALID_ARG, "q in place needs one token stride");
-    if (q && q != q_out && rows_meet(q, q_token_stride, q_out, q_out_token_stride, qrow, num_tokens))
+    if (q && q != q_out && rows_meet(q, q_token_stride, qrow, q_out, q_out_token_stride, qrow, num_tokens))
         return fail(PKV_ERR_INVALID_ARG, "q_out overlaps q");
+    // q's blocks write beside those that still read K and V
+    for (const void* kv : {k_new, v_new})
+        if (q && rows_meet(q_out, q_out_token_stride, qrow, kv, new_token_stride, kvrow, num_tokens))
+            return fail(PKV_ERR_INVALID_ARG, "q_out overlaps %s", kv == k_new ? "k_new" : "v_new");
     pkv::QuantArgs a;
     st = quant_args(desc, k_pool, v_pool, k_scale, v_scale, stream, &a);
     if (st != PKV_OK) return st;
