@@ -32,6 +32,7 @@ struct Library {
     decltype(&pkv_quant_load_blocks) load_blocks;
     decltype(&pkv_quant_decode) decode;
 } g_lib{};
+PyObject* g_table;  // the name "table"
 
 struct Refusal : std::exception {
     PyObject* type;
@@ -124,7 +125,7 @@ T structure(PyObject* o, const char* name) {
 // was filled by hand has none) was on the device that was current then: it must be on this one.
 pkv_rope rotation(PyObject* o, int64_t device) {
     const pkv_rope r = structure<pkv_rope>(o, "rope");
-    PyObject* table = PyObject_GetAttrString(o, "table");
+    PyObject* table = PyObject_GetAttr(o, g_table);
     if (!table) {
         PyErr_Clear();
         return r;
@@ -372,6 +373,7 @@ PyObject* init(PyObject*, PyObject* path) {
     find(l.load_blocks, "pkv_quant_load_blocks");
     find(l.decode, "pkv_quant_decode");
     if (PyErr_Occurred()) return nullptr;
+    if (!g_table && !(g_table = PyUnicode_InternFromString("table"))) return nullptr;
     g_lib = l;
     Py_RETURN_NONE;
 }
