@@ -602,8 +602,9 @@ pkv_status pkv_quant_load_blocks(const pkv_cache_desc *desc, const void *k_pool,
  * but for dims below 2^-19 of their head's largest, which are rounded by at most 2^-27 of
  * it), and the softmax weights (int8: times V's row scale) rounded to f16, by 2^-11
  * of them or 2^-25 of the head's largest; sums and softmax statistics are fp32.
- *   chunk_blocks: blocks per chunk; 0 lets the planner choose, else 1..512; a
- *                 context is cut into at most 256 chunks.
+ *   chunk_blocks: blocks per chunk; 0 lets the planner choose (pkv_decode_plan), else
+ *                 1..512; a context is cut into at most 256 chunks, so that its visible
+ *                 keys are limited to 256 x 512 x 16 tokens (PKV_ERR_UNSUPPORTED beyond).
  *   workspace   : >= pkv_quant_decode_workspace_size(...) bytes, 256-byte aligned, no
  *                 initial contents.  Calls that share a workspace must not overlap on
  *                 the GPU (nor the replays of graphs that captured them).

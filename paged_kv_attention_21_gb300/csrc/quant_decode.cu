@@ -29,24 +29,24 @@
 // P^T in the second product's operand layout is the first's result transposed
 // per 8x8: one movmatrix each.
 //
-// Operands are exact: codes are integers below 128, or e2m1 times e4m3 (6
-// significant bits, at least 2^-10), q is scaled by a power of two into f16's range: one
-// for the group's heads, or where they lie more than 2^10 apart one for each (a common one
-// rounds a head away beside one of 2^40 times its size).  The int8 row
-// scale of K multiplies the logit, that of V the weight, and a power of two for each head
-// brings their product into f16's range: it follows the largest product, not the largest
-// scale, so that a row of little weight takes no bits from the others.  What goes into the
-// MMA is rounded to f16 (by 2^-11 of it or 2^-25 of the largest weight, int8: 2^-29 of the
-// largest product); the statistics, l and O are fp32.
+// Operands are exact: codes are integers below 128, or e2m1 times e4m3 (6 significant
+// bits, at least 2^-10), q is scaled by a power of two into f16's range: one for the
+// group's heads, or where they lie more than 2^10 apart one for each (a common one rounds
+// a head away beside one of 2^40 times its size).  The int8 row scale of K multiplies the
+// logit, that of V the weight, and a power of two for each head brings their product into
+// f16's range: it follows the largest product, not the largest scale, so that a row of
+// little weight takes no bits from the others.  What goes into the MMA is rounded to f16
+// (by 2^-11 of it or 2^-25 of the largest weight, int8: 2^-29 of the largest product);
+// the statistics, l and O are fp32.
 //
 // What bounds it.  Per token and KV head it reads 2 (D + 4) bytes (int8) or 2 (D/2 + D/16)
 // (4-bit) for 4 D G flops: HBM by the roofline.  int8 gets there (76 sequences x 8 KV heads
-// of 512 blocks, one steady wave: 6.18 TB/s at D = 128, 5.98 at 64; its copies alone 6.58
-// and 6.50).  A 4-bit block of D = 128 is 2304 bytes and costs a warp about 264 instructions
+// of 512 blocks, one steady wave: 6.18 TB/s at D = 128, 6.02 at 64; its copies alone 6.58
+// and 6.50).  A 4-bit block of D = 128 is 2304 bytes and costs a warp about 265 instructions
 // beside 16 MMAs, which hold the issue port for 8 cycles each (an MMA with 4 independent
 // FMAs measured 11.7 cycles, alone 8.0): some 390 issue cycles where HBM delivers a block
-// every 404.  So one steady wave runs at 6.20 TB/s and its copies alone at 6.89; at D = 64,
-// half the bytes for more than half the instructions, at 5.12 and 6.18.  Tried and dropped:
+// every 404.  So one steady wave runs at 6.24 TB/s and its copies alone at 6.89; at D = 64,
+// half the bytes for more than half the instructions, at 5.07 and 6.18.  Tried and dropped:
 // one bulk copy per record (5.49 TB/s where this was 6.01: a copy's issue costs a warp more
 // than 5 per-lane ones), one block per pass (5.60), 5 or 6 CTAs per SM (5.49, 4.07: the port,
 // not latency, is short), 8-warp CTAs (long batch 462 us, 426 with 4 warps).
@@ -279,9 +279,11 @@ __device__ __forceinline__ void accumulate(float (&o)[NT][D / 16][4], const uint
 // NB consecutive blocks, K and V records of block i at stage + i * kBlock: tok_base is
 // the first one's first position, keys in [lo, hi) take part.  kEdge: some of the blocks'
 // tokens may lie outside (masking them as they come cost 24 instructions a block in the
-// passes that have none), the group's heads have scales of their own (a pair of them instead
-// of one, in every pass, cost the 4-bit kernel of D = 128 1.7 %), or, 4-bit, the logits may
-// reach kFar.  sl: what the logits are scaled by; kEdge: head_sl[h] those of head h.
+// passes that have none), the group's heads have scales of their own (a pair of them in
+// registers, in every pass, cost the 4-bit kernel of D = 128 1.7 %; with heads 2^12 apart
+// it takes 96.8 us where it takes 89.4 with heads alike, 57 sequences x 8 KV heads of 512
+// blocks), or, 4-bit, the logits may reach kFar.  sl: what the logits are scaled by;
+// kEdge: head_sl[h] those of head h.
 template <int D, bool kFp4, int NT, bool kEdge>
 __device__ __forceinline__ void attend(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2], const uint8_t* stage,
                                        int lane, uint32_t tok_base, uint32_t lo, uint32_t hi,

@@ -349,12 +349,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_con
 // D/16 lanes per row, two vectors of 8 dims each: a rotation's pair of vectors where the
 // pairs are half-split, so that every byte and every (cos, sin) is read once.
 //
-// The quantisation takes some 430 instructions per warp and 512 values, so that K and V
-// of 4096 tokens of 8 heads of 128 (21 MB) take 8.8 us in a replayed graph where HBM would
-// take 3.2, and with 32 rotated q heads (88 MB) 20 where it would take 13.0.  32 dims a
-// lane, which halves the instructions, were tried when those took 9.8 and 20.4: 8.6 and
-// 20.3, but K and V of 256 tokens 3.1 us instead of 2.6, and 999 tokens of 64 + 8 heads of
-// 64 5.8 instead of 4.3.
+// Latency bounds it: a row waits for its token's position, then the block id, then goes
+// through some 430 instructions per warp and 512 values that start from its largest
+// magnitude.  At 43 % of an SM's warps 4.7 wait for a load at any issue, while the issue
+// slots are 48 % busy, the ALU 44 %, DRAM 34 %.  K and V of 4096 tokens of 8 heads of 128
+// (21 MB) take 8.8 us in a replayed graph where HBM would take 3.2, and with 32 rotated q
+// heads (88 MB) 20 where it would take 13.0.  32 dims a lane, which halves the
+// instructions, were tried when those took 9.8 and 20.4: 8.6 and 20.3, but K and V of 256
+// tokens 3.1 us instead of 2.6, and 999 tokens of 64 + 8 heads of 64 5.8 instead of 4.3.
 
 // The sequence and position of a token: false for padding and, flagged by `report`,
 // for a bad one.
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(const __gr
 }
 
 // With q: blocks that rotate it as the rotation's kernels do (four heads a thread, bound
-// by HBM) beside blocks that quantise K and V (bound by instruction issue).  While the whole
+// by HBM) beside blocks that quantise K and V (bound by their waits).  While the whole
 // call is a few waves, K and V go first, whose chain of loads and work is the longer; beyond,
 // the two kinds alternate evenly, so that each SM runs both (4-bit, 32 + 8 heads of 128, K and
 // V first against alternating: 1024 tokens 5.5 and 5.7 us, 4096 tokens 19.8 and 19.9, 16384
