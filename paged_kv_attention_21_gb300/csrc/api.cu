@@ -1467,7 +1467,7 @@ pkv_status check_rows(const pkv_rows* r, const char* name, int64_t tokens, int64
 }
 
 // Whether n bf16 rows of rx elements at x (stride sx >= rx) and n of ry at y (sy >= ry) share
-// bytes; where the strides differ, whether their extents do.
+// bytes.
 bool rows_meet(const void* x, int64_t sx, int64_t rx, const void* y, int64_t sy, int64_t ry, int64_t n) {
     if (reinterpret_cast<uintptr_t>(x) > reinterpret_cast<uintptr_t>(y)) {
         std::swap(x, y);
@@ -1476,9 +1476,15 @@ bool rows_meet(const void* x, int64_t sx, int64_t rx, const void* y, int64_t sy,
     }
     const uintptr_t delta = reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x);
     if (delta >= 2 * (uintptr_t(n - 1) * uintptr_t(sx) + uintptr_t(rx))) return false;
-    if (n == 1 || sx != sy) return true;
-    const uintptr_t at = delta % (2 * uintptr_t(sx));  // of a row of y behind the row of x before it
-    return at < 2 * uintptr_t(rx) || at > 2 * uintptr_t(sx - ry);
+    if (n == 1) return true;
+    // row by row of y, or where the strides are one for all: its place behind the row of x before it
+    for (int64_t i = 0; i < (sx == sy ? 1 : n); ++i) {
+        const uintptr_t from = delta + 2 * uintptr_t(i) * uintptr_t(sy), j = from / (2 * uintptr_t(sx));
+        if (j >= uintptr_t(n)) return false;
+        const uintptr_t at = from - 2 * j * uintptr_t(sx);
+        if (at < 2 * uintptr_t(rx) || (at + 2 * uintptr_t(ry) > 2 * uintptr_t(sx) && (j + 1 < uintptr_t(n) || sx == sy))) return true;
+    }
+    return false;
 }
 
 pkv::RotateRows rotate_rows(const pkv_rows* r) {

@@ -43,11 +43,7 @@ def test_rows_of_one_buffer(n, in_place):
             with pytest.raises(pkv.PkvError, match="q_out overlaps"):
                 pkv.pkv_quant_append(**kw)
         else:
-            try:
-                pkv.pkv_quant_append(**kw)
-            except pkv.PkvError as e:  # rows apart whose extents meet, of strides that differ
-                assert "q_out overlaps" in str(e) and n > 1 and new != qos
-                continue
+            pkv.pkv_quant_append(**kw)
         seen[bool(met)] = seen.get(bool(met), 0) + 1
     assert min(seen[True], seen[False]) > 20
     torch.cuda.synchronize()
