@@ -132,3 +132,24 @@ def test_a_bad_block_id_among_a_warps_later_ones_is_flagged(fmt, at):
         got = decode(p, q, tables, [16 * at], chunk=512, max_len=16 * 300)
         assert pkv.pkv_device_errors() == 0
         check(p, q, tables, [16 * at], got, 512)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp4"])
+def test_the_longest_context_and_one_key_more(fmt):
+    """256 chunks of 512 blocks, over a table of a few blocks again and again."""
+    rng = np.random.default_rng(21)
+    p = B.Pools(rng, fmt, 40, 1, 64)
+    n = 256 * 512 * 16
+    tables = rng.integers(0, p.nb, (1, n // 16 + 1)).astype(np.int32)
+    q = Q.bf16(rng.standard_normal((1, 2, 64)))
+    got = decode(p, q, tables, [n], max_len=n)
+    every = np.arange(p.nb)
+    copies = np.repeat(np.bincount(tables[0, :n // 16], minlength=p.nb), 16)
+    ro, rl, tol, ltol = B.attention(fmt, q[0].astype(np.float64), p.rows(0, every, 0, 16 * p.nb),
+                                    p.rows(1, every, 0, 16 * p.nb), np.float64(np.float32(0.125)), 512,
+                                    p.units(every, 0, 16 * p.nb), copies)
+    within(got[0][0], ro, tol, "o")
+    within(got[1][0], rl, ltol, "lse")
+    with pytest.raises(pkv.PkvError, match="256 chunks of 512 blocks"):
+        decode(p, q, tables, [n], max_len=n + 1)
+    assert pkv.pkv_device_errors() == 0
