@@ -200,7 +200,7 @@ class ClockSampler:
 
 
 TRAFFIC_JSON = os.path.join(ROOT, "profiles", "traffic.json")
-KERNEL_SOURCES = {"decode_kernel": "decode.cu", "prefill_tc_kernel": "prefill_tc.cu"}
+KERNEL_SOURCES = {"decode_kernel": "decode_kernel.cuh", "prefill_tc_kernel": "prefill_tc_kernel.cuh"}
 
 
 def kernel_traffic_per_launch(kernel, config):

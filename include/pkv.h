@@ -623,6 +623,120 @@ size_t pkv_quant_decode_workspace_size(const pkv_cache_desc *desc, int32_t num_s
                                        int32_t max_context_len, int32_t window,
                                        int32_t chunk_blocks);
 
+/* ---- attention under a score rule ----------------------------------------
+ * Attention whose logits are capped by a tanh, fall with the distance to the key,
+ * or whose mask has a bidirectional prefix.  A query of head h at position p sees
+ * key t of its sequence (0 <= t < kv_len) iff
+ *   t <= p, or p < prefix_lens[s] and t < prefix_lens[s],  and
+ *   window <= 0 or t > p - window,
+ * with the logit, in fp32,
+ *   x = sm_scale q.k;  cap > 0: x = cap tanh(x / cap);  slopes: x -= slopes[h] |p - t|,
+ * and o = sum_t e^{x_t} v_t / (e^{sinks[h]} + sum_t e^{x_t}), lse = ln of that
+ * denominator (without sinks: their term is 0).  A query that sees no key has
+ * o = 0 and lse = -inf (or the sink's logit).
+ * All pointers nullable.  prefix_lens[s] may be any value: at most kv_len of it
+ * counts, and none below 1. */
+typedef struct {
+    float sm_scale;             /* finite, > 0 */
+    float cap;                  /* 0: none; else finite, > 0, sm_scale / cap a normal fp32 number */
+    int32_t window;             /* <= 0: none */
+    int32_t reserved;           /* 0 */
+    const float *slopes;        /* fp32 [Hq], finite; any sign */
+    const float *sinks;         /* fp32 [Hq] */
+    const int32_t *prefix_lens; /* int32 [num_seqs] */
+} pkv_score;
+
+/* pkv_decode_attention under a score rule: arguments, workspace
+ * (pkv_decode_workspace_size with score->window), plan, rings, DESC flags, pinned
+ * host arrays and errors as there.  The query is its sequence's last position: a
+ * prefix changes nothing here.  context_lens[s] may be 0 or less. */
+pkv_status pkv_score_decode(const pkv_cache_desc *desc, const pkv_score *score, const void *q,
+                            const void *k_cache, const void *v_cache, const float *k_scale,
+                            const float *v_scale, const int32_t *block_tables,
+                            const int32_t *context_lens, int32_t num_seqs, int32_t max_context_len,
+                            int32_t chunk_blocks, void *out, float *lse_out, void *workspace,
+                            size_t workspace_bytes, pkv_stream_t stream);
+
+/* pkv_prefill_attention_ragged under a score rule: arguments, kernels and errors as
+ * there (causal == 0 drops t <= p; distances are |p - t|).  No workspace.  Slots past
+ * kv_lens[s], and those of blocks wholly below every query's window, may hold anything,
+ * and the latter's table entries may name no block.  A V row that some query of the
+ * sequence sees must be finite: where another query of the same tile does not see it,
+ * 0 times it is part of that query's sum. */
+pkv_status pkv_score_prefill(const pkv_cache_desc *desc, const pkv_score *score, const void *q,
+                             const int32_t *qo_indptr, const void *k_cache, const void *v_cache,
+                             const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                             const int32_t *kv_lens, int32_t num_seqs, int32_t total_q_tokens,
+                             const int32_t *qo_indptr_host, const int32_t *kv_lens_host,
+                             int32_t causal, void *out, float *lse_out, pkv_stream_t stream);
+
+/* ---- the weight that each cached key receives ------------------------------
+ * mass[s][g][t] (fp32 [num_seqs][Hkv][mass_stride]) becomes, for 0 <= t < kv_lens[s],
+ *   keep * mass[s][g][t] + sum over the sequence's queries i and the heads h of KV
+ *   head g, where i sees t, of exp(x_{i,h,t} - lse[i][h]),
+ * x and "sees" as above.  The last q_len keys are this call's own: what mass held for
+ * them counts as 0, and with keep == 0 nothing of mass is read.  Entries from
+ * kv_lens[s] on stay as they are.  A query whose lse is -inf adds nothing.  Over
+ * the sums the order of the queries is fixed: a call repeats its bits.
+ *   q, qo_indptr, k_cache, k_scale, block_tables, kv_lens : as in pkv_score_prefill;
+ *               qo_indptr NULL: one query per sequence, q [num_seqs][Hq][D].
+ *   lse        : fp32 [total_q_tokens][Hq], as the attention calls return it (a sink's
+ *               share is in it; score->sinks is not read).
+ *   max_kv_len : host, >= every kv_lens[s], <= mass_stride and the table's capacity; a
+ *               longer one is cut to it and sets PKV_DEVERR_LENGTH.
+ *   max_q_len  : host, >= every q_len; more queries of a sequence are not counted and
+ *               set PKV_DEVERR_LENGTH.  (1 with qo_indptr NULL.)
+ *   keep       : finite, >= 0.
+ * No ring cache (PKV_ERR_UNSUPPORTED).  Over e4m3 pools q is rounded to f16. */
+pkv_status pkv_score_mass(const pkv_cache_desc *desc, const pkv_score *score, const void *q,
+                          const int32_t *qo_indptr, const void *k_cache, const float *k_scale,
+                          const int32_t *block_tables, const int32_t *kv_lens, int32_t num_seqs,
+                          int32_t total_q_tokens, int32_t max_q_len, int32_t max_kv_len,
+                          int32_t causal, const float *lse, float keep, float *mass,
+                          int64_t mass_stride, pkv_stream_t stream);
+
+/* ---- eviction ---------------------------------------------------------------
+ * Which keys to keep: with n = kv_lens[s] and c = min(n, budget) (0 for n <= 0),
+ * kept[s][g][0 .. c) are c positions in ascending order: all of them if n <= budget;
+ * else the `first` first and the `recent` last ones and, between them, the budget -
+ * first - recent of the largest mass[s][g][t] (of equal ones, those of the lowest
+ * positions; -0 equals 0; a NaN counts as less than every number).  kept_lens[s] = c.
+ * kept beyond c stays as it is.
+ *   mass      : fp32 [num_seqs][num_kv_heads][mass_stride].
+ *   max_kv_len: host, >= every kv_lens[s], <= mass_stride; a longer one is cut to it
+ *               and sets PKV_DEVERR_LENGTH.
+ *   budget    : >= 1; first, recent >= 0, first + recent <= budget.
+ *   kept      : int32 [num_seqs][num_kv_heads][kept_stride], kept_stride >= min(budget,
+ *               max_kv_len).     kept_lens: int32 [num_seqs]. */
+pkv_status pkv_evict_select(const float *mass, int64_t mass_stride, const int32_t *kv_lens,
+                            int32_t num_seqs, int32_t num_kv_heads, int32_t max_kv_len,
+                            int32_t budget, int32_t first, int32_t recent, int32_t *kept,
+                            int64_t kept_stride, int32_t *kept_lens, pkv_stream_t stream);
+
+/* Move the kept rows together: for j < kept_lens[s], row j of (s, g) through dst_tables
+ * in k_dst / v_dst receives the K and V bytes of row kept[s][g][j] through block_tables in
+ * k_cache / v_cache, and mass_out[s][g][j] = mass[s][g][kept[s][g][j]] (mass and mass_out
+ * both NULL: not).  The keys keep the rotation of the positions they had: a new token's is
+ * its true position (pkv_rope_rotate, then pkv_append_rope without a table), its slot
+ * kept_lens[s].
+ *   dst_desc   : k_dst's and v_dst's num_blocks and max_blocks_per_seq; the other fields
+ *               as in desc.
+ *   max_kept   : host, >= every kept_lens[s], <= kept_stride (and mass_out_stride); a
+ *               larger one is cut to it and sets PKV_DEVERR_LENGTH.
+ * In place: dst_tables == block_tables, k_dst == k_cache and v_dst == v_cache, with equal
+ * tables' shapes; kept must then ascend, as pkv_evict_select leaves it, and mass_out may
+ * be mass (with its stride).  Otherwise no block that is written may be read in the same
+ * call, and mass_out shares nothing with mass.  A position outside [0, mass_stride) or
+ * the source table sets PKV_DEVERR_POSITION, a block id out of range PKV_DEVERR_BLOCK_ID;
+ * that row (and weight) stays as it is.  Without mass, mass_stride is not looked at.
+ * No ring cache (PKV_ERR_UNSUPPORTED). */
+pkv_status pkv_evict_compact(const pkv_cache_desc *desc, const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, const int32_t *kept, int64_t kept_stride,
+                             const int32_t *kept_lens, int32_t num_seqs, int32_t max_kept,
+                             const pkv_cache_desc *dst_desc, void *k_dst, void *v_dst,
+                             const int32_t *dst_tables, const float *mass, int64_t mass_stride,
+                             float *mass_out, int64_t mass_out_stride, pkv_stream_t stream);
+
 /* ---- diagnostics --------------------------------------------------------- */
 
 /* Message for the last non-OK status on this thread ("" if none). */

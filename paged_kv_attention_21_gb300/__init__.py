@@ -5,9 +5,9 @@ function carries the C entry point's name and only marshals arguments: torch
 tensors become pointers (device memory, or pinned host memory where the C
 declaration allows it), the current torch stream becomes the launch stream,
 and a non-OK status raises :class:`PkvError` with the library's message.  The
-calls go through ctypes, those on rotary positions and quantised pools through
-an extension module that first checks each tensor's type, device, shape and
-layout.  Every step of the computation runs in the library's kernels; if the
+calls go through ctypes, those on rotary positions, quantised pools, score rules
+and eviction through an extension module that first checks each tensor's type,
+device, shape and layout.  Every step of the computation runs in the library's kernels; if the
 library is missing the call fails loudly -- there is no fallback.
 
 PyTorch is used here for device memory and streams only.
@@ -94,6 +94,14 @@ class RopeScaling(ctypes.Structure):
                 ("high_freq", ctypes.c_double), ("attention", ctypes.c_double)]
 
 
+class Score(ctypes.Structure):
+    """pkv_score; keeps its tensors alive (see make_score)."""
+
+    _fields_ = [("sm_scale", ctypes.c_float), ("cap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("sinks", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -154,6 +162,14 @@ def load_library():
             "pkv_quant_decode": (ctypes.c_int, [D, P, P, P, P, P, P, P, i32, i32, f32, i32, P, i32, P,
                                                 P, P, ctypes.c_size_t, P]),
             "pkv_quant_decode_workspace_size": (ctypes.c_size_t, [D, i32, i32, i32, i32]),
+            "pkv_score_decode": (ctypes.c_int, [D, P, P, P, P, P, P, P, P, i32, i32, i32, P, P, P,
+                                                ctypes.c_size_t, P]),
+            "pkv_score_prefill": (ctypes.c_int, [D, P, P, P, P, P, P, P, P, P, i32, i32, P, P, i32, P, P, P]),
+            "pkv_score_mass": (ctypes.c_int, [D, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, P, f32, P,
+                                              i64, P]),
+            "pkv_evict_select": (ctypes.c_int, [P, i64, P, i32, i32, i32, i32, i32, i32, P, i64, P, P]),
+            "pkv_evict_compact": (ctypes.c_int, [D, P, P, P, P, i64, P, i32, i32, D, P, P, P, P, i64, P, i64,
+                                                 P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -531,6 +547,78 @@ def pkv_quant_decode(desc, q, k_pool, v_pool, block_tables, context_lens, max_co
                                    sinks, chunk_blocks, out, lse, workspace))
 
 
+# ------------------------------------------------ score rules and eviction --
+#
+# These check their tensors in _marshal too; all of them are on the current device.
+
+def make_score(sm_scale, cap=0.0, slopes=None, sinks=None, window=0, prefix_lens=None) -> Score:
+    """A score rule for the pkv_score_* calls (see pkv.h): logits sm_scale q.k, capped as
+    cap tanh(x / cap), less slopes[head] times the distance to the key.  slopes, sinks:
+    fp32 [Hq]; prefix_lens: int32 [num_seqs], sequences' bidirectional prefixes."""
+    for name, t, kind in (("slopes", slopes, "torch.float32"), ("sinks", sinks, "torch.float32"),
+                          ("prefix_lens", prefix_lens, "torch.int32")):
+        if t is not None and (t.dim() != 1 or str(t.dtype) != kind or not t.is_contiguous()):
+            raise ValueError("%s: %s of shape %s, expected one contiguous row of %s"
+                             % (name, t.dtype, tuple(t.shape), kind))
+        if t is not None and not t.is_cuda:
+            raise ValueError("%s: on %s, expected the current CUDA device" % (name, t.device))
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    s = Score(float(sm_scale), float(cap), int(window), 0, at(slopes), at(sinks), at(prefix_lens))
+    s.tensors = (slopes, sinks, prefix_lens)
+    return s
+
+
+def _host_ints(x):
+    return None if x is None else np.ascontiguousarray(x, np.int32)
+
+
+def pkv_score_decode(desc, score, q, k_cache, v_cache, block_tables, context_lens, max_context_len, out,
+                     lse=None, workspace=None, chunk_blocks=0, k_scale=None, v_scale=None, stream=None):
+    """pkv_decode_attention under a score rule; the workspace is
+    pkv_decode_workspace_size's with the rule's window."""
+    _check(_checked().score_decode(desc, score, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                   context_lens, max_context_len, chunk_blocks, out, lse, workspace,
+                                   _address(stream)))
+
+
+def pkv_score_prefill(desc, score, q, qo_indptr, k_cache, v_cache, block_tables, kv_lens, out, lse=None,
+                      qo_indptr_host=None, kv_lens_host=None, causal=True, k_scale=None, v_scale=None,
+                      stream=None):
+    """pkv_prefill_attention_ragged under a score rule."""
+    _check(_checked().score_prefill(desc, score, q, qo_indptr, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                    kv_lens, _host_ints(qo_indptr_host), _host_ints(kv_lens_host), causal, out,
+                                    lse, _address(stream)))
+
+
+def pkv_score_mass(desc, score, q, qo_indptr, k_cache, block_tables, kv_lens, max_kv_len, lse, mass, keep=1.0,
+                   max_q_len=1, causal=True, k_scale=None, stream=None):
+    """mass (fp32 [num_seqs][Hkv][at least max_kv_len]) becomes keep * mass plus the weight that
+    the queries give each key; their own keys start at 0.  lse is what the attention call
+    returned.  qo_indptr None: one query per sequence."""
+    _check(_checked().score_mass(desc, score, q, qo_indptr, k_cache, k_scale, block_tables, kv_lens, max_q_len,
+                                 max_kv_len, causal, lse, keep, mass, _address(stream)))
+
+
+def pkv_evict_select(mass, kv_lens, max_kv_len, budget, first, recent, kept, kept_lens, stream=None):
+    """The positions to keep, ascending, into kept (int32 [num_seqs][Hkv][at least
+    min(budget, max_kv_len)]), and their number into kept_lens (int32 [num_seqs])."""
+    _check(_checked().evict_select(mass, kv_lens, max_kv_len, budget, first, recent, kept, kept_lens,
+                                   _address(stream)))
+
+
+def pkv_evict_compact(desc, k_cache, v_cache, block_tables, kept, kept_lens, max_kept=None, dst_desc=None,
+                      k_dst=None, v_dst=None, dst_tables=None, mass=None, mass_out=None, stream=None):
+    """Move the kept rows (and, with mass and mass_out, their weights) together into dst_tables'
+    blocks of k_dst / v_dst; without these, in place.  max_kept None: as many as kept holds."""
+    given = [x is not None for x in (dst_desc, k_dst, v_dst, dst_tables)]
+    if any(given) and not all(given):
+        raise ValueError("dst_desc, k_dst, v_dst and dst_tables: all of them, or none (in place)")
+    if not any(given):
+        dst_desc, k_dst, v_dst, dst_tables = desc, k_cache, v_cache, block_tables
+    _check(_checked().evict_compact(desc, k_cache, v_cache, block_tables, kept, kept_lens, max_kept, dst_desc,
+                                    k_dst, v_dst, dst_tables, mass, mass_out, _address(stream)))
+
+
 def pkv_device_errors(reset: bool = True) -> int:
     """Synchronously read (and by default clear) the device error word."""
     v = ctypes.c_uint32()
@@ -551,4 +639,4 @@ def pkv_last_error() -> str:
 __all__ = [n for n in dir() if n.startswith("pkv_")] + [
     "CacheDesc", "make_desc", "PkvError", "load_library", "library_path", "KV_BF16",
     "KV_FP8_E4M3", "KV_INT8", "KV_FP4", "Rope", "make_rope", "ROPE_HALF", "ROPE_INTERLEAVED",
-    "ROPE_INVERSE", "ROPE_SCALINGS", "BoundCall", "bind_decode_step"]
+    "ROPE_INVERSE", "ROPE_SCALINGS", "Score", "make_score", "BoundCall", "bind_decode_step"]

@@ -1,7 +1,6 @@
 // api.cu -- the C ABI of libpkv: argument validation, split planning,
 // tensor-map descriptors, launches and error reporting.  Everything the
-// path computes runs in the kernels of decode.cu, prefill_tc.cu and
-// append_gather_merge.cu; this file only decides and launches.
+// path computes runs in the other files' kernels; this file only decides and launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -525,7 +524,7 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
                        int32_t max_context_len, float sm_scale, int32_t window, const float* sinks,
                        int32_t chunk_blocks, void* out, float* lse_out, void* workspace,
                        size_t workspace_bytes, pkv_stream_t stream, const StepIn* step,
-                       Scratch scratch = Scratch::kCaller) {
+                       Scratch scratch = Scratch::kCaller, const pkv_score* score = nullptr) {
     g_last_error[0] = 0;
     pkv_status st = check_desc(desc);
     if (st != PKV_OK) return st;
@@ -631,7 +630,12 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
         a.k_pool = const_cast<void*>(k_cache);
         a.v_pool = const_cast<void*>(v_cache);
     }
-    cudaError_t e = pkv::launch_decode(a, kmap, vmap, reinterpret_cast<cudaStream_t>(stream));
+    if (score) {
+        a.cap = score->cap;
+        a.slopes = score->slopes;
+    }
+    cudaError_t e = score ? pkv::launch_score_decode(a, kmap, vmap, reinterpret_cast<cudaStream_t>(stream))
+                          : pkv::launch_decode(a, kmap, vmap, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, step ? "decode step launch" : "decode launch");
     return PKV_OK;
 }
@@ -686,7 +690,8 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const int32_t
                         const float* v_scale, const int32_t* block_tables, const int32_t* kv_lens,
                         int32_t num_seqs, int32_t total_q_tokens, const int32_t* qo_indptr_host,
                         const int32_t* kv_lens_host, float sm_scale, int32_t causal, int32_t window,
-                        void* out, float* lse_out, pkv_stream_t stream, bool scaled_codes) {
+                        void* out, float* lse_out, pkv_stream_t stream, bool scaled_codes,
+                        const pkv_score* score = nullptr) {
     pkv_status st = check_desc(desc);
     if (st != PKV_OK) return st;
     if (desc->ring_blocks > 0)
@@ -763,6 +768,12 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const int32_t
     a.total_q = total_q_tokens;
     a.num_blocks = desc->num_blocks;
     a.sm_scale = sm_scale;
+    if (score) {
+        a.cap = score->cap;
+        a.slopes = score->slopes;
+        a.sinks = score->sinks;
+        a.prefix_lens = score->prefix_lens;
+    }
     if (qo_indptr_host && kv_lens_host && num_seqs <= pkv::kPrefillOrderMax) {
         // dispatch the sequences with the most causal work first: key-query
         // pairs q (kv - q) + q (q + 1) / 2 of each sequence
@@ -786,7 +797,8 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const int32_t
         a.sq_splits = sq_splits;
         a.sq_row_tiles = (max_q * G + 15) / 16;
         a.fp8 = fp8 ? 1 : 0;
-        cudaError_t e = pkv::launch_short_query(a, tkmap, tvmap, reinterpret_cast<cudaStream_t>(stream));
+        cudaError_t e = score ? pkv::launch_score_short_query(a, tkmap, tvmap, reinterpret_cast<cudaStream_t>(stream))
+                              : pkv::launch_short_query(a, tkmap, tvmap, reinterpret_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return cuda_fail(e, "short-query launch");
         return PKV_OK;
     }
@@ -803,7 +815,8 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const int32_t
     a.fp8 = fp8 ? 1 : 0;
     a.inject_timeout = (g_inject_kernels.load() >> 1) & 1;
     a.inject_limit_us = g_inject_limit_us.load();
-    cudaError_t e = pkv::launch_prefill_tc(a, qmap, kmap, vmap, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = score ? pkv::launch_score_prefill_tc(a, qmap, kmap, vmap, reinterpret_cast<cudaStream_t>(stream))
+                          : pkv::launch_prefill_tc(a, qmap, kmap, vmap, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     return PKV_OK;
 }
@@ -1904,6 +1917,243 @@ pkv_status pkv_quant_decode(const pkv_cache_desc* desc, const void* q, const voi
     a.sm_scale = sm_scale;
     const cudaError_t e = pkv::launch_quant_decode(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "quantised decode launch");
+    return PKV_OK;
+}
+
+}  // extern "C"
+
+// ----------------------------- the score rule, the keys' weights, eviction --
+
+namespace {
+
+pkv_status check_score(const pkv_score* s) {
+    if (!s) return fail(PKV_ERR_INVALID_ARG, "score is NULL");
+    if (!(s->sm_scale > 0.f) || !std::isfinite(s->sm_scale))
+        return fail(PKV_ERR_INVALID_ARG, "sm_scale must be finite and > 0");
+    // what the kernels multiply by: sm_scale / cap, and cap in log2 units
+    if (s->cap != 0.f && (!(s->cap > 0.f) || !std::isnormal(s->sm_scale / s->cap) || !std::isfinite(s->cap * 2.f)))
+        return fail(PKV_ERR_INVALID_ARG, "cap %g with sm_scale %g", double(s->cap), double(s->sm_scale));
+    if (s->reserved != 0) return fail(PKV_ERR_INVALID_ARG, "score: reserved must be 0");
+    if (!aligned(s->slopes, 4) || !aligned(s->sinks, 4) || !aligned(s->prefix_lens, 4))
+        return fail(PKV_ERR_INVALID_ARG, "slopes, sinks and prefix_lens must be 4-byte aligned");
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_score_decode(const pkv_cache_desc* desc, const pkv_score* score, const void* q, const void* k_cache,
+                            const void* v_cache, const float* k_scale, const float* v_scale,
+                            const int32_t* block_tables, const int32_t* context_lens, int32_t num_seqs,
+                            int32_t max_context_len, int32_t chunk_blocks, void* out, float* lse_out, void* workspace,
+                            size_t workspace_bytes, pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    const pkv_status st = check_score(score);
+    if (st != PKV_OK) return st;
+    return decode_impl(desc, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, num_seqs,
+                       max_context_len, score->sm_scale, score->window, score->sinks, chunk_blocks, out, lse_out,
+                       workspace, workspace_bytes, stream, nullptr, Scratch::kCaller, score);
+}
+
+pkv_status pkv_score_prefill(const pkv_cache_desc* desc, const pkv_score* score, const void* q,
+                             const int32_t* qo_indptr, const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, const int32_t* block_tables, const int32_t* kv_lens,
+                             int32_t num_seqs, int32_t total_q_tokens, const int32_t* qo_indptr_host,
+                             const int32_t* kv_lens_host, int32_t causal, void* out, float* lse_out,
+                             pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    const pkv_status st = check_score(score);
+    if (st != PKV_OK) return st;
+    return prefill_impl(desc, q, qo_indptr, k_cache, v_cache, k_scale, v_scale, block_tables, kv_lens, num_seqs,
+                        total_q_tokens, qo_indptr_host, kv_lens_host, score->sm_scale, causal, score->window, out,
+                        lse_out, stream, false, score);
+}
+
+pkv_status pkv_score_mass(const pkv_cache_desc* desc, const pkv_score* score, const void* q, const int32_t* qo_indptr,
+                          const void* k_cache, const float* k_scale, const int32_t* block_tables,
+                          const int32_t* kv_lens, int32_t num_seqs, int32_t total_q_tokens, int32_t max_q_len,
+                          int32_t max_kv_len, int32_t causal, const float* lse, float keep, float* mass,
+                          int64_t mass_stride, pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    pkv_status st = check_score(score);
+    if (st != PKV_OK) return st;
+    st = check_desc(desc);
+    if (st != PKV_OK) return st;
+    if (desc->ring_blocks > 0) return fail(PKV_ERR_UNSUPPORTED, "the keys' weights read linear tables, not a ring cache");
+    const bool fp8 = desc->kv_dtype == PKV_KV_FP8_E4M3;
+    if (num_seqs < 0 || num_seqs > 65535)
+        return fail(PKV_ERR_INVALID_ARG, "num_seqs %d out of range [0, 65535]", num_seqs);
+    if (desc->num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", desc->num_kv_heads);
+    if (total_q_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "total_q_tokens < 0");
+    if (max_q_len < 0) return fail(PKV_ERR_INVALID_ARG, "max_q_len < 0");
+    if (!qo_indptr && (total_q_tokens != num_seqs || max_q_len != 1))
+        return fail(PKV_ERR_INVALID_ARG, "without qo_indptr: one query per sequence (total_q_tokens %d, num_seqs %d, max_q_len %d)",
+                    total_q_tokens, num_seqs, max_q_len);
+    if (num_seqs == 0) return PKV_OK;
+    if (max_kv_len < 1 || max_kv_len > table_tokens(desc) || max_kv_len > mass_stride)
+        return fail(PKV_ERR_INVALID_ARG, "max_kv_len %d outside [1, %lld]", max_kv_len,
+                    (long long)std::min<int64_t>(table_tokens(desc), mass_stride));
+    if (!(keep >= 0.f) || !std::isfinite(keep)) return fail(PKV_ERR_INVALID_ARG, "keep must be finite and >= 0");
+    if (!k_cache || !block_tables || !kv_lens || !mass || (total_q_tokens > 0 && (!q || !lse)))
+        return fail(PKV_ERR_INVALID_ARG, "null device pointer");
+    if (fp8 && !k_scale) return fail(PKV_ERR_INVALID_ARG, "e4m3 pools need k_scale");
+    if (!aligned(q, 16) || !aligned(k_cache, 16)) return fail(PKV_ERR_INVALID_ARG, "q and the pool must be 16-byte aligned");
+    if (!aligned(lse, 4) || !aligned(mass, 4) || !aligned(kv_lens, 4) || !aligned(block_tables, 4) || !aligned(qo_indptr, 4))
+        return fail(PKV_ERR_INVALID_ARG, "lse, mass and the index arrays must be 4-byte aligned");
+    uint32_t* err = nullptr;
+    int sms = 0;
+    st = device_state(&err, &sms);
+    if (st != PKV_OK) return st;
+    pkv::MassArgs a{};
+    a.q = q;
+    a.k_cache = k_cache;
+    a.k_scale = fp8 ? k_scale : nullptr;
+    a.qo_indptr = qo_indptr;
+    a.kv_lens = kv_lens;
+    a.block_tables = block_tables;
+    a.lse = lse;
+    a.mass = mass;
+    a.mass_stride = mass_stride;
+    a.keep = keep;
+    a.slopes = score->slopes;
+    a.prefix_lens = score->prefix_lens;
+    a.cap = score->cap;
+    a.sm_scale = score->sm_scale;
+    a.window = score->window;
+    a.causal = causal ? 1 : 0;
+    a.err = err;
+    a.num_seqs = num_seqs;
+    a.hq = desc->num_q_heads;
+    a.hkv = desc->num_kv_heads;
+    a.group = desc->num_q_heads / desc->num_kv_heads;
+    a.d = desc->head_dim;
+    a.fp8 = fp8 ? 1 : 0;
+    a.mbps = desc->max_blocks_per_seq;
+    a.total_q = total_q_tokens;
+    a.max_q = max_q_len;
+    a.max_kv = max_kv_len;
+    a.num_blocks = desc->num_blocks;
+    a.num_sms = sms;
+    const cudaError_t e = pkv::launch_mass(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "weight launch");
+    return PKV_OK;
+}
+
+pkv_status pkv_evict_select(const float* mass, int64_t mass_stride, const int32_t* kv_lens, int32_t num_seqs,
+                            int32_t num_kv_heads, int32_t max_kv_len, int32_t budget, int32_t first, int32_t recent,
+                            int32_t* kept, int64_t kept_stride, int32_t* kept_lens, pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    if (num_seqs < 0 || num_seqs > 65535)
+        return fail(PKV_ERR_INVALID_ARG, "num_seqs %d out of range [0, 65535]", num_seqs);
+    if (num_kv_heads < 1 || num_kv_heads > 65535)
+        return fail(PKV_ERR_INVALID_ARG, "num_kv_heads %d out of range [1, 65535]", num_kv_heads);
+    if (max_kv_len < 1 || max_kv_len > mass_stride)
+        return fail(PKV_ERR_INVALID_ARG, "max_kv_len %d outside [1, mass_stride = %lld]", max_kv_len, (long long)mass_stride);
+    if (budget < 1) return fail(PKV_ERR_INVALID_ARG, "budget %d < 1", budget);
+    if (first < 0 || recent < 0 || int64_t(first) + recent > budget)
+        return fail(PKV_ERR_INVALID_ARG, "first %d and recent %d: each >= 0, together at most the budget %d", first, recent, budget);
+    if (kept_stride < std::min(budget, max_kv_len))
+        return fail(PKV_ERR_INVALID_ARG, "kept_stride %lld < %d", (long long)kept_stride, std::min(budget, max_kv_len));
+    if (num_seqs == 0) return PKV_OK;
+    if (!mass || !kv_lens || !kept || !kept_lens) return fail(PKV_ERR_INVALID_ARG, "null device pointer");
+    if (!aligned(mass, 4) || !aligned(kv_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4))
+        return fail(PKV_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
+    uint32_t* err = nullptr;
+    int sms = 0;
+    const pkv_status st = device_state(&err, &sms);
+    if (st != PKV_OK) return st;
+    pkv::SelectArgs a{};
+    a.mass = mass;
+    a.mass_stride = mass_stride;
+    a.kv_lens = kv_lens;
+    a.kept = kept;
+    a.kept_stride = kept_stride;
+    a.kept_lens = kept_lens;
+    a.num_seqs = num_seqs;
+    a.hkv = num_kv_heads;
+    a.max_kv = max_kv_len;
+    a.budget = budget;
+    a.first = first;
+    a.recent = recent;
+    a.num_sms = sms;
+    a.err = err;
+    const cudaError_t e = pkv::launch_select(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "selection launch");
+    return PKV_OK;
+}
+
+pkv_status pkv_evict_compact(const pkv_cache_desc* desc, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, const int32_t* kept, int64_t kept_stride,
+                             const int32_t* kept_lens, int32_t num_seqs, int32_t max_kept,
+                             const pkv_cache_desc* dst_desc, void* k_dst, void* v_dst, const int32_t* dst_tables,
+                             const float* mass, int64_t mass_stride, float* mass_out, int64_t mass_out_stride,
+                             pkv_stream_t stream) {
+    g_last_error[0] = 0;
+    pkv_status st = check_desc(desc);
+    if (st != PKV_OK) return st;
+    st = check_desc(dst_desc);
+    if (st != PKV_OK) return st;
+    if (desc->ring_blocks > 0 || dst_desc->ring_blocks > 0)
+        return fail(PKV_ERR_UNSUPPORTED, "eviction moves the rows of linear tables, not of a ring cache");
+    if (desc->num_kv_heads != dst_desc->num_kv_heads || desc->head_dim != dst_desc->head_dim ||
+        desc->kv_dtype != dst_desc->kv_dtype)
+        return fail(PKV_ERR_INVALID_ARG, "desc and dst_desc differ in heads, head_dim or kv_dtype");
+    if (desc->num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", desc->num_kv_heads);
+    if (num_seqs < 0 || num_seqs > 65535)
+        return fail(PKV_ERR_INVALID_ARG, "num_seqs %d out of range [0, 65535]", num_seqs);
+    if (max_kept < 0 || max_kept > table_tokens(dst_desc) || max_kept > kept_stride)
+        return fail(PKV_ERR_INVALID_ARG, "max_kept %d outside [0, %lld]", max_kept,
+                    (long long)std::min<int64_t>(table_tokens(dst_desc), kept_stride));
+    if ((mass == nullptr) != (mass_out == nullptr)) return fail(PKV_ERR_INVALID_ARG, "mass and mass_out: both or neither");
+    if (mass && (mass_stride < 1 || mass_out_stride < max_kept))
+        return fail(PKV_ERR_INVALID_ARG, "mass_stride %lld, mass_out_stride %lld (max_kept %d)", (long long)mass_stride,
+                    (long long)mass_out_stride, max_kept);
+    if (num_seqs == 0 || max_kept == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !block_tables || !kept || !kept_lens || !k_dst || !v_dst || !dst_tables)
+        return fail(PKV_ERR_INVALID_ARG, "null device pointer");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_dst, 16) || !aligned(v_dst, 16))
+        return fail(PKV_ERR_INVALID_ARG, "pools must be 16-byte aligned");
+    if (!aligned(block_tables, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4) || !aligned(dst_tables, 4) ||
+        !aligned(mass, 4) || !aligned(mass_out, 4))
+        return fail(PKV_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
+    const bool in_place = dst_tables == block_tables;
+    if (in_place && (k_dst != k_cache || v_dst != v_cache || desc->num_blocks != dst_desc->num_blocks ||
+                     desc->max_blocks_per_seq != dst_desc->max_blocks_per_seq))
+        return fail(PKV_ERR_INVALID_ARG, "dst_tables == block_tables: in place, with equal pools and descs");
+    if (k_dst == v_dst || k_dst == v_cache || v_dst == k_cache)
+        return fail(PKV_ERR_INVALID_ARG, "K rows and V rows share a pool");
+    if (mass && mass == mass_out && (!in_place || mass_stride != mass_out_stride))
+        return fail(PKV_ERR_INVALID_ARG, "mass_out == mass: in place only, with equal strides");
+    uint32_t* err = nullptr;
+    st = device_state(&err, nullptr);
+    if (st != PKV_OK) return st;
+    pkv::CompactArgs a{};
+    a.k_src = k_cache;
+    a.v_src = v_cache;
+    a.k_dst = k_dst;
+    a.v_dst = v_dst;
+    a.src_tables = block_tables;
+    a.dst_tables = dst_tables;
+    a.kept = kept;
+    a.kept_lens = kept_lens;
+    a.mass = mass;
+    a.mass_out = mass_out;
+    a.kept_stride = kept_stride;
+    a.mass_stride = mass_stride;
+    a.mass_out_stride = mass_out_stride;
+    a.src_blocks = desc->num_blocks;
+    a.dst_blocks = dst_desc->num_blocks;
+    a.num_seqs = num_seqs;
+    a.hkv = desc->num_kv_heads;
+    a.row_bytes = desc->head_dim * elem_bytes(desc);
+    a.src_mbps = desc->max_blocks_per_seq;
+    a.dst_mbps = dst_desc->max_blocks_per_seq;
+    a.max_kept = max_kept;
+    a.in_place = in_place ? 1 : 0;
+    a.err = err;
+    const cudaError_t e = pkv::launch_compact(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
     return PKV_OK;
 }
 

@@ -143,9 +143,14 @@ struct DecodeArgs {
     const int32_t* group_indptr;
     const int32_t* group_suffix_lens;
     int32_t num_groups;
+    // the score rule's part (launch_score_decode)
+    float cap;             // 0: none
+    const float* slopes;   // nullable: fp32 [hq]
 };
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           cudaStream_t stream);
+cudaError_t launch_score_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                cudaStream_t stream);
 // True when a plan of `splits` chunks per (sequence, KV head) merges through
 // the workspace tickets (more chunks than one cluster merges).
 bool decode_uses_tickets(int splits);
@@ -181,6 +186,11 @@ struct PrefillArgs {
     // the tcgen05 kernel give up its first K-tile wait after inject_limit_us
     int32_t inject_timeout;
     uint32_t inject_limit_us;
+    // the score rule's part (launch_score_prefill_tc, launch_score_short_query)
+    float cap;                   // 0: none
+    const float* slopes;         // nullable: fp32 [hq]
+    const float* sinks;          // nullable: fp32 [hq]
+    const int32_t* prefix_lens;  // nullable: int32 [num_seqs]
 };
 constexpr int kSqMaxRowTiles = 4;   // 64 query rows (tokens x heads of a KV group)
 constexpr int kSqMaxSplits = 4;     // chunks per (sequence, KV head): one cluster
@@ -189,11 +199,16 @@ constexpr int kSqMaxChunk = 512;    // blocks per chunk (a warp's ids: 4 per lan
 // pools; tensor maps as for decode (one 5-D box per (block, head) tile).
 cudaError_t launch_short_query(const PrefillArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                cudaStream_t stream);
+cudaError_t launch_score_short_query(const PrefillArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                     cudaStream_t stream);
 // Query tokens per CTA tile for a group size (rows = tokens * group <= 128).
 int prefill_tc_q_tile(int group);
 // qmap: 3-D tiled view of q [total_q][Hq][D], box {64, G, q_tile}, 128-byte swizzle.
 cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                               const CUtensorMap& vmap, cudaStream_t stream);
+
+cudaError_t launch_score_prefill_tc(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                    const CUtensorMap& vmap, cudaStream_t stream);
 
 // Rotary positions over strided rows (rope_quant.cu).
 struct RotateRows {
@@ -269,6 +284,54 @@ constexpr int kQuantMaxChunk = 512;   // blocks per CTA
 constexpr int kQuantMaxSplits = 256;  // chunks per (sequence, KV head)
 cudaError_t launch_quant_decode(const QuantDecodeArgs& a, cudaStream_t stream);
 int quant_decode_ctas(int d, int group);  // resident per SM
+
+// The weight that each cached key receives (mass.cu).
+struct MassArgs {
+    const void* q;
+    const void* k_cache;
+    const float* k_scale;        // e4m3 only
+    const int32_t* qo_indptr;    // nullable: one query per sequence
+    const int32_t* kv_lens;
+    const int32_t* block_tables;
+    const float* lse;
+    const float* slopes;         // nullable
+    const int32_t* prefix_lens;  // nullable
+    float* mass;
+    int64_t mass_stride, num_blocks;
+    float keep, cap, sm_scale;
+    int32_t num_seqs, hq, hkv, group, d, fp8, mbps, window, causal, total_q, max_q, max_kv, num_sms;
+    uint32_t* err;
+};
+cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream);
+
+// Eviction (evict.cu): the positions to keep, and their rows moved together.
+struct SelectArgs {
+    const float* mass;
+    const int32_t* kv_lens;
+    int32_t* kept;
+    int32_t* kept_lens;
+    int64_t mass_stride, kept_stride;
+    int32_t num_seqs, hkv, max_kv, budget, first, recent, num_sms;
+    uint32_t* err;
+};
+cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream);
+
+struct CompactArgs {
+    const void* k_src;
+    const void* v_src;
+    void* k_dst;
+    void* v_dst;
+    const int32_t* src_tables;
+    const int32_t* dst_tables;
+    const int32_t* kept;
+    const int32_t* kept_lens;
+    const float* mass;  // nullable
+    float* mass_out;
+    int64_t kept_stride, mass_stride, mass_out_stride, src_blocks, dst_blocks;
+    int32_t num_seqs, hkv, row_bytes, src_mbps, dst_mbps, max_kept, in_place;
+    uint32_t* err;
+};
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
 
 // Tensor-map box shape used by the attention kernels for a pool:
 // innermost box extent in elements, and the swizzle.

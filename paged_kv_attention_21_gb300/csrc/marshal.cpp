@@ -1,5 +1,5 @@
-// marshal.cpp -- the Python binding's argument checks for the rotary and quantised-pool
-// entry points, next to torch's tensors: type, device, shape and layout of each tensor,
+// marshal.cpp -- the Python binding's argument checks for the rotary, quantised-pool,
+// score-rule and eviction entry points, next to torch's tensors: type, device, shape and layout of each tensor,
 // then one call through the C ABI on torch's current stream or the one given.  A call takes
 // the host 2.2 us, 1.65 of them the launch; the same checks over torch's Python attributes
 // took 6 us more.
@@ -31,8 +31,14 @@ struct Library {
     decltype(&pkv_quant_read) read;
     decltype(&pkv_quant_load_blocks) load_blocks;
     decltype(&pkv_quant_decode) decode;
+    decltype(&pkv_score_decode) score_decode;
+    decltype(&pkv_score_prefill) score_prefill;
+    decltype(&pkv_score_mass) score_mass;
+    decltype(&pkv_evict_select) evict_select;
+    decltype(&pkv_evict_compact) evict_compact;
 } g_lib{};
-PyObject* g_table;  // the name "table"
+PyObject* g_table;    // the name "table"
+PyObject* g_tensors;  // the name "tensors"
 
 struct Refusal : std::exception {
     PyObject* type;
@@ -356,6 +362,212 @@ PyObject* quant_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// ------------------------------------------- the score rule and eviction --
+
+// A bf16 pool, or an e4m3 pool's codes as bytes or float8_e4m3fn.
+void* paged_pool(PyObject* o, const char* name, const pkv_cache_desc& desc, int64_t device) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, name);
+    at::ScalarType type = at::kBFloat16;
+    if (desc.kv_dtype == PKV_KV_FP8_E4M3)
+        type = t.scalar_type() == at::kFloat8_e4m3fn ? at::kFloat8_e4m3fn : at::kByte;
+    return address(o, name, type, device, {desc.num_blocks, desc.num_kv_heads, desc.block_size, desc.head_dim});
+}
+
+const float* floats(PyObject* o, const char* name, int64_t device, std::initializer_list<int64_t> shape) {
+    return static_cast<const float*>(address(o, name, at::kFloat, device, shape));
+}
+
+// The score rule behind o.  The tensors that make_score keeps beside their addresses (a
+// structure that was filled by hand has none) are held to this call's sizes and device.
+pkv_score score_of(PyObject* o, int64_t device, int64_t hq, int64_t seqs) {
+    pkv_score s = structure<pkv_score>(o, "score");
+    PyObject* kept = PyObject_GetAttr(o, g_tensors);
+    if (!kept) {
+        PyErr_Clear();
+        return s;
+    }
+    struct Held {
+        PyObject* p;
+        ~Held() { Py_DECREF(p); }
+    } held{kept};
+    if (!PyTuple_Check(kept) || PyTuple_GET_SIZE(kept) != 3) throw Refusal(PyExc_ValueError, "score: tensors are not make_score's");
+    s.slopes = floats(PyTuple_GET_ITEM(kept, 0), "slopes", device, {hq});
+    s.sinks = floats(PyTuple_GET_ITEM(kept, 1), "sinks", device, {hq});
+    s.prefix_lens = indexes(PyTuple_GET_ITEM(kept, 2), "prefix_lens", device, {seqs});
+    return s;
+}
+
+// Host int32 values behind an object with a buffer (a numpy array); None for none.
+struct HostInts {
+    Py_buffer view{};
+    const int32_t* data = nullptr;
+    HostInts(PyObject* o, const char* name, int64_t want) {
+        if (o == Py_None) return;
+        if (PyObject_GetBuffer(o, &view, PyBUF_CONTIG_RO) != 0) throw Raised();
+        if (view.itemsize != 4 || view.len != 4 * want) {
+            const long long got = view.len;
+            PyBuffer_Release(&view);
+            throw Refusal(PyExc_ValueError, "%s: %lld bytes, expected %lld int32 values", name, got, static_cast<long long>(want));
+        }
+        data = static_cast<const int32_t*>(view.buf);
+    }
+    HostInts(const HostInts&) = delete;
+    ~HostInts() {
+        if (data) PyBuffer_Release(&view);
+    }
+};
+
+float number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised();
+    return static_cast<float>(v);
+}
+
+// desc, score, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, max_context_len, chunk_blocks, out,
+// lse, workspace, stream
+PyObject* score_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&] {
+        const int64_t device = current_device();
+        const pkv_cache_desc desc = structure<pkv_cache_desc>(a[0], "desc");
+        const pkv_stream_t stream = stream_of(a[14], device);
+        const int64_t seqs = rows_of(a[8], "context_lens"), hq = desc.num_q_heads, hkv = desc.num_kv_heads, dim = desc.head_dim;
+        const pkv_score score = score_of(a[1], device, hq, seqs);
+        const void* q = address(a[2], "q", at::kBFloat16, device, {seqs, hq, dim});
+        const void* k = paged_pool(a[3], "k_cache", desc, device);
+        const void* v = paged_pool(a[4], "v_cache", desc, device);
+        const float* ks = floats(a[5], "k_scale", device, {hkv});
+        const float* vs = floats(a[6], "v_scale", device, {hkv});
+        const int32_t* tables = indexes(a[7], "block_tables", device, {seqs, desc.max_blocks_per_seq});
+        const int32_t* lens = indexes(a[8], "context_lens", device, {seqs});
+        const int32_t max_len = int32(a[9], "max_context_len"), chunk = int32(a[10], "chunk_blocks");
+        void* out = address(a[11], "out", at::kBFloat16, device, {seqs, hq, dim});
+        float* lse = const_cast<float*>(floats(a[12], "lse", device, {seqs, hq}));
+        void* ws = address(a[13], "workspace", at::kByte, device, {kAny});
+        const size_t ws_bytes = ws ? static_cast<size_t>(rows_of(a[13], "workspace")) : 0;
+        const int32_t num_seqs = count(seqs, "context_lens");
+        return without_gil([&] {
+            return g_lib.score_decode(&desc, &score, q, k, v, ks, vs, tables, lens, num_seqs, max_len, chunk, out, lse, ws,
+                                      ws_bytes, stream);
+        });
+    });
+}
+
+// desc, score, q, qo_indptr, k_cache, v_cache, k_scale, v_scale, block_tables, kv_lens, qo_indptr_host, kv_lens_host,
+// causal, out, lse, stream
+PyObject* score_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 16, [&] {
+        const int64_t device = current_device();
+        const pkv_cache_desc desc = structure<pkv_cache_desc>(a[0], "desc");
+        const pkv_stream_t stream = stream_of(a[15], device);
+        const int64_t seqs = rows_of(a[9], "kv_lens"), rows = rows_of(a[2], "q");
+        const int64_t hq = desc.num_q_heads, hkv = desc.num_kv_heads, dim = desc.head_dim;
+        const pkv_score score = score_of(a[1], device, hq, seqs);
+        const void* q = address(a[2], "q", at::kBFloat16, device, {rows, hq, dim});
+        const int32_t* qo = indexes(a[3], "qo_indptr", device, {seqs + 1});
+        const void* k = paged_pool(a[4], "k_cache", desc, device);
+        const void* v = paged_pool(a[5], "v_cache", desc, device);
+        const float* ks = floats(a[6], "k_scale", device, {hkv});
+        const float* vs = floats(a[7], "v_scale", device, {hkv});
+        const int32_t* tables = indexes(a[8], "block_tables", device, {seqs, desc.max_blocks_per_seq});
+        const int32_t* lens = indexes(a[9], "kv_lens", device, {seqs});
+        const HostInts qo_host(a[10], "qo_indptr_host", seqs + 1), lens_host(a[11], "kv_lens_host", seqs);
+        const int causal = PyObject_IsTrue(a[12]);
+        if (causal < 0) throw Raised();
+        void* out = address(a[13], "out", at::kBFloat16, device, {rows, hq, dim});
+        float* lse = const_cast<float*>(floats(a[14], "lse", device, {rows, hq}));
+        const int32_t num_seqs = count(seqs, "kv_lens"), total = count(rows, "q");
+        return without_gil([&] {
+            return g_lib.score_prefill(&desc, &score, q, qo, k, v, ks, vs, tables, lens, num_seqs, total, qo_host.data,
+                                       lens_host.data, causal, out, lse, stream);
+        });
+    });
+}
+
+// desc, score, q, qo_indptr, k_cache, k_scale, block_tables, kv_lens, max_q_len, max_kv_len, causal, lse, keep, mass,
+// stream
+PyObject* score_mass(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&] {
+        const int64_t device = current_device();
+        const pkv_cache_desc desc = structure<pkv_cache_desc>(a[0], "desc");
+        const pkv_stream_t stream = stream_of(a[14], device);
+        const int64_t seqs = rows_of(a[7], "kv_lens"), rows = rows_of(a[2], "q");
+        const int64_t hq = desc.num_q_heads, hkv = desc.num_kv_heads;
+        const pkv_score score = score_of(a[1], device, hq, seqs);
+        const void* q = address(a[2], "q", at::kBFloat16, device, {rows, hq, desc.head_dim});
+        const int32_t* qo = indexes(a[3], "qo_indptr", device, {seqs + 1});
+        const void* k = paged_pool(a[4], "k_cache", desc, device);
+        const float* ks = floats(a[5], "k_scale", device, {hkv});
+        const int32_t* tables = indexes(a[6], "block_tables", device, {seqs, desc.max_blocks_per_seq});
+        const int32_t* lens = indexes(a[7], "kv_lens", device, {seqs});
+        const int32_t max_q = int32(a[8], "max_q_len"), max_kv = int32(a[9], "max_kv_len");
+        const int causal = PyObject_IsTrue(a[10]);
+        if (causal < 0) throw Raised();
+        const float* lse = floats(a[11], "lse", device, {rows, hq});
+        const float keep = number(a[12]);
+        float* mass = const_cast<float*>(floats(a[13], "mass", device, {seqs, hkv, kAny}));
+        const int64_t stride = mass ? tensor(a[13], "mass").sizes()[2] : 0;
+        const int32_t num_seqs = count(seqs, "kv_lens"), total = count(rows, "q");
+        return without_gil([&] {
+            return g_lib.score_mass(&desc, &score, q, qo, k, ks, tables, lens, num_seqs, total, max_q, max_kv, causal, lse,
+                                    keep, mass, stride, stream);
+        });
+    });
+}
+
+// mass, kv_lens, max_kv_len, budget, first, recent, kept, kept_lens, stream
+PyObject* evict_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&] {
+        const int64_t device = current_device();
+        const pkv_stream_t stream = stream_of(a[8], device);
+        const int64_t seqs = rows_of(a[1], "kv_lens");
+        const float* mass = floats(a[0], "mass", device, {seqs, kAny, kAny});
+        if (!mass && a[0] == Py_None) throw Refusal(PyExc_ValueError, "mass is None");
+        const int64_t heads = tensor(a[0], "mass").sizes()[1], stride = tensor(a[0], "mass").sizes()[2];
+        const int32_t* lens = indexes(a[1], "kv_lens", device, {seqs});
+        const int32_t max_kv = int32(a[2], "max_kv_len"), budget = int32(a[3], "budget"), first = int32(a[4], "first"),
+                      recent = int32(a[5], "recent");
+        int32_t* kept = const_cast<int32_t*>(indexes(a[6], "kept", device, {seqs, heads, kAny}));
+        const int64_t kept_stride = kept ? tensor(a[6], "kept").sizes()[2] : 0;
+        int32_t* kept_lens = const_cast<int32_t*>(indexes(a[7], "kept_lens", device, {seqs}));
+        const int32_t num_seqs = count(seqs, "kv_lens"), num_heads = count(heads, "mass");
+        return without_gil([&] {
+            return g_lib.evict_select(mass, stride, lens, num_seqs, num_heads, max_kv, budget, first, recent, kept,
+                                      kept_stride, kept_lens, stream);
+        });
+    });
+}
+
+// desc, k_cache, v_cache, block_tables, kept, kept_lens, max_kept (None: kept's rows), dst_desc, k_dst, v_dst,
+// dst_tables, mass, mass_out, stream
+PyObject* evict_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 14, [&] {
+        const int64_t device = current_device();
+        const pkv_cache_desc desc = structure<pkv_cache_desc>(a[0], "desc"), dst = structure<pkv_cache_desc>(a[7], "dst_desc");
+        const pkv_stream_t stream = stream_of(a[13], device);
+        const int64_t seqs = rows_of(a[5], "kept_lens"), hkv = desc.num_kv_heads;
+        const void* k = paged_pool(a[1], "k_cache", desc, device);
+        const void* v = paged_pool(a[2], "v_cache", desc, device);
+        const int32_t* tables = indexes(a[3], "block_tables", device, {seqs, desc.max_blocks_per_seq});
+        const int32_t* kept = indexes(a[4], "kept", device, {seqs, hkv, kAny});
+        const int64_t kept_stride = a[4] == Py_None ? 0 : tensor(a[4], "kept").sizes()[2];
+        const int32_t* kept_lens = indexes(a[5], "kept_lens", device, {seqs});
+        void* kd = paged_pool(a[8], "k_dst", dst, device);
+        void* vd = paged_pool(a[9], "v_dst", dst, device);
+        const int32_t* dst_tables = indexes(a[10], "dst_tables", device, {seqs, dst.max_blocks_per_seq});
+        const float* mass = floats(a[11], "mass", device, {seqs, hkv, kAny});
+        float* mass_out = const_cast<float*>(floats(a[12], "mass_out", device, {seqs, hkv, kAny}));
+        const int64_t stride = a[11] == Py_None ? 0 : tensor(a[11], "mass").sizes()[2];
+        const int64_t out_stride = a[12] == Py_None ? 0 : tensor(a[12], "mass_out").sizes()[2];
+        const int32_t max_kept = a[6] == Py_None ? count(kept_stride, "kept") : int32(a[6], "max_kept");
+        const int32_t num_seqs = count(seqs, "kept_lens");
+        return without_gil([&] {
+            return g_lib.evict_compact(&desc, k, v, tables, kept, kept_stride, kept_lens, num_seqs, max_kept, &dst, kd, vd,
+                                       dst_tables, mass, stride, mass_out, out_stride, stream);
+        });
+    });
+}
+
 // Look the entry points up in the library at `path`.
 PyObject* init(PyObject*, PyObject* path) {
     const char* name = PyUnicode_AsUTF8(path);
@@ -372,8 +584,14 @@ PyObject* init(PyObject*, PyObject* path) {
     find(l.read, "pkv_quant_read");
     find(l.load_blocks, "pkv_quant_load_blocks");
     find(l.decode, "pkv_quant_decode");
+    find(l.score_decode, "pkv_score_decode");
+    find(l.score_prefill, "pkv_score_prefill");
+    find(l.score_mass, "pkv_score_mass");
+    find(l.evict_select, "pkv_evict_select");
+    find(l.evict_compact, "pkv_evict_compact");
     if (PyErr_Occurred()) return nullptr;
     if (!g_table && !(g_table = PyUnicode_InternFromString("table"))) return nullptr;
+    if (!g_tensors && !(g_tensors = PyUnicode_InternFromString("tensors"))) return nullptr;
     g_lib = l;
     Py_RETURN_NONE;
 }
@@ -385,6 +603,11 @@ PyMethodDef g_methods[] = {
     {"quant_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quant_read)), METH_FASTCALL, nullptr},
     {"quant_load_blocks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quant_load_blocks)), METH_FASTCALL, nullptr},
     {"quant_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quant_decode)), METH_FASTCALL, nullptr},
+    {"score_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(score_decode)), METH_FASTCALL, nullptr},
+    {"score_prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(score_prefill)), METH_FASTCALL, nullptr},
+    {"score_mass", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(score_mass)), METH_FASTCALL, nullptr},
+    {"evict_select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(evict_select)), METH_FASTCALL, nullptr},
+    {"evict_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(evict_compact)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
