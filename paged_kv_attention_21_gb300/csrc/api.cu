@@ -2035,7 +2035,18 @@ pkv_status pkv_score_mass(const pkv_cache_desc* desc, const pkv_score* score, co
     a.max_kv = max_kv_len;
     a.num_blocks = desc->num_blocks;
     a.num_sms = sms;
-    const cudaError_t e = pkv::launch_mass(a, reinterpret_cast<cudaStream_t>(stream));
+    a.q_tile = pkv::prefill_tc_q_tile(a.group);
+    cudaError_t e;
+    if (int64_t(max_q_len) * a.group <= pkv::kMassRows || total_q_tokens == 0) {
+        e = pkv::launch_mass_rows(a, reinterpret_cast<cudaStream_t>(stream));
+    } else {
+        CUtensorMap kmap, qmap;
+        st = pool_map(k_cache, desc, &kmap, fp8 ? kMapBlockRows : kMapTileGroups);
+        if (st != PKV_OK) return st;
+        st = q_map(q, total_q_tokens, desc, a.group, a.q_tile, &qmap);
+        if (st != PKV_OK) return st;
+        e = pkv::launch_mass_tc(a, qmap, kmap, reinterpret_cast<cudaStream_t>(stream));
+    }
     if (e != cudaSuccess) return cuda_fail(e, "weight launch");
     return PKV_OK;
 }

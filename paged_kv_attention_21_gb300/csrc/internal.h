@@ -300,9 +300,15 @@ struct MassArgs {
     int64_t mass_stride, num_blocks;
     float keep, cap, sm_scale;
     int32_t num_seqs, hq, hkv, group, d, fp8, mbps, window, causal, total_q, max_q, max_kv, num_sms;
+    int32_t q_tile;  // query tokens per 128-row tile (tcgen05)
     uint32_t* err;
 };
-cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream);
+// At most kMassRows query rows (queries x heads of a KV head) per sequence: mma.sync
+// fragments straight from global memory (mass.cu); more: tcgen05 (mass_tc.cu), with the
+// tile-group (bf16) or block-row (e4m3) view of the pool and the 3-D view of q.
+constexpr int kMassRows = 64;
+cudaError_t launch_mass_rows(const MassArgs& a, cudaStream_t stream);
+cudaError_t launch_mass_tc(const MassArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, cudaStream_t stream);
 
 // Eviction (evict.cu): the positions to keep, and their rows moved together.
 struct SelectArgs {

@@ -7,9 +7,7 @@
 // The product K Q^T is taken with the keys as the rows of the MMA: a key's weights
 // then sit in one lane's accumulators for every query, and the sum over the queries
 // stays in registers.
-#include "common.cuh"
-#include "internal.h"
-#include "score.cuh"
+#include "mass.cuh"
 
 namespace pkv {
 
@@ -17,47 +15,6 @@ namespace {
 
 constexpr int kMassWarps = 4;
 constexpr int kMassBlocksPerWarp = 4;
-
-// One sequence's queries and the keys they see.
-struct MassSeq {
-    int q0, q_len, rows;  // first query row of q, queries, rows counted (queries x group)
-    int kv_len, off;      // keys; position of the first query
-    int prefix;
-    bool ok;
-};
-
-__device__ __forceinline__ MassSeq mass_seq(const MassArgs& a, int seq, bool flag) {
-    MassSeq s;
-    s.q0 = a.qo_indptr ? a.qo_indptr[seq] : seq;
-    s.q_len = a.qo_indptr ? a.qo_indptr[seq + 1] - s.q0 : 1;
-    s.kv_len = a.kv_lens[seq];
-    s.prefix = a.prefix_lens ? a.prefix_lens[seq] : 0;
-    s.ok = s.kv_len > 0;
-    if (s.ok && (s.q0 < 0 || s.q_len < 0 || s.q_len > a.total_q - s.q0 || s.kv_len < s.q_len)) {
-        if (flag) flag_error(a.err, PKV_DEVERR_POSITION);
-        s.ok = false;
-    }
-    if (s.kv_len > a.max_kv) {
-        if (flag) flag_error(a.err, PKV_DEVERR_LENGTH);
-        s.kv_len = a.max_kv;
-        if (s.kv_len < s.q_len) s.ok = false;
-    }
-    s.off = s.kv_len - s.q_len;
-    int counted = s.q_len;
-    if (counted > a.max_q) {
-        if (flag && s.ok) flag_error(a.err, PKV_DEVERR_LENGTH);
-        counted = a.max_q;
-    }
-    s.rows = s.ok ? counted * a.group : 0;
-    return s;
-}
-
-// The keys [lo, hi] that a query at position pos sees (hi < lo: none).
-__device__ __forceinline__ void mass_span(const MassArgs& a, const MassSeq& s, int pos, int& lo, int& hi) {
-    hi = s.kv_len - 1;
-    if (a.causal) hi = min(hi, pos < s.prefix ? s.prefix - 1 : pos);
-    lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-}
 
 // Any number of rows: a warp holds a block's 16 keys as A operands and takes the
 // rows eight at a time.  A lane reads 16-byte pieces of K and q and takes them as
@@ -152,9 +109,9 @@ __global__ void __launch_bounds__(kMassWarps * 32) mass_rows_kernel(const MassAr
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int t = t0 + g + 8 * e;
-                        float x = sc(acc[2 * e + c]);
+                        float x = sc(acc[2 * e + c], -lse * kLog2e);
                         if (a.slopes) x = fmaf(-slope2, fabsf(static_cast<float>(pos - t)), x);
-                        const float w = fast_exp2(fmaf(-lse, kLog2e, x));
+                        const float w = fast_exp2(x);
                         if (t >= lo && t <= hi) {
                             if (e == 0) sum0 += w; else sum1 += w;
                         }
@@ -186,7 +143,7 @@ cudaError_t launch_mass_t(const MassArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_mass(const MassArgs& a, cudaStream_t stream) {
+cudaError_t launch_mass_rows(const MassArgs& a, cudaStream_t stream) {
     if (a.fp8) return a.d == 64 ? launch_mass_t<64, true>(a, stream) : launch_mass_t<128, true>(a, stream);
     return a.d == 64 ? launch_mass_t<64, false>(a, stream) : launch_mass_t<128, false>(a, stream);
 }

@@ -1,0 +1,61 @@
+// mass.cuh -- what the weight kernels (mass.cu, mass_tc.cu) share: a sequence's
+// queries, and the keys that each of them sees.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "score.cuh"
+
+namespace pkv {
+
+// One sequence's queries and the keys they see.
+struct MassSeq {
+    int q0, q_len, rows;  // first query row of q, queries, rows counted (queries x group)
+    int kv_len, off;      // keys; position of the first query
+    int prefix;
+    bool ok;
+};
+
+__device__ __forceinline__ MassSeq mass_seq(const MassArgs& a, int seq, bool flag) {
+    MassSeq s;
+    s.q0 = a.qo_indptr ? a.qo_indptr[seq] : seq;
+    s.q_len = a.qo_indptr ? a.qo_indptr[seq + 1] - s.q0 : 1;
+    s.kv_len = a.kv_lens[seq];
+    s.prefix = a.prefix_lens ? a.prefix_lens[seq] : 0;
+    s.ok = s.kv_len > 0;
+    if (s.ok && (s.q0 < 0 || s.q_len < 0 || s.q_len > a.total_q - s.q0 || s.kv_len < s.q_len)) {
+        if (flag) flag_error(a.err, PKV_DEVERR_POSITION);
+        s.ok = false;
+    }
+    if (s.kv_len > a.max_kv) {
+        if (flag) flag_error(a.err, PKV_DEVERR_LENGTH);
+        s.kv_len = a.max_kv;
+        if (s.kv_len < s.q_len) s.ok = false;
+    }
+    s.off = s.kv_len - s.q_len;
+    int counted = s.q_len;
+    if (counted > a.max_q) {
+        if (flag && s.ok) flag_error(a.err, PKV_DEVERR_LENGTH);
+        counted = a.max_q;
+    }
+    s.rows = s.ok ? counted * a.group : 0;
+    return s;
+}
+
+// The tokens [first, last] of the counted ones that see some key of [k0, k1]
+// (last < first: none).  hi and lo of mass_span both ascend with the position.
+__device__ __forceinline__ void mass_tokens(const MassArgs& a, const MassSeq& s, int k0, int k1, int& first, int& last) {
+    first = 0;
+    if (a.causal && !(s.off < s.prefix && k0 < s.prefix)) first = max(0, k0 - s.off);
+    const int64_t end = a.window > 0 ? static_cast<int64_t>(k1) + a.window - 1 - s.off : INT32_MAX;
+    last = static_cast<int>(min(static_cast<int64_t>(s.rows / a.group) - 1, end));
+}
+
+// The keys [lo, hi] that a query at position pos sees (hi < lo: none).
+__device__ __forceinline__ void mass_span(const MassArgs& a, const MassSeq& s, int pos, int& lo, int& hi) {
+    hi = s.kv_len - 1;
+    if (a.causal) hi = min(hi, pos < s.prefix ? s.prefix - 1 : pos);
+    lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+
+}  // namespace pkv

@@ -98,15 +98,6 @@ struct TcCfg {
     static constexpr uint32_t col_o(int x) { return static_cast<uint32_t>(kTcQTiles * kTcN + x * D); }
 };
 
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
-                                            int c0, int c1, int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-        : "memory");
-}
-
 // The KV tiles one query tile needs, as a range [lo, hi) of tile indices.
 struct TileSpan {
     int tok0, ntok;      // first token (within the sequence) and token count
@@ -169,12 +160,27 @@ __device__ __forceinline__ void convert_e4m3_block(const uint8_t* codes, uint8_t
 
 // The scores of one row over a KV tile, raw on entry, in log2 units under the
 // score rule on exit.  dist0: the row's position minus the tile's first key.
-__device__ __forceinline__ void score_tile(float (&sv)[kTcN], const ScoreScale& sc, float slope2, int dist0) {
+__device__ __forceinline__ void score_tile(float (&sv)[kTcN], const ScoreScale& sc, const TanhPair& tp, bool biased,
+                                           float slope2, int dist0) {
+    if (sc.out > 0.f) {
+        // (the warp takes one branch: the columns past the keys are whatever the tile holds)
+        if (__all_sync(0xFFFFFFFFu, in_poly(sv, sc.in))) {
 #pragma unroll
-    for (int e = 0; e < kTcN; ++e) sv[e] = sc(sv[e]);
-    if (slope2 != 0.f) {
+            for (int e = 0; e < kTcN; e += 2) unpack_f32x2(tp(pack_f32x2(sv[e], sv[e + 1])), sv[e], sv[e + 1]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < kTcN; ++e) sv[e] = fmaf(-slope2, fabsf(static_cast<float>(dist0 - e)), sv[e]);
+            for (int e = 0; e < kTcN; ++e) sv[e] = sc.capped(sv[e]);
+        }
+    } else {
+        const uint64_t in = pack_f32x2(sc.in, sc.in);
+#pragma unroll
+        for (int e = 0; e < kTcN; e += 2) unpack_f32x2(mul_f32x2(pack_f32x2(sv[e], sv[e + 1]), in), sv[e], sv[e + 1]);
+    }
+    if (biased) {
+        // (a distance past 2^24 is rounded, by 2^-24 of itself)
+        const float d0 = static_cast<float>(dist0);
+#pragma unroll
+        for (int e = 0; e < kTcN; ++e) sv[e] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e)), sv[e]);
     }
 }
 
@@ -599,7 +605,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
         const ScoreScale sc(a.sm_scale, kScore ? a.cap : 0.f, a.k_scale ? a.k_scale[kvh] : 1.f);
-        const float slope2 = kScore && a.slopes ? a.slopes[kvh * G + r % G] * kLog2e : 0.f;
+        const TanhPair tp(sc);
+        const bool biased = kScore && a.slopes != nullptr;
+        const float slope2 = biased ? a.slopes[kvh * G + r % G] * kLog2e : 0.f;
         float m_used = -INFINITY;
         float l = 0.f;                             // the row sum
         for (int i = 0; ok && i < nx; ++i) {
@@ -622,7 +630,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // and the window edge) take the max of the raw scores, scaled once;
             // the others scale and mask every score (masked scores become -inf).
             float mx;
-            if constexpr (kScore) score_tile(sv, sc, slope2, pos - k0);
+            if constexpr (kScore) score_tile(sv, sc, tp, biased, slope2, pos - k0);
             if (full_vis) {
                 float m8[8];
 #pragma unroll

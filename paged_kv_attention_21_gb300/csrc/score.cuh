@@ -14,7 +14,7 @@ constexpr float kTanhPoly = 0.7f;
 
 // tanh(y) = y (1 + z P(z)), z = y^2, for |y| <= 0.7: P is the fit of least
 // relative error (reweighted least squares on Chebyshev nodes), off by 1.5e-8;
-// with fp32 arithmetic 8.5e-8 of the value.  1 - 2 / (e^2y + 1), used beyond,
+// with fp32 arithmetic 1e-7 of the value.  1 - 2 / (e^2y + 1), used beyond,
 // is off by about 1.5e-7 of 1 wherever it is evaluated: near 0 that would be an
 // absolute error of 1.5e-7 cap in every logit, 7e-6 for a cap of 50.
 constexpr float kTanhC0 = -0.3333319127559662f;
@@ -23,26 +23,17 @@ constexpr float kTanhC2 = -0.05355885997414589f;
 constexpr float kTanhC3 = 0.020091967657208443f;
 constexpr float kTanhC4 = -0.005138659384101629f;
 
-__device__ __forceinline__ float tanh_poly(float y) {
-    const float z = y * y;
-    float p = fmaf(z, kTanhC4, kTanhC3);
-    p = fmaf(z, p, kTanhC2);
-    p = fmaf(z, p, kTanhC1);
-    p = fmaf(z, p, kTanhC0);
-    return fmaf(y * z, p, y);
-}
-
 // For any y: e^2|y| overflows to inf from |y| = 44 on, where tanh is 1 to fp32.
 __device__ __forceinline__ float tanh_exp(float y) {
     const float e = fast_exp2(fabsf(y) * 2.8853900817779268f);
     return copysignf(1.f - __fdividef(2.f, e + 1.f), y);
 }
 
-__device__ __forceinline__ float tanh_any(float y) { return fabsf(y) <= kTanhPoly ? tanh_poly(y) : tanh_exp(y); }
-
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What a kernel needs of the rule for one KV head (kscale: the head's e4m3 scale, or 1).
+// A score's logit has the same bits whichever of the forms below computes it: which one
+// does may depend on the scores beside it.
 struct ScoreScale {
     float in;    // s -> y = sm_scale s / cap with a cap, else s -> log2 units
     float out;   // cap log2(e) with a cap, else 0
@@ -50,10 +41,61 @@ struct ScoreScale {
         in = cap > 0.f ? sm_scale * kscale / cap : sm_scale * kLog2e * kscale;
         out = cap > 0.f ? cap * kLog2e : 0.f;
     }
-    __device__ __forceinline__ float operator()(float s) const {
+    // out tanh(y) / y for |y| <= kTanhPoly: the factor `out` is in the coefficients
+    __device__ __forceinline__ float factor(float y) const {
+        const float z = y * y;
+        float p = fmaf(z, kTanhC4 * out, kTanhC3 * out);
+        p = fmaf(z, p, kTanhC2 * out);
+        p = fmaf(z, p, kTanhC1 * out);
+        p = fmaf(z, p, kTanhC0 * out);
+        return fmaf(z, p, out);
+    }
+    __device__ __forceinline__ float capped(float s) const {
         const float y = s * in;
-        return out > 0.f ? out * tanh_any(y) : y;
+        return fabsf(y) <= kTanhPoly ? y * factor(y) : out * tanh_exp(y);
+    }
+    __device__ __forceinline__ float capped(float s, float c) const {
+        const float y = s * in;
+        return fabsf(y) <= kTanhPoly ? fmaf(y, factor(y), c) : fmaf(out, tanh_exp(y), c);
+    }
+    __device__ __forceinline__ float operator()(float s) const { return out > 0.f ? capped(s) : s * in; }
+    __device__ __forceinline__ float operator()(float s, float c) const { return out > 0.f ? capped(s, c) : fmaf(s, in, c); }
+};
+
+// ScoreScale's capped(), two logits at a time, where every |y| <= kTanhPoly.
+struct TanhPair {
+    uint64_t in, c0, c1, c2, c3, c4, one;
+    __device__ __forceinline__ explicit TanhPair(const ScoreScale& sc) {
+        in = pack_f32x2(sc.in, sc.in);
+        auto twice = [&](float k) { return pack_f32x2(k * sc.out, k * sc.out); };
+        one = twice(1.f), c0 = twice(kTanhC0), c1 = twice(kTanhC1), c2 = twice(kTanhC2);
+        c3 = twice(kTanhC3), c4 = twice(kTanhC4);
+    }
+    __device__ __forceinline__ uint64_t factor(uint64_t y) const {  // out tanh(y) / y
+        const uint64_t z = mul_f32x2(y, y);
+        uint64_t p = fma_f32x2(z, c4, c3);
+        p = fma_f32x2(z, p, c2);
+        p = fma_f32x2(z, p, c1);
+        p = fma_f32x2(z, p, c0);
+        return fma_f32x2(z, p, one);
+    }
+    __device__ __forceinline__ uint64_t operator()(uint64_t s) const {
+        const uint64_t y = mul_f32x2(s, in);
+        return mul_f32x2(y, factor(y));
+    }
+    __device__ __forceinline__ uint64_t operator()(uint64_t s, uint64_t c) const {
+        const uint64_t y = mul_f32x2(s, in);
+        return fma_f32x2(y, factor(y), c);
     }
 };
+
+// Whether max |s| over the N scores lies where the polynomial holds (a NaN: not looked at).
+template <int N>
+__device__ __forceinline__ bool in_poly(const float (&v)[N], float in) {
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < N; e += 2) m[(e >> 1) & 3] = fmax3(m[(e >> 1) & 3], fabsf(v[e]), fabsf(v[e + 1]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * in <= kTanhPoly;
+}
 
 }  // namespace pkv
