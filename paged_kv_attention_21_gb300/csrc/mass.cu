@@ -34,17 +34,14 @@ __global__ void __launch_bounds__(kMassWarps * 32) mass_rows_kernel(const MassAr
     const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.mbps;
     float* mrow = a.mass + (static_cast<size_t>(seq) * a.hkv + kvh) * a.mass_stride;
     const int nblk = (s.kv_len + kBlockSize - 1) / kBlockSize;
+    int seen_lo, seen_hi;  // blocks that no query sees are not read
+    mass_seen(a, s, s.rows / G, seen_lo, seen_hi);
     for (int i = 0; i < kMassBlocksPerWarp; ++i) {
         const int blk = (static_cast<int>(blockIdx.x) * kMassBlocksPerWarp + i) * kMassWarps + warp;
         if (blk >= nblk) return;
         const int t0 = blk * kBlockSize;
-        // blocks that no query sees are not read
-        int first_lo, last_hi, tmp;
-        mass_span(a, s, s.off, first_lo, tmp);
-        mass_span(a, s, s.off + s.rows / G - 1, tmp, last_hi);
-        if (a.causal && s.off < s.prefix) last_hi = max(last_hi, min(s.prefix, s.kv_len) - 1);
         float sum0 = 0.f, sum1 = 0.f;
-        if (s.rows > 0 && t0 <= last_hi && t0 + kBlockSize > first_lo) {
+        if (t0 <= seen_hi && t0 + kBlockSize > seen_lo) {
             int id = bt[blk];
             if (id < 0 || id >= a.num_blocks) {
                 if (lane == 0) flag_error(a.err, PKV_DEVERR_BLOCK_ID);

@@ -42,13 +42,15 @@ __device__ __forceinline__ MassSeq mass_seq(const MassArgs& a, int seq, bool fla
     return s;
 }
 
-// The tokens [first, last] of the counted ones that see some key of [k0, k1]
-// (last < first: none).  hi and lo of mass_span both ascend with the position.
-__device__ __forceinline__ void mass_tokens(const MassArgs& a, const MassSeq& s, int k0, int k1, int& first, int& last) {
+// The tokens [first, last] of the first ntok that see some key of [k0, k1] (last < first:
+// none).  hi and lo of mass_span both ascend with the position.
+__device__ __forceinline__ void mass_tokens(const MassArgs& a, const MassSeq& s, int ntok, int k0, int k1, int& first,
+                                            int& last) {
     first = 0;
     if (a.causal && !(s.off < s.prefix && k0 < s.prefix)) first = max(0, k0 - s.off);
-    const int64_t end = a.window > 0 ? static_cast<int64_t>(k1) + a.window - 1 - s.off : INT32_MAX;
-    last = static_cast<int>(min(static_cast<int64_t>(s.rows / a.group) - 1, end));
+    last = ntok - 1;
+    // the last position that sees k1 is k1 + window - 1 (past 32 bits: every one does)
+    if (a.window > 0 && a.window - 1 < INT32_MAX - k1) last = min(last, k1 + a.window - 1 - s.off);
 }
 
 // The keys [lo, hi] that a query at position pos sees (hi < lo: none).
@@ -56,6 +58,15 @@ __device__ __forceinline__ void mass_span(const MassArgs& a, const MassSeq& s, i
     hi = s.kv_len - 1;
     if (a.causal) hi = min(hi, pos < s.prefix ? s.prefix - 1 : pos);
     lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+
+// The keys [lo, hi] outside of which none of the first ntok queries sees one.
+__device__ __forceinline__ void mass_seen(const MassArgs& a, const MassSeq& s, int ntok, int& lo, int& hi) {
+    int unused;
+    mass_span(a, s, s.off, lo, unused);
+    mass_span(a, s, s.off + ntok - 1, unused, hi);
+    if (a.causal && s.off < s.prefix) hi = max(hi, min(s.prefix, s.kv_len) - 1);
+    if (ntok <= 0) lo = 0, hi = -1;
 }
 
 }  // namespace pkv

@@ -13,9 +13,8 @@
 //          steps stay where they are, and a single one leaves its second stage's place
 //          to more key tiles in flight), and each step's constants per query row;
 //   1      MMA issuer: S of (step, tile) into the tile's TMEM buffer of 256 columns;
-//   2..17  epilogue: 2^(x - lse) summed over the columns, four warps a quarter of a
-//          step's columns; a warp takes its scores into registers at once and hands
-//          the buffer back before it computes.
+//   2..17  epilogue: 2^(x - lse) summed over the columns; eight warps for each tile of
+//          the pair, four for each half of a step's columns, 32 at a time.
 // e4m3 codes become bf16 in shared memory (exactly; the epilogue's warps convert a
 // tile as it lands), so that q stays as it is.
 #include "mass.cuh"
@@ -28,8 +27,7 @@ namespace {
 constexpr int kMtKeys = 128;                      // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBlockSize;
 constexpr int kMtCols = 256;                      // query rows per step: two tiles of 128
-constexpr int kMtGroups = 4;                      // of four epilogue warps: one per TMEM lane quarter
-constexpr int kMtEpiWarps = 4 * kMtGroups;
+constexpr int kMtEpiWarps = 16;
 constexpr int kMtThreads = (2 + kMtEpiWarps) * 32;
 
 template <int D, bool kFp8>
@@ -60,8 +58,8 @@ struct MtRows {
     float neg_lse[kMtCols];   // -log2(e) lse; -inf: the row adds nothing
     float slope[kMtCols];     // log2 units
     float tok[kMtCols];       // token index
-    int lo[kMtCols];          // the keys [lo, hi] that it sees; hi -1: no such row
-    int hi[kMtCols];
+    int2 span[kMtCols];       // the keys [x, y] that it sees; [0, -1]: no such row
+    int4 chunk[kMtCols / 32]; // of 32 columns: keys [x, y] that all see, [z, w] outside of which none does
 };
 
 // The weights of 32 columns, all seen by this key, without a bias, summed.
@@ -106,7 +104,8 @@ __device__ __forceinline__ float sum_edge(const float (&v)[32], const MtRows& q,
         float z = x[e];
         if (biased) z = fmaf(-q.slope[c], fabsf(q.tok[c] - tf), z);
         const float w = fast_exp2(z);
-        part[e & 1] += t >= q.lo[c] && t <= q.hi[c] ? w : 0.f;
+        const int2 sp = q.span[c];
+        part[e & 1] += t >= sp.x && t <= sp.y ? w : 0.f;
     }
     return part[0] + part[1];
 }
@@ -144,7 +143,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     __shared__ __align__(16) MtRows rows[2];
-    __shared__ float s_part[2][kMtGroups - 1][2][kMtKeys];
+    __shared__ float s_part[2][2][kMtKeys];
     __shared__ __align__(8) uint64_t bar_raw[C::kMaxRaw], bar_raw_empty[C::kMaxRaw];
     __shared__ __align__(8) uint64_t bar_k[C::kMaxK], bar_k_empty[C::kMaxK];
     __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_s_empty[2], bar_step[2], bar_fin;
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar_q[i], 2);  // the copies, and the rows' constants
             mbar_init(&bar_s[i], 1);
-            mbar_init(&bar_s_empty[i], kMtEpiWarps);
+            mbar_init(&bar_s_empty[i], kMtEpiWarps / 2);
             mbar_init(&bar_step[i], kMtEpiWarps);
         }
         for (int i = 0; i < C::kMaxK; ++i) {
@@ -202,19 +201,16 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     auto steps_of = [&](int kt, int& lo, int& hi) {
         const int nt = min(2, tile1 - kt);
         int first, last;
-        mass_tokens(a, s, kt * kMtKeys, min((kt + nt) * kMtKeys, s.kv_len) - 1, first, last);
-        lo = hi = 0;
-        if (last >= first && ntok > 0) {
-            lo = first / per_step;
-            hi = last / per_step + 1;
-        }
+        mass_tokens(a, s, ntok, kt * kMtKeys, min((kt + nt) * kMtKeys, s.kv_len) - 1, first, last);
+        const bool some = last >= first;
+        lo = some && nsteps_all > 1 ? first / per_step : 0;
+        hi = !some ? 0 : nsteps_all > 1 ? last / per_step + 1 : 1;
         return nt;
     };
-    auto block_seen = [&](int blk) {
-        int first, last;
-        mass_tokens(a, s, blk * kBlockSize, min(blk * kBlockSize + kBlockSize, s.kv_len) - 1, first, last);
-        return last >= first;
-    };
+    // keys outside of these are seen by no query: their blocks may be any
+    int seen_lo, seen_hi;
+    mass_seen(a, s, ntok, seen_lo, seen_hi);
+    auto block_seen = [&](int blk) { return blk * kBlockSize <= seen_hi && blk * kBlockSize + kBlockSize > seen_lo; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -222,6 +218,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         int step = 0;       // steps begun, as the MMA warp and the epilogue count them
         bool ok = true;
         int nq[2] = {0, 0};   // loads of each query stage
+        // this lane's rows of a 128-row tile: token and head of r = lane + 32 i
+        int row_tok[4], row_head[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            row_tok[i] = (lane + 32 * i) / G;
+            row_head[i] = (lane + 32 * i) % G;
+        }
         auto load_q = [&](int qs, int st) {
             const int t0 = qs * per_step;
             const int nt = ntok - t0 > QT ? 2 : 1;
@@ -232,13 +235,15 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                         tma_load_3d(smem + C::kOffQ + st * C::kQBytes + h * C::kQHalf + x * (128 * 128), &qmap,
                                     &bar_q[st], h * 64, kvh * G, s.q0 + t0 + x * QT);
             }
-            for (int c = lane; c < kMtCols; c += 32) {
-                const int r = c & 127, tok = t0 + (c >> 7) * QT + r / G;
-                const bool real = r < QT * G && tok < ntok;
+#pragma unroll
+            for (int i = 0; i < kMtCols / 32; ++i) {
+                const int c = lane + 32 * i;
+                const int tok = t0 + (i >> 2) * QT + row_tok[i & 3];
+                const bool real = row_tok[i & 3] < QT && tok < ntok;
                 float nl = -INFINITY, slope = 0.f;
                 int lo = 0, hi = -1;
                 if (real) {
-                    const int h = kvh * G + r % G;
+                    const int h = kvh * G + row_head[i & 3];
                     const float lse = a.lse[static_cast<size_t>(s.q0 + tok) * a.hq + h];
                     nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
                     if (a.slopes) slope = a.slopes[h] * kLog2e;
@@ -247,8 +252,11 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 rows[st].neg_lse[c] = nl;
                 rows[st].slope[c] = slope;
                 rows[st].tok[c] = static_cast<float>(tok);
-                rows[st].lo[c] = lo;
-                rows[st].hi[c] = hi;
+                rows[st].span[c] = make_int2(lo, hi);
+                const int all_lo = __reduce_max_sync(0xFFFFFFFFu, lo), all_hi = __reduce_min_sync(0xFFFFFFFFu, hi);
+                const int any_lo = __reduce_min_sync(0xFFFFFFFFu, real ? lo : INT32_MAX);
+                const int any_hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+                if (lane == 0) rows[st].chunk[i] = make_int4(all_lo, all_hi, any_lo, any_hi);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_q[st]);
@@ -256,18 +264,28 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         };
         if (resident)
             for (int qs = 0; qs < nsteps_all; ++qs) load_q(qs, qs);
-        auto load_keys = [&](int kt) {
-            // block ids: lane b < 8 has block b of the tile
-            const int blk = kt * kMtBlocks + lane;
-            const int nvalid = min(kMtBlocks, (s.kv_len + kBlockSize - 1) / kBlockSize - kt * kMtBlocks);
-            int id = 0;
-            if (lane < nvalid && block_seen(blk)) {
-                id = bt[blk];
-                if (id < 0 || id >= a.num_blocks) {
-                    flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-                    id = 0;  // read a valid block; the keys' weights are not written
-                }
+        // block ids: lane l has block l % 8 of tile l / 8 of a group of four tiles; the next
+        // group's are read one group ahead
+        const int nblk = (s.kv_len + kBlockSize - 1) / kBlockSize;
+        auto read_ids = [&](int grp) {
+            const int blk = (tile0 + 4 * grp) * kMtBlocks + lane;
+            return blk < min(nblk, tile1 * kMtBlocks) && block_seen(blk) ? __ldg(bt + blk) : 0;
+        };
+        auto check_ids = [&](int id) {
+            if (id < 0 || id >= a.num_blocks) {
+                flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                id = 0;  // read a valid block; the keys' weights are not written
             }
+            return id;
+        };
+        int ids_grp = 0, ids = check_ids(read_ids(0)), ids_next = read_ids(1);
+        auto load_keys = [&](int kt) {
+            while (ids_grp < (kt - tile0) >> 2) {
+                ids = check_ids(ids_next);
+                ids_next = read_ids(++ids_grp + 1);
+            }
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, ((kt - tile0) & 3) * kMtBlocks + (lane & (kMtBlocks - 1)));
+            const int nvalid = min(kMtBlocks, nblk - kt * kMtBlocks);
             if constexpr (kFp8) {
                 const int st = nload % nraw;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw_empty[st], ((nload / nraw) & 1) ^ 1, kWaitLimitNs, abort)))
@@ -369,35 +387,30 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         tc::fence_after_sync();
     } else {
         // ------------------------------------------------------------ epilogue
-        const int ew = warp - 2, grp = ew >> 2;
+        const int ew = warp - 2, x = ew >> 3, second = (ew >> 2) & 1;  // tile of the pair, half of the columns
         const int key = (warp & 3) * 32 + lane;  // the TMEM lane this thread may read
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t s_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * kMtCols;
         const ScoreScale sc(a.sm_scale, a.cap, kFp8 ? a.k_scale[kvh] : 1.f);
         const bool capped = sc.out > 0.f, biased = a.slopes != nullptr;
         const TanhPair tp(sc);
         const uint64_t scl = pack_f32x2(sc.in, sc.in);
         float* mrow = a.mass + (static_cast<size_t>(seq) * a.hkv + kvh) * a.mass_stride;
-        int nload = 0, step = 0, turn = 0, used[2] = {0, 0};
-        bool ok = true;
+        int nload = 0, step = 0, turn = 0, used = 0;
+        bool ok = true, q_here = false;
         for (int kt = tile0; kt < tile1; kt += 2, ++turn) {
             int slo, shi;
             const int nt = steps_of(kt, slo, shi);
-            float old[2] = {0.f, 0.f}, sum[2] = {0.f, 0.f};
-            bool write[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = (kt + x) * kMtKeys + key;
-                write[x] = x < nt && t < s.kv_len;
-                if (grp == 0 && write[x]) {
-                    if (a.keep != 0.f && t < s.off) old[x] = a.keep * mrow[t];
-                    if (slo < shi && block_seen(t / kBlockSize)) {
-                        const int id = bt[t / kBlockSize];
-                        write[x] = id >= 0 && id < a.num_blocks;
-                    }
-                }
+            const int k0 = (kt + x) * kMtKeys, t = k0 + key;
+            const int k_last = min(k0 + kMtKeys, s.kv_len) - 1;
+            float old = 0.f, sum = 0.f;
+            int id = 0;
+            const bool mine = !second && t < s.kv_len && x < nt;
+            if (mine) {
+                if (a.keep != 0.f && t < s.off) old = a.keep * mrow[t];
+                if (slo < shi && block_seen(t / kBlockSize)) id = bt[t / kBlockSize];
             }
             if constexpr (kFp8) {
-                for (int x = 0; ok && slo < shi && x < nt; ++x) {
+                for (int y = 0; ok && slo < shi && y < nt; ++y) {
                     const int rs = nload % nraw, ks = nload % nk;
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw[rs], (nload / nraw) & 1, kWaitLimitNs, abort) &&
                                                      mbar_wait(&bar_k_empty[ks], ((nload / nk) & 1) ^ 1, kWaitLimitNs,
@@ -416,59 +429,47 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             }
             for (int qs = slo; ok && qs < shi; ++qs, ++step) {
                 const int st = resident ? qs : step & 1;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[st], resident ? 0 : (step >> 1) & 1, kWaitLimitNs, abort));
-                const MtRows& q = rows[st];
-                const bool wide = ntok - qs * per_step > QT;
-                const int c0 = grp * (wide ? 64 : 32);  // this group's columns
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (!ok || x >= nt) break;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_s[x], used[x] & 1, kWaitLimitNs, abort));
+                // (warps without a tile in this pair wait too: their arrival on bar_step must not
+                // run ahead of the step)
+                if (!resident || !q_here)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[st], resident ? 0 : (step >> 1) & 1, kWaitLimitNs, abort));
+                if (!ok) break;
+                if (x < nt) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_s[x], used & 1, kWaitLimitNs, abort));
                     if (!ok) break;
-                    ++used[x];
+                    ++used;
                     tc::fence_after_sync();
-                    float v[2][32];
-                    tc::ld32(lane_base + x * kMtCols + c0, v[0]);
-                    if (wide) tc::ld32(lane_base + x * kMtCols + c0 + 32, v[1]);
-                    tc::wait_ld();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_s_empty[x]);
-                    const int k0 = (kt + x) * kMtKeys, t = k0 + key;
-                    const int k_last = min(k0 + kMtKeys, s.kv_len) - 1;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        if (u == 1 && !wide) break;
-                        const int c = c0 + 32 * u;
-                        // hi and lo ascend over a tile's columns; those past its rows (hi = -1) come last
-                        const bool seen = q.hi[c + 31] >= 0 && q.hi[c] >= k_last && q.lo[c + 31] <= k0;
-                        const bool poly = !capped || __all_sync(0xFFFFFFFFu, in_poly(v[u], sc.in));
-                        if (seen && poly && !biased)
-                            sum[x] += capped ? sum_seen<true>(v[u], q.neg_lse + c, scl, tp)
-                                             : sum_seen<false>(v[u], q.neg_lse + c, scl, tp);
+                    const MtRows& q = rows[st];
+                    const int cols = ntok - qs * per_step > QT ? 128 : 64;  // of this half
+                    const int c_end = (second + 1) * cols;
+                    for (int c = second * cols; c < c_end; c += 32) {
+                        float v[32];
+                        tc::ld32(s_base + c, v);
+                        tc::wait_ld();
+                        if (c + 32 == c_end) {
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar_s_empty[x]);
+                        }
+                        const int4 ch = q.chunk[c >> 5];
+                        if (ch.z > k_last || ch.w < k0) continue;
+                        const bool poly = !capped || __all_sync(0xFFFFFFFFu, in_poly(v, sc.in));
+                        if (ch.x <= k0 && ch.y >= k_last && poly && !biased)
+                            sum += capped ? sum_seen<true>(v, q.neg_lse + c, scl, tp)
+                                          : sum_seen<false>(v, q.neg_lse + c, scl, tp);
                         else
-                            sum[x] += sum_edge(v[u], q, c, sc, tp, poly, biased, static_cast<float>(t - s.off), t);
+                            sum += sum_edge(v, q, c, sc, tp, poly, biased, static_cast<float>(t - s.off), t);
                     }
                 }
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(&bar_step[step & 1]);
+                if (!resident && lane == 0) mbar_arrive(&bar_step[step & 1]);
             }
+            q_here = q_here || (slo == 0 && shi == nsteps_all);
             if (!ok && lane == 0) atomicOr(&s_fail, 1);
-            // the groups' sums meet, in their order; a warp that gave up comes here for every pair all the same
-            if (grp) {
-                s_part[turn & 1][grp - 1][0][key] = sum[0];
-                s_part[turn & 1][grp - 1][1][key] = sum[1];
-            }
+            // the halves' sums meet; a warp that gave up comes here for every pair all the same
+            if (second) s_part[turn & 1][x][key] = sum;
             asm volatile("bar.sync 1, %0;" ::"n"(kMtEpiWarps * 32) : "memory");
-            const bool good = *abort == 0;
-            if (!grp) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                    for (int i = 0; i < kMtGroups - 1; ++i) sum[x] += s_part[turn & 1][i][x][key];
-                    if (write[x] && good) mrow[(kt + x) * kMtKeys + key] = old[x] + sum[x];
-                }
-            }
+            if (mine && id >= 0 && id < a.num_blocks && *abort == 0) mrow[t] = old + (sum + s_part[turn & 1][x][key]);
         }
         if (!ok && lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
     }
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
 template <int D, bool kFp8>
 cudaError_t launch_mass_tc_t(const MassArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, cudaStream_t stream) {
     using C = MtCfg<D, kFp8>;
-    static_assert(C::kSmemBytes <= 227 * 1024 - 17 * 1024, "shared memory: the arena, the rows' constants, the barriers");
+    static_assert(C::kSmemBytes <= 227 * 1024 - 14 * 1024, "shared memory: the arena, the rows' constants, the barriers");
     auto kern = mass_tc_kernel<D, kFp8>;
     static bool attr_set[64] = {};
     int dev = 0;
