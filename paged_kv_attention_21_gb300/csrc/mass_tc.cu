@@ -6,9 +6,10 @@
 // (its TMEM lane), so a key's sum over the queries is a sum over columns in one
 // register, and the same constants (a query's lse) serve all lanes of a warp.
 //
-// One CTA owns consecutive tiles of 128 keys of one (sequence, KV head) and takes them two
-// at a time over the steps of 256 query rows that see them: a step's 64 KB of q come from
-// L2 once for 256 keys (one tile at a time was bound by those reads).  Warps:
+// One CTA per SM takes an equal part of the work, cut along (sequence, KV head, pair of key
+// tiles) with a sequence's pairs weighted by its steps of 256 query rows; it goes, pair by
+// pair, over the steps that see it: a step's 64 KB of q come from L2 once for 256 keys (one
+// tile at a time was bound by those reads).  Warps:
 //   0      TMA: the key tiles (two stages), the query steps (two stages; at most two
 //          steps stay where they are, and a single one leaves its second stage's place
 //          to more key tiles in flight), and each step's constants per query row;
@@ -64,7 +65,9 @@ struct MtRows {
 
 // The weights of 32 columns, all seen by this key, without a bias, summed.
 template <bool kCap>
-__device__ __forceinline__ float sum_seen(const float (&v)[32], const float* neg_lse, uint64_t scl, const TanhPair& tp) {
+__device__ __forceinline__ float sum_seen(const float (&v)[32], const float* neg_lse, const ScoreScale& sc,
+                                          const TanhPair& tp) {
+    const uint64_t scl = pack_f32x2(sc.in, sc.in);
     uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
     for (int u = 0; u < 16; u += 2) {
@@ -134,9 +137,97 @@ __device__ __forceinline__ void convert_keys(const uint8_t* raw, uint8_t* dst, i
     }
 }
 
+// The cost of a sequence's key-tile pairs, summed over the heads, as the work is cut over
+// the CTAs: a pair's steps, and what a pair costs without any.
+struct MtCost {
+    int pairs, weight;  // per head; of a pair
+    __device__ __forceinline__ MtCost(const MassSeq& s, int group, int per_step) {
+        pairs = s.ok ? (s.kv_len + 2 * kMtKeys - 1) / (2 * kMtKeys) : 0;
+        weight = 2 + 3 * ((s.rows / group + per_step - 1) / per_step);
+    }
+    __device__ __forceinline__ int64_t all(int hkv) const { return static_cast<int64_t>(pairs) * weight * hkv; }
+};
+
+// A CTA's part of the work: pairs of key tiles, in the order (sequence, head, pair), whose
+// costs before them lie in [lo, hi) of the whole.  Every warp walks it by itself.
+struct MtWalk {
+    const MassArgs& a;
+    int64_t base, hi;
+    int seq, kvh, pair, pairs, weight, per_step;
+    MassSeq s;
+    int ntok, nsteps, seen_lo, seen_hi;
+    bool resident, fresh;  // fresh: the first pair of a (sequence, head)
+    __device__ __forceinline__ MtWalk(const MassArgs& args, int seq0, int64_t base0, int64_t lo, int64_t hi_)
+        : a(args), base(base0), hi(hi_), seq(seq0), per_step(2 * args.q_tile) {
+        load();
+        const int64_t item = (lo - base + weight - 1) / weight;
+        kvh = static_cast<int>(item / pairs);
+        pair = static_cast<int>(item % pairs) - 1;  // next() comes first
+        base += item * weight;
+        if (pair < 0) {  // a head's first pair
+            --kvh;
+            pair = pairs - 1;
+        }
+        fresh = false;
+        first_ = true;
+    }
+    __device__ __forceinline__ bool next() {
+        fresh = first_;
+        first_ = false;
+        if (++pair == pairs) {
+            pair = 0;
+            ++kvh;
+            fresh = true;
+        }
+        while (kvh == a.hkv) {  // (sequences without work have no pairs)
+            if (base >= hi || ++seq >= a.num_seqs) return false;
+            load();
+            kvh = pairs > 0 ? 0 : a.hkv;
+        }
+        if (base >= hi) return false;
+        base += weight;
+        return true;
+    }
+    // the steps [lo, hi) that see the pair's key tiles, and how many these are
+    __device__ __forceinline__ int steps(int& lo, int& hi_) const {
+        const int k0 = pair * 2 * kMtKeys;
+        int first, last;
+        mass_tokens(a, s, ntok, k0, min(k0 + 2 * kMtKeys, s.kv_len) - 1, first, last);
+        const bool some = last >= first;
+        lo = some && nsteps > 1 ? first / per_step : 0;
+        hi_ = !some ? 0 : nsteps > 1 ? last / per_step + 1 : 1;
+        return s.kv_len - k0 > kMtKeys ? 2 : 1;
+    }
+    // blocks that no query sees are not read: their table entries may name none
+    __device__ __forceinline__ bool block_seen(int blk) const {
+        return blk * kBlockSize <= seen_hi && blk * kBlockSize + kBlockSize > seen_lo;
+    }
+
+   private:
+    bool first_;
+    __device__ __forceinline__ void load() {
+        s = mass_seq(a, seq, false);
+        const MtCost c(s, a.group, per_step);
+        pairs = c.pairs;
+        weight = c.weight;
+        ntok = s.rows / a.group;
+        nsteps = (ntok + per_step - 1) / per_step;
+        resident = nsteps <= 2;
+        mass_seen(a, s, ntok, seen_lo, seen_hi);
+    }
+};
+
+// Which stage the next step's (or a resident segment's) rows of q are in, as the producer,
+// the MMA warp and the epilogue each count it: uses[i] loads of stage i so far.
+struct MtStages {
+    int uses[2] = {0, 0}, turn = 0;
+    __device__ __forceinline__ int parity(int st) const { return (uses[st] - 1) & 1; }
+};
+
+// single: no sequence has more than one step, so that the second query stage holds keys.
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kMtThreads, 1)
-    mass_tc_kernel(const MassArgs a, const int tiles_per_cta, const __grid_constant__ CUtensorMap qmap,
+    mass_tc_kernel(const MassArgs a, const int single, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap) {
     using C = MtCfg<D, kFp8>;
     extern __shared__ uint8_t smem_raw[];
@@ -147,23 +238,17 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     __shared__ __align__(8) uint64_t bar_raw[C::kMaxRaw], bar_raw_empty[C::kMaxRaw];
     __shared__ __align__(8) uint64_t bar_k[C::kMaxK], bar_k_empty[C::kMaxK];
     __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_s_empty[2], bar_step[2], bar_fin;
+    __shared__ int64_t s_cost[kMtThreads / 32];
+    __shared__ int64_t s_base;
+    __shared__ int s_seq;
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
     pdl_wait();
     pdl_launch_dependents();
-    const int seq = blockIdx.z, kvh = blockIdx.y, G = a.group, QT = a.q_tile;
-    const MassSeq s = mass_seq(a, seq, blockIdx.x == 0 && threadIdx.x == 0 && kvh == 0);
-    const int ntiles = s.ok ? (s.kv_len + kMtKeys - 1) / kMtKeys : 0;
-    const int tile0 = static_cast<int>(blockIdx.x) * tiles_per_cta;
-    const int tile1 = min(ntiles, tile0 + tiles_per_cta);
-    if (tile0 >= tile1) return;
-    const int ntok = s.rows / G;
-    const int per_step = 2 * QT;
-    const int nsteps_all = (ntok + per_step - 1) / per_step;
-    const bool resident = nsteps_all <= 2;
-    const int nk = nsteps_all <= 1 ? C::kMaxK : 2, nraw = nsteps_all <= 1 ? C::kMaxRaw : 1;
+    const int G = a.group, QT = a.q_tile, per_step = 2 * QT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nk = single ? C::kMaxK : 2, nraw = single ? C::kMaxRaw : 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kMaxRaw; ++i) {
@@ -182,9 +267,49 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         }
         mbar_init(&bar_fin, 1);
         s_fail = 0;
+        s_seq = -1;
         tma_prefetch_desc(&qmap);
         tma_prefetch_desc(&kmap);
     }
+    // The cut: thread i sums the costs of its part of the sequences; the CTA's part of the
+    // whole begins in the part of one thread, which finds the sequence.
+    int64_t lo, hi;
+    {
+        const int per = (a.num_seqs + kMtThreads - 1) / kMtThreads;
+        const int s0 = min(a.num_seqs, static_cast<int>(threadIdx.x) * per), s1 = min(a.num_seqs, s0 + per);
+        int64_t mine = 0;
+        for (int i = s0; i < s1; ++i) mine += MtCost(mass_seq(a, i, blockIdx.x == 0), G, per_step).all(a.hkv);
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        if (lane == 31) s_cost[warp] = upto;
+        __syncthreads();
+        int64_t total = 0;
+        for (int w = 0; w < kMtThreads / 32; ++w) {
+            if (w == warp) upto += total;
+            total += s_cost[w];
+        }
+        const int64_t n = gridDim.x, part = total / n, rest = total % n, c = blockIdx.x;
+        lo = part * c + min(c, rest);
+        hi = lo + part + (c < rest ? 1 : 0);
+        int64_t base = upto - mine;
+        if (mine > 0 && base <= lo && lo < upto) {
+            for (int i = s0; i < s1; ++i) {
+                const int64_t cost = MtCost(mass_seq(a, i, false), G, per_step).all(a.hkv);
+                if (lo < base + cost) {
+                    s_seq = i;
+                    s_base = base;
+                    break;
+                }
+                base += cost;
+            }
+        }
+    }
+    __syncthreads();
+    if (lo >= hi || s_seq < 0) return;
     if (warp == 1) {
         tc::tmem_alloc(&s_tmem, 512);
         tc::tmem_relinquish();
@@ -195,29 +320,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
     const volatile int* abort = &s_fail;
-    const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.mbps;
-
-    // the steps [lo, hi) that see the pair of key tiles kt, kt + 1; how many of these there are
-    auto steps_of = [&](int kt, int& lo, int& hi) {
-        const int nt = min(2, tile1 - kt);
-        int first, last;
-        mass_tokens(a, s, ntok, kt * kMtKeys, min((kt + nt) * kMtKeys, s.kv_len) - 1, first, last);
-        const bool some = last >= first;
-        lo = some && nsteps_all > 1 ? first / per_step : 0;
-        hi = !some ? 0 : nsteps_all > 1 ? last / per_step + 1 : 1;
-        return nt;
-    };
-    // keys outside of these are seen by no query: their blocks may be any
-    int seen_lo, seen_hi;
-    mass_seen(a, s, ntok, seen_lo, seen_hi);
-    auto block_seen = [&](int blk) { return blk * kBlockSize <= seen_hi && blk * kBlockSize + kBlockSize > seen_lo; };
+    MtWalk w(a, s_seq, s_base, lo, hi);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        int nload = 0;      // key tiles loaded
-        int step = 0;       // steps begun, as the MMA warp and the epilogue count them
+        int nload = 0;  // key tiles loaded
         bool ok = true;
-        int nq[2] = {0, 0};   // loads of each query stage
+        MtStages q;
         // this lane's rows of a 128-row tile: token and head of r = lane + 32 i
         int row_tok[4], row_head[4];
 #pragma unroll
@@ -225,51 +334,56 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             row_tok[i] = (lane + 32 * i) / G;
             row_head[i] = (lane + 32 * i) % G;
         }
+        // step qs into stage st, once the epilogue is done with what was there
         auto load_q = [&](int qs, int st) {
+            if (q.uses[st] > 0 &&
+                !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_step[st], q.parity(st), kWaitLimitNs, abort)))
+                return false;
             const int t0 = qs * per_step;
-            const int nt = ntok - t0 > QT ? 2 : 1;
+            const int nt = w.ntok - t0 > QT ? 2 : 1;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bar_q[st], nt * C::kHalves * 64 * 2 * G * QT);
                 for (int x = 0; x < nt; ++x)
                     for (int h = 0; h < C::kHalves; ++h)
                         tma_load_3d(smem + C::kOffQ + st * C::kQBytes + h * C::kQHalf + x * (128 * 128), &qmap,
-                                    &bar_q[st], h * 64, kvh * G, s.q0 + t0 + x * QT);
+                                    &bar_q[st], h * 64, w.kvh * G, w.s.q0 + t0 + x * QT);
             }
 #pragma unroll
             for (int i = 0; i < kMtCols / 32; ++i) {
                 const int c = lane + 32 * i;
                 const int tok = t0 + (i >> 2) * QT + row_tok[i & 3];
-                const bool real = row_tok[i & 3] < QT && tok < ntok;
+                const bool real = row_tok[i & 3] < QT && tok < w.ntok;
                 float nl = -INFINITY, slope = 0.f;
-                int lo = 0, hi = -1;
+                int klo = 0, khi = -1;
                 if (real) {
-                    const int h = kvh * G + row_head[i & 3];
-                    const float lse = a.lse[static_cast<size_t>(s.q0 + tok) * a.hq + h];
+                    const int h = w.kvh * G + row_head[i & 3];
+                    const float lse = a.lse[static_cast<size_t>(w.s.q0 + tok) * a.hq + h];
                     nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
                     if (a.slopes) slope = a.slopes[h] * kLog2e;
-                    mass_span(a, s, s.off + tok, lo, hi);
+                    mass_span(a, w.s, w.s.off + tok, klo, khi);
                 }
                 rows[st].neg_lse[c] = nl;
                 rows[st].slope[c] = slope;
                 rows[st].tok[c] = static_cast<float>(tok);
-                rows[st].span[c] = make_int2(lo, hi);
-                const int all_lo = __reduce_max_sync(0xFFFFFFFFu, lo), all_hi = __reduce_min_sync(0xFFFFFFFFu, hi);
-                const int any_lo = __reduce_min_sync(0xFFFFFFFFu, real ? lo : INT32_MAX);
-                const int any_hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+                rows[st].span[c] = make_int2(klo, khi);
+                const int all_lo = __reduce_max_sync(0xFFFFFFFFu, klo), all_hi = __reduce_min_sync(0xFFFFFFFFu, khi);
+                const int any_lo = __reduce_min_sync(0xFFFFFFFFu, real ? klo : INT32_MAX);
+                const int any_hi = __reduce_max_sync(0xFFFFFFFFu, khi);
                 if (lane == 0) rows[st].chunk[i] = make_int4(all_lo, all_hi, any_lo, any_hi);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_q[st]);
-            ++nq[st];
+            ++q.uses[st];
+            return true;
         };
-        if (resident)
-            for (int qs = 0; qs < nsteps_all; ++qs) load_q(qs, qs);
         // block ids: lane l has block l % 8 of tile l / 8 of a group of four tiles; the next
         // group's are read one group ahead
-        const int nblk = (s.kv_len + kBlockSize - 1) / kBlockSize;
+        int ids_grp = 0, ids = 0, ids_next = 0;
         auto read_ids = [&](int grp) {
-            const int blk = (tile0 + 4 * grp) * kMtBlocks + lane;
-            return blk < min(nblk, tile1 * kMtBlocks) && block_seen(blk) ? __ldg(bt + blk) : 0;
+            const int blk = 4 * grp * kMtBlocks + lane;
+            return blk * kBlockSize < w.s.kv_len && w.block_seen(blk)
+                       ? __ldg(a.block_tables + static_cast<size_t>(w.seq) * a.mbps + blk)
+                       : 0;
         };
         auto check_ids = [&](int id) {
             if (id < 0 || id >= a.num_blocks) {
@@ -278,14 +392,15 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             }
             return id;
         };
-        int ids_grp = 0, ids = check_ids(read_ids(0)), ids_next = read_ids(1);
         auto load_keys = [&](int kt) {
-            while (ids_grp < (kt - tile0) >> 2) {
-                ids = check_ids(ids_next);
-                ids_next = read_ids(++ids_grp + 1);
+            const int grp = kt >> 2;
+            if (grp != ids_grp) {
+                ids = check_ids(grp == ids_grp + 1 ? ids_next : read_ids(grp));
+                ids_next = read_ids(grp + 1);
+                ids_grp = grp;
             }
-            const int id = __shfl_sync(0xFFFFFFFFu, ids, ((kt - tile0) & 3) * kMtBlocks + (lane & (kMtBlocks - 1)));
-            const int nvalid = min(kMtBlocks, nblk - kt * kMtBlocks);
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, (kt & 3) * kMtBlocks + (lane & (kMtBlocks - 1)));
+            const int nvalid = min(kMtBlocks, (w.s.kv_len + kBlockSize - 1) / kBlockSize - kt * kMtBlocks);
             if constexpr (kFp8) {
                 const int st = nload % nraw;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw_empty[st], ((nload / nraw) & 1) ^ 1, kWaitLimitNs, abort)))
@@ -293,7 +408,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&bar_raw[st], nvalid * (C::kBlkBytes / 2));
                 __syncwarp();
                 if (lane < nvalid)
-                    tma_load_4d(smem + C::raw_stage(st) + lane * (C::kBlkBytes / 2), &kmap, &bar_raw[st], 0, 0, kvh, id);
+                    tma_load_4d(smem + C::raw_stage(st) + lane * (C::kBlkBytes / 2), &kmap, &bar_raw[st], 0, 0, w.kvh, id);
             } else {
                 const int st = nload % nk;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_k_empty[st], ((nload / nk) & 1) ^ 1, kWaitLimitNs, abort)))
@@ -301,33 +416,41 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&bar_k[st], nvalid * C::kBlkBytes);
                 __syncwarp();
                 if (lane < nvalid)
-                    tma_load_5d(smem + C::k_stage(st) + lane * C::kBlkBytes, &kmap, &bar_k[st], 0, 0, 0, 0, id * a.hkv + kvh);
+                    tma_load_5d(smem + C::k_stage(st) + lane * C::kBlkBytes, &kmap, &bar_k[st], 0, 0, 0, 0,
+                                id * a.hkv + w.kvh);
             }
             ++nload;
             return true;
         };
-        for (int kt = tile0; ok && kt < tile1; kt += 2) {
-            int lo, hi;
-            const int nt = steps_of(kt, lo, hi);
-            if (lo >= hi) continue;  // no query sees them: nothing of them is read
-            ok = load_keys(kt);
-            if (resident) {
-                if (ok && nt > 1) ok = load_keys(kt + 1);
-                continue;
+        bool q_due = false;  // a resident segment's rows are not loaded yet
+        while (ok && w.next()) {
+            const int kt = 2 * w.pair;
+            if (w.fresh) {
+                q_due = true;
+                ids_grp = kt >> 2;
+                ids = check_ids(read_ids(ids_grp));
+                ids_next = read_ids(ids_grp + 1);
             }
-            for (int qs = lo; ok && qs < hi; ++qs, ++step) {
-                // the stage's last step has been read from TMEM for the pair's last tile, which every
-                // step has an arrival of: its MMAs and its constants are done with
-                const int st = step & 1;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_step[st], ((step >> 1) & 1) ^ 1, kWaitLimitNs, abort));
-                if (ok) load_q(qs, st);
-                if (ok && qs == lo && nt > 1) ok = load_keys(kt + 1);
+            int slo, shi;
+            const int nt = w.steps(slo, shi);
+            if (slo >= shi) continue;  // no query sees the pair: nothing of it is read
+            if (w.resident) {
+                ok = load_keys(kt) && (nt == 1 || load_keys(kt + 1));
+                for (int qs = 0; ok && q_due && qs < w.nsteps; ++qs) ok = load_q(qs, qs);
+                q_due = false;
+            } else {
+                ok = load_keys(kt);
+                for (int qs = slo; ok && qs < shi; ++qs) {
+                    ok = load_q(qs, q.turn);
+                    q.turn ^= 1;
+                    if (ok && qs == slo && nt > 1) ok = load_keys(kt + 1);
+                }
             }
         }
         if (!ok && lane == 0) atomicOr(&s_fail, 1);
         // drain: every copy issued has landed before this CTA exits
         for (int i = 0; i < 2; ++i)
-            if (nq[i] > 0) (void)mbar_wait(&bar_q[i], (nq[i] - 1) & 1);
+            if (q.uses[i] > 0) (void)mbar_wait(&bar_q[i], q.parity(i));
         if constexpr (kFp8) {
             for (int j = max(0, nload - nraw); j < nload; ++j) (void)mbar_wait(&bar_raw[j % nraw], (j / nraw) & 1);
         } else {
@@ -338,26 +461,37 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         // ---------------------------------------------------------- MMA issuer
         constexpr uint32_t kWide = tc::idesc_bf16_f32(kMtKeys, 256, false, false);
         constexpr uint32_t kHalf = tc::idesc_bf16_f32(kMtKeys, 128, false, false);
-        int nload = 0, step = 0, used[2] = {0, 0};  // S buffer x: times used
-        bool ok = true;
-        for (int kt = tile0; ok && kt < tile1; kt += 2) {
-            int lo, hi;
-            const int nt = steps_of(kt, lo, hi);
-            for (int qs = lo; ok && qs < hi; ++qs, ++step) {
-                const int st = resident ? qs : step & 1;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[st], resident ? 0 : (step >> 1) & 1, kWaitLimitNs, abort));
+        int nload = 0, used[2] = {0, 0};  // key tiles; S buffer x: times used
+        bool ok = true, q_due = false;
+        MtStages q;
+        while (ok && w.next()) {
+            q_due = q_due || w.fresh;
+            int slo, shi;
+            const int nt = w.steps(slo, shi);
+            if (slo >= shi) continue;
+            if (w.resident && q_due)
+                for (int qs = 0; qs < w.nsteps; ++qs) ++q.uses[qs];
+            q_due = false;
+            for (int qs = slo; ok && qs < shi; ++qs) {
+                int st = qs;
+                if (!w.resident) {
+                    st = q.turn;
+                    ++q.uses[st];
+                    q.turn ^= 1;
+                }
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[st], q.parity(st), kWaitLimitNs, abort));
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (!ok || x >= nt) break;
                     const int ks = (nload + x) % nk;
-                    bool r = qs > lo || mbar_wait(&bar_k[ks], ((nload + x) / nk) & 1, kWaitLimitNs, abort);
+                    bool r = qs > slo || mbar_wait(&bar_k[ks], ((nload + x) / nk) & 1, kWaitLimitNs, abort);
                     r = r && mbar_wait(&bar_s_empty[x], (used[x] & 1) ^ 1, kWaitLimitNs, abort);
                     ok = __all_sync(0xFFFFFFFFu, r);
                     if (!ok) break;
                     ++used[x];
                     tc::fence_after_sync();
                     if (lane == 0) {
-                        const uint32_t idesc = ntok - qs * per_step > QT ? kWide : kHalf;
+                        const uint32_t idesc = w.ntok - qs * per_step > QT ? kWide : kHalf;
                         const uint32_t sk = smem_u32(smem + C::k_stage(ks));
                         const uint32_t sq = smem_u32(smem + C::kOffQ + st * C::kQBytes);
 #pragma unroll
@@ -369,12 +503,12 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                             tc::mma_bf16(tmem + x * kMtCols, ad, bd, idesc, kk > 0 ? 1u : 0u);
                         }
                         tc::commit(&bar_s[x]);
-                        if (qs == hi - 1) tc::commit(&bar_k_empty[ks]);
+                        if (qs == shi - 1) tc::commit(&bar_k_empty[ks]);
                     }
                     __syncwarp();
                 }
             }
-            if (lo < hi) nload += nt;
+            nload += nt;
         }
         if (!ok && lane == 0) {
             flag_error(a.err, PKV_DEVERR_TIMEOUT);
@@ -389,25 +523,43 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int ew = warp - 2, x = ew >> 3, second = (ew >> 2) & 1;  // tile of the pair, half of the columns
         const int key = (warp & 3) * 32 + lane;  // the TMEM lane this thread may read
-        const uint32_t s_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * kMtCols;
-        const ScoreScale sc(a.sm_scale, a.cap, kFp8 ? a.k_scale[kvh] : 1.f);
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * kMtCols;
+        ScoreScale sc(a.sm_scale, a.cap, 1.f);
+        TanhPair tp(sc);
+        const float in1 = sc.in;  // with a scale of 1
         const bool capped = sc.out > 0.f, biased = a.slopes != nullptr;
-        const TanhPair tp(sc);
-        const uint64_t scl = pack_f32x2(sc.in, sc.in);
-        float* mrow = a.mass + (static_cast<size_t>(seq) * a.hkv + kvh) * a.mass_stride;
-        int nload = 0, step = 0, turn = 0, used = 0;
-        bool ok = true, q_here = false;
-        for (int kt = tile0; kt < tile1; kt += 2, ++turn) {
+        int nload = 0, turn = 0, used = 0;
+        bool ok = true, q_due = false, q_held = false;  // a resident segment's rows are in use
+        MtStages q;
+        // a resident segment is over: its stages may be loaded anew
+        auto release = [&](int n) {
+            if (q_held && lane == 0)
+                for (int i = 0; i < n; ++i) mbar_arrive(&bar_step[i]);
+            q_held = false;
+        };
+        int held = 0;
+        while (w.next()) {
+            const int k0 = (2 * w.pair + x) * kMtKeys, t = k0 + key;
+            if (w.fresh) {
+                __syncwarp();
+                release(held);
+                q_due = true;
+                if constexpr (kFp8) {
+                    sc.in = in1 * a.k_scale[w.kvh];
+                    tp.in = pack_f32x2(sc.in, sc.in);
+                }
+            }
             int slo, shi;
-            const int nt = steps_of(kt, slo, shi);
-            const int k0 = (kt + x) * kMtKeys, t = k0 + key;
-            const int k_last = min(k0 + kMtKeys, s.kv_len) - 1;
+            const int nt = w.steps(slo, shi);
+            const int k_last = min(k0 + kMtKeys, w.s.kv_len) - 1;
+            float* mrow = a.mass + (static_cast<size_t>(w.seq) * a.hkv + w.kvh) * a.mass_stride;
             float old = 0.f, sum = 0.f;
             int id = 0;
-            const bool mine = !second && t < s.kv_len && x < nt;
+            const bool mine = !second && t < w.s.kv_len;
             if (mine) {
-                if (a.keep != 0.f && t < s.off) old = a.keep * mrow[t];
-                if (slo < shi && block_seen(t / kBlockSize)) id = bt[t / kBlockSize];
+                if (a.keep != 0.f && t < w.s.off) old = a.keep * mrow[t];
+                if (slo < shi && w.block_seen(t / kBlockSize))
+                    id = a.block_tables[static_cast<size_t>(w.seq) * a.mbps + t / kBlockSize];
             }
             if constexpr (kFp8) {
                 for (int y = 0; ok && slo < shi && y < nt; ++y) {
@@ -427,49 +579,62 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                     }
                 }
             }
-            for (int qs = slo; ok && qs < shi; ++qs, ++step) {
-                const int st = resident ? qs : step & 1;
-                // (warps without a tile in this pair wait too: their arrival on bar_step must not
-                // run ahead of the step)
-                if (!resident || !q_here)
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[st], resident ? 0 : (step >> 1) & 1, kWaitLimitNs, abort));
-                if (!ok) break;
+            if (w.resident && q_due && slo < shi) {
+                for (int qs = 0; ok && qs < w.nsteps; ++qs) {
+                    ++q.uses[qs];
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[qs], q.parity(qs), kWaitLimitNs, abort));
+                }
+                q_held = true;
+                held = w.nsteps;
+                q_due = false;
+            }
+            for (int qs = slo; ok && qs < shi; ++qs) {
+                int st = qs;
+                if (!w.resident) {
+                    // (warps without a tile in this pair wait too: their arrival on bar_step must not
+                    // run ahead of the step)
+                    st = q.turn;
+                    ++q.uses[st];
+                    q.turn ^= 1;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[st], q.parity(st), kWaitLimitNs, abort));
+                    if (!ok) break;
+                }
                 if (x < nt) {
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_s[x], used & 1, kWaitLimitNs, abort));
                     if (!ok) break;
                     ++used;
                     tc::fence_after_sync();
-                    const MtRows& q = rows[st];
-                    const int cols = ntok - qs * per_step > QT ? 128 : 64;  // of this half
+                    const MtRows& r = rows[st];
+                    const int cols = w.ntok - qs * per_step > QT ? 128 : 64;  // of this half
                     const int c_end = (second + 1) * cols;
                     for (int c = second * cols; c < c_end; c += 32) {
                         float v[32];
-                        tc::ld32(s_base + c, v);
+                        tc::ld32(s_addr + c, v);
                         tc::wait_ld();
                         if (c + 32 == c_end) {
                             tc::fence_before_sync();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bar_s_empty[x]);
                         }
-                        const int4 ch = q.chunk[c >> 5];
+                        const int4 ch = r.chunk[c >> 5];
                         if (ch.z > k_last || ch.w < k0) continue;
                         const bool poly = !capped || __all_sync(0xFFFFFFFFu, in_poly(v, sc.in));
                         if (ch.x <= k0 && ch.y >= k_last && poly && !biased)
-                            sum += capped ? sum_seen<true>(v, q.neg_lse + c, scl, tp)
-                                          : sum_seen<false>(v, q.neg_lse + c, scl, tp);
+                            sum += capped ? sum_seen<true>(v, r.neg_lse + c, sc, tp)
+                                          : sum_seen<false>(v, r.neg_lse + c, sc, tp);
                         else
-                            sum += sum_edge(v, q, c, sc, tp, poly, biased, static_cast<float>(t - s.off), t);
+                            sum += sum_edge(v, r, c, sc, tp, poly, biased, static_cast<float>(t - w.s.off), t);
                     }
                 }
                 __syncwarp();
-                if (!resident && lane == 0) mbar_arrive(&bar_step[step & 1]);
+                if (!w.resident && lane == 0) mbar_arrive(&bar_step[st]);
             }
-            q_here = q_here || (slo == 0 && shi == nsteps_all);
             if (!ok && lane == 0) atomicOr(&s_fail, 1);
             // the halves' sums meet; a warp that gave up comes here for every pair all the same
             if (second) s_part[turn & 1][x][key] = sum;
             asm volatile("bar.sync 1, %0;" ::"n"(kMtEpiWarps * 32) : "memory");
             if (mine && id >= 0 && id < a.num_blocks && *abort == 0) mrow[t] = old + (sum + s_part[turn & 1][x][key]);
+            ++turn;
         }
         if (!ok && lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
     }
@@ -496,14 +661,10 @@ cudaError_t launch_mass_tc_t(const MassArgs& a, const CUtensorMap& qmap, const C
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const int tiles = (a.max_kv + kMtKeys - 1) / kMtKeys;
-    const int steps = (a.max_q + 2 * a.q_tile - 1) / (2 * a.q_tile);
-    // Pairs of tiles per CTA: about 16 (pair, step)s, as long as that leaves four CTAs an SM.
-    const int64_t pairs = static_cast<int64_t>((tiles + 1) / 2) * a.hkv * a.num_seqs;
-    int per = (16 + steps - 1) / steps;
-    per = 2 * static_cast<int>(max(int64_t{1}, min(int64_t{per}, pairs / (4 * max(1, a.num_sms)))));
-    const dim3 grid((tiles + per - 1) / per, a.hkv, a.num_seqs);
-    return launch_pdl(kern, grid, dim3(kMtThreads), C::kSmemBytes, stream, a, per, qmap, kmap);
+    // one CTA an SM, fewer where there are fewer pairs
+    const int64_t pairs = static_cast<int64_t>((a.max_kv + 2 * kMtKeys - 1) / (2 * kMtKeys)) * a.hkv * a.num_seqs;
+    const dim3 grid(static_cast<unsigned>(min(int64_t{max(1, a.num_sms)}, pairs)));
+    return launch_pdl(kern, grid, dim3(kMtThreads), C::kSmemBytes, stream, a, a.max_q <= 2 * a.q_tile ? 1 : 0, qmap, kmap);
 }
 
 }  // namespace
