@@ -1,21 +1,20 @@
 // mass_tc.cu -- the weight that each cached key receives from many queries, on the
 // 5th-generation tensor cores (tcgen05 + TMEM + TMA).
 //
-// S^T = K Q^T with 128 keys as the rows of the MMA and up to 256 query rows (query
-// token x head of the KV group) as its columns: a thread of the epilogue owns one key
-// (its TMEM lane), so a key's sum over the queries is a sum over columns in one
-// register, and the same constants (a query's lse) serve all lanes of a warp.
+// S^T = K Q^T with 128 keys as the rows of the MMA and 128 query rows (query token x head
+// of the KV group) as its columns: a thread of the epilogue owns one key (its TMEM lane),
+// so a key's sum over the queries is a sum over columns in one register, and the same
+// constants (a query's lse) serve all lanes of a warp.
 //
-// One CTA per SM takes an equal part of the work, cut along (sequence, KV head, pair of key
-// tiles) with a sequence's pairs weighted by its steps of 256 query rows; it goes, pair by
-// pair, over the steps that see it: a step's 64 KB of q come from L2 once for 256 keys (one
-// tile at a time was bound by those reads).  Warps:
-//   0      TMA: the key tiles (two stages), the query steps (two stages; at most two
-//          steps stay where they are, and a single one leaves its second stage's place
-//          to more key tiles in flight), and each step's constants per query row;
-//   1      MMA issuer: S of (step, tile) into the tile's TMEM buffer of 256 columns;
-//   2..17  epilogue: 2^(x - lse) summed over the columns; eight warps for each tile of
-//          the pair, four for each half of a step's columns, 32 at a time.
+// One CTA per SM takes an equal part of the work, cut along (sequence, KV head, four key
+// tiles) with a sequence's fours weighted by its steps of 128 query rows; it goes, four by
+// four, over the steps that see them: a step's 32 KB of q come from L2 once for 512 keys
+// (one tile at a time was bound by those reads).  Warps:
+//   0      TMA: the key tiles (four stages), the query steps (two stages; at most two
+//          steps stay where they are), and each step's constants per query row;
+//   1      MMA issuer: S of (step, tile) into the tile's TMEM buffer of 128 columns;
+//   2..17  epilogue: 2^(x - lse) summed over the columns, 32 at a time; four warps for
+//          each tile of the four, which meet no others.
 // e4m3 codes become bf16 in shared memory (exactly; the epilogue's warps convert a
 // tile as it lands), so that q stays as it is.
 #include "mass.cuh"
@@ -27,8 +26,10 @@ namespace {
 
 constexpr int kMtKeys = 128;                      // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBlockSize;
-constexpr int kMtCols = 256;                      // query rows per step: two tiles of 128
-constexpr int kMtEpiWarps = 16;
+constexpr int kMtTiles = 4;                       // key tiles side by side
+constexpr int kMtSpan = kMtTiles * kMtKeys;
+constexpr int kMtCols = 128;                      // query rows per step
+constexpr int kMtEpiWarps = 4 * kMtTiles;
 constexpr int kMtThreads = (2 + kMtEpiWarps) * 32;
 
 template <int D, bool kFp8>
@@ -42,14 +43,8 @@ struct MtCfg {
     static constexpr int kRawBytes = kFp8 ? kMtKeys * D : 0;  // e4m3: a tile of codes
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + 2 * kQBytes;
-    static constexpr int kOffRaw = kOffK + 2 * kKBytes;
+    static constexpr int kOffRaw = kOffK + kMtTiles * kKBytes;
     static constexpr int kBody = kOffRaw + kRawBytes;
-    // stages of key tiles and (e4m3) of codes, with one query step or more; those
-    // beyond the first two (one) lie in the second query stage
-    static constexpr int kMaxK = kFp8 ? 2 : 4;
-    static constexpr int kMaxRaw = kFp8 ? 4 : 1;
-    __device__ static uint32_t k_stage(int i) { return i < 2 ? kOffK + i * kKBytes : kOffQ + kQBytes + (i - 2) * kKBytes; }
-    __device__ static uint32_t raw_stage(int i) { return i < 1 ? kOffRaw : kOffQ + kQBytes + (i - 1) * kRawBytes; }
     // at least 120 KB, so that one CTA has an SM and its 512 TMEM columns
     static constexpr int kSmemBytes = kBody + 1024 > 120 * 1024 ? kBody + 1024 : 120 * 1024;
 };
@@ -113,7 +108,7 @@ __device__ __forceinline__ float sum_edge(const float (&v)[32], const MtRows& q,
     return part[0] + part[1];
 }
 
-// A tile's codes to bf16, exactly, by the epilogue's threads, in the layout that the
+// A tile's codes to bf16, exactly, by the tile's four warps, in the layout that the
 // tile-group box writes: a block's rows in 8-row groups of 128-byte slices, 16-byte
 // chunks swizzled by the row.
 template <int D>
@@ -121,7 +116,7 @@ __device__ __forceinline__ void convert_keys(const uint8_t* raw, uint8_t* dst, i
     using C = MtCfg<D, true>;
     constexpr int kCh = D / 8;  // chunks of 8 dims of a row
 #pragma unroll 2
-    for (int i = thread; i < kMtKeys * kCh; i += kMtEpiWarps * 32) {
+    for (int i = thread; i < kMtKeys * kCh; i += 128) {
         const int row = i / kCh, ch = i % kCh, r8 = row & 7;
         const uint2 w = *reinterpret_cast<const uint2*>(raw + row * D + ch * 8);
         uint32_t f[4];
@@ -137,66 +132,65 @@ __device__ __forceinline__ void convert_keys(const uint8_t* raw, uint8_t* dst, i
     }
 }
 
-// The cost of a sequence's key-tile pairs, summed over the heads, as the work is cut over
-// the CTAs: a pair's steps, and what a pair costs without any.
+// The cost of a sequence's spans of four key tiles, as the work is cut over the CTAs: a
+// span's steps, and what a span costs without any.
 struct MtCost {
-    int pairs, weight;  // per head; of a pair
+    int spans, weight;  // spans per head; of a span
     __device__ __forceinline__ MtCost(const MassSeq& s, int group, int per_step) {
-        pairs = s.ok ? (s.kv_len + 2 * kMtKeys - 1) / (2 * kMtKeys) : 0;
-        weight = 2 + 3 * ((s.rows / group + per_step - 1) / per_step);
+        spans = s.ok ? (s.kv_len - 1) / kMtSpan + 1 : 0;
+        weight = 1 + 2 * ((s.rows / group + per_step - 1) / per_step);
     }
-    __device__ __forceinline__ int64_t all(int hkv) const { return static_cast<int64_t>(pairs) * weight * hkv; }
+    __device__ __forceinline__ int64_t all(int hkv) const { return static_cast<int64_t>(spans) * weight * hkv; }
 };
 
-// A CTA's part of the work: pairs of key tiles, in the order (sequence, head, pair), whose
-// costs before them lie in [lo, hi) of the whole.  Every warp walks it by itself.
+// A CTA's part of the work: the spans, in the order (sequence, head, span), whose costs
+// before them lie in [lo, hi) of the whole.  Every warp walks it by itself.
 struct MtWalk {
     const MassArgs& a;
     int64_t base, hi;
-    int seq, kvh, pair, pairs, weight, per_step;
+    int seq, kvh, span, spans, weight, per_step;
     MassSeq s;
     int ntok, nsteps, seen_lo, seen_hi;
-    bool resident, fresh;  // fresh: the first pair of a (sequence, head)
+    bool resident, fresh;  // fresh: the first span of a (sequence, head)
     __device__ __forceinline__ MtWalk(const MassArgs& args, int seq0, int64_t base0, int64_t lo, int64_t hi_)
-        : a(args), base(base0), hi(hi_), seq(seq0), per_step(2 * args.q_tile) {
+        : a(args), base(base0), hi(hi_), seq(seq0), per_step(args.q_tile), first_(true) {
         load();
         const int64_t item = (lo - base + weight - 1) / weight;
-        kvh = static_cast<int>(item / pairs);
-        pair = static_cast<int>(item % pairs) - 1;  // next() comes first
+        kvh = static_cast<int>(item / spans);
+        span = static_cast<int>(item % spans) - 1;  // next() comes first
         base += item * weight;
-        if (pair < 0) {  // a head's first pair
+        if (span < 0) {  // a head's first span
             --kvh;
-            pair = pairs - 1;
+            span = spans - 1;
         }
         fresh = false;
-        first_ = true;
     }
     __device__ __forceinline__ bool next() {
         fresh = first_;
         first_ = false;
-        if (++pair == pairs) {
-            pair = 0;
+        if (++span == spans) {
+            span = 0;
             ++kvh;
             fresh = true;
         }
-        while (kvh == a.hkv) {  // (sequences without work have no pairs)
+        while (kvh == a.hkv) {  // (sequences without work have no spans)
             if (base >= hi || ++seq >= a.num_seqs) return false;
             load();
-            kvh = pairs > 0 ? 0 : a.hkv;
+            kvh = spans > 0 ? 0 : a.hkv;
         }
         if (base >= hi) return false;
         base += weight;
         return true;
     }
-    // the steps [lo, hi) that see the pair's key tiles, and how many these are
+    // the steps [lo, hi) that see the span's keys, and how many tiles it has
     __device__ __forceinline__ int steps(int& lo, int& hi_) const {
-        const int k0 = pair * 2 * kMtKeys;
+        const int k0 = span * kMtSpan, left = s.kv_len - k0;
         int first, last;
-        mass_tokens(a, s, ntok, k0, min(k0 + 2 * kMtKeys, s.kv_len) - 1, first, last);
+        mass_tokens(a, s, ntok, k0, k0 + min(kMtSpan, left) - 1, first, last);
         const bool some = last >= first;
         lo = some && nsteps > 1 ? first / per_step : 0;
         hi_ = !some ? 0 : nsteps > 1 ? last / per_step + 1 : 1;
-        return s.kv_len - k0 > kMtKeys ? 2 : 1;
+        return min(kMtTiles, (left + kMtKeys - 1) / kMtKeys);
     }
     // blocks that no query sees are not read: their table entries may name none
     __device__ __forceinline__ bool block_seen(int blk) const {
@@ -208,7 +202,7 @@ struct MtWalk {
     __device__ __forceinline__ void load() {
         s = mass_seq(a, seq, false);
         const MtCost c(s, a.group, per_step);
-        pairs = c.pairs;
+        spans = c.spans;
         weight = c.weight;
         ntok = s.rows / a.group;
         nsteps = (ntok + per_step - 1) / per_step;
@@ -224,20 +218,17 @@ struct MtStages {
     __device__ __forceinline__ int parity(int st) const { return (uses[st] - 1) & 1; }
 };
 
-// single: no sequence has more than one step, so that the second query stage holds keys.
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kMtThreads, 1)
-    mass_tc_kernel(const MassArgs a, const int single, const __grid_constant__ CUtensorMap qmap,
+    mass_tc_kernel(const MassArgs a, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap) {
     using C = MtCfg<D, kFp8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     __shared__ __align__(16) MtRows rows[2];
-    __shared__ float s_part[2][2][kMtKeys];
-    __shared__ __align__(8) uint64_t bar_raw[C::kMaxRaw], bar_raw_empty[C::kMaxRaw];
-    __shared__ __align__(8) uint64_t bar_k[C::kMaxK], bar_k_empty[C::kMaxK];
-    __shared__ __align__(8) uint64_t bar_q[2], bar_s[2], bar_s_empty[2], bar_step[2], bar_fin;
+    __shared__ __align__(8) uint64_t bar_raw[kMtTiles], bar_raw_empty, bar_q[2], bar_step[2], bar_fin;
+    __shared__ __align__(8) uint64_t bar_k[kMtTiles], bar_k_empty[kMtTiles], bar_s[kMtTiles], bar_s_empty[kMtTiles];
     __shared__ int64_t s_cost[kMtThreads / 32];
     __shared__ int64_t s_base;
     __shared__ int s_seq;
@@ -246,24 +237,21 @@ __global__ void __launch_bounds__(kMtThreads, 1)
 
     pdl_wait();
     pdl_launch_dependents();
-    const int G = a.group, QT = a.q_tile, per_step = 2 * QT;
+    const int G = a.group, QT = a.q_tile, per_step = QT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nk = single ? C::kMaxK : 2, nraw = single ? C::kMaxRaw : 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kMaxRaw; ++i) {
-            mbar_init(&bar_raw[i], 1);
-            mbar_init(&bar_raw_empty[i], kMtEpiWarps);
-        }
+        mbar_init(&bar_raw_empty, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar_q[i], 2);  // the copies, and the rows' constants
-            mbar_init(&bar_s[i], 1);
-            mbar_init(&bar_s_empty[i], kMtEpiWarps / 2);
             mbar_init(&bar_step[i], kMtEpiWarps);
         }
-        for (int i = 0; i < C::kMaxK; ++i) {
-            mbar_init(&bar_k[i], kFp8 ? kMtEpiWarps : 1);
+        for (int i = 0; i < kMtTiles; ++i) {
+            mbar_init(&bar_raw[i], 1);
+            mbar_init(&bar_k[i], kFp8 ? 4 : 1);
             mbar_init(&bar_k_empty[i], 1);
+            mbar_init(&bar_s[i], 1);
+            mbar_init(&bar_s_empty[i], 4);
         }
         mbar_init(&bar_fin, 1);
         s_fail = 0;
@@ -324,10 +312,10 @@ __global__ void __launch_bounds__(kMtThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        int nload = 0;  // key tiles loaded
+        int nraw = 0, loads[kMtTiles] = {0, 0, 0, 0};  // key tiles: in all, and by stage
         bool ok = true;
         MtStages q;
-        // this lane's rows of a 128-row tile: token and head of r = lane + 32 i
+        // this lane's rows of a step: token and head of row lane + 32 i
         int row_tok[4], row_head[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -340,23 +328,21 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_step[st], q.parity(st), kWaitLimitNs, abort)))
                 return false;
             const int t0 = qs * per_step;
-            const int nt = w.ntok - t0 > QT ? 2 : 1;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&bar_q[st], nt * C::kHalves * 64 * 2 * G * QT);
-                for (int x = 0; x < nt; ++x)
-                    for (int h = 0; h < C::kHalves; ++h)
-                        tma_load_3d(smem + C::kOffQ + st * C::kQBytes + h * C::kQHalf + x * (128 * 128), &qmap,
-                                    &bar_q[st], h * 64, w.kvh * G, w.s.q0 + t0 + x * QT);
+                mbar_arrive_expect_tx(&bar_q[st], C::kHalves * 64 * 2 * G * QT);
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(smem + C::kOffQ + st * C::kQBytes + h * C::kQHalf, &qmap, &bar_q[st], h * 64, w.kvh * G,
+                                w.s.q0 + t0);
             }
 #pragma unroll
             for (int i = 0; i < kMtCols / 32; ++i) {
                 const int c = lane + 32 * i;
-                const int tok = t0 + (i >> 2) * QT + row_tok[i & 3];
-                const bool real = row_tok[i & 3] < QT && tok < w.ntok;
+                const int tok = t0 + row_tok[i];
+                const bool real = row_tok[i] < QT && tok < w.ntok;
                 float nl = -INFINITY, slope = 0.f;
                 int klo = 0, khi = -1;
                 if (real) {
-                    const int h = w.kvh * G + row_head[i & 3];
+                    const int h = w.kvh * G + row_head[i];
                     const float lse = a.lse[static_cast<size_t>(w.s.q0 + tok) * a.hq + h];
                     nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
                     if (a.slopes) slope = a.slopes[h] * kLog2e;
@@ -376,74 +362,62 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             ++q.uses[st];
             return true;
         };
-        // block ids: lane l has block l % 8 of tile l / 8 of a group of four tiles; the next
-        // group's are read one group ahead
-        int ids_grp = 0, ids = 0, ids_next = 0;
-        auto read_ids = [&](int grp) {
-            const int blk = 4 * grp * kMtBlocks + lane;
-            return blk * kBlockSize < w.s.kv_len && w.block_seen(blk)
+        // block ids: lane l has block l of the span; the next span's are read one ahead
+        int ids_span = 0, ids = 0, ids_next = 0;
+        auto read_ids = [&](int span) {
+            const int64_t blk = static_cast<int64_t>(span) * (kMtSpan / kBlockSize) + lane;
+            return blk * kBlockSize < w.s.kv_len && w.block_seen(static_cast<int>(blk))
                        ? __ldg(a.block_tables + static_cast<size_t>(w.seq) * a.mbps + blk)
                        : 0;
         };
-        auto check_ids = [&](int id) {
-            if (id < 0 || id >= a.num_blocks) {
-                flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-                id = 0;  // read a valid block; the keys' weights are not written
-            }
-            return id;
-        };
-        auto load_keys = [&](int kt) {
-            const int grp = kt >> 2;
-            if (grp != ids_grp) {
-                ids = check_ids(grp == ids_grp + 1 ? ids_next : read_ids(grp));
-                ids_next = read_ids(grp + 1);
-                ids_grp = grp;
-            }
-            const int id = __shfl_sync(0xFFFFFFFFu, ids, (kt & 3) * kMtBlocks + (lane & (kMtBlocks - 1)));
-            const int nvalid = min(kMtBlocks, (w.s.kv_len + kBlockSize - 1) / kBlockSize - kt * kMtBlocks);
+        // tile x of the span into stage x
+        auto load_keys = [&](int x) {
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, x * kMtBlocks + (lane & (kMtBlocks - 1)));
+            const int nvalid = min(kMtBlocks, (w.s.kv_len + kBlockSize - 1) / kBlockSize - (w.span * kMtTiles + x) * kMtBlocks);
             if constexpr (kFp8) {
-                const int st = nload % nraw;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw_empty[st], ((nload / nraw) & 1) ^ 1, kWaitLimitNs, abort)))
-                    return false;
-                if (lane == 0) mbar_arrive_expect_tx(&bar_raw[st], nvalid * (C::kBlkBytes / 2));
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw_empty, (nraw & 1) ^ 1, kWaitLimitNs, abort))) return false;
+                ++nraw;
+                ++loads[x];
+                if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], nvalid * (C::kBlkBytes / 2));
                 __syncwarp();
                 if (lane < nvalid)
-                    tma_load_4d(smem + C::raw_stage(st) + lane * (C::kBlkBytes / 2), &kmap, &bar_raw[st], 0, 0, w.kvh, id);
+                    tma_load_4d(smem + C::kOffRaw + lane * (C::kBlkBytes / 2), &kmap, &bar_raw[x], 0, 0, w.kvh, id);
             } else {
-                const int st = nload % nk;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_k_empty[st], ((nload / nk) & 1) ^ 1, kWaitLimitNs, abort)))
-                    return false;
-                if (lane == 0) mbar_arrive_expect_tx(&bar_k[st], nvalid * C::kBlkBytes);
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_k_empty[x], (loads[x] & 1) ^ 1, kWaitLimitNs, abort))) return false;
+                ++loads[x];
+                if (lane == 0) mbar_arrive_expect_tx(&bar_k[x], nvalid * C::kBlkBytes);
                 __syncwarp();
                 if (lane < nvalid)
-                    tma_load_5d(smem + C::k_stage(st) + lane * C::kBlkBytes, &kmap, &bar_k[st], 0, 0, 0, 0,
+                    tma_load_5d(smem + C::kOffK + x * C::kKBytes + lane * C::kBlkBytes, &kmap, &bar_k[x], 0, 0, 0, 0,
                                 id * a.hkv + w.kvh);
             }
-            ++nload;
             return true;
         };
         bool q_due = false;  // a resident segment's rows are not loaded yet
         while (ok && w.next()) {
-            const int kt = 2 * w.pair;
-            if (w.fresh) {
-                q_due = true;
-                ids_grp = kt >> 2;
-                ids = check_ids(read_ids(ids_grp));
-                ids_next = read_ids(ids_grp + 1);
-            }
             int slo, shi;
             const int nt = w.steps(slo, shi);
-            if (slo >= shi) continue;  // no query sees the pair: nothing of it is read
+            q_due = q_due || w.fresh;
+            if (slo >= shi) continue;  // no query sees the span: nothing of it is read
+            ids = !w.fresh && ids_span == w.span ? ids_next : read_ids(w.span);
+            ids_span = w.span + 1;
+            ids_next = read_ids(ids_span);
+            if (ids < 0 || ids >= a.num_blocks) {
+                flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                ids = 0;  // read a valid block; the keys' weights are not written
+            }
+            ok = load_keys(0);
             if (w.resident) {
-                ok = load_keys(kt) && (nt == 1 || load_keys(kt + 1));
                 for (int qs = 0; ok && q_due && qs < w.nsteps; ++qs) ok = load_q(qs, qs);
                 q_due = false;
+                for (int x = 1; ok && x < kMtTiles; ++x)
+                    if (x < nt) ok = load_keys(x);
             } else {
-                ok = load_keys(kt);
                 for (int qs = slo; ok && qs < shi; ++qs) {
                     ok = load_q(qs, q.turn);
                     q.turn ^= 1;
-                    if (ok && qs == slo && nt > 1) ok = load_keys(kt + 1);
+                    for (int x = 1; ok && qs == slo && x < kMtTiles; ++x)
+                        if (x < nt) ok = load_keys(x);
                 }
             }
         }
@@ -451,17 +425,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         // drain: every copy issued has landed before this CTA exits
         for (int i = 0; i < 2; ++i)
             if (q.uses[i] > 0) (void)mbar_wait(&bar_q[i], q.parity(i));
-        if constexpr (kFp8) {
-            for (int j = max(0, nload - nraw); j < nload; ++j) (void)mbar_wait(&bar_raw[j % nraw], (j / nraw) & 1);
-        } else {
-            for (int j = max(0, nload - nk); j < nload; ++j) (void)mbar_wait(&bar_k[j % nk], (j / nk) & 1);
-        }
+        for (int x = 0; x < kMtTiles; ++x)
+            if (loads[x] > 0) (void)mbar_wait(kFp8 ? &bar_raw[x] : &bar_k[x], (loads[x] - 1) & 1);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
-        constexpr uint32_t kWide = tc::idesc_bf16_f32(kMtKeys, 256, false, false);
-        constexpr uint32_t kHalf = tc::idesc_bf16_f32(kMtKeys, 128, false, false);
-        int nload = 0, used[2] = {0, 0};  // key tiles; S buffer x: times used
+        constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kMtKeys, kMtCols, false, false);
+        int loads[kMtTiles] = {0, 0, 0, 0}, used[kMtTiles] = {0, 0, 0, 0};  // of key stage and S buffer x
         bool ok = true, q_due = false;
         MtStages q;
         while (ok && w.next()) {
@@ -481,18 +451,16 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 }
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[st], q.parity(st), kWaitLimitNs, abort));
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < kMtTiles; ++x) {
                     if (!ok || x >= nt) break;
-                    const int ks = (nload + x) % nk;
-                    bool r = qs > slo || mbar_wait(&bar_k[ks], ((nload + x) / nk) & 1, kWaitLimitNs, abort);
-                    r = r && mbar_wait(&bar_s_empty[x], (used[x] & 1) ^ 1, kWaitLimitNs, abort);
+                    bool r = true;
+                    if (qs == slo) r = mbar_wait(&bar_k[x], loads[x]++ & 1, kWaitLimitNs, abort);
+                    r = r && mbar_wait(&bar_s_empty[x], (used[x]++ & 1) ^ 1, kWaitLimitNs, abort);
                     ok = __all_sync(0xFFFFFFFFu, r);
                     if (!ok) break;
-                    ++used[x];
                     tc::fence_after_sync();
                     if (lane == 0) {
-                        const uint32_t idesc = w.ntok - qs * per_step > QT ? kWide : kHalf;
-                        const uint32_t sk = smem_u32(smem + C::k_stage(ks));
+                        const uint32_t sk = smem_u32(smem + C::kOffK + x * C::kKBytes);
                         const uint32_t sq = smem_u32(smem + C::kOffQ + st * C::kQBytes);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
@@ -500,15 +468,14 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                             const uint32_t ko = (kk & 3) * 32;
                             const uint64_t ad = tc::smem_desc(sk + h * 1024 + ko, 16, C::kGrpBytes);
                             const uint64_t bd = tc::smem_desc(sq + h * C::kQHalf + ko, 16, 1024);
-                            tc::mma_bf16(tmem + x * kMtCols, ad, bd, idesc, kk > 0 ? 1u : 0u);
+                            tc::mma_bf16(tmem + x * kMtCols, ad, bd, kIdesc, kk > 0 ? 1u : 0u);
                         }
                         tc::commit(&bar_s[x]);
-                        if (qs == shi - 1) tc::commit(&bar_k_empty[ks]);
+                        if (qs == shi - 1) tc::commit(&bar_k_empty[x]);
                     }
                     __syncwarp();
                 }
             }
-            nload += nt;
         }
         if (!ok && lane == 0) {
             flag_error(a.err, PKV_DEVERR_TIMEOUT);
@@ -521,28 +488,24 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         tc::fence_after_sync();
     } else {
         // ------------------------------------------------------------ epilogue
-        const int ew = warp - 2, x = ew >> 3, second = (ew >> 2) & 1;  // tile of the pair, half of the columns
+        const int x = (warp - 2) >> 2;           // tile of the span
         const int key = (warp & 3) * 32 + lane;  // the TMEM lane this thread may read
         const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * kMtCols;
         ScoreScale sc(a.sm_scale, a.cap, 1.f);
         TanhPair tp(sc);
         const float in1 = sc.in;  // with a scale of 1
         const bool capped = sc.out > 0.f, biased = a.slopes != nullptr;
-        int nload = 0, turn = 0, used = 0;
-        bool ok = true, q_due = false, q_held = false;  // a resident segment's rows are in use
+        int loads = 0, used = 0, held = 0;  // held: stages of a resident segment's rows in use
+        bool ok = true, q_due = false;
         MtStages q;
-        // a resident segment is over: its stages may be loaded anew
-        auto release = [&](int n) {
-            if (q_held && lane == 0)
-                for (int i = 0; i < n; ++i) mbar_arrive(&bar_step[i]);
-            q_held = false;
-        };
-        int held = 0;
         while (w.next()) {
-            const int k0 = (2 * w.pair + x) * kMtKeys, t = k0 + key;
+            const int k0 = w.span * kMtSpan + x * kMtKeys, t = k0 + key;
             if (w.fresh) {
+                // a resident segment is over: its stages may be loaded anew
                 __syncwarp();
-                release(held);
+                if (lane == 0)
+                    for (int i = 0; i < held; ++i) mbar_arrive(&bar_step[i]);
+                held = 0;
                 q_due = true;
                 if constexpr (kFp8) {
                     sc.in = in1 * a.k_scale[w.kvh];
@@ -552,30 +515,29 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             int slo, shi;
             const int nt = w.steps(slo, shi);
             const int k_last = min(k0 + kMtKeys, w.s.kv_len) - 1;
-            float* mrow = a.mass + (static_cast<size_t>(w.seq) * a.hkv + w.kvh) * a.mass_stride;
+            float* at = a.mass + (static_cast<size_t>(w.seq) * a.hkv + w.kvh) * a.mass_stride + t;
             float old = 0.f, sum = 0.f;
             int id = 0;
-            const bool mine = !second && t < w.s.kv_len;
+            const bool mine = x < nt && t < w.s.kv_len;
             if (mine) {
-                if (a.keep != 0.f && t < w.s.off) old = a.keep * mrow[t];
+                if (a.keep != 0.f && t < w.s.off) old = a.keep * *at;
                 if (slo < shi && w.block_seen(t / kBlockSize))
                     id = a.block_tables[static_cast<size_t>(w.seq) * a.mbps + t / kBlockSize];
             }
             if constexpr (kFp8) {
-                for (int y = 0; ok && slo < shi && y < nt; ++y) {
-                    const int rs = nload % nraw, ks = nload % nk;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw[rs], (nload / nraw) & 1, kWaitLimitNs, abort) &&
-                                                     mbar_wait(&bar_k_empty[ks], ((nload / nk) & 1) ^ 1, kWaitLimitNs,
-                                                               abort));
+                // the codes come one tile after the other through one stage; a tile's own warps convert them
+                if (ok && slo < shi && x < nt) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw[x], loads & 1, kWaitLimitNs, abort) &&
+                                                     mbar_wait(&bar_k_empty[x], (loads & 1) ^ 1, kWaitLimitNs, abort));
+                    ++loads;
                     if (ok) {
-                        convert_keys<D>(smem + C::raw_stage(rs), smem + C::k_stage(ks), ew * 32 + lane);
+                        convert_keys<D>(smem + C::kOffRaw, smem + C::kOffK + x * C::kKBytes, (warp - 2 - 4 * x) * 32 + lane);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(&bar_k[ks]);
-                            mbar_arrive(&bar_raw_empty[rs]);
+                            mbar_arrive(&bar_k[x]);
+                            mbar_arrive(&bar_raw_empty);
                         }
-                        ++nload;
                     }
                 }
             }
@@ -584,14 +546,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                     ++q.uses[qs];
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_q[qs], q.parity(qs), kWaitLimitNs, abort));
                 }
-                q_held = true;
                 held = w.nsteps;
                 q_due = false;
             }
             for (int qs = slo; ok && qs < shi; ++qs) {
                 int st = qs;
                 if (!w.resident) {
-                    // (warps without a tile in this pair wait too: their arrival on bar_step must not
+                    // (warps without a tile in this span wait too: their arrival on bar_step must not
                     // run ahead of the step)
                     st = q.turn;
                     ++q.uses[st];
@@ -600,18 +561,15 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                     if (!ok) break;
                 }
                 if (x < nt) {
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_s[x], used & 1, kWaitLimitNs, abort));
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_s[x], used++ & 1, kWaitLimitNs, abort));
                     if (!ok) break;
-                    ++used;
                     tc::fence_after_sync();
                     const MtRows& r = rows[st];
-                    const int cols = w.ntok - qs * per_step > QT ? 128 : 64;  // of this half
-                    const int c_end = (second + 1) * cols;
-                    for (int c = second * cols; c < c_end; c += 32) {
+                    for (int c = 0; c < kMtCols; c += 32) {
                         float v[32];
                         tc::ld32(s_addr + c, v);
                         tc::wait_ld();
-                        if (c + 32 == c_end) {
+                        if (c + 32 == kMtCols) {
                             tc::fence_before_sync();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bar_s_empty[x]);
@@ -629,14 +587,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 __syncwarp();
                 if (!w.resident && lane == 0) mbar_arrive(&bar_step[st]);
             }
-            if (!ok && lane == 0) atomicOr(&s_fail, 1);
-            // the halves' sums meet; a warp that gave up comes here for every pair all the same
-            if (second) s_part[turn & 1][x][key] = sum;
-            asm volatile("bar.sync 1, %0;" ::"n"(kMtEpiWarps * 32) : "memory");
-            if (mine && id >= 0 && id < a.num_blocks && *abort == 0) mrow[t] = old + (sum + s_part[turn & 1][x][key]);
-            ++turn;
+            if (!ok) break;
+            if (mine && id >= 0 && id < a.num_blocks) *at = old + sum;
         }
-        if (!ok && lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
+        if (!ok && lane == 0) {
+            flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            atomicOr(&s_fail, 1);
+        }
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -661,10 +618,10 @@ cudaError_t launch_mass_tc_t(const MassArgs& a, const CUtensorMap& qmap, const C
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    // one CTA an SM, fewer where there are fewer pairs
-    const int64_t pairs = static_cast<int64_t>((a.max_kv + 2 * kMtKeys - 1) / (2 * kMtKeys)) * a.hkv * a.num_seqs;
-    const dim3 grid(static_cast<unsigned>(min(int64_t{max(1, a.num_sms)}, pairs)));
-    return launch_pdl(kern, grid, dim3(kMtThreads), C::kSmemBytes, stream, a, a.max_q <= 2 * a.q_tile ? 1 : 0, qmap, kmap);
+    // one CTA an SM, fewer where there are fewer spans
+    const int64_t spans = static_cast<int64_t>((a.max_kv - 1) / kMtSpan + 1) * a.hkv * a.num_seqs;
+    const dim3 grid(static_cast<unsigned>(min(int64_t{max(1, a.num_sms)}, spans)));
+    return launch_pdl(kern, grid, dim3(kMtThreads), C::kSmemBytes, stream, a, qmap, kmap);
 }
 
 }  // namespace
