@@ -6,9 +6,9 @@
 // so a key's sum over the queries is a sum over columns in one register, and the same
 // constants (a query's lse) serve all lanes of a warp.
 //
-// One CTA per SM takes an equal part of the work, cut along (sequence, KV head, four key
-// tiles) with a sequence's fours weighted by its steps of 128 query rows; it goes, four by
-// four, over the steps that see them: a step's 32 KB of q come from L2 once for 512 keys
+// One CTA per SM takes an equal part of the work, cut along (sequence, KV head, key tile)
+// with a sequence's tiles weighted by its steps of 128 query rows; it goes, up to four tiles
+// at a time, over the steps that see them: a step's 32 KB of q come from L2 once for 512 keys
 // (one tile at a time was bound by those reads).  Warps:
 //   0      TMA: the key tiles (four stages), the query steps (two stages; at most two
 //          steps stay where they are), and each step's constants per query row;
@@ -27,7 +27,6 @@ namespace {
 constexpr int kMtKeys = 128;                      // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBlockSize;
 constexpr int kMtTiles = 4;                       // key tiles side by side
-constexpr int kMtSpan = kMtTiles * kMtKeys;
 constexpr int kMtCols = 128;                      // query rows per step
 constexpr int kMtEpiWarps = 4 * kMtTiles;
 constexpr int kMtThreads = (2 + kMtEpiWarps) * 32;
@@ -132,65 +131,64 @@ __device__ __forceinline__ void convert_keys(const uint8_t* raw, uint8_t* dst, i
     }
 }
 
-// The cost of a sequence's spans of four key tiles, as the work is cut over the CTAs: a
-// span's steps, and what a span costs without any.
+// The cost of a sequence's key tiles, as the work is cut over the CTAs: a tile's steps, and
+// what a tile costs without any.
 struct MtCost {
-    int spans, weight;  // spans per head; of a span
+    int tiles, weight;  // tiles per head; of a tile
     __device__ __forceinline__ MtCost(const MassSeq& s, int group, int per_step) {
-        spans = s.ok ? (s.kv_len - 1) / kMtSpan + 1 : 0;
+        tiles = s.ok ? (s.kv_len - 1) / kMtKeys + 1 : 0;
         weight = 1 + 2 * ((s.rows / group + per_step - 1) / per_step);
     }
-    __device__ __forceinline__ int64_t all(int hkv) const { return static_cast<int64_t>(spans) * weight * hkv; }
+    __device__ __forceinline__ int64_t all(int hkv) const { return static_cast<int64_t>(tiles) * weight * hkv; }
 };
 
-// A CTA's part of the work: the spans, in the order (sequence, head, span), whose costs
-// before them lie in [lo, hi) of the whole.  Every warp walks it by itself.
+// A CTA's part of the work: the tiles, in the order (sequence, head, tile), whose costs
+// before them lie in [lo, hi) of the whole, taken up to four of a head at a time.  Every
+// warp walks it by itself.
 struct MtWalk {
     const MassArgs& a;
-    int64_t base, hi;
-    int seq, kvh, span, spans, weight, per_step;
+    int64_t base, hi, left;  // costs before the sequence and at the end; tiles of it to come
+    int seq, kvh, tile, n, tiles, weight, per_step;  // now: n tiles from `tile` on
     MassSeq s;
     int ntok, nsteps, seen_lo, seen_hi;
-    bool resident, fresh;  // fresh: the first span of a (sequence, head)
+    bool resident, fresh;  // fresh: the first ones of a (sequence, head)
     __device__ __forceinline__ MtWalk(const MassArgs& args, int seq0, int64_t base0, int64_t lo, int64_t hi_)
-        : a(args), base(base0), hi(hi_), seq(seq0), per_step(args.q_tile), first_(true) {
+        : a(args), base(base0), hi(hi_), seq(seq0), n(0), per_step(args.q_tile), fresh(false), first_(true) {
         load();
-        const int64_t item = (lo - base + weight - 1) / weight;
-        kvh = static_cast<int>(item / spans);
-        span = static_cast<int>(item % spans) - 1;  // next() comes first
-        base += item * weight;
-        if (span < 0) {  // a head's first span
-            --kvh;
-            span = spans - 1;
-        }
-        fresh = false;
+        const int64_t item = (lo - base + weight - 1) / weight;  // hkv * tiles at most
+        kvh = static_cast<int>(item / tiles);
+        tile = static_cast<int>(item % tiles);
+        left -= item;
     }
     __device__ __forceinline__ bool next() {
         fresh = first_;
         first_ = false;
-        if (++span == spans) {
-            span = 0;
+        tile += n;
+        if (tile == tiles) {
+            tile = 0;
             ++kvh;
             fresh = true;
         }
-        while (kvh == a.hkv) {  // (sequences without work have no spans)
+        while (kvh == a.hkv) {  // (sequences without work have no tiles)
+            base += static_cast<int64_t>(tiles) * weight * a.hkv;
             if (base >= hi || ++seq >= a.num_seqs) return false;
             load();
-            kvh = spans > 0 ? 0 : a.hkv;
+            kvh = tiles > 0 ? 0 : a.hkv;
+            fresh = true;
         }
-        if (base >= hi) return false;
-        base += weight;
+        if (left <= 0) return false;
+        n = static_cast<int>(min(min(int64_t{kMtTiles}, left), int64_t{tiles - tile}));
+        left -= n;
         return true;
     }
-    // the steps [lo, hi) that see the span's keys, and how many tiles it has
-    __device__ __forceinline__ int steps(int& lo, int& hi_) const {
-        const int k0 = span * kMtSpan, left = s.kv_len - k0;
+    // the steps [lo, hi) that see the tiles' keys
+    __device__ __forceinline__ void steps(int& lo, int& hi_) const {
+        const int k0 = tile * kMtKeys;
         int first, last;
-        mass_tokens(a, s, ntok, k0, k0 + min(kMtSpan, left) - 1, first, last);
+        mass_tokens(a, s, ntok, k0, k0 + min(n * kMtKeys, s.kv_len - k0) - 1, first, last);
         const bool some = last >= first;
         lo = some && nsteps > 1 ? first / per_step : 0;
         hi_ = !some ? 0 : nsteps > 1 ? last / per_step + 1 : 1;
-        return min(kMtTiles, (left + kMtKeys - 1) / kMtKeys);
     }
     // blocks that no query sees are not read: their table entries may name none
     __device__ __forceinline__ bool block_seen(int blk) const {
@@ -202,8 +200,9 @@ struct MtWalk {
     __device__ __forceinline__ void load() {
         s = mass_seq(a, seq, false);
         const MtCost c(s, a.group, per_step);
-        spans = c.spans;
+        tiles = c.tiles;
         weight = c.weight;
+        left = (hi - base + weight - 1) / weight;
         ntok = s.rows / a.group;
         nsteps = (ntok + per_step - 1) / per_step;
         resident = nsteps <= 2;
@@ -362,18 +361,18 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             ++q.uses[st];
             return true;
         };
-        // block ids: lane l has block l of the span; the next span's are read one ahead
-        int ids_span = 0, ids = 0, ids_next = 0;
-        auto read_ids = [&](int span) {
-            const int64_t blk = static_cast<int64_t>(span) * (kMtSpan / kBlockSize) + lane;
+        // block ids: lane l has block l of the tiles; the next ones' are read ahead
+        int ids_tile = 0, ids = 0, ids_next = 0;
+        auto read_ids = [&](int tile) {
+            const int64_t blk = static_cast<int64_t>(tile) * kMtBlocks + lane;
             return blk * kBlockSize < w.s.kv_len && w.block_seen(static_cast<int>(blk))
                        ? __ldg(a.block_tables + static_cast<size_t>(w.seq) * a.mbps + blk)
                        : 0;
         };
-        // tile x of the span into stage x
+        // tile x of them into stage x
         auto load_keys = [&](int x) {
             const int id = __shfl_sync(0xFFFFFFFFu, ids, x * kMtBlocks + (lane & (kMtBlocks - 1)));
-            const int nvalid = min(kMtBlocks, (w.s.kv_len + kBlockSize - 1) / kBlockSize - (w.span * kMtTiles + x) * kMtBlocks);
+            const int nvalid = min(kMtBlocks, (w.s.kv_len - 1) / kBlockSize + 1 - (w.tile + x) * kMtBlocks);
             if constexpr (kFp8) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw_empty, (nraw & 1) ^ 1, kWaitLimitNs, abort))) return false;
                 ++nraw;
@@ -396,12 +395,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         bool q_due = false;  // a resident segment's rows are not loaded yet
         while (ok && w.next()) {
             int slo, shi;
-            const int nt = w.steps(slo, shi);
+            w.steps(slo, shi);
+            const int nt = w.n;
             q_due = q_due || w.fresh;
-            if (slo >= shi) continue;  // no query sees the span: nothing of it is read
-            ids = !w.fresh && ids_span == w.span ? ids_next : read_ids(w.span);
-            ids_span = w.span + 1;
-            ids_next = read_ids(ids_span);
+            if (slo >= shi) continue;  // no query sees the tiles: nothing of them is read
+            ids = !w.fresh && ids_tile == w.tile ? ids_next : read_ids(w.tile);
+            ids_tile = w.tile + nt;
+            ids_next = read_ids(ids_tile);
             if (ids < 0 || ids >= a.num_blocks) {
                 flag_error(a.err, PKV_DEVERR_BLOCK_ID);
                 ids = 0;  // read a valid block; the keys' weights are not written
@@ -437,7 +437,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         while (ok && w.next()) {
             q_due = q_due || w.fresh;
             int slo, shi;
-            const int nt = w.steps(slo, shi);
+            w.steps(slo, shi);
+            const int nt = w.n;
             if (slo >= shi) continue;
             if (w.resident && q_due)
                 for (int qs = 0; qs < w.nsteps; ++qs) ++q.uses[qs];
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         tc::fence_after_sync();
     } else {
         // ------------------------------------------------------------ epilogue
-        const int x = (warp - 2) >> 2;           // tile of the span
+        const int x = (warp - 2) >> 2;           // its tile of those at hand
         const int key = (warp & 3) * 32 + lane;  // the TMEM lane this thread may read
         const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * kMtCols;
         ScoreScale sc(a.sm_scale, a.cap, 1.f);
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         bool ok = true, q_due = false;
         MtStages q;
         while (w.next()) {
-            const int k0 = w.span * kMtSpan + x * kMtKeys, t = k0 + key;
+            const int k0 = (w.tile + x) * kMtKeys, t = k0 + key;
             if (w.fresh) {
                 // a resident segment is over: its stages may be loaded anew
                 __syncwarp();
@@ -513,7 +514,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 }
             }
             int slo, shi;
-            const int nt = w.steps(slo, shi);
+            w.steps(slo, shi);
+            const int nt = w.n;
             const int k_last = min(k0 + kMtKeys, w.s.kv_len) - 1;
             float* at = a.mass + (static_cast<size_t>(w.seq) * a.hkv + w.kvh) * a.mass_stride + t;
             float old = 0.f, sum = 0.f;
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             for (int qs = slo; ok && qs < shi; ++qs) {
                 int st = qs;
                 if (!w.resident) {
-                    // (warps without a tile in this span wait too: their arrival on bar_step must not
+                    // (warps without a tile of these wait too: their arrival on bar_step must not
                     // run ahead of the step)
                     st = q.turn;
                     ++q.uses[st];
@@ -618,9 +620,9 @@ cudaError_t launch_mass_tc_t(const MassArgs& a, const CUtensorMap& qmap, const C
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    // one CTA an SM, fewer where there are fewer spans
-    const int64_t spans = static_cast<int64_t>((a.max_kv - 1) / kMtSpan + 1) * a.hkv * a.num_seqs;
-    const dim3 grid(static_cast<unsigned>(min(int64_t{max(1, a.num_sms)}, spans)));
+    // one CTA an SM, fewer where there are fewer tiles
+    const int64_t tiles = static_cast<int64_t>((a.max_kv - 1) / kMtKeys + 1) * a.hkv * a.num_seqs;
+    const dim3 grid(static_cast<unsigned>(min(int64_t{max(1, a.num_sms)}, tiles)));
     return launch_pdl(kern, grid, dim3(kMtThreads), C::kSmemBytes, stream, a, qmap, kmap);
 }
 
