@@ -46,110 +46,173 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
     return x - v + (warp > 0 ? part[warp - 1] : 0);
 }
 
-// One CTA per (KV head, sequence).  The k-th largest key is found digit by digit (11, 11
-// and 10 bits) by histograms; then every warp takes a contiguous part of the row, counts
-// what it keeps, and writes it in order.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
-    __shared__ int hist[kSelBins];
+// A cluster of C CTAs per (KV head, sequence), each with a contiguous part of the row, held
+// in shared memory as ordered integers where it fits.  The threshold key is found digit
+// by digit (11, 11 and 10 bits) from histograms, which the CTAs read from one another;
+// no further digit is looked at once the keys that share the found ones are all kept.
+// Then every warp counts what it keeps of a contiguous part, and writes it in order.
+template <int C>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a, const int cached) {
+    extern __shared__ uint32_t s_key[];            // [cached]
+    __shared__ __align__(16) int hist[2][kSelBins];  // by turns: a peer may still read the other
     __shared__ int part[kSelWarps];
-    __shared__ int s_digit, s_rest;
-    __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
+    __shared__ int s_digit, s_rest, s_all;
+    __shared__ int s_gt[kSelWarps], s_eq[kSelWarps], s_sum[2];
     pdl_wait();
     pdl_launch_dependents();
-    const int seq = blockIdx.y, head = blockIdx.x;
+    const int seq = blockIdx.y, head = blockIdx.x / C, rank = blockIdx.x % C;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int n = a.kv_lens[seq];
     if (n > a.max_kv) {
-        if (tid == 0 && head == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
+        if (tid == 0 && blockIdx.x == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
         n = a.max_kv;
     }
     n = max(n, 0);
-    if (tid == 0 && head == 0) a.kept_lens[seq] = min(n, a.budget);
+    if (tid == 0 && blockIdx.x == 0) a.kept_lens[seq] = min(n, a.budget);
     int* out = a.kept + (static_cast<size_t>(seq) * a.hkv + head) * a.kept_stride;
     if (n <= a.budget) {
-        for (int t = tid; t < n; t += kSelThreads) out[t] = t;
+        for (int64_t t = rank * kSelThreads + tid; t < n; t += C * kSelThreads) out[t] = static_cast<int>(t);
         return;
     }
     const float* row = a.mass + (static_cast<size_t>(seq) * a.hkv + head) * a.mass_stride;
     const int lo = a.first, hi = n - a.recent;  // the middle, at least one longer than what it may keep
     int rest = a.budget - a.first - a.recent;   // of it to keep
-    uint32_t key = 0xFFFFFFFFu;                 // threshold: keep keys above it, and `rest` equal ones
+    // this CTA's part [c0, c0 + m) of the row
+    const int size = (n - 1) / C + 1;
+    const int c0 = min(static_cast<int64_t>(n), static_cast<int64_t>(rank) * size), m = min(n - c0, size);
+    const bool in_smem = m <= cached;
+    auto key_at = [&](int i) { return in_smem ? s_key[i] : weight_key(row[c0 + i]); };
+    if (in_smem) {
+#pragma unroll 4
+        for (int i = tid; i < m; i += kSelThreads) s_key[i] = weight_key(row[c0 + i]);
+        // (read by other threads after the barriers below)
+    }
+    uint32_t found = 0, mask = 0;  // the threshold's digits so far
+    bool all = rest == 0;          // every key with them is kept (rest == 0: none, by what follows)
     if (rest > 0) {
-        uint32_t found = 0, mask = 0;
-        for (int pass = 0; pass < 3; ++pass) {
+#pragma unroll 1
+        for (int pass = 0; pass < 3 && !all; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const int bits = pass == 2 ? 10 : 11;
-            for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+            const uint32_t digit = pass == 2 ? 1023u : 2047u;
+            int* h = hist[pass & 1];
+            reinterpret_cast<int4*>(h)[tid] = make_int4(0, 0, 0, 0);
             __syncthreads();
-            for (int t = lo + tid; t < hi; t += kSelThreads) {
-                const uint32_t k = weight_key(row[t]);
-                if ((k & mask) == found) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+            const int i0 = max(0, lo - c0), i1 = min(m, hi - c0);
+            for (int i = i0 + tid; i < i1; i += kSelThreads) {
+                const uint32_t k = key_at(i);
+                if ((k & mask) == found) atomicAdd(&h[(k >> shift) & digit], 1);
             }
-            __syncthreads();
+            if constexpr (C > 1) cluster_sync();
+            else __syncthreads();
             // thread i has the bins 2047 - 4 i .. 2044 - 4 i: the largest first
-            int c[4], sum = 0, total;
+            int4 c = make_int4(0, 0, 0, 0);
+            if constexpr (C > 1) {
+                const uint32_t at = smem_u32(h + kSelBins - 4 - 4 * tid);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) sum += c[u] = hist[kSelBins - 1 - 4 * tid - u];
-            int before = block_scan(sum, part, &total);
+                for (int r = 0; r < C; ++r) {
+                    const float4 v = ld_cluster_f32x4(cluster_map(at, r));  // bits of four counts
+                    c.x += __float_as_int(v.x), c.y += __float_as_int(v.y);
+                    c.z += __float_as_int(v.z), c.w += __float_as_int(v.w);
+                }
+            } else {
+                c = *reinterpret_cast<const int4*>(h + kSelBins - 4 - 4 * tid);
+            }
+            const int bins[4] = {c.w, c.z, c.y, c.x};
+            int total;
+            int before = block_scan(c.x + c.y + c.z + c.w, part, &total);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (before < rest && before + c[u] >= rest) {
+                if (before < rest && before + bins[u] >= rest) {
                     s_digit = kSelBins - 1 - 4 * tid - u;
                     s_rest = rest - before;
+                    s_all = before + bins[u] == rest;
                 }
-                before += c[u];
+                before += bins[u];
             }
             __syncthreads();
             found |= static_cast<uint32_t>(s_digit) << shift;
-            mask |= ((1u << bits) - 1) << shift;
+            mask |= digit << shift;
             rest = s_rest;
-            __syncthreads();
+            all = s_all != 0;
+            // (s_digit is written again after two barriers at least)
         }
-        key = found;
+    } else {
+        __syncthreads();
     }
+    // a key k is kept if its digits are above the found ones, and the first `rest` of those that share them
+    const bool none = a.budget == a.first + a.recent;
     // a warp's part: whole 32s, contiguous
-    const int per = ((n + kSelThreads - 1) / kSelThreads) * 32;
-    const int t0 = min(n, warp * per), t1 = min(n, t0 + per);
-    int gt = 0, eq = 0;
-    for (int t = t0 + lane; t < t1; t += 32) {
+    const int per = (m + kSelThreads - 1) / kSelThreads * 32;
+    const int t0 = static_cast<int>(min(static_cast<int64_t>(m), static_cast<int64_t>(warp) * per));
+    const int t1 = static_cast<int>(min(static_cast<int64_t>(m), static_cast<int64_t>(t0) + per));
+    auto look = [&](int i, bool& gt, bool& eq) {
+        const int t = c0 + i;
+        gt = eq = false;
         if (t < lo || t >= hi) {
-            ++gt;
-        } else if (rest > 0) {
-            const uint32_t k = weight_key(row[t]);
-            gt += k > key;
-            eq += k == key;
+            gt = true;
+        } else if (!none) {
+            const uint32_t k = key_at(i) & mask;
+            gt = k > found;
+            eq = k == found;
         }
+    };
+    int gts = 0, eqs = 0;
+    for (int i = t0 + lane; i < t1; i += 32) {
+        bool gt, eq;
+        look(i, gt, eq);
+        gts += gt;
+        eqs += eq;
     }
-    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
-    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-    if (lane == 0) s_gt[warp] = gt, s_eq[warp] = eq;
+    gts = __reduce_add_sync(0xFFFFFFFFu, gts);
+    eqs = __reduce_add_sync(0xFFFFFFFFu, eqs);
+    if (lane == 0) s_gt[warp] = gts, s_eq[warp] = eqs;
     __syncthreads();
-    int at = 0, eq_left = rest;
-    for (int w = 0; w < warp; ++w) {
-        const int take = min(eq_left, s_eq[w]);
-        at += s_gt[w] + take;
-        eq_left -= take;
-    }
-    for (int tb = t0; tb < t1; tb += 32) {
-        const int t = tb + lane;
-        bool keep = false, tie = false;
-        if (t < t1) {
-            if (t < lo || t >= hi) {
-                keep = true;
-            } else if (rest > 0) {
-                const uint32_t k = weight_key(row[t]);
-                keep = k > key;
-                tie = k == key;
-            }
+    int gt_before = 0, eq_before = 0;
+    if constexpr (C > 1) {
+        if (tid == 0) {
+            int x = 0, y = 0;
+            for (int w = 0; w < kSelWarps; ++w) x += s_gt[w], y += s_eq[w];
+            s_sum[0] = x, s_sum[1] = y;
         }
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t ties = __ballot_sync(0xFFFFFFFFu, tie);
-        keep = keep || (tie && __popc(ties & below) < eq_left);
-        eq_left -= min(eq_left, __popc(ties));
-        const uint32_t kept = __ballot_sync(0xFFFFFFFFu, keep);
-        if (keep) out[at + __popc(kept & below)] = t;
-        at += __popc(kept);
+        cluster_sync();
+        for (int r = 0; r < rank; ++r) {
+            gt_before += __float_as_int(ld_cluster_f32(cluster_map(smem_u32(&s_sum[0]), r)));
+            eq_before += __float_as_int(ld_cluster_f32(cluster_map(smem_u32(&s_sum[1]), r)));
+        }
     }
+    for (int w = 0; w < warp; ++w) gt_before += s_gt[w], eq_before += s_eq[w];
+    for (int ib = t0; ib < t1; ib += 32) {
+        const int i = ib + lane;
+        bool gt = false, eq = false;
+        if (i < t1) look(i, gt, eq);
+        const uint32_t below = (1u << lane) - 1;
+        const uint32_t gt_mask = __ballot_sync(0xFFFFFFFFu, gt), eq_mask = __ballot_sync(0xFFFFFFFFu, eq);
+        const int eq_rank = eq_before + __popc(eq_mask & below);
+        if (gt || (eq && eq_rank < rest))
+            out[gt_before + __popc(gt_mask & below) + min(eq_rank, rest)] = c0 + i;
+        gt_before += __popc(gt_mask);
+        eq_before += __popc(eq_mask);
+    }
+    if constexpr (C > 1) cluster_sync();  // no CTA leaves while a peer may still read its shared memory
+}
+
+template <int C>
+cudaError_t launch_select_t(const SelectArgs& a, cudaStream_t stream) {
+    auto kern = select_kernel<C>;
+    constexpr int kMost = 48 * 1024;  // keys a CTA holds (192 KB beside 17 KB of histograms)
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    const int cached = min((a.max_kv - 1) / C + 1, kMost);
+    return launch_pdl_cluster(kern, dim3(a.hkv * C, a.num_seqs), dim3(kSelThreads), static_cast<size_t>(cached) * 4, stream,
+                              static_cast<unsigned>(C), a, cached);
 }
 
 // ------------------------------------------------------------ compaction --
@@ -242,7 +305,13 @@ __global__ void __launch_bounds__(kCmpThreads) compact_in_place_kernel(const Com
 }  // namespace
 
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream) {
-    return launch_pdl(select_kernel, dim3(a.hkv, a.num_seqs), dim3(kSelThreads), 0, stream, a);
+    // CTAs per row: more while a CTA would hold more than 4096 keys and the GPU has room for
+    // them, and while it could not hold its keys in 64 KB
+    const int64_t rows = static_cast<int64_t>(a.hkv) * a.num_seqs;
+    int c = 1;
+    while (c < 8 && ((a.max_kv / c > 4096 && rows * c < 2 * a.num_sms) || a.max_kv / c > 16384)) c *= 2;
+    return c == 1 ? launch_select_t<1>(a, stream) : c == 2 ? launch_select_t<2>(a, stream)
+         : c == 4 ? launch_select_t<4>(a, stream) : launch_select_t<8>(a, stream);
 }
 
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
