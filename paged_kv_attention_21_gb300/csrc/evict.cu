@@ -47,13 +47,16 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
 }
 
 // A cluster of C CTAs per (KV head, sequence), each with a contiguous part of the row, held
-// in shared memory as ordered integers where it fits.  The threshold key is found digit
-// by digit (11, 11 and 10 bits) from histograms, which the CTAs read from one another;
-// no further digit is looked at once the keys that share the found ones are all kept.
-// Then every warp counts what it keeps of a contiguous part, and writes it in order.
+// in shared memory as ordered integers where it fits.  The first and the last keys, kept in
+// any case, count as larger than any weight, so that one selection of the `budget` largest
+// is left.  The threshold is found digit by digit (11, 11 and 10 bits) from histograms,
+// which the CTAs read from one another; no further digit is looked at once the keys that
+// share the found ones are all kept.  Then every warp counts what it keeps of a contiguous
+// part, and writes it in order.  Four keys a thread: instructions bound it (one key at a
+// time took 31 us for 512 rows of up to 16384 keys).
 template <int C>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a, const int cached) {
-    extern __shared__ uint32_t s_key[];            // [cached]
+    extern __shared__ uint4 s_key[];                 // [cached / 4]
     __shared__ __align__(16) int hist[2][kSelBins];  // by turns: a peer may still read the other
     __shared__ int part[kSelWarps];
     __shared__ int s_digit, s_rest, s_all;
@@ -75,93 +78,107 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
         return;
     }
     const float* row = a.mass + (static_cast<size_t>(seq) * a.hkv + head) * a.mass_stride;
-    const int lo = a.first, hi = n - a.recent;  // the middle, at least one longer than what it may keep
-    int rest = a.budget - a.first - a.recent;   // of it to keep
-    // this CTA's part [c0, c0 + m) of the row
-    const int size = (n - 1) / C + 1;
-    const int c0 = min(static_cast<int64_t>(n), static_cast<int64_t>(rank) * size), m = min(n - c0, size);
+    const int lo = a.first, hi = n - a.recent;
+    int rest = a.budget;  // to keep of the keys that share the digits found so far
+    // this CTA's part [c0, c0 + m) of the row: whole fours, but for the row's end
+    const int64_t size = (static_cast<int64_t>((n - 1) / C + 1) + 3) / 4 * 4;
+    const int c0 = static_cast<int>(min(static_cast<int64_t>(n), rank * size));
+    const int m = static_cast<int>(min(static_cast<int64_t>(n - c0), size));
+    const int fours = (m - 1) / 4 + (m > 0 ? 1 : 0);
     const bool in_smem = m <= cached;
-    auto key_at = [&](int i) { return in_smem ? s_key[i] : weight_key(row[c0 + i]); };
+    // keys 4 i .. 4 i + 3 of the part; those past the row's end are 0: the least, and the last of their equals
+    const bool wide = reinterpret_cast<uintptr_t>(row) % 16 == 0;
+    auto load = [&](int i) {
+        const int t = c0 + 4 * i, left = m - 4 * i;
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        if (wide && left >= 4) {
+            const float4 v = *reinterpret_cast<const float4*>(row + t);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (u < left) w[u] = row[t + u];
+        }
+        uint32_t k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            k[u] = u >= left ? 0u : t + u < lo || t + u >= hi ? 0xFFFFFFFFu : weight_key(w[u]);
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    };
+    auto keys = [&](int i) { return in_smem ? s_key[i] : load(i); };
     if (in_smem) {
 #pragma unroll 4
-        for (int i = tid; i < m; i += kSelThreads) s_key[i] = weight_key(row[c0 + i]);
-        // (read by other threads after the barriers below)
+        for (int i = tid; i < fours; i += kSelThreads) s_key[i] = load(i);
     }
     uint32_t found = 0, mask = 0;  // the threshold's digits so far
-    bool all = rest == 0;          // every key with them is kept (rest == 0: none, by what follows)
-    if (rest > 0) {
 #pragma unroll 1
-        for (int pass = 0; pass < 3 && !all; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const uint32_t digit = pass == 2 ? 1023u : 2047u;
-            int* h = hist[pass & 1];
-            reinterpret_cast<int4*>(h)[tid] = make_int4(0, 0, 0, 0);
-            __syncthreads();
-            const int i0 = max(0, lo - c0), i1 = min(m, hi - c0);
-            for (int i = i0 + tid; i < i1; i += kSelThreads) {
-                const uint32_t k = key_at(i);
-                if ((k & mask) == found) atomicAdd(&h[(k >> shift) & digit], 1);
-            }
-            if constexpr (C > 1) cluster_sync();
-            else __syncthreads();
-            // thread i has the bins 2047 - 4 i .. 2044 - 4 i: the largest first
-            int4 c = make_int4(0, 0, 0, 0);
-            if constexpr (C > 1) {
-                const uint32_t at = smem_u32(h + kSelBins - 4 - 4 * tid);
-#pragma unroll
-                for (int r = 0; r < C; ++r) {
-                    const float4 v = ld_cluster_f32x4(cluster_map(at, r));  // bits of four counts
-                    c.x += __float_as_int(v.x), c.y += __float_as_int(v.y);
-                    c.z += __float_as_int(v.z), c.w += __float_as_int(v.w);
-                }
-            } else {
-                c = *reinterpret_cast<const int4*>(h + kSelBins - 4 - 4 * tid);
-            }
-            const int bins[4] = {c.w, c.z, c.y, c.x};
-            int total;
-            int before = block_scan(c.x + c.y + c.z + c.w, part, &total);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (before < rest && before + bins[u] >= rest) {
-                    s_digit = kSelBins - 1 - 4 * tid - u;
-                    s_rest = rest - before;
-                    s_all = before + bins[u] == rest;
-                }
-                before += bins[u];
-            }
-            __syncthreads();
-            found |= static_cast<uint32_t>(s_digit) << shift;
-            mask |= digit << shift;
-            rest = s_rest;
-            all = s_all != 0;
-            // (s_digit is written again after two barriers at least)
-        }
-    } else {
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t digit = pass == 2 ? 1023u : 2047u;
+        int* h = hist[pass & 1];
+        reinterpret_cast<int4*>(h)[tid] = make_int4(0, 0, 0, 0);
         __syncthreads();
+        for (int i = tid; i < fours; i += kSelThreads) {  // (the fours that this thread stored)
+            const uint4 q = keys(i);
+            const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if ((k[u] & mask) == found) atomicAdd(&h[(k[u] >> shift) & digit], 1);
+        }
+        if constexpr (C > 1) cluster_sync();
+        else __syncthreads();
+        // thread i has the bins 2047 - 4 i .. 2044 - 4 i: the largest first
+        int4 c = make_int4(0, 0, 0, 0);
+        if constexpr (C > 1) {
+            const uint32_t at = smem_u32(h + kSelBins - 4 - 4 * tid);
+#pragma unroll
+            for (int r = 0; r < C; ++r) {
+                const float4 v = ld_cluster_f32x4(cluster_map(at, r));  // bits of four counts
+                c.x += __float_as_int(v.x), c.y += __float_as_int(v.y);
+                c.z += __float_as_int(v.z), c.w += __float_as_int(v.w);
+            }
+        } else {
+            c = *reinterpret_cast<const int4*>(h + kSelBins - 4 - 4 * tid);
+        }
+        const int bins[4] = {c.w, c.z, c.y, c.x};
+        int total;
+        int before = block_scan(c.x + c.y + c.z + c.w, part, &total);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (before < rest && before + bins[u] >= rest) {
+                s_digit = kSelBins - 1 - 4 * tid - u;
+                s_rest = rest - before;
+                s_all = before + bins[u] == rest;
+            }
+            before += bins[u];
+        }
+        __syncthreads();
+        found |= static_cast<uint32_t>(s_digit) << shift;
+        mask |= digit << shift;
+        rest = s_rest;
+        if (s_all) break;
+        // (s_digit is written again after two barriers at least)
     }
-    // a key k is kept if its digits are above the found ones, and the first `rest` of those that share them
-    const bool none = a.budget == a.first + a.recent;
-    // a warp's part: whole 32s, contiguous
-    const int per = (m + kSelThreads - 1) / kSelThreads * 32;
-    const int t0 = static_cast<int>(min(static_cast<int64_t>(m), static_cast<int64_t>(warp) * per));
-    const int t1 = static_cast<int>(min(static_cast<int64_t>(m), static_cast<int64_t>(t0) + per));
-    auto look = [&](int i, bool& gt, bool& eq) {
-        const int t = c0 + i;
-        gt = eq = false;
-        if (t < lo || t >= hi) {
-            gt = true;
-        } else if (!none) {
-            const uint32_t k = key_at(i) & mask;
-            gt = k > found;
-            eq = k == found;
+    // a key is kept if its digits are above the found ones, and the first `rest` of those that share them
+    auto look = [&](int i, uint32_t& gt, uint32_t& eq) {  // bit u: key 4 i + u
+        const uint4 q = keys(i);
+        const uint32_t k[4] = {q.x & mask, q.y & mask, q.z & mask, q.w & mask};
+        gt = eq = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            gt |= k[u] > found ? 1u << u : 0u;
+            eq |= k[u] == found ? 1u << u : 0u;
         }
     };
+    // a warp's part: whole 32 fours, contiguous
+    const int per = (fours + kSelThreads - 1) / kSelThreads * 32;
+    const int f0 = min(fours, warp * per), f1 = min(fours, f0 + per);
     int gts = 0, eqs = 0;
-    for (int i = t0 + lane; i < t1; i += 32) {
-        bool gt, eq;
+    for (int i = f0 + lane; i < f1; i += 32) {
+        uint32_t gt, eq;
         look(i, gt, eq);
-        gts += gt;
-        eqs += eq;
+        gts += __popc(gt);
+        eqs += __popc(eq);
     }
     gts = __reduce_add_sync(0xFFFFFFFFu, gts);
     eqs = __reduce_add_sync(0xFFFFFFFFu, eqs);
@@ -181,17 +198,29 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
         }
     }
     for (int w = 0; w < warp; ++w) gt_before += s_gt[w], eq_before += s_eq[w];
-    for (int ib = t0; ib < t1; ib += 32) {
+    for (int ib = f0; ib < f1; ib += 32) {
         const int i = ib + lane;
-        bool gt = false, eq = false;
-        if (i < t1) look(i, gt, eq);
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t gt_mask = __ballot_sync(0xFFFFFFFFu, gt), eq_mask = __ballot_sync(0xFFFFFFFFu, eq);
-        const int eq_rank = eq_before + __popc(eq_mask & below);
-        if (gt || (eq && eq_rank < rest))
-            out[gt_before + __popc(gt_mask & below) + min(eq_rank, rest)] = c0 + i;
-        gt_before += __popc(gt_mask);
-        eq_before += __popc(eq_mask);
+        uint32_t gt = 0, eq = 0;
+        if (i < f1) look(i, gt, eq);
+        // prefix sums over the warp of both counts (at most 128 each)
+        const int mine = __popc(gt) | __popc(eq) << 16;
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        int g = gt_before + ((upto - mine) & 0xFFFF), e = eq_before + ((upto - mine) >> 16);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool is_gt = gt >> u & 1, is_eq = eq >> u & 1;
+            if (is_gt || (is_eq && e < rest)) out[g + min(e, rest)] = c0 + 4 * i + u;
+            g += is_gt;
+            e += is_eq;
+        }
+        gt_before += all & 0xFFFF;
+        eq_before += all >> 16;
     }
     if constexpr (C > 1) cluster_sync();  // no CTA leaves while a peer may still read its shared memory
 }
@@ -210,7 +239,7 @@ cudaError_t launch_select_t(const SelectArgs& a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const int cached = min((a.max_kv - 1) / C + 1, kMost);
+    const int cached = static_cast<int>(min((static_cast<int64_t>((a.max_kv - 1) / C + 1) + 3) / 4 * 4, int64_t{kMost}));
     return launch_pdl_cluster(kern, dim3(a.hkv * C, a.num_seqs), dim3(kSelThreads), static_cast<size_t>(cached) * 4, stream,
                               static_cast<unsigned>(C), a, cached);
 }
