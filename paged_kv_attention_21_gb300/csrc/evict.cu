@@ -101,15 +101,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
         }
         uint32_t k[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            k[u] = u >= left ? 0u : t + u < lo || t + u >= hi ? 0xFFFFFFFFu : weight_key(w[u]);
+        for (int u = 0; u < 4; ++u) k[u] = weight_key(w[u]);
+        if (t < lo || t + 4 > hi) {  // (left < 4 is past hi)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (t + u < lo || t + u >= hi) k[u] = 0xFFFFFFFFu;
+                if (u >= left) k[u] = 0u;
+            }
+        }
         return make_uint4(k[0], k[1], k[2], k[3]);
     };
     auto keys = [&](int i) { return in_smem ? s_key[i] : load(i); };
-    if (in_smem) {
-#pragma unroll 4
-        for (int i = tid; i < fours; i += kSelThreads) s_key[i] = load(i);
-    }
     uint32_t found = 0, mask = 0;  // the threshold's digits so far
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
@@ -118,12 +120,25 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
         int* h = hist[pass & 1];
         reinterpret_cast<int4*>(h)[tid] = make_int4(0, 0, 0, 0);
         __syncthreads();
-        for (int i = tid; i < fours; i += kSelThreads) {  // (the fours that this thread stored)
-            const uint4 q = keys(i);
-            const uint32_t k[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if ((k[u] & mask) == found) atomicAdd(&h[(k[u] >> shift) & digit], 1);
+        if (pass == 0) {  // the row comes in, and all of it counts
+#pragma unroll 4
+            for (int i = tid; i < fours; i += kSelThreads) {
+                const uint4 q = load(i);
+                if (in_smem) s_key[i] = q;
+                atomicAdd(&h[q.x >> 21], 1);
+                atomicAdd(&h[q.y >> 21], 1);
+                atomicAdd(&h[q.z >> 21], 1);
+                atomicAdd(&h[q.w >> 21], 1);
+            }
+        } else {
+#pragma unroll 2
+            for (int i = tid; i < fours; i += kSelThreads) {  // (the fours that this thread stored)
+                const uint4 q = keys(i);
+                if ((q.x & mask) == found) atomicAdd(&h[(q.x >> shift) & digit], 1);
+                if ((q.y & mask) == found) atomicAdd(&h[(q.y >> shift) & digit], 1);
+                if ((q.z & mask) == found) atomicAdd(&h[(q.z >> shift) & digit], 1);
+                if ((q.w & mask) == found) atomicAdd(&h[(q.w >> shift) & digit], 1);
+            }
         }
         if constexpr (C > 1) cluster_sync();
         else __syncthreads();
@@ -159,26 +174,34 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
         if (s_all) break;
         // (s_digit is written again after two barriers at least)
     }
-    // a key is kept if its digits are above the found ones, and the first `rest` of those that share them
-    auto look = [&](int i, uint32_t& gt, uint32_t& eq) {  // bit u: key 4 i + u
+    // a key is kept if its digits are above the found ones, and the first `rest` of those that share them.
+    // Of four keys: bits 0..3 above, bits 16..19 equal
+    auto look = [&](int i) {
         const uint4 q = keys(i);
-        const uint32_t k[4] = {q.x & mask, q.y & mask, q.z & mask, q.w & mask};
-        gt = eq = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            gt |= k[u] > found ? 1u << u : 0u;
-            eq |= k[u] == found ? 1u << u : 0u;
-        }
+        uint32_t x = 0, y = 0;
+        x |= (q.x & mask) > found ? 1u : 0u, y |= (q.x & mask) == found ? 1u : 0u;
+        x |= (q.y & mask) > found ? 2u : 0u, y |= (q.y & mask) == found ? 2u : 0u;
+        x |= (q.z & mask) > found ? 4u : 0u, y |= (q.z & mask) == found ? 4u : 0u;
+        x |= (q.w & mask) > found ? 8u : 0u, y |= (q.w & mask) == found ? 8u : 0u;
+        return x | y << 16;
     };
-    // a warp's part: whole 32 fours, contiguous
+    // a warp's part: whole 32 fours, contiguous; what its first eight turns saw is kept for the writing
+    constexpr int kSeen = 8;
     const int per = (fours + kSelThreads - 1) / kSelThreads * 32;
     const int f0 = min(fours, warp * per), f1 = min(fours, f0 + per);
+    uint32_t seen[kSeen];
     int gts = 0, eqs = 0;
-    for (int i = f0 + lane; i < f1; i += 32) {
-        uint32_t gt, eq;
-        look(i, gt, eq);
-        gts += __popc(gt);
-        eqs += __popc(eq);
+#pragma unroll
+    for (int u = 0; u < kSeen; ++u) {
+        const int i = f0 + lane + 32 * u;
+        seen[u] = i < f1 ? look(i) : 0u;
+        gts += __popc(seen[u] & 0xFu);
+        eqs += __popc(seen[u] >> 16);
+    }
+    for (int i = f0 + lane + 32 * kSeen; i < f1; i += 32) {
+        const uint32_t x = look(i);
+        gts += __popc(x & 0xFu);
+        eqs += __popc(x >> 16);
     }
     gts = __reduce_add_sync(0xFFFFFFFFu, gts);
     eqs = __reduce_add_sync(0xFFFFFFFFu, eqs);
@@ -198,12 +221,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
         }
     }
     for (int w = 0; w < warp; ++w) gt_before += s_gt[w], eq_before += s_eq[w];
-    for (int ib = f0; ib < f1; ib += 32) {
-        const int i = ib + lane;
-        uint32_t gt = 0, eq = 0;
-        if (i < f1) look(i, gt, eq);
+    auto write = [&](int i, uint32_t x) {
         // prefix sums over the warp of both counts (at most 128 each)
-        const int mine = __popc(gt) | __popc(eq) << 16;
+        const int mine = __popc(x & 0xFu) | __popc(x >> 16) << 16;
         int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -211,17 +231,23 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
             if (lane >= o) upto += y;
         }
         const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        int g = gt_before + ((upto - mine) & 0xFFFF), e = eq_before + ((upto - mine) >> 16);
+        if (mine) {
+            int g = gt_before + ((upto - mine) & 0xFFFF), e = eq_before + ((upto - mine) >> 16);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const bool is_gt = gt >> u & 1, is_eq = eq >> u & 1;
-            if (is_gt || (is_eq && e < rest)) out[g + min(e, rest)] = c0 + 4 * i + u;
-            g += is_gt;
-            e += is_eq;
+            for (int u = 0; u < 4; ++u) {
+                const bool is_gt = x >> u & 1, is_eq = x >> (16 + u) & 1;
+                if (is_gt || (is_eq && e < rest)) out[g + min(e, rest)] = c0 + 4 * i + u;
+                g += is_gt;
+                e += is_eq;
+            }
         }
         gt_before += all & 0xFFFF;
         eq_before += all >> 16;
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < kSeen; ++u)
+        if (f0 + 32 * u < f1) write(f0 + lane + 32 * u, seen[u]);
+    for (int ib = f0 + 32 * kSeen; ib < f1; ib += 32) write(ib + lane, ib + lane < f1 ? look(ib + lane) : 0u);
     if constexpr (C > 1) cluster_sync();  // no CTA leaves while a peer may still read its shared memory
 }
 
