@@ -57,7 +57,9 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
 template <int C>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a, const int cached) {
     extern __shared__ uint4 s_key[];                 // [cached / 4]
-    __shared__ __align__(16) int hist[2][kSelBins];  // by turns: a peer may still read the other
+    __shared__ __align__(16) int hist[kSelBins];
+    // the cluster's histogram: the CTAs add their bins to one another's, by turns to one of two
+    __shared__ __align__(16) int whole[C > 1 ? 2 : 1][C > 1 ? kSelBins : 4];
     __shared__ int part[kSelWarps];
     __shared__ int s_digit, s_rest, s_all;
     __shared__ int s_gt[kSelWarps], s_eq[kSelWarps], s_sum[2];
@@ -117,8 +119,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t digit = pass == 2 ? 1023u : 2047u;
-        int* h = hist[pass & 1];
+        int* h = hist;
         reinterpret_cast<int4*>(h)[tid] = make_int4(0, 0, 0, 0);
+        if constexpr (C > 1) {  // (peers add to the first after the pass's first cluster barrier, to the other later)
+            reinterpret_cast<int4*>(whole[pass & 1])[tid] = make_int4(0, 0, 0, 0);
+            cluster_arrive();
+        }
         __syncthreads();
         if (pass == 0) {  // the row comes in, and all of it counts
 #pragma unroll 4
@@ -140,20 +146,20 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
                 if ((q.w & mask) == found) atomicAdd(&h[(q.w >> shift) & digit], 1);
             }
         }
-        if constexpr (C > 1) cluster_sync();
-        else __syncthreads();
+        __syncthreads();
         // thread i has the bins 2047 - 4 i .. 2044 - 4 i: the largest first
-        int4 c = make_int4(0, 0, 0, 0);
+        const int at = kSelBins - 4 - 4 * tid;
+        int4 c = *reinterpret_cast<const int4*>(h + at);
         if constexpr (C > 1) {
-            const uint32_t at = smem_u32(h + kSelBins - 4 - 4 * tid);
+            cluster_wait();  // every CTA has cleared its whole[]
+            const uint32_t to = smem_u32(whole[pass & 1] + at);
+            const int v[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int r = 0; r < C; ++r) {
-                const float4 v = ld_cluster_f32x4(cluster_map(at, r));  // bits of four counts
-                c.x += __float_as_int(v.x), c.y += __float_as_int(v.y);
-                c.z += __float_as_int(v.z), c.w += __float_as_int(v.w);
-            }
-        } else {
-            c = *reinterpret_cast<const int4*>(h + kSelBins - 4 - 4 * tid);
+            for (int u = 0; u < 4; ++u)
+                if (v[u])  // few bins are in use
+                    for (int r = 0; r < C; ++r) red_cluster_add(cluster_map(to + 4 * u, r), v[u]);
+            cluster_sync();
+            c = *reinterpret_cast<const int4*>(whole[pass & 1] + at);
         }
         const int bins[4] = {c.w, c.z, c.y, c.x};
         int total;
@@ -176,14 +182,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
     }
     // a key is kept if its digits are above the found ones, and the first `rest` of those that share them.
     // Of four keys: bits 0..3 above, bits 16..19 equal
+    const uint32_t top = found | ~mask;
     auto look = [&](int i) {
         const uint4 q = keys(i);
-        uint32_t x = 0, y = 0;
-        x |= (q.x & mask) > found ? 1u : 0u, y |= (q.x & mask) == found ? 1u : 0u;
-        x |= (q.y & mask) > found ? 2u : 0u, y |= (q.y & mask) == found ? 2u : 0u;
-        x |= (q.z & mask) > found ? 4u : 0u, y |= (q.z & mask) == found ? 4u : 0u;
-        x |= (q.w & mask) > found ? 8u : 0u, y |= (q.w & mask) == found ? 8u : 0u;
-        return x | y << 16;
+        uint32_t x = 0;
+        x |= q.x > top ? 0x1u : q.x >= found ? 0x10000u : 0u;
+        x |= q.y > top ? 0x2u : q.y >= found ? 0x20000u : 0u;
+        x |= q.z > top ? 0x4u : q.z >= found ? 0x40000u : 0u;
+        x |= q.w > top ? 0x8u : q.w >= found ? 0x80000u : 0u;
+        return x;
     };
     // a warp's part: whole 32 fours, contiguous; what its first eight turns saw is kept for the writing
     constexpr int kSeen = 8;
@@ -222,17 +229,23 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
     }
     for (int w = 0; w < warp; ++w) gt_before += s_gt[w], eq_before += s_eq[w];
     auto write = [&](int i, uint32_t x) {
-        // prefix sums over the warp of both counts (at most 128 each)
-        const int mine = __popc(x & 0xFu) | __popc(x >> 16) << 16;
-        int upto = mine;
+        const uint32_t below = (1u << lane) - 1;
+        int g = gt_before, e = eq_before;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-            if (lane >= o) upto += y;
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t b = __ballot_sync(0xFFFFFFFFu, x >> u & 1);
+            g += __popc(b & below);
+            gt_before += __popc(b);
         }
-        const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        if (mine) {
-            int g = gt_before + ((upto - mine) & 0xFFFF), e = eq_before + ((upto - mine) >> 16);
+        if (__any_sync(0xFFFFFFFFu, x >> 16)) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t b = __ballot_sync(0xFFFFFFFFu, x >> (16 + u) & 1);
+                e += __popc(b & below);
+                eq_before += __popc(b);
+            }
+        }
+        if (x) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const bool is_gt = x >> u & 1, is_eq = x >> (16 + u) & 1;
@@ -241,8 +254,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
                 e += is_eq;
             }
         }
-        gt_before += all & 0xFFFF;
-        eq_before += all >> 16;
     };
 #pragma unroll
     for (int u = 0; u < kSeen; ++u)
@@ -254,7 +265,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
 template <int C>
 cudaError_t launch_select_t(const SelectArgs& a, cudaStream_t stream) {
     auto kern = select_kernel<C>;
-    constexpr int kMost = 48 * 1024;  // keys a CTA holds (192 KB beside 17 KB of histograms)
+    constexpr int kMost = 48 * 1024;  // keys a CTA holds (192 KB beside 25 KB of histograms)
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
