@@ -306,7 +306,7 @@ struct MassArgs {
 // At most kMassRows query rows (queries x heads of a KV head) per sequence: mma.sync
 // fragments straight from global memory (mass.cu); more: tcgen05 (mass_tc.cu), with the
 // tile-group (bf16) or block-row (e4m3) view of the pool and the 3-D view of q.
-constexpr int kMassRows = 64;
+constexpr int kMassRows = 32;
 cudaError_t launch_mass_rows(const MassArgs& a, cudaStream_t stream);
 cudaError_t launch_mass_tc(const MassArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, cudaStream_t stream);
 
