@@ -44,6 +44,10 @@ struct MtCfg {
     static constexpr int kOffK = kOffQ + 2 * kQBytes;
     static constexpr int kOffRaw = kOffK + kMtTiles * kKBytes;
     static constexpr int kBody = kOffRaw + kRawBytes;
+    // stages of codes: one, or three where no sequence has more than one step: two then lie in
+    // the second query stage (32 observers of 64 sequences: 40 us with one)
+    static constexpr int kMaxRaw = 3;
+    __device__ static uint32_t raw_stage(int i) { return i == 0 ? kOffRaw : kOffQ + kQBytes + (i - 1) * kRawBytes; }
     // at least 120 KB, so that one CTA has an SM and its 512 TMEM columns
     static constexpr int kSmemBytes = kBody + 1024 > 120 * 1024 ? kBody + 1024 : 120 * 1024;
 };
@@ -219,14 +223,14 @@ struct MtStages {
 
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kMtThreads, 1)
-    mass_tc_kernel(const MassArgs a, const __grid_constant__ CUtensorMap qmap,
+    mass_tc_kernel(const MassArgs a, const int raw_stages, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap) {
     using C = MtCfg<D, kFp8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     __shared__ __align__(16) MtRows rows[2];
-    __shared__ __align__(8) uint64_t bar_raw[kMtTiles], bar_raw_empty, bar_q[2], bar_step[2], bar_fin;
+    __shared__ __align__(8) uint64_t bar_raw[kMtTiles], bar_conv[kMtTiles], bar_q[2], bar_step[2], bar_fin;
     __shared__ __align__(8) uint64_t bar_k[kMtTiles], bar_k_empty[kMtTiles], bar_s[kMtTiles], bar_s_empty[kMtTiles];
     __shared__ int64_t s_cost[kMtThreads / 32];
     __shared__ int64_t s_base;
@@ -240,13 +244,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(&bar_raw_empty, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar_q[i], 2);  // the copies, and the rows' constants
             mbar_init(&bar_step[i], kMtEpiWarps);
         }
         for (int i = 0; i < kMtTiles; ++i) {
             mbar_init(&bar_raw[i], 1);
+            mbar_init(&bar_conv[i], 4);
             mbar_init(&bar_k[i], kFp8 ? 4 : 1);
             mbar_init(&bar_k_empty[i], 1);
             mbar_init(&bar_s[i], 1);
@@ -369,18 +373,30 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                        ? __ldg(a.block_tables + static_cast<size_t>(w.seq) * a.mbps + blk)
                        : 0;
         };
+        // e4m3: the first `count` loads of tile x have been converted; what each stage of codes holds
+        int done[kMtTiles] = {0, 0, 0, 0}, in_stage[C::kMaxRaw] = {0, 0, 0}, stage_load[C::kMaxRaw] = {0, 0, 0};
+        auto converted = [&](int x, int count) {
+            if (done[x] >= count) return true;  // (count is at most one more)
+            done[x] = count;
+            return __all_sync(0xFFFFFFFFu, mbar_wait(&bar_conv[x], (count - 1) & 1, kWaitLimitNs, abort)) != 0;
+        };
         // tile x of them into stage x
         auto load_keys = [&](int x) {
             const int id = __shfl_sync(0xFFFFFFFFu, ids, x * kMtBlocks + (lane & (kMtBlocks - 1)));
             const int nvalid = min(kMtBlocks, (w.s.kv_len - 1) / kBlockSize + 1 - (w.tile + x) * kMtBlocks);
             if constexpr (kFp8) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw_empty, (nraw & 1) ^ 1, kWaitLimitNs, abort))) return false;
+                // the tile's codes before these have been converted (so that its warps see every phase
+                // of bar_raw[x]), and so have those that the stage holds
+                const int rs = nraw % raw_stages;
+                if (!converted(x, loads[x]) || (nraw >= raw_stages && !converted(in_stage[rs], stage_load[rs]))) return false;
                 ++nraw;
                 ++loads[x];
+                in_stage[rs] = x;
+                stage_load[rs] = loads[x];
                 if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], nvalid * (C::kBlkBytes / 2));
                 __syncwarp();
                 if (lane < nvalid)
-                    tma_load_4d(smem + C::kOffRaw + lane * (C::kBlkBytes / 2), &kmap, &bar_raw[x], 0, 0, w.kvh, id);
+                    tma_load_4d(smem + C::raw_stage(rs) + lane * (C::kBlkBytes / 2), &kmap, &bar_raw[x], 0, 0, w.kvh, id);
             } else {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_k_empty[x], (loads[x] & 1) ^ 1, kWaitLimitNs, abort))) return false;
                 ++loads[x];
@@ -496,7 +512,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         TanhPair tp(sc);
         const float in1 = sc.in;  // with a scale of 1
         const bool capped = sc.out > 0.f, biased = a.slopes != nullptr;
-        int loads = 0, used = 0, held = 0;  // held: stages of a resident segment's rows in use
+        int nraw = 0, loads = 0, used = 0, held = 0;  // held: stages of a resident segment's rows in use
         bool ok = true, q_due = false;
         MtStages q;
         while (w.next()) {
@@ -527,18 +543,20 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                     id = a.block_tables[static_cast<size_t>(w.seq) * a.mbps + t / kBlockSize];
             }
             if constexpr (kFp8) {
-                // the codes come one tile after the other through one stage; a tile's own warps convert them
+                // the codes come one tile after the other through the stages; a tile's own warps convert them
+                const int rs = (nraw + x) % raw_stages;
+                if (slo < shi) nraw += nt;
                 if (ok && slo < shi && x < nt) {
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw[x], loads & 1, kWaitLimitNs, abort) &&
                                                      mbar_wait(&bar_k_empty[x], (loads & 1) ^ 1, kWaitLimitNs, abort));
                     ++loads;
                     if (ok) {
-                        convert_keys<D>(smem + C::kOffRaw, smem + C::kOffK + x * C::kKBytes, (warp - 2 - 4 * x) * 32 + lane);
+                        convert_keys<D>(smem + C::raw_stage(rs), smem + C::kOffK + x * C::kKBytes, (warp - 2 - 4 * x) * 32 + lane);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(&bar_k[x]);
-                            mbar_arrive(&bar_raw_empty);
+                            mbar_arrive(&bar_conv[x]);
                         }
                     }
                 }
@@ -623,7 +641,8 @@ cudaError_t launch_mass_tc_t(const MassArgs& a, const CUtensorMap& qmap, const C
     // one CTA an SM, fewer where there are fewer tiles
     const int64_t tiles = static_cast<int64_t>((a.max_kv - 1) / kMtKeys + 1) * a.hkv * a.num_seqs;
     const dim3 grid(static_cast<unsigned>(min(int64_t{max(1, a.num_sms)}, tiles)));
-    return launch_pdl(kern, grid, dim3(kMtThreads), C::kSmemBytes, stream, a, qmap, kmap);
+    return launch_pdl(kern, grid, dim3(kMtThreads), C::kSmemBytes, stream, a, a.max_q <= a.q_tile ? C::kMaxRaw : 1,
+                      qmap, kmap);
 }
 
 }  // namespace

@@ -259,3 +259,22 @@ def test_mass_flags_what_it_cannot_read():
     got = mass_of(p, r, q, bad, lse, start, 1.0, 3)
     assert pkv.pkv_device_errors() == pkv.DEVERR_POSITION
     assert torch.equal(got, start)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,d,q_max", [(8, 2, 64, 32), (8, 2, 128, 30), (12, 4, 128, 80), (2, 2, 64, 200)])
+def test_mass_of_many_ragged_sequences(kv, hq, hkv, d, q_max):
+    """Every CTA goes from tile to tile, head to head and sequence to sequence: many short
+    sequences (one to four key tiles at a time), a few long ones, some without queries."""
+    rng = np.random.default_rng(hq + q_max)
+    q_lens = [int(x) for x in rng.integers(0, q_max + 1, 70)]
+    q_lens[3] = q_max
+    lens = [m + int(x) for m, x in zip(q_lens, np.where(rng.random(70) < 0.1, rng.integers(0, 3000, 70), rng.integers(0, 700, 70)))]
+    p = Paged(lens, hq, hkv, d, kv, seed=hq)
+    r = Rule(d, hq, 70, cap=30.0)
+    qo, qo_t, q, q64 = problem(p, q_lens)
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+    pkv.pkv_score_prefill(p.desc, r.score, q, qo_t, p.k_pool, p.v_pool, p.t, p.lens_t, torch.empty_like(q), lse, **p.scales)
+    start = torch.rand(70, hkv, max(lens), device="cuda")
+    got = mass_of(p, r, q, qo_t, lse, start, 1.0, q_max)
+    check_mass(p, r, q64, qo, lse, start, 1.0, got)
