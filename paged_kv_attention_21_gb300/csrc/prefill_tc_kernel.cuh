@@ -636,10 +636,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) m8[e] = sv[e];
 #pragma unroll
-                for (int e = 8; e < kTcN; e += 16) {
+                for (int e = 8; e + 16 <= kTcN; e += 16) {
 #pragma unroll
                     for (int u = 0; u < 8; ++u) m8[u] = fmax3(m8[u], sv[e + u], sv[e + 8 + u]);
                 }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) m8[u] = fmaxf(m8[u], sv[kTcN - 8 + u]);
                 mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
                 if constexpr (!kScore) mx *= scale_log2;  // scale_log2 > 0: the max commutes with it
             } else {
