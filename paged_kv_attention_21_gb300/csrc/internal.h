@@ -209,6 +209,8 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& qmap, con
 
 cudaError_t launch_score_prefill_tc(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                                     const CUtensorMap& vmap, cudaStream_t stream);
+cudaError_t launch_bias_prefill_tc(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                   const CUtensorMap& vmap, cudaStream_t stream);
 
 // Rotary positions over strided rows (rope_quant.cu).
 struct RotateRows {

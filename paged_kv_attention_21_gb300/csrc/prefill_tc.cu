@@ -7,7 +7,7 @@ int prefill_tc_q_tile(int group) { return group >= 1 && group <= kTcM ? kTcM / g
 
 cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                               const CUtensorMap& vmap, cudaStream_t stream) {
-    return launch_prefill_tc_any<false>(a, qmap, kmap, vmap, stream);
+    return launch_prefill_tc_any<kTcPlain>(a, qmap, kmap, vmap, stream);
 }
 
 }  // namespace pkv

@@ -158,38 +158,58 @@ __device__ __forceinline__ void convert_e4m3_block(const uint8_t* codes, uint8_t
     }
 }
 
-// The scores of one row over a KV tile, raw on entry, in log2 units under the
-// score rule on exit.  dist0: the row's position minus the tile's first key.
-__device__ __forceinline__ void score_tile(float (&sv)[kTcN], const ScoreScale& sc, const TanhPair& tp, bool biased,
-                                           float slope2, int dist0) {
-    if (sc.out > 0.f) {
-        // (the warp takes one branch: the columns past the keys are whatever the tile holds)
-        if (__all_sync(0xFFFFFFFFu, in_poly(sv, sc.in))) {
+// The scores of one row over a KV tile, raw on entry, in log2 units with the bias and,
+// where the polynomial holds for all, the cap on exit.  d0: the row's position minus the
+// tile's first key.
+template <bool kCap>
+__device__ __forceinline__ void bias_tile(float (&sv)[kTcN], const ScoreScale& sc, const TanhPair& tp, float slope2,
+                                          float d0) {
+    if constexpr (kCap) {
 #pragma unroll
-            for (int e = 0; e < kTcN; e += 2) unpack_f32x2(tp(pack_f32x2(sv[e], sv[e + 1])), sv[e], sv[e + 1]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kTcN; ++e) sv[e] = sc.capped(sv[e]);
-        }
+        for (int e = 0; e < kTcN; e += 2) unpack_f32x2(tp(pack_f32x2(sv[e], sv[e + 1])), sv[e], sv[e + 1]);
     } else {
         const uint64_t in = pack_f32x2(sc.in, sc.in);
 #pragma unroll
         for (int e = 0; e < kTcN; e += 2) unpack_f32x2(mul_f32x2(pack_f32x2(sv[e], sv[e + 1]), in), sv[e], sv[e + 1]);
     }
-    if (biased) {
-        // (a distance past 2^24 is rounded, by 2^-24 of itself)
-        const float d0 = static_cast<float>(dist0);
 #pragma unroll
-        for (int e = 0; e < kTcN; ++e) sv[e] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e)), sv[e]);
+    for (int e = 0; e < kTcN; ++e) sv[e] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e)), sv[e]);
+}
+
+// 32 columns of a row from TMEM, any cap (and bias), columns past `cnt` masked: x - mu.
+template <bool kBiased>
+__device__ __forceinline__ void score_chunk(uint32_t addr, float (&v)[32], const ScoreScale& sc, const TanhPair& tp,
+                                            float slope2, float d0, int base, uint32_t cnt, float mu) {
+    tc::ld32(addr, v);
+    tc::wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        if constexpr (kBiased) {
+            float x0, x1;
+            capped_pair(sc, tp, v[e], v[e + 1], x0, x1);
+            v[e] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e)), x0) - mu;
+            v[e + 1] = fmaf(-slope2, fabsf(d0 - static_cast<float>(e + 1)), x1) - mu;
+        } else {
+            capped_pair(sc, tp, v[e], v[e + 1], -mu, v[e], v[e + 1]);
+        }
+        if (static_cast<uint32_t>(base + e) >= cnt) v[e] = -INFINITY;
+        if (static_cast<uint32_t>(base + e + 1) >= cnt) v[e + 1] = -INFINITY;
     }
 }
 
-template <int D, bool kFp8, bool kScore>
+// What a score rule asks of the softmax; each has its own kernel, as the code of those
+// that a call does not use cost the others up to a tenth.
+enum TcMode { kTcPlain, kTcRule, kTcCap, kTcBias, kTcBoth };  // kTcRule: its prefix and sinks alone
+
+template <int D, bool kFp8, int kMode>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
     using C = TcCfg<D, kFp8>;
+    constexpr bool kScore = kMode != kTcPlain;
+    constexpr bool kCapped = kMode == kTcCap;                     // a cap alone
+    constexpr bool kBiased = kMode == kTcBias || kMode == kTcBoth;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -604,10 +624,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 0) mbar_arrive(&bar_qc);
             }
         }
-        const ScoreScale sc(a.sm_scale, kScore ? a.cap : 0.f, a.k_scale ? a.k_scale[kvh] : 1.f);
+        const ScoreScale sc(a.sm_scale, kMode >= kTcCap ? a.cap : 0.f, a.k_scale ? a.k_scale[kvh] : 1.f);
         const TanhPair tp(sc);
-        const bool biased = kScore && a.slopes != nullptr;
-        const float slope2 = biased ? a.slopes[kvh * G + r % G] * kLog2e : 0.f;
+        const float slope2 = kBiased ? a.slopes[kvh * G + r % G] * kLog2e : 0.f;
         float m_used = -INFINITY;
         float l = 0.f;                             // the row sum
         for (int i = 0; ok && i < nx; ++i) {
@@ -629,35 +648,67 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // Row max.  Tiles wholly visible to the row (all but the diagonal
             // and the window edge) take the max of the raw scores, scaled once;
             // the others scale and mask every score (masked scores become -inf).
+            // Under a score rule: a bias changes the order of the scores, so that they are turned
+            // into logits first; a cap alone does not, and is taken off the largest and with the
+            // exponents.  Where a cap alone meets a mask, or any a score past its polynomial, the tile
+            // is read from TMEM again, 32 columns at a time (`slow`): unrolled over 128 columns that
+            // code was fetched so often that every tile paid.
             float mx;
-            if constexpr (kScore) score_tile(sv, sc, tp, biased, slope2, pos - k0);
+            bool slow = false;
+            int base = 0;  // column e holds a key that the row sees iff base + e < cnt, unsigned
+            uint32_t cnt = kTcN;
+            const float d0 = kBiased ? static_cast<float>(pos - k0) : 0.f;  // (past 2^24 rounded, by 2^-24 of itself)
+            auto row_keys = [&]() {  // the row sees keys [key_lo, key_hi]: one unsigned compare per score
+                const int key_hi = a.causal ? min(pos < prefix ? prefix - 1 : pos, kv_len - 1) : kv_len - 1;
+                const int key_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                cnt = key_hi >= key_lo ? static_cast<uint32_t>(key_hi + 1 - key_lo) : 0u;
+                base = k0 - key_lo;
+            };
+            if constexpr (kCapped || kMode == kTcBoth) {
+                if (!full_vis) row_keys();
+                slow = (kCapped && !full_vis) || !__all_sync(0xFFFFFFFFu, in_poly(sv, sc.in));
+            }
+            if constexpr (kBiased) {
+                if (!slow) bias_tile<kMode == kTcBoth>(sv, sc, tp, slope2, d0);
+            }
+            const float scale_now = kCapped || kBiased ? 1.f : scale_log2;
             if (full_vis) {
                 float m8[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m8[e] = sv[e];
+                for (int e = 0; e < 8; ++e) m8[e] = fmaxf(sv[e], sv[8 + e]);
 #pragma unroll
-                for (int e = 8; e + 16 <= kTcN; e += 16) {
+                for (int e = 16; e < kTcN; e += 16) {
 #pragma unroll
                     for (int u = 0; u < 8; ++u) m8[u] = fmax3(m8[u], sv[e + u], sv[e + 8 + u]);
                 }
-#pragma unroll
-                for (int u = 0; u < 8; ++u) m8[u] = fmaxf(m8[u], sv[kTcN - 8 + u]);
                 mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-                if constexpr (!kScore) mx *= scale_log2;  // scale_log2 > 0: the max commutes with it
+                mx *= scale_now;  // scale_now > 0: the max commutes with it
             } else {
-                // the row sees keys [key_lo, key_hi]: one unsigned compare per score
-                const int key_hi = a.causal ? min(pos < prefix ? prefix - 1 : pos, kv_len - 1) : kv_len - 1;
-                const int key_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-                const uint32_t cnt = key_hi >= key_lo ? static_cast<uint32_t>(key_hi + 1 - key_lo) : 0u;
-                const int base = k0 - key_lo;
+                if constexpr (!(kCapped || kMode == kTcBoth)) row_keys();
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < kTcN; ++e) {
                     const bool vis = static_cast<uint32_t>(base + e) < cnt;
-                    sv[e] = vis ? (kScore ? sv[e] : sv[e] * scale_log2) : -INFINITY;
+                    sv[e] = vis ? sv[e] * scale_now : -INFINITY;
                     m4[e & 3] = fmaxf(m4[e & 3], sv[e]);
                 }
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            }
+            if constexpr (kCapped)
+                mx = base + kTcN > 0 && (base < 0 || static_cast<uint32_t>(base) < cnt) ? sc.capped(mx) : -INFINITY;
+            if constexpr (kMode == kTcBoth) {
+                if (slow) {
+                    mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < kTcN; c += 32) {
+                        float v[32];
+                        score_chunk<true>(s_base + c, v, sc, tp, slope2, d0 - static_cast<float>(c), base + c, cnt, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) mx = fmax3(mx, v[e], v[e + 1]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kTcN; ++e) sv[e] = 0.f;  // not read again: their registers are free above
+                }
             }
             // lazy rescale: keep a stale max unless the new one exceeds it by 2^8
             const float m_new = fmaxf(m_used, mx);
@@ -705,18 +756,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // bf16 pairs (the lower key in the low half): keys 32 c .. 32 c + 31
             // go to P columns 16 c .. 16 c + 15
             const float mu = m_used == -INFINITY ? 0.f : m_used;
-            const float scale_p = full_vis && !kScore ? scale_log2 : 1.f;
+            const float scale_p = full_vis ? scale_now : 1.f;
             const uint64_t scl = pack_f32x2(scale_p, scale_p);
             const uint64_t neg = pack_f32x2(-mu, -mu);
             uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-            for (int c = 0; c < kTcN / 32; ++c) {
+            // the weights of columns 32 c .. from their exponents x(u), pairs
+            auto weights = [&](int c, auto x) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int u = 0; u < 16; ++u) {
-                    const uint64_t xv = fma_f32x2(pack_f32x2(sv[32 * c + 2 * u], sv[32 * c + 2 * u + 1]), scl, neg);
                     float x0, x1;
-                    unpack_f32x2(xv, x0, x1);
+                    unpack_f32x2(x(u), x0, x1);
                     const float p0 = fast_exp2(x0);
                     const float p1 = fast_exp2(x1);
                     const uint64_t pp = pack_f32x2(p0, p1);
@@ -724,12 +774,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     pk[u] = pack2<kFp8>(p0, p1);
                 }
                 tc::st16u(s_base + 16 * c, pk);
+            };
+            if ((kCapped || kMode == kTcBoth) && slow) {
+                // (P's columns 16 c .. cover scores of chunks that have been read)
+#pragma unroll 1
+                for (int c = 0; c < kTcN / 32; ++c) {
+                    float v[32];
+                    score_chunk<kBiased>(s_base + 32 * c, v, sc, tp, slope2, d0 - static_cast<float>(32 * c), base + 32 * c, cnt,
+                                         mu);
+                    weights(c, [&](int u) { return pack_f32x2(v[2 * u], v[2 * u + 1]); });
+                }
+            } else if (kCapped) {
+#pragma unroll
+                for (int c = 0; c < kTcN / 32; ++c)
+                    weights(c, [&](int u) { return tp(pack_f32x2(sv[32 * c + 2 * u], sv[32 * c + 2 * u + 1]), neg); });
+            } else {
+#pragma unroll
+                for (int c = 0; c < kTcN / 32; ++c)
+                    weights(c, [&](int u) {
+                        return fma_f32x2(pack_f32x2(sv[32 * c + 2 * u], sv[32 * c + 2 * u + 1]), scl, neg);
+                    });
             }
             {
-                float a0, a1, b0, b1, c0, c1, d0, d1;
+                float a0, a1, b0, b1;
                 unpack_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
                 unpack_f32x2(add_f32x2(acc[2], acc[3]), b0, b1);
-                (void)c0; (void)c1; (void)d0; (void)d1;
                 l += (a0 + a1) + (b0 + b1);
             }
             // PV_x(j-1) is done (S_x(j), issued after it, is done), so O may be rescaled
@@ -762,8 +831,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // epilogue: the row's O / l -> bf16 (or fp32), and its lse.  A tile
             // that gave up writes o = 0 and lse = -inf.
             float inv = ok && l > 0.f ? (a.v_scale ? a.v_scale[kvh] : 1.f) / l : 0.f;
-            float lse = ok && l > 0.f ? (m_used + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+            auto row_lse = [&]() { return ok && l > 0.f ? (m_used + __log2f(l)) * 0.6931471805599453f : -INFINITY; };
+            float lse = 0.f;
             if constexpr (kScore) {
+                lse = row_lse();
                 // a sink joins the normaliser: lse' = ln(e^lse + e^sink), o scaled by e^(lse - lse')
                 if (a.sinks && ok) {
                     const float sk = a.sinks[kvh * G + r % G];
@@ -802,7 +873,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             if (row_ok && a.lse_out)
-                a.lse_out[static_cast<size_t>(q0 + sp.tok0 + t) * a.hq + kvh * G + r % G] = lse;
+                a.lse_out[static_cast<size_t>(q0 + sp.tok0 + t) * a.hq + kvh * G + r % G] = kScore ? lse : row_lse();
         }
     }
 
@@ -814,12 +885,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-template <int D, bool kFp8, bool kScore>
+template <int D, bool kFp8, int kMode>
 cudaError_t launch_prefill_tc_t(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, cudaStream_t stream) {
     using C = TcCfg<D, kFp8>;
     static_assert(C::kSmemBytes <= 227 * 1024, "shared memory budget");
-    auto kern = prefill_tc_kernel<D, kFp8, kScore>;
+    auto kern = prefill_tc_kernel<D, kFp8, kMode>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -834,14 +905,14 @@ cudaError_t launch_prefill_tc_t(const PrefillArgs& a, const CUtensorMap& qmap, c
     return launch_pdl(kern, grid, dim3(kTcThreads), C::kSmemBytes, stream, a, qmap, kmap, vmap);
 }
 
-template <bool kScore>
+template <int kMode>
 cudaError_t launch_prefill_tc_any(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                                   const CUtensorMap& vmap, cudaStream_t stream) {
     if (a.fp8)
-        return a.d == 64 ? launch_prefill_tc_t<64, true, kScore>(a, qmap, kmap, vmap, stream)
-                         : launch_prefill_tc_t<128, true, kScore>(a, qmap, kmap, vmap, stream);
-    return a.d == 64 ? launch_prefill_tc_t<64, false, kScore>(a, qmap, kmap, vmap, stream)
-                     : launch_prefill_tc_t<128, false, kScore>(a, qmap, kmap, vmap, stream);
+        return a.d == 64 ? launch_prefill_tc_t<64, true, kMode>(a, qmap, kmap, vmap, stream)
+                         : launch_prefill_tc_t<128, true, kMode>(a, qmap, kmap, vmap, stream);
+    return a.d == 64 ? launch_prefill_tc_t<64, false, kMode>(a, qmap, kmap, vmap, stream)
+                     : launch_prefill_tc_t<128, false, kMode>(a, qmap, kmap, vmap, stream);
 }
 
 }  // namespace

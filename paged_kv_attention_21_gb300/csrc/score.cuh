@@ -89,6 +89,28 @@ struct TanhPair {
     }
 };
 
+// ScoreScale's capped(s) and capped(s, c) of two scores of every lane of the warp: the
+// pair's polynomial, and where some lane's |y| lies past it, capped() as well.
+__device__ __forceinline__ bool past_poly(const ScoreScale& sc, float s0, float s1) {
+    return __any_sync(0xFFFFFFFFu, !(fabsf(s0) * sc.in <= kTanhPoly && fabsf(s1) * sc.in <= kTanhPoly));
+}
+__device__ __forceinline__ void capped_pair(const ScoreScale& sc, const TanhPair& tp, float s0, float s1, float& x0,
+                                            float& x1) {
+    unpack_f32x2(tp(pack_f32x2(s0, s1)), x0, x1);
+    if (past_poly(sc, s0, s1)) {
+        x0 = sc.capped(s0);
+        x1 = sc.capped(s1);
+    }
+}
+__device__ __forceinline__ void capped_pair(const ScoreScale& sc, const TanhPair& tp, float s0, float s1, float c,
+                                            float& x0, float& x1) {
+    unpack_f32x2(tp(pack_f32x2(s0, s1), pack_f32x2(c, c)), x0, x1);
+    if (past_poly(sc, s0, s1)) {
+        x0 = sc.capped(s0, c);
+        x1 = sc.capped(s1, c);
+    }
+}
+
 // Whether max |s| over the N scores lies where the polynomial holds (a NaN: not looked at).
 template <int N>
 __device__ __forceinline__ bool in_poly(const float (&v)[N], float in) {
