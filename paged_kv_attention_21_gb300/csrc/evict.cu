@@ -312,58 +312,81 @@ __device__ __forceinline__ int compact_count(const CompactArgs& a, int seq, bool
     return min(n, a.max_kept);
 }
 
-// A thread moves one 16-byte piece of a row's K and V.
+// A thread moves one 16-byte piece of the K and V of kCmpRows rows.
+constexpr int kCmpRows = 2;
 __global__ void __launch_bounds__(kCmpThreads) compact_kernel(const CompactArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int seq = blockIdx.z, head = blockIdx.y;
-    const int pieces = a.row_bytes / 16;
+    const int pieces = a.row_bytes / 16, step = kCmpThreads / pieces;
     const int n = compact_count(a, seq, blockIdx.x == 0 && head == 0 && threadIdx.x == 0);
-    const int j = blockIdx.x * (kCmpThreads / pieces) + threadIdx.x / pieces;
+    const int j0 = blockIdx.x * step * kCmpRows + threadIdx.x / pieces;
     const int c = threadIdx.x % pieces;
-    if (j >= n) return;
-    int pos;
-    size_t src, dst;
-    if (!compact_rows(a, seq, head, j, pieces, &pos, &src, &dst)) return;
-    const uint4 k = __ldg(static_cast<const uint4*>(a.k_src) + src + c);
-    const uint4 v = __ldg(static_cast<const uint4*>(a.v_src) + src + c);
-    static_cast<uint4*>(a.k_dst)[dst + c] = k;
-    static_cast<uint4*>(a.v_dst)[dst + c] = v;
-    if (a.mass && c == 0) {
-        const size_t line = static_cast<size_t>(seq) * a.hkv + head;
-        a.mass_out[line * a.mass_out_stride + j] = a.mass[line * a.mass_stride + pos];
+    if (j0 >= n) return;
+    const size_t line = static_cast<size_t>(seq) * a.hkv + head;
+    int pos[kCmpRows];
+    size_t src[kCmpRows], dst[kCmpRows];
+    bool ok[kCmpRows];
+    uint4 k[kCmpRows], v[kCmpRows];
+    float w[kCmpRows];
+#pragma unroll
+    for (int r = 0; r < kCmpRows; ++r)
+        ok[r] = j0 + r * step < n && compact_rows(a, seq, head, j0 + r * step, pieces, &pos[r], &src[r], &dst[r]);
+#pragma unroll
+    for (int r = 0; r < kCmpRows; ++r) {
+        if (!ok[r]) continue;
+        k[r] = __ldg(static_cast<const uint4*>(a.k_src) + src[r] + c);
+        v[r] = __ldg(static_cast<const uint4*>(a.v_src) + src[r] + c);
+        if (a.mass && c == 0) w[r] = a.mass[line * a.mass_stride + pos[r]];
+    }
+#pragma unroll
+    for (int r = 0; r < kCmpRows; ++r) {
+        if (!ok[r]) continue;
+        static_cast<uint4*>(a.k_dst)[dst[r] + c] = k[r];
+        static_cast<uint4*>(a.v_dst)[dst[r] + c] = v[r];
+        if (a.mass && c == 0) a.mass_out[line * a.mass_out_stride + j0 + r * step] = w[r];
     }
 }
 
-// In place, one CTA per (KV head, sequence): kept ascends, so row j comes from a row
-// at or behind j.  The rows are taken in steps; every thread has read its row of the step
-// before any is written, and what later steps read lies behind all that is written.
+// In place: kept ascends, so row j comes from a row at or behind j.  One CTA per (KV head,
+// sequence, pool, 128-byte slice of its rows) -- slices never meet -- takes the rows in steps:
+// every thread has read its rows of a step before any is written, and what later steps read
+// lies behind all that is written.  A step costs a round trip to memory, so it is long: kInRows
+// rows a thread.  Slice 0 of K takes the weights along.
+constexpr int kInRows = 8;
 __global__ void __launch_bounds__(kCmpThreads) compact_in_place_kernel(const CompactArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int seq = blockIdx.y, head = blockIdx.x;
-    const int pieces = a.row_bytes / 16;
-    const int step = kCmpThreads / pieces;
-    const int n = compact_count(a, seq, head == 0 && threadIdx.x == 0);
-    const int c = threadIdx.x % pieces;
+    const int seq = blockIdx.z, head = blockIdx.y;
+    const int pieces = a.row_bytes / 16, mine = min(pieces, 8), step = kCmpThreads / mine;
+    const int slice = blockIdx.x >> 1;
+    uint4* pool = static_cast<uint4*>(blockIdx.x & 1 ? a.v_dst : a.k_dst) + slice * 8;
+    const int n = compact_count(a, seq, blockIdx.x == 0 && head == 0 && threadIdx.x == 0);
+    const int c = threadIdx.x % mine, row = threadIdx.x / mine;
+    const bool weights = a.mass && blockIdx.x == 0 && c == 0;
     const size_t line = static_cast<size_t>(seq) * a.hkv + head;
-    for (int j0 = 0; j0 < n; j0 += step) {
-        const int j = j0 + threadIdx.x / pieces;
-        int pos = 0;
-        size_t src = 0, dst = 0;
-        bool ok = j < n && compact_rows(a, seq, head, j, pieces, &pos, &src, &dst);
-        uint4 k, v;
-        float w = 0.f;
-        if (ok) {
-            k = static_cast<const uint4*>(a.k_dst)[src + c];
-            v = static_cast<const uint4*>(a.v_dst)[src + c];
-            if (a.mass && c == 0) w = a.mass[line * a.mass_stride + pos];
+    for (int j0 = row; j0 - row < n; j0 += step * kInRows) {
+        size_t dst[kInRows];
+        uint4 x[kInRows];
+        float w[kInRows];
+        uint32_t ok = 0;
+#pragma unroll
+        for (int r = 0; r < kInRows; ++r) {
+            int pos;
+            size_t src;
+            const int j = j0 + r * step;
+            if (j < n && compact_rows(a, seq, head, j, pieces, &pos, &src, &dst[r])) {
+                ok |= 1u << r;
+                x[r] = pool[src + c];
+                if (weights) w[r] = a.mass[line * a.mass_stride + pos];
+            }
         }
         __syncthreads();
-        if (ok) {
-            static_cast<uint4*>(a.k_dst)[dst + c] = k;
-            static_cast<uint4*>(a.v_dst)[dst + c] = v;
-            if (a.mass && c == 0) a.mass_out[line * a.mass_out_stride + j] = w;
+#pragma unroll
+        for (int r = 0; r < kInRows; ++r) {
+            if (!(ok >> r & 1u)) continue;
+            pool[dst[r] + c] = x[r];
+            if (weights) a.mass_out[line * a.mass_out_stride + j0 + r * step] = w[r];
         }
     }
 }
@@ -381,9 +404,12 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
-    if (a.in_place) return launch_pdl(compact_in_place_kernel, dim3(a.hkv, a.num_seqs), dim3(kCmpThreads), 0, stream, a);
-    const int step = kCmpThreads / (a.row_bytes / 16);
-    const dim3 grid((a.max_kept + step - 1) / step, a.hkv, a.num_seqs);
+    if (a.in_place) {
+        const unsigned slices = (a.row_bytes + 127) / 128;
+        return launch_pdl(compact_in_place_kernel, dim3(2 * slices, a.hkv, a.num_seqs), dim3(kCmpThreads), 0, stream, a);
+    }
+    const int64_t step = static_cast<int64_t>(kCmpThreads) / (a.row_bytes / 16) * kCmpRows;
+    const dim3 grid(static_cast<unsigned>((a.max_kept + step - 1) / step), a.hkv, a.num_seqs);
     return launch_pdl(compact_kernel, grid, dim3(kCmpThreads), 0, stream, a);
 }
 
