@@ -62,7 +62,8 @@ struct MtRows {
 };
 
 // The weights of 32 columns, all seen by this key, without a bias, summed.
-template <bool kCap>
+enum { kMtPlain, kMtNear, kMtPoly };  // no cap; every |y| <= kTanhNear, kTanhPoly
+template <int kCap>
 __device__ __forceinline__ float sum_seen(const float (&v)[32], const float* neg_lse, const ScoreScale& sc,
                                           const TanhPair& tp) {
     const uint64_t scl = pack_f32x2(sc.in, sc.in);
@@ -74,7 +75,7 @@ __device__ __forceinline__ float sum_seen(const float (&v)[32], const float* neg
         for (int w = 0; w < 2; ++w) {
             const uint64_t s = pack_f32x2(v[2 * (u + w)], v[2 * (u + w) + 1]);
             const uint64_t n = w ? nl.y : nl.x;
-            const uint64_t e = kCap ? tp(s, n) : fma_f32x2(s, scl, n);
+            const uint64_t e = kCap == kMtNear ? tp.near(s, n) : kCap == kMtPoly ? tp(s, n) : fma_f32x2(s, scl, n);
             float x0, x1;
             unpack_f32x2(e, x0, x1);
             acc[w] = add_f32x2(acc[w], pack_f32x2(fast_exp2(x0), fast_exp2(x1)));
@@ -596,10 +597,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                         }
                         const int4 ch = r.chunk[c >> 5];
                         if (ch.z > k_last || ch.w < k0) continue;
-                        const bool poly = !capped || __all_sync(0xFFFFFFFFu, in_poly(v, sc.in));
+                        // (keys past the last are whatever the tile holds: not looked at)
+                        const float y = capped && t <= k_last ? largest(v, sc.in) : 0.f;
+                        const bool poly = __all_sync(0xFFFFFFFFu, y <= kTanhPoly);
                         if (ch.x <= k0 && ch.y >= k_last && poly && !biased)
-                            sum += capped ? sum_seen<true>(v, r.neg_lse + c, sc, tp)
-                                          : sum_seen<false>(v, r.neg_lse + c, sc, tp);
+                            sum += !capped ? sum_seen<kMtPlain>(v, r.neg_lse + c, sc, tp)
+                                   : __all_sync(0xFFFFFFFFu, y <= kTanhNear) ? sum_seen<kMtNear>(v, r.neg_lse + c, sc, tp)
+                                                                             : sum_seen<kMtPoly>(v, r.neg_lse + c, sc, tp);
                         else
                             sum += sum_edge(v, r, c, sc, tp, poly, biased, static_cast<float>(t - w.s.off), t);
                     }

@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // is read from TMEM again, 32 columns at a time (`slow`): unrolled over 128 columns that
             // code was fetched so often that every tile paid.
             float mx;
-            bool slow = false;
+            bool slow = false, near = false;
             int base = 0;  // column e holds a key that the row sees iff base + e < cnt, unsigned
             uint32_t cnt = kTcN;
             const float d0 = kBiased ? static_cast<float>(pos - k0) : 0.f;  // (past 2^24 rounded, by 2^-24 of itself)
@@ -666,7 +666,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             if constexpr (kCapped || kMode == kTcBoth) {
                 if (!full_vis) row_keys();
-                slow = (kCapped && !full_vis) || !__all_sync(0xFFFFFFFFu, in_poly(sv, sc.in));
+                const float y = largest(sv, sc.in);
+                slow = (kCapped && !full_vis) || !__all_sync(0xFFFFFFFFu, y <= kTanhPoly);
+                near = __all_sync(0xFFFFFFFFu, y <= kTanhNear);
             }
             if constexpr (kBiased) {
                 if (!slow) bias_tile<kMode == kTcBoth>(sv, sc, tp, slope2, d0);
@@ -784,6 +786,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                          mu);
                     weights(c, [&](int u) { return pack_f32x2(v[2 * u], v[2 * u + 1]); });
                 }
+            } else if (kCapped && near) {  // (a wholly visible tile: no score of it is chance)
+#pragma unroll
+                for (int c = 0; c < kTcN / 32; ++c)
+                    weights(c, [&](int u) { return tp.near(pack_f32x2(sv[32 * c + 2 * u], sv[32 * c + 2 * u + 1]), neg); });
             } else if (kCapped) {
 #pragma unroll
                 for (int c = 0; c < kTcN / 32; ++c)

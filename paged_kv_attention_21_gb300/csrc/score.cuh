@@ -23,6 +23,13 @@ constexpr float kTanhC2 = -0.05355885997414589f;
 constexpr float kTanhC3 = 0.020091967657208443f;
 constexpr float kTanhC4 = -0.005138659384101629f;
 
+// The same for |y| <= 0.3, off by 1.2e-8: three coefficients serve where all of a tile's
+// scores are that small, as most are.
+constexpr float kTanhNear = 0.3f;
+constexpr float kTanhN0 = -0.33333060145378113f;
+constexpr float kTanhN1 = 0.13314832746982574f;
+constexpr float kTanhN2 = -0.05036623775959015f;
+
 // For any y: e^2|y| overflows to inf from |y| = 44 on, where tanh is 1 to fp32.
 __device__ __forceinline__ float tanh_exp(float y) {
     const float e = fast_exp2(fabsf(y) * 2.8853900817779268f);
@@ -32,8 +39,8 @@ __device__ __forceinline__ float tanh_exp(float y) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What a kernel needs of the rule for one KV head (kscale: the head's e4m3 scale, or 1).
-// A score's logit has the same bits whichever of the forms below computes it: which one
-// does may depend on the scores beside it.
+// A score's logit has the same bits whichever of the forms below computes it, but for
+// TanhPair::near: which form does may depend on the scores beside it.
 struct ScoreScale {
     float in;    // s -> y = sm_scale s / cap with a cap, else s -> log2 units
     float out;   // cap log2(e) with a cap, else 0
@@ -64,12 +71,18 @@ struct ScoreScale {
 
 // ScoreScale's capped(), two logits at a time, where every |y| <= kTanhPoly.
 struct TanhPair {
-    uint64_t in, c0, c1, c2, c3, c4, one;
+    uint64_t in, c0, c1, c2, c3, c4, one, n0, n1, n2;
     __device__ __forceinline__ explicit TanhPair(const ScoreScale& sc) {
         in = pack_f32x2(sc.in, sc.in);
         auto twice = [&](float k) { return pack_f32x2(k * sc.out, k * sc.out); };
         one = twice(1.f), c0 = twice(kTanhC0), c1 = twice(kTanhC1), c2 = twice(kTanhC2);
         c3 = twice(kTanhC3), c4 = twice(kTanhC4);
+        n0 = twice(kTanhN0), n1 = twice(kTanhN1), n2 = twice(kTanhN2);
+    }
+    // |y| <= kTanhNear.  Chosen by scores that are the sequence's own, so that a call repeats its bits
+    __device__ __forceinline__ uint64_t near(uint64_t s, uint64_t c) const {
+        const uint64_t y = mul_f32x2(s, in), z = mul_f32x2(y, y);
+        return fma_f32x2(y, fma_f32x2(z, fma_f32x2(z, fma_f32x2(z, n2, n1), n0), one), c);
     }
     __device__ __forceinline__ uint64_t factor(uint64_t y) const {  // out tanh(y) / y
         const uint64_t z = mul_f32x2(y, y);
@@ -111,13 +124,13 @@ __device__ __forceinline__ void capped_pair(const ScoreScale& sc, const TanhPair
     }
 }
 
-// Whether max |s| over the N scores lies where the polynomial holds (a NaN: not looked at).
+// The largest |y| of N scores (a NaN: not looked at).
 template <int N>
-__device__ __forceinline__ bool in_poly(const float (&v)[N], float in) {
+__device__ __forceinline__ float largest(const float (&v)[N], float in) {
     float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < N; e += 2) m[(e >> 1) & 3] = fmax3(m[(e >> 1) & 3], fabsf(v[e]), fabsf(v[e + 1]));
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * in <= kTanhPoly;
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * in;
 }
 
 }  // namespace pkv
