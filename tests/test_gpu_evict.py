@@ -239,3 +239,87 @@ def test_a_cache_is_thinned_and_served_on(kv, d, hq, hkv, in_place):
                     want[:, :n - 1] += float(np.float32(0.9)) * before[s, :, :n - 1]
                     close(mass[s, :, :n], want, bound + 8 * 2.0 ** -24 * want)
     assert pkv.pkv_device_errors() == 0
+
+
+def test_a_step_and_a_thinning_captured_and_replayed():
+    """Decode, weights, choice and move in one graph, replayed on new queries; the same bits as
+    eager calls on another stream."""
+    p = Paged([200, 333, 90], 8, 2, 128, seed=21)
+    r = Rule(128, 8, 3, cap=15.0, slopes=0.05)
+    qs = [p.queries(3)[0] for _ in range(3)]
+    q = qs[0].clone()
+    ws = torch.zeros(max(256, pkv.pkv_decode_workspace_size(p.desc, 3, 333)), dtype=torch.uint8, device=DEV)
+    dst_tables = torch.arange(12, dtype=torch.int32, device=DEV).reshape(3, 4)
+    dst_desc = p.make_desc(num_blocks=12, max_blocks_per_seq=4)
+
+    def buffers():
+        return dict(out=torch.zeros_like(q), lse=torch.zeros(3, 8, device=DEV), mass=torch.zeros(3, 2, 336, device=DEV),
+                    kept=torch.zeros(3, 2, 50, dtype=torch.int32, device=DEV),
+                    kept_lens=torch.zeros(3, dtype=torch.int32, device=DEV),
+                    k=torch.zeros(12, 2, 16, 128, dtype=torch.bfloat16, device=DEV),
+                    v=torch.zeros(12, 2, 16, 128, dtype=torch.bfloat16, device=DEV), m=torch.zeros(3, 2, 50, device=DEV))
+
+    def step(b):
+        pkv.pkv_score_decode(p.desc, r.score, q, p.k_pool, p.v_pool, p.t, p.lens_t, 333, b["out"], b["lse"], ws)
+        pkv.pkv_score_mass(p.desc, r.score, q, None, p.k_pool, p.t, p.lens_t, 333, b["lse"], b["mass"], keep=0.5)
+        pkv.pkv_evict_select(b["mass"], p.lens_t, 333, 50, 2, 5, b["kept"], b["kept_lens"])
+        pkv.pkv_evict_compact(p.desc, p.k_pool, p.v_pool, p.t, b["kept"], b["kept_lens"], dst_desc=dst_desc, k_dst=b["k"],
+                              v_dst=b["v"], dst_tables=dst_tables, mass=b["mass"], mass_out=b["m"])
+    eager, graphed = buffers(), buffers()
+    step(buffers())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(graphed)
+    for x in graphed.values():
+        x.zero_()
+    side = torch.cuda.Stream()
+    for new in qs:
+        q.copy_(new)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            step(eager)
+        torch.cuda.synchronize()
+        for name in eager:
+            assert torch.equal(eager[name], graphed[name]), name
+    assert pkv.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("e4m3", 64)])
+def test_in_place_over_many_steps(kv, d):
+    """Thousands of rows of one sequence: every step of the move reads behind what it writes, also
+    where hardly anything moves, and where all of it moves far."""
+    n = 9000
+    p = Paged([n], 2, 2, d, kv, seed=22)
+    rng = np.random.default_rng(23)
+    for kind in range(3):
+        kept = np.zeros((1, 2, 5000), np.int32)
+        for h in range(2):
+            kept[0, h] = (np.sort(rng.permutation(n)[:5000]) if kind == 0 else
+                          np.concatenate([np.arange(4999), [n - 1]]) if kind == 1 else np.arange(n - 5000, n))
+        src = [x.clone() for x in (p.k_pool, p.v_pool)]
+        pkv.pkv_evict_compact(p.desc, p.k_pool, p.v_pool, p.t, torch.from_numpy(kept).to(DEV),
+                              torch.tensor([5000], dtype=torch.int32, device=DEV))
+        for h in range(2):
+            for a, b in zip(src, (p.k_pool, p.v_pool)):
+                assert np.array_equal(rows_of(b, p.tables, 0, h, range(5000)), rows_of(a, p.tables, 0, h, kept[0, h])), kind
+    assert pkv.pkv_device_errors() == 0
+
+
+def test_blocks_past_32_bits_are_moved():
+    k, v = (torch.zeros(140004, 8, 16, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k[140000:] = torch.randn(4, 8, 16, 128, device=DEV).bfloat16()
+    v[140000:] = torch.randn(4, 8, 16, 128, device=DEV).bfloat16()
+    desc = pkv.make_desc(num_q_heads=8, num_kv_heads=8, head_dim=128, num_blocks=140004, max_blocks_per_seq=4)
+    src = torch.arange(140000, 140004, dtype=torch.int32, device=DEV)[None]
+    dst = torch.tensor([[139999, 139998, 0, 1]], dtype=torch.int32, device=DEV)
+    kept = torch.stack([torch.sort(torch.randperm(64)[:40]).values for _ in range(8)])[None].int().to(DEV)
+    pkv.pkv_evict_compact(desc, k, v, src, kept, torch.tensor([40], dtype=torch.int32, device=DEV), dst_desc=desc, k_dst=k,
+                          v_dst=v, dst_tables=dst)
+    assert pkv.pkv_device_errors() == 0
+    for pool in (k, v):
+        rows = pool[140000:].transpose(0, 1).reshape(8, 64, 128)
+        got = torch.cat([pool[139999], pool[139998], pool[0]], 1)[:, :40]
+        assert torch.equal(got, torch.gather(rows, 1, kept[0].long()[..., None].expand(-1, -1, 128)))

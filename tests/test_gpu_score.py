@@ -278,3 +278,88 @@ def test_mass_of_many_ragged_sequences(kv, hq, hkv, d, q_max):
     start = torch.rand(70, hkv, max(lens), device="cuda")
     got = mass_of(p, r, q, qo_t, lse, start, 1.0, q_max)
     check_mass(p, r, q64, qo, lse, start, 1.0, got)
+
+
+def test_mass_counts_at_most_max_q_len():
+    """More queries than the bound: the first ones count, the flag says so."""
+    p = Paged([90, 200], 4, 2, 64, seed=12)
+    r = Rule(64, 4, 2)
+    for q_lens, top in (([3, 6], 4), ([60, 90], 70)):
+        qo, qo_t, q, q64 = problem(p, q_lens)
+        lse = torch.rand(q.shape[:2], device="cuda") + 4
+        start = torch.rand(2, 2, 200, device="cuda")
+        got = mass_of(p, r, q, qo_t, lse, start, 1.0, top).cpu().numpy().astype(np.float64)
+        assert pkv.pkv_device_errors() == pkv.DEVERR_LENGTH
+        for s, n in enumerate(p.lens):
+            a, m = int(qo[s]), min(q_lens[s], top)
+            pos = np.arange(n - q_lens[s], n)[:m]
+            want, bound = r.mass(p, s, q64[a:a + m], pos, lse[a:a + m].cpu().numpy())
+            own = n - q_lens[s]
+            want[:, :own] += start[s, :, :own].cpu().numpy()
+            close(got[s, :, :n], want, bound + 2.0 ** -24 * (m + 8) * want + 1e-38)
+
+
+def test_mass_refuses_on_the_device_more_queries_than_keys():
+    p = Paged([3, 40], 4, 2, 64, seed=13)
+    r = Rule(64, 4, 2)
+    qo_t = torch.tensor([0, 5, 7], dtype=torch.int32, device="cuda")
+    q, _ = p.queries(7)
+    start = torch.rand(2, 2, 40, device="cuda")
+    for top in (5, 40):
+        got = mass_of(p, r, q, qo_t, torch.zeros(7, 4, device="cuda"), start, 1.0, top)
+        assert pkv.pkv_device_errors() == pkv.DEVERR_POSITION
+        assert torch.equal(got[0], start[0]) and not torch.equal(got[1], start[1])
+
+
+def test_infinite_keys_that_no_query_sees_change_nothing():
+    """Values no query may look at: K and V rows behind the window, and behind a query's
+    position where the keys of the same tile are K alone."""
+    p = Paged([400], 8, 2, 64, seed=14)
+    r = Rule(64, 8, 1, cap=12.0, window=100)
+    q, q64 = p.queries(1)
+    lse0 = decode(p, r, q)
+    mass0 = mass_of(p, r, q, None, lse0[1], torch.zeros(1, 2, 400, device="cuda"), 0.0, 1)
+    for bad in (float("inf"), float("-inf"), float("nan"), 3e38, -3e38):
+        for t in (0, 150, 299):
+            for pool in (p.k_pool, p.v_pool):
+                pool[p.tables[0, t // 16], :, t % 16] = bad
+        out, lse = decode(p, r, q)
+        assert torch.equal(out, lse0[0]) and torch.equal(lse, lse0[1])
+        got = mass_of(p, r, q, None, lse, torch.zeros(1, 2, 400, device="cuda"), 0.0, 1)
+        assert torch.equal(got, mass0)
+    # the observers of a prompt's end: keys past a query's position are masked, not multiplied
+    p = Paged([256], 2, 1, 64, seed=15)
+    r = Rule(64, 2, 1)
+    for m in (8, 100):
+        q, q64 = p.queries(m)
+        qo_t = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+        lse = torch.full((m, 2), 5.0, device="cuda")
+        lse[-1] = float("-inf")  # the only query that sees the last key counts for nothing
+        start = torch.zeros(1, 1, 256, device="cuda")
+        want = mass_of(p, r, q, qo_t, lse, start, 0.0, m)
+        kept = p.k_pool.clone()
+        p.k_pool[p.tables[0, 15], :, 15] = 1e30
+        got = mass_of(p, r, q, qo_t, lse, start, 0.0, m)
+        assert torch.equal(got[..., :255], want[..., :255])
+        p.k_pool.copy_(kept)
+
+
+def test_pools_past_32_bits():
+    """Blocks whose bytes lie past 2^32 in pools of 4.6 GB."""
+    p = Paged([100, 300], 32, 8, 128, seed=16)
+    far = 140000
+    k, v = (torch.zeros(far + p.nb, 8, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[far:], v[far:] = p.k_pool, p.v_pool
+    p.k_pool, p.v_pool, p.nb = k, v, far + p.nb
+    p.tables = np.where(p.tables >= 0, p.tables + far, -1).astype(np.int32)
+    p.t, p.desc = torch.from_numpy(p.tables).to("cuda"), p.make_desc()
+    r = Rule(128, 32, 2, cap=20.0)
+    q, q64 = p.queries(2)
+    out, lse = decode(p, r, q)
+    check_decode(p, r, q64, out, lse)
+    for q_lens in ([3, 5], [60, 90]):
+        qo, qo_t, q, q64 = problem(p, q_lens)
+        out, lse = prefill(p, r, q, qo, qo_t)
+        check_prefill(p, r, q64, qo, out, lse)
+        start = torch.rand(2, 8, 300, device="cuda")
+        check_mass(p, r, q64, qo, lse, start, 1.0, mass_of(p, r, q, qo_t, lse, start, 1.0, max(q_lens)))
