@@ -412,11 +412,14 @@ __global__ void __launch_bounds__(kCmpThreads) compact_in_place_kernel(const Com
 }  // namespace
 
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream) {
-    // CTAs per row: more while a CTA would hold more than 4096 keys and the GPU has room for
-    // them, and while it could not hold its keys in 64 KB
+    // CTAs per row.  A CTA alone takes 7.5 us for 8192 keys, 10 for 16384 and 17 for 32768;
+    // eight take 8, 8 and 9 for one of a few rows, but clusters are launched one after the other,
+    // some 27 CTAs a microsecond: 128 rows of 16384 keys take 11.5, 14, 22 and 42 us with 1, 2, 4
+    // and 8, 256 rows of 32768 keys 42 and 38 with 1 and 2.  So: as many as hold 16384 keys each, and more
+    // while the CTAs are few.
     const int64_t rows = static_cast<int64_t>(a.hkv) * a.num_seqs;
     int c = 1;
-    while (c < 8 && ((a.max_kv / c > 4096 && rows * c < 2 * a.num_sms) || a.max_kv / c > 16384)) c *= 2;
+    while (c < 8 && (a.max_kv > 16384 * c || (a.max_kv > 8192 && rows * 2 * c <= 128))) c *= 2;
     return c == 1 ? launch_select_t<1>(a, stream) : c == 2 ? launch_select_t<2>(a, stream)
          : c == 4 ? launch_select_t<4>(a, stream) : launch_select_t<8>(a, stream);
 }
