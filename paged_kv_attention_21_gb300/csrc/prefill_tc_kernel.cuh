@@ -677,12 +677,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (full_vis) {
                 float m8[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m8[e] = fmaxf(sv[e], sv[8 + e]);
+                for (int e = 0; e < 8; ++e) m8[e] = sv[e];
 #pragma unroll
-                for (int e = 16; e < kTcN; e += 16) {
+                for (int e = 8; e + 16 <= kTcN; e += 16) {
 #pragma unroll
                     for (int u = 0; u < 8; ++u) m8[u] = fmax3(m8[u], sv[e + u], sv[e + 8 + u]);
                 }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) m8[u] = fmax3(m8[u], sv[kTcN - 8 + 2 * u], sv[kTcN - 7 + 2 * u]);
                 mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
                 mx *= scale_now;  // scale_now > 0: the max commutes with it
             } else {
