@@ -52,6 +52,10 @@ struct MtCfg {
     static constexpr int kSmemBytes = kBody + 1024 > 120 * 1024 ? kBody + 1024 : 120 * 1024;
 };
 
+// What a score rule asks of the epilogue: neither cap nor bias, a cap alone, a bias with or
+// without a cap.
+enum MtMode { kMtNone, kMtCap, kMtBias };
+
 // What the epilogue needs of a step's query rows, by column.
 struct MtRows {
     float neg_lse[kMtCols];   // -log2(e) lse; -inf: the row adds nothing
@@ -88,23 +92,24 @@ __device__ __forceinline__ float sum_seen(const float (&v)[32], const float* neg
 
 // The weights of 32 columns, of which this key (tf: its distance to the first query) may
 // be hidden from some.  poly: the polynomial holds for every score of the warp.
+template <int kMode>
 __device__ __forceinline__ float sum_edge(const float (&v)[32], const MtRows& q, int c0, const ScoreScale& sc,
-                                          const TanhPair& tp, bool poly, bool biased, float tf, int t) {
+                                          const TanhPair& tp, bool poly, float tf, int t) {
     float x[32];
-    if (poly && sc.out > 0.f) {
+    if (kMode != kMtNone && poly && sc.out > 0.f) {
 #pragma unroll
         for (int e = 0; e < 32; e += 2)
             unpack_f32x2(tp(pack_f32x2(v[e], v[e + 1]), pack_f32x2(q.neg_lse[c0 + e], q.neg_lse[c0 + e + 1])), x[e], x[e + 1]);
     } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = sc(v[e], q.neg_lse[c0 + e]);
+        for (int e = 0; e < 32; ++e) x[e] = kMode == kMtNone ? fmaf(v[e], sc.in, q.neg_lse[c0 + e]) : sc(v[e], q.neg_lse[c0 + e]);
     }
     float part[2] = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
         const int c = c0 + e;
         float z = x[e];
-        if (biased) z = fmaf(-q.slope[c], fabsf(q.tok[c] - tf), z);
+        if (kMode == kMtBias) z = fmaf(-q.slope[c], fabsf(q.tok[c] - tf), z);
         const float w = fast_exp2(z);
         const int2 sp = q.span[c];
         part[e & 1] += t >= sp.x && t <= sp.y ? w : 0.f;
@@ -222,7 +227,7 @@ struct MtStages {
     __device__ __forceinline__ int parity(int st) const { return (uses[st] - 1) & 1; }
 };
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, int kMode>
 __global__ void __launch_bounds__(kMtThreads, 1)
     mass_tc_kernel(const MassArgs a, const int raw_stages, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap) {
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         ScoreScale sc(a.sm_scale, a.cap, 1.f);
         TanhPair tp(sc);
         const float in1 = sc.in;  // with a scale of 1
-        const bool capped = sc.out > 0.f, biased = a.slopes != nullptr;
+        const bool capped = kMode == kMtCap || (kMode == kMtBias && sc.out > 0.f);
         int nraw = 0, loads = 0, used = 0, held = 0;  // held: stages of a resident segment's rows in use
         bool ok = true, q_due = false;
         MtStages q;
@@ -586,6 +591,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                     if (!ok) break;
                     tc::fence_after_sync();
                     const MtRows& r = rows[st];
+#pragma unroll 1
                     for (int c = 0; c < kMtCols; c += 32) {
                         float v[32];
                         tc::ld32(s_addr + c, v);
@@ -600,12 +606,15 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                         // (keys past the last are whatever the tile holds: not looked at)
                         const float y = capped && t <= k_last ? largest(v, sc.in) : 0.f;
                         const bool poly = __all_sync(0xFFFFFFFFu, y <= kTanhPoly);
-                        if (ch.x <= k0 && ch.y >= k_last && poly && !biased)
-                            sum += !capped ? sum_seen<kMtPlain>(v, r.neg_lse + c, sc, tp)
-                                   : __all_sync(0xFFFFFFFFu, y <= kTanhNear) ? sum_seen<kMtNear>(v, r.neg_lse + c, sc, tp)
-                                                                             : sum_seen<kMtPoly>(v, r.neg_lse + c, sc, tp);
-                        else
-                            sum += sum_edge(v, r, c, sc, tp, poly, biased, static_cast<float>(t - w.s.off), t);
+                        if (kMode != kMtBias && ch.x <= k0 && ch.y >= k_last && poly) {
+                            if constexpr (kMode == kMtNone)
+                                sum += sum_seen<kMtPlain>(v, r.neg_lse + c, sc, tp);
+                            else
+                                sum += __all_sync(0xFFFFFFFFu, y <= kTanhNear) ? sum_seen<kMtNear>(v, r.neg_lse + c, sc, tp)
+                                                                               : sum_seen<kMtPoly>(v, r.neg_lse + c, sc, tp);
+                        } else {
+                            sum += sum_edge<kMode>(v, r, c, sc, tp, poly, static_cast<float>(t - w.s.off), t);
+                        }
                     }
                 }
                 __syncwarp();
@@ -627,11 +636,11 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     }
 }
 
-template <int D, bool kFp8>
-cudaError_t launch_mass_tc_t(const MassArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, cudaStream_t stream) {
+template <int D, bool kFp8, int kMode>
+cudaError_t launch_mass_tc_m(const MassArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, cudaStream_t stream) {
     using C = MtCfg<D, kFp8>;
     static_assert(C::kSmemBytes <= 227 * 1024 - 14 * 1024, "shared memory: the arena, the rows' constants, the barriers");
-    auto kern = mass_tc_kernel<D, kFp8>;
+    auto kern = mass_tc_kernel<D, kFp8, kMode>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -647,6 +656,13 @@ cudaError_t launch_mass_tc_t(const MassArgs& a, const CUtensorMap& qmap, const C
     const dim3 grid(static_cast<unsigned>(min(int64_t{max(1, a.num_sms)}, tiles)));
     return launch_pdl(kern, grid, dim3(kMtThreads), C::kSmemBytes, stream, a, a.max_q <= a.q_tile ? C::kMaxRaw : 1,
                       qmap, kmap);
+}
+
+template <int D, bool kFp8>
+cudaError_t launch_mass_tc_t(const MassArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, cudaStream_t stream) {
+    if (a.slopes) return launch_mass_tc_m<D, kFp8, kMtBias>(a, qmap, kmap, stream);
+    return a.cap > 0.f ? launch_mass_tc_m<D, kFp8, kMtCap>(a, qmap, kmap, stream)
+                       : launch_mass_tc_m<D, kFp8, kMtNone>(a, qmap, kmap, stream);
 }
 
 }  // namespace
