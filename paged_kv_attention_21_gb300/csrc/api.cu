@@ -2070,6 +2070,8 @@ pkv_status pkv_evict_select(const float* mass, int64_t mass_stride, const int32_
     if (!mass || !kv_lens || !kept || !kept_lens) return fail(PKV_ERR_INVALID_ARG, "null device pointer");
     if (!aligned(mass, 4) || !aligned(kv_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4))
         return fail(PKV_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
+    if (kept_lens < kv_lens + num_seqs && kv_lens < kept_lens + num_seqs)  // written while other heads' CTAs read kv_lens
+        return fail(PKV_ERR_INVALID_ARG, "kept_lens overlaps kv_lens");
     uint32_t* err = nullptr;
     int sms = 0;
     const pkv_status st = device_state(&err, &sms);

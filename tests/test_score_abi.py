@@ -148,6 +148,12 @@ def test_select_refusals(lib):
     assert call_select(lib, n=0) == 0
 
 
+@pytest.mark.parametrize("at,n", [(0, 2), (4, 2), (-4, 2), (0, 1), (-4 * 65534, 65535), (4 * 65534, 65535)])
+def test_select_refuses_lengths_written_over_those_it_reads(lib, at, n):
+    lens = 0x500000
+    refused(call_select(lib, n=n, lens=ctypes.c_void_p(lens), kl=ctypes.c_void_p(lens + at)), 1, "overlaps")
+
+
 def call_compact(lib, d=None, dd=None, **kw):
     a = dict(k=P, v=P2, bt=P, kept=P, ks=8, kl=P, n=1, top=8, kd=ctypes.c_void_p(0x300000), vd=ctypes.c_void_p(0x400000),
              dt=P3, mass=None, ms=0, mo=None, mos=0)
