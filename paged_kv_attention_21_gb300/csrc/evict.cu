@@ -51,22 +51,25 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
 // any case, count as larger than any weight, so that one selection of the `budget` largest
 // is left.  The threshold is found digit by digit (11, 11 and 10 bits) from histograms,
 // which the CTAs read from one another; no further digit is looked at once the keys that
-// share the found ones are all kept.  Then every warp counts what it keeps of a contiguous
-// part, and writes it in order.  Four keys a thread: instructions bound it (one key at a
-// time took 31 us for 512 rows of up to 16384 keys).
+// share the found ones are all kept.  The first digit's histogram is of all keys.  Then a
+// thread takes up to 32 neighbouring keys and has a bit for each that is above the digits and
+// for each that shares them; later digits look at the latter alone, and at the end a scan
+// over the threads' counts says where each writes its own.  Instructions bound it (512 rows of
+// up to 16384 keys: 31 us with one key at a time, 20 with every digit over all keys and the
+// places from a ballot for every 32 keys, 17 so; the loads alone 6.8).
 template <int C>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a, const int cached) {
+__global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs a, const int cached) {
     extern __shared__ uint4 s_key[];                 // [cached / 4]
     __shared__ __align__(16) int hist[kSelBins];
     // the cluster's histogram: the CTAs add their bins to one another's, by turns to one of two
     __shared__ __align__(16) int whole[C > 1 ? 2 : 1][C > 1 ? kSelBins : 4];
     __shared__ int part[kSelWarps];
     __shared__ int s_digit, s_rest, s_all;
-    __shared__ int s_gt[kSelWarps], s_eq[kSelWarps], s_sum[2];
+    __shared__ int s_sum[2];
     pdl_wait();
     pdl_launch_dependents();
     const int seq = blockIdx.y, head = blockIdx.x / C, rank = blockIdx.x % C;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     int n = a.kv_lens[seq];
     if (n > a.max_kv) {
         if (tid == 0 && blockIdx.x == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
@@ -113,8 +116,38 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
         }
         return make_uint4(k[0], k[1], k[2], k[3]);
     };
-    auto keys = [&](int i) { return in_smem ? s_key[i] : load(i); };
+    // fours are stored so that neither eight neighbours nor eight that lie two, four or eight apart meet in a bank
+    auto slot = [](int i) { return i ^ (i >> 3 & 7); };
+    auto key_at = [&](int j) {  // key j of the part
+        if (in_smem) return reinterpret_cast<const uint32_t*>(s_key)[4 * slot(j >> 2) + (j & 3)];
+        if (j >= m) return 0u;
+        return c0 + j < lo || c0 + j >= hi ? 0xFFFFFFFFu : weight_key(row[c0 + j]);
+    };
     uint32_t found = 0, mask = 0;  // the threshold's digits so far
+    // From the second digit on a thread has up to eight neighbouring fours, a bit for each key; a part
+    // of more than 16384 keys takes several rounds.  A key is kept if its digits are above the found ones,
+    // and the first `rest` of those that share them
+    const int per = min(8, (fours + kSelThreads - 1) / kSelThreads);
+    const int rounds = per > 0 ? (fours - 1) / (kSelThreads * per) + 1 : 1;
+    auto first_key = [&](int round) { return (round * kSelThreads + tid) * per * 4; };
+    auto classify = [&](int round, uint32_t& above, uint32_t& equal) {
+        const uint32_t top = found | ~mask;
+        const int i0 = (round * kSelThreads + tid) * per;
+        uint32_t a_ = 0, e_ = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (u >= per || i0 + u >= fours) break;
+            const uint4 q = in_smem ? s_key[slot(i0 + u)] : load(i0 + u);
+            const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (k[c] > top) a_ |= 1u << (4 * u + c);
+                if (k[c] >= found) e_ |= 1u << (4 * u + c);
+            }
+        }
+        above = a_, equal = e_ & ~a_;
+    };
+    uint32_t gt = 0, eq = 0;  // of the first round
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
@@ -130,20 +163,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
 #pragma unroll 4
             for (int i = tid; i < fours; i += kSelThreads) {
                 const uint4 q = load(i);
-                if (in_smem) s_key[i] = q;
+                if (in_smem) s_key[slot(i)] = q;
                 atomicAdd(&h[q.x >> 21], 1);
                 atomicAdd(&h[q.y >> 21], 1);
                 atomicAdd(&h[q.z >> 21], 1);
                 atomicAdd(&h[q.w >> 21], 1);
             }
         } else {
-#pragma unroll 2
-            for (int i = tid; i < fours; i += kSelThreads) {  // (the fours that this thread stored)
-                const uint4 q = keys(i);
-                if ((q.x & mask) == found) atomicAdd(&h[(q.x >> shift) & digit], 1);
-                if ((q.y & mask) == found) atomicAdd(&h[(q.y >> shift) & digit], 1);
-                if ((q.z & mask) == found) atomicAdd(&h[(q.z >> shift) & digit], 1);
-                if ((q.w & mask) == found) atomicAdd(&h[(q.w >> shift) & digit], 1);
+            for (int r = 0; r < rounds; ++r) {
+                uint32_t g = gt, e = eq;
+                if (r > 0 || pass == 1) classify(r, g, e);
+                if (r == 0) gt = g, eq = e;
+                for (uint32_t x = e; x; x &= x - 1) atomicAdd(&h[(key_at(first_key(r) + __ffs(x) - 1) >> shift) & digit], 1);
             }
         }
         __syncthreads();
@@ -177,88 +208,52 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
         found |= static_cast<uint32_t>(s_digit) << shift;
         mask |= digit << shift;
         rest = s_rest;
+        const uint32_t top = found | ~mask;
+        if (pass > 0)  // the first round's keys that shared the digits before
+            for (uint32_t x = eq; x; x &= x - 1) {
+                const uint32_t bit = x & -x, k = key_at(first_key(0) + __ffs(x) - 1);
+                if (k > top) gt |= bit;
+                if (k > top || k < found) eq &= ~bit;
+            }
+        else if (s_all) classify(0, gt, eq);
         if (s_all) break;
         // (s_digit is written again after two barriers at least)
     }
-    // a key is kept if its digits are above the found ones, and the first `rest` of those that share them.
-    // Of four keys: bits 0..3 above, bits 16..19 equal
-    const uint32_t top = found | ~mask;
-    auto look = [&](int i) {
-        const uint4 q = keys(i);
-        uint32_t x = 0;
-        x |= q.x > top ? 0x1u : q.x >= found ? 0x10000u : 0u;
-        x |= q.y > top ? 0x2u : q.y >= found ? 0x20000u : 0u;
-        x |= q.z > top ? 0x4u : q.z >= found ? 0x40000u : 0u;
-        x |= q.w > top ? 0x8u : q.w >= found ? 0x80000u : 0u;
-        return x;
-    };
-    // a warp's part: whole 32 fours, contiguous; what its first eight turns saw is kept for the writing
-    constexpr int kSeen = 8;
-    const int per = (fours + kSelThreads - 1) / kSelThreads * 32;
-    const int f0 = min(fours, warp * per), f1 = min(fours, f0 + per);
-    uint32_t seen[kSeen];
-    int gts = 0, eqs = 0;
-#pragma unroll
-    for (int u = 0; u < kSeen; ++u) {
-        const int i = f0 + lane + 32 * u;
-        seen[u] = i < f1 ? look(i) : 0u;
-        gts += __popc(seen[u] & 0xFu);
-        eqs += __popc(seen[u] >> 16);
-    }
-    for (int i = f0 + lane + 32 * kSeen; i < f1; i += 32) {
-        const uint32_t x = look(i);
-        gts += __popc(x & 0xFu);
-        eqs += __popc(x >> 16);
-    }
-    gts = __reduce_add_sync(0xFFFFFFFFu, gts);
-    eqs = __reduce_add_sync(0xFFFFFFFFu, eqs);
-    if (lane == 0) s_gt[warp] = gts, s_eq[warp] = eqs;
-    __syncthreads();
+    // counts of a round, above in the low half, equal in the high: at most 16384 each
+    int total;
+    int before = block_scan(__popc(gt) | __popc(eq) << 16, part, &total);
     int gt_before = 0, eq_before = 0;
     if constexpr (C > 1) {
-        if (tid == 0) {
-            int x = 0, y = 0;
-            for (int w = 0; w < kSelWarps; ++w) x += s_gt[w], y += s_eq[w];
-            s_sum[0] = x, s_sum[1] = y;
+        int gts = total & 0xFFFF, eqs = total >> 16;
+#pragma unroll 1
+        for (int r = 1; r < rounds; ++r) {
+            uint32_t g, e;
+            classify(r, g, e);
+            int more;
+            __syncthreads();
+            (void)block_scan(__popc(g) | __popc(e) << 16, part, &more);
+            gts += more & 0xFFFF, eqs += more >> 16;
         }
+        if (tid == 0) s_sum[0] = gts, s_sum[1] = eqs;
         cluster_sync();
         for (int r = 0; r < rank; ++r) {
             gt_before += __float_as_int(ld_cluster_f32(cluster_map(smem_u32(&s_sum[0]), r)));
             eq_before += __float_as_int(ld_cluster_f32(cluster_map(smem_u32(&s_sum[1]), r)));
         }
     }
-    for (int w = 0; w < warp; ++w) gt_before += s_gt[w], eq_before += s_eq[w];
-    auto write = [&](int i, uint32_t x) {
-        const uint32_t below = (1u << lane) - 1;
-        int g = gt_before, e = eq_before;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint32_t b = __ballot_sync(0xFFFFFFFFu, x >> u & 1);
-            g += __popc(b & below);
-            gt_before += __popc(b);
-        }
-        if (__any_sync(0xFFFFFFFFu, x >> 16)) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t b = __ballot_sync(0xFFFFFFFFu, x >> (16 + u) & 1);
-                e += __popc(b & below);
-                eq_before += __popc(b);
-            }
-        }
-        if (x) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool is_gt = x >> u & 1, is_eq = x >> (16 + u) & 1;
-                if (is_gt || (is_eq && e < rest)) out[g + min(e, rest)] = c0 + 4 * i + u;
-                g += is_gt;
-                e += is_eq;
-            }
-        }
-    };
-#pragma unroll
-    for (int u = 0; u < kSeen; ++u)
-        if (f0 + 32 * u < f1) write(f0 + lane + 32 * u, seen[u]);
-    for (int ib = f0 + 32 * kSeen; ib < f1; ib += 32) write(ib + lane, ib + lane < f1 ? look(ib + lane) : 0u);
+#pragma unroll 1
+    for (int r = 0;;) {
+        const int e0 = eq_before + (before >> 16);
+        while (eq && e0 + __popc(eq) > rest) eq ^= 0x80000000u >> __clz(eq);
+        int* to = out + gt_before + (before & 0xFFFF) + min(e0, rest);
+        const int t0 = c0 + first_key(r) - 1;
+        for (uint32_t x = gt | eq; x; x &= x - 1) *to++ = t0 + __ffs(x);
+        if (++r >= rounds) break;
+        gt_before += total & 0xFFFF, eq_before += total >> 16;
+        classify(r, gt, eq);
+        __syncthreads();
+        before = block_scan(__popc(gt) | __popc(eq) << 16, part, &total);
+    }
     if constexpr (C > 1) cluster_sync();  // no CTA leaves while a peer may still read its shared memory
 }
 
@@ -276,9 +271,14 @@ cudaError_t launch_select_t(const SelectArgs& a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const int cached = static_cast<int>(min((static_cast<int64_t>((a.max_kv - 1) / C + 1) + 3) / 4 * 4, int64_t{kMost}));
-    return launch_pdl_cluster(kern, dim3(a.hkv * C, a.num_seqs), dim3(kSelThreads), static_cast<size_t>(cached) * 4, stream,
-                              static_cast<unsigned>(C), a, cached);
+    const int cached = static_cast<int>(min((static_cast<int64_t>((a.max_kv - 1) / C + 1) + 31) / 32 * 32, int64_t{kMost}));
+    // Three CTAs an SM serve where two leave CTAs waiting (512 rows of up to 16384 keys: 19.2 us with two,
+    // 17.3 with three), but where two hold all, three would gather on some of the SMs (256 rows of 16384
+    // keys: 12.7 and 16.5 us): shared memory that no second fellow fits beside keeps them apart.
+    const bool two = static_cast<int64_t>(a.hkv) * a.num_seqs * C <= 2 * a.num_sms;
+    const size_t bytes = max(static_cast<size_t>(cached) * 4, two ? size_t{70 * 1024} : size_t{0});
+    return launch_pdl_cluster(kern, dim3(a.hkv * C, a.num_seqs), dim3(kSelThreads), bytes, stream, static_cast<unsigned>(C), a,
+                              cached);
 }
 
 // ------------------------------------------------------------ compaction --
@@ -412,14 +412,15 @@ __global__ void __launch_bounds__(kCmpThreads) compact_in_place_kernel(const Com
 }  // namespace
 
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream) {
-    // CTAs per row.  A CTA alone takes 7.5 us for 8192 keys, 10 for 16384 and 17 for 32768;
-    // eight take 8, 8 and 9 for one of a few rows, but clusters are launched one after the other,
-    // some 27 CTAs a microsecond: 128 rows of 16384 keys take 11.5, 14, 22 and 42 us with 1, 2, 4
-    // and 8, 256 rows of 32768 keys 42 and 38 with 1 and 2.  So: as many as hold 16384 keys each, and more
-    // while the CTAs are few.
+    // CTAs per row.  A CTA alone takes 6.6 us for 8192 keys, 8.7 for 16384 and 13.1 for 32768; eight
+    // take 7.7, 7.8 and 8.8 for one of two rows, but clusters are launched one after the other, some 27
+    // CTAs a microsecond: 128 rows of 16384 keys take 9.7, 12, 19 and 35 us with 1, 2, 4 and 8, 32 rows of
+    // them 9.5, 9.7, 9.4 and 12, 32 rows of 32768 keys 15, 12, 10 and 12, 256 of these 36 and 31 with 1 and 2.
+    // So: as many as hold 16384 keys each, and more while the CTAs are few.
     const int64_t rows = static_cast<int64_t>(a.hkv) * a.num_seqs;
+    const int few = min(128, a.max_kv / 256);
     int c = 1;
-    while (c < 8 && (a.max_kv > 16384 * c || (a.max_kv > 8192 && rows * 2 * c <= 128))) c *= 2;
+    while (c < 8 && (a.max_kv > 16384 * c || (a.max_kv > 8192 && rows * 2 * c <= few))) c *= 2;
     return c == 1 ? launch_select_t<1>(a, stream) : c == 2 ? launch_select_t<2>(a, stream)
          : c == 4 ? launch_select_t<4>(a, stream) : launch_select_t<8>(a, stream);
 }

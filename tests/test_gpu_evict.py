@@ -89,6 +89,22 @@ def rows_of(pool, tables, s, h, at):
     return np.stack([raw[tables[s, t // 16], h, t % 16] for t in at]) if len(at) else np.zeros((0,) + raw.shape[3:], raw.dtype)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal"])
+@pytest.mark.parametrize("heads,lens,budget", [
+    (35, [16384, 16383, 2049], 2048), (35, [6145, 10241, 14336], 5000), (70, [4097, 8193], 4000),  # a CTA a row
+    (1, [8195, 16384], 8000), (3, [140001], 70000), (1, [400003], 3), (1, [420000], 419990)])
+def test_select_at_every_width(heads, lens, budget, kind):
+    """One to eight fours a thread, several rounds of them, parts that shared memory does not hold;
+    with weights of which few or none differ."""
+    rng = np.random.default_rng(heads + budget)
+    mass = np.exp(2 * rng.standard_normal((len(lens), heads, max(lens) + 3))).astype(np.float32)
+    if kind == "ties":
+        mass = np.minimum(np.round(mass), 3).astype(np.float32)
+    elif kind == "equal":
+        mass[:] = 0.25
+    check_select(mass, lens, budget, 2, min(70, budget - 2))
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("in_place", [False, True])
