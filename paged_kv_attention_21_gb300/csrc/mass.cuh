@@ -12,7 +12,7 @@ namespace pkv {
 struct MassSeq {
     int q0, q_len, rows;  // first query row of q, queries, rows counted (queries x group)
     int kv_len, off;      // keys; position of the first query
-    int prefix;
+    int prefix;           // 0 .. kv_len (or 0)
     bool ok;
 };
 
@@ -21,7 +21,6 @@ __device__ __forceinline__ MassSeq mass_seq(const MassArgs& a, int seq, bool fla
     s.q0 = a.qo_indptr ? a.qo_indptr[seq] : seq;
     s.q_len = a.qo_indptr ? a.qo_indptr[seq + 1] - s.q0 : 1;
     s.kv_len = a.kv_lens[seq];
-    s.prefix = a.prefix_lens ? a.prefix_lens[seq] : 0;
     s.ok = s.kv_len > 0;
     if (s.ok && (s.q0 < 0 || s.q_len < 0 || s.q_len > a.total_q - s.q0 || s.kv_len < s.q_len)) {
         if (flag) flag_error(a.err, PKV_DEVERR_POSITION);
@@ -32,6 +31,7 @@ __device__ __forceinline__ MassSeq mass_seq(const MassArgs& a, int seq, bool fla
         s.kv_len = a.max_kv;
         if (s.kv_len < s.q_len) s.ok = false;
     }
+    s.prefix = a.prefix_lens ? max(0, min(a.prefix_lens[seq], s.kv_len)) : 0;
     s.off = s.kv_len - s.q_len;
     int counted = s.q_len;
     if (counted > a.max_q) {
@@ -65,7 +65,7 @@ __device__ __forceinline__ void mass_seen(const MassArgs& a, const MassSeq& s, i
     int unused;
     mass_span(a, s, s.off, lo, unused);
     mass_span(a, s, s.off + ntok - 1, unused, hi);
-    if (a.causal && s.off < s.prefix) hi = max(hi, min(s.prefix, s.kv_len) - 1);
+    if (a.causal && s.off < s.prefix) hi = max(hi, s.prefix - 1);
     if (ntok <= 0) lo = 0, hi = -1;
 }
 

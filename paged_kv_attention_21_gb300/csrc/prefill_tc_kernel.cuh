@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (threadIdx.x == 0 && blockIdx.x == 0) flag_error(a.err, PKV_DEVERR_LENGTH);
         kv_len = cap;
     }
-    const int prefix = kScore && a.prefix_lens ? a.prefix_lens[seq] : 0;
+    // any value may stand there: prefix - 1 of the lowest would wrap to the highest
+    const int prefix = kScore && a.prefix_lens ? max(0, min(a.prefix_lens[seq], kv_len)) : 0;
     const int ntiles_q = (q_len + QT - 1) / QT;
     const int npairs = (ntiles_q + kTcQTiles - 1) / kTcQTiles;
     if (static_cast<int>(blockIdx.x) >= npairs) return;

@@ -184,14 +184,14 @@ __global__ void __launch_bounds__(kSqThreads) short_query_kernel(const PrefillAr
     int hi_r[2], lo_r[2];
     int pos_r[2] = {0, 0};
     float slope2[2] = {0.f, 0.f};
-    const int prefix = kScore && a.prefix_lens ? a.prefix_lens[seq] : 0;
+    const int prefix = kScore && a.prefix_lens ? max(0, min(a.prefix_lens[seq], kv_len)) : 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int r = g0 + 8 * h;
         const int pos = off + (16 * tile + r) / G;  // the window is relative to the query's position
         hi_r[h] = r < trows ? (a.causal ? pos : kv_len - 1) : -1;  // padding rows see no key
         if constexpr (kScore) {  // positions of a prefix see all of it
-            if (r < trows && a.causal && pos < prefix) hi_r[h] = min(prefix, kv_len) - 1;
+            if (r < trows && a.causal && pos < prefix) hi_r[h] = prefix - 1;
             pos_r[h] = pos;
             if (a.slopes && r < trows) slope2[h] = a.slopes[kvh * G + (16 * tile + r) % G] * kLog2e;
         }
