@@ -930,6 +930,9 @@ __global__ void __launch_bounds__(kW * 32) decode_kernel(const DecodeArgs a,
                 l[c] = c < nsplit ? ld_cluster_f32(cluster_map(smem_u32(&s_l[0][r]), c)) : -INFINITY;
                 M = fmaxf(M, l[c]);
             }
+            // a sink joins the normaliser, and the maximum: it may lie any way above the logits
+            const float sk = a.sinks && r < G ? a.sinks[kvh * G + r] : -INFINITY;
+            M = fmaxf(M, sk);
             float W = 0.f;
 #pragma unroll
             for (int c = 0; c < kMaxClusterSplits; ++c) {
@@ -937,7 +940,7 @@ __global__ void __launch_bounds__(kW * 32) decode_kernel(const DecodeArgs a,
                 wts[c * 16 + r] = wv;
                 W += wv;
             }
-            if (a.sinks && r < G && M != -INFINITY) W += __expf(a.sinks[kvh * G + r] - M);
+            if (sk != -INFINITY) W += __expf(sk - M);
             rowM[r] = M;
             rowW[r] = W;
         }
@@ -1004,6 +1007,9 @@ __global__ void __launch_bounds__(kW * 32) decode_kernel(const DecodeArgs a,
                 M = fmaxf(M, __ldcg(a.part_lse + (pair * a.max_splits + i) * G + r));
 #pragma unroll
         for (int off = 1; off < 8; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+        // a sink joins the normaliser, and the maximum: it may lie any way above the logits
+        const float sk = a.sinks && r < G ? a.sinks[kvh * G + r] : -INFINITY;
+        M = fmaxf(M, sk);
         float W = 0.f;
         if (r < G)
             for (int i = sub; i < nsplit; i += 8) {
@@ -1015,8 +1021,7 @@ __global__ void __launch_bounds__(kW * 32) decode_kernel(const DecodeArgs a,
 #pragma unroll
         for (int off = 1; off < 8; off <<= 1) W += __shfl_xor_sync(0xFFFFFFFFu, W, off);
         if (sub == 0) {
-            // a sink joins the normaliser (M is finite: every split has keys)
-            if (a.sinks && r < G) W += __expf(a.sinks[kvh * G + r] - M);
+            if (sk != -INFINITY) W += __expf(sk - M);
             rowM[r] = M;
             rowW[r] = W;
         }

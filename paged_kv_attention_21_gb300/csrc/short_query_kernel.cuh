@@ -530,6 +530,13 @@ __global__ void __launch_bounds__(kSqThreads) short_query_kernel(const PrefillAr
                 l[c] = c < nsplit ? ld_cluster_f32(cluster_map(smem_u32(&s_l[0][r]), c)) : -INFINITY;
                 M = fmaxf(M, l[c]);
             }
+            float sk = -INFINITY;
+            if constexpr (kScore) {
+                // a sink joins the normaliser, and the maximum: it may lie any way above the logits
+                // (a row that saw nothing in any chunk: o = 0, lse = sink)
+                if (a.sinks && r < trows) sk = a.sinks[kvh * G + (16 * tile + r) % G];
+                M = fmaxf(M, sk);
+            }
             float W = 0.f;
 #pragma unroll
             for (int c = 0; c < kSqMaxSplits; ++c) {
@@ -538,12 +545,7 @@ __global__ void __launch_bounds__(kSqThreads) short_query_kernel(const PrefillAr
                 W += wv;
             }
             if constexpr (kScore) {
-                // (a row that saw nothing in any chunk keeps M = the sink: o = 0, lse = sink)
-                if (a.sinks && r < trows) {
-                    const float sk = a.sinks[kvh * G + (16 * tile + r) % G];
-                    if (M == -INFINITY) M = sk;
-                    W += M == -INFINITY ? 0.f : __expf(sk - M);
-                }
+                if (sk != -INFINITY) W += __expf(sk - M);
             }
             rowM[r] = M;
             rowW[r] = W;
