@@ -667,7 +667,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             if constexpr (kCapped || kMode == kTcBoth) {
                 if (!full_vis) row_keys();
-                const float y = largest(sv, sc.in);
+                // rows of no query hold a neighbour's queries or what ran before: they have no say
+                const float y = row_ok ? largest(sv, sc.in) : 0.f;
                 slow = (kCapped && !full_vis) || !__all_sync(0xFFFFFFFFu, y <= kTanhPoly);
                 near = __all_sync(0xFFFFFFFFu, y <= kTanhNear);
             }
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                          mu);
                     weights(c, [&](int u) { return pack_f32x2(v[2 * u], v[2 * u + 1]); });
                 }
-            } else if (kCapped && near) {  // (a wholly visible tile: no score of it is chance)
+            } else if (kCapped && near) {  // (a wholly visible tile, and its own rows: no score is chance)
 #pragma unroll
                 for (int c = 0; c < kTcN / 32; ++c)
                     weights(c, [&](int u) { return tp.near(pack_f32x2(sv[32 * c + 2 * u], sv[32 * c + 2 * u + 1]), neg); });
