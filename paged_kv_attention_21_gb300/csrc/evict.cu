@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
         uint32_t k[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) k[u] = weight_key(w[u]);
-        if (t < lo || t + 4 > hi) {  // (left < 4 is past hi)
+        if (t < lo || t > hi - 4) {  // (left < 4 is past hi; t + 4 may pass 32 bits)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (t + u < lo || t + u >= hi) k[u] = 0xFFFFFFFFu;
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
         const int e0 = eq_before + (before >> 16);
         while (eq && e0 + __popc(eq) > rest) eq ^= 0x80000000u >> __clz(eq);
         int* to = out + gt_before + (before & 0xFFFF) + min(e0, rest);
-        const int t0 = c0 + first_key(r) - 1;
-        for (uint32_t x = gt | eq; x; x &= x - 1) *to++ = t0 + __ffs(x);
+        const int j0 = first_key(r) - 1;
+        for (uint32_t x = gt | eq; x; x &= x - 1) *to++ = c0 + (j0 + __ffs(x));
         if (++r >= rounds) break;
         gt_before += total & 0xFFFF, eq_before += total >> 16;
         classify(r, gt, eq);
