@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) mass_rows_kernel(const MassAr
     int seen_lo, seen_hi;  // blocks that no query sees are not read: their table entries may name none
     mass_seen(a, s, s.rows / G, seen_lo, seen_hi);
     const int32_t* bt = a.block_tables + static_cast<size_t>(seq) * a.mbps;
-    auto block_seen = [&](int blk) { return blk * kBlockSize <= seen_hi && blk * kBlockSize + kBlockSize > seen_lo; };
+    auto block_seen = [&](int blk) { return mass_block_seen(blk, seen_lo, seen_hi); };
     int ids = -1;  // lane k: of the k-th block; -1 where the block is not read or not there
     bool bad = false;
     if (lane < mine && block_seen(first + kMassWarps * lane)) {
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) mass_rows_kernel(const MassAr
         const int id_next = __shfl_sync(0xFFFFFFFFu, ids, (k + 1) & 31);
         if (k + 1 < mine && id_next >= 0) next.load(a, id_next, kvh, g, tig);
         const int t0 = (first + kMassWarps * k) * kBlockSize;
-        const int t_mine = t0 + g + 8 * tig;  // lanes of tig 0 and 1 write
+        const int t_mine = t0 + g + 8 * (tig & 1);  // lanes of tig 0 and 1 write
         float old = 0.f;
         if (a.keep != 0.f && tig < 2 && t_mine < s.off) old = a.keep * mrow[t_mine];
         float sum0 = 0.f, sum1 = 0.f;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) mass_rows_kernel(const MassAr
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_16816<kFp8>(acc[nt], f, qb[nt][kk][0], qb[nt][kk][1]);
             }
-            const bool seen = all_lo <= t0 && all_hi >= min(t0 + kBlockSize, s.kv_len) - 1;
+            const bool seen = all_lo <= t0 && all_hi >= min(t0 + (kBlockSize - 1), s.kv_len - 1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll

@@ -69,4 +69,10 @@ __device__ __forceinline__ void mass_seen(const MassArgs& a, const MassSeq& s, i
     if (ntok <= 0) lo = 0, hi = -1;
 }
 
+// Whether some key of block blk lies in [lo, hi].  (The sums of the last block and of the last
+// tile pass 32 bits in contexts that end there: what is compared stays at or below the last key.)
+__device__ __forceinline__ bool mass_block_seen(int blk, int lo, int hi) {
+    return blk * kBlockSize <= hi && blk * kBlockSize > lo - kBlockSize;
+}
+
 }  // namespace pkv

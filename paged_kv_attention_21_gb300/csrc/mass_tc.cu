@@ -202,7 +202,7 @@ struct MtWalk {
     }
     // blocks that no query sees are not read: their table entries may name none
     __device__ __forceinline__ bool block_seen(int blk) const {
-        return blk * kBlockSize <= seen_hi && blk * kBlockSize + kBlockSize > seen_lo;
+        return mass_block_seen(blk, seen_lo, seen_hi);
     }
 
    private:
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         bool ok = true, q_due = false;
         MtStages q;
         while (w.next()) {
-            const int k0 = (w.tile + x) * kMtKeys, t = k0 + key;
+            const int k0 = (w.tile + min(x, w.n - 1)) * kMtKeys, t = k0 + key;  // (x < n where it counts)
             if (w.fresh) {
                 // a resident segment is over: its stages may be loaded anew
                 __syncwarp();
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             int slo, shi;
             w.steps(slo, shi);
             const int nt = w.n;
-            const int k_last = min(k0 + kMtKeys, w.s.kv_len) - 1;
+            const int k_last = min(k0 + (kMtKeys - 1), w.s.kv_len - 1);
             float* at = a.mass + (static_cast<size_t>(w.seq) * a.hkv + w.kvh) * a.mass_stride + t;
             float old = 0.f, sum = 0.f;
             int id = 0;
