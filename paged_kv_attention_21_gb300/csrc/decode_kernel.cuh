@@ -302,7 +302,7 @@ __device__ __forceinline__ void attend_block(const uint32_t (&qa)[D / 16][4], fl
     (void)kaddr;
 
     // ---- mask + online softmax (exp2 domain)
-    const bool edge = tok_base < lo || tok_base + kBlockSize > ctx;
+    const bool edge = tok_base < lo || tok_base > ctx - kBlockSize;  // (tok_base + 16 may pass 32 bits)
     float x[2][4];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
