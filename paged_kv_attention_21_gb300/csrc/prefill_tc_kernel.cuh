@@ -639,7 +639,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             }
             tc::fence_after_sync();
-            const bool full_vis = (!a.causal || k0 + kTcN - 1 <= max(sp.pos_min, prefix - 1)) && (k0 + kTcN <= kv_len) &&
+            // (k0 + kTcN passes 32 bits in the last tile of a context that ends there)
+            const bool full_vis = (!a.causal || k0 + (kTcN - 1) <= max(sp.pos_min, prefix - 1)) && (k0 <= kv_len - kTcN) &&
                                   (a.window <= 0 || k0 > sp.pos_max - a.window);
             float sv[kTcN];
 #pragma unroll
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             }
             if constexpr (kCapped)
-                mx = base + kTcN > 0 && (base < 0 || static_cast<uint32_t>(base) < cnt) ? sc.capped(mx) : -INFINITY;
+                mx = base > -kTcN && (base < 0 || static_cast<uint32_t>(base) < cnt) ? sc.capped(mx) : -INFINITY;
             if constexpr (kMode == kTcBoth) {
                 if (slow) {
                     mx = -INFINITY;
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // keys past kv_len in the last tile: zero their V rows so that a
             // NaN in an unused slot never meets a zero weight in the MMA.  The
             // tile whose PV reads V_j first does it (A when it uses V_j).
-            const bool zero_v = (k0 + kTcN > kv_len || (kScore && k0 < key_min)) && (x == 0 || j < jlo[0] || j >= jhi[0]);
+            const bool zero_v = (k0 > kv_len - kTcN || (kScore && k0 < key_min)) && (x == 0 || j < jlo[0] || j >= jhi[0]);
             if (zero_v) {
                 const int st = j % C::kVStages;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_v[st], (j / C::kVStages) & 1, kWaitLimitNs, abort))) {
