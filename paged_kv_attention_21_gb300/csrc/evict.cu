@@ -289,9 +289,10 @@ constexpr int kCmpThreads = 256;
 // pieces of the pools; bit r of the answer: row r is there, its position and block ids in
 // range.  Every load of a kind is issued before one is looked at: row by row, a step of
 // eight rows took eight times the round trips (8192 rows of a head in place: 136 us, now 98).
+// (Row numbers are unsigned: those behind the last row, up to 2^31 - 2, pass 31 bits.)
 template <int R>
-__device__ __forceinline__ uint32_t compact_rows(const CompactArgs& a, int seq, int head, int j0, int step, int n, int pieces,
-                                                 int (&pos)[R], size_t (&src)[R], size_t (&dst)[R]) {
+__device__ __forceinline__ uint32_t compact_rows(const CompactArgs& a, int seq, int head, uint32_t j0, uint32_t step, uint32_t n,
+                                                 int pieces, int (&pos)[R], size_t (&src)[R], size_t (&dst)[R]) {
     const int* kept = a.kept + (static_cast<size_t>(seq) * a.hkv + head) * a.kept_stride;
     const int* from = a.src_tables + static_cast<size_t>(seq) * a.src_mbps;
     const int* to = a.dst_tables + static_cast<size_t>(seq) * a.dst_mbps;
@@ -325,10 +326,10 @@ __device__ __forceinline__ uint32_t compact_rows(const CompactArgs& a, int seq, 
     return ok & ~bad;
 }
 
-__device__ __forceinline__ int compact_count(const CompactArgs& a, int seq, bool flag) {
+__device__ __forceinline__ uint32_t compact_count(const CompactArgs& a, int seq, bool flag) {
     const int n = a.kept_lens[seq];
     if (n > a.max_kept && flag) flag_error(a.err, PKV_DEVERR_LENGTH);
-    return min(n, a.max_kept);
+    return static_cast<uint32_t>(max(0, min(n, a.max_kept)));
 }
 
 // A thread moves one 16-byte piece of the K and V of kCmpRows rows.
@@ -337,9 +338,10 @@ __global__ void __launch_bounds__(kCmpThreads) compact_kernel(const CompactArgs 
     pdl_wait();
     pdl_launch_dependents();
     const int seq = blockIdx.z, head = blockIdx.y;
-    const int pieces = a.row_bytes / 16, step = kCmpThreads / pieces;
-    const int n = compact_count(a, seq, blockIdx.x == 0 && head == 0 && threadIdx.x == 0);
-    const int j0 = blockIdx.x * step * kCmpRows + threadIdx.x / pieces;
+    const int pieces = a.row_bytes / 16;
+    const uint32_t step = kCmpThreads / pieces;
+    const uint32_t n = compact_count(a, seq, blockIdx.x == 0 && head == 0 && threadIdx.x == 0);
+    const uint32_t j0 = blockIdx.x * step * kCmpRows + threadIdx.x / pieces;
     const int c = threadIdx.x % pieces;
     if (j0 >= n) return;
     const size_t line = static_cast<size_t>(seq) * a.hkv + head;
@@ -374,17 +376,19 @@ __global__ void __launch_bounds__(kCmpThreads) compact_in_place_kernel(const Com
     pdl_wait();
     pdl_launch_dependents();
     const int seq = blockIdx.z, head = blockIdx.y;
-    const int pieces = a.row_bytes / 16, mine = min(pieces, 8), step = kCmpThreads / mine;
+    const int pieces = a.row_bytes / 16, mine = min(pieces, 8);
+    const uint32_t step = kCmpThreads / mine;
     const int slice = blockIdx.x >> 1;
     uint4* pool = static_cast<uint4*>(blockIdx.x & 1 ? a.v_dst : a.k_dst) + slice * 8;
-    const int n = compact_count(a, seq, blockIdx.x == 0 && head == 0 && threadIdx.x == 0);
-    const int c = threadIdx.x % mine, row = threadIdx.x / mine;
+    const uint32_t n = compact_count(a, seq, blockIdx.x == 0 && head == 0 && threadIdx.x == 0);
+    const int c = threadIdx.x % mine;
+    const uint32_t row = threadIdx.x / mine;
     const bool weights = a.mass && blockIdx.x == 0 && c == 0;
     const size_t line = static_cast<size_t>(seq) * a.hkv + head;
     int pos[kInRows];
     size_t src[kInRows], dst[kInRows];
     uint32_t ok = compact_rows(a, seq, head, row, step, n, pieces, pos, src, dst);
-    for (int j0 = row; j0 - row < n; j0 += step * kInRows) {
+    for (uint32_t j0 = row; j0 - row < n; j0 += step * kInRows) {
         uint4 x[kInRows];
         float w[kInRows];
 #pragma unroll
