@@ -676,8 +676,8 @@ pkv_status pkv_score_prefill(const pkv_cache_desc *desc, const pkv_score *score,
  *   head g, where i sees t, of exp(x_{i,h,t} - lse[i][h]),
  * x and "sees" as above.  The last q_len keys are this call's own: what mass held for
  * them counts as 0, and with keep == 0 nothing of mass is read.  Entries from
- * kv_lens[s] on stay as they are.  A query whose lse is -inf adds nothing.  Over
- * the sums the order of the queries is fixed: a call repeats its bits.
+ * kv_lens[s] on stay as they are.  A query row whose lse is -inf adds nothing, whatever
+ * its q holds.  The order of the queries in a sum is fixed: a call repeats its bits.
  *   q, qo_indptr, k_cache, k_scale, block_tables, kv_lens : as in pkv_score_prefill;
  *               qo_indptr NULL: one query per sequence, q [num_seqs][Hq][D].
  *   lse        : fp32 [total_q_tokens][Hq], as the attention calls return it (a sink's

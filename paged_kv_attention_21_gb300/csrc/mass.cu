@@ -128,10 +128,12 @@ __global__ void __launch_bounds__(kMassWarps * 32) mass_rows_kernel(const MassAr
             if (r2 < s.rows) {
                 const int h = kvh * G + r2 % G;
                 const float lse = a.lse[static_cast<size_t>(s.q0 + r2 / G) * a.hq + h];
-                if (lse != -INFINITY) neg_lse[nt][c] = -lse * kLog2e;
                 if (a.slopes) slope2[nt][c] = a.slopes[h] * kLog2e;
                 pos[nt][c] = s.off + r2 / G;
-                mass_span(a, s, pos[nt][c], lo[nt][c], hi[nt][c]);
+                if (lse != -INFINITY) {  // else the row sees no key: its q may hold anything
+                    neg_lse[nt][c] = -lse * kLog2e;
+                    mass_span(a, s, pos[nt][c], lo[nt][c], hi[nt][c]);
+                }
             }
             all_lo = max(all_lo, lo[nt][c]);
             all_hi = min(all_hi, hi[nt][c]);  // (-1 with rows past the last: 0 times an infinite k is not taken)

@@ -61,7 +61,7 @@ struct MtRows {
     float neg_lse[kMtCols];   // -log2(e) lse; -inf: the row adds nothing
     float slope[kMtCols];     // log2 units
     float tok[kMtCols];       // token index
-    int2 span[kMtCols];       // the keys [x, y] that it sees; [0, -1]: no such row
+    int2 span[kMtCols];       // the keys [x, y] that it sees; [0, -1]: no such row, or none that counts
     int4 chunk[kMtCols / 32]; // of 32 columns: keys [x, y] that all see, [z, w] outside of which none does
 };
 
@@ -347,15 +347,18 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             for (int i = 0; i < kMtCols / 32; ++i) {
                 const int c = lane + 32 * i;
                 const int tok = t0 + row_tok[i];
-                const bool real = row_tok[i] < QT && tok < w.ntok;
+                bool real = row_tok[i] < QT && tok < w.ntok;
                 float nl = -INFINITY, slope = 0.f;
                 int klo = 0, khi = -1;
                 if (real) {
                     const int h = w.kvh * G + row_head[i];
                     const float lse = a.lse[static_cast<size_t>(w.s.q0 + tok) * a.hq + h];
-                    nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-                    if (a.slopes) slope = a.slopes[h] * kLog2e;
-                    mass_span(a, w.s, w.s.off + tok, klo, khi);
+                    real = lse != -INFINITY;  // such a row sees no key: its q may hold anything
+                    if (real) {
+                        nl = -lse * kLog2e;
+                        if (a.slopes) slope = a.slopes[h] * kLog2e;
+                        mass_span(a, w.s, w.s.off + tok, klo, khi);
+                    }
                 }
                 rows[st].neg_lse[c] = nl;
                 rows[st].slope[c] = slope;
