@@ -591,10 +591,15 @@ def pkv_score_prefill(desc, score, q, qo_indptr, k_cache, v_cache, block_tables,
 
 
 def pkv_score_mass(desc, score, q, qo_indptr, k_cache, block_tables, kv_lens, max_kv_len, lse, mass, keep=1.0,
-                   max_q_len=1, causal=True, k_scale=None, stream=None):
+                   max_q_len=None, causal=True, k_scale=None, stream=None):
     """mass (fp32 [num_seqs][Hkv][at least max_kv_len]) becomes keep * mass plus the weight that
     the queries give each key; their own keys start at 0.  lse is what the attention call
-    returned.  qo_indptr None: one query per sequence."""
+    returned.  qo_indptr None: one query per sequence; with it, max_q_len is needed: the most
+    queries that a sequence has (those beyond are not counted)."""
+    if max_q_len is None:
+        if qo_indptr is not None:
+            raise ValueError("max_q_len: needed beside qo_indptr")
+        max_q_len = 1
     _check(_checked().score_mass(desc, score, q, qo_indptr, k_cache, k_scale, block_tables, kv_lens, max_q_len,
                                  max_kv_len, causal, lse, keep, mass, _address(stream)))
 
