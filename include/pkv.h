@@ -687,6 +687,7 @@ pkv_status pkv_score_prefill(const pkv_cache_desc *desc, const pkv_score *score,
  *   max_q_len  : host, >= every q_len; more queries of a sequence are not counted and
  *               set PKV_DEVERR_LENGTH.  (1 with qo_indptr NULL.)
  *   keep       : finite, >= 0.
+ *   mass       : shares nothing with what the call reads.
  * No ring cache (PKV_ERR_UNSUPPORTED).  Over e4m3 pools q may be rounded to f16. */
 pkv_status pkv_score_mass(const pkv_cache_desc *desc, const pkv_score *score, const void *q,
                           const int32_t *qo_indptr, const void *k_cache, const float *k_scale,
@@ -707,7 +708,8 @@ pkv_status pkv_score_mass(const pkv_cache_desc *desc, const pkv_score *score, co
  *               and sets PKV_DEVERR_LENGTH.
  *   budget    : >= 1; first, recent >= 0, first + recent <= budget.
  *   kept      : int32 [num_seqs][num_kv_heads][kept_stride], kept_stride >= min(budget,
- *               max_kv_len).     kept_lens: int32 [num_seqs], shares nothing with kv_lens. */
+ *               max_kv_len).     kept_lens: int32 [num_seqs].  Neither shares anything with the
+ *               other, with mass or with kv_lens. */
 pkv_status pkv_evict_select(const float *mass, int64_t mass_stride, const int32_t *kv_lens,
                             int32_t num_seqs, int32_t num_kv_heads, int32_t max_kv_len,
                             int32_t budget, int32_t first, int32_t recent, int32_t *kept,
@@ -726,10 +728,11 @@ pkv_status pkv_evict_select(const float *mass, int64_t mass_stride, const int32_
  * In place: dst_tables == block_tables, k_dst == k_cache and v_dst == v_cache, with equal
  * tables' shapes; kept must then ascend, as pkv_evict_select leaves it, and mass_out may
  * be mass (with its stride).  Otherwise no block that is written may be read in the same
- * call, and mass_out shares nothing with mass.  Either way dst_tables names a block that is
- * written once only: a prefix that sequences share is given blocks of their own first.  A position outside [0, mass_stride) or
- * the source table sets PKV_DEVERR_POSITION, a block id out of range PKV_DEVERR_BLOCK_ID;
- * that row (and weight) stays as it is.  Without mass, mass_stride is not looked at.
+ * call.  mass_out shares nothing else with what the call reads.  Either way dst_tables names
+ * a block that is written once only: a prefix that sequences share is given blocks of their
+ * own first.  A position outside [0, mass_stride) or the source table sets
+ * PKV_DEVERR_POSITION, a block id out of range PKV_DEVERR_BLOCK_ID; that row (and weight)
+ * stays as it is.  Without mass, mass_stride is not looked at.
  * No ring cache (PKV_ERR_UNSUPPORTED). */
 pkv_status pkv_evict_compact(const pkv_cache_desc *desc, const void *k_cache, const void *v_cache,
                              const int32_t *block_tables, const int32_t *kept, int64_t kept_stride,

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <utility>
 #include <vector>
 #include <cstdarg>
@@ -1939,6 +1940,27 @@ pkv_status check_score(const pkv_score* s) {
     return PKV_OK;
 }
 
+// An array of 4-byte words; rows of `width` words, `stride` apart.
+struct Words {
+    const char* name;
+    const void* at;  // nullptr: none
+    int64_t count;
+    Words(const char* n, const void* p, int64_t c) : name(n), at(p), count(c) {}
+    Words(const char* n, const void* p, int64_t rows, int64_t stride, int64_t width)
+        : name(n), at(p), count((rows - 1) * stride + width) {}
+    bool meets(const Words& o) const {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(at), y = reinterpret_cast<uintptr_t>(o.at);
+        return at && o.at && count > 0 && o.count > 0 && x < y + 4 * o.count && y < x + 4 * count;
+    }
+};
+
+// A kernel's CTAs read their inputs at different times: what one of them writes is no other's input.
+pkv_status check_apart(const Words& out, std::initializer_list<Words> others) {
+    for (const Words& o : others)
+        if (out.meets(o)) return fail(PKV_ERR_INVALID_ARG, "%s overlaps %s", out.name, o.name);
+    return PKV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -2001,6 +2023,12 @@ pkv_status pkv_score_mass(const pkv_cache_desc* desc, const pkv_score* score, co
     if (!aligned(q, 16) || !aligned(k_cache, 16)) return fail(PKV_ERR_INVALID_ARG, "q and the pool must be 16-byte aligned");
     if (!aligned(lse, 4) || !aligned(mass, 4) || !aligned(kv_lens, 4) || !aligned(block_tables, 4) || !aligned(qo_indptr, 4))
         return fail(PKV_ERR_INVALID_ARG, "lse, mass and the index arrays must be 4-byte aligned");
+    st = check_apart(Words("mass", mass, int64_t(num_seqs) * desc->num_kv_heads, mass_stride, max_kv_len),
+                     {Words("lse", lse, int64_t(total_q_tokens) * desc->num_q_heads), Words("kv_lens", kv_lens, num_seqs),
+                      Words("qo_indptr", qo_indptr, num_seqs + 1),
+                      Words("block_tables", block_tables, int64_t(num_seqs) * desc->max_blocks_per_seq),
+                      Words("slopes", score->slopes, desc->num_q_heads), Words("prefix_lens", score->prefix_lens, num_seqs)});
+    if (st != PKV_OK) return st;
     uint32_t* err = nullptr;
     int sms = 0;
     st = device_state(&err, &sms);
@@ -2070,11 +2098,15 @@ pkv_status pkv_evict_select(const float* mass, int64_t mass_stride, const int32_
     if (!mass || !kv_lens || !kept || !kept_lens) return fail(PKV_ERR_INVALID_ARG, "null device pointer");
     if (!aligned(mass, 4) || !aligned(kv_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4))
         return fail(PKV_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
-    if (kept_lens < kv_lens + num_seqs && kv_lens < kept_lens + num_seqs)  // written while other heads' CTAs read kv_lens
-        return fail(PKV_ERR_INVALID_ARG, "kept_lens overlaps kv_lens");
+    const int64_t rows = int64_t(num_seqs) * num_kv_heads;
+    const Words weights("mass", mass, rows, mass_stride, max_kv_len), lens("kv_lens", kv_lens, num_seqs),
+        out("kept", kept, rows, kept_stride, std::min(budget, max_kv_len)), out_lens("kept_lens", kept_lens, num_seqs);
+    pkv_status st = check_apart(out_lens, {lens, weights, out});
+    if (st == PKV_OK) st = check_apart(out, {lens, weights});
+    if (st != PKV_OK) return st;
     uint32_t* err = nullptr;
     int sms = 0;
-    const pkv_status st = device_state(&err, &sms);
+    st = device_state(&err, &sms);
     if (st != PKV_OK) return st;
     pkv::SelectArgs a{};
     a.mass = mass;
@@ -2138,6 +2170,15 @@ pkv_status pkv_evict_compact(const pkv_cache_desc* desc, const void* k_cache, co
         return fail(PKV_ERR_INVALID_ARG, "K rows and V rows share a pool");
     if (mass && mass == mass_out && (!in_place || mass_stride != mass_out_stride))
         return fail(PKV_ERR_INVALID_ARG, "mass_out == mass: in place only, with equal strides");
+    if (mass) {
+        const int64_t rows = int64_t(num_seqs) * desc->num_kv_heads;
+        const Words out("mass_out", mass_out, rows, mass_out_stride, max_kept),
+            in("mass", mass == mass_out ? nullptr : mass, rows, mass_stride, mass_stride);
+        st = check_apart(out, {in, Words("kept", kept, rows, kept_stride, max_kept), Words("kept_lens", kept_lens, num_seqs),
+                               Words("block_tables", block_tables, int64_t(num_seqs) * desc->max_blocks_per_seq),
+                               Words("dst_tables", dst_tables, int64_t(num_seqs) * dst_desc->max_blocks_per_seq)});
+        if (st != PKV_OK) return st;
+    }
     uint32_t* err = nullptr;
     st = device_state(&err, nullptr);
     if (st != PKV_OK) return st;
