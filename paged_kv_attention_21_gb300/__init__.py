@@ -562,6 +562,8 @@ def make_score(sm_scale, cap=0.0, slopes=None, sinks=None, window=0, prefix_lens
                              % (name, t.dtype, tuple(t.shape), kind))
         if t is not None and not t.is_cuda:
             raise ValueError("%s: on %s, expected the current CUDA device" % (name, t.device))
+    if not -2 ** 31 <= int(window) < 2 ** 31:  # (the structure would keep its low 32 bits)
+        raise ValueError("window: %d is no int32" % window)
     at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     s = Score(float(sm_scale), float(cap), int(window), 0, at(slopes), at(sinks), at(prefix_lens))
     s.tensors = (slopes, sinks, prefix_lens)

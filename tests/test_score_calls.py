@@ -68,3 +68,11 @@ def test_weights_refuse_to_be_written_over_what_they_read(lib):
         refused(call_mass(lib, **dict(kw, **{name: at(FAR, 35)})), 1, "mass overlaps " + word)
     refused(call_mass(lib, rule(slopes=FAR + 4), **kw), 1, "mass overlaps slopes")
     refused(call_mass(lib, rule(prefix_lens=FAR + 140), **kw), 1, "mass overlaps prefix_lens")
+
+
+def test_a_window_past_32_bits_is_refused():
+    for window in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="window"):
+            pkv.make_score(0.1, window=window)
+    assert pkv.make_score(0.1, window=2 ** 31 - 1).window == 2 ** 31 - 1
+    assert pkv.make_score(0.1, window=-1).window == -1
