@@ -630,6 +630,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float slope2 = kBiased ? a.slopes[kvh * G + r % G] * kLog2e : 0.f;
         float m_used = -INFINITY;
         float l = 0.f;                             // the row sum
+        // the last key that every row of the tile sees, but for windows
+        const int seen_by_all = a.causal ? min(max(sp.pos_min, prefix - 1), kv_len - 1) : kv_len - 1;
         for (int i = 0; ok && i < nx; ++i) {
             const int j = j0 + i;
             const int k0 = (t_begin + j) * kTcN;
@@ -640,8 +642,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             tc::fence_after_sync();
             // (k0 + kTcN passes 32 bits in the last tile of a context that ends there)
-            const bool full_vis = (!a.causal || k0 + (kTcN - 1) <= max(sp.pos_min, prefix - 1)) && (k0 <= kv_len - kTcN) &&
-                                  (a.window <= 0 || k0 > sp.pos_max - a.window);
+            const bool full_vis = k0 + (kTcN - 1) <= seen_by_all && (a.window <= 0 || k0 > sp.pos_max - a.window);
             float sv[kTcN];
 #pragma unroll
             for (int c = 0; c < kTcN / 32; ++c)
