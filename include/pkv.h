@@ -635,7 +635,9 @@ size_t pkv_quant_decode_workspace_size(const pkv_cache_desc *desc, int32_t num_s
  * denominator (without sinks: their term is 0).  A query that sees no key has
  * o = 0 and lse = -inf (or the sink's logit).
  * All pointers nullable.  prefix_lens[s] may be any value: at most kv_len of it
- * counts, and none below 1. */
+ * counts, and none below 1.  p and t are slots of the cache: where pkv_evict_compact has
+ * moved rows together they are positions no longer, and slopes, window and prefix_lens
+ * would take the distances between slots.  Such a cache is served without them. */
 typedef struct {
     float sm_scale;             /* finite, > 0 */
     float cap;                  /* 0: none; else finite, > 0, sm_scale / cap a normal fp32 number */

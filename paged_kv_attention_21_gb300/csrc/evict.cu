@@ -287,8 +287,9 @@ constexpr int kCmpThreads = 256;
 
 // Where the rows j0, j0 + step, ... below n of (seq, head) come from and go to, in 16-byte
 // pieces of the pools; bit r of the answer: row r is there, its position and block ids in
-// range.  Every load of a kind is issued before one is looked at: row by row, a step of
-// eight rows took eight times the round trips (8192 rows of a head in place: 136 us, now 98).
+// range.  Every load of a kind is issued before one is looked at: row by row, a step took
+// as many round trips as it has rows (8192 rows of one sequence of 8 heads in place: 150 us
+// with eight rows a thread and step, 98 so with kInRows).
 // (Row numbers are unsigned: those behind the last row, up to 2^31 - 2, pass 31 bits.)
 template <int R>
 __device__ __forceinline__ uint32_t compact_rows(const CompactArgs& a, int seq, int head, uint32_t j0, uint32_t step, uint32_t n,

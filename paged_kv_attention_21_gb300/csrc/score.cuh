@@ -24,7 +24,10 @@ constexpr float kTanhC3 = 0.020091967657208443f;
 constexpr float kTanhC4 = -0.005138659384101629f;
 
 // The same for |y| <= 0.3, off by 1.2e-8: three coefficients serve where all of a tile's
-// scores are that small, as most are.
+// scores are that small.  Logits of standard deviation 2 are under a cap of 50 (8 x 512 tokens
+// over up to 8704 keys: prefill 362 us, weights 250), under one of 20 they are not (393, 282),
+// and under one of 10 and of 6.7 ever more tiles hold a score past kTanhPoly (639 and 862; 429
+// and 565).
 constexpr float kTanhNear = 0.3f;
 constexpr float kTanhN0 = -0.33333060145378113f;
 constexpr float kTanhN1 = 0.13314832746982574f;
